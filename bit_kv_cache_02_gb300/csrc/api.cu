@@ -215,6 +215,8 @@ int kvq_set_wait_test(int64_t limit_cycles, int32_t wait_before_fetch) {
 
 namespace kvq {
 
+void count_launches(uint64_t n) { g_launches.fetch_add(n); }
+
 int decode_attn_clearing(const kvq_cache *cache, int32_t num_q_heads, const uint16_t *q, float softmax_scale,
                          uint16_t *out, void *workspace, size_t workspace_bytes, int32_t max_len, void *stream) {
   return ::decode_attn(cache, num_q_heads, q, softmax_scale, out, workspace, workspace_bytes, max_len, stream, true);

@@ -1,0 +1,125 @@
+// Internal definitions shared by the kernels of the 8-bit paged KV cache
+// (include/kv8.h).
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "../../include/kv8.h"
+#include "kvq_internal.cuh"
+
+namespace kv8 {
+
+using kvq::set_status;
+
+// Cache geometry and buffers as the kernels see them.
+struct Geo {
+  int S, H, D, B, fmt, bf16, capacity, max_blocks, num_blocks;
+  uint8_t *codes;
+  float *scales;
+  uint16_t *k_win, *v_win;
+  const int *seq_len;
+  const int *table;
+  int *status;
+};
+
+// A 16-bit tensor [rows][heads][D] (strides in elements).
+struct Rows {
+  uint16_t *p;
+  long long row, head;
+};
+
+// The new rows of sequence s and its length; ok: the row range is usable.
+struct Seq {
+  int L, n, row0;
+  bool ok;
+};
+
+__device__ __forceinline__ Seq load_seq(const Geo &geo, const int *row_start, int rows, int max_new, int s) {
+  Seq q;
+  q.L = geo.seq_len[s];
+  long long r0 = s, r1 = s + 1;
+  if (row_start) {
+    r0 = row_start[s];
+    r1 = row_start[s + 1];
+  }
+  q.ok = r0 >= 0 && r1 >= r0 && r1 <= rows && r1 - r0 <= max_new;
+  q.row0 = static_cast<int>(r0);
+  q.n = q.ok ? static_cast<int>(r1 - r0) : 0;
+  return q;
+}
+
+// Largest s with key(s) <= x, where key rises with s (0 if there is none).
+template <typename F>
+__device__ __forceinline__ int last_at_or_below(int S, int x, F key) {
+  int lo = 0, hi = S - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (key(mid) <= x)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+// 2^e as fp32 for -126 <= e <= 127.
+__device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 127) << 23); }
+
+// The two 16-bit floats of a word as fp32.
+template <bool BF16>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+
+// Two fp32 values rounded to a word of 16-bit floats (x0 in the low half).
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float x0, float x1) {
+  if (BF16) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(x0, x1);
+    return *reinterpret_cast<const uint32_t *>(&b);
+  }
+  return kvq::h2_as_u32(__floats2half2_rn(x0, x1));
+}
+
+// Magnitude bits from which a 16-bit float is an infinity or a NaN.
+template <bool BF16>
+__host__ __device__ constexpr uint32_t nonfinite_bits() {
+  return BF16 ? 0x7f80u : 0x7c00u;
+}
+
+// ------------------------------------------------------- host-side launchers
+
+cudaError_t launch_append(const Geo &geo, const Rows &k, const Rows &v, const Rows &q, const Rows &q_out, int Hq,
+                          const int *row_start, int rows, int max_new, const float *rope, int rot_dim,
+                          int interleaved, cudaStream_t stream, uint64_t *launches);
+
+// CTAs of one attention launch at most (sizes the workspace's partial slots).
+constexpr int kMaxCtas = 640;
+constexpr int kRowTile = 16;  // (token, query head) rows that share one pass over the keys
+
+// Byte offsets of the workspace regions: partial outputs [2 kMaxCtas][16][D],
+// their (max, sum), and one merge counter per CTA.
+struct AttnPlan {
+  size_t off_ml, off_cnt, bytes;
+};
+AttnPlan plan_attn(int D);
+
+struct AttnArgs {
+  Geo geo;
+  int Hq, group;
+  Rows q, out;
+  const int *row_start;
+  int rows, max_new, max_len;
+  float zscale;       // softmax scale * log2(e)
+  float *part_o;      // [2 kMaxCtas][16][D] unnormalized partial outputs
+  float2 *part_ml;    // [2 kMaxCtas][16] (max, sum) in log2 units
+  int *counters;      // [kMaxCtas], zero on entry, left zero on exit
+};
+
+cudaError_t launch_attn(const AttnArgs &a, cudaStream_t stream, uint64_t *launches);
+// the rows kernel for one head dimension (one translation unit each)
+cudaError_t launch_rows_128(const AttnArgs &a, cudaStream_t stream);
+cudaError_t launch_rows_64(const AttnArgs &a, cudaStream_t stream);
+
+}  // namespace kv8

@@ -1,0 +1,819 @@
+// Attention over the 8-bit paged cache for few rows per sequence: single
+// tokens, drafts (a "row" is one query head of one new token; the rows of a
+// KV head share its keys).
+//
+// Mathematics: for each row an online softmax over 32-token units (16 in the
+// 16-bit window): z = (q . k_code) * scale_k * softmax_scale * log2(e), m the
+// running maximum, p = 2^(z - m + 15), l the sum of p, o the sum of
+// scale_v * (p . v_code).  Codes are exact in fp16, so both products run on
+// mma.sync m16n8k16 with fp32 accumulators: rows are M, tokens N of the first
+// product and K of the second, whose A operand is the first one's accumulator
+// fragment as it lies in registers.  Roundings to 16 bits: p to fp16 (the factor
+// 2^15, taken back where o and l are formed, keeps weights down to 2^-29 of the
+// largest at full precision), and bf16 queries, which a power of two per row
+// brings into fp16's range: a rounding only of elements 2^-29 below the row's
+// largest.  Window tokens in bf16 are multiplied as they are (mma in bf16), so
+// that no token's size touches another's; their weights go in as a bf16 part
+// and the bf16 remainder, 2^-17 of themselves off.
+//
+// The units of all (sequence, KV head, 16-row tile) triples form one line,
+// cut into one equal range per CTA whatever the sequences' lengths.  The four
+// warps of a CTA take the units of a triple in turn, each with its own ring of
+// shared-memory slots filled by asynchronous copies, and merge their softmax
+// states through shared memory when the triple (or the CTA's part of it)
+// ends.  A triple cut by CTA borders is merged by the last CTA that finishes.
+//
+// Bound: HBM (2 D bytes per token and KV head).  16-byte chunks are XOR
+// swizzled by the token so that neither operand's shared-memory reads
+// conflict: a lane's 16-byte read covers 16 channels of one token, which is
+// four k-steps of the first product, or one channel of each of 16 n-tiles of
+// the second; the channel order within the products is free as long as both
+// operands agree on it.
+#pragma once
+
+#include <type_traits>
+
+#include "kv8_internal.cuh"
+
+namespace kv8 {
+namespace rows {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kWarps = 4;
+constexpr int kUnit = 32;     // tokens of a unit of quantized blocks
+constexpr int kWinUnit = 16;  // tokens of a unit of the window
+#ifndef KV8_ROWS_SLOTS
+#define KV8_ROWS_SLOTS 3
+#endif
+
+template <int D>
+struct Smem {
+  static constexpr int SLOTS = D == 128 ? KV8_ROWS_SLOTS : 2 * KV8_ROWS_SLOTS;
+  static constexpr int HALF = kUnit * D;   // bytes of a unit's keys (and of its values)
+  static constexpr int SLOT = 2 * HALF;    // a window unit has the same size
+  static constexpr int NT = D / 8;         // n-tiles of the output
+  static constexpr int META = kWarps * SLOTS * SLOT;                 // scales of each slot: float2
+  static constexpr int ML = META + kWarps * SLOTS * 8;               // [kWarps][16] float2
+  static constexpr int XCH = (ML + kWarps * kRowTile * 8 + 15) / 16 * 16;  // merge buffer, one row half
+  static constexpr int FLAG = XCH + kWarps * 3 * (NT / 4) * 2 * 32 * 4;
+  static constexpr int BYTES = FLAG + 16;
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// 16 bytes, or zeros when `full` is false
+__device__ __forceinline__ void cp16z(uint32_t dst, const void *src, bool full) {
+  const int n = full ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp8(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+
+// d = a * b + c with c = 0
+__device__ __forceinline__ void mma_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  kvq::mma16816(d, a[0], a[1], a[2], a[3], b0, b1);
+}
+
+// Four code bytes of a word to fp16 pairs (bytes 0, 1) and (bytes 2, 3).
+// int8: with the sign bit flipped a byte is code + 128, and 0x64 above it
+// makes the fp16 number 1024 + 128 + code.
+template <int FMT>
+__device__ __forceinline__ void widen(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  if (FMT == KV8_INT8) {
+    const uint32_t u = w ^ 0x80808080u;
+    uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 off = __floats2half2_rn(1152.f, 1152.f);
+    lo = kvq::h2_as_u32(__hsub2(*reinterpret_cast<__half2 *>(&a), off));
+    hi = kvq::h2_as_u32(__hsub2(*reinterpret_cast<__half2 *>(&b), off));
+  } else {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+  }
+}
+
+// d = a * b + d in bf16
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Weights are formed as 2^15 p.
+constexpr float kShift = 15.f, kUnshift = 1.f / 32768.f;
+
+// A power-of-two pair (f, 1/f) that brings bf16 magnitudes up to `bits` to
+// just below 2^15.  Magnitudes below 2^-107 count as that.
+__device__ __forceinline__ float2 bf16_norm(uint32_t bits) {
+  const int e = max(static_cast<int>(bits >> 7), 20);  // biased exponent of the largest, <= 254
+  return make_float2(__int_as_float((268 - e) << 23), __int_as_float((e - 14) << 23));
+}
+
+// A word of two bf16, scaled, as a word of two fp16.
+__device__ __forceinline__ uint32_t bf16_to_fp16(uint32_t w, float f) {
+  const float2 x = unpack2<true>(w);
+  return kvq::h2_as_u32(__floats2half2_rn(x.x * f, x.y * f));
+}
+
+// Largest finite magnitude of two 16-bit floats, folded into m.
+__device__ __forceinline__ uint32_t finite_max(uint32_t m, uint32_t w, uint32_t limit) {
+  const uint32_t lo = w & 0x7fffu, hi = (w >> 16) & 0x7fffu;
+  m = max(m, lo < limit ? lo : 0u);
+  return max(m, hi < limit ? hi : 0u);
+}
+
+// Work of one sequence: its units per (KV head, row tile) pair, and pairs.
+struct Work {
+  Seq q;
+  int full;   // units of complete blocks
+  int units;  // all units
+  int tiles;  // row tiles per KV head
+};
+
+__device__ __forceinline__ Work seq_work(const AttnArgs &a, int s) {
+  Work w;
+  w.q = load_seq(a.geo, a.row_start, a.rows, a.max_new, s);
+  const int L = w.q.L;
+  const bool some = w.q.n > 0 && L > 0 && L <= a.max_len;
+  const int nb = L / a.geo.B;
+  w.full = some ? nb * (a.geo.B / kUnit) : 0;
+  w.units = some ? w.full + (L - nb * a.geo.B + kWinUnit - 1) / kWinUnit : 0;
+  w.tiles = some ? (w.q.n * a.group + kRowTile - 1) / kRowTile : 0;
+  return w;
+}
+__device__ __forceinline__ long long line_of(const Work &w, int H) {
+  return static_cast<long long>(w.units) * w.tiles * H;
+}
+
+// Walks a CTA's range of the line, one part of a (sequence, head, tile)
+// triple at a time.
+struct Walk {
+  Work w;
+  int s, h, tile;
+  long long at, end;  // line position and end of the range
+  int u0, u1;         // units of the current part
+  long long start;    // line position of the triple's unit 0
+
+  __device__ __forceinline__ void part() {
+    u1 = static_cast<int>(min(static_cast<long long>(w.units), u0 + (end - at)));
+    start = at - u0;
+  }
+  // the sequence that holds line position `pos`, whose own line starts at `base`
+  __device__ __forceinline__ void enter(const AttnArgs &a, int seq, long long base, long long pos, long long end_) {
+    s = seq;
+    w = seq_work(a, s);
+    at = pos;
+    end = end_;
+    const int pair = static_cast<int>((pos - base) / w.units);
+    u0 = static_cast<int>((pos - base) - static_cast<long long>(pair) * w.units);
+    h = pair / w.tiles;
+    tile = pair - h * w.tiles;
+    part();
+  }
+  // the next part; false at the end of the range
+  __device__ __forceinline__ bool next(const AttnArgs &a) {
+    at += u1 - u0;
+    if (at >= end) return false;
+    u0 = 0;
+    if (++tile >= w.tiles) {
+      tile = 0;
+      if (++h >= a.geo.H) {
+        h = 0;
+        do {
+          if (++s >= a.geo.S) return false;
+          w = seq_work(a, s);
+        } while (w.units == 0);
+      }
+    }
+    part();
+    return true;
+  }
+};
+
+template <int D, int FMT, bool BF16, int HALVES>
+__global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
+  using SM = Smem<D>;
+  constexpr int NT = SM::NT;      // output n-tiles
+  constexpr int KS = D / 16;      // k-steps of the scores
+  constexpr int REGS = 2 * HALVES;  // accumulator registers in use per n-tile
+  extern __shared__ __align__(128) unsigned char smem[];
+  const Geo &geo = a.geo;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q4 = lane & 3;
+  const int B = geo.B, H = geo.H;
+  const float ninf = __int_as_float(0xff800000);
+
+  // Sequences with rows and nothing to see: zero rows.
+  for (int s = blockIdx.x; s < geo.S; s += gridDim.x) {
+    const Seq sq = load_seq(geo, a.row_start, a.rows, a.max_new, s);
+    if (!sq.ok) {
+      if (tid == 0) set_status(geo.status, KVQ_STATUS_BAD_LEN);
+      continue;
+    }
+    if (sq.n == 0 || (sq.L > 0 && sq.L <= a.max_len)) continue;
+    if (tid == 0 && sq.L != 0) set_status(geo.status, KVQ_STATUS_MAX_LEN);
+    const int per_row = a.Hq * (D / 8);
+    for (long long i = tid; i < static_cast<long long>(sq.n) * per_row; i += kWarps * 32) {
+      const int row = static_cast<int>(i / per_row), c = static_cast<int>(i % per_row);
+      *reinterpret_cast<uint4 *>(a.out.p + (sq.row0 + row) * a.out.row + (c / (D / 8)) * a.out.head +
+                                 (c % (D / 8)) * 8) = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+
+  // The line's length, this CTA's range of it, and where the range starts.
+  long long total = 0;
+  for (int s = lane; s < geo.S; s += 32) total += line_of(seq_work(a, s), H);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
+  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + kWarps - 1) / kWarps));
+  if (static_cast<int>(blockIdx.x) >= ctas) return;
+  const long long lo = blockIdx.x * total / ctas, hi = (blockIdx.x + 1) * total / ctas;
+  Walk use;
+  {
+    long long base = 0;
+    for (int s0 = 0;; s0 += 32) {
+      const long long mine = s0 + lane < geo.S ? line_of(seq_work(a, s0 + lane), H) : 0;
+      long long incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(kAll, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const unsigned past = __ballot_sync(kAll, base + incl > lo);
+      if (past) {
+        const int j = __ffs(past) - 1;
+        use.enter(a, s0 + j, base + __shfl_sync(kAll, incl - mine, j), lo, hi);
+        break;
+      }
+      base += __shfl_sync(kAll, incl, 31);
+    }
+  }
+
+  // ---- fetch: the warp's units, in the order it will use them
+  Walk get = use;
+  bool more = true;
+  int gu = get.u0 + warp;  // next unit to fetch
+  const uint32_t ring = kvq::smem_u32(smem) + warp * SM::SLOTS * SM::SLOT;
+  const uint32_t meta = kvq::smem_u32(smem) + SM::META + warp * SM::SLOTS * 8;
+  const int upb = B / kUnit;
+  // lane -> (row, chunk) of the copies, the swizzled place included
+  constexpr int CPR = D / 16;                 // 16-byte chunks of a code row
+  constexpr int RPI = 32 / CPR;               // code rows per instruction
+  const int cr = lane / CPR, cc = lane % CPR;
+
+  auto settle = [&]() {  // move to a part that has a unit for this warp
+    while (more && gu >= get.u1) {
+      more = get.next(a);
+      gu = get.u0 + warp;
+    }
+  };
+  auto table_entry = [&]() -> int {
+    if (!more || gu >= get.w.full) return 0;
+    return geo.table[static_cast<size_t>(get.s) * geo.max_blocks + gu / upb];
+  };
+  settle();
+  int entry = table_entry();
+
+  auto fetch = [&](int slot) {
+    if (more) {
+      const uint32_t kdst = ring + slot * SM::SLOT, vdst = kdst + SM::HALF;
+      if (gu < get.w.full) {
+        const bool good = entry >= 0 && entry < geo.num_blocks;
+        const size_t bh = static_cast<size_t>(good ? entry : 0) * H + get.h;
+        const uint8_t *ks = geo.codes + (bh * 2 * B + (gu % upb) * kUnit) * D + lane * 16;
+        const uint8_t *vs = ks + static_cast<size_t>(B) * D;
+#pragma unroll
+        for (int i = 0; i < kUnit / RPI; ++i) {
+          const int row = i * RPI + cr;
+          const int sw = D == 128 ? (row & 7) : ((row >> 1) & 3);
+          const uint32_t off = row * D + ((cc ^ sw) << 4);
+          cp16(kdst + off, ks + i * 512);
+          cp16(vdst + off, vs + i * 512);
+        }
+        if (good) {
+          if (lane == 0) cp8(meta + slot * 8, geo.scales + bh * 2);
+        } else if (lane == 0) {
+          set_status(geo.status, KVQ_STATUS_BAD_BLOCK);
+          const float nan = __int_as_float(0x7fc00000);
+          *reinterpret_cast<float2 *>(smem + SM::META + (warp * SM::SLOTS + slot) * 8) = make_float2(nan, nan);
+        }
+      } else {
+        const int t0 = (gu - get.w.full) * kWinUnit;
+        const int r = get.w.q.L % B - t0;  // tokens of the window from t0 on
+        const size_t row0 = (static_cast<size_t>(get.s) * H + get.h) * B + t0;
+#pragma unroll
+        for (int i = 0; i < kWinUnit * CPR * 2 / 32; ++i) {
+          const int c = i * 32 + lane, row = c / (2 * CPR), col = c % (2 * CPR);
+          const uint32_t off = row * 2 * D + ((col ^ (row & 7)) << 4);
+          // slots past the sequence's end are not read: zeros
+          const size_t src = (row0 + (row < r ? row : 0)) * D + col * 8;
+          cp16z(kdst + off, geo.k_win + src, row < r);
+          cp16z(vdst + off, geo.v_win + src, row < r);
+        }
+      }
+      gu += kWarps;
+      settle();
+      entry = table_entry();
+    }
+    cp_commit();
+  };
+
+#pragma unroll
+  for (int i = 0; i < SM::SLOTS; ++i) fetch(i);
+  int slot = 0;
+
+  for (bool live = true; live; live = use.next(a)) {
+    const Work &w = use.w;
+    const int n_rows = w.q.n * a.group;  // rows of this KV head
+    const int r0 = use.tile * kRowTile;  // first row of the tile
+
+    // ---- the tile's queries as A fragments; lane (g, q4) holds 16 channels
+    // of rows g and g + 8 per 64 channels
+    uint32_t qa[KS][4];
+    float qf[2];
+    int lim[2];  // last position each row sees
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = r0 + g + 8 * r;
+      const bool valid = (r == 0 || HALVES == 2) && row < n_rows;
+      const int tok = valid ? row / a.group : 0;
+      lim[r] = valid ? w.q.L - w.q.n + tok : -1;
+      const uint16_t *src = a.q.p + (static_cast<long long>(w.q.row0) + tok) * a.q.row +
+                            (static_cast<long long>(use.h) * a.group + (valid ? row - tok * a.group : 0)) * a.q.head;
+      uint32_t big = 0;
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
+        if (valid) {
+          x = *reinterpret_cast<const uint4 *>(src + (c * 4 + q4) * 16);
+          y = *reinterpret_cast<const uint4 *>(src + (c * 4 + q4) * 16 + 8);
+        }
+        const uint32_t e[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          qa[c * 4 + i / 2][r + 2 * (i & 1)] = e[i];
+          if (BF16) big = finite_max(big, e[i], 0x7f80u);
+        }
+      }
+      qf[r] = a.zscale;
+      if (BF16) {
+        big = max(big, __shfl_xor_sync(kAll, big, 1));
+        big = max(big, __shfl_xor_sync(kAll, big, 2));
+        const float2 f = bf16_norm(big);
+        qf[r] *= f.y;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          qa[k][r] = bf16_to_fp16(qa[k][r], f.x);
+          qa[k][r + 2] = bf16_to_fp16(qa[k][r + 2], f.x);
+        }
+      }
+    }
+    // every row of the tile sees at least the tokens up to here
+    const int seen_by_all = w.q.L - w.q.n + r0 / a.group;
+
+    float acc[NT][REGS], m[2] = {ninf, ninf}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int r = 0; r < REGS; ++r) acc[j][r] = 0.f;
+
+    // Scores of one unit to weights 2^15 p: NB n-tiles of 8 tokens from position t0;
+    // column 2 q4 of a tile is token 2 q4, column 2 q4 + 1 token (2 q4 + 1) ^ 4.
+    auto softmax = [&](auto nb, float (*sc)[4], float ks, int t0, bool window, uint32_t nan_mask) {
+      constexpr int NB = decltype(nb)::value;
+      float mx[2] = {m[0], m[1]};
+      const float kf[2] = {ks * qf[0], ks * qf[1]};
+      const bool edge = t0 + 8 * NB - 1 > seen_by_all;
+#pragma unroll
+      for (int t = 0; t < NB; ++t) {
+#pragma unroll
+        for (int i = 0; i < REGS; ++i) {
+          const int r = i >> 1, col = 8 * t + ((i & 1) ? ((2 * q4 + 1) ^ 4) : 2 * q4);
+          float z = sc[t][i] * kf[r];
+          if (window) z += z - z;  // an infinite score becomes NaN
+          if (nan_mask >> col & 1u) z = __int_as_float(0x7fc00000);
+          if (edge && t0 + col > lim[r]) z = ninf;
+          sc[t][i] = z;
+          mx[r] = fmaxf(mx[r], z);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < HALVES; ++r) {
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(kAll, mx[r], 1));
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(kAll, mx[r], 2));
+      }
+      bool moved = mx[0] != m[0];
+      if (HALVES == 2) moved |= mx[1] != m[1];
+      if (__any_sync(kAll, moved)) {
+#pragma unroll
+        for (int r = 0; r < HALVES; ++r) {
+          const float f = mx[r] == m[r] ? 1.f : kvq::fast_exp2(m[r] - mx[r]);  // -inf before the first token
+          m[r] = mx[r];
+          l[r] *= f;
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            acc[j][2 * r] *= f;
+            acc[j][2 * r + 1] *= f;
+          }
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < NB; ++t) {
+#pragma unroll
+        for (int r = 0; r < HALVES; ++r) {
+          const float ms = m[r] == ninf ? 0.f : m[r] - kShift;
+          sc[t][2 * r] = kvq::fast_exp2(sc[t][2 * r] - ms);
+          sc[t][2 * r + 1] = kvq::fast_exp2(sc[t][2 * r + 1] - ms);
+          l[r] += sc[t][2 * r] + sc[t][2 * r + 1];
+        }
+        if (HALVES == 1) sc[t][2] = sc[t][3] = 0.f;
+      }
+    };
+    // the weights of n-tiles 2 k, 2 k + 1 as the A operand of k-step k
+    auto weights = [&](uint32_t (&p)[4], const float *lo, const float *hi) {
+      p[0] = kvq::h2_as_u32(__floats2half2_rn(lo[0], lo[1]));
+      p[1] = kvq::h2_as_u32(__floats2half2_rn(lo[2], lo[3]));
+      p[2] = kvq::h2_as_u32(__floats2half2_rn(hi[0], hi[1]));
+      p[3] = kvq::h2_as_u32(__floats2half2_rn(hi[2], hi[3]));
+    };
+
+    for (int u = use.u0 + warp; u < use.u1; u += kWarps) {
+      cp_wait<SM::SLOTS - 1>();
+      __syncwarp();
+      const uint32_t kt = ring + slot * SM::SLOT, vt = kt + SM::HALF;
+      if (u < w.full) {
+        const float2 sc2 = *reinterpret_cast<const float2 *>(smem + SM::META + (warp * SM::SLOTS + slot) * 8);
+        float sc[4][4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int row = 8 * t + (g ^ ((g & 1) << 2));
+          const int sw = D == 128 ? (row & 7) : ((row >> 1) & 3);
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) {
+            const uint4 x = lds16(kt + row * D + (((c * 4 + q4) ^ sw) << 4));
+            const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t b0, b1;
+              widen<FMT>(e[i], b0, b1);
+              if (c == 0 && i == 0)
+                mma_zero(sc[t], qa[0], b0, b1);
+              else
+                mma(sc[t], qa[c * 4 + i], b0, b1);
+            }
+          }
+        }
+        // values without a finite scale make the rows that see them NaN
+        const bool vbad = !(fabsf(sc2.y) < __int_as_float(0x7f800000));
+        softmax(std::integral_constant<int, 4>{}, sc, sc2.x, u * kUnit, false, vbad ? 0xffffffffu : 0u);
+        uint32_t p[2][4];
+        weights(p[0], sc[0], sc[1]);
+        weights(p[1], sc[2], sc[3]);
+        const float vs = vbad ? 0.f : sc2.y * kUnshift;
+        // values: lane (g, q4) reads its channels of the 8 tokens of its k indices
+        constexpr int VW = D / 32;  // words per token
+        uint32_t v[8][VW];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {  // token: k-step i / 4, k index 2 q4 + (i & 1) + 8 (i / 2 & 1)
+          const int row = 16 * (i >> 2) + 8 * (i >> 1 & 1) + ((i & 1) ? ((2 * q4 + 1) ^ 4) : 2 * q4);
+          if (D == 128) {
+            const uint4 x = lds16(vt + row * D + ((g ^ (row & 7)) << 4));
+            v[i][0] = x.x;
+            v[i][1] = x.y;
+            v[i][VW > 2 ? 2 : 0] = VW > 2 ? x.z : x.x;
+            v[i][VW > 3 ? 3 : 0] = VW > 3 ? x.w : x.x;
+          } else {
+            const uint2 x = lds8(vt + row * D + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8);
+            v[i][0] = x.x;
+            v[i][1] = x.y;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < VW; ++j) {
+          uint32_t b[2][2][4];  // [k-step][b0, b1][channel of the word]
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t x = v[2 * i][j], y = v[2 * i + 1][j];
+            uint32_t(&d)[4] = b[i >> 1][i & 1];
+            widen<FMT>(__byte_perm(x, y, 0x5140), d[0], d[1]);
+            widen<FMT>(__byte_perm(x, y, 0x7362), d[2], d[3]);
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float o[4];
+            mma_zero(o, p[0], b[0][0][c], b[0][1][c]);
+            mma(o, p[1], b[1][0][c], b[1][1][c]);
+#pragma unroll
+            for (int r = 0; r < REGS; ++r) acc[4 * j + c][r] = fmaf(o[r], vs, acc[4 * j + c][r]);
+          }
+        }
+      } else {
+        // ---- 16 window tokens in 16 bits
+        const int t0 = (u - w.full) * kWinUnit;
+        float sc[2][4];
+        uint32_t qb[BF16 ? KS : 1][4];  // the queries in bf16: exact, they came from it
+        if (BF16) {
+#pragma unroll
+          for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 x = unpack2<false>(qa[k][i]);
+              qb[BF16 ? k : 0][i] = pack2<true>(x.x, x.y);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int row = 8 * t + (g ^ ((g & 1) << 2));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sc[t][i] = 0.f;
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) {
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const uint4 x = lds16(kt + row * 2 * D + ((((c * 4 + q4) * 2 + hf) ^ (row & 7)) << 4));
+              const int k = c * 4 + 2 * hf;
+              if (BF16) {
+                mma_bf16(sc[t], qb[BF16 ? k : 0], x.x, x.y);
+                mma_bf16(sc[t], qb[BF16 ? k + 1 : 0], x.z, x.w);
+              } else {
+                mma(sc[t], qa[k], x.x, x.y);
+                mma(sc[t], qa[k + 1], x.z, x.w);
+              }
+            }
+          }
+        }
+        constexpr int VW = D / 16;  // words of the lane's channels per token (2 channels each)
+        uint32_t v[4][VW];
+        uint32_t bad = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = 8 * (i >> 1) + ((i & 1) ? ((2 * q4 + 1) ^ 4) : 2 * q4);
+          uint32_t any = 0;
+#pragma unroll
+          for (int k = 0; k < VW / 4; ++k) {
+            const uint4 x = lds16(vt + row * 2 * D + (((g * (VW / 4) + k) ^ (row & 7)) << 4));
+            const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              v[i][4 * k + c] = e[c];
+              any |= __vcmpgeu2(e[c] & 0x7fff7fffu, nonfinite_bits<BF16>() * 0x10001u);
+            }
+          }
+          if (any) bad |= 1u << row;
+        }
+        bad = __reduce_or_sync(kAll, bad);
+        softmax(std::integral_constant<int, 2>{}, sc, 1.f, w.full * kUnit + t0, true, bad);
+        uint32_t p[4], rest[4];
+        if (BF16) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float x = sc[i >> 1][2 * (i & 1)] * kUnshift, y = sc[i >> 1][2 * (i & 1) + 1] * kUnshift;
+            p[i] = pack2<true>(x, y);
+            const float2 f = unpack2<true>(p[i]);
+            rest[i] = pack2<true>(x - f.x, y - f.y);
+          }
+        } else {
+          weights(p, sc[0], sc[1]);
+        }
+        if (bad) {  // their weights are NaN where they are seen, and 0 elsewhere
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = 8 * (i >> 1) + ((i & 1) ? ((2 * q4 + 1) ^ 4) : 2 * q4);
+            if (bad >> row & 1u)
+#pragma unroll
+              for (int k = 0; k < VW; ++k) v[i][k] = 0u;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < VW; ++k) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t b0 = __byte_perm(v[0][k], v[1][k], c ? 0x7632 : 0x5410);
+            const uint32_t b1 = __byte_perm(v[2][k], v[3][k], c ? 0x7632 : 0x5410);
+            float o[4] = {0.f, 0.f, 0.f, 0.f};
+            if (BF16) {
+              mma_bf16(o, p, b0, b1);
+              mma_bf16(o, rest, b0, b1);
+            } else {
+              mma(o, p, b0, b1);
+            }
+#pragma unroll
+            for (int r = 0; r < REGS; ++r) acc[2 * k + c][r] = fmaf(o[r], BF16 ? 1.f : kUnshift, acc[2 * k + c][r]);
+          }
+        }
+      }
+      __syncwarp();  // every lane has read the slot
+      fetch(slot);
+      slot = slot + 1 == SM::SLOTS ? 0 : slot + 1;
+    }
+
+    // ---- merge the four warps' states; warp w ends up with quarter w of the
+    // n-tiles
+    float2 *ml = reinterpret_cast<float2 *>(smem + SM::ML);
+    float *xch = reinterpret_cast<float *>(smem + SM::XCH);
+#pragma unroll
+    for (int r = 0; r < HALVES; ++r) {
+      l[r] += __shfl_xor_sync(kAll, l[r], 1);
+      l[r] += __shfl_xor_sync(kAll, l[r], 2);
+      l[r] *= kUnshift;
+      if (q4 == 0) ml[warp * kRowTile + g + 8 * r] = make_float2(m[r], l[r]);
+    }
+    __syncthreads();
+    const bool whole = use.u0 == 0 && use.u1 == w.units;
+    const int part = 2 * blockIdx.x + (use.start + use.u0 == lo ? 0 : 1);
+    constexpr int QT = NT / 4;
+#pragma unroll
+    for (int r = 0; r < HALVES; ++r) {
+      float mm = ninf, ll = 0.f;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) mm = fmaxf(mm, ml[i * kRowTile + g + 8 * r].x);
+      const float base = mm == ninf ? 0.f : mm;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) {
+        const float2 e = ml[i * kRowTile + g + 8 * r];
+        ll += e.y * kvq::fast_exp2(e.x - base);
+      }
+      const float f = kvq::fast_exp2(m[r] - base);
+      if (r) __syncthreads();  // the buffer of the first half has been read
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        acc[j][2 * r] *= f;
+        acc[j][2 * r + 1] *= f;
+        const int dst = j / QT;
+        if (dst != warp) {
+          float *o = xch + ((dst * 3 + ((warp - dst - 1) & 3)) * QT + j % QT) * 64 + lane;
+          o[0] = acc[j][2 * r];
+          o[32] = acc[j][2 * r + 1];
+        }
+      }
+      __syncthreads();
+      float o0[QT], o1[QT];
+#pragma unroll
+      for (int j = 0; j < QT; ++j) {
+        o0[j] = o1[j] = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (k == warp) {
+            o0[j] = acc[k * QT + j][2 * r];
+            o1[j] = acc[k * QT + j][2 * r + 1];
+          }
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          const float *x = xch + ((warp * 3 + i) * QT + j) * 64 + lane;
+          o0[j] += x[0];
+          o1[j] += x[32];
+        }
+      }
+      // n-tile j, column c holds channel (D / 8) c + j
+      const int ch0 = (D / 8) * (2 * q4) + warp * QT, ch1 = ch0 + D / 8;
+      const int row = r0 + g + 8 * r;
+      if (row < n_rows) {
+        if (whole) {
+          const float inv = ll == 0.f ? 0.f : 1.f / ll;
+          const int tok = row / a.group;
+          uint16_t *dst = a.out.p + (static_cast<long long>(w.q.row0) + tok) * a.out.row +
+                          (static_cast<long long>(use.h) * a.group + row - tok * a.group) * a.out.head;
+#pragma unroll
+          for (int j = 0; j < QT; j += 2) {
+            *reinterpret_cast<uint32_t *>(dst + ch0 + j) = pack2<BF16>(o0[j] * inv, o0[j + 1] * inv);
+            *reinterpret_cast<uint32_t *>(dst + ch1 + j) = pack2<BF16>(o1[j] * inv, o1[j + 1] * inv);
+          }
+        } else {
+          float *dst = a.part_o + (static_cast<size_t>(part) * kRowTile + g + 8 * r) * D;
+#pragma unroll
+          for (int j = 0; j < QT; j += 2) {
+            *reinterpret_cast<float2 *>(dst + ch0 + j) = make_float2(o0[j], o0[j + 1]);
+            *reinterpret_cast<float2 *>(dst + ch1 + j) = make_float2(o1[j], o1[j + 1]);
+          }
+          if (warp == 0 && q4 == 0) a.part_ml[part * kRowTile + g + 8 * r] = make_float2(mm, ll);
+        }
+      }
+    }
+
+    if (!whole) {
+      // ---- the last CTA with a part of this triple merges them all
+      const long long s0 = use.start, s1 = s0 + w.units;  // the triple's place on the line
+      auto owner = [&](long long pos) { return static_cast<int>(((pos + 1) * ctas - 1) / total); };
+      const int c0 = owner(s0), c1 = owner(s1 - 1);
+      int *flag = reinterpret_cast<int *>(smem + SM::FLAG);
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        const int before = kvq::atom_add_acq_rel(a.counters + c0, 1);
+        const bool last = before == c1 - c0;
+        if (last) a.counters[c0] = 0;
+        *flag = last;
+      }
+      __syncthreads();
+      if (*flag) {
+        __threadfence();
+        const int first = 2 * c0 + (c0 * total / ctas < s0 ? 1 : 0);  // later CTAs begin with their part
+        const int parts = c1 - c0 + 1;
+        constexpr int W = D / 32;  // channels per lane
+        for (int row = warp; row < kRowTile && r0 + row < n_rows; row += kWarps) {
+          float mm = ninf;
+          for (int i = lane; i < parts; i += 32) {
+            const int sl = i == 0 ? first : 2 * (c0 + i);
+            mm = fmaxf(mm, __ldcg(&a.part_ml[sl * kRowTile + row]).x);
+          }
+#pragma unroll
+          for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(kAll, mm, o));
+          const float base = mm == ninf ? 0.f : mm;
+          float ll = 0.f, o[W];
+#pragma unroll
+          for (int k = 0; k < W; ++k) o[k] = 0.f;
+#pragma unroll 4
+          for (int i = 0; i < parts; ++i) {
+            const int sl = i == 0 ? first : 2 * (c0 + i);
+            const float2 e = __ldcg(&a.part_ml[sl * kRowTile + row]);
+            const float f = kvq::fast_exp2(e.x - base);
+            ll += e.y * f;
+            const float *src = a.part_o + (static_cast<size_t>(sl) * kRowTile + row) * D + lane * W;
+            if (W == 4) {
+              const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
+              o[0] += x.x * f;
+              o[1] += x.y * f;
+              o[W > 2 ? 2 : 0] += W > 2 ? x.z * f : 0.f;
+              o[W > 3 ? 3 : 0] += W > 3 ? x.w * f : 0.f;
+            } else {
+              const float2 x = __ldcg(reinterpret_cast<const float2 *>(src));
+              o[0] += x.x * f;
+              o[1] += x.y * f;
+            }
+          }
+          const float inv = ll == 0.f ? 0.f : 1.f / ll;
+          const int tok = (r0 + row) / a.group;
+          uint16_t *dst = a.out.p + (static_cast<long long>(w.q.row0) + tok) * a.out.row +
+                          (static_cast<long long>(use.h) * a.group + r0 + row - tok * a.group) * a.out.head + lane * W;
+#pragma unroll
+          for (int k = 0; k < W; k += 2)
+            *reinterpret_cast<uint32_t *>(dst + k) = pack2<BF16>(o[k] * inv, o[k + 1] * inv);
+        }
+      }
+    }
+    __syncthreads();  // the merge buffers are free for the next part
+  }
+  cp_wait<0>();
+}
+
+template <int D, int FMT, bool BF16, int HALVES>
+cudaError_t launch_one(const AttnArgs &a, cudaStream_t stream) {
+  auto kernel = rows_kernel<D, FMT, BF16, HALVES>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::BYTES);
+  if (e != cudaSuccess) return e;
+  int dev = 0, sms = 0, per = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+  if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kWarps * 32, Smem<D>::BYTES)) != cudaSuccess)
+    return e;
+  // no more CTAs than units for their warps, as far as the host can tell
+  const long long tiles = (static_cast<long long>(a.max_new) * a.group + kRowTile - 1) / kRowTile;
+  const long long units = (a.max_len / kUnit + a.geo.B / kWinUnit) * tiles * a.geo.H * a.geo.S;
+  long long grid = min(static_cast<long long>(kMaxCtas), static_cast<long long>(sms) * max(per, 1));
+  grid = max(1LL, min(grid, (units + kWarps - 1) / kWarps));
+  kernel<<<static_cast<unsigned>(grid), kWarps * 32, Smem<D>::BYTES, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <int D, int FMT, bool BF16>
+cudaError_t launch_halves(const AttnArgs &a, cudaStream_t stream) {
+  return static_cast<long long>(a.max_new) * a.group <= 8 ? launch_one<D, FMT, BF16, 1>(a, stream)
+                                                          : launch_one<D, FMT, BF16, 2>(a, stream);
+}
+
+template <int D>
+cudaError_t launch_dim(const AttnArgs &a, cudaStream_t stream) {
+  if (a.geo.fmt == KV8_INT8)
+    return a.geo.bf16 ? launch_halves<D, KV8_INT8, true>(a, stream) : launch_halves<D, KV8_INT8, false>(a, stream);
+  return a.geo.bf16 ? launch_halves<D, KV8_E4M3, true>(a, stream) : launch_halves<D, KV8_E4M3, false>(a, stream);
+}
+
+}  // namespace rows
+}  // namespace kv8

@@ -280,6 +280,8 @@ cudaError_t launch_decode(const Geo &geo, int Hq, const __half *q, float softmax
 int decode_attn_clearing(const kvq_cache *cache, int32_t num_q_heads, const uint16_t *q, float softmax_scale,
                          uint16_t *out, void *workspace, size_t workspace_bytes, int32_t max_len, void *stream);
 int set_decode_warps(int warps);
+// Adds to what kvq_launch_count reports.
+void count_launches(uint64_t n);
 // Test aid: cycle limit of the decode kernel's pipeline waits (0: the
 // default) and whether each warp's first wait comes before its first copy.
 int set_wait_test(long long cycles, int wait_before_fetch);

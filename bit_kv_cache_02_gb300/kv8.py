@@ -1,0 +1,225 @@
+"""Python binding of the 8-bit paged KV cache, include/kv8.h (ctypes).
+
+Argument marshalling only, as in kvq.py: torch tensors serve as device memory
+and torch streams as CUDA streams.
+"""
+
+from __future__ import annotations
+
+import ctypes
+from ctypes import c_float, c_int32, c_int64, c_size_t, c_void_p
+
+import torch
+
+from .kvq import KVQ_OK, KvqError, lib
+
+FORMATS = {"int8": 0, "e4m3": 1}
+DTYPES = {torch.float16: 0, torch.bfloat16: 1}
+CODE_DTYPES = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}
+BUF_CODES, BUF_SCALES, BUF_K_WIN, BUF_V_WIN, BUF_SEQ_LEN, BUF_BLOCK_TABLE = range(6)
+
+EXPORTED = ("kv8_max_blocks", "kv8_buffer_bytes", "kv8_append", "kv8_attn_workspace_bytes", "kv8_attn")
+
+
+class CacheStruct(ctypes.Structure):
+    """Mirror of `kv8_cache` (include/kv8.h)."""
+    _fields_ = [
+        ("num_seqs", c_int32), ("num_kv_heads", c_int32), ("head_dim", c_int32), ("block", c_int32),
+        ("format", c_int32), ("dtype", c_int32), ("capacity", c_int32), ("num_blocks", c_int32),
+        ("codes", c_void_p), ("scales", c_void_p), ("k_win", c_void_p), ("v_win", c_void_p),
+        ("seq_len", c_void_p), ("block_table", c_void_p), ("status", c_void_p),
+    ]
+
+
+class RowsStruct(ctypes.Structure):
+    """Mirror of `kv8_rows` (include/kv8.h)."""
+    _fields_ = [("data", c_void_p), ("row_stride", c_int64), ("head_stride", c_int64)]
+
+
+def _sign():
+    C, R = ctypes.POINTER(CacheStruct), ctypes.POINTER(RowsStruct)
+    sig = {
+        "kv8_max_blocks": (c_int32, [C]),
+        "kv8_buffer_bytes": (c_int64, [C, c_int32]),
+        "kv8_append": (ctypes.c_int, [C, R, R, R, R, c_int32, c_void_p, c_int32, c_int32, c_void_p, c_int32, c_int32,
+                                      c_int32, c_void_p]),
+        "kv8_attn_workspace_bytes": (c_int64, [C, c_int32, c_int32]),
+        "kv8_attn": (ctypes.c_int, [C, c_int32, R, R, c_void_p, c_int32, c_int32, c_float, c_void_p, c_size_t,
+                                    c_int32, c_void_p]),
+    }
+    for name, (res, args) in sig.items():
+        fn = getattr(lib, name)
+        fn.restype = res
+        fn.argtypes = args
+
+
+_sign()
+
+
+def _check(code: int, what: str):
+    if code != KVQ_OK:
+        raise KvqError(code, what)
+
+
+class KV8Cache:
+    """Device buffers of one 8-bit paged cache (one layer) and its descriptor.
+
+    num_blocks: blocks of the pool; the caller assigns them to sequences in
+    block_table [S][capacity // block] (int32, filled with -1) before the
+    appends that complete them.  seq_len (int32 [S], zeros) counts the tokens
+    of each sequence, those of the step in progress included; the caller
+    advances it.  Buffers given as arguments are used as they are (another
+    layer's seq_len and block_table, say), the others allocated.
+    """
+
+    def __init__(self, num_seqs, num_kv_heads, capacity, num_blocks, head_dim=128, block=64, fmt="int8",
+                 dtype=torch.float16, device="cuda", codes=None, scales=None, k_win=None, v_win=None, seq_len=None,
+                 block_table=None, status=None):
+        if fmt not in FORMATS or dtype not in DTYPES:
+            raise ValueError(f"format {fmt!r} or dtype {dtype} not supported")
+        st = CacheStruct(num_seqs, num_kv_heads, head_dim, block, FORMATS[fmt], DTYPES[dtype], capacity, num_blocks)
+        self.max_blocks = lib.kv8_max_blocks(ctypes.byref(st))
+        if self.max_blocks < 0:
+            raise KvqError(-2, "kv8_max_blocks")
+        self.num_seqs, self.num_kv_heads, self.head_dim, self.block = num_seqs, num_kv_heads, head_dim, block
+        self.capacity, self.num_blocks, self.fmt, self.dtype = capacity, num_blocks, fmt, dtype
+        if codes is not None:
+            device = codes.device
+        self.device = torch.device(device)
+        if self.device.type == "cuda" and self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        S, H, B, D = num_seqs, num_kv_heads, block, head_dim
+
+        def buffer(name, given, shape, dt, fill=0):
+            if given is None:
+                n = 1
+                for x in shape:
+                    n *= x
+                # an empty buffer still has an address
+                t = torch.full((max(n, 1),), fill, dtype=torch.uint8 if dt in CODE_DTYPES.values() else dt,
+                               device=self.device)
+                return (t.view(dt) if t.dtype != dt else t)[:n].view(shape)
+            if tuple(given.shape) != shape or given.dtype != dt or not given.is_contiguous() \
+                    or given.device != self.device:
+                raise ValueError(f"{name}: a contiguous {dt} tensor of shape {shape} on {self.device} is needed")
+            return given
+
+        self.codes = buffer("codes", codes, (num_blocks, H, 2, B, D), CODE_DTYPES[fmt])
+        self.scales = buffer("scales", scales, (num_blocks, H, 2), torch.float32)
+        self.k_win = buffer("k_win", k_win, (S, H, B, D), dtype)
+        self.v_win = buffer("v_win", v_win, (S, H, B, D), dtype)
+        self.seq_len = buffer("seq_len", seq_len, (S,), torch.int32)
+        self.block_table = buffer("block_table", block_table, (S, self.max_blocks), torch.int32, -1)
+        self.status = buffer("status", status, (1,), torch.int32)
+        for name in ("codes", "scales", "k_win", "v_win", "seq_len", "block_table", "status"):
+            setattr(st, name, getattr(self, name).data_ptr() or None)
+        self.struct = st
+
+    @property
+    def ref(self):
+        return ctypes.byref(self.struct)
+
+
+def rope_table(rows: int, rot_dim: int, theta: float = 10000.0, device="cuda"):
+    """The rope argument of kv8_append for plain rotary embeddings: row p has
+    the cosines, then the sines, of p * theta^(-2 i / rot_dim), formed in 64
+    bits and rounded to fp32."""
+    i = torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device)
+    ang = torch.arange(rows, dtype=torch.float64, device=device)[:, None] * theta ** (-i / rot_dim)
+    return torch.cat([ang.cos(), ang.sin()], 1).float()
+
+
+def _rows(t, cache, name):
+    """RowsStruct of a [rows][heads][D] tensor (any row and head strides)."""
+    if t.dtype != cache.dtype or t.dim() != 3 or t.shape[2] != cache.head_dim or t.device != cache.device:
+        raise ValueError(f"{name}: a {cache.dtype} tensor [rows][heads][{cache.head_dim}] on {cache.device} is needed")
+    row, head, one = t.stride()
+    if one != 1:
+        raise ValueError(f"{name}: the elements of a head must be contiguous")
+    return RowsStruct(t.data_ptr(), row, head)
+
+
+def _row_start(row_start, cache):
+    if row_start is None:
+        return None
+    if row_start.dtype != torch.int32 or row_start.numel() != cache.num_seqs + 1 or not row_start.is_contiguous() \
+            or row_start.device != cache.device:
+        raise ValueError(f"row_start: a contiguous int32 tensor [{cache.num_seqs + 1}] on {cache.device} is needed")
+    return row_start.data_ptr()
+
+
+class _On:
+    """Makes the cache's device current for a launch, where it is not already."""
+
+    def __init__(self, device):
+        self.device = device
+
+    def __enter__(self):
+        self.before = torch.cuda.current_device()
+        if self.before != self.device.index:
+            torch.cuda.set_device(self.device)
+
+    def __exit__(self, *exc):
+        if self.before != self.device.index:
+            torch.cuda.set_device(self.before)
+
+
+def _stream(stream, device):
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def kv8_append(cache: KV8Cache, k, v, row_start=None, max_new: int = 1, q=None, q_out=None, rope=None,
+               interleaved: bool = False, stream=None):
+    """k, v: [rows][Hkv][D]; q, q_out: [rows][Hq][D] (rotated along; q_out may
+    be q); rope: fp32 [positions][rot_dim] (rope_table) or None.  row_start:
+    int32 [S + 1], or None for one row per sequence."""
+    H = cache.num_kv_heads
+    if k.shape != v.shape or k.shape[1] != H:
+        raise ValueError(f"k and v: [rows][{H}][{cache.head_dim}]")
+    ks, vs = _rows(k, cache, "k"), _rows(v, cache, "v")
+    qs = os = None
+    heads = 0
+    if q is not None:
+        if q_out is None or q_out.shape != q.shape or q.shape[0] != k.shape[0]:
+            raise ValueError("q_out: the shape of q, and the rows of k, are needed")
+        heads = q.shape[1]
+        qs, os = ctypes.byref(_rows(q, cache, "q")), ctypes.byref(_rows(q_out, cache, "q_out"))
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rot = rope_rows = 0
+    if rope is not None:
+        if rope.dtype != torch.float32 or rope.dim() != 2 or not rope.is_contiguous() or rope.device != cache.device:
+            raise ValueError(f"rope: a contiguous float32 tensor [positions][rot_dim] on {cache.device} is needed")
+        rope_rows, rot = rope.shape
+    start = _row_start(row_start, cache)
+    with _On(cache.device):
+        _check(lib.kv8_append(cache.ref, ctypes.byref(ks), ctypes.byref(vs), qs, os, heads,
+                              start, k.shape[0], int(max_new),
+                              rope.data_ptr() if rot else None, rope_rows, rot, int(bool(interleaved)),
+                              _stream(stream, cache.device)), "kv8_append")
+
+
+def attn_workspace_bytes(cache: KV8Cache, num_q_heads: int, max_new: int = 1) -> int:
+    n = lib.kv8_attn_workspace_bytes(cache.ref, num_q_heads, max_new)
+    if n < 0:
+        raise KvqError(-1, "kv8_attn_workspace_bytes")
+    return n
+
+
+def alloc_workspace(cache: KV8Cache, num_q_heads: int, max_new: int = 1):
+    """A torch-allocated, zero-filled workspace for kv8_attn."""
+    return torch.zeros(attn_workspace_bytes(cache, num_q_heads, max_new), dtype=torch.uint8, device=cache.device)
+
+
+def kv8_attn(cache: KV8Cache, q, out, workspace, max_len: int, row_start=None, max_new: int = 1,
+             softmax_scale: float = 0.0, stream=None):
+    """q, out: [rows][Hq][D] (out may be q); max_len: a bound on seq_len."""
+    if q.shape != out.shape:
+        raise ValueError("q and out differ in shape")
+    if workspace.device != cache.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace: a contiguous tensor on {cache.device} is needed")
+    qs, os, start = _rows(q, cache, "q"), _rows(out, cache, "out"), _row_start(row_start, cache)
+    with _On(cache.device):
+        _check(lib.kv8_attn(cache.ref, q.shape[1], ctypes.byref(qs), ctypes.byref(os), start, q.shape[0],
+                            int(max_new), float(softmax_scale), workspace.data_ptr(), workspace.numel() * workspace.element_size(), int(max_len),
+                            _stream(stream, cache.device)), "kv8_attn")
