@@ -31,6 +31,7 @@
 // operands agree on it.
 #pragma once
 
+#include <atomic>
 #include <type_traits>
 
 #include "kv8_internal.cuh"
@@ -785,18 +786,28 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
 template <int D, int FMT, bool BF16, int HALVES>
 cudaError_t launch_one(const AttnArgs &a, cudaStream_t stream) {
   auto kernel = rows_kernel<D, FMT, BF16, HALVES>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::BYTES);
+  // resident CTAs and SMs of each device, once looked up
+  static std::atomic<int> resident[64], sm_count[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  int dev = 0, sms = 0, per = 0;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-  if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kWarps * 32, Smem<D>::BYTES)) != cudaSuccess)
-    return e;
+  int per = dev < 64 ? resident[dev].load() : 0, sms = dev < 64 ? sm_count[dev].load() : 0;
+  if (per == 0 || sms == 0) {
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::BYTES)) != cudaSuccess)
+      return e;
+    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kWarps * 32, Smem<D>::BYTES)) != cudaSuccess)
+      return e;
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    per = max(per, 1);
+    if (dev < 64) {
+      sm_count[dev].store(sms);
+      resident[dev].store(per);
+    }
+  }
   // no more CTAs than units for their warps, as far as the host can tell
   const long long tiles = (static_cast<long long>(a.max_new) * a.group + kRowTile - 1) / kRowTile;
   const long long units = (a.max_len / kUnit + a.geo.B / kWinUnit) * tiles * a.geo.H * a.geo.S;
-  long long grid = min(static_cast<long long>(kMaxCtas), static_cast<long long>(sms) * max(per, 1));
+  long long grid = min(static_cast<long long>(kMaxCtas), static_cast<long long>(sms) * per);
   grid = max(1LL, min(grid, (units + kWarps - 1) / kWarps));
   kernel<<<static_cast<unsigned>(grid), kWarps * 32, Smem<D>::BYTES, stream>>>(a);
   return cudaGetLastError();

@@ -7,6 +7,7 @@ and torch streams as CUDA streams.
 from __future__ import annotations
 
 import ctypes
+import struct
 from ctypes import c_float, c_int32, c_int64, c_size_t, c_void_p
 
 import torch
@@ -36,8 +37,14 @@ class RowsStruct(ctypes.Structure):
     _fields_ = [("data", c_void_p), ("row_stride", c_int64), ("head_stride", c_int64)]
 
 
+# The same bytes, packed at a tenth of the cost of a ctypes structure: a call's
+# host time is what a one-token step waits for.
+_pack_rows = struct.Struct("@Pqq").pack
+assert struct.calcsize("@Pqq") == ctypes.sizeof(RowsStruct)
+
+
 def _sign():
-    C, R = ctypes.POINTER(CacheStruct), ctypes.POINTER(RowsStruct)
+    C, R = ctypes.POINTER(CacheStruct), c_void_p  # R: packed bytes, or a reference to a RowsStruct
     sig = {
         "kv8_max_blocks": (c_int32, [C]),
         "kv8_buffer_bytes": (c_int64, [C, c_int32]),
@@ -54,11 +61,6 @@ def _sign():
 
 
 _sign()
-
-
-def _check(code: int, what: str):
-    if code != KVQ_OK:
-        raise KvqError(code, what)
 
 
 class KV8Cache:
@@ -114,10 +116,8 @@ class KV8Cache:
         for name in ("codes", "scales", "k_win", "v_win", "seq_len", "block_table", "status"):
             setattr(st, name, getattr(self, name).data_ptr() or None)
         self.struct = st
-
-    @property
-    def ref(self):
-        return ctypes.byref(self.struct)
+        self.ref = ctypes.byref(st)
+        self.device_index = self.codes.get_device()  # -1 on the CPU
 
 
 def rope_table(rows: int, rot_dim: int, theta: float = 10000.0, device="cuda"):
@@ -130,42 +130,37 @@ def rope_table(rows: int, rot_dim: int, theta: float = 10000.0, device="cuda"):
 
 
 def _rows(t, cache, name):
-    """RowsStruct of a [rows][heads][D] tensor (any row and head strides)."""
-    if t.dtype != cache.dtype or t.dim() != 3 or t.shape[2] != cache.head_dim or t.device != cache.device:
+    """kv8_rows of a [rows][heads][D] tensor (any row and head strides)."""
+    if t.dtype != cache.dtype or t.dim() != 3 or t.get_device() != cache.device_index:
         raise ValueError(f"{name}: a {cache.dtype} tensor [rows][heads][{cache.head_dim}] on {cache.device} is needed")
     row, head, one = t.stride()
-    if one != 1:
-        raise ValueError(f"{name}: the elements of a head must be contiguous")
-    return RowsStruct(t.data_ptr(), row, head)
+    if one != 1 or t.shape[2] != cache.head_dim:
+        raise ValueError(f"{name}: heads of {cache.head_dim} contiguous elements are needed")
+    return _pack_rows(t.data_ptr(), row, head)
 
 
 def _row_start(row_start, cache):
     if row_start is None:
         return None
     if row_start.dtype != torch.int32 or row_start.numel() != cache.num_seqs + 1 or not row_start.is_contiguous() \
-            or row_start.device != cache.device:
+            or row_start.get_device() != cache.device_index:
         raise ValueError(f"row_start: a contiguous int32 tensor [{cache.num_seqs + 1}] on {cache.device} is needed")
     return row_start.data_ptr()
 
 
-class _On:
-    """Makes the cache's device current for a launch, where it is not already."""
-
-    def __init__(self, device):
-        self.device = device
-
-    def __enter__(self):
-        self.before = torch.cuda.current_device()
-        if self.before != self.device.index:
-            torch.cuda.set_device(self.device)
-
-    def __exit__(self, *exc):
-        if self.before != self.device.index:
-            torch.cuda.set_device(self.before)
-
-
-def _stream(stream, device):
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+def _launch(fn, what, cache, stream, *args):
+    """fn(*args, stream) with the cache's device current."""
+    index = cache.device_index
+    if index < 0:
+        raise ValueError("the cache is not on a CUDA device")
+    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        code = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            code = fn(*args, raw)
+    if code != KVQ_OK:
+        raise KvqError(code, what)
 
 
 def kv8_append(cache: KV8Cache, k, v, row_start=None, max_new: int = 1, q=None, q_out=None, rope=None,
@@ -183,20 +178,18 @@ def kv8_append(cache: KV8Cache, k, v, row_start=None, max_new: int = 1, q=None, 
         if q_out is None or q_out.shape != q.shape or q.shape[0] != k.shape[0]:
             raise ValueError("q_out: the shape of q, and the rows of k, are needed")
         heads = q.shape[1]
-        qs, os = ctypes.byref(_rows(q, cache, "q")), ctypes.byref(_rows(q_out, cache, "q_out"))
+        qs, os = _rows(q, cache, "q"), _rows(q_out, cache, "q_out")
     elif q_out is not None:
         raise ValueError("q_out without q")
-    rot = rope_rows = 0
+    table, rot, positions = None, 0, 0
     if rope is not None:
-        if rope.dtype != torch.float32 or rope.dim() != 2 or not rope.is_contiguous() or rope.device != cache.device:
+        if rope.dtype != torch.float32 or rope.dim() != 2 or not rope.is_contiguous() \
+                or rope.get_device() != cache.device_index:
             raise ValueError(f"rope: a contiguous float32 tensor [positions][rot_dim] on {cache.device} is needed")
-        rope_rows, rot = rope.shape
-    start = _row_start(row_start, cache)
-    with _On(cache.device):
-        _check(lib.kv8_append(cache.ref, ctypes.byref(ks), ctypes.byref(vs), qs, os, heads,
-                              start, k.shape[0], int(max_new),
-                              rope.data_ptr() if rot else None, rope_rows, rot, int(bool(interleaved)),
-                              _stream(stream, cache.device)), "kv8_append")
+        positions, rot = rope.shape
+        table = rope.data_ptr() if rot else None
+    _launch(lib.kv8_append, "kv8_append", cache, stream, cache.ref, ks, vs, qs, os, heads,
+            _row_start(row_start, cache), k.shape[0], max_new, table, positions, rot, 1 if interleaved else 0)
 
 
 def attn_workspace_bytes(cache: KV8Cache, num_q_heads: int, max_new: int = 1) -> int:
@@ -216,10 +209,8 @@ def kv8_attn(cache: KV8Cache, q, out, workspace, max_len: int, row_start=None, m
     """q, out: [rows][Hq][D] (out may be q); max_len: a bound on seq_len."""
     if q.shape != out.shape:
         raise ValueError("q and out differ in shape")
-    if workspace.device != cache.device or not workspace.is_contiguous():
+    if workspace.get_device() != cache.device_index or not workspace.is_contiguous():
         raise ValueError(f"workspace: a contiguous tensor on {cache.device} is needed")
-    qs, os, start = _rows(q, cache, "q"), _rows(out, cache, "out"), _row_start(row_start, cache)
-    with _On(cache.device):
-        _check(lib.kv8_attn(cache.ref, q.shape[1], ctypes.byref(qs), ctypes.byref(os), start, q.shape[0],
-                            int(max_new), float(softmax_scale), workspace.data_ptr(), workspace.numel() * workspace.element_size(), int(max_len),
-                            _stream(stream, cache.device)), "kv8_attn")
+    _launch(lib.kv8_attn, "kv8_attn", cache, stream, cache.ref, q.shape[1], _rows(q, cache, "q"),
+            _rows(out, cache, "out"), _row_start(row_start, cache), q.shape[0], max_new, softmax_scale,
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), max_len)
