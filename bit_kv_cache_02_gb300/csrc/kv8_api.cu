@@ -143,7 +143,8 @@ int kv8_append(const kv8_cache *cache, const kv8_rows *k, const kv8_rows *v, con
 int64_t kv8_attn_workspace_bytes(const kv8_cache *cache, int32_t num_q_heads, int32_t max_new) {
   if (check_geometry(cache) || max_new < 1 || max_new > cache->capacity || check_heads(cache, num_q_heads, max_new))
     return -1;
-  return static_cast<int64_t>(kv8::plan_attn(cache->head_dim).bytes);
+  const int64_t group = num_q_heads / cache->num_kv_heads;
+  return static_cast<int64_t>(kv8::plan_attn(cache->head_dim, group * max_new).bytes);
 }
 
 int kv8_attn(const kv8_cache *cache, int32_t num_q_heads, const kv8_rows *q, const kv8_rows *out,
@@ -160,7 +161,8 @@ int kv8_attn(const kv8_cache *cache, int32_t num_q_heads, const kv8_rows *q, con
   if ((e = check_rows(out, num_q_heads, rows, cache->head_dim, true))) return e;
   if (q->data == out->data && (q->row_stride != out->row_stride || q->head_stride != out->head_stride))
     return KVQ_ERR_INVALID_ARG;
-  const kv8::AttnPlan plan = kv8::plan_attn(cache->head_dim);
+  const int64_t group = num_q_heads / cache->num_kv_heads;
+  const kv8::AttnPlan plan = kv8::plan_attn(cache->head_dim, group * max_new);
   if (!workspace || workspace_bytes < plan.bytes) return KVQ_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return KVQ_ERR_ALIGNMENT;
   if (!(softmax_scale > 0.f) || !isfinite(softmax_scale))
@@ -168,7 +170,7 @@ int kv8_attn(const kv8_cache *cache, int32_t num_q_heads, const kv8_rows *q, con
   kv8::AttnArgs a;
   a.geo = make_geo(cache);
   a.Hq = num_q_heads;
-  a.group = num_q_heads / cache->num_kv_heads;
+  a.group = static_cast<int>(group);
   a.q = make_rows(q);
   a.out = make_rows(out);
   a.row_start = row_start;
@@ -180,8 +182,12 @@ int kv8_attn(const kv8_cache *cache, int32_t num_q_heads, const kv8_rows *q, con
   a.part_o = reinterpret_cast<float *>(ws);
   a.part_ml = reinterpret_cast<float2 *>(ws + plan.off_ml);
   a.counters = reinterpret_cast<int *>(ws + plan.off_cnt);
+  a.tile_counters = reinterpret_cast<int *>(ws + plan.off_tile_cnt);
+  a.tile_o = reinterpret_cast<float *>(ws + plan.off_tile_o);
+  a.tile_ml = reinterpret_cast<float2 *>(ws + plan.off_tile_ml);
+  a.rows_max = plan.tiles ? kv8::kRowsMax : 2147483647;
   uint64_t n = 0;
-  const cudaError_t ce = kv8::launch_attn(a, static_cast<cudaStream_t>(stream), &n);
+  const cudaError_t ce = kv8::launch_attn(a, plan.tiles, static_cast<cudaStream_t>(stream), &n);
   return from_cuda(ce, n);
 }
 
@@ -189,17 +195,26 @@ int kv8_attn(const kv8_cache *cache, int32_t num_q_heads, const kv8_rows *q, con
 
 namespace kv8 {
 
-AttnPlan plan_attn(int D) {
+AttnPlan plan_attn(int D, long long rows_per_head) {
   AttnPlan p;
+  auto align = [](size_t x) { return (x + 255) / 256 * 256; };
+  p.tiles = rows_per_head > kRowsMax;
   p.off_ml = static_cast<size_t>(2) * kMaxCtas * kRowTile * D * sizeof(float);
-  p.off_cnt = p.off_ml + static_cast<size_t>(2) * kMaxCtas * kRowTile * sizeof(float2);
-  p.bytes = (p.off_cnt + kMaxCtas * sizeof(int) + 255) / 256 * 256;
+  p.off_cnt = align(p.off_ml + static_cast<size_t>(2) * kMaxCtas * kRowTile * sizeof(float2));
+  p.off_tile_cnt = p.off_cnt + align(kMaxCtas * sizeof(int));
+  p.off_tile_o = p.off_tile_cnt + align(kMaxTileCtas * sizeof(int));
+  p.off_tile_ml = p.off_tile_o + static_cast<size_t>(2) * kMaxTileCtas * kTileRows * D * sizeof(float);
+  p.bytes = p.tiles ? align(p.off_tile_ml + static_cast<size_t>(2) * kMaxTileCtas * kTileRows * sizeof(float2))
+                    : p.off_tile_o;
   return p;
 }
 
-cudaError_t launch_attn(const AttnArgs &a, cudaStream_t stream, uint64_t *launches) {
+cudaError_t launch_attn(const AttnArgs &a, bool tiles, cudaStream_t stream, uint64_t *launches) {
   ++*launches;
-  return a.geo.D == 128 ? launch_rows_128(a, stream) : launch_rows_64(a, stream);
+  cudaError_t e = a.geo.D == 128 ? launch_rows_128(a, stream) : launch_rows_64(a, stream);
+  if (e != cudaSuccess || !tiles) return e;
+  ++*launches;
+  return a.geo.D == 128 ? launch_tiles_128(a, stream) : launch_tiles_64(a, stream);
 }
 
 }  // namespace kv8

@@ -98,12 +98,20 @@ cudaError_t launch_append(const Geo &geo, const Rows &k, const Rows &v, const Ro
 constexpr int kMaxCtas = 640;
 constexpr int kRowTile = 16;  // (token, query head) rows that share one pass over the keys
 
-// Byte offsets of the workspace regions: partial outputs [2 kMaxCtas][16][D],
-// their (max, sum), and one merge counter per CTA.
+// Sequences with more rows per KV head than this go to the tile kernel.
+constexpr int kRowsMax = 64;
+constexpr int kTileRows = 256;      // rows of an item of the tile kernel
+constexpr int kMaxTileCtas = 160;
+
+// Byte offsets of the workspace regions.  Rows kernel: partial outputs
+// [2 kMaxCtas][16][D], their (max, sum), one merge counter per CTA.  Tile
+// kernel, where a sequence can bring enough rows: the same for
+// [2 kMaxTileCtas][256].
 struct AttnPlan {
-  size_t off_ml, off_cnt, bytes;
+  size_t off_ml, off_cnt, off_tile_cnt, off_tile_o, off_tile_ml, bytes;
+  bool tiles;
 };
-AttnPlan plan_attn(int D);
+AttnPlan plan_attn(int D, long long rows_per_head);
 
 struct AttnArgs {
   Geo geo;
@@ -115,11 +123,17 @@ struct AttnArgs {
   float *part_o;      // [2 kMaxCtas][16][D] unnormalized partial outputs
   float2 *part_ml;    // [2 kMaxCtas][16] (max, sum) in log2 units
   int *counters;      // [kMaxCtas], zero on entry, left zero on exit
+  float *tile_o;      // [2 kMaxTileCtas][D / 4][256][4] unnormalized partial outputs
+  float2 *tile_ml;    // [2 kMaxTileCtas][256] (reference, sum)
+  int *tile_counters; // [kMaxTileCtas], zero on entry, left zero on exit
+  int rows_max;       // rows per KV head up to which the rows kernel takes a sequence
 };
 
-cudaError_t launch_attn(const AttnArgs &a, cudaStream_t stream, uint64_t *launches);
-// the rows kernel for one head dimension (one translation unit each)
+cudaError_t launch_attn(const AttnArgs &a, bool tiles, cudaStream_t stream, uint64_t *launches);
+// the kernels for one head dimension (one translation unit each)
 cudaError_t launch_rows_128(const AttnArgs &a, cudaStream_t stream);
 cudaError_t launch_rows_64(const AttnArgs &a, cudaStream_t stream);
+cudaError_t launch_tiles_128(const AttnArgs &a, cudaStream_t stream);
+cudaError_t launch_tiles_64(const AttnArgs &a, cudaStream_t stream);
 
 }  // namespace kv8

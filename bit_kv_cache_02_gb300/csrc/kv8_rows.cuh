@@ -162,7 +162,7 @@ __device__ __forceinline__ Work seq_work(const AttnArgs &a, int s) {
   Work w;
   w.q = load_seq(a.geo, a.row_start, a.rows, a.max_new, s);
   const int L = w.q.L;
-  const bool some = w.q.n > 0 && L > 0 && L <= a.max_len;
+  const bool some = w.q.n > 0 && w.q.n * a.group <= a.rows_max && L > 0 && L <= a.max_len;
   const int nb = L / a.geo.B;
   w.full = some ? nb * (a.geo.B / kUnit) : 0;
   w.units = some ? w.full + (L - nb * a.geo.B + kWinUnit - 1) / kWinUnit : 0;
@@ -805,7 +805,8 @@ cudaError_t launch_one(const AttnArgs &a, cudaStream_t stream) {
     }
   }
   // no more CTAs than units for their warps, as far as the host can tell
-  const long long tiles = (static_cast<long long>(a.max_new) * a.group + kRowTile - 1) / kRowTile;
+  const long long most = min(static_cast<long long>(a.max_new) * a.group, static_cast<long long>(a.rows_max));
+  const long long tiles = (most + kRowTile - 1) / kRowTile;
   const long long units = (a.max_len / kUnit + a.geo.B / kWinUnit) * tiles * a.geo.H * a.geo.S;
   long long grid = min(static_cast<long long>(kMaxCtas), static_cast<long long>(sms) * per);
   grid = max(1LL, min(grid, (units + kWarps - 1) / kWarps));

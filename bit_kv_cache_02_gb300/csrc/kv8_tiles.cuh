@@ -1,0 +1,972 @@
+// Attention over the 8-bit paged cache for many rows per sequence (chunks of
+// prompts), on the tcgen05 tensor cores.
+//
+// A work item is 256 rows -- (new token, query head) pairs of one KV head, two
+// tiles of 128 -- against the keys they see, 128 at a time.  Roles of a CTA:
+//
+//   warps 0-3, 4-7   softmax of row tile 0 and 1: one thread per row.  S comes
+//                    from tensor memory, the weights go back there as fp16.
+//   warps 8-11       bring 128 tokens' codes from the blocks (prefetched one
+//                    tile ahead in registers), widen them to fp16 and store them
+//                    in the 128-byte-swizzled layout the tensor core reads:
+//                    tokens as rows for keys (K-major) and values (MN-major).
+//   warp 12          issues the products: S = Q K^T, then O += P V with P in
+//                    tensor memory.  The two row tiles alternate, so one tile's
+//                    softmax runs under the other's products.
+//
+// Mathematics, in log2 units per row: z_t = q.k_t scale_k softmax_scale log2(e),
+// w_t = 2^(z_t + log2(scale_v) - M + 9), O = sum w_t v_code_t, l = sum w_t /
+// scale_v, out = O / l.  Folding scale_v into the exponent lets O accumulate
+// codes of blocks with different scales in tensor memory.  M follows the row's
+// maximum of z + log2(scale_v) lazily: O is rescaled only when it grew by more
+// than 2^6, so w stays below 2^15 and weights down to 2^-23 of the largest
+// keep fp16's full precision.  Roundings: w to fp16; bf16 queries scaled to
+// fp16's range as in the rows kernel; bf16 window tokens scaled token by token
+// (the factors enter z and M like the blocks' scales).
+//
+// The keys of all items form one line of 128-token units which is cut into
+// one equal range per SM; items cut by a border are merged by the last CTA
+// that finishes (fp32 partial O, M and l in the workspace).
+//
+// Bound: the tensor cores (4 D flop per row and key; 128 x 128 x 128 twice per
+// row tile and unit).
+#pragma once
+
+#include <atomic>
+
+#include "kv8_internal.cuh"
+
+namespace kv8 {
+namespace tiles {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kThreads = 512;
+constexpr int kRows = kTileRows;  // 256 rows of an item
+constexpr int kKeys = 128;        // tokens of a unit
+constexpr int kMetas = 4;
+constexpr float kGrow = 6.f;      // how far the maximum may pass M
+constexpr float kShift = 9.f;     // w = 2^(z' - M + kShift) <= 2^15
+
+template <int D>
+struct Smem {
+  static constexpr int HALF = 128 * 128;          // 128 rows of 64 channels in fp16
+  static constexpr int TILE = HALF * (D / 64);    // 128 rows of D channels
+  static constexpr int Q = 0;                     // two row tiles
+  static constexpr int K = Q + 2 * TILE;          // two stages
+  static constexpr int V = K + 2 * TILE;          // two stages
+  static constexpr int META = V + 2 * TILE;       // [kMetas] Meta
+  static constexpr int COL = META + kMetas * 64;  // [kMetas] window columns: scale_k, log2 scale_v, 1 / scale_v
+  static constexpr int BAR = COL + kMetas * 3 * kKeys * 4;
+  static constexpr int MISC = BAR + 16 * 8;
+  static constexpr int BYTES = MISC + 256 + 1024;  // and the alignment of the base
+};
+
+// Scales of a unit's four groups of 32 tokens.  A ring of four: keys are
+// brought at most two units ahead of the products, and a unit's products wait
+// for the softmax of the unit before.
+struct Meta {
+  float k[4], lv[4], inv[4];
+  int flush, pad[3];
+};
+
+enum Bar { kQFull, kKFull, kKEmpty = kKFull + 2, kVFull = kKEmpty + 2, kVEmpty = kVFull + 2, kSFull = kVEmpty + 2,
+           kPFull = kSFull + 2, kOFull = kPFull + 2 };  // 15 barriers
+
+// ------------------------------------------------------------ tcgen05 in PTX
+
+__device__ __forceinline__ void tmem_alloc(uint32_t smem_dst) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_dst) : "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// D[tmem] (+)= A[smem] B[smem]
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] B[smem]
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+      : "memory");
+}
+
+#define KV8_R8(v, i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), "=r"(v[i + 4]), "=r"(v[i + 5]), "=r"(v[i + 6]), "=r"(v[i + 7])
+#define KV8_W8(v, i) "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), "r"(v[i + 6]), "r"(v[i + 7])
+
+// 32 columns of the warp's 32 lanes
+__device__ __forceinline__ void tmem_ld32(uint32_t *v, uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : KV8_R8(v, 0), KV8_R8(v, 8), KV8_R8(v, 16), KV8_R8(v, 24)
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      KV8_W8(v, 0), KV8_W8(v, 8), KV8_W8(v, 16), KV8_W8(v, 24)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          addr),
+      KV8_W8(v, 0), KV8_W8(v, 8)
+      : "memory");
+}
+
+// Shared-memory matrix descriptor, 128-byte swizzle: 8-row groups of 1024
+// bytes follow each other; `lead` is the step between 64-element halves of an
+// MN-major operand (K-major operands do not use it).
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3fff) | (static_cast<uint64_t>(lead >> 4) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+// kind::f16 with fp16 operands and fp32 accumulators, M = 128
+__host__ __device__ constexpr uint32_t instr_desc(int n, bool b_mn_major) {
+  return (1u << 4) | (b_mn_major ? 1u << 16 : 0u) | (static_cast<uint32_t>(n / 8) << 17) | (8u << 24);
+}
+
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// A barrier of `threads` threads that says whether `ok` held for all of them.
+__device__ __forceinline__ bool bar_all(int id, int threads, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.and.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(ok))
+      : "memory");
+  return r != 0;
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+__device__ __forceinline__ void sts16(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ uint64_t pack64(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpack64(uint64_t v, float &x, float &y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Place of 16-byte chunk cc (8 channels) of row `row` in a tile.
+__device__ __forceinline__ uint32_t place(int row, int cc) {
+  return (cc >> 3) * 16384 + row * 128 + (((cc & 7) ^ (row & 7)) << 4);
+}
+
+// ------------------------------------------------------------------- the line
+
+// A (sequence, row tile pair): what its items share.
+struct Pair {
+  Seq q;
+  int s, rt;
+  int last_seen;  // last position that any of its rows sees (at least 0)
+  int stored;     // tokens in complete blocks
+  int packed;     // units of complete blocks
+  int units;      // and one for the window, where seen; 0: not a pair
+};
+
+__device__ __forceinline__ int row_start_of(const AttnArgs &a, int s) {
+  return a.row_start ? max(a.row_start[s], 0) : s;
+}
+
+__device__ __forceinline__ Pair make_pair(const AttnArgs &a, int s, int rt) {
+  Pair p;
+  p.s = s;
+  p.rt = rt;
+  p.q = load_seq(a.geo, a.row_start, a.rows, a.max_new, s);
+  const int L = p.q.L;
+  const int n_rows = p.q.n * a.group;
+  p.units = 0;
+  if (n_rows <= kRowsMax || L <= 0 || L > a.max_len || rt < 0 || rt * kRows >= n_rows) return p;
+  const int last_row = min((rt + 1) * kRows, n_rows) - 1;
+  p.last_seen = max(L - p.q.n + last_row / a.group, 0);
+  p.stored = L / a.geo.B * a.geo.B;
+  p.packed = min(p.last_seen / kKeys + 1, (p.stored + kKeys - 1) / kKeys);
+  p.units = p.packed + (p.last_seen >= p.stored ? 1 : 0);
+  return p;
+}
+
+// Sequence s owns the slots from row_start[s] * group / 256 + s on: at least
+// as many as row tile pairs.
+__device__ __forceinline__ Pair pair_of_slot(const AttnArgs &a, int slot) {
+  auto base = [&](int s) { return static_cast<int>(static_cast<long long>(row_start_of(a, s)) * a.group / kRows) + s; };
+  const int s = last_at_or_below(a.geo.S, slot, base);
+  return make_pair(a, s, slot - base(s));
+}
+
+struct Walk {
+  Pair p;
+  int h, u0, u1;           // KV head and units of the current part
+  long long at, end;       // line position, end of the CTA's range
+  long long start;         // line position of the item's unit 0
+
+  __device__ __forceinline__ void part() {
+    u1 = static_cast<int>(min(static_cast<long long>(p.units), u0 + (end - at)));
+    start = at - u0;
+  }
+  __device__ __forceinline__ bool next(const AttnArgs &a) {
+    at += u1 - u0;
+    if (at >= end) return false;
+    u0 = 0;
+    if (++h >= a.geo.H) {
+      h = 0;
+      int s = p.s, rt = p.rt + 1;
+      for (;;) {
+        p = make_pair(a, s, rt);
+        if (p.units) break;
+        rt = 0;
+        if (++s >= a.geo.S) return false;
+      }
+    }
+    part();
+    return true;
+  }
+  __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == p.units; }
+};
+
+// Sum over the CTA, and each thread's exclusive prefix.
+__device__ __forceinline__ long long cta_scan(long long v, long long &before, long long *buf) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(kAll, incl, o);
+    if (lane >= o) incl += x;
+  }
+  __syncthreads();
+  if (lane == 31) buf[warp] = incl;
+  __syncthreads();
+  long long total = 0;
+  before = incl - v;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += buf[w];
+    total += buf[w];
+  }
+  return total;
+}
+
+// --------------------------------------------------------------- code widening
+
+template <int FMT>
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  if (FMT == KV8_INT8) {
+    const uint32_t u = w ^ 0x80808080u;
+    uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 off = __floats2half2_rn(1152.f, 1152.f);
+    lo = kvq::h2_as_u32(__hsub2(*reinterpret_cast<__half2 *>(&a), off));
+    hi = kvq::h2_as_u32(__hsub2(*reinterpret_cast<__half2 *>(&b), off));
+  } else {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+  }
+}
+
+template <int D, int FMT, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
+  using SM = Smem<D>;
+  extern __shared__ unsigned char raw[];
+  unsigned char *smem = raw + ((1024 - (kvq::smem_u32(raw) & 1023)) & 1023);
+  const uint32_t base = kvq::smem_u32(smem);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + SM::BAR);
+  volatile int *dead = reinterpret_cast<volatile int *>(smem + SM::MISC);       // a wait gave up
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + SM::MISC + 8);
+  int *flag = reinterpret_cast<int *>(smem + SM::MISC + 16);
+  long long *found = reinterpret_cast<long long *>(smem + SM::MISC + 32);       // [2]
+  long long *scan_buf = reinterpret_cast<long long *>(smem + SM::MISC + 64);    // [16]
+  const Geo &geo = a.geo;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int B = geo.B, H = geo.H;
+  const float ninf = __int_as_float(0xff800000), nan = __int_as_float(0x7fc00000);
+
+  // ---- this CTA's range of the line
+  long long total = 0;
+  const int slots = static_cast<int>(static_cast<long long>(a.row_start ? min(max(a.row_start[geo.S], 0), a.rows)
+                                                                        : geo.S) * a.group / kRows) + geo.S;
+  Pair mine;
+  {
+    // the slots below need row_start to rise
+    bool falls = false;
+    if (a.row_start)
+      for (int s = tid; s < geo.S; s += kThreads)
+        falls |= a.row_start[s] < 0 || a.row_start[s + 1] < a.row_start[s] || a.row_start[s + 1] > a.rows;
+    if (__syncthreads_or(falls)) return;  // the rows kernel has set the status
+    long long sum = 0;
+    for (int i = tid; i < slots; i += kThreads) {
+      mine = pair_of_slot(a, i);
+      sum += static_cast<long long>(mine.units) * H;
+    }
+    long long before;
+    total = cta_scan(sum, before, scan_buf);
+  }
+  if (total == 0) return;
+  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + 3) / 4));
+  if (static_cast<int>(blockIdx.x) >= ctas) return;
+  const long long lo = blockIdx.x * total / ctas, hi = (blockIdx.x + 1) * total / ctas;
+  {
+    long long at = 0;
+    for (int i0 = 0; i0 < slots; i0 += kThreads) {
+      if (i0 + tid < slots && slots > kThreads) mine = pair_of_slot(a, i0 + tid);
+      const long long u = i0 + tid < slots ? static_cast<long long>(mine.units) * H : 0;
+      long long before;
+      const long long sum = cta_scan(u, before, scan_buf);
+      if (lo >= at + before && lo < at + before + u) {
+        found[0] = i0 + tid;
+        found[1] = lo - (at + before);
+      }
+      at += sum;
+      if (lo < at) break;
+    }
+  }
+  if (tid == 0) {
+    *dead = 0;
+    kvq::mbar_init(bars + kQFull, 256);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      kvq::mbar_init(bars + kKFull + i, 128);
+      kvq::mbar_init(bars + kKEmpty + i, 1);
+      kvq::mbar_init(bars + kVFull + i, 128);
+      kvq::mbar_init(bars + kVEmpty + i, 1);
+      kvq::mbar_init(bars + kSFull + i, 1);
+      kvq::mbar_init(bars + kPFull + i, 128);
+      kvq::mbar_init(bars + kOFull + i, 1);
+    }
+    kvq::fence_mbar_init();
+  }
+  if (warp == 12) {
+    tmem_alloc(kvq::smem_u32(tmem_slot));
+    tmem_relinquish();
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  Walk use;
+  {
+    use.p = pair_of_slot(a, static_cast<int>(found[0]));
+    const long long in = found[1];
+    use.h = static_cast<int>(in / use.p.units);
+    use.u0 = static_cast<int>(in - static_cast<long long>(use.h) * use.p.units);
+    use.at = lo;
+    use.end = hi;
+    use.part();
+  }
+  // A wait of a role; false ends the role (another one's wait ran out, or this).
+  auto wait = [&](int bar, uint32_t parity) -> bool {
+    if (kvq::mbar_try_wait(bars + bar, parity)) return true;
+    const long long since = clock64();
+    while (!kvq::mbar_try_wait_hint(bars + bar, parity, 100000u)) {
+      if (*dead) return false;
+      if (clock64() - since > kvq::kWaitLimitCycles) {
+        *dead = 1;
+        set_status(geo.status, KVQ_STATUS_TIMEOUT);
+        return false;
+      }
+    }
+    return true;
+  };
+
+  if (warp >= 12) {
+    // =================================================== the products
+    // 2 x 184 + 96 + 48 = 4 x 128, what the CTA was launched with
+    regs_dec<48>();
+    if (warp == 12 && lane == 0) {
+      constexpr uint32_t id_qk = instr_desc(kKeys, false), id_pv = instr_desc(D, true);
+      uint32_t n_unit = 0, n_part = 0;  // units and parts issued so far
+      uint32_t np[2] = {0, 0};          // weights consumed, per row tile
+      auto qk = [&](int t, uint32_t unit) {
+        const uint32_t q = base + SM::Q + t * SM::TILE, k = base + SM::K + (unit & 1) * SM::TILE;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const uint32_t off = (i >> 2) * SM::HALF + (i & 3) * 32;
+          mma_ss(tmem + t * 128, smem_desc(q + off, 16), smem_desc(k + off, 16), id_qk, i != 0);
+        }
+        commit(base + SM::BAR + (kSFull + t) * 8);
+      };
+      auto pv = [&](int t, uint32_t unit, bool add) {
+        const uint32_t v = base + SM::V + (unit & 1) * SM::TILE;
+#pragma unroll
+        for (int i = 0; i < kKeys / 16; ++i)
+          mma_ts(tmem + 256 + t * 128, tmem + t * 128 + i * 8, smem_desc(v + i * 2048, SM::HALF), id_pv, add || i != 0);
+        commit(base + SM::BAR + (kOFull + t) * 8);
+      };
+      bool ok = true;
+      do {
+        const int tiles = use.p.q.n * a.group - use.p.rt * kRows > 128 ? 2 : 1;
+        const int units = use.u1 - use.u0;
+        ok = wait(kQFull, n_part & 1) && wait(kKFull + (n_unit & 1), (n_unit >> 1) & 1);
+        if (!ok) break;
+        fence_after();
+        for (int t = 0; t < tiles; ++t) qk(t, n_unit);
+        commit(base + SM::BAR + (kKEmpty + (n_unit & 1)) * 8);
+        for (int u = 0; u < units && ok; ++u, ++n_unit) {
+          ok = wait(kVFull + (n_unit & 1), (n_unit >> 1) & 1);
+          if (ok && u + 1 < units) ok = wait(kKFull + ((n_unit + 1) & 1), ((n_unit + 1) >> 1) & 1);
+          for (int t = 0; t < tiles && ok; ++t) {
+            ok = wait(kPFull + t, np[t] & 1);
+            if (!ok) break;
+            ++np[t];
+            fence_after();
+            pv(t, n_unit, u != 0);
+            if (u + 1 < units) qk(t, n_unit + 1);
+          }
+          if (!ok) break;
+          commit(base + SM::BAR + (kVEmpty + (n_unit & 1)) * 8);
+          if (u + 1 < units) commit(base + SM::BAR + (kKEmpty + ((n_unit + 1) & 1)) * 8);
+        }
+        ++n_part;
+      } while (ok && use.next(a));
+    }
+  } else if (warp >= 8) {
+    // =================================================== keys and values
+    regs_dec<96>();
+    const int ct = tid - 256;                  // 0 .. 127
+    constexpr int CPR = D / 16;                // 16-code chunks of a token
+    constexpr int RPI = 128 / CPR;             // tokens per instruction: 16 or 32
+    constexpr int NI = 128 / RPI;              // instructions per unit
+    const int cr = ct / CPR, cc = ct % CPR;
+    const int shift = 31 - __clz(B);           // block = 1 << shift
+    uint4 kb[NI], vb[NI];
+    int ent[4], ahead[4];               // table entries of the unit to fetch, and of the one behind it
+    float2 sc = make_float2(1.f, 1.f);  // scales of group ct, for ct < 4
+    uint32_t n_unit = 0;
+    bool ok = true;
+    Walk &get = use;  // the part and the unit whose codes are fetched next
+    int gu = get.u0;
+
+    // table entries of unit u of the part; -1: a bad one, -2: nothing there
+    auto entries = [&](int *e, int u) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        e[i] = -2;
+        const int tok = u * kKeys + i * 32;
+        if (u < min(get.p.packed, get.u1) && tok < get.p.stored)
+          e[i] = geo.table[static_cast<size_t>(get.p.s) * geo.max_blocks + (tok >> shift)];
+      }
+    };
+    auto good = [&](int e) { return e >= 0 && e < geo.num_blocks; };
+    auto load = [&](uint4 *buf, bool values) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        buf[i] = make_uint4(0u, 0u, 0u, 0u);
+        const int row = i * RPI + cr, e = ent[i * RPI / 32];
+        if (good(e)) {
+          const size_t off = (((static_cast<size_t>(e) * H + get.h) * 2 + (values ? 1 : 0)) * B +
+                              ((gu * kKeys + row) & (B - 1))) * D + cc * 16;
+          buf[i] = __ldg(reinterpret_cast<const uint4 *>(geo.codes + off));
+        }
+      }
+    };
+    auto load_scales = [&]() {
+      sc = make_float2(1.f, 1.f);
+      if (ct < 4) {
+        int e = ent[0];
+#pragma unroll
+        for (int i = 1; i < 4; ++i)
+          if (ct == i) e = ent[i];
+        if (good(e)) {
+          sc = *reinterpret_cast<const float2 *>(geo.scales + (static_cast<size_t>(e) * H + get.h) * 2);
+        } else if (e != -2) {
+          sc = make_float2(nan, nan);
+          set_status(geo.status, KVQ_STATUS_BAD_BLOCK);
+        }
+      }
+    };
+    // `flush`: groups of 32 tokens whose values are stored as zeros
+    auto store = [&](uint32_t dst, const uint4 *buf, int flush) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int row = i * RPI + cr;
+        uint4 x = buf[i];
+        if (flush >> (i * RPI / 32) & 1) x = make_uint4(0u, 0u, 0u, 0u);
+        uint32_t e[8];
+        widen4<FMT>(x.x, e[0], e[1]);
+        widen4<FMT>(x.y, e[2], e[3]);
+        widen4<FMT>(x.z, e[4], e[5]);
+        widen4<FMT>(x.w, e[6], e[7]);
+        // the two chunks in an order that keeps eight threads' stores in eight banks groups
+        const bool swap = D == 128 && cc >= 4;
+        const uint32_t a0 = dst + place(row, 2 * cc), a1 = dst + place(row, 2 * cc + 1);
+        sts16(swap ? a1 : a0, swap ? e[4] : e[0], swap ? e[5] : e[1], swap ? e[6] : e[2], swap ? e[7] : e[3]);
+        sts16(swap ? a0 : a1, swap ? e[0] : e[4], swap ? e[1] : e[5], swap ? e[2] : e[6], swap ? e[3] : e[7]);
+      }
+    };
+    // One window token (thread ct's) of keys or values: what scales it.
+    auto window_row = [&](const uint16_t *src, bool valid, float &f, bool &bad) {
+      uint32_t big = 0;
+      bad = false;
+      f = 1.f;
+      if (!valid) return;
+#pragma unroll 4
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(src + 8 * c);
+        const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t lo16 = e[i] & 0x7fffu, hi16 = (e[i] >> 16) & 0x7fffu;
+          if (lo16 >= nonfinite_bits<BF16>() || hi16 >= nonfinite_bits<BF16>()) bad = true;
+          big = max(big, lo16 < nonfinite_bits<BF16>() ? lo16 : 0u);
+          big = max(big, hi16 < nonfinite_bits<BF16>() ? hi16 : 0u);
+        }
+      }
+      // a power of two that brings the largest element to [2^14, 2^15)
+      if (BF16 && big) f = __int_as_float((268 - max(static_cast<int>(big >> 7), 20)) << 23);
+    };
+    auto store_window = [&](uint32_t dst, const uint16_t *src, bool zero, float f) {
+#pragma unroll 4
+      for (int c = 0; c < D / 8; ++c) {
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (!zero) x = *reinterpret_cast<const uint4 *>(src + 8 * c);
+        if (BF16) {
+          uint32_t *e = &x.x;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 y = unpack2<true>(e[i]);
+            e[i] = kvq::h2_as_u32(__floats2half2_rn(y.x * f, y.y * f));
+          }
+        }
+        sts16(dst + place(ct, c), x.x, x.y, x.z, x.w);
+      }
+    };
+
+    entries(ent, gu);
+    entries(ahead, gu + 1);
+    load_scales();
+    load(kb, false);
+    load(vb, true);
+    for (bool more = true; more;) {
+      const int st = n_unit & 1;
+      const uint32_t reuse = ((n_unit >> 1) & 1) ^ 1;  // the stage's previous user must be done
+      const uint32_t kd = base + SM::K + st * SM::TILE, vd = base + SM::V + st * SM::TILE;
+      Meta *meta = reinterpret_cast<Meta *>(smem + SM::META) + n_unit % kMetas;
+      const bool window = gu >= get.p.packed;
+      const size_t win = ((static_cast<size_t>(get.p.s) * H + get.h) * B + ct) * D;
+      const bool wvalid = window && ct < get.p.q.L - get.p.stored;
+      float vf = 1.f;
+      bool vbad = false;
+      if (n_unit >= 2) ok = wait(kKEmpty + st, reuse);
+      if (!bar_all(1, 128, ok)) break;
+      if (!window) {
+        store(kd, kb, 0);
+        if (ct < 4) {
+          const bool bad = !(fabsf(sc.x) < __int_as_float(0x7f800000) && fabsf(sc.y) < __int_as_float(0x7f800000));
+          // values of magnitude 2^-100 or less (the scale's floor): zeros, of any scale
+          const bool flush = !bad && sc.y < 8.8e-33f;
+          meta->k[ct] = bad ? 1.f : sc.x;
+          meta->lv[ct] = bad ? nan : flush ? 0.f : log2f(sc.y);
+          meta->inv[ct] = bad || flush ? 1.f : 1.f / sc.y;
+          const unsigned bits = __ballot_sync(0xfu, flush);
+          if (ct == 0) meta->flush = static_cast<int>(bits);
+        }
+      } else {
+        float *col = reinterpret_cast<float *>(smem + SM::COL) + (n_unit % kMetas) * 3 * kKeys + ct;
+        float kf;
+        bool kbad;
+        window_row(geo.k_win + win, wvalid, kf, kbad);
+        window_row(geo.v_win + win, wvalid, vf, vbad);
+        store_window(kd, geo.k_win + win, !wvalid, kf);
+        col[0] = 1.f / kf;
+        // tokens that are not finite turn the rows that see them to NaN
+        col[kKeys] = kbad || vbad ? nan : -log2f(vf);
+        col[2 * kKeys] = kbad || vbad ? 1.f : vf;
+      }
+      kvq::fence_proxy_async();
+      kvq::mbar_arrive(bars + kKFull + st);
+      // the next unit's keys
+      if (++gu < get.u1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ent[i] = ahead[i];
+      } else {
+        more = get.next(a);
+        gu = get.u0;
+        if (more) {
+          entries(ent, gu);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) ent[i] = -2;
+        }
+      }
+      load(kb, false);
+      if (n_unit >= 2) ok = wait(kVEmpty + st, reuse);
+      if (!bar_all(1, 128, ok)) break;  // also: the groups to flush are known to all
+      if (!window)
+        store(vd, vb, meta->flush);
+      else
+        store_window(vd, geo.v_win + win, !wvalid || vbad, vf);
+      kvq::fence_proxy_async();
+      kvq::mbar_arrive(bars + kVFull + st);
+      load(vb, true);
+      load_scales();
+      if (more) entries(ahead, gu + 1);
+      ++n_unit;
+    }
+  } else {
+    // =================================================== softmax
+    regs_inc<184>();
+    const int t = warp >> 2;         // row tile
+    const int r = tid & 127;         // row of the tile = lane of tensor memory
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21);
+    const uint32_t s_at = lanes + t * 128, o_at = lanes + 256 + t * 128;
+    const Meta *metas = reinterpret_cast<const Meta *>(smem + SM::META);
+    uint32_t n_unit = 0;  // units so far
+    uint32_t n_own = 0;   // units of this row tile so far
+    bool ok = true;
+    do {
+      const Pair &p = use.p;
+      const int n_rows = p.q.n * a.group;
+      const int row = p.rt * kRows + t * 128 + r;
+      const bool active = n_rows - p.rt * kRows > t * 128;  // the tile has rows
+      const bool valid = row < n_rows;
+      const int tok = valid ? row / a.group : 0;
+      const int lim = valid ? p.q.L - p.q.n + tok : -1;  // last position the row sees
+      const long long q_row = static_cast<long long>(p.q.row0) + tok;
+      const long long q_head = static_cast<long long>(use.h) * a.group + (valid ? row - tok * a.group : 0);
+      // every row of the tile sees at least the tokens up to here
+      const int seen_by_all = p.q.L - p.q.n + (p.rt * kRows + t * 128) / a.group;
+
+      // ---- the row's query to shared memory
+      float qf = a.zscale;
+      if (active) {
+        const uint16_t *src = a.q.p + q_row * a.q.row + q_head * a.q.head;
+        const uint32_t dst = base + SM::Q + t * SM::TILE;
+        float f = 1.f;
+        if (BF16 && valid) {
+          uint32_t big = 0;
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(src + 8 * c);
+            const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t l16 = e[i] & 0x7fffu, h16 = (e[i] >> 16) & 0x7fffu;
+              big = max(big, l16 < 0x7f80u ? l16 : 0u);
+              big = max(big, h16 < 0x7f80u ? h16 : 0u);
+            }
+          }
+          const int e = max(static_cast<int>(big >> 7), 20);
+          f = __int_as_float((268 - e) << 23);
+          qf *= __int_as_float((e - 14) << 23);
+        }
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          uint4 x = make_uint4(0u, 0u, 0u, 0u);
+          if (valid) x = *reinterpret_cast<const uint4 *>(src + 8 * c);
+          if (BF16) {
+            uint32_t *e = &x.x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 y = unpack2<true>(e[i]);
+              e[i] = kvq::h2_as_u32(__floats2half2_rn(y.x * f, y.y * f));
+            }
+          }
+          sts16(dst + place(r, c), x.x, x.y, x.z, x.w);
+        }
+        kvq::fence_proxy_async();
+      }
+      fence_before();
+      kvq::mbar_arrive(bars + kQFull);
+
+      float M = ninf, l = 0.f;
+      if (active) {
+        for (int u = use.u0; u < use.u1; ++u, ++n_unit, ++n_own) {
+          ok = wait(kSFull + t, n_own & 1);
+          if (!__all_sync(kAll, ok)) {
+            ok = false;
+            break;
+          }
+          fence_after();
+          uint32_t sr[128];
+          float *s = reinterpret_cast<float *>(sr);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(sr + 32 * c, s_at + 32 * c);
+          wait_ld();
+          const bool window = u >= p.packed;
+          const int t0 = window ? p.stored : u * kKeys;
+          const int here = min(kKeys, window ? p.q.L - p.stored : p.stored - t0);  // tokens of the unit
+          const Meta &meta = metas[n_unit % kMetas];
+          const float *col_k = reinterpret_cast<const float *>(smem + SM::COL) + (n_unit % kMetas) * 3 * kKeys,
+                      *col_lv = col_k + kKeys, *col_inv = col_lv + kKeys;
+          const bool edge = window || here < kKeys || t0 + kKeys - 1 > seen_by_all;
+          float mx = ninf;
+          float ka[4], kl[4];
+          if (!edge) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              ka[c] = meta.k[c] * qf;
+              kl[c] = meta.lv[c];
+              float m0 = s[32 * c], m1 = s[32 * c + 1];
+#pragma unroll
+              for (int i = 2; i < 32; i += 2) {
+                m0 = fmaxf(m0, s[32 * c + i]);
+                m1 = fmaxf(m1, s[32 * c + i + 1]);
+              }
+              mx = fmaxf(mx, fmaf(fmaxf(m0, m1), ka[c], kl[c]));
+            }
+          } else {
+            const int cmax = min(here, lim - t0 + 1);  // columns below it are seen
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              ka[c] = 1.f;
+              kl[c] = 0.f;
+              const float k = window ? 0.f : meta.k[c] * qf, lv = window ? 0.f : meta.lv[c];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const int col = 32 * c + i;
+                float z;
+                if (window) {
+                  z = s[col] * (col_k[col] * qf) + col_lv[col];
+                  z += z - z;  // an infinite score becomes NaN
+                } else {
+                  z = fmaf(s[col], k, lv);
+                }
+                z = col < cmax ? z : ninf;
+                s[col] = z;
+                mx = fmaxf(mx, z);
+              }
+            }
+          }
+          // ---- the reference M, and O where it moved
+          const bool move = mx > M + kGrow || (M == ninf && mx > ninf);
+          if (__any_sync(kAll, move)) {
+            const float to = move ? mx : M;
+            const float f = M == ninf ? (move ? 0.f : 1.f) : kvq::fast_exp2(M - to);
+            M = to;
+            l *= f;
+            if (u > use.u0) {
+              ok = wait(kOFull + t, (n_own - 1) & 1);
+              if (!__all_sync(kAll, ok)) {
+                ok = false;
+                break;
+              }
+              fence_after();
+#pragma unroll
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t o[16];
+                asm volatile(
+                    "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, "
+                    "[%16];"
+                    : KV8_R8(o, 0), KV8_R8(o, 8)
+                    : "r"(o_at + 16 * c)
+                    : "memory");
+                wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st16(o_at + 16 * c, o);
+              }
+            }
+          }
+          const float ref = M == ninf ? 0.f : M - kShift;
+          // ---- weights
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float bias = kl[c] - ref;
+            const uint64_t a2 = pack64(ka[c], ka[c]), b2 = pack64(bias, bias);
+            uint64_t sum = pack64(0.f, 0.f);
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              float x, y;
+              unpack64(fma2(pack64(s[32 * c + i], s[32 * c + i + 1]), a2, b2), x, y);
+              x = kvq::fast_exp2(x);
+              y = kvq::fast_exp2(y);
+              if (window) {
+                l = fmaf(x, col_inv[32 * c + i], l);
+                l = fmaf(y, col_inv[32 * c + i + 1], l);
+              } else {
+                sum = add2(sum, pack64(x, y));
+              }
+              pk[i / 2] = kvq::h2_as_u32(__floats2half2_rn(x, y));
+            }
+            if (!window) {
+              float x, y;
+              unpack64(sum, x, y);
+              l = fmaf(x + y, meta.inv[c], l);
+            }
+            tmem_st16(s_at + 16 * c, pk);
+          }
+          wait_st();
+          fence_before();
+          kvq::mbar_arrive(bars + kPFull + t);
+        }
+      } else {
+        n_unit += use.u1 - use.u0;
+      }
+
+      // ---- the part's result
+      const bool whole = use.whole();
+      const int slot = 2 * blockIdx.x + (use.start + use.u0 == lo ? 0 : 1);
+      float4 *part = reinterpret_cast<float4 *>(a.tile_o) + static_cast<size_t>(slot) * (D / 4) * kRows + t * 128 + r;
+      uint16_t *dst = a.out.p + q_row * a.out.row + q_head * a.out.head;
+      if (active && ok) ok = __all_sync(kAll, wait(kOFull + t, (n_own - 1) & 1));
+      if (active && ok) {
+        fence_after();
+        const float inv = 1.f / l;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(o, o_at + 32 * c);
+          wait_ld();
+          if (whole) {
+            if (valid) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const float x = __uint_as_float(o[i + 2 * k]), y = __uint_as_float(o[i + 2 * k + 1]);
+                  w[k] = l == 0.f ? 0u : pack2<BF16>(x * inv, y * inv);
+                }
+                *reinterpret_cast<uint4 *>(dst + 32 * c + i) = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              part[static_cast<size_t>(8 * c + i / 4) * kRows] =
+                  make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]),
+                              __uint_as_float(o[i + 3]));
+          }
+        }
+        if (!whole) a.tile_ml[slot * kRows + t * 128 + r] = make_float2(M, l);
+        fence_before();
+      }
+      if (!whole) {
+        const long long s0 = use.start, s1 = s0 + p.units;
+        auto owner = [&](long long pos) { return static_cast<int>(((pos + 1) * ctas - 1) / total); };
+        const int c0 = owner(s0), c1 = owner(s1 - 1);
+        __threadfence();
+        ok = bar_all(2, 256, ok);
+        if (!ok) break;
+        if (tid == 0) {
+          const bool last = kvq::atom_add_acq_rel(a.tile_counters + c0, 1) == c1 - c0;
+          if (last) a.tile_counters[c0] = 0;
+          *flag = last;
+        }
+        bar_sync(2, 256);
+        const bool merge = *flag;
+        bar_sync(2, 256);  // read before it is set again
+        if (merge && valid) {
+          __threadfence();
+          const int first = 2 * c0 + (c0 * total / ctas < s0 ? 1 : 0), parts = c1 - c0 + 1;
+          auto slot_of = [&](int i) { return i == 0 ? first : 2 * (c0 + i); };
+          float mm = ninf, ll = 0.f;
+          for (int i = 0; i < parts; ++i) mm = fmaxf(mm, __ldcg(&a.tile_ml[slot_of(i) * kRows + t * 128 + r]).x);
+          const float ref = mm == ninf ? 0.f : mm;
+          for (int i = 0; i < parts; ++i) {
+            const float2 e = __ldcg(&a.tile_ml[slot_of(i) * kRows + t * 128 + r]);
+            ll += e.y * kvq::fast_exp2(e.x - ref);
+          }
+          const float inv = ll == 0.f ? 0.f : 1.f / ll;
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            float o[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = 0.f;
+            for (int i = 0; i < parts; ++i) {
+              const int sl = slot_of(i);
+              const float f = kvq::fast_exp2(__ldcg(&a.tile_ml[sl * kRows + t * 128 + r]).x - ref) * inv;
+              const float4 *src = reinterpret_cast<const float4 *>(a.tile_o) +
+                                  (static_cast<size_t>(sl) * (D / 4) + 4 * c) * kRows + t * 128 + r;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float4 x = __ldcg(src + static_cast<size_t>(k) * kRows);
+                o[4 * k] += x.x * f;
+                o[4 * k + 1] += x.y * f;
+                o[4 * k + 2] += x.z * f;
+                o[4 * k + 3] += x.w * f;
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < 16; k += 8)
+              *reinterpret_cast<uint4 *>(dst + 16 * c + k) =
+                  make_uint4(pack2<BF16>(o[k], o[k + 1]), pack2<BF16>(o[k + 2], o[k + 3]),
+                             pack2<BF16>(o[k + 4], o[k + 5]), pack2<BF16>(o[k + 6], o[k + 7]));
+          }
+        }
+      }
+      // all softmax warps leave together
+      if (whole) ok = bar_all(2, 256, ok);
+    } while (ok && use.next(a));
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    fence_after();
+    tmem_free(tmem);
+  }
+}
+
+template <int D, int FMT, bool BF16>
+cudaError_t launch_one(const AttnArgs &a, cudaStream_t stream) {
+  auto kernel = tiles_kernel<D, FMT, BF16>;
+  static std::atomic<int> sm_count[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int sms = dev < 64 ? sm_count[dev].load() : 0;
+  if (sms == 0) {
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::BYTES)) != cudaSuccess)
+      return e;
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    if (dev < 64) sm_count[dev].store(sms);
+  }
+  kernel<<<min(sms, kMaxTileCtas), kThreads, Smem<D>::BYTES, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_dim(const AttnArgs &a, cudaStream_t stream) {
+  if (a.geo.fmt == KV8_INT8)
+    return a.geo.bf16 ? launch_one<D, KV8_INT8, true>(a, stream) : launch_one<D, KV8_INT8, false>(a, stream);
+  return a.geo.bf16 ? launch_one<D, KV8_E4M3, true>(a, stream) : launch_one<D, KV8_E4M3, false>(a, stream);
+}
+
+}  // namespace tiles
+}  // namespace kv8

@@ -134,7 +134,7 @@ def _rows(t, cache, name):
     if t.dtype != cache.dtype or t.dim() != 3 or t.get_device() != cache.device_index:
         raise ValueError(f"{name}: a {cache.dtype} tensor [rows][heads][{cache.head_dim}] on {cache.device} is needed")
     row, head, one = t.stride()
-    if one != 1 or t.shape[2] != cache.head_dim:
+    if (one != 1 and t.shape[0]) or t.shape[2] != cache.head_dim:  # no rows: any strides
         raise ValueError(f"{name}: heads of {cache.head_dim} contiguous elements are needed")
     return _pack_rows(t.data_ptr(), row, head)
 

@@ -116,18 +116,23 @@ class OracleKV8:
         """q [rows, Hq, D] -> (out, bound): float64 attention, and what the
         kernels' roundings may change it by before the output's own rounding.
 
-        The bound: 2^15 times a weight (of the largest, which is 1 or less) is
-        rounded to fp16: 2^-11 of itself, or 2^-25 in fp16's subnormals, which
-        is 2^-40 of a largest weight and matters where the tokens of large
-        weight have zeros in a channel; so 2^-40 sum_p |v_p|.  Its score is a
-        sum of D products accumulated in fp32 (at most (D + 16) 2^-24 of the
-        sum of magnitudes, the weight's relative change being e^x - 1 < 2 x),
-        the normalizer is a sum of fp32 numbers (2^-24 of itself per term),
+        The bound.  A weight is rounded to fp16: 2^-11 of itself, or half a
+        step of fp16's subnormals, 2^-25.  The kernels form weights as 2^15 w,
+        or as w scale_v / (the largest of those so far, up to 2^6 more) * 2^9:
+        at least 2^9 of the largest, so the subnormals' part is at most 2^-34
+        of the largest weighted value for each token, 2^-34 seen max|v| in
+        all.  (It matters where the tokens of large weight have zeros in a
+        channel.)  A score is a sum of D products accumulated in fp32 (at most
+        (D + 16) 2^-24 of the sum of magnitudes, the weight's relative change
+        being e^x - 1 < 2 x); adding log2(scale_v) and the reference, both
+        below 128 but for the score, rounds four times at 2^-24 * 128: 2^-15.
+        The normalizer is a sum of fp32 numbers (2^-24 of itself per term),
         and sums over tokens and partial results are of fp32 too.  All but the
         subnormals' part is relative to sum_p w_p |v_p|.  A bf16 query is
         scaled by a power of two so that its largest element lies in
         [2^14, 2^15) and rounded to fp16: elements that become subnormal are
-        off by 2^-25, 2^-39 of the largest."""
+        off by 2^-25, 2^-39 of the largest; so are the elements of a window
+        token, of that token's largest."""
         scale = softmax_scale or 1 / math.sqrt(self.D)
         rows, Hq, _ = q.shape
         g = Hq // self.H
@@ -157,6 +162,7 @@ class OracleKV8:
                         dz = (self.D + 16) * 2.0 ** -24 * mags.max()
                         if self.dtype == "bfloat16":
                             dz += 2.0 ** -39 * np.abs(x).max() * np.abs(K[:seen]).sum(1).max() * scale
-                        rel = 2.0 ** -11 + 2 * dz + (2 * seen + 64) * 2.0 ** -24
-                        bound[a + i, j] = rel * (w @ np.abs(V[:seen])) + 2.0 ** -40 * np.abs(V[:seen]).sum(0)
+                            dz += 2.0 ** -39 * np.abs(K[:seen]).max() * np.abs(x).sum() * scale
+                        rel = 2.0 ** -11 + 2.0 ** -15 + 2 * dz + (2 * seen + 64) * 2.0 ** -24
+                        bound[a + i, j] = rel * (w @ np.abs(V[:seen])) + 2.0 ** -34 * seen * np.abs(V[:seen]).max()
         return out, bound

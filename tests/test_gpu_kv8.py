@@ -284,12 +284,43 @@ def test_several_tokens(kv8, fmt, dtype, D, g, new):
 
 
 @pytest.mark.parametrize("fmt,dtype", TYPES)
+@pytest.mark.parametrize("D,B,g", [(128, 32, 4), (128, 64, 1), (128, 128, 2), (64, 32, 1), (64, 64, 5), (64, 128, 3)])
+def test_chunks(kv8, fmt, dtype, D, B, g):
+    """Chunks of more rows than the rows kernel takes: one and two row tiles,
+    prefixes of none to many units, partly filled last blocks and windows."""
+    r = Run(kv8, 6, 2, g, D, B, fmt, dtype, 700, seed=8)
+    r.append([0, 1, B, 130, 400, 299])
+    r.append([70, 129, 65 + B, 257, 128, 300])
+    r.check_state()
+    r.attend()
+
+
+def test_chunk_layouts(kv8):
+    """Query groups that do not divide the row tiles, many items for few CTAs
+    and few items for many."""
+    for H, g, ctx, new in ((1, 17, [40, 0, 300], [60, 5, 100]), (9, 1, [0] * 3, [129, 70, 200]),
+                           (1, 1, [5000], [90]), (1, 3, [0, 0, 0, 0], [300, 0, 100, 1])):
+        r = Run(kv8, len(ctx), H, g, 128, 64, "int8", "bfloat16", 6000, seed=g)
+        r.append(ctx)
+        r.append(new)
+        ws = kv8.alloc_workspace(r.cache, H * g, max(new))
+        a = r.attend(ws=ws)
+        assert torch.equal(a, r.attend(ws=ws, check=False)), "a repeated call gave another result"
+
+
+@pytest.mark.parametrize("fmt,dtype", TYPES)
 def test_rows_without_keys_get_zeros(kv8, fmt, dtype):
-    """More rows than tokens, and sequences without a token."""
-    r = Run(kv8, 3, 1, 2, 64, 32, fmt, dtype, 100)
+    """More rows than tokens, and sequences without a token; with more query
+    heads the same rows take the other kernel."""
+    for g in (2, 9):
+        _rows_without_keys(kv8, fmt, dtype, g)
+
+
+def _rows_without_keys(kv8, fmt, dtype, g):
+    r = Run(kv8, 3, 1, g, 64, 32, fmt, dtype, 100)
     r.append([5, 0, 40])
     start = np.array([0, 9, 12, 60], np.int32)
-    q = r.numbers((60, 2, 64))
+    q = r.numbers((60, g, 64))
     out = _host(r.attend(start, q))
     assert (out[0:4] == 0).all() and (out[9:12] == 0).all() and (out[12:20] == 0).all()
     assert (out[4] != 0).any() and (out[20] != 0).any()
@@ -298,7 +329,8 @@ def test_rows_without_keys_get_zeros(kv8, fmt, dtype):
 @pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
 @pytest.mark.parametrize("where", ["window", "block"])
 @pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
-def test_nonfinite_tokens(kv8, dtype, where, value):
+@pytest.mark.parametrize("g", [1, 3])
+def test_nonfinite_tokens(kv8, dtype, where, value, g):
     """NaN in the rows that see a NaN or infinite token (its block, once
     quantized), nothing in the others; a later, hidden one does no harm."""
     B = 32
@@ -309,11 +341,11 @@ def test_nonfinite_tokens(kv8, dtype, where, value):
             (k, v)[which][at, 0, 3] = value
             (k, v)[which][at, 0, 64] = value
 
-        r = Run(kv8, 1, 2, 2, 128, B, "int8", dtype, 200, rot=0)
+        r = Run(kv8, 1, 2, g, 128, B, "int8", dtype, 200, rot=0)
         r.append([50], change)
         out = _host(r.attend())
         first = at if where == "window" else 0
-        assert np.isnan(out[first:, :2]).all() and not np.isnan(out[:, 2:]).any()
+        assert np.isnan(out[first:, :g]).all() and not np.isnan(out[:, g:]).any()
         assert not np.isnan(out[:first]).any()
 
 
@@ -333,6 +365,22 @@ def test_large_scores_and_spread_scales(kv8, dtype):
         r = Run(kv8, 1, 1, 4, 128, 32, fmt, dtype, 200, rot=0)
         r.append([110], change)
         r.check_state()
+        r.attend()
+        r.append([3])  # few rows
+        r.attend()
+
+
+def test_blocks_of_zeros(kv8):
+    """Values of zero have no scale to speak of, and their tokens still weigh."""
+    def change(q, k, v):
+        v[:96] = 0
+        k[:32] = 0
+
+    for dtype in ("float16", "bfloat16"):
+        r = Run(kv8, 1, 1, 2, 128, 32, "int8", dtype, 200, rot=0)
+        r.append([140], change)
+        r.attend()
+        r.append([1])
         r.attend()
 
 
