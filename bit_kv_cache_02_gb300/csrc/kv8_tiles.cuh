@@ -13,6 +13,12 @@
 //   warp 12          issues the products: S = Q K^T, then O += P V with P in
 //                    tensor memory.  The two row tiles alternate, so one tile's
 //                    softmax runs under the other's products.
+//   warp 13          walks the CTA's share of the work: a ring of Parts.
+//   warp 14          looks up blocks and scales: a ring of Metas, one per unit.
+//
+// Parts and Metas live in shared memory so that the other roles keep their
+// registers for data: a spilled register costs an L2 round trip here, as the
+// tiles leave no first-level cache to speak of.
 //
 // Mathematics, in log2 units per row: z_t = q.k_t scale_k softmax_scale log2(e),
 // w_t = 2^(z_t + log2(scale_v) - M + 9), O = sum w_t v_code_t, l = sum w_t /
@@ -43,7 +49,7 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr int kThreads = 512;
 constexpr int kRows = kTileRows;  // 256 rows of an item
 constexpr int kKeys = 128;        // tokens of a unit
-constexpr int kMetas = 4;
+constexpr int kMetas = 8, kParts = 4, kCols = 4;
 constexpr float kGrow = 6.f;      // how far the maximum may pass M
 constexpr float kShift = 9.f;     // w = 2^(z' - M + kShift) <= 2^15
 
@@ -55,22 +61,47 @@ struct Smem {
   static constexpr int K = Q + 2 * TILE;          // two stages
   static constexpr int V = K + 2 * TILE;          // two stages
   static constexpr int META = V + 2 * TILE;       // [kMetas] Meta
-  static constexpr int COL = META + kMetas * 64;  // [kMetas] window columns: scale_k, log2 scale_v, 1 / scale_v
-  static constexpr int BAR = COL + kMetas * 3 * kKeys * 4;
-  static constexpr int MISC = BAR + 16 * 8;
+  static constexpr int PART = META + kMetas * 128;  // [kParts] Part
+  static constexpr int COL = PART + kParts * 64;  // [kCols] window columns: scale_k, log2 scale_v, 1 / scale_v
+  static constexpr int BAR = COL + kCols * 3 * kKeys * 4;
+  static constexpr int MISC = BAR + 48 * 8;
   static constexpr int BYTES = MISC + 256 + 1024;  // and the alignment of the base
 };
 
-// Scales of a unit's four groups of 32 tokens.  A ring of four: keys are
-// brought at most two units ahead of the products, and a unit's products wait
-// for the softmax of the unit before.
+// What the roles need to know of one unit.  A ring of eight: warp 14 reuses a
+// slot once keys are stored three units later, which means that the products
+// two units before those are done, and the softmax of the unit before that.
+enum { kPacked, kWindow, kEnd };
 struct Meta {
-  float k[4], lv[4], inv[4];
-  int flush, pad[3];
+  long long off[4];           // pool offset of each group of 32 tokens' block, or -1: zeros
+  float k[4], lv[4], inv[4];  // scales of keys, log2 and inverse of those of values
+  long long win;              // window offset of the (sequence, head)
+  int kind;                   // kPacked, kWindow or kEnd
+  int valid;                  // tokens of a window unit
+  int flush;                  // groups whose values count as zeros
+  int pad[7];
 };
+static_assert(sizeof(Meta) == 128, "Meta");
 
-enum Bar { kQFull, kKFull, kKEmpty = kKFull + 2, kVFull = kKEmpty + 2, kVEmpty = kVFull + 2, kSFull = kVEmpty + 2,
-           kPFull = kSFull + 2, kOFull = kPFull + 2 };  // 15 barriers
+// One part of an item: units u0 .. u1 - 1 for 256 rows of one KV head.
+struct Part {
+  int u0, u1;           // u0 == u1: the end
+  int packed, stored;   // units and tokens of complete blocks
+  int L, n, row0;       // the sequence's tokens, new rows and first row
+  int row;              // the item's first row among the sequence's rows of a KV head
+  int h, s;
+  int slot;             // partial slot, or -1: the part is the whole item
+  int first, c0, cuts;  // the item's first partial slot, its first CTA, and how many CTAs follow
+  int pad[2];
+};
+static_assert(sizeof(Part) == 64, "Part");
+
+enum Bar {
+  kQFull, kKFull, kKEmpty = kKFull + 2, kVFull = kKEmpty + 2, kVEmpty = kVFull + 2, kSFull = kVEmpty + 2,
+  kPFull = kSFull + 2, kOFull = kPFull + 2, kPartFull = kOFull + 2, kPartFree = kPartFull + kParts,
+  kMetaFull = kPartFree + kParts, kMetaFree = kMetaFull + kMetas, kBars = kMetaFree + kMetas
+};
+static_assert(kBars <= 48, "barriers");
 
 // ------------------------------------------------------------ tcgen05 in PTX
 
@@ -91,20 +122,30 @@ __device__ __forceinline__ void commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
+// Shared-memory matrix descriptors, 128-byte swizzle: 8-row groups of 1024
+// bytes follow each other; `lead` is the step between 64-element halves of an
+// MN-major operand (K-major operands do not use it).  The high words are the
+// same for all; desc_lo gives the low one, to which byte offsets / 16 add.
+constexpr uint32_t kDescHi = (1024 >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lead) {
+  return ((addr >> 4) & 0x3fff) | (lead >> 4 << 16);
+}
+
 // D[tmem] (+)= A[smem] B[smem]
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)), "n"(kDescHi)
       : "memory");
 }
 // D[tmem] (+)= A[tmem] B[smem]
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.u32 p, %4, 0;\n\tmov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)), "n"(kDescHi)
       : "memory");
 }
 
@@ -120,11 +161,11 @@ __device__ __forceinline__ void tmem_ld32(uint32_t *v, uint32_t addr) {
       : "r"(addr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *v) {
+__device__ __forceinline__ void tmem_ld16(uint32_t *v, uint32_t addr) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-      KV8_W8(v, 0), KV8_W8(v, 8), KV8_W8(v, 16), KV8_W8(v, 24)
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : KV8_R8(v, 0), KV8_R8(v, 8)
+      : "r"(addr)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *v) {
@@ -135,13 +176,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *v) {
       : "memory");
 }
 
-// Shared-memory matrix descriptor, 128-byte swizzle: 8-row groups of 1024
-// bytes follow each other; `lead` is the step between 64-element halves of an
-// MN-major operand (K-major operands do not use it).
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead) {
-  return static_cast<uint64_t>((addr >> 4) & 0x3fff) | (static_cast<uint64_t>(lead >> 4) << 16) |
-         (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
-}
 // kind::f16 with fp16 operands and fp32 accumulators, M = 128
 __host__ __device__ constexpr uint32_t instr_desc(int n, bool b_mn_major) {
   return (1u << 4) | (b_mn_major ? 1u << 16 : 0u) | (static_cast<uint32_t>(n / 8) << 17) | (8u << 24);
@@ -264,7 +298,6 @@ struct Walk {
     part();
     return true;
   }
-  __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == p.units; }
 };
 
 // Sum over the CTA, and each thread's exclusive prefix.
@@ -305,6 +338,17 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi) {
         : "=r"(lo), "=r"(hi)
         : "r"(w));
   }
+}
+
+// Eight bf16 numbers, scaled, as fp16.
+__device__ __forceinline__ uint4 bf16_row_to_fp16(uint4 x, float f) {
+  uint32_t e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 y = unpack2<true>(e[i]);
+    e[i] = kvq::h2_as_u32(__floats2half2_rn(y.x * f, y.y * f));
+  }
+  return make_uint4(e[0], e[1], e[2], e[3]);
 }
 
 template <int D, int FMT, bool BF16>
@@ -366,6 +410,14 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
   if (tid == 0) {
     *dead = 0;
     kvq::mbar_init(bars + kQFull, 256);
+    for (int i = 0; i < kParts; ++i) {
+      kvq::mbar_init(bars + kPartFull + i, 1);
+      kvq::mbar_init(bars + kPartFree + i, 10);  // eight softmax warps, the products, the tables
+    }
+    for (int i = 0; i < kMetas; ++i) {
+      kvq::mbar_init(bars + kMetaFull + i, 1);
+      kvq::mbar_init(bars + kMetaFree + i, 1);
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       kvq::mbar_init(bars + kKFull + i, 128);
@@ -387,21 +439,13 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
   fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  Walk use;
-  {
-    use.p = pair_of_slot(a, static_cast<int>(found[0]));
-    const long long in = found[1];
-    use.h = static_cast<int>(in / use.p.units);
-    use.u0 = static_cast<int>(in - static_cast<long long>(use.h) * use.p.units);
-    use.at = lo;
-    use.end = hi;
-    use.part();
-  }
+  Part *const parts = reinterpret_cast<Part *>(smem + SM::PART);
+  Meta *const metas = reinterpret_cast<Meta *>(smem + SM::META);
   // A wait of a role; false ends the role (another one's wait ran out, or this).
   auto wait = [&](int bar, uint32_t parity) -> bool {
     if (kvq::mbar_try_wait(bars + bar, parity)) return true;
     const long long since = clock64();
-    while (!kvq::mbar_try_wait_hint(bars + bar, parity, 100000u)) {
+    while (!kvq::mbar_try_wait(bars + bar, parity)) {
       if (*dead) return false;
       if (clock64() - since > kvq::kWaitLimitCycles) {
         *dead = 1;
@@ -413,33 +457,38 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
   };
 
   if (warp >= 12) {
-    // =================================================== the products
-    // 2 x 184 + 96 + 48 = 4 x 128, what the CTA was launched with
+    // 2 x 176 + 112 + 48 = 4 x 128, what the CTA was launched with
     regs_dec<48>();
     if (warp == 12 && lane == 0) {
+      // ================================================= the products
       constexpr uint32_t id_qk = instr_desc(kKeys, false), id_pv = instr_desc(D, true);
-      uint32_t n_unit = 0, n_part = 0;  // units and parts issued so far
-      uint32_t np[2] = {0, 0};          // weights consumed, per row tile
+      uint32_t n_unit = 0;      // units issued so far
+      uint32_t np[2] = {0, 0};  // weights consumed, per row tile
       auto qk = [&](int t, uint32_t unit) {
         const uint32_t q = base + SM::Q + t * SM::TILE, k = base + SM::K + (unit & 1) * SM::TILE;
+        const uint32_t qd = desc_lo(q, 16), kd = desc_lo(k, 16);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-          const uint32_t off = (i >> 2) * SM::HALF + (i & 3) * 32;
-          mma_ss(tmem + t * 128, smem_desc(q + off, 16), smem_desc(k + off, 16), id_qk, i != 0);
+          const uint32_t off = ((i >> 2) * SM::HALF + (i & 3) * 32) >> 4;
+          mma_ss(tmem + t * 128, qd + off, kd + off, id_qk, i != 0);
         }
         commit(base + SM::BAR + (kSFull + t) * 8);
       };
       auto pv = [&](int t, uint32_t unit, bool add) {
-        const uint32_t v = base + SM::V + (unit & 1) * SM::TILE;
+        const uint32_t vd = desc_lo(base + SM::V + (unit & 1) * SM::TILE, SM::HALF);
 #pragma unroll
         for (int i = 0; i < kKeys / 16; ++i)
-          mma_ts(tmem + 256 + t * 128, tmem + t * 128 + i * 8, smem_desc(v + i * 2048, SM::HALF), id_pv, add || i != 0);
+          mma_ts(tmem + 256 + t * 128, tmem + t * 128 + i * 8, vd + i * (2048 >> 4), id_pv, add || i != 0);
         commit(base + SM::BAR + (kOFull + t) * 8);
       };
       bool ok = true;
-      do {
-        const int tiles = use.p.q.n * a.group - use.p.rt * kRows > 128 ? 2 : 1;
-        const int units = use.u1 - use.u0;
+      for (uint32_t n_part = 0; ok; ++n_part) {
+        ok = wait(kPartFull + n_part % kParts, (n_part / kParts) & 1);
+        if (!ok) break;
+        const Part &p = parts[n_part % kParts];
+        const int units = p.u1 - p.u0, tiles = p.n * a.group - p.row > 128 ? 2 : 1;
+        kvq::mbar_arrive(bars + kPartFree + n_part % kParts);
+        if (units == 0) break;
         ok = wait(kQFull, n_part & 1) && wait(kKFull + (n_unit & 1), (n_unit >> 1) & 1);
         if (!ok) break;
         fence_after();
@@ -460,65 +509,136 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           commit(base + SM::BAR + (kVEmpty + (n_unit & 1)) * 8);
           if (u + 1 < units) commit(base + SM::BAR + (kKEmpty + ((n_unit + 1) & 1)) * 8);
         }
-        ++n_part;
-      } while (ok && use.next(a));
+      }
+    } else if (warp == 13 && lane == 0) {
+      // ================================================= the walk
+      Walk use;
+      use.p = pair_of_slot(a, static_cast<int>(found[0]));
+      use.h = static_cast<int>(found[1] / use.p.units);
+      use.u0 = static_cast<int>(found[1] - static_cast<long long>(use.h) * use.p.units);
+      use.at = lo;
+      use.end = hi;
+      use.part();
+      bool more = true;
+      for (uint32_t n_part = 0;; ++n_part) {
+        if (n_part >= kParts && !wait(kPartFree + n_part % kParts, ((n_part / kParts) & 1) ^ 1)) break;
+        Part &p = parts[n_part % kParts];
+        p.u0 = more ? use.u0 : 0;
+        p.u1 = more ? use.u1 : 0;
+        if (more) {
+          p.packed = use.p.packed;
+          p.stored = use.p.stored;
+          p.L = use.p.q.L;
+          p.n = use.p.q.n;
+          p.row0 = use.p.q.row0;
+          p.row = use.p.rt * kRows;
+          p.h = use.h;
+          p.s = use.p.s;
+          p.slot = -1;
+          if (use.u0 != 0 || use.u1 != use.p.units) {
+            const long long s0 = use.start, s1 = s0 + use.p.units;  // the item's place on the line
+            auto owner = [&](long long pos) { return static_cast<int>(((pos + 1) * ctas - 1) / total); };
+            const int c0 = owner(s0);
+            p.slot = 2 * blockIdx.x + (s0 + use.u0 == lo ? 0 : 1);
+            p.c0 = c0;
+            p.cuts = owner(s1 - 1) - c0;
+            p.first = 2 * c0 + (c0 * total / ctas < s0 ? 1 : 0);  // later CTAs begin with their part
+          }
+        }
+        kvq::mbar_arrive(bars + kPartFull + n_part % kParts);
+        if (!more) break;
+        more = use.next(a);
+      }
+    } else if (warp == 14) {
+      // ================================================= blocks and scales
+      uint32_t n_unit = 0;
+      bool ok = true;
+      auto slot_free = [&]() {
+        if (n_unit >= kMetas) ok = __all_sync(kAll, wait(kMetaFree + n_unit % kMetas, ((n_unit / kMetas) & 1) ^ 1));
+        return ok;
+      };
+      auto publish = [&]() {
+        __syncwarp();
+        if (lane == 0) kvq::mbar_arrive(bars + kMetaFull + n_unit % kMetas);
+        ++n_unit;
+      };
+      for (uint32_t n_part = 0; ok; ++n_part) {
+        ok = __all_sync(kAll, wait(kPartFull + n_part % kParts, (n_part / kParts) & 1));
+        if (!ok) break;
+        const Part p = parts[n_part % kParts];
+        __syncwarp();
+        if (lane == 0) kvq::mbar_arrive(bars + kPartFree + n_part % kParts);
+        // eight units at a time, a lane per group of 32 tokens
+        for (int u = p.u0; u < p.u1 && ok; u += 8) {
+          const int mu = u + (lane >> 2), tok = mu * kKeys + (lane & 3) * 32;
+          long long off = -1;
+          float2 sc = make_float2(1.f, 1.f);
+          if (mu < min(p.packed, p.u1) && tok < p.stored) {
+            const int e = geo.table[static_cast<size_t>(p.s) * geo.max_blocks + tok / B];
+            if (e >= 0 && e < geo.num_blocks) {
+              const long long bh = static_cast<long long>(e) * H + p.h;
+              off = bh * 2 * B * D;
+              sc = *reinterpret_cast<const float2 *>(geo.scales + bh * 2);
+            } else {
+              set_status(geo.status, KVQ_STATUS_BAD_BLOCK);
+              sc = make_float2(nan, nan);
+            }
+          }
+          const float inf = __int_as_float(0x7f800000);
+          const bool bad = !(fabsf(sc.x) < inf && fabsf(sc.y) < inf);
+          // values of magnitude 2^-100 or less (the scale's floor): zeros, of any scale
+          const bool flush = !bad && sc.y < 8.8e-33f;
+          const unsigned flushes = __ballot_sync(kAll, flush);
+          const float lv = bad ? nan : flush ? 0.f : log2f(sc.y), inv = bad || flush ? 1.f : 1.f / sc.y;
+          for (int i = 0; i < 8 && u + i < p.u1; ++i) {
+            if (!slot_free()) break;
+            Meta &m = metas[n_unit % kMetas];
+            if (lane >> 2 == i) {
+              const int gr = lane & 3;
+              m.off[gr] = off;
+              m.k[gr] = bad ? 1.f : sc.x;
+              m.lv[gr] = lv;
+              m.inv[gr] = inv;
+              if (gr == 0) {
+                m.kind = mu < p.packed ? kPacked : kWindow;
+                m.valid = p.L - p.stored;
+                m.flush = (flushes >> (4 * i)) & 15;
+                m.win = (static_cast<long long>(p.s) * H + p.h) * B * D;
+              }
+            }
+            publish();
+          }
+        }
+        if (p.u0 == p.u1) {
+          if (slot_free()) {
+            if (lane == 0) metas[n_unit % kMetas].kind = kEnd;
+            publish();
+          }
+          break;
+        }
+      }
     }
   } else if (warp >= 8) {
     // =================================================== keys and values
-    regs_dec<96>();
+    regs_dec<112>();
     const int ct = tid - 256;                  // 0 .. 127
     constexpr int CPR = D / 16;                // 16-code chunks of a token
     constexpr int RPI = 128 / CPR;             // tokens per instruction: 16 or 32
     constexpr int NI = 128 / RPI;              // instructions per unit
     const int cr = ct / CPR, cc = ct % CPR;
-    const int shift = 31 - __clz(B);           // block = 1 << shift
     uint4 kb[NI], vb[NI];
-    int ent[4], ahead[4];               // table entries of the unit to fetch, and of the one behind it
-    float2 sc = make_float2(1.f, 1.f);  // scales of group ct, for ct < 4
-    uint32_t n_unit = 0;
-    bool ok = true;
-    Walk &get = use;  // the part and the unit whose codes are fetched next
-    int gu = get.u0;
 
-    // table entries of unit u of the part; -1: a bad one, -2: nothing there
-    auto entries = [&](int *e, int u) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        e[i] = -2;
-        const int tok = u * kKeys + i * 32;
-        if (u < min(get.p.packed, get.u1) && tok < get.p.stored)
-          e[i] = geo.table[static_cast<size_t>(get.p.s) * geo.max_blocks + (tok >> shift)];
-      }
-    };
-    auto good = [&](int e) { return e >= 0 && e < geo.num_blocks; };
-    auto load = [&](uint4 *buf, bool values) {
+    auto load = [&](uint4 *buf, const Meta &m, int extra) {
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
+        const long long off = m.off[i * RPI / 32];
         buf[i] = make_uint4(0u, 0u, 0u, 0u);
-        const int row = i * RPI + cr, e = ent[i * RPI / 32];
-        if (good(e)) {
-          const size_t off = (((static_cast<size_t>(e) * H + get.h) * 2 + (values ? 1 : 0)) * B +
-                              ((gu * kKeys + row) & (B - 1))) * D + cc * 16;
-          buf[i] = __ldg(reinterpret_cast<const uint4 *>(geo.codes + off));
-        }
+        if (off >= 0)
+          buf[i] = __ldg(reinterpret_cast<const uint4 *>(geo.codes + off + extra +
+                                                         ((i * RPI + cr) & (B - 1)) * D + cc * 16));
       }
     };
-    auto load_scales = [&]() {
-      sc = make_float2(1.f, 1.f);
-      if (ct < 4) {
-        int e = ent[0];
-#pragma unroll
-        for (int i = 1; i < 4; ++i)
-          if (ct == i) e = ent[i];
-        if (good(e)) {
-          sc = *reinterpret_cast<const float2 *>(geo.scales + (static_cast<size_t>(e) * H + get.h) * 2);
-        } else if (e != -2) {
-          sc = make_float2(nan, nan);
-          set_status(geo.status, KVQ_STATUS_BAD_BLOCK);
-        }
-      }
-    };
-    // `flush`: groups of 32 tokens whose values are stored as zeros
+    // `flush`: groups of 32 tokens that are stored as zeros
     auto store = [&](uint32_t dst, const uint4 *buf, int flush) {
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
@@ -530,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
         widen4<FMT>(x.y, e[2], e[3]);
         widen4<FMT>(x.z, e[4], e[5]);
         widen4<FMT>(x.w, e[6], e[7]);
-        // the two chunks in an order that keeps eight threads' stores in eight banks groups
+        // the two chunks in an order that keeps eight threads' stores in eight bank groups
         const bool swap = D == 128 && cc >= 4;
         const uint32_t a0 = dst + place(row, 2 * cc), a1 = dst + place(row, 2 * cc + 1);
         sts16(swap ? a1 : a0, swap ? e[4] : e[0], swap ? e[5] : e[1], swap ? e[6] : e[2], swap ? e[7] : e[3]);
@@ -543,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       bad = false;
       f = 1.f;
       if (!valid) return;
-#pragma unroll 4
+#pragma unroll 1
       for (int c = 0; c < D / 8; ++c) {
         const uint4 x = *reinterpret_cast<const uint4 *>(src + 8 * c);
         const uint32_t e[4] = {x.x, x.y, x.z, x.w};
@@ -559,58 +679,45 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       if (BF16 && big) f = __int_as_float((268 - max(static_cast<int>(big >> 7), 20)) << 23);
     };
     auto store_window = [&](uint32_t dst, const uint16_t *src, bool zero, float f) {
-#pragma unroll 4
+#pragma unroll 1
       for (int c = 0; c < D / 8; ++c) {
         uint4 x = make_uint4(0u, 0u, 0u, 0u);
         if (!zero) x = *reinterpret_cast<const uint4 *>(src + 8 * c);
-        if (BF16) {
-          uint32_t *e = &x.x;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 y = unpack2<true>(e[i]);
-            e[i] = kvq::h2_as_u32(__floats2half2_rn(y.x * f, y.y * f));
-          }
-        }
+        if (BF16) x = bf16_row_to_fp16(x, f);
         sts16(dst + place(ct, c), x.x, x.y, x.z, x.w);
       }
     };
 
-    entries(ent, gu);
-    entries(ahead, gu + 1);
-    load_scales();
-    load(kb, false);
-    load(vb, true);
-    for (bool more = true; more;) {
+    bool ok = wait(kMetaFull, 0);
+    int kind = kEnd;
+    if (bar_all(1, 128, ok)) {
+      kind = metas[0].kind;
+      if (kind == kPacked) {
+        load(kb, metas[0], 0);
+        load(vb, metas[0], B * D);
+      }
+    }
+    for (uint32_t n_unit = 0; kind != kEnd; ++n_unit) {
       const int st = n_unit & 1;
       const uint32_t reuse = ((n_unit >> 1) & 1) ^ 1;  // the stage's previous user must be done
       const uint32_t kd = base + SM::K + st * SM::TILE, vd = base + SM::V + st * SM::TILE;
-      Meta *meta = reinterpret_cast<Meta *>(smem + SM::META) + n_unit % kMetas;
-      const bool window = gu >= get.p.packed;
-      const size_t win = ((static_cast<size_t>(get.p.s) * H + get.h) * B + ct) * D;
-      const bool wvalid = window && ct < get.p.q.L - get.p.stored;
+      const Meta &m = metas[n_unit % kMetas], &m1 = metas[(n_unit + 1) % kMetas];
       float vf = 1.f;
-      bool vbad = false;
+      bool vzero = true;
       if (n_unit >= 2) ok = wait(kKEmpty + st, reuse);
       if (!bar_all(1, 128, ok)) break;
-      if (!window) {
+      if (kind == kPacked) {
         store(kd, kb, 0);
-        if (ct < 4) {
-          const bool bad = !(fabsf(sc.x) < __int_as_float(0x7f800000) && fabsf(sc.y) < __int_as_float(0x7f800000));
-          // values of magnitude 2^-100 or less (the scale's floor): zeros, of any scale
-          const bool flush = !bad && sc.y < 8.8e-33f;
-          meta->k[ct] = bad ? 1.f : sc.x;
-          meta->lv[ct] = bad ? nan : flush ? 0.f : log2f(sc.y);
-          meta->inv[ct] = bad || flush ? 1.f : 1.f / sc.y;
-          const unsigned bits = __ballot_sync(0xfu, flush);
-          if (ct == 0) meta->flush = static_cast<int>(bits);
-        }
       } else {
-        float *col = reinterpret_cast<float *>(smem + SM::COL) + (n_unit % kMetas) * 3 * kKeys + ct;
+        float *col = reinterpret_cast<float *>(smem + SM::COL) + (n_unit % kCols) * 3 * kKeys + ct;
+        const uint16_t *ks = geo.k_win + m.win + ct * D, *vs = geo.v_win + m.win + ct * D;
+        const bool valid = ct < m.valid;
         float kf;
-        bool kbad;
-        window_row(geo.k_win + win, wvalid, kf, kbad);
-        window_row(geo.v_win + win, wvalid, vf, vbad);
-        store_window(kd, geo.k_win + win, !wvalid, kf);
+        bool kbad, vbad;
+        window_row(ks, valid, kf, kbad);
+        window_row(vs, valid, vf, vbad);
+        store_window(kd, ks, !valid, kf);
+        vzero = !valid || vbad;
         col[0] = 1.f / kf;
         // tokens that are not finite turn the rows that see them to NaN
         col[kKeys] = kbad || vbad ? nan : -log2f(vf);
@@ -618,67 +725,56 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       }
       kvq::fence_proxy_async();
       kvq::mbar_arrive(bars + kKFull + st);
-      // the next unit's keys
-      if (++gu < get.u1) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) ent[i] = ahead[i];
-      } else {
-        more = get.next(a);
-        gu = get.u0;
-        if (more) {
-          entries(ent, gu);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) ent[i] = -2;
-        }
-      }
-      load(kb, false);
-      if (n_unit >= 2) ok = wait(kVEmpty + st, reuse);
-      if (!bar_all(1, 128, ok)) break;  // also: the groups to flush are known to all
-      if (!window)
-        store(vd, vb, meta->flush);
+      if (ct == 0 && n_unit >= 3) kvq::mbar_arrive(bars + kMetaFree + (n_unit - 3) % kMetas);
+      // the next unit's keys, and its values once this one's are stored
+      ok = wait(kMetaFull + (n_unit + 1) % kMetas, ((n_unit + 1) / kMetas) & 1);
+      const int next = ok ? m1.kind : static_cast<int>(kEnd);
+      if (next == kPacked) load(kb, m1, 0);
+      if (ok && n_unit >= 2) ok = wait(kVEmpty + st, reuse);
+      if (!bar_all(1, 128, ok)) break;
+      if (kind == kPacked)
+        store(vd, vb, m.flush);
       else
-        store_window(vd, geo.v_win + win, !wvalid || vbad, vf);
+        store_window(vd, geo.v_win + m.win + ct * D, vzero, vf);
       kvq::fence_proxy_async();
       kvq::mbar_arrive(bars + kVFull + st);
-      load(vb, true);
-      load_scales();
-      if (more) entries(ahead, gu + 1);
-      ++n_unit;
+      if (next == kPacked) load(vb, m1, B * D);
+      kind = next;
     }
   } else {
     // =================================================== softmax
-    regs_inc<184>();
+    regs_inc<176>();
     const int t = warp >> 2;         // row tile
     const int r = tid & 127;         // row of the tile = lane of tensor memory
     const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21);
     const uint32_t s_at = lanes + t * 128, o_at = lanes + 256 + t * 128;
-    const Meta *metas = reinterpret_cast<const Meta *>(smem + SM::META);
     uint32_t n_unit = 0;  // units so far
     uint32_t n_own = 0;   // units of this row tile so far
     bool ok = true;
-    do {
-      const Pair &p = use.p;
-      const int n_rows = p.q.n * a.group;
-      const int row = p.rt * kRows + t * 128 + r;
-      const bool active = n_rows - p.rt * kRows > t * 128;  // the tile has rows
+    for (uint32_t n_part = 0;; ++n_part) {
+      // all eight warps go on together, or leave together
+      ok = ok && wait(kPartFull + n_part % kParts, (n_part / kParts) & 1);
+      if (!bar_all(2, 256, ok)) break;
+      const Part &p = parts[n_part % kParts];
+      const int u0 = p.u0, u1 = p.u1;
+      if (u0 == u1) break;
+      const int n_rows = p.n * a.group;
+      const int row = p.row + t * 128 + r;
+      const bool active = n_rows - p.row > t * 128;  // the tile has rows
       const bool valid = row < n_rows;
       const int tok = valid ? row / a.group : 0;
-      const int lim = valid ? p.q.L - p.q.n + tok : -1;  // last position the row sees
-      const long long q_row = static_cast<long long>(p.q.row0) + tok;
-      const long long q_head = static_cast<long long>(use.h) * a.group + (valid ? row - tok * a.group : 0);
-      // every row of the tile sees at least the tokens up to here
-      const int seen_by_all = p.q.L - p.q.n + (p.rt * kRows + t * 128) / a.group;
+      const int lim = valid ? p.L - p.n + tok : -1;  // last position the row sees
 
       // ---- the row's query to shared memory
       float qf = a.zscale;
       if (active) {
-        const uint16_t *src = a.q.p + q_row * a.q.row + q_head * a.q.head;
+        const uint16_t *src = a.q.p + (static_cast<long long>(p.row0) + tok) * a.q.row +
+                              (static_cast<long long>(p.h) * a.group + (valid ? row - tok * a.group : 0)) * a.q.head;
         const uint32_t dst = base + SM::Q + t * SM::TILE;
         float f = 1.f;
         if (BF16 && valid) {
           uint32_t big = 0;
-#pragma unroll
+#pragma unroll 4
           for (int c = 0; c < D / 8; ++c) {
             const uint4 x = *reinterpret_cast<const uint4 *>(src + 8 * c);
             const uint32_t e[4] = {x.x, x.y, x.z, x.w};
@@ -693,18 +789,11 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           f = __int_as_float((268 - e) << 23);
           qf *= __int_as_float((e - 14) << 23);
         }
-#pragma unroll
+#pragma unroll 4
         for (int c = 0; c < D / 8; ++c) {
           uint4 x = make_uint4(0u, 0u, 0u, 0u);
           if (valid) x = *reinterpret_cast<const uint4 *>(src + 8 * c);
-          if (BF16) {
-            uint32_t *e = &x.x;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 y = unpack2<true>(e[i]);
-              e[i] = kvq::h2_as_u32(__floats2half2_rn(y.x * f, y.y * f));
-            }
-          }
+          if (BF16) x = bf16_row_to_fp16(x, f);
           sts16(dst + place(r, c), x.x, x.y, x.z, x.w);
         }
         kvq::fence_proxy_async();
@@ -714,59 +803,62 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
 
       float M = ninf, l = 0.f;
       if (active) {
-        for (int u = use.u0; u < use.u1; ++u, ++n_unit, ++n_own) {
-          ok = wait(kSFull + t, n_own & 1);
-          if (!__all_sync(kAll, ok)) {
-            ok = false;
-            break;
-          }
+        // every row of the tile sees at least the tokens up to here
+        const int seen_by_all = p.L - p.n + (p.row + t * 128) / a.group;
+        for (int u = u0; u < u1; ++u, ++n_unit, ++n_own) {
+          ok = __all_sync(kAll, wait(kSFull + t, n_own & 1));
+          if (!ok) break;
           fence_after();
+          const Meta &meta = metas[n_unit % kMetas];
+          const bool window = meta.kind == kWindow;
+          const int t0 = window ? p.stored : u * kKeys;
+          const int here = min(kKeys, window ? meta.valid : p.stored - t0);  // tokens of the unit
+          const float *col = reinterpret_cast<const float *>(smem + SM::COL) + (n_unit % kCols) * 3 * kKeys;
+          const bool edge = window || here < kKeys || t0 + kKeys - 1 > seen_by_all;
+          const int cmax = min(here, lim - t0 + 1);  // columns below it are seen
+          if (window) {
+            // each token has its own scales: S becomes z + log2 scale_v in place
+#pragma unroll 1
+            for (int c = 0; c < kKeys; c += 16) {
+              uint32_t z[16];
+              tmem_ld16(z, s_at + c);
+              wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                float x = __uint_as_float(z[i]) * (col[c + i] * qf) + col[kKeys + c + i];
+                x += x - x;  // an infinite score becomes NaN
+                z[i] = __float_as_uint(c + i < cmax ? x : ninf);
+              }
+              tmem_st16(s_at + c, z);
+            }
+            wait_st();
+          }
           uint32_t sr[128];
-          float *s = reinterpret_cast<float *>(sr);
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld32(sr + 32 * c, s_at + 32 * c);
           wait_ld();
-          const bool window = u >= p.packed;
-          const int t0 = window ? p.stored : u * kKeys;
-          const int here = min(kKeys, window ? p.q.L - p.stored : p.stored - t0);  // tokens of the unit
-          const Meta &meta = metas[n_unit % kMetas];
-          const float *col_k = reinterpret_cast<const float *>(smem + SM::COL) + (n_unit % kMetas) * 3 * kKeys,
-                      *col_lv = col_k + kKeys, *col_inv = col_lv + kKeys;
-          const bool edge = window || here < kKeys || t0 + kKeys - 1 > seen_by_all;
           float mx = ninf;
-          float ka[4], kl[4];
           if (!edge) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              ka[c] = meta.k[c] * qf;
-              kl[c] = meta.lv[c];
-              float m0 = s[32 * c], m1 = s[32 * c + 1];
+              float m0 = __uint_as_float(sr[32 * c]), m1 = __uint_as_float(sr[32 * c + 1]);
 #pragma unroll
               for (int i = 2; i < 32; i += 2) {
-                m0 = fmaxf(m0, s[32 * c + i]);
-                m1 = fmaxf(m1, s[32 * c + i + 1]);
+                m0 = fmaxf(m0, __uint_as_float(sr[32 * c + i]));
+                m1 = fmaxf(m1, __uint_as_float(sr[32 * c + i + 1]));
               }
-              mx = fmaxf(mx, fmaf(fmaxf(m0, m1), ka[c], kl[c]));
+              mx = fmaxf(mx, fmaf(fmaxf(m0, m1), meta.k[c] * qf, meta.lv[c]));
             }
           } else {
-            const int cmax = min(here, lim - t0 + 1);  // columns below it are seen
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              ka[c] = 1.f;
-              kl[c] = 0.f;
-              const float k = window ? 0.f : meta.k[c] * qf, lv = window ? 0.f : meta.lv[c];
+              const float k = window ? 1.f : meta.k[c] * qf, lv = window ? 0.f : meta.lv[c];
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
-                const int col = 32 * c + i;
-                float z;
-                if (window) {
-                  z = s[col] * (col_k[col] * qf) + col_lv[col];
-                  z += z - z;  // an infinite score becomes NaN
-                } else {
-                  z = fmaf(s[col], k, lv);
-                }
-                z = col < cmax ? z : ninf;
-                s[col] = z;
+                const int cl = 32 * c + i;
+                float z = fmaf(__uint_as_float(sr[cl]), k, lv);
+                z = cl < cmax ? z : ninf;
+                sr[cl] = __float_as_uint(z);
                 mx = fmaxf(mx, z);
               }
             }
@@ -778,22 +870,14 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
             const float f = M == ninf ? (move ? 0.f : 1.f) : kvq::fast_exp2(M - to);
             M = to;
             l *= f;
-            if (u > use.u0) {
-              ok = wait(kOFull + t, (n_own - 1) & 1);
-              if (!__all_sync(kAll, ok)) {
-                ok = false;
-                break;
-              }
+            if (u > u0) {
+              ok = __all_sync(kAll, wait(kOFull + t, (n_own - 1) & 1));
+              if (!ok) break;
               fence_after();
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < D / 16; ++c) {
                 uint32_t o[16];
-                asm volatile(
-                    "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, "
-                    "[%16];"
-                    : KV8_R8(o, 0), KV8_R8(o, 8)
-                    : "r"(o_at + 16 * c)
-                    : "memory");
+                tmem_ld16(o, o_at + 16 * c);
                 wait_ld();
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
@@ -802,32 +886,36 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
             }
           }
           const float ref = M == ninf ? 0.f : M - kShift;
+          if (window) {
+#pragma unroll 1
+            for (int c = 0; c < kKeys; c += 16) {
+              uint32_t z[16];
+              tmem_ld16(z, s_at + c);
+              wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                l = fmaf(c + i < cmax ? kvq::fast_exp2(__uint_as_float(z[i]) - ref) : 0.f, col[2 * kKeys + c + i], l);
+            }
+          }
           // ---- weights
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const float bias = kl[c] - ref;
-            const uint64_t a2 = pack64(ka[c], ka[c]), b2 = pack64(bias, bias);
+            const float k = edge ? 1.f : meta.k[c] * qf, bias = (edge ? 0.f : meta.lv[c]) - ref;
+            const uint64_t a2 = pack64(k, k), b2 = pack64(bias, bias);
             uint64_t sum = pack64(0.f, 0.f);
             uint32_t pk[16];
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
               float x, y;
-              unpack64(fma2(pack64(s[32 * c + i], s[32 * c + i + 1]), a2, b2), x, y);
+              unpack64(fma2(pack64(__uint_as_float(sr[32 * c + i]), __uint_as_float(sr[32 * c + i + 1])), a2, b2), x, y);
               x = kvq::fast_exp2(x);
               y = kvq::fast_exp2(y);
-              if (window) {
-                l = fmaf(x, col_inv[32 * c + i], l);
-                l = fmaf(y, col_inv[32 * c + i + 1], l);
-              } else {
-                sum = add2(sum, pack64(x, y));
-              }
               pk[i / 2] = kvq::h2_as_u32(__floats2half2_rn(x, y));
+              sum = add2(sum, pack64(x, y));
             }
-            if (!window) {
-              float x, y;
-              unpack64(sum, x, y);
-              l = fmaf(x + y, meta.inv[c], l);
-            }
+            float x, y;
+            unpack64(sum, x, y);
+            if (!window) l = fmaf(x + y, meta.inv[c], l);
             tmem_st16(s_at + 16 * c, pk);
           }
           wait_st();
@@ -835,19 +923,21 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           kvq::mbar_arrive(bars + kPFull + t);
         }
       } else {
-        n_unit += use.u1 - use.u0;
+        n_unit += u1 - u0;
       }
 
       // ---- the part's result
-      const bool whole = use.whole();
-      const int slot = 2 * blockIdx.x + (use.start + use.u0 == lo ? 0 : 1);
-      float4 *part = reinterpret_cast<float4 *>(a.tile_o) + static_cast<size_t>(slot) * (D / 4) * kRows + t * 128 + r;
-      uint16_t *dst = a.out.p + q_row * a.out.row + q_head * a.out.head;
+      const int slot = p.slot;
+      const bool whole = slot < 0;
+      float4 *part = reinterpret_cast<float4 *>(a.tile_o) + static_cast<size_t>(max(slot, 0)) * (D / 4) * kRows +
+                     t * 128 + r;
+      uint16_t *dst = a.out.p + (static_cast<long long>(p.row0) + tok) * a.out.row +
+                      (static_cast<long long>(p.h) * a.group + (valid ? row - tok * a.group : 0)) * a.out.head;
       if (active && ok) ok = __all_sync(kAll, wait(kOFull + t, (n_own - 1) & 1));
       if (active && ok) {
         fence_after();
         const float inv = 1.f / l;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
           tmem_ld32(o, o_at + 32 * c);
@@ -877,15 +967,12 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
         fence_before();
       }
       if (!whole) {
-        const long long s0 = use.start, s1 = s0 + p.units;
-        auto owner = [&](long long pos) { return static_cast<int>(((pos + 1) * ctas - 1) / total); };
-        const int c0 = owner(s0), c1 = owner(s1 - 1);
         __threadfence();
         ok = bar_all(2, 256, ok);
         if (!ok) break;
         if (tid == 0) {
-          const bool last = kvq::atom_add_acq_rel(a.tile_counters + c0, 1) == c1 - c0;
-          if (last) a.tile_counters[c0] = 0;
+          const bool last = kvq::atom_add_acq_rel(a.tile_counters + p.c0, 1) == p.cuts;
+          if (last) a.tile_counters[p.c0] = 0;
           *flag = last;
         }
         bar_sync(2, 256);
@@ -893,12 +980,12 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
         bar_sync(2, 256);  // read before it is set again
         if (merge && valid) {
           __threadfence();
-          const int first = 2 * c0 + (c0 * total / ctas < s0 ? 1 : 0), parts = c1 - c0 + 1;
+          const int first = p.first, c0 = p.c0, n = p.cuts + 1;
           auto slot_of = [&](int i) { return i == 0 ? first : 2 * (c0 + i); };
           float mm = ninf, ll = 0.f;
-          for (int i = 0; i < parts; ++i) mm = fmaxf(mm, __ldcg(&a.tile_ml[slot_of(i) * kRows + t * 128 + r]).x);
+          for (int i = 0; i < n; ++i) mm = fmaxf(mm, __ldcg(&a.tile_ml[slot_of(i) * kRows + t * 128 + r]).x);
           const float ref = mm == ninf ? 0.f : mm;
-          for (int i = 0; i < parts; ++i) {
+          for (int i = 0; i < n; ++i) {
             const float2 e = __ldcg(&a.tile_ml[slot_of(i) * kRows + t * 128 + r]);
             ll += e.y * kvq::fast_exp2(e.x - ref);
           }
@@ -908,7 +995,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
             float o[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) o[k] = 0.f;
-            for (int i = 0; i < parts; ++i) {
+            for (int i = 0; i < n; ++i) {
               const int sl = slot_of(i);
               const float f = kvq::fast_exp2(__ldcg(&a.tile_ml[sl * kRows + t * 128 + r]).x - ref) * inv;
               const float4 *src = reinterpret_cast<const float4 *>(a.tile_o) +
@@ -930,9 +1017,9 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           }
         }
       }
-      // all softmax warps leave together
-      if (whole) ok = bar_all(2, 256, ok);
-    } while (ok && use.next(a));
+      __syncwarp();
+      if (lane == 0) kvq::mbar_arrive(bars + kPartFree + n_part % kParts);
+    }
   }
   __syncwarp();
   fence_before();
