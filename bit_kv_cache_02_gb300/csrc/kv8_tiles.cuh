@@ -39,6 +39,7 @@
 #pragma once
 
 #include <atomic>
+#include <type_traits>
 
 #include "kv8_internal.cuh"
 
@@ -96,6 +97,9 @@ struct Part {
 };
 static_assert(sizeof(Part) == 64, "Part");
 
+// All 512 columns of tensor memory are one CTA's: the address is 0.
+constexpr uint32_t kS = 0, kO = 256;  // two tiles of 128 columns each
+
 enum Bar {
   kQFull, kKFull, kKEmpty = kKFull + 2, kVFull = kKEmpty + 2, kVEmpty = kVFull + 2, kSFull = kVEmpty + 2,
   kPFull = kSFull + 2, kOFull = kPFull + 2, kPartFull = kOFull + 2, kPartFree = kPartFull + kParts,
@@ -116,7 +120,6 @@ __device__ __forceinline__ void tmem_relinquish() {
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
@@ -150,7 +153,17 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint3
 }
 
 #define KV8_R8(v, i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), "=r"(v[i + 4]), "=r"(v[i + 5]), "=r"(v[i + 6]), "=r"(v[i + 7])
+#define KV8_X8(v, i) "+r"(v[i]), "+r"(v[i + 1]), "+r"(v[i + 2]), "+r"(v[i + 3]), "+r"(v[i + 4]), "+r"(v[i + 5]), "+r"(v[i + 6]), "+r"(v[i + 7])
 #define KV8_W8(v, i) "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), "r"(v[i + 6]), "r"(v[i + 7])
+
+// Waits for this thread's loads from tensor memory; the registers go through
+// it, so that nothing touches them before.
+__device__ __forceinline__ void wait_ld32(uint32_t *v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : KV8_X8(v, 0), KV8_X8(v, 8), KV8_X8(v, 16), KV8_X8(v, 24)::"memory");
+}
+__device__ __forceinline__ void wait_ld16(uint32_t *v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : KV8_X8(v, 0), KV8_X8(v, 8)::"memory");
+}
 
 // 32 columns of the warp's 32 lanes
 __device__ __forceinline__ void tmem_ld32(uint32_t *v, uint32_t addr) {
@@ -183,6 +196,11 @@ __host__ __device__ constexpr uint32_t instr_desc(int n, bool b_mn_major) {
 
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 // A barrier of `threads` threads that says whether `ok` held for all of them.
 __device__ __forceinline__ bool bar_all(int id, int threads, bool ok) {
@@ -351,6 +369,86 @@ __device__ __forceinline__ uint4 bf16_row_to_fp16(uint4 x, float f) {
   return make_uint4(e[0], e[1], e[2], e[3]);
 }
 
+// The largest z' = S k + log2(scale_v) of a row's 128 columns (EDGE: of the
+// first cmax).  In a window S holds z' already.
+template <bool EDGE>
+__device__ __forceinline__ float unit_max(std::integral_constant<bool, EDGE>, uint32_t s_at, const Meta &meta, float qf,
+                                          bool window, int cmax) {
+  const float ninf = __int_as_float(0xff800000);
+  float mx = ninf;
+#pragma unroll 1
+  for (int c = 0; c < 4; c += 2) {
+    uint32_t s[64];
+    tmem_ld32(s, s_at + 32 * c);
+    tmem_ld32(s + 32, s_at + 32 * c + 32);
+    wait_ld32(s);
+    wait_ld32(s + 32);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float k = EDGE && window ? 1.f : meta.k[c + h] * qf, lv = EDGE && window ? 0.f : meta.lv[c + h];
+      float m[4] = {ninf, ninf, ninf, ninf};
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        float x = __uint_as_float(s[32 * h + i]), y = __uint_as_float(s[32 * h + i + 1]);
+        if (EDGE) {
+          const int col = 32 * (c + h) + i;
+          x = col < cmax ? x : ninf;
+          y = col + 1 < cmax ? y : ninf;
+        }
+        m[i / 2 & 3] = fmaxf(fmaxf(m[i / 2 & 3], x), y);
+      }
+      mx = fmaxf(mx, fmaf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), k, lv));
+    }
+  }
+  return mx;
+}
+
+// Weights 2^(z' - ref) of a row's columns, as fp16 over the start of S; their
+// sum over scale_v.
+template <bool EDGE>
+__device__ __forceinline__ float unit_weights(std::integral_constant<bool, EDGE>, uint32_t s_at, const Meta &meta,
+                                              float qf, float ref, bool window, int cmax) {
+  const float ninf = __int_as_float(0xff800000);
+  float l = 0.f;
+  uint32_t s[2][32];
+  tmem_ld32(s[0], s_at);
+  wait_ld32(s[0]);
+#pragma unroll 1
+  for (int c = 0; c < 4; c += 2) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      // the next 32 columns are on their way meanwhile
+      if (h == 0 || c == 0) tmem_ld32(s[h ^ 1], s_at + 32 * (c + h + 1));
+      const float k = EDGE && window ? 1.f : meta.k[c + h] * qf;
+      const float bias = (EDGE && window ? 0.f : meta.lv[c + h]) - ref;
+      const uint64_t a2 = pack64(k, k), b2 = pack64(bias, bias);
+      uint64_t sum[2] = {pack64(0.f, 0.f), pack64(0.f, 0.f)};
+      uint32_t pk[16];
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        float x, y;
+        unpack64(fma2(pack64(__uint_as_float(s[h][i]), __uint_as_float(s[h][i + 1])), a2, b2), x, y);
+        if (EDGE) {
+          const int col = 32 * (c + h) + i;
+          x = col < cmax ? x : ninf;
+          y = col + 1 < cmax ? y : ninf;
+        }
+        x = kvq::fast_exp2(x);
+        y = kvq::fast_exp2(y);
+        pk[i / 2] = kvq::h2_as_u32(__floats2half2_rn(x, y));
+        sum[i / 2 & 1] = add2(sum[i / 2 & 1], pack64(x, y));
+      }
+      float x, y;
+      unpack64(add2(sum[0], sum[1]), x, y);
+      l = fmaf(x + y, EDGE && window ? 1.f : meta.inv[c + h], l);
+      if (h == 0 || c == 0) wait_ld32(s[h ^ 1]);
+      // columns 16 .. behind the chunks already read
+      tmem_st16(s_at + 16 * (c + h), pk);
+    }
+  }
+  return l;
+}
+
 template <int D, int FMT, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
   using SM = Smem<D>;
@@ -437,7 +535,6 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = *tmem_slot;
 
   Part *const parts = reinterpret_cast<Part *>(smem + SM::PART);
   Meta *const metas = reinterpret_cast<Meta *>(smem + SM::META);
@@ -459,55 +556,71 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
   if (warp >= 12) {
     // 2 x 176 + 112 + 48 = 4 x 128, what the CTA was launched with
     regs_dec<48>();
-    if (warp == 12 && lane == 0) {
+    if (warp == 12) {
       // ================================================= the products
+      // The whole warp goes through the loop, so that addresses and
+      // descriptors are uniform, and one lane issues.  The loops over the
+      // k-steps stay rolled: unrolled, their code is fetched anew for every
+      // unit, among eleven other warps' code (385 against 315 us a chunk).
+      const bool leader = elect_one();
       constexpr uint32_t id_qk = instr_desc(kKeys, false), id_pv = instr_desc(D, true);
       uint32_t n_unit = 0;      // units issued so far
-      uint32_t np[2] = {0, 0};  // weights consumed, per row tile
+      uint32_t np0 = 0, np1 = 0;  // weights consumed, per row tile
       auto qk = [&](int t, uint32_t unit) {
-        const uint32_t q = base + SM::Q + t * SM::TILE, k = base + SM::K + (unit & 1) * SM::TILE;
-        const uint32_t qd = desc_lo(q, 16), kd = desc_lo(k, 16);
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const uint32_t off = ((i >> 2) * SM::HALF + (i & 3) * 32) >> 4;
-          mma_ss(tmem + t * 128, qd + off, kd + off, id_qk, i != 0);
+        if (leader) {
+          const uint32_t qd = desc_lo(base + SM::Q + t * SM::TILE, 16);
+          const uint32_t kd = desc_lo(base + SM::K + (unit & 1) * SM::TILE, 16);
+#pragma unroll 2
+          for (int i = 0; i < D / 16; ++i) {
+            const uint32_t off = ((i >> 2) * SM::HALF + (i & 3) * 32) >> 4;
+            mma_ss(kS + t * 128, qd + off, kd + off, id_qk, i != 0);
+          }
+          commit(base + SM::BAR + (kSFull + t) * 8);
         }
-        commit(base + SM::BAR + (kSFull + t) * 8);
       };
       auto pv = [&](int t, uint32_t unit, bool add) {
-        const uint32_t vd = desc_lo(base + SM::V + (unit & 1) * SM::TILE, SM::HALF);
-#pragma unroll
-        for (int i = 0; i < kKeys / 16; ++i)
-          mma_ts(tmem + 256 + t * 128, tmem + t * 128 + i * 8, vd + i * (2048 >> 4), id_pv, add || i != 0);
-        commit(base + SM::BAR + (kOFull + t) * 8);
+        if (leader) {
+          const uint32_t vd = desc_lo(base + SM::V + (unit & 1) * SM::TILE, SM::HALF);
+#pragma unroll 2
+          for (int i = 0; i < kKeys / 16; ++i)
+            mma_ts(kO + t * 128, kS + t * 128 + i * 8, vd + i * (2048 >> 4), id_pv, add || i != 0);
+          commit(base + SM::BAR + (kOFull + t) * 8);
+        }
+      };
+      auto free_stage = [&](int bar) {
+        if (leader) commit(base + SM::BAR + bar * 8);
       };
       bool ok = true;
       for (uint32_t n_part = 0; ok; ++n_part) {
-        ok = wait(kPartFull + n_part % kParts, (n_part / kParts) & 1);
+        ok = __all_sync(kAll, wait(kPartFull + n_part % kParts, (n_part / kParts) & 1));
         if (!ok) break;
         const Part &p = parts[n_part % kParts];
         const int units = p.u1 - p.u0, tiles = p.n * a.group - p.row > 128 ? 2 : 1;
-        kvq::mbar_arrive(bars + kPartFree + n_part % kParts);
+        __syncwarp();
+        if (leader) kvq::mbar_arrive(bars + kPartFree + n_part % kParts);
         if (units == 0) break;
-        ok = wait(kQFull, n_part & 1) && wait(kKFull + (n_unit & 1), (n_unit >> 1) & 1);
+        ok = __all_sync(kAll, wait(kQFull, n_part & 1) && wait(kKFull + (n_unit & 1), (n_unit >> 1) & 1));
         if (!ok) break;
         fence_after();
         for (int t = 0; t < tiles; ++t) qk(t, n_unit);
-        commit(base + SM::BAR + (kKEmpty + (n_unit & 1)) * 8);
+        free_stage(kKEmpty + (n_unit & 1));
         for (int u = 0; u < units && ok; ++u, ++n_unit) {
+          const bool more = u + 1 < units;
           ok = wait(kVFull + (n_unit & 1), (n_unit >> 1) & 1);
-          if (ok && u + 1 < units) ok = wait(kKFull + ((n_unit + 1) & 1), ((n_unit + 1) >> 1) & 1);
+          if (ok && more) ok = wait(kKFull + ((n_unit + 1) & 1), ((n_unit + 1) >> 1) & 1);
+          ok = __all_sync(kAll, ok);
           for (int t = 0; t < tiles && ok; ++t) {
-            ok = wait(kPFull + t, np[t] & 1);
+            ok = __all_sync(kAll, wait(kPFull + t, (t ? np1 : np0) & 1));
             if (!ok) break;
-            ++np[t];
             fence_after();
             pv(t, n_unit, u != 0);
-            if (u + 1 < units) qk(t, n_unit + 1);
+            if (more) qk(t, n_unit + 1);
           }
           if (!ok) break;
-          commit(base + SM::BAR + (kVEmpty + (n_unit & 1)) * 8);
-          if (u + 1 < units) commit(base + SM::BAR + (kKEmpty + ((n_unit + 1) & 1)) * 8);
+          ++np0;
+          if (tiles == 2) ++np1;
+          free_stage(kVEmpty + (n_unit & 1));
+          if (more) free_stage(kKEmpty + ((n_unit + 1) & 1));
         }
       }
     } else if (warp == 13 && lane == 0) {
@@ -746,8 +859,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
     regs_inc<176>();
     const int t = warp >> 2;         // row tile
     const int r = tid & 127;         // row of the tile = lane of tensor memory
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21);
-    const uint32_t s_at = lanes + t * 128, o_at = lanes + 256 + t * 128;
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
+    const uint32_t s_at = lanes + kS + t * 128, o_at = lanes + kO + t * 128;
     uint32_t n_unit = 0;  // units so far
     uint32_t n_own = 0;   // units of this row tile so far
     bool ok = true;
@@ -822,7 +935,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
             for (int c = 0; c < kKeys; c += 16) {
               uint32_t z[16];
               tmem_ld16(z, s_at + c);
-              wait_ld();
+              wait_ld16(z);
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
                 float x = __uint_as_float(z[i]) * (col[c + i] * qf) + col[kKeys + c + i];
@@ -833,36 +946,9 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
             }
             wait_st();
           }
-          uint32_t sr[128];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(sr + 32 * c, s_at + 32 * c);
-          wait_ld();
-          float mx = ninf;
-          if (!edge) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              float m0 = __uint_as_float(sr[32 * c]), m1 = __uint_as_float(sr[32 * c + 1]);
-#pragma unroll
-              for (int i = 2; i < 32; i += 2) {
-                m0 = fmaxf(m0, __uint_as_float(sr[32 * c + i]));
-                m1 = fmaxf(m1, __uint_as_float(sr[32 * c + i + 1]));
-              }
-              mx = fmaxf(mx, fmaf(fmaxf(m0, m1), meta.k[c] * qf, meta.lv[c]));
-            }
-          } else {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const float k = window ? 1.f : meta.k[c] * qf, lv = window ? 0.f : meta.lv[c];
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const int cl = 32 * c + i;
-                float z = fmaf(__uint_as_float(sr[cl]), k, lv);
-                z = cl < cmax ? z : ninf;
-                sr[cl] = __float_as_uint(z);
-                mx = fmaxf(mx, z);
-              }
-            }
-          }
+          // ---- the maximum
+          const float mx = edge ? unit_max(std::true_type{}, s_at, meta, qf, window, cmax)
+                                : unit_max(std::false_type{}, s_at, meta, qf, window, cmax);
           // ---- the reference M, and O where it moved
           const bool move = mx > M + kGrow || (M == ninf && mx > ninf);
           if (__any_sync(kAll, move)) {
@@ -878,7 +964,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
               for (int c = 0; c < D / 16; ++c) {
                 uint32_t o[16];
                 tmem_ld16(o, o_at + 16 * c);
-                wait_ld();
+                wait_ld16(o);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
                 tmem_st16(o_at + 16 * c, o);
@@ -891,33 +977,16 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
             for (int c = 0; c < kKeys; c += 16) {
               uint32_t z[16];
               tmem_ld16(z, s_at + c);
-              wait_ld();
+              wait_ld16(z);
 #pragma unroll
               for (int i = 0; i < 16; ++i)
                 l = fmaf(c + i < cmax ? kvq::fast_exp2(__uint_as_float(z[i]) - ref) : 0.f, col[2 * kKeys + c + i], l);
             }
           }
           // ---- weights
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float k = edge ? 1.f : meta.k[c] * qf, bias = (edge ? 0.f : meta.lv[c]) - ref;
-            const uint64_t a2 = pack64(k, k), b2 = pack64(bias, bias);
-            uint64_t sum = pack64(0.f, 0.f);
-            uint32_t pk[16];
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              float x, y;
-              unpack64(fma2(pack64(__uint_as_float(sr[32 * c + i]), __uint_as_float(sr[32 * c + i + 1])), a2, b2), x, y);
-              x = kvq::fast_exp2(x);
-              y = kvq::fast_exp2(y);
-              pk[i / 2] = kvq::h2_as_u32(__floats2half2_rn(x, y));
-              sum = add2(sum, pack64(x, y));
-            }
-            float x, y;
-            unpack64(sum, x, y);
-            if (!window) l = fmaf(x + y, meta.inv[c], l);
-            tmem_st16(s_at + 16 * c, pk);
-          }
+          const float sum = edge ? unit_weights(std::true_type{}, s_at, meta, qf, ref, window, cmax)
+                                 : unit_weights(std::false_type{}, s_at, meta, qf, ref, window, cmax);
+          if (!window) l += sum;
           wait_st();
           fence_before();
           kvq::mbar_arrive(bars + kPFull + t);
@@ -941,7 +1010,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
           tmem_ld32(o, o_at + 32 * c);
-          wait_ld();
+          wait_ld32(o);
           if (whole) {
             if (valid) {
 #pragma unroll
@@ -1026,7 +1095,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
   __syncthreads();
   if (warp == 12) {
     fence_after();
-    tmem_free(tmem);
+    tmem_free(*tmem_slot);
   }
 }
 
