@@ -30,9 +30,10 @@
 // fp16's range as in the rows kernel; bf16 window tokens scaled token by token
 // (the factors enter z and M like the blocks' scales).
 //
-// The keys of all items form one line of 128-token units which is cut into
-// one equal range per SM; items cut by a border are merged by the last CTA
-// that finishes (fp32 partial O, M and l in the workspace).
+// The keys of all items form one line of 128-token units, with kOver more for
+// what an item costs by itself, which is cut into one equal range per SM; items
+// cut by a border are merged by the last CTA that finishes (fp32 partial O, M
+// and l in the workspace).
 //
 // Bound: the tensor cores (4 D flop per row and key; 128 x 128 x 128 twice per
 // row tile and unit).
@@ -51,6 +52,7 @@ constexpr int kThreads = 512;
 constexpr int kRows = kTileRows;  // 256 rows of an item
 constexpr int kKeys = 128;        // tokens of a unit
 constexpr int kMetas = 8, kParts = 4, kCols = 4;
+constexpr int kOver = 3;          // queries and outputs of an item cost about as much as three units
 constexpr float kGrow = 6.f;      // how far the maximum may pass M
 constexpr float kShift = 9.f;     // w = 2^(z' - M + kShift) <= 2^15
 
@@ -74,7 +76,7 @@ struct Smem {
 // two units before those are done, and the softmax of the unit before that.
 enum { kPacked, kWindow, kEnd };
 struct Meta {
-  long long off[4];           // pool offset of each group of 32 tokens' block, or -1: zeros
+  long long off[4];           // pool offset of each group of 32 tokens' keys, or -1: zeros
   float k[4], lv[4], inv[4];  // scales of keys, log2 and inverse of those of values
   long long win;              // window offset of the (sequence, head)
   int kind;                   // kPacked, kWindow or kEnd
@@ -224,6 +226,11 @@ __device__ __forceinline__ void regs_dec() {
 __device__ __forceinline__ void sts16(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
 __device__ __forceinline__ uint64_t pack64(float x, float y) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
@@ -289,20 +296,23 @@ __device__ __forceinline__ Pair pair_of_slot(const AttnArgs &a, int slot) {
   return make_pair(a, s, slot - base(s));
 }
 
+// An item's kOver + units line positions; unit u is at start + kOver + u.
 struct Walk {
   Pair p;
-  int h, u0, u1;           // KV head and units of the current part
-  long long at, end;       // line position, end of the CTA's range
-  long long start;         // line position of the item's unit 0
+  int h, u0, u1;    // KV head and units of the current part
+  long long start;  // the item's first line position
+  long long lo, end;
 
-  __device__ __forceinline__ void part() {
-    u1 = static_cast<int>(min(static_cast<long long>(p.units), u0 + (end - at)));
-    start = at - u0;
+  // the part of the range in this item; false: the range ends before its units
+  __device__ __forceinline__ bool part() {
+    const long long first = start + kOver;
+    u0 = static_cast<int>(max(lo - first, 0ll));
+    u1 = static_cast<int>(min(static_cast<long long>(p.units), end - first));
+    return u1 > u0;
   }
   __device__ __forceinline__ bool next(const AttnArgs &a) {
-    at += u1 - u0;
-    if (at >= end) return false;
-    u0 = 0;
+    start += kOver + p.units;
+    if (start + kOver >= end) return false;
     if (++h >= a.geo.H) {
       h = 0;
       int s = p.s, rt = p.rt + 1;
@@ -313,10 +323,13 @@ struct Walk {
         if (++s >= a.geo.S) return false;
       }
     }
-    part();
-    return true;
+    return part();
   }
 };
+// Line positions of a pair's items.
+__device__ __forceinline__ long long line_of(const Pair &p, int H) {
+  return p.units ? static_cast<long long>(p.units + kOver) * H : 0;
+}
 
 // Sum over the CTA, and each thread's exclusive prefix.
 __device__ __forceinline__ long long cta_scan(long long v, long long &before, long long *buf) {
@@ -356,6 +369,14 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi) {
         : "=r"(lo), "=r"(hi)
         : "r"(w));
   }
+}
+
+// Bits of the largest magnitude of eight bf16 numbers (a row with an infinity
+// or a NaN gives NaN whatever its scale).
+__device__ __forceinline__ uint32_t mag_max8(const uint4 &x) {
+  const uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                              __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+  return max(m & 0xffffu, m >> 16);
 }
 
 // Eight bf16 numbers, scaled, as fp16.
@@ -481,20 +502,20 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
     long long sum = 0;
     for (int i = tid; i < slots; i += kThreads) {
       mine = pair_of_slot(a, i);
-      sum += static_cast<long long>(mine.units) * H;
+      sum += line_of(mine, H);
     }
     long long before;
     total = cta_scan(sum, before, scan_buf);
   }
   if (total == 0) return;
-  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + 3) / 4));
+  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + 7) / 8));
   if (static_cast<int>(blockIdx.x) >= ctas) return;
   const long long lo = blockIdx.x * total / ctas, hi = (blockIdx.x + 1) * total / ctas;
   {
     long long at = 0;
     for (int i0 = 0; i0 < slots; i0 += kThreads) {
       if (i0 + tid < slots && slots > kThreads) mine = pair_of_slot(a, i0 + tid);
-      const long long u = i0 + tid < slots ? static_cast<long long>(mine.units) * H : 0;
+      const long long u = i0 + tid < slots ? line_of(mine, H) : 0;
       long long before;
       const long long sum = cta_scan(u, before, scan_buf);
       if (lo >= at + before && lo < at + before + u) {
@@ -539,23 +560,35 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
   Part *const parts = reinterpret_cast<Part *>(smem + SM::PART);
   Meta *const metas = reinterpret_cast<Meta *>(smem + SM::META);
   // A wait of a role; false ends the role (another one's wait ran out, or this).
-  auto wait = [&](int bar, uint32_t parity) -> bool {
-    if (kvq::mbar_try_wait(bars + bar, parity)) return true;
-    const long long since = clock64();
-    while (!kvq::mbar_try_wait(bars + bar, parity)) {
+  auto wait = [&](int bar, uint32_t parity, unsigned nap = 0) -> bool {
+    long long since = 0;
+    for (;;) {
+#pragma unroll 1
+      for (int i = 0; i < 256; ++i) {
+        if (kvq::mbar_try_wait(bars + bar, parity)) return true;
+        if (nap) __nanosleep(nap);
+      }
       if (*dead) return false;
-      if (clock64() - since > kvq::kWaitLimitCycles) {
+      const long long now = clock64();
+      if (since == 0) since = now;
+      if (now - since > kvq::kWaitLimitCycles) {
         *dead = 1;
         set_status(geo.status, KVQ_STATUS_TIMEOUT);
         return false;
       }
     }
-    return true;
+  };
+  // The same for all `threads` threads of a role: its first warp polls, the
+  // others wait at barrier `id`.  Most roles wait most of the time, and what a
+  // polling warp issues is missing to the working ones.
+  auto wait_all = [&](int bar, uint32_t parity, bool first, int id, int threads, bool ok) -> bool {
+    if (first) ok = ok && wait(bar, parity);
+    return bar_all(id, threads, ok);
   };
 
   if (warp >= 12) {
-    // 2 x 176 + 112 + 48 = 4 x 128, what the CTA was launched with
-    regs_dec<48>();
+    // 2 x 144 + 112 + 80 <= 4 x 128, what the CTA was launched with
+    regs_dec<80>();
     if (warp == 12) {
       // ================================================= the products
       // The whole warp goes through the loop, so that addresses and
@@ -607,14 +640,20 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
         for (int u = 0; u < units && ok; ++u, ++n_unit) {
           const bool more = u + 1 < units;
           ok = wait(kVFull + (n_unit & 1), (n_unit >> 1) & 1);
-          if (ok && more) ok = wait(kKFull + ((n_unit + 1) & 1), ((n_unit + 1) >> 1) & 1);
           ok = __all_sync(kAll, ok);
           for (int t = 0; t < tiles && ok; ++t) {
             ok = __all_sync(kAll, wait(kPFull + t, (t ? np1 : np0) & 1));
             if (!ok) break;
             fence_after();
             pv(t, n_unit, u != 0);
-            if (more) qk(t, n_unit + 1);
+            if (more) {
+              if (t == 0) {
+                ok = __all_sync(kAll, wait(kKFull + ((n_unit + 1) & 1), ((n_unit + 1) >> 1) & 1));
+                if (!ok) break;
+                fence_after();
+              }
+              qk(t, n_unit + 1);
+            }
           }
           if (!ok) break;
           ++np0;
@@ -627,14 +666,13 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       // ================================================= the walk
       Walk use;
       use.p = pair_of_slot(a, static_cast<int>(found[0]));
-      use.h = static_cast<int>(found[1] / use.p.units);
-      use.u0 = static_cast<int>(found[1] - static_cast<long long>(use.h) * use.p.units);
-      use.at = lo;
+      use.h = static_cast<int>(found[1] / (use.p.units + kOver));
+      use.start = lo - (found[1] - static_cast<long long>(use.h) * (use.p.units + kOver));
+      use.lo = lo;
       use.end = hi;
-      use.part();
-      bool more = true;
+      bool more = use.part();
       for (uint32_t n_part = 0;; ++n_part) {
-        if (n_part >= kParts && !wait(kPartFree + n_part % kParts, ((n_part / kParts) & 1) ^ 1)) break;
+        if (n_part >= kParts && !wait(kPartFree + n_part % kParts, ((n_part / kParts) & 1) ^ 1, 200)) break;
         Part &p = parts[n_part % kParts];
         p.u0 = more ? use.u0 : 0;
         p.u1 = more ? use.u1 : 0;
@@ -649,13 +687,14 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           p.s = use.p.s;
           p.slot = -1;
           if (use.u0 != 0 || use.u1 != use.p.units) {
-            const long long s0 = use.start, s1 = s0 + use.p.units;  // the item's place on the line
+            const long long unit0 = use.start + kOver;
             auto owner = [&](long long pos) { return static_cast<int>(((pos + 1) * ctas - 1) / total); };
-            const int c0 = owner(s0);
-            p.slot = 2 * blockIdx.x + (s0 + use.u0 == lo ? 0 : 1);
+            const int c0 = owner(unit0);
             p.c0 = c0;
-            p.cuts = owner(s1 - 1) - c0;
-            p.first = 2 * c0 + (c0 * total / ctas < s0 ? 1 : 0);  // later CTAs begin with their part
+            p.cuts = owner(unit0 + use.p.units - 1) - c0;
+            // a CTA has partial slots for its range's first part and its last one
+            p.slot = 2 * blockIdx.x + (lo < use.start ? 1 : 0);
+            p.first = 2 * c0 + (c0 * total / ctas < use.start ? 1 : 0);
           }
         }
         kvq::mbar_arrive(bars + kPartFull + n_part % kParts);
@@ -667,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       uint32_t n_unit = 0;
       bool ok = true;
       auto slot_free = [&]() {
-        if (n_unit >= kMetas) ok = __all_sync(kAll, wait(kMetaFree + n_unit % kMetas, ((n_unit / kMetas) & 1) ^ 1));
+        if (n_unit >= kMetas) ok = __all_sync(kAll, wait(kMetaFree + n_unit % kMetas, ((n_unit / kMetas) & 1) ^ 1, 100));
         return ok;
       };
       auto publish = [&]() {
@@ -690,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
             const int e = geo.table[static_cast<size_t>(p.s) * geo.max_blocks + tok / B];
             if (e >= 0 && e < geo.num_blocks) {
               const long long bh = static_cast<long long>(e) * H + p.h;
-              off = bh * 2 * B * D;
+              off = bh * 2 * B * D + (tok & (B - 1)) * D;
               sc = *reinterpret_cast<const float2 *>(geo.scales + bh * 2);
             } else {
               set_status(geo.status, KVQ_STATUS_BAD_BLOCK);
@@ -734,40 +773,36 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
   } else if (warp >= 8) {
     // =================================================== keys and values
     regs_dec<112>();
-    const int ct = tid - 256;                  // 0 .. 127
-    constexpr int CPR = D / 16;                // 16-code chunks of a token
-    constexpr int RPI = 128 / CPR;             // tokens per instruction: 16 or 32
-    constexpr int NI = 128 / RPI;              // instructions per unit
-    const int cr = ct / CPR, cc = ct % CPR;
+    const int ct = tid & 127;
+    // Four threads take 64 bytes of a token, a warp eight tokens: with the
+    // swizzle, eight threads' 16-byte stores meet eight bank groups.
+    constexpr int CH = D / 64;                 // 64-byte pieces of a token's codes
+    constexpr int NI = 4 * CH;                 // pieces per thread
+    const int cr = ct >> 2, cc = ct & 3;       // token among 32, 16-byte chunk of the piece
+    const uint32_t at0 = place(cr, 2 * cc), at1 = place(cr, 2 * cc + 1);
     uint4 kb[NI], vb[NI];
 
-    auto load = [&](uint4 *buf, const Meta &m, int extra) {
+    const uint8_t *const codes = geo.codes + cr * D + cc * 16;
+    auto load = [&](uint4 *buf, const Meta &m, int values) {
+      const uint8_t *src = codes + values * B * D;
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const long long off = m.off[i * RPI / 32];
+        const long long off = m.off[i / CH];
         buf[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (off >= 0)
-          buf[i] = __ldg(reinterpret_cast<const uint4 *>(geo.codes + off + extra +
-                                                         ((i * RPI + cr) & (B - 1)) * D + cc * 16));
+        if (off >= 0) buf[i] = __ldg(reinterpret_cast<const uint4 *>(src + off + (i % CH) * 64));
       }
     };
-    // `flush`: groups of 32 tokens that are stored as zeros
-    auto store = [&](uint32_t dst, const uint4 *buf, int flush) {
+    auto store = [&](uint32_t dst, const uint4 *buf) {
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const int row = i * RPI + cr;
-        uint4 x = buf[i];
-        if (flush >> (i * RPI / 32) & 1) x = make_uint4(0u, 0u, 0u, 0u);
         uint32_t e[8];
-        widen4<FMT>(x.x, e[0], e[1]);
-        widen4<FMT>(x.y, e[2], e[3]);
-        widen4<FMT>(x.z, e[4], e[5]);
-        widen4<FMT>(x.w, e[6], e[7]);
-        // the two chunks in an order that keeps eight threads' stores in eight bank groups
-        const bool swap = D == 128 && cc >= 4;
-        const uint32_t a0 = dst + place(row, 2 * cc), a1 = dst + place(row, 2 * cc + 1);
-        sts16(swap ? a1 : a0, swap ? e[4] : e[0], swap ? e[5] : e[1], swap ? e[6] : e[2], swap ? e[7] : e[3]);
-        sts16(swap ? a0 : a1, swap ? e[0] : e[4], swap ? e[1] : e[5], swap ? e[2] : e[6], swap ? e[3] : e[7]);
+        widen4<FMT>(buf[i].x, e[0], e[1]);
+        widen4<FMT>(buf[i].y, e[2], e[3]);
+        widen4<FMT>(buf[i].z, e[4], e[5]);
+        widen4<FMT>(buf[i].w, e[6], e[7]);
+        const uint32_t at = dst + (i / CH) * 4096 + (i % CH) * SM::HALF;
+        sts16(at + at0, e[0], e[1], e[2], e[3]);
+        sts16(at + at1, e[4], e[5], e[6], e[7]);
       }
     };
     // One window token (thread ct's) of keys or values: what scales it.
@@ -776,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       bad = false;
       f = 1.f;
       if (!valid) return;
-#pragma unroll 1
+#pragma unroll 4
       for (int c = 0; c < D / 8; ++c) {
         const uint4 x = *reinterpret_cast<const uint4 *>(src + 8 * c);
         const uint32_t e[4] = {x.x, x.y, x.z, x.w};
@@ -792,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       if (BF16 && big) f = __int_as_float((268 - max(static_cast<int>(big >> 7), 20)) << 23);
     };
     auto store_window = [&](uint32_t dst, const uint16_t *src, bool zero, float f) {
-#pragma unroll 1
+#pragma unroll 4
       for (int c = 0; c < D / 8; ++c) {
         uint4 x = make_uint4(0u, 0u, 0u, 0u);
         if (!zero) x = *reinterpret_cast<const uint4 *>(src + 8 * c);
@@ -801,13 +836,14 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       }
     };
 
-    bool ok = wait(kMetaFull, 0);
+    const bool first = warp == 8;
+    bool ok = true;
     int kind = kEnd;
-    if (bar_all(1, 128, ok)) {
+    if (wait_all(kMetaFull, 0, first, 1, 128, true)) {
       kind = metas[0].kind;
       if (kind == kPacked) {
         load(kb, metas[0], 0);
-        load(vb, metas[0], B * D);
+        load(vb, metas[0], 1);
       }
     }
     for (uint32_t n_unit = 0; kind != kEnd; ++n_unit) {
@@ -817,10 +853,9 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       const Meta &m = metas[n_unit % kMetas], &m1 = metas[(n_unit + 1) % kMetas];
       float vf = 1.f;
       bool vzero = true;
-      if (n_unit >= 2) ok = wait(kKEmpty + st, reuse);
-      if (!bar_all(1, 128, ok)) break;
+      if (n_unit >= 2 && !wait_all(kKEmpty + st, reuse, first, 1, 128, true)) break;
       if (kind == kPacked) {
-        store(kd, kb, 0);
+        store(kd, kb);
       } else {
         float *col = reinterpret_cast<float *>(smem + SM::COL) + (n_unit % kCols) * 3 * kKeys + ct;
         const uint16_t *ks = geo.k_win + m.win + ct * D, *vs = geo.v_win + m.win + ct * D;
@@ -840,34 +875,45 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       kvq::mbar_arrive(bars + kKFull + st);
       if (ct == 0 && n_unit >= 3) kvq::mbar_arrive(bars + kMetaFree + (n_unit - 3) % kMetas);
       // the next unit's keys, and its values once this one's are stored
-      ok = wait(kMetaFull + (n_unit + 1) % kMetas, ((n_unit + 1) / kMetas) & 1);
-      const int next = ok ? m1.kind : static_cast<int>(kEnd);
-      if (next == kPacked) load(kb, m1, 0);
-      if (ok && n_unit >= 2) ok = wait(kVEmpty + st, reuse);
+      if (first) {
+        ok = wait(kMetaFull + (n_unit + 1) % kMetas, ((n_unit + 1) / kMetas) & 1);
+        if (ok && n_unit >= 2) ok = wait(kVEmpty + st, reuse);
+      }
       if (!bar_all(1, 128, ok)) break;
-      if (kind == kPacked)
-        store(vd, vb, m.flush);
-      else
+      const int next = m1.kind;
+      if (next == kPacked) load(kb, m1, 0);
+      if (kind == kPacked) {
+        const int flush = m.flush;  // groups of 32 tokens whose values are stored as zeros
+        if (flush) {
+#pragma unroll
+          for (int i = 0; i < NI; ++i)
+            if (flush >> (i / CH) & 1) vb[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        store(vd, vb);
+      } else {
         store_window(vd, geo.v_win + m.win + ct * D, vzero, vf);
+      }
       kvq::fence_proxy_async();
       kvq::mbar_arrive(bars + kVFull + st);
-      if (next == kPacked) load(vb, m1, B * D);
+      if (next == kPacked) load(vb, m1, 1);
       kind = next;
     }
   } else {
     // =================================================== softmax
-    regs_inc<176>();
+    regs_inc<144>();
     const int t = warp >> 2;         // row tile
     const int r = tid & 127;         // row of the tile = lane of tensor memory
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
     const uint32_t s_at = lanes + kS + t * 128, o_at = lanes + kO + t * 128;
     uint32_t n_unit = 0;  // units so far
     uint32_t n_own = 0;   // units of this row tile so far
+    // copies of whole rows: LPR lanes a row, RPI rows at a time, NQ times for the warp's 32
+    constexpr int LPR = D / 8, RPI = 32 / LPR, NQ = 32 / RPI;
     bool ok = true;
     for (uint32_t n_part = 0;; ++n_part) {
       // all eight warps go on together, or leave together
-      ok = ok && wait(kPartFull + n_part % kParts, (n_part / kParts) & 1);
-      if (!bar_all(2, 256, ok)) break;
+      ok = wait_all(kPartFull + n_part % kParts, (n_part / kParts) & 1, warp == 0, 2, 256, ok);
+      if (!ok) break;
       const Part &p = parts[n_part % kParts];
       const int u0 = p.u0, u1 = p.u1;
       if (u0 == u1) break;
@@ -878,37 +924,34 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       const int tok = valid ? row / a.group : 0;
       const int lim = valid ? p.L - p.n + tok : -1;  // last position the row sees
 
-      // ---- the row's query to shared memory
+      // ---- the warp's 32 queries to shared memory: LPR lanes bring a row
+      const long long head = static_cast<long long>(p.h) * a.group + (valid ? row - tok * a.group : 0);
+      const long long q_off = valid ? (static_cast<long long>(p.row0) + tok) * a.q.row + head * a.q.head : -1;
       float qf = a.zscale;
       if (active) {
-        const uint16_t *src = a.q.p + (static_cast<long long>(p.row0) + tok) * a.q.row +
-                              (static_cast<long long>(p.h) * a.group + (valid ? row - tok * a.group : 0)) * a.q.head;
         const uint32_t dst = base + SM::Q + t * SM::TILE;
-        float f = 1.f;
-        if (BF16 && valid) {
-          uint32_t big = 0;
-#pragma unroll 4
-          for (int c = 0; c < D / 8; ++c) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(src + 8 * c);
-            const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+        uint4 x[NQ];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t l16 = e[i] & 0x7fffu, h16 = (e[i] >> 16) & 0x7fffu;
-              big = max(big, l16 < 0x7f80u ? l16 : 0u);
-              big = max(big, h16 < 0x7f80u ? h16 : 0u);
-            }
+        for (int i = 0; i < NQ; ++i) {
+          const long long off = __shfl_sync(kAll, q_off, i * RPI + lane / LPR);
+          x[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (off >= 0) x[i] = *reinterpret_cast<const uint4 *>(a.q.p + off + lane % LPR * 8);
+        }
+        int mine = 0;
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+          if (BF16) {
+            uint32_t big = mag_max8(x[i]);
+#pragma unroll
+            for (int o = 1; o < LPR; o <<= 1) big = max(big, __shfl_xor_sync(kAll, big, o));
+            const int e = big ? min(max(static_cast<int>(big >> 7), 20), 254) : 141;
+            x[i] = bf16_row_to_fp16(x[i], __int_as_float((268 - e) << 23));
+            const int of_row = __shfl_sync(kAll, e, lane % RPI * LPR);
+            if (lane / RPI == i) mine = of_row;
           }
-          const int e = max(static_cast<int>(big >> 7), 20);
-          f = __int_as_float((268 - e) << 23);
-          qf *= __int_as_float((e - 14) << 23);
+          sts16(dst + place(32 * (warp & 3) + i * RPI + lane / LPR, lane % LPR), x[i].x, x[i].y, x[i].z, x[i].w);
         }
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          uint4 x = make_uint4(0u, 0u, 0u, 0u);
-          if (valid) x = *reinterpret_cast<const uint4 *>(src + 8 * c);
-          if (BF16) x = bf16_row_to_fp16(x, f);
-          sts16(dst + place(r, c), x.x, x.y, x.z, x.w);
-        }
+        if (BF16) qf *= __int_as_float((mine - 14) << 23);
         kvq::fence_proxy_async();
       }
       fence_before();
@@ -1000,8 +1043,28 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       const bool whole = slot < 0;
       float4 *part = reinterpret_cast<float4 *>(a.tile_o) + static_cast<size_t>(max(slot, 0)) * (D / 4) * kRows +
                      t * 128 + r;
-      uint16_t *dst = a.out.p + (static_cast<long long>(p.row0) + tok) * a.out.row +
-                      (static_cast<long long>(p.h) * a.group + (valid ? row - tok * a.group : 0)) * a.out.head;
+      const long long out_off = valid ? (static_cast<long long>(p.row0) + tok) * a.out.row + head * a.out.head : -1;
+      // Outputs go through the queries' place, which the products are done
+      // with, so that whole rows are stored: 32 channels of the thread's row
+      // from channel 32 c on, then the warp's rows.
+      const uint32_t stage = base + SM::Q + t * SM::TILE;
+      auto put = [&](int c, const float *o, float f) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          sts16(stage + place(r, 4 * c + k), pack2<BF16>(o[8 * k] * f, o[8 * k + 1] * f),
+                pack2<BF16>(o[8 * k + 2] * f, o[8 * k + 3] * f), pack2<BF16>(o[8 * k + 4] * f, o[8 * k + 5] * f),
+                pack2<BF16>(o[8 * k + 6] * f, o[8 * k + 7] * f));
+      };
+      auto store_rows = [&]() {
+        __syncwarp();
+#pragma unroll 4
+        for (int i = 0; i < NQ; ++i) {
+          const long long off = __shfl_sync(kAll, out_off, i * RPI + lane / LPR);
+          const uint4 x = lds16(stage + place(32 * (warp & 3) + i * RPI + lane / LPR, lane % LPR));
+          if (off >= 0) *reinterpret_cast<uint4 *>(a.out.p + off + lane % LPR * 8) = x;
+        }
+        __syncwarp();
+      };
       if (active && ok) ok = __all_sync(kAll, wait(kOFull + t, (n_own - 1) & 1));
       if (active && ok) {
         fence_after();
@@ -1012,18 +1075,10 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           tmem_ld32(o, o_at + 32 * c);
           wait_ld32(o);
           if (whole) {
-            if (valid) {
+            float x[32];
 #pragma unroll
-              for (int i = 0; i < 32; i += 8) {
-                uint32_t w[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const float x = __uint_as_float(o[i + 2 * k]), y = __uint_as_float(o[i + 2 * k + 1]);
-                  w[k] = l == 0.f ? 0u : pack2<BF16>(x * inv, y * inv);
-                }
-                *reinterpret_cast<uint4 *>(dst + 32 * c + i) = make_uint4(w[0], w[1], w[2], w[3]);
-              }
-            }
+            for (int i = 0; i < 32; ++i) x[i] = l == 0.f ? 0.f : __uint_as_float(o[i]);
+            put(c, x, l == 0.f ? 0.f : inv);
           } else {
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
@@ -1032,7 +1087,10 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
                               __uint_as_float(o[i + 3]));
           }
         }
-        if (!whole) a.tile_ml[slot * kRows + t * 128 + r] = make_float2(M, l);
+        if (whole)
+          store_rows();
+        else
+          a.tile_ml[slot * kRows + t * 128 + r] = make_float2(M, l);
         fence_before();
       }
       if (!whole) {
@@ -1047,7 +1105,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
         bar_sync(2, 256);
         const bool merge = *flag;
         bar_sync(2, 256);  // read before it is set again
-        if (merge && valid) {
+        if (merge && active) {
           __threadfence();
           const int first = p.first, c0 = p.c0, n = p.cuts + 1;
           auto slot_of = [&](int i) { return i == 0 ? first : 2 * (c0 + i); };
@@ -1060,30 +1118,30 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           }
           const float inv = ll == 0.f ? 0.f : 1.f / ll;
 #pragma unroll 1
-          for (int c = 0; c < D / 16; ++c) {
-            float o[16];
+          for (int c = 0; c < D / 32; ++c) {
+            float o[32];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] = 0.f;
+            for (int k = 0; k < 32; ++k) o[k] = 0.f;
+#pragma unroll 1
             for (int i = 0; i < n; ++i) {
               const int sl = slot_of(i);
-              const float f = kvq::fast_exp2(__ldcg(&a.tile_ml[sl * kRows + t * 128 + r]).x - ref) * inv;
               const float4 *src = reinterpret_cast<const float4 *>(a.tile_o) +
-                                  (static_cast<size_t>(sl) * (D / 4) + 4 * c) * kRows + t * 128 + r;
+                                  (static_cast<size_t>(sl) * (D / 4) + 8 * c) * kRows + t * 128 + r;
+              float4 x[8];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float4 x = __ldcg(src + static_cast<size_t>(k) * kRows);
-                o[4 * k] += x.x * f;
-                o[4 * k + 1] += x.y * f;
-                o[4 * k + 2] += x.z * f;
-                o[4 * k + 3] += x.w * f;
+              for (int k = 0; k < 8; ++k) x[k] = __ldcg(src + static_cast<size_t>(k) * kRows);
+              const float f = kvq::fast_exp2(__ldcg(&a.tile_ml[sl * kRows + t * 128 + r]).x - ref) * inv;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                o[4 * k] += x[k].x * f;
+                o[4 * k + 1] += x[k].y * f;
+                o[4 * k + 2] += x[k].z * f;
+                o[4 * k + 3] += x[k].w * f;
               }
             }
-#pragma unroll
-            for (int k = 0; k < 16; k += 8)
-              *reinterpret_cast<uint4 *>(dst + 16 * c + k) =
-                  make_uint4(pack2<BF16>(o[k], o[k + 1]), pack2<BF16>(o[k + 2], o[k + 3]),
-                             pack2<BF16>(o[k + 4], o[k + 5]), pack2<BF16>(o[k + 6], o[k + 7]));
+            put(c, o, 1.f);
           }
+          store_rows();
         }
       }
       __syncwarp();
