@@ -3,18 +3,23 @@
 // KV head share its keys).
 //
 // Mathematics: for each row an online softmax over 32-token units (16 in the
-// 16-bit window): z = (q . k_code) * scale_k * softmax_scale * log2(e), m the
-// running maximum, p = 2^(z - m + 15), l the sum of p, o the sum of
-// scale_v * (p . v_code).  Codes are exact in fp16, so both products run on
-// mma.sync m16n8k16 with fp32 accumulators: rows are M, tokens N of the first
-// product and K of the second, whose A operand is the first one's accumulator
-// fragment as it lies in registers.  Roundings to 16 bits: p to fp16 (the factor
-// 2^15, taken back where o and l are formed, keeps weights down to 2^-29 of the
-// largest at full precision), and bf16 queries, which a power of two per row
-// brings into fp16's range: a rounding only of elements 2^-29 below the row's
-// largest.  Window tokens in bf16 are multiplied as they are (mma in bf16), so
-// that no token's size touches another's; their weights go in as a bf16 part
-// and the bf16 remainder, 2^-17 of themselves off.
+// 16-bit window), in log2 units: z = q.k scale_k softmax_scale log2(e) +
+// log2(scale_v), m the running maximum of z, w = 2^(z - m + 15), o the sum of
+// w v_code, l the sum of w / scale_v, out = o / l.  With scale_v in the
+// exponent, o accumulates codes of blocks with different scales in the mma's
+// own registers.  Both products run on mma.sync m16n8k16 in fp16 with fp32
+// accumulators: rows are M, tokens N of the first product and K of the second,
+// whose A operand is the first one's accumulator fragment as it lies in
+// registers.  int8 codes enter as (code + 128) 2^-24, fp16 subnormals that are
+// two byte permutes away from the code; what the 128 adds is known: 128 sum(q)
+// in a score, taken off in its fused multiply-add, and 128 sum(w) in an
+// output, with sum(w) of the rounded weights from one more n-tile of ones.
+// Roundings to 16 bits: w to fp16 (the factor 2^15 keeps weights down to 2^-29
+// of the largest at full precision), and bf16 queries, which a power of two
+// per row brings into fp16's range: a rounding only of elements 2^-29 below
+// the row's largest.  Window tokens in bf16 are multiplied as they are (mma in
+// bf16), so that no token's size touches another's; their weights go in as a
+// bf16 part and the bf16 remainder, 2^-17 of themselves off.
 //
 // The units of all (sequence, KV head, 16-row tile) triples form one line,
 // cut into one equal range per CTA whatever the sequences' lengths.  The four
@@ -87,35 +92,49 @@ __device__ __forceinline__ uint2 lds8(uint32_t a) {
   return v;
 }
 
-// d = a * b + c with c = 0
-__device__ __forceinline__ void mma_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+// d = a * b + c with c = 0; a B fragment is one 64-bit register pair
+__device__ __forceinline__ void mma_zero(float (&d)[4], const uint32_t (&a)[4], uint64_t b) {
   asm volatile(
+      "{\n\t.reg .b32 x, y;\n\tmov.b64 {x, y}, %8;\n\t"
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
-      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {x,y}, {%9,%9,%9,%9};\n\t}"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "l"(b), "f"(0.f));
+}
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint64_t b) {
+  asm volatile(
+      "{\n\t.reg .b32 x, y;\n\tmov.b64 {x, y}, %8;\n\t"
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {x,y}, {%0,%1,%2,%3};\n\t}"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "l"(b));
 }
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   kvq::mma16816(d, a[0], a[1], a[2], a[3], b0, b1);
 }
 
-// Four code bytes of a word to fp16 pairs (bytes 0, 1) and (bytes 2, 3).
-// int8: with the sign bit flipped a byte is code + 128, and 0x64 above it
-// makes the fp16 number 1024 + 128 + code.
+// Bytes 2 h and 2 h + 1 of two code words as a B fragment in fp16: the codes'
+// values or, for int8 codes with the sign bit flipped, (code + 128) 2^-24.
 template <int FMT>
-__device__ __forceinline__ void widen(uint32_t w, uint32_t &lo, uint32_t &hi) {
+__device__ __forceinline__ uint64_t widen(uint32_t w0, int h0, uint32_t w1, int h1) {
+  uint64_t r;
   if (FMT == KV8_INT8) {
-    const uint32_t u = w ^ 0x80808080u;
-    uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-    const __half2 off = __floats2half2_rn(1152.f, 1152.f);
-    lo = kvq::h2_as_u32(__hsub2(*reinterpret_cast<__half2 *>(&a), off));
-    hi = kvq::h2_as_u32(__hsub2(*reinterpret_cast<__half2 *>(&b), off));
+    asm("{\n\t.reg .b32 x, y;\n\tprmt.b32 x, %1, 0, %3;\n\tprmt.b32 y, %2, 0, %4;\n\tmov.b64 %0, {x, y};\n\t}"
+        : "=l"(r)
+        : "r"(w0), "r"(w1), "r"(h0 ? 0x4342 : 0x4140), "r"(h1 ? 0x4342 : 0x4140));
   } else {
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(w));
+    const uint16_t c0 = static_cast<uint16_t>(h0 ? w0 >> 16 : w0), c1 = static_cast<uint16_t>(h1 ? w1 >> 16 : w1);
+    asm("{\n\t.reg .b32 x, y;\n\tcvt.rn.f16x2.e4m3x2 x, %1;\n\tcvt.rn.f16x2.e4m3x2 y, %2;\n\t"
+        "mov.b64 %0, {x, y};\n\t}"
+        : "=l"(r)
+        : "h"(c0), "h"(c1));
   }
+  return r;
+}
+// int8 codes to offset binary
+template <int FMT>
+__device__ __forceinline__ uint32_t flip(uint32_t w) {
+  return FMT == KV8_INT8 ? w ^ 0x80808080u : w;
 }
 
 // d = a * b + d in bf16
@@ -127,7 +146,7 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Weights are formed as 2^15 p.
+// Weights are formed as 2^15 w.
 constexpr float kShift = 15.f, kUnshift = 1.f / 32768.f;
 
 // A power-of-two pair (f, 1/f) that brings bf16 magnitudes up to `bits` to
@@ -282,7 +301,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
   int gu = get.u0 + warp;  // next unit to fetch
   const uint32_t ring = kvq::smem_u32(smem) + warp * SM::SLOTS * SM::SLOT;
   const uint32_t meta = kvq::smem_u32(smem) + SM::META + warp * SM::SLOTS * 8;
-  const int upb = B / kUnit;
+  const int ushift = 26 - __clz(B);  // units per block: 1 << ushift
   // lane -> (row, chunk) of the copies, the swizzled place included
   constexpr int CPR = D / 16;                 // 16-byte chunks of a code row
   constexpr int RPI = 32 / CPR;               // code rows per instruction
@@ -296,7 +315,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
   };
   auto table_entry = [&]() -> int {
     if (!more || gu >= get.w.full) return 0;
-    return geo.table[static_cast<size_t>(get.s) * geo.max_blocks + gu / upb];
+    return geo.table[static_cast<size_t>(get.s) * geo.max_blocks + (gu >> ushift)];
   };
   settle();
   int entry = table_entry();
@@ -307,7 +326,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
       if (gu < get.w.full) {
         const bool good = entry >= 0 && entry < geo.num_blocks;
         const size_t bh = static_cast<size_t>(good ? entry : 0) * H + get.h;
-        const uint8_t *ks = geo.codes + (bh * 2 * B + (gu % upb) * kUnit) * D + lane * 16;
+        const uint8_t *ks = geo.codes + (bh * 2 * B + (gu & ((1 << ushift) - 1)) * kUnit) * D + lane * 16;
         const uint8_t *vs = ks + static_cast<size_t>(B) * D;
 #pragma unroll
         for (int i = 0; i < kUnit / RPI; ++i) {
@@ -357,7 +376,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
     // ---- the tile's queries as A fragments; lane (g, q4) holds 16 channels
     // of rows g and g + 8 per 64 channels
     uint32_t qa[KS][4];
-    float qf[2];
+    float qf[2], q128[2] = {0.f, 0.f};
     int lim[2];  // last position each row sees
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -394,36 +413,54 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
           qa[k][r + 2] = bf16_to_fp16(qa[k][r + 2], f.x);
         }
       }
+      if (FMT == KV8_INT8 && r < HALVES) {
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const float2 x = unpack2<false>(qa[k][r]), y = unpack2<false>(qa[k][r + 2]);
+          sum += (x.x + x.y) + (y.x + y.y);
+        }
+        sum += __shfl_xor_sync(kAll, sum, 1);
+        sum += __shfl_xor_sync(kAll, sum, 2);
+        q128[r] = 128.f * sum;
+      }
     }
     // every row of the tile sees at least the tokens up to here
     const int seen_by_all = w.q.L - w.q.n + r0 / a.group;
 
-    float acc[NT][REGS], m[2] = {ninf, ninf}, l[2] = {0.f, 0.f};
+    float acc[NT][4], accw[4] = {0.f, 0.f, 0.f, 0.f}, m[2] = {ninf, ninf}, l[2] = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int r = 0; r < REGS; ++r) acc[j][r] = 0.f;
+      for (int r = 0; r < 4; ++r) acc[j][r] = 0.f;
 
-    // Scores of one unit to weights 2^15 p: NB n-tiles of 8 tokens from position t0;
-    // column 2 q4 of a tile is token 2 q4, column 2 q4 + 1 token (2 q4 + 1) ^ 4.
-    auto softmax = [&](auto nb, float (*sc)[4], float ks, int t0, bool window, uint32_t nan_mask) {
+    // Scores of one unit to weights 2^15 w: NB n-tiles of 8 tokens from position
+    // t0; column 2 q4 of a tile is token 2 q4, column 2 q4 + 1 token (2 q4 + 1) ^ 4.
+    // z = s a + b for the two rows; `bad`: tokens that turn what sees them to NaN.
+    auto softmax = [&](auto nb, float (*sc)[4], const float (&ka)[2], const float (&kb)[2], float inv, int t0,
+                       bool window, uint32_t bad) {
       constexpr int NB = decltype(nb)::value;
       float mx[2] = {m[0], m[1]};
-      const float kf[2] = {ks * qf[0], ks * qf[1]};
-      const bool edge = t0 + 8 * NB - 1 > seen_by_all;
 #pragma unroll
-      for (int t = 0; t < NB; ++t) {
+      for (int t = 0; t < NB; ++t)
 #pragma unroll
-        for (int i = 0; i < REGS; ++i) {
-          const int r = i >> 1, col = 8 * t + ((i & 1) ? ((2 * q4 + 1) ^ 4) : 2 * q4);
-          float z = sc[t][i] * kf[r];
-          if (window) z += z - z;  // an infinite score becomes NaN
-          if (nan_mask >> col & 1u) z = __int_as_float(0x7fc00000);
-          if (edge && t0 + col > lim[r]) z = ninf;
-          sc[t][i] = z;
-          mx[r] = fmaxf(mx[r], z);
-        }
+        for (int i = 0; i < REGS; ++i) sc[t][i] = fmaf(sc[t][i], ka[i >> 1], kb[i >> 1]);
+      if (window || bad || t0 + 8 * NB - 1 > seen_by_all) {
+#pragma unroll
+        for (int t = 0; t < NB; ++t)
+#pragma unroll
+          for (int i = 0; i < REGS; ++i) {
+            const int col = 8 * t + ((i & 1) ? ((2 * q4 + 1) ^ 4) : 2 * q4);
+            float z = sc[t][i];
+            if (window) z += z - z;  // an infinite score becomes NaN
+            if (bad >> col & 1u) z = __int_as_float(0x7fc00000);
+            sc[t][i] = t0 + col > lim[i >> 1] ? ninf : z;
+          }
       }
+#pragma unroll
+      for (int t = 0; t < NB; ++t)
+#pragma unroll
+        for (int i = 0; i < REGS; i += 2) mx[i >> 1] = fmaxf(fmaxf(mx[i >> 1], sc[t][i]), sc[t][i + 1]);
 #pragma unroll
       for (int r = 0; r < HALVES; ++r) {
         mx[r] = fmaxf(mx[r], __shfl_xor_sync(kAll, mx[r], 1));
@@ -437,6 +474,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
           const float f = mx[r] == m[r] ? 1.f : kvq::fast_exp2(m[r] - mx[r]);  // -inf before the first token
           m[r] = mx[r];
           l[r] *= f;
+          accw[2 * r] *= f;
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
             acc[j][2 * r] *= f;
@@ -444,17 +482,21 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
           }
         }
       }
+      float sum[2] = {0.f, 0.f};
 #pragma unroll
-      for (int t = 0; t < NB; ++t) {
+      for (int r = 0; r < HALVES; ++r) {
+        const float ms = m[r] == ninf ? 0.f : m[r] - kShift;
 #pragma unroll
-        for (int r = 0; r < HALVES; ++r) {
-          const float ms = m[r] == ninf ? 0.f : m[r] - kShift;
+        for (int t = 0; t < NB; ++t) {
           sc[t][2 * r] = kvq::fast_exp2(sc[t][2 * r] - ms);
           sc[t][2 * r + 1] = kvq::fast_exp2(sc[t][2 * r + 1] - ms);
-          l[r] += sc[t][2 * r] + sc[t][2 * r + 1];
+          sum[r] += sc[t][2 * r] + sc[t][2 * r + 1];
         }
-        if (HALVES == 1) sc[t][2] = sc[t][3] = 0.f;
+        l[r] = fmaf(sum[r], inv, l[r]);
       }
+      if (HALVES == 1)
+#pragma unroll
+        for (int t = 0; t < NB; ++t) sc[t][2] = sc[t][3] = 0.f;
     };
     // the weights of n-tiles 2 k, 2 k + 1 as the A operand of k-step k
     auto weights = [&](uint32_t (&p)[4], const float *lo, const float *hi) {
@@ -481,22 +523,35 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
             const uint32_t e[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              uint32_t b0, b1;
-              widen<FMT>(e[i], b0, b1);
+              const uint32_t word = flip<FMT>(e[i]);
+              const uint64_t b = widen<FMT>(word, 0, word, 1);
               if (c == 0 && i == 0)
-                mma_zero(sc[t], qa[0], b0, b1);
+                mma_zero(sc[t], qa[0], b);
               else
-                mma(sc[t], qa[c * 4 + i], b0, b1);
+                mma(sc[t], qa[c * 4 + i], b);
             }
           }
         }
-        // values without a finite scale make the rows that see them NaN
-        const bool vbad = !(fabsf(sc2.y) < __int_as_float(0x7f800000));
-        softmax(std::integral_constant<int, 4>{}, sc, sc2.x, u * kUnit, false, vbad ? 0xffffffffu : 0u);
+        const float inf = __int_as_float(0x7f800000);
+        // scales that are not finite make the rows that see the block NaN;
+        // values of magnitude 2^-100 or less (their scale's floor) count as
+        // zeros, of any scale
+        const bool bad = !(fabsf(sc2.x) < inf && fabsf(sc2.y) < inf), none = sc2.y < 8.8e-33f;
+        const float ks = bad ? 1.f : sc2.x, vs = bad || none ? 1.f : sc2.y, lv = __log2f(vs);
+        float ka[2], kb[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float f = ks * qf[r];
+          ka[r] = FMT == KV8_INT8 ? f * 16777216.f : f;
+          kb[r] = FMT == KV8_INT8 ? fmaf(-q128[r], f, lv) : lv;
+        }
+        softmax(std::integral_constant<int, 4>{}, sc, ka, kb, __fdividef(1.f, vs), u * kUnit, false, bad ? kAll : 0u);
         uint32_t p[2][4];
         weights(p[0], sc[0], sc[1]);
         weights(p[1], sc[2], sc[3]);
-        const float vs = vbad ? 0.f : sc2.y * kUnshift;
+        if (none)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) p[i >> 2][i & 3] = 0u;
         // values: lane (g, q4) reads its channels of the 8 tokens of its k indices
         constexpr int VW = D / 32;  // words per token
         uint32_t v[8][VW];
@@ -517,22 +572,24 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
         }
 #pragma unroll
         for (int j = 0; j < VW; ++j) {
-          uint32_t b[2][2][4];  // [k-step][b0, b1][channel of the word]
+          // two tokens' codes interleaved: channels 0, 1 and 2, 3 of the word
+          uint32_t lo[4], hi[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t x = v[2 * i][j], y = v[2 * i + 1][j];
-            uint32_t(&d)[4] = b[i >> 1][i & 1];
-            widen<FMT>(__byte_perm(x, y, 0x5140), d[0], d[1]);
-            widen<FMT>(__byte_perm(x, y, 0x7362), d[2], d[3]);
+            lo[i] = flip<FMT>(__byte_perm(v[2 * i][j], v[2 * i + 1][j], 0x5140));
+            hi[i] = flip<FMT>(__byte_perm(v[2 * i][j], v[2 * i + 1][j], 0x7362));
           }
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float o[4];
-            mma_zero(o, p[0], b[0][0][c], b[0][1][c]);
-            mma(o, p[1], b[1][0][c], b[1][1][c]);
-#pragma unroll
-            for (int r = 0; r < REGS; ++r) acc[4 * j + c][r] = fmaf(o[r], vs, acc[4 * j + c][r]);
+          for (int k = 0; k < 2; ++k) {
+            mma(acc[4 * j], p[k], widen<FMT>(lo[2 * k], 0, lo[2 * k + 1], 0));
+            mma(acc[4 * j + 1], p[k], widen<FMT>(lo[2 * k], 1, lo[2 * k + 1], 1));
+            mma(acc[4 * j + 2], p[k], widen<FMT>(hi[2 * k], 0, hi[2 * k + 1], 0));
+            mma(acc[4 * j + 3], p[k], widen<FMT>(hi[2 * k], 1, hi[2 * k + 1], 1));
           }
+        }
+        if (FMT == KV8_INT8) {  // sums of the rounded weights
+          mma(accw, p[0], 0x3c003c00u, 0x3c003c00u);
+          mma(accw, p[1], 0x3c003c00u, 0x3c003c00u);
         }
       } else {
         // ---- 16 window tokens in 16 bits
@@ -589,7 +646,10 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
           if (any) bad |= 1u << row;
         }
         bad = __reduce_or_sync(kAll, bad);
-        softmax(std::integral_constant<int, 2>{}, sc, 1.f, w.full * kUnit + t0, true, bad);
+        const float zero[2] = {0.f, 0.f};
+        softmax(std::integral_constant<int, 2>{}, sc, qf, zero, 1.f, w.full * kUnit + t0, true, bad);
+        // what a window value times its weight counts in acc
+        constexpr float kWin = (BF16 ? 32768.f : 1.f) / (FMT == KV8_INT8 ? 16777216.f : 1.f);
         uint32_t p[4], rest[4];
         if (BF16) {
 #pragma unroll
@@ -625,7 +685,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
               mma(o, p, b0, b1);
             }
 #pragma unroll
-            for (int r = 0; r < REGS; ++r) acc[2 * k + c][r] = fmaf(o[r], BF16 ? 1.f : kUnshift, acc[2 * k + c][r]);
+            for (int r = 0; r < REGS; ++r) acc[2 * k + c][r] = fmaf(o[r], kWin, acc[2 * k + c][r]);
           }
         }
       }
@@ -643,6 +703,12 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
       l[r] += __shfl_xor_sync(kAll, l[r], 1);
       l[r] += __shfl_xor_sync(kAll, l[r], 2);
       l[r] *= kUnshift;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          acc[j][2 * r + i] = FMT == KV8_INT8 ? fmaf(acc[j][2 * r + i], 512.f, accw[2 * r] * (-128.f * kUnshift))
+                                              : acc[j][2 * r + i] * kUnshift;
       if (q4 == 0) ml[warp * kRowTile + g + 8 * r] = make_float2(m[r], l[r]);
     }
     __syncthreads();
