@@ -19,8 +19,6 @@
 namespace kv8 {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kQueryItems = 4;  // (row, head, chunk pair) items per thread of a query CTA
 
 struct AppendArgs {
   Geo geo;
@@ -31,7 +29,10 @@ struct AppendArgs {
   const float *rope;
   int rot, interleaved;
   int kv_tasks;     // CTAs that store keys and values
-  int slots;        // block slots per KV head (0: one per sequence)
+  int slots;        // block slots per group of heads (0: one per sequence)
+  int heads;        // KV heads per CTA, one after the other
+  int head_groups;  // CTAs that share a block
+  int lanes;        // threads that share a query row's chunk pair: 1 << lanes
 };
 
 // The two 8-channel chunks of chunk pair `pi` (of D / 16): the halves that
@@ -60,35 +61,41 @@ __device__ __forceinline__ uint32_t turn_adjacent(uint32_t w, float c, float s) 
                      __fadd_rn(__fmul_rn(x.y, c), __fmul_rn(x.x, s)));
 }
 
-// Rotates chunk pair `pi` of one head to position `pos`.  Each product and
-// sum is rounded on its own, so the result is a function of the table alone.
+// The 16 table values that turn chunk pair `pi` at position `pos`: cosines and
+// sines of its angles (interleaved: chunk a's four, then chunk b's).
+struct Turn {
+  float4 c0, c1, s0, s1;
+};
+__device__ __forceinline__ Turn load_turn(int pi, int pos, const AppendArgs &a) {
+  const int2 ch = chunk_pair(pi, a.rot);
+  const float *first = a.rope + static_cast<size_t>(pos) * a.rot + (a.interleaved ? 4 * ch.x : 8 * pi);
+  const int second = a.interleaved ? 4 * (ch.y - ch.x) : 4, half = a.rot >> 1;
+  Turn t;
+  t.c0 = __ldg(reinterpret_cast<const float4 *>(first));
+  t.c1 = __ldg(reinterpret_cast<const float4 *>(first + second));
+  t.s0 = __ldg(reinterpret_cast<const float4 *>(first + half));
+  t.s1 = __ldg(reinterpret_cast<const float4 *>(first + half + second));
+  return t;
+}
+
+// Rotates a chunk pair of one head.  Each product and sum is rounded on its
+// own, so the result is a function of the table alone.
 template <bool BF16>
-__device__ __forceinline__ void rotate(uint4 &ca, uint4 &cb, int pi, int pos, const AppendArgs &a) {
-  if (pi >= (a.rot >> 4)) return;
-  const float *row = a.rope + static_cast<size_t>(pos) * a.rot;
-  const int half = a.rot >> 1;
-  if (!a.interleaved) {
-    const float4 *c = reinterpret_cast<const float4 *>(row + 8 * pi);
-    const float4 *s = reinterpret_cast<const float4 *>(row + half + 8 * pi);
-    const float4 c0 = __ldg(c), c1 = __ldg(c + 1), s0 = __ldg(s), s1 = __ldg(s + 1);
-    turn<BF16>(ca.x, cb.x, c0.x, c0.y, s0.x, s0.y);
-    turn<BF16>(ca.y, cb.y, c0.z, c0.w, s0.z, s0.w);
-    turn<BF16>(ca.z, cb.z, c1.x, c1.y, s1.x, s1.y);
-    turn<BF16>(ca.w, cb.w, c1.z, c1.w, s1.z, s1.w);
+__device__ __forceinline__ void rotate(uint4 &ca, uint4 &cb, const Turn &t, bool interleaved) {
+  if (!interleaved) {
+    turn<BF16>(ca.x, cb.x, t.c0.x, t.c0.y, t.s0.x, t.s0.y);
+    turn<BF16>(ca.y, cb.y, t.c0.z, t.c0.w, t.s0.z, t.s0.w);
+    turn<BF16>(ca.z, cb.z, t.c1.x, t.c1.y, t.s1.x, t.s1.y);
+    turn<BF16>(ca.w, cb.w, t.c1.z, t.c1.w, t.s1.z, t.s1.w);
   } else {
-    const int2 ch = chunk_pair(pi, a.rot);
-    const float4 ac = __ldg(reinterpret_cast<const float4 *>(row + 4 * ch.x));
-    const float4 as = __ldg(reinterpret_cast<const float4 *>(row + half + 4 * ch.x));
-    const float4 bc = __ldg(reinterpret_cast<const float4 *>(row + 4 * ch.y));
-    const float4 bs = __ldg(reinterpret_cast<const float4 *>(row + half + 4 * ch.y));
-    ca.x = turn_adjacent<BF16>(ca.x, ac.x, as.x);
-    ca.y = turn_adjacent<BF16>(ca.y, ac.y, as.y);
-    ca.z = turn_adjacent<BF16>(ca.z, ac.z, as.z);
-    ca.w = turn_adjacent<BF16>(ca.w, ac.w, as.w);
-    cb.x = turn_adjacent<BF16>(cb.x, bc.x, bs.x);
-    cb.y = turn_adjacent<BF16>(cb.y, bc.y, bs.y);
-    cb.z = turn_adjacent<BF16>(cb.z, bc.z, bs.z);
-    cb.w = turn_adjacent<BF16>(cb.w, bc.w, bs.w);
+    ca.x = turn_adjacent<BF16>(ca.x, t.c0.x, t.s0.x);
+    ca.y = turn_adjacent<BF16>(ca.y, t.c0.y, t.s0.y);
+    ca.z = turn_adjacent<BF16>(ca.z, t.c0.z, t.s0.z);
+    ca.w = turn_adjacent<BF16>(ca.w, t.c0.w, t.s0.w);
+    cb.x = turn_adjacent<BF16>(cb.x, t.c1.x, t.s1.x);
+    cb.y = turn_adjacent<BF16>(cb.y, t.c1.y, t.s1.y);
+    cb.z = turn_adjacent<BF16>(cb.z, t.c1.z, t.s1.z);
+    cb.w = turn_adjacent<BF16>(cb.w, t.c1.w, t.s1.w);
   }
 }
 
@@ -139,58 +146,60 @@ __device__ __forceinline__ uint2 code8(const uint4 &v, float f, bool bad) {
   return make_uint2(code4<FMT, BF16>(v.x, v.y, f), code4<FMT, BF16>(v.z, v.w, f));
 }
 
-// Queries: thread items (row, head, chunk pair), four in flight.
-template <int D, bool BF16>
-__device__ void rotate_queries(const AppendArgs &a, int cta) {
+// Queries: a thread turns one chunk pair of every (1 << lanes)-th head of a row,
+// two heads at a time, with one set of table values.
+template <int D, bool BF16, int T>
+__device__ __forceinline__ void rotate_queries(const AppendArgs &a, int cta) {
   constexpr int PAIRS = D / 16;
-  const long long items = static_cast<long long>(a.rows) * a.Hq * PAIRS;
-  const long long base = static_cast<long long>(cta) * kThreads * kQueryItems + threadIdx.x;
-  uint4 x[kQueryItems], y[kQueryItems];
-  long long off[kQueryItems];
-  int pos[kQueryItems];
-#pragma unroll
-  for (int i = 0; i < kQueryItems; ++i) {
-    const long long it = base + static_cast<long long>(i) * kThreads;
-    pos[i] = -1;
-    if (it >= items) continue;
-    const int pi = static_cast<int>(it % PAIRS);
-    const long long rh = it / PAIRS;
-    const int row = static_cast<int>(rh / a.Hq), head = static_cast<int>(rh % a.Hq);
-    int s = row;
-    if (a.row_start) s = last_at_or_below(a.geo.S, row, [&](int j) { return a.row_start[j]; });
-    if (s >= a.geo.S) continue;
-    const Seq sq = load_seq(a.geo, a.row_start, a.rows, a.max_new, s);
-    if (!sq.ok || row < sq.row0 || row >= sq.row0 + sq.n || sq.L < sq.n || sq.L > a.geo.capacity) continue;
-    pos[i] = sq.L - sq.n + row - sq.row0;
-    const int2 ch = chunk_pair(pi, a.rot);
-    const uint16_t *src = a.q.p + row * a.q.row + head * a.q.head;
-    x[i] = load16(src + 8 * ch.x);
-    y[i] = load16(src + 8 * ch.y);
-    off[i] = row * a.q_out.row + head * a.q_out.head;
-  }
-#pragma unroll
-  for (int i = 0; i < kQueryItems; ++i) {
-    if (pos[i] < 0) continue;
-    const int pi = static_cast<int>((base + static_cast<long long>(i) * kThreads) % PAIRS);
-    const int2 ch = chunk_pair(pi, a.rot);
-    rotate<BF16>(x[i], y[i], pi, pos[i], a);
-    store16(a.q_out.p + off[i] + 8 * ch.x, x[i]);
-    store16(a.q_out.p + off[i] + 8 * ch.y, y[i]);
+  const int lanes = 1 << a.lanes, at = threadIdx.x / PAIRS;
+  const int pi = threadIdx.x % PAIRS, lane = at & (lanes - 1);
+  const int row = cta * ((T / PAIRS) >> a.lanes) + (at >> a.lanes);
+  if (row >= a.rows || lane >= a.Hq) return;
+  int s = row;
+  if (a.row_start) s = last_at_or_below(a.geo.S, row, [&](int j) { return a.row_start[j]; });
+  if (s >= a.geo.S) return;
+  const Seq sq = load_seq(a.geo, a.row_start, a.rows, a.max_new, s);
+  if (!sq.ok || row < sq.row0 || row >= sq.row0 + sq.n || sq.L < sq.n || sq.L > a.geo.capacity) return;
+  const bool turns = pi < (a.rot >> 4);
+  Turn t;
+  if (turns) t = load_turn(pi, sq.L - sq.n + row - sq.row0, a);
+  const int2 ch = chunk_pair(pi, a.rot);
+  const uint16_t *src = a.q.p + row * a.q.row + lane * a.q.head;
+  uint16_t *dst = a.q_out.p + row * a.q_out.row + lane * a.q_out.head;
+  const long long in = a.q.head << a.lanes, out = a.q_out.head << a.lanes;
+#pragma unroll 1
+  for (int h = lane; h < a.Hq; h += 2 * lanes, src += 2 * in, dst += 2 * out) {
+    const bool two = h + lanes < a.Hq;
+    uint4 x = load16(src + 8 * ch.x), y = load16(src + 8 * ch.y), z, w;
+    if (two) {
+      z = load16(src + in + 8 * ch.x);
+      w = load16(src + in + 8 * ch.y);
+    }
+    if (turns) rotate<BF16>(x, y, t, a.interleaved);
+    store16(dst + 8 * ch.x, x);
+    store16(dst + 8 * ch.y, y);
+    if (two) {
+      if (turns) rotate<BF16>(z, w, t, a.interleaved);
+      store16(dst + out + 8 * ch.x, z);
+      store16(dst + out + 8 * ch.y, w);
+    }
   }
 }
 
-// NI: chunk pairs of a block's keys (and of its values) per thread.
-template <int D, int FMT, bool BF16, int NI>
-__global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
+// T threads, and NI chunk pairs of a block's keys (and of its values) per
+// thread: one where 512 threads suffice, for then a thread needs few registers
+// and the SM holds 1024 of them.
+template <int D, int FMT, bool BF16, int T, int NI>
+__global__ void __launch_bounds__(T, 1024 / T / NI) append_kernel(const AppendArgs a) {
   constexpr int PAIRS = D / 16;
   if (static_cast<int>(blockIdx.x) >= a.kv_tasks) {
-    rotate_queries<D, BF16>(a, blockIdx.x - a.kv_tasks);
+    rotate_queries<D, BF16, T>(a, blockIdx.x - a.kv_tasks);
     return;
   }
   const Geo &geo = a.geo;
   const int B = geo.B, tid = threadIdx.x;
-  const int h = blockIdx.x % geo.H;
-  int s = blockIdx.x / geo.H, t = 0;
+  const int h0 = static_cast<int>(blockIdx.x % a.head_groups) * a.heads;
+  int s = blockIdx.x / a.head_groups, t = 0;
   if (a.slots) {
     // slot -> (sequence, block): sequence s owns the slots from
     // row_start[s] / B + s on, at least as many as blocks it can complete
@@ -200,127 +209,135 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
   }
   const Seq sq = load_seq(geo, a.row_start, a.rows, a.max_new, s);
   if (!sq.ok || sq.n > sq.L) {
-    if (t == 0 && h == 0 && tid == 0) set_status(geo.status, KVQ_STATUS_BAD_LEN);
+    if (t == 0 && h0 == 0 && tid == 0) set_status(geo.status, KVQ_STATUS_BAD_LEN);
     return;
   }
   if (sq.L > geo.capacity) {
-    if (t == 0 && h == 0 && tid == 0) set_status(geo.status, KVQ_STATUS_CAPACITY);
+    if (t == 0 && h0 == 0 && tid == 0) set_status(geo.status, KVQ_STATUS_CAPACITY);
     return;
   }
   if (sq.n == 0) return;
   const int L = sq.L, old = L - sq.n, first = old / B, done = L / B - first;
   if (t < 0 || t >= max(done, 1)) return;
   const int p0 = (first + t) * B;  // position of the block's slot 0
-  const size_t win0 = (static_cast<size_t>(s) * geo.H + h) * B * D;
-  const uint16_t *kr = a.k.p + h * a.k.head, *vr = a.v.p + h * a.v.head;
+  const int blk = t < done ? geo.table[static_cast<size_t>(s) * geo.max_blocks + first + t] : -1;
+  const int from = max(old, L / B * B);  // first new token that stays in the window
+  const int items = B * PAIRS;
 
-  // one token's chunk pair of the block: window slot or new row, rotated
-  auto load_key = [&](int slot, int pi, uint4 &x, uint4 &y) {
-    const int p = p0 + slot;
+  __shared__ uint32_t red[2][2][T / 32];
+
+  // Where the thread's chunk pairs of the block come from in head 0 (a window
+  // slot or a new row), and how far head h is from there.
+  const uint16_t *kp[NI], *vp[NI];
+  long long kstep[NI], vstep[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int it = tid + i * T, slot = it / PAIRS, pi = it % PAIRS, p = p0 + slot;
     const int2 ch = chunk_pair(pi, a.rot);
-    const uint16_t *src =
-        p < old ? geo.k_win + win0 + slot * D : kr + static_cast<long long>(sq.row0 + p - old) * a.k.row;
-    x = load16(src + 8 * ch.x);
-    y = load16(src + 8 * ch.y);
-  };
-  auto load_value = [&](int slot, int pi, uint4 &x, uint4 &y) {
-    const int p = p0 + slot;
-    const uint16_t *src =
-        p < old ? geo.v_win + win0 + slot * D : vr + static_cast<long long>(sq.row0 + p - old) * a.v.row;
-    x = load16(src + 8 * pi);
-    y = load16(src + 8 * (pi + PAIRS));
-  };
-
-  if (t < done) {
-    __shared__ uint32_t red[2][kThreads / 32];
-    uint4 ka[NI], kb[NI], va[NI], vb[NI];
-    const int items = B * PAIRS;
-    uint32_t km = 0, vm = 0;
+    const long long row = static_cast<long long>(sq.row0) + p - old;
+    const size_t win = (static_cast<size_t>(s) * geo.H * B + slot) * D;
+    kp[i] = (p < old ? geo.k_win + win : a.k.p + row * a.k.row) + 8 * ch.x;
+    vp[i] = (p < old ? geo.v_win + win : a.v.p + row * a.v.row) + 8 * pi;
+    kstep[i] = p < old ? B * D : a.k.head;
+    vstep[i] = p < old ? B * D : a.v.head;
+  }
+#pragma unroll 1
+  for (int h = h0; h < min(h0 + a.heads, geo.H); ++h) {
+    const size_t win0 = (static_cast<size_t>(s) * geo.H + h) * B * D;
+    if (t < done) {
+      uint4 ka[NI], kb[NI], va[NI], vb[NI];
+      uint32_t km = 0, vm = 0;
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int it = tid + i * kThreads;
-      if (it < items) {
-        load_key(it / PAIRS, it % PAIRS, ka[i], kb[i]);
-        load_value(it / PAIRS, it % PAIRS, va[i], vb[i]);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int it = tid + i * kThreads;
-      if (it < items) {
-        const int p = p0 + it / PAIRS;
-        if (p >= old) rotate<BF16>(ka[i], kb[i], it % PAIRS, p, a);
-        km = mag_max(mag_max(km, ka[i]), kb[i]);
-        vm = mag_max(mag_max(vm, va[i]), vb[i]);
-      }
-    }
-    km = __reduce_max_sync(0xffffffffu, max(km & 0xffffu, km >> 16));
-    vm = __reduce_max_sync(0xffffffffu, max(vm & 0xffffu, vm >> 16));
-    if ((tid & 31) == 0) {
-      red[0][tid >> 5] = km;
-      red[1][tid >> 5] = vm;
-    }
-    __syncthreads();  // also: every window slot of the block has been read
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      km = max(km, red[0][w]);
-      vm = max(vm, red[1][w]);
-    }
-    const int blk = geo.table[static_cast<size_t>(s) * geo.max_blocks + first + t];
-    if (blk < 0 || blk >= geo.num_blocks) {
-      if (tid == 0) set_status(geo.status, KVQ_STATUS_BAD_BLOCK);
-    } else {
-      const bool kbad = km >= nonfinite_bits<BF16>(), vbad = vm >= nonfinite_bits<BF16>();
-      const float2 ks = scale_and_factor<FMT>(kbad ? 0.f : unpack2<BF16>(km).x);
-      const float2 vs = scale_and_factor<FMT>(vbad ? 0.f : unpack2<BF16>(vm).x);
-      const size_t bh = static_cast<size_t>(blk) * geo.H + h;
-      uint8_t *kc = geo.codes + bh * 2 * B * D, *vc = kc + B * D;
-      if (tid == 0) {
-        const float nan = __int_as_float(0x7fc00000);
-        *reinterpret_cast<float2 *>(geo.scales + bh * 2) = make_float2(kbad ? nan : ks.x, vbad ? nan : vs.x);
+      for (int i = 0; i < NI; ++i) {
+        if (tid + i * T < items) {
+          const int2 ch = chunk_pair(tid % PAIRS, a.rot);
+          const uint16_t *ks = kp[i] + h * kstep[i], *vs = vp[i] + h * vstep[i];
+          ka[i] = load16(ks);
+          kb[i] = load16(ks + 8 * (ch.y - ch.x));
+          va[i] = load16(vs);
+          vb[i] = load16(vs + 8 * PAIRS);
+        }
       }
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const int it = tid + i * kThreads;
+        const int it = tid + i * T;
         if (it < items) {
-          const int slot = it / PAIRS, pi = it % PAIRS;
-          const int2 ch = chunk_pair(pi, a.rot);
-          *reinterpret_cast<uint2 *>(kc + slot * D + 8 * ch.x) = code8<FMT, BF16>(ka[i], ks.y, kbad);
-          *reinterpret_cast<uint2 *>(kc + slot * D + 8 * ch.y) = code8<FMT, BF16>(kb[i], ks.y, kbad);
-          *reinterpret_cast<uint2 *>(vc + slot * D + 8 * pi) = code8<FMT, BF16>(va[i], vs.y, vbad);
-          *reinterpret_cast<uint2 *>(vc + slot * D + 8 * (pi + PAIRS)) = code8<FMT, BF16>(vb[i], vs.y, vbad);
+          const int p = p0 + it / PAIRS, pi = it % PAIRS;
+          if (p >= old && pi < (a.rot >> 4)) rotate<BF16>(ka[i], kb[i], load_turn(pi, p, a), a.interleaved);
+          km = mag_max(mag_max(km, ka[i]), kb[i]);
+          vm = mag_max(mag_max(vm, va[i]), vb[i]);
+        }
+      }
+      km = __reduce_max_sync(0xffffffffu, max(km & 0xffffu, km >> 16));
+      vm = __reduce_max_sync(0xffffffffu, max(vm & 0xffffu, vm >> 16));
+      uint32_t(&r)[2][T / 32] = red[h & 1];  // the other half may still be read
+      if ((tid & 31) == 0) {
+        r[0][tid >> 5] = km;
+        r[1][tid >> 5] = vm;
+      }
+      __syncthreads();  // also: every window slot of the block has been read
+#pragma unroll
+      for (int w = 0; w < T / 32; ++w) {
+        km = max(km, r[0][w]);
+        vm = max(vm, r[1][w]);
+      }
+      if (blk < 0 || blk >= geo.num_blocks) {
+        if (tid == 0) set_status(geo.status, KVQ_STATUS_BAD_BLOCK);
+      } else {
+        const bool kbad = km >= nonfinite_bits<BF16>(), vbad = vm >= nonfinite_bits<BF16>();
+        const float2 ks = scale_and_factor<FMT>(kbad ? 0.f : unpack2<BF16>(km).x);
+        const float2 vs = scale_and_factor<FMT>(vbad ? 0.f : unpack2<BF16>(vm).x);
+        const size_t bh = static_cast<size_t>(blk) * geo.H + h;
+        uint8_t *kc = geo.codes + bh * 2 * B * D, *vc = kc + B * D;
+        if (tid == 0) {
+          const float nan = __int_as_float(0x7fc00000);
+          *reinterpret_cast<float2 *>(geo.scales + bh * 2) = make_float2(kbad ? nan : ks.x, vbad ? nan : vs.x);
+        }
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const int it = tid + i * T;
+          if (it < items) {
+            const int slot = it / PAIRS, pi = it % PAIRS;
+            const int2 ch = chunk_pair(pi, a.rot);
+            *reinterpret_cast<uint2 *>(kc + slot * D + 8 * ch.x) = code8<FMT, BF16>(ka[i], ks.y, kbad);
+            *reinterpret_cast<uint2 *>(kc + slot * D + 8 * ch.y) = code8<FMT, BF16>(kb[i], ks.y, kbad);
+            *reinterpret_cast<uint2 *>(vc + slot * D + 8 * pi) = code8<FMT, BF16>(va[i], vs.y, vbad);
+            *reinterpret_cast<uint2 *>(vc + slot * D + 8 * (pi + PAIRS)) = code8<FMT, BF16>(vb[i], vs.y, vbad);
+          }
         }
       }
     }
-  }
-  if (t > 0) return;
+    if (t > 0) continue;
 
-  // the tokens that stay in the window: all new ones when nothing filled,
-  // else those behind the last complete block
-  const int from = max(old, L / B * B);
-  for (int it = tid; it < (L - from) * PAIRS; it += kThreads) {
-    const int p = from + it / PAIRS, pi = it % PAIRS, slot = p % B;
-    const long long row = sq.row0 + p - old;
-    const int2 ch = chunk_pair(pi, a.rot);
-    uint4 x = load16(kr + row * a.k.row + 8 * ch.x), y = load16(kr + row * a.k.row + 8 * ch.y);
-    const uint4 z = load16(vr + row * a.v.row + 8 * pi), w = load16(vr + row * a.v.row + 8 * (pi + PAIRS));
-    rotate<BF16>(x, y, pi, p, a);
-    store16(geo.k_win + win0 + slot * D + 8 * ch.x, x);
-    store16(geo.k_win + win0 + slot * D + 8 * ch.y, y);
-    store16(geo.v_win + win0 + slot * D + 8 * pi, z);
-    store16(geo.v_win + win0 + slot * D + 8 * (pi + PAIRS), w);
+    // the tokens that stay in the window: all new ones when nothing filled,
+    // else those behind the last complete block
+    const uint16_t *kr = a.k.p + h * a.k.head, *vr = a.v.p + h * a.v.head;
+    for (int it = tid; it < (L - from) * PAIRS; it += T) {
+      const int p = from + it / PAIRS, pi = it % PAIRS, slot = p & (B - 1);
+      const long long row = static_cast<long long>(sq.row0) + p - old;
+      const int2 ch = chunk_pair(pi, a.rot);
+      uint4 x = load16(kr + row * a.k.row + 8 * ch.x), y = load16(kr + row * a.k.row + 8 * ch.y);
+      const uint4 z = load16(vr + row * a.v.row + 8 * pi), w = load16(vr + row * a.v.row + 8 * (pi + PAIRS));
+      if (pi < (a.rot >> 4)) rotate<BF16>(x, y, load_turn(pi, p, a), a.interleaved);
+      store16(geo.k_win + win0 + slot * D + 8 * ch.x, x);
+      store16(geo.k_win + win0 + slot * D + 8 * ch.y, y);
+      store16(geo.v_win + win0 + slot * D + 8 * pi, z);
+      store16(geo.v_win + win0 + slot * D + 8 * (pi + PAIRS), w);
+    }
   }
 }
 
 template <int D, int FMT, bool BF16>
 cudaError_t launch_ni(const AppendArgs &a, unsigned grid, cudaStream_t stream) {
   const int items = a.geo.B * D / 16;
-  if (items <= kThreads)
-    append_kernel<D, FMT, BF16, 1><<<grid, kThreads, 0, stream>>>(a);
-  else if (items <= 2 * kThreads)
-    append_kernel<D, FMT, BF16, 2><<<grid, kThreads, 0, stream>>>(a);
+  if (items == 128)
+    append_kernel<D, FMT, BF16, 128, 1><<<grid, 128, 0, stream>>>(a);
+  else if (items == 256)
+    append_kernel<D, FMT, BF16, 256, 1><<<grid, 256, 0, stream>>>(a);
+  else if (items == 512)
+    append_kernel<D, FMT, BF16, 512, 1><<<grid, 512, 0, stream>>>(a);
   else
-    append_kernel<D, FMT, BF16, 4><<<grid, kThreads, 0, stream>>>(a);
+    append_kernel<D, FMT, BF16, 512, 2><<<grid, 512, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -351,9 +368,18 @@ cudaError_t launch_append(const Geo &geo, const Rows &k, const Rows &v, const Ro
   a.interleaved = interleaved;
   // up to B new tokens complete at most one block of a sequence
   a.slots = max_new > geo.B ? rows / geo.B + geo.S : 0;
-  const long long tasks = static_cast<long long>(a.slots ? a.slots : geo.S) * geo.H;
-  const long long items = static_cast<long long>(rows) * Hq * (geo.D / 16);
-  const long long grid = tasks + (items + kThreads * kQueryItems - 1) / (kThreads * kQueryItems);
+  // With many blocks a CTA takes four heads of each, so that the table's
+  // values, as many bytes per token as a head's keys and values together, come
+  // from the first-level cache for three of them; with few, every head has its
+  // own CTA.
+  const long long blocks = a.slots ? a.slots : geo.S;
+  a.heads = blocks * geo.H >= 8192 && rot_dim ? 4 : 1;
+  a.head_groups = (geo.H + a.heads - 1) / a.heads;
+  const long long tasks = blocks * a.head_groups;
+  // eight threads share a query row's chunk pair, fewer where there are fewer heads
+  a.lanes = Hq >= 8 ? 3 : Hq >= 4 ? 2 : Hq >= 2 ? 1 : 0;
+  const int per = (min(geo.B * geo.D / 16, 512) / (geo.D / 16)) >> a.lanes;  // query rows of a CTA, see launch_ni
+  const long long grid = tasks + (Hq ? (static_cast<long long>(rows) + per - 1) / per : 0);
   if (grid > 2147483647LL) return cudaErrorInvalidConfiguration;
   a.kv_tasks = static_cast<int>(tasks);
   ++*launches;
