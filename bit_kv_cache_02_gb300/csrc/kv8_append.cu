@@ -16,6 +16,10 @@
 
 #include "kv8_internal.cuh"
 
+#ifndef KV8_APPEND_SPLIT
+#define KV8_APPEND_SPLIT 2048
+#endif
+
 namespace kv8 {
 namespace {
 
@@ -31,7 +35,8 @@ struct AppendArgs {
   int kv_tasks;     // CTAs that store keys and values
   int slots;        // block slots per group of heads (0: one per sequence)
   int heads;        // KV heads per CTA, one after the other
-  int head_groups;  // CTAs that share a block
+  int head_groups;  // groups of heads
+  int split;        // 1: keys and values by CTAs of their own
   int lanes;        // threads that share a query row's chunk pair: 1 << lanes
 };
 
@@ -186,11 +191,9 @@ __device__ __forceinline__ void rotate_queries(const AppendArgs &a, int cta) {
   }
 }
 
-// T threads, and NI chunk pairs of a block's keys (and of its values) per
-// thread: one where 512 threads suffice, for then a thread needs few registers
-// and the SM holds 1024 of them.
+// T threads, and NI chunk pairs of a block's keys (or values) per thread.
 template <int D, int FMT, bool BF16, int T, int NI>
-__global__ void __launch_bounds__(T, 1024 / T / NI) append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(T, NI == 4 ? 3 : 1024 / T) append_kernel(const AppendArgs a) {
   constexpr int PAIRS = D / 16;
   if (static_cast<int>(blockIdx.x) >= a.kv_tasks) {
     rotate_queries<D, BF16, T>(a, blockIdx.x - a.kv_tasks);
@@ -198,8 +201,13 @@ __global__ void __launch_bounds__(T, 1024 / T / NI) append_kernel(const AppendAr
   }
   const Geo &geo = a.geo;
   const int B = geo.B, tid = threadIdx.x;
-  const int h0 = static_cast<int>(blockIdx.x % a.head_groups) * a.heads;
-  int s = blockIdx.x / a.head_groups, t = 0;
+  int task = blockIdx.x, which = 0;  // 0: keys, 1: values
+  if (a.split) {
+    which = task & 1;
+    task >>= 1;
+  }
+  const int h0 = task % a.head_groups * a.heads, h1 = min(h0 + a.heads, geo.H);
+  int s = task / a.head_groups, t = 0;
   if (a.slots) {
     // slot -> (sequence, block): sequence s owns the slots from
     // row_start[s] / B + s on, at least as many as blocks it can complete
@@ -223,107 +231,80 @@ __global__ void __launch_bounds__(T, 1024 / T / NI) append_kernel(const AppendAr
   const int blk = t < done ? geo.table[static_cast<size_t>(s) * geo.max_blocks + first + t] : -1;
   const int from = max(old, L / B * B);  // first new token that stays in the window
   const int items = B * PAIRS;
+  const int2 ch = chunk_pair(tid % PAIRS, a.rot);
+  const int apart = 8 * (ch.y - ch.x);
+  __shared__ uint32_t red[2][T / 32];
+  int phase = 0;
 
-  __shared__ uint32_t red[2][2][T / 32];
-
-  // Where the thread's chunk pairs of the block come from in head 0 (a window
-  // slot or a new row), and how far head h is from there.
-  const uint16_t *kp[NI], *vp[NI];
-  long long kstep[NI], vstep[NI];
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const int it = tid + i * T, slot = it / PAIRS, pi = it % PAIRS, p = p0 + slot;
-    const int2 ch = chunk_pair(pi, a.rot);
-    const long long row = static_cast<long long>(sq.row0) + p - old;
-    const size_t win = (static_cast<size_t>(s) * geo.H * B + slot) * D;
-    kp[i] = (p < old ? geo.k_win + win : a.k.p + row * a.k.row) + 8 * ch.x;
-    vp[i] = (p < old ? geo.v_win + win : a.v.p + row * a.v.row) + 8 * pi;
-    kstep[i] = p < old ? B * D : a.k.head;
-    vstep[i] = p < old ? B * D : a.v.head;
-  }
 #pragma unroll 1
-  for (int h = h0; h < min(h0 + a.heads, geo.H); ++h) {
-    const size_t win0 = (static_cast<size_t>(s) * geo.H + h) * B * D;
-    if (t < done) {
-      uint4 ka[NI], kb[NI], va[NI], vb[NI];
-      uint32_t km = 0, vm = 0;
+  for (;; ++which) {
+    const Rows &rows = which ? a.v : a.k;
+    const bool turns = !which && tid % PAIRS < (a.rot >> 4);
+    uint16_t *const win = (which ? geo.v_win : geo.k_win) + static_cast<size_t>(s) * geo.H * B * D + 8 * ch.x;
+    const uint16_t *const fresh = rows.p + (static_cast<long long>(sq.row0) - old) * rows.row + 8 * ch.x;
+#pragma unroll 1
+    for (int h = h0; h < h1; ++h, phase ^= 1) {
+      if (t < done) {
+        uint4 x[NI], y[NI];
+        uint32_t m = 0;
+        // a token's chunk pair from its window slot or new row
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        if (tid + i * T < items) {
-          const int2 ch = chunk_pair(tid % PAIRS, a.rot);
-          const uint16_t *ks = kp[i] + h * kstep[i], *vs = vp[i] + h * vstep[i];
-          ka[i] = load16(ks);
-          kb[i] = load16(ks + 8 * (ch.y - ch.x));
-          va[i] = load16(vs);
-          vb[i] = load16(vs + 8 * PAIRS);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int it = tid + i * T;
-        if (it < items) {
-          const int p = p0 + it / PAIRS, pi = it % PAIRS;
-          if (p >= old && pi < (a.rot >> 4)) rotate<BF16>(ka[i], kb[i], load_turn(pi, p, a), a.interleaved);
-          km = mag_max(mag_max(km, ka[i]), kb[i]);
-          vm = mag_max(mag_max(vm, va[i]), vb[i]);
-        }
-      }
-      km = __reduce_max_sync(0xffffffffu, max(km & 0xffffu, km >> 16));
-      vm = __reduce_max_sync(0xffffffffu, max(vm & 0xffffu, vm >> 16));
-      uint32_t(&r)[2][T / 32] = red[h & 1];  // the other half may still be read
-      if ((tid & 31) == 0) {
-        r[0][tid >> 5] = km;
-        r[1][tid >> 5] = vm;
-      }
-      __syncthreads();  // also: every window slot of the block has been read
-#pragma unroll
-      for (int w = 0; w < T / 32; ++w) {
-        km = max(km, r[0][w]);
-        vm = max(vm, r[1][w]);
-      }
-      if (blk < 0 || blk >= geo.num_blocks) {
-        if (tid == 0) set_status(geo.status, KVQ_STATUS_BAD_BLOCK);
-      } else {
-        const bool kbad = km >= nonfinite_bits<BF16>(), vbad = vm >= nonfinite_bits<BF16>();
-        const float2 ks = scale_and_factor<FMT>(kbad ? 0.f : unpack2<BF16>(km).x);
-        const float2 vs = scale_and_factor<FMT>(vbad ? 0.f : unpack2<BF16>(vm).x);
-        const size_t bh = static_cast<size_t>(blk) * geo.H + h;
-        uint8_t *kc = geo.codes + bh * 2 * B * D, *vc = kc + B * D;
-        if (tid == 0) {
-          const float nan = __int_as_float(0x7fc00000);
-          *reinterpret_cast<float2 *>(geo.scales + bh * 2) = make_float2(kbad ? nan : ks.x, vbad ? nan : vs.x);
+        for (int i = 0; i < NI; ++i) {
+          const int it = tid + i * T, slot = it / PAIRS, p = p0 + slot;
+          if (it < items) {
+            const uint16_t *src = p < old ? win + (static_cast<size_t>(h) * B + slot) * D
+                                          : fresh + p * rows.row + h * rows.head;
+            x[i] = load16(src);
+            y[i] = load16(src + apart);
+          }
         }
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-          const int it = tid + i * T;
+          const int it = tid + i * T, p = p0 + it / PAIRS;
           if (it < items) {
-            const int slot = it / PAIRS, pi = it % PAIRS;
-            const int2 ch = chunk_pair(pi, a.rot);
-            *reinterpret_cast<uint2 *>(kc + slot * D + 8 * ch.x) = code8<FMT, BF16>(ka[i], ks.y, kbad);
-            *reinterpret_cast<uint2 *>(kc + slot * D + 8 * ch.y) = code8<FMT, BF16>(kb[i], ks.y, kbad);
-            *reinterpret_cast<uint2 *>(vc + slot * D + 8 * pi) = code8<FMT, BF16>(va[i], vs.y, vbad);
-            *reinterpret_cast<uint2 *>(vc + slot * D + 8 * (pi + PAIRS)) = code8<FMT, BF16>(vb[i], vs.y, vbad);
+            if (turns && p >= old) rotate<BF16>(x[i], y[i], load_turn(tid % PAIRS, p, a), a.interleaved);
+            m = mag_max(mag_max(m, x[i]), y[i]);
+          }
+        }
+        m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+        if ((tid & 31) == 0) red[phase][tid >> 5] = m;  // the other half may still be read
+        __syncthreads();  // also: every window slot of the block has been read
+#pragma unroll
+        for (int w = 0; w < T / 32; ++w) m = max(m, red[phase][w]);
+        if (blk < 0 || blk >= geo.num_blocks) {
+          if (tid == 0) set_status(geo.status, KVQ_STATUS_BAD_BLOCK);
+        } else {
+          const bool bad = m >= nonfinite_bits<BF16>();
+          const float2 sc = scale_and_factor<FMT>(bad ? 0.f : unpack2<BF16>(m).x);
+          const size_t bh = (static_cast<size_t>(blk) * geo.H + h) * 2 + which;
+          uint8_t *codes = geo.codes + bh * B * D + 8 * ch.x;
+          if (tid == 0) geo.scales[bh] = bad ? __int_as_float(0x7fc00000) : sc.x;
+#pragma unroll
+          for (int i = 0; i < NI; ++i) {
+            const int it = tid + i * T;
+            if (it < items) {
+              uint8_t *dst = codes + it / PAIRS * D;
+              *reinterpret_cast<uint2 *>(dst) = code8<FMT, BF16>(x[i], sc.y, bad);
+              *reinterpret_cast<uint2 *>(dst + apart) = code8<FMT, BF16>(y[i], sc.y, bad);
+            }
           }
         }
       }
-    }
-    if (t > 0) continue;
+      if (t > 0) continue;
 
-    // the tokens that stay in the window: all new ones when nothing filled,
-    // else those behind the last complete block
-    const uint16_t *kr = a.k.p + h * a.k.head, *vr = a.v.p + h * a.v.head;
-    for (int it = tid; it < (L - from) * PAIRS; it += T) {
-      const int p = from + it / PAIRS, pi = it % PAIRS, slot = p & (B - 1);
-      const long long row = static_cast<long long>(sq.row0) + p - old;
-      const int2 ch = chunk_pair(pi, a.rot);
-      uint4 x = load16(kr + row * a.k.row + 8 * ch.x), y = load16(kr + row * a.k.row + 8 * ch.y);
-      const uint4 z = load16(vr + row * a.v.row + 8 * pi), w = load16(vr + row * a.v.row + 8 * (pi + PAIRS));
-      if (pi < (a.rot >> 4)) rotate<BF16>(x, y, load_turn(pi, p, a), a.interleaved);
-      store16(geo.k_win + win0 + slot * D + 8 * ch.x, x);
-      store16(geo.k_win + win0 + slot * D + 8 * ch.y, y);
-      store16(geo.v_win + win0 + slot * D + 8 * pi, z);
-      store16(geo.v_win + win0 + slot * D + 8 * (pi + PAIRS), w);
+      // the tokens that stay in the window: all new ones when nothing filled,
+      // else those behind the last complete block
+      for (int it = tid; it < (L - from) * PAIRS; it += T) {
+        const int p = from + it / PAIRS, slot = p & (B - 1);
+        const uint16_t *src = fresh + p * rows.row + h * rows.head;
+        uint4 x = load16(src), y = load16(src + apart);
+        if (turns) rotate<BF16>(x, y, load_turn(tid % PAIRS, p, a), a.interleaved);
+        uint16_t *dst = win + (static_cast<size_t>(h) * B + slot) * D;
+        store16(dst, x);
+        store16(dst + apart, y);
+      }
     }
+    if (a.split || which) break;
   }
 }
 
@@ -335,9 +316,9 @@ cudaError_t launch_ni(const AppendArgs &a, unsigned grid, cudaStream_t stream) {
   else if (items == 256)
     append_kernel<D, FMT, BF16, 256, 1><<<grid, 256, 0, stream>>>(a);
   else if (items == 512)
-    append_kernel<D, FMT, BF16, 512, 1><<<grid, 512, 0, stream>>>(a);
+    append_kernel<D, FMT, BF16, 256, 2><<<grid, 256, 0, stream>>>(a);
   else
-    append_kernel<D, FMT, BF16, 512, 2><<<grid, 512, 0, stream>>>(a);
+    append_kernel<D, FMT, BF16, 256, 4><<<grid, 256, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -368,17 +349,18 @@ cudaError_t launch_append(const Geo &geo, const Rows &k, const Rows &v, const Ro
   a.interleaved = interleaved;
   // up to B new tokens complete at most one block of a sequence
   a.slots = max_new > geo.B ? rows / geo.B + geo.S : 0;
-  // With many blocks a CTA takes four heads of each, so that the table's
-  // values, as many bytes per token as a head's keys and values together, come
-  // from the first-level cache for three of them; with few, every head has its
-  // own CTA.
+  // With many blocks keys and values have CTAs of their own, and a CTA takes
+  // eight heads, so that the table's values, as many bytes per token as a head's
+  // keys and values together, come from the first-level cache for seven of them.
+  // With few, a head's keys and values share a CTA.
   const long long blocks = a.slots ? a.slots : geo.S;
-  a.heads = blocks * geo.H >= 8192 && rot_dim ? 4 : 1;
+  a.split = blocks * geo.H >= KV8_APPEND_SPLIT;
+  a.heads = blocks * geo.H >= 8192 && rot_dim ? 8 : 1;
   a.head_groups = (geo.H + a.heads - 1) / a.heads;
-  const long long tasks = blocks * a.head_groups;
+  const long long tasks = blocks * a.head_groups * (a.split ? 2 : 1);
   // eight threads share a query row's chunk pair, fewer where there are fewer heads
   a.lanes = Hq >= 8 ? 3 : Hq >= 4 ? 2 : Hq >= 2 ? 1 : 0;
-  const int per = (min(geo.B * geo.D / 16, 512) / (geo.D / 16)) >> a.lanes;  // query rows of a CTA, see launch_ni
+  const int per = (min(geo.B * geo.D / 16, 256) / (geo.D / 16)) >> a.lanes;  // query rows of a CTA, see launch_ni
   const long long grid = tasks + (Hq ? (static_cast<long long>(rows) + per - 1) / per : 0);
   if (grid > 2147483647LL) return cudaErrorInvalidConfiguration;
   a.kv_tasks = static_cast<int>(tasks);
