@@ -8,12 +8,14 @@
 // w v_code, l the sum of w / scale_v, out = o / l.  With scale_v in the
 // exponent, o accumulates codes of blocks with different scales in the mma's
 // own registers.  Both products run on mma.sync m16n8k16 in fp16 with fp32
-// accumulators: rows are M, tokens N of the first product and K of the second,
-// whose A operand is the first one's accumulator fragment as it lies in
-// registers.  int8 codes enter as (code + 128) 2^-24, fp16 subnormals that are
-// two byte permutes away from the code; what the 128 adds is known: 128 sum(q)
-// in a score, taken off in its fused multiply-add, and 128 sum(w) in an
-// output, with sum(w) of the rounded weights from one more n-tile of ones.
+// accumulators.  Up to sixteen rows are M, tokens N of the first product and K
+// of the second, whose A operand is the first one's accumulator fragment as it
+// lies in registers; up to eight rows are N, with half the products and
+// registers, and the weights become B fragments by 8 x 8 transposes.  int8 keys
+// enter as (code + 128) 2^-24, fp16 subnormals that are two byte permutes away
+// from the code; the 128 sum(q) that this adds to a score is taken off in its
+// fused multiply-add.  (Values enter as they are: their sums nearly cancel over
+// a long context, and 128 sum(w) would drown what is left.)
 // Roundings to 16 bits: w to fp16 (the factor 2^15 keeps weights down to 2^-29
 // of the largest at full precision), and bf16 queries, which a power of two
 // per row brings into fp16's range: a rounding only of elements 2^-29 below
@@ -49,10 +51,10 @@ constexpr int kWarps = 4;
 constexpr int kUnit = 32;     // tokens of a unit of quantized blocks
 constexpr int kWinUnit = 16;  // tokens of a unit of the window
 #ifndef KV8_ROWS_SLOTS
-#define KV8_ROWS_SLOTS 3
+#define KV8_ROWS_SLOTS 2
 #endif
 
-template <int D>
+template <int D, int HALVES>
 struct Smem {
   static constexpr int SLOTS = D == 128 ? KV8_ROWS_SLOTS : 2 * KV8_ROWS_SLOTS;
   static constexpr int HALF = kUnit * D;   // bytes of a unit's keys (and of its values)
@@ -60,8 +62,8 @@ struct Smem {
   static constexpr int NT = D / 8;         // n-tiles of the output
   static constexpr int META = kWarps * SLOTS * SLOT;                 // scales of each slot: float2
   static constexpr int ML = META + kWarps * SLOTS * 8;               // [kWarps][16] float2
-  static constexpr int XCH = (ML + kWarps * kRowTile * 8 + 15) / 16 * 16;  // merge buffer, one row half
-  static constexpr int FLAG = XCH + kWarps * 3 * (NT / 4) * 2 * 32 * 4;
+  static constexpr int XCH = (ML + kWarps * kRowTile * 8 + 15) / 16 * 16;  // merge buffer
+  static constexpr int FLAG = XCH + kWarps * 3 * (NT / 4) * HALVES * 32 * 4;
   static constexpr int BYTES = FLAG + 16;
 };
 
@@ -113,15 +115,21 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
   kvq::mma16816(d, a[0], a[1], a[2], a[3], b0, b1);
 }
 
-// Bytes 2 h and 2 h + 1 of two code words as a B fragment in fp16: the codes'
-// values or, for int8 codes with the sign bit flipped, (code + 128) 2^-24.
-template <int FMT>
+// Bytes 2 h and 2 h + 1 of two code words as fp16 pairs: the codes' values or,
+// for int8 keys, (code + 128) 2^-24.  int8 words have their sign bits flipped.
+template <int FMT, bool KEYS>
 __device__ __forceinline__ uint64_t widen(uint32_t w0, int h0, uint32_t w1, int h1) {
   uint64_t r;
-  if (FMT == KV8_INT8) {
+  if (FMT == KV8_INT8 && KEYS) {
     asm("{\n\t.reg .b32 x, y;\n\tprmt.b32 x, %1, 0, %3;\n\tprmt.b32 y, %2, 0, %4;\n\tmov.b64 %0, {x, y};\n\t}"
         : "=l"(r)
         : "r"(w0), "r"(w1), "r"(h0 ? 0x4342 : 0x4140), "r"(h1 ? 0x4342 : 0x4140));
+  } else if (FMT == KV8_INT8) {
+    // 0x64 above a byte makes 1024 + 128 + code
+    asm("{\n\t.reg .b32 x, y;\n\tprmt.b32 x, %1, %5, %3;\n\tprmt.b32 y, %2, %5, %4;\n\t"
+        "sub.rn.f16x2 x, x, %6;\n\tsub.rn.f16x2 y, y, %6;\n\tmov.b64 %0, {x, y};\n\t}"
+        : "=l"(r)
+        : "r"(w0), "r"(w1), "r"(h0 ? 0x4342 : 0x4140), "r"(h1 ? 0x4342 : 0x4140), "r"(0x64646464u), "r"(0x64806480u));
   } else {
     const uint16_t c0 = static_cast<uint16_t>(h0 ? w0 >> 16 : w0), c1 = static_cast<uint16_t>(h1 ? w1 >> 16 : w1);
     asm("{\n\t.reg .b32 x, y;\n\tcvt.rn.f16x2.e4m3x2 x, %1;\n\tcvt.rn.f16x2.e4m3x2 y, %2;\n\t"
@@ -131,6 +139,26 @@ __device__ __forceinline__ uint64_t widen(uint32_t w0, int h0, uint32_t w1, int 
   }
   return r;
 }
+// d = a * b + d with A from code words: fragment registers 0..3 are bytes 2 h
+// and 2 h + 1 of w0..w3.
+template <int FMT, bool KEYS>
+__device__ __forceinline__ void mma_a(float (&d)[4], uint32_t w0, int h0, uint32_t w1, int h1, uint32_t w2, int h2,
+                                      uint32_t w3, int h3, const uint32_t (&b)[2]) {
+  const uint64_t x = widen<FMT, KEYS>(w0, h0, w1, h1), y = widen<FMT, KEYS>(w2, h2, w3, h3);
+  asm volatile(
+      "{\n\t.reg .b32 a, b, c, d;\n\tmov.b64 {a, b}, %4;\n\tmov.b64 {c, d}, %5;\n\t"
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {a,b,c,d}, {%6,%7}, {%0,%1,%2,%3};\n\t}"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "l"(x), "l"(y), "r"(b[0]), "r"(b[1]));
+}
+
+// The 8 x 8 matrix of 16-bit numbers held two to a lane, transposed.
+__device__ __forceinline__ uint32_t transpose(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
 // int8 codes to offset binary
 template <int FMT>
 __device__ __forceinline__ uint32_t flip(uint32_t w) {
@@ -239,7 +267,7 @@ struct Walk {
 
 template <int D, int FMT, bool BF16, int HALVES>
 __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
-  using SM = Smem<D>;
+  using SM = Smem<D, HALVES>;
   constexpr int NT = SM::NT;      // output n-tiles
   constexpr int KS = D / 16;      // k-steps of the scores
   constexpr int REGS = 2 * HALVES;  // accumulator registers in use per n-tile
@@ -389,414 +417,776 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
     const int n_rows = w.q.n * a.group;  // rows of this KV head
     const int r0 = use.tile * kRowTile;  // first row of the tile
 
-    // ---- the tile's queries as A fragments; lane (g, q4) holds 16 channels
-    // of rows g and g + 8 per 64 channels
-    uint32_t qa[KS][4];
-    float qf[2], q128[2] = {0.f, 0.f};
-    int lim[2];  // last position each row sees
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int row = r0 + g + 8 * r;
-      const bool valid = (r == 0 || HALVES == 2) && row < n_rows;
-      const int tok = valid ? row / a.group : 0;
-      lim[r] = valid ? w.q.L - w.q.n + tok : -1;
-      const uint16_t *src = a.q.p + (static_cast<long long>(w.q.row0) + tok) * a.q.row +
-                            (static_cast<long long>(use.h) * a.group + (valid ? row - tok * a.group : 0)) * a.q.head;
-      uint32_t big = 0;
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
-        if (valid) {
-          x = *reinterpret_cast<const uint4 *>(src + (c * 4 + q4) * 16);
-          y = *reinterpret_cast<const uint4 *>(src + (c * 4 + q4) * 16 + 8);
-        }
-        const uint32_t e[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          qa[c * 4 + i / 2][r + 2 * (i & 1)] = e[i];
-          if (BF16) big = finite_max(big, e[i], 0x7f80u);
-        }
-      }
-      qf[r] = a.zscale;
-      if (BF16) {
-        big = max(big, __shfl_xor_sync(kAll, big, 1));
-        big = max(big, __shfl_xor_sync(kAll, big, 2));
-        const float2 f = bf16_norm(big);
-        qf[r] *= f.y;
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          qa[k][r] = bf16_to_fp16(qa[k][r], f.x);
-          qa[k][r + 2] = bf16_to_fp16(qa[k][r + 2], f.x);
-        }
-      }
-      if (FMT == KV8_INT8 && r < HALVES) {
-        float sum = 0.f;
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const float2 x = unpack2<false>(qa[k][r]), y = unpack2<false>(qa[k][r + 2]);
-          sum += (x.x + x.y) + (y.x + y.y);
-        }
-        sum += __shfl_xor_sync(kAll, sum, 1);
-        sum += __shfl_xor_sync(kAll, sum, 2);
-        q128[r] = 128.f * sum;
-      }
-    }
-    // every row of the tile sees at least the tokens up to here
-    const int seen_by_all = w.q.L - w.q.n + r0 / a.group;
+    bool whole;
+    // what a window value times its weight counts in the output's sum
+    constexpr float kWin = BF16 ? 32768.f : 1.f;
 
-    float acc[NT][4], accw[4] = {0.f, 0.f, 0.f, 0.f}, m[2] = {ninf, ninf}, l[2] = {0.f, 0.f};
+    if constexpr (HALVES == 1) {
+      // ================ up to eight rows: tokens (then channels) are M, rows N.
+      // Lane (g, q4) holds 16 channels per 64 of row g as B fragments, and
+      // rows 2 q4, 2 q4 + 1 of the results.
+      uint32_t qb[KS][2];
+      float rf[2], r128[2] = {0.f, 0.f};  // of rows 2 q4, 2 q4 + 1: score factor, 128 sum(q)
+      int lim[2];                         // last position they see
+      {
+        const int row = r0 + g;
+        const bool valid = row < n_rows;
+        const int tok = valid ? row / a.group : 0;
+        const uint16_t *src =
+            a.q.p + (static_cast<long long>(w.q.row0) + tok) * a.q.row +
+            (static_cast<long long>(use.h) * a.group + (valid ? row - tok * a.group : 0)) * a.q.head;
+        uint32_t big = 0;
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+        for (int c = 0; c < D / 64; ++c) {
+          uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
+          if (valid) {
+            x = *reinterpret_cast<const uint4 *>(src + (c * 4 + q4) * 16);
+            y = *reinterpret_cast<const uint4 *>(src + (c * 4 + q4) * 16 + 8);
+          }
+          const uint32_t e[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-      for (int r = 0; r < 4; ++r) acc[j][r] = 0.f;
+          for (int i = 0; i < 8; ++i) {
+            qb[c * 4 + i / 2][i & 1] = e[i];
+            if (BF16) big = finite_max(big, e[i], 0x7f80u);
+          }
+        }
+        float f = a.zscale, sum = 0.f;
+        if (BF16) {
+          big = max(big, __shfl_xor_sync(kAll, big, 1));
+          big = max(big, __shfl_xor_sync(kAll, big, 2));
+          const float2 n = bf16_norm(big);
+          f *= n.y;
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            qb[k][0] = bf16_to_fp16(qb[k][0], n.x);
+            qb[k][1] = bf16_to_fp16(qb[k][1], n.x);
+          }
+        }
+        if (FMT == KV8_INT8) {
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            const float2 x = unpack2<false>(qb[k][0]), y = unpack2<false>(qb[k][1]);
+            sum += (x.x + x.y) + (y.x + y.y);
+          }
+          sum += __shfl_xor_sync(kAll, sum, 1);
+          sum += __shfl_xor_sync(kAll, sum, 2);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          rf[i] = __shfl_sync(kAll, f, 4 * (2 * q4 + i));
+          if (FMT == KV8_INT8) r128[i] = 128.f * __shfl_sync(kAll, sum, 4 * (2 * q4 + i));
+          const int rr = r0 + 2 * q4 + i;
+          lim[i] = rr < n_rows ? w.q.L - w.q.n + rr / a.group : -1;
+        }
+      }
+      const int seen_by_all = w.q.L - w.q.n + r0 / a.group;
+      constexpr int MT = D / 16;  // m-tiles of the output
+      float acc[MT][4], m[2] = {ninf, ninf}, l[2] = {0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
 
-    // Scores of one unit to weights 2^15 w: NB n-tiles of 8 tokens from position
-    // t0; column 2 q4 of a tile is token 2 q4, column 2 q4 + 1 token (2 q4 + 1) ^ 4.
-    // z = s a + b for the two rows; `bad`: tokens that turn what sees them to NaN.
-    auto softmax = [&](auto nb, float (*sc)[4], const float (&ka)[2], const float (&kb)[2], float inv, int t0,
-                       bool window, uint32_t bad) {
-      constexpr int NB = decltype(nb)::value;
-      float mx[2] = {m[0], m[1]};
-#pragma unroll
-      for (int t = 0; t < NB; ++t)
-#pragma unroll
-        for (int i = 0; i < REGS; ++i) sc[t][i] = fmaf(sc[t][i], ka[i >> 1], kb[i >> 1]);
-      if (window || bad || t0 + 8 * NB - 1 > seen_by_all) {
+      // Scores of NB m-tiles of 16 tokens from position t0 to weights 2^15 w.
+      // Row g of a tile is token g ^ 4 (g & 1), row g + 8 the same behind 8.
+      const int tok0 = g ^ ((g & 1) << 2);
+      auto softmax = [&](auto nb, float (*sc)[4], const float (&ka)[2], const float (&kb)[2], float inv, int t0,
+                         bool window, uint32_t bad) {
+        constexpr int NB = decltype(nb)::value;
+        float mx[2] = {m[0], m[1]};
 #pragma unroll
         for (int t = 0; t < NB; ++t)
 #pragma unroll
-          for (int i = 0; i < REGS; ++i) {
-            const int col = 8 * t + ((i & 1) ? ((2 * q4 + 1) ^ 4) : 2 * q4);
-            float z = sc[t][i];
-            if (window) z += z - z;  // an infinite score becomes NaN
-            if (bad >> col & 1u) z = __int_as_float(0x7fc00000);
-            sc[t][i] = t0 + col > lim[i >> 1] ? ninf : z;
-          }
-      }
+          for (int i = 0; i < 4; ++i) sc[t][i] = fmaf(sc[t][i], ka[i & 1], kb[i & 1]);
+        if (window || bad || t0 + 16 * NB - 1 > seen_by_all) {
 #pragma unroll
-      for (int t = 0; t < NB; ++t)
-#pragma unroll
-        for (int i = 0; i < REGS; i += 2) mx[i >> 1] = fmaxf(fmaxf(mx[i >> 1], sc[t][i]), sc[t][i + 1]);
-#pragma unroll
-      for (int r = 0; r < HALVES; ++r) {
-        mx[r] = fmaxf(mx[r], __shfl_xor_sync(kAll, mx[r], 1));
-        mx[r] = fmaxf(mx[r], __shfl_xor_sync(kAll, mx[r], 2));
-      }
-      bool moved = mx[0] != m[0];
-      if (HALVES == 2) moved |= mx[1] != m[1];
-      if (__any_sync(kAll, moved)) {
-#pragma unroll
-        for (int r = 0; r < HALVES; ++r) {
-          const float f = mx[r] == m[r] ? 1.f : kvq::fast_exp2(m[r] - mx[r]);  // -inf before the first token
-          m[r] = mx[r];
-          l[r] *= f;
-          accw[2 * r] *= f;
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            acc[j][2 * r] *= f;
-            acc[j][2 * r + 1] *= f;
-          }
-        }
-      }
-      float sum[2] = {0.f, 0.f};
-#pragma unroll
-      for (int r = 0; r < HALVES; ++r) {
-        const float ms = m[r] == ninf ? 0.f : m[r] - kShift;
-#pragma unroll
-        for (int t = 0; t < NB; ++t) {
-          sc[t][2 * r] = kvq::fast_exp2(sc[t][2 * r] - ms);
-          sc[t][2 * r + 1] = kvq::fast_exp2(sc[t][2 * r + 1] - ms);
-          sum[r] += sc[t][2 * r] + sc[t][2 * r + 1];
-        }
-        l[r] = fmaf(sum[r], inv, l[r]);
-      }
-      if (HALVES == 1)
-#pragma unroll
-        for (int t = 0; t < NB; ++t) sc[t][2] = sc[t][3] = 0.f;
-    };
-    // the weights of n-tiles 2 k, 2 k + 1 as the A operand of k-step k
-    auto weights = [&](uint32_t (&p)[4], const float *lo, const float *hi) {
-      p[0] = kvq::h2_as_u32(__floats2half2_rn(lo[0], lo[1]));
-      p[1] = kvq::h2_as_u32(__floats2half2_rn(lo[2], lo[3]));
-      p[2] = kvq::h2_as_u32(__floats2half2_rn(hi[0], hi[1]));
-      p[3] = kvq::h2_as_u32(__floats2half2_rn(hi[2], hi[3]));
-    };
-
-    for (int u = use.u0 + warp; u < use.u1; u += kWarps) {
-      cp_wait<SM::SLOTS - 1>();
-      __syncwarp();
-      const uint32_t kt = ring + slot * SM::SLOT, vt = kt + SM::HALF;
-      if (u < w.full) {
-        const float2 sc2 = *reinterpret_cast<const float2 *>(smem + SM::META + (warp * SM::SLOTS + slot) * 8);
-        float sc[4][4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int row = 8 * t + (g ^ ((g & 1) << 2));
-          const int sw = D == 128 ? (row & 7) : ((row >> 1) & 3);
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
-            const uint4 x = lds16(kt + row * D + (((c * 4 + q4) ^ sw) << 4));
-            const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+          for (int t = 0; t < NB; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const uint32_t word = flip<FMT>(e[i]);
-              const uint64_t b = widen<FMT>(word, 0, word, 1);
-              if (c == 0 && i == 0)
-                mma_zero(sc[t], qa[0], b);
-              else
-                mma(sc[t], qa[c * 4 + i], b);
+              const int col = 16 * t + 8 * (i >> 1) + tok0;
+              float z = sc[t][i];
+              if (window) z += z - z;  // an infinite score becomes NaN
+              if (bad >> col & 1u) z = __int_as_float(0x7fc00000);
+              sc[t][i] = t0 + col > lim[i & 1] ? ninf : z;
             }
-          }
         }
-        const float inf = __int_as_float(0x7f800000);
-        // scales that are not finite make the rows that see the block NaN;
-        // values of magnitude 2^-100 or less (their scale's floor) count as
-        // zeros, of any scale
-        const bool bad = !(fabsf(sc2.x) < inf && fabsf(sc2.y) < inf), none = sc2.y < 8.8e-33f;
-        const float ks = bad ? 1.f : sc2.x, vs = bad || none ? 1.f : sc2.y, lv = __log2f(vs);
-        float ka[2], kb[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float f = ks * qf[r];
-          ka[r] = FMT == KV8_INT8 ? f * 16777216.f : f;
-          kb[r] = FMT == KV8_INT8 ? fmaf(-q128[r], f, lv) : lv;
+#pragma unroll
+          for (int t = 0; t < NB; ++t) mx[r] = fmaxf(fmaxf(mx[r], sc[t][r]), sc[t][r + 2]);
+          mx[r] = fmaxf(mx[r], __shfl_xor_sync(kAll, mx[r], 4));
+          mx[r] = fmaxf(mx[r], __shfl_xor_sync(kAll, mx[r], 8));
+          mx[r] = fmaxf(mx[r], __shfl_xor_sync(kAll, mx[r], 16));
         }
-        softmax(std::integral_constant<int, 4>{}, sc, ka, kb, __fdividef(1.f, vs), u * kUnit, false, bad ? kAll : 0u);
-        uint32_t p[2][4];
-        weights(p[0], sc[0], sc[1]);
-        weights(p[1], sc[2], sc[3]);
-        if (none)
+        if (__any_sync(kAll, mx[0] != m[0] || mx[1] != m[1])) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) p[i >> 2][i & 3] = 0u;
-        // values: lane (g, q4) reads its channels of the 8 tokens of its k indices
-        constexpr int VW = D / 32;  // words per token
-        uint32_t v[8][VW];
+          for (int r = 0; r < 2; ++r) {
+            const float f = mx[r] == m[r] ? 1.f : kvq::fast_exp2(m[r] - mx[r]);  // -inf before the first token
+            m[r] = mx[r];
+            l[r] *= f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {  // token: k-step i / 4, k index 2 q4 + (i & 1) + 8 (i / 2 & 1)
-          const int row = 16 * (i >> 2) + 8 * (i >> 1 & 1) + ((i & 1) ? ((2 * q4 + 1) ^ 4) : 2 * q4);
-          if (D == 128) {
-            const uint4 x = lds16(vt + row * D + ((g ^ (row & 7)) << 4));
-            v[i][0] = x.x;
-            v[i][1] = x.y;
-            v[i][VW > 2 ? 2 : 0] = VW > 2 ? x.z : x.x;
-            v[i][VW > 3 ? 3 : 0] = VW > 3 ? x.w : x.x;
-          } else {
-            const uint2 x = lds8(vt + row * D + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8);
-            v[i][0] = x.x;
-            v[i][1] = x.y;
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < VW; ++j) {
-          // two tokens' codes interleaved: channels 0, 1 and 2, 3 of the word
-          uint32_t lo[4], hi[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            lo[i] = flip<FMT>(__byte_perm(v[2 * i][j], v[2 * i + 1][j], 0x5140));
-            hi[i] = flip<FMT>(__byte_perm(v[2 * i][j], v[2 * i + 1][j], 0x7362));
-          }
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            mma(acc[4 * j], p[k], widen<FMT>(lo[2 * k], 0, lo[2 * k + 1], 0));
-            mma(acc[4 * j + 1], p[k], widen<FMT>(lo[2 * k], 1, lo[2 * k + 1], 1));
-            mma(acc[4 * j + 2], p[k], widen<FMT>(hi[2 * k], 0, hi[2 * k + 1], 0));
-            mma(acc[4 * j + 3], p[k], widen<FMT>(hi[2 * k], 1, hi[2 * k + 1], 1));
-          }
-        }
-        if (FMT == KV8_INT8) {  // sums of the rounded weights
-          mma(accw, p[0], 0x3c003c00u, 0x3c003c00u);
-          mma(accw, p[1], 0x3c003c00u, 0x3c003c00u);
-        }
-      } else {
-        // ---- 16 window tokens in 16 bits
-        const int t0 = (u - w.full) * kWinUnit;
-        float sc[2][4];
-        uint32_t qb[BF16 ? KS : 1][4];  // the queries in bf16: exact, they came from it
-        if (BF16) {
-#pragma unroll
-          for (int k = 0; k < KS; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 x = unpack2<false>(qa[k][i]);
-              qb[BF16 ? k : 0][i] = pack2<true>(x.x, x.y);
+            for (int j = 0; j < MT; ++j) {
+              acc[j][r] *= f;
+              acc[j][r + 2] *= f;
             }
+          }
         }
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int row = 8 * t + (g ^ ((g & 1) << 2));
+        for (int r = 0; r < 2; ++r) {
+          const float ms = m[r] == ninf ? 0.f : m[r] - kShift;
+          float sum = 0.f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sc[t][i] = 0.f;
+          for (int t = 0; t < NB; ++t) {
+            sc[t][r] = kvq::fast_exp2(sc[t][r] - ms);
+            sc[t][r + 2] = kvq::fast_exp2(sc[t][r + 2] - ms);
+            sum += sc[t][r] + sc[t][r + 2];
+          }
+          l[r] = fmaf(sum, inv, l[r]);
+        }
+      };
+
+      for (int u = use.u0 + warp; u < use.u1; u += kWarps) {
+        cp_wait<SM::SLOTS - 1>();
+        __syncwarp();
+        const uint32_t kt = ring + slot * SM::SLOT, vt = kt + SM::HALF;
+        if (u < w.full) {
+          const float2 sc2 = *reinterpret_cast<const float2 *>(smem + SM::META + (warp * SM::SLOTS + slot) * 8);
+          float sc[2][4];
 #pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
+          for (int t = 0; t < 2; ++t) {
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              const uint4 x = lds16(kt + row * 2 * D + ((((c * 4 + q4) * 2 + hf) ^ (row & 7)) << 4));
-              const int k = c * 4 + 2 * hf;
-              if (BF16) {
-                mma_bf16(sc[t], qb[BF16 ? k : 0], x.x, x.y);
-                mma_bf16(sc[t], qb[BF16 ? k + 1 : 0], x.z, x.w);
-              } else {
-                mma(sc[t], qa[k], x.x, x.y);
-                mma(sc[t], qa[k + 1], x.z, x.w);
+            for (int i = 0; i < 4; ++i) sc[t][i] = 0.f;
+            const int row = 16 * t + tok0;  // and row + 8: the same swizzle
+            const int sw0 = D == 128 ? (row & 7) : ((row >> 1) & 3), sw1 = D == 128 ? sw0 : (((row + 8) >> 1) & 3);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+              const uint4 x = lds16(kt + row * D + (((c * 4 + q4) ^ sw0) << 4));
+              const uint4 y = lds16(kt + (row + 8) * D + (((c * 4 + q4) ^ sw1) << 4));
+              const uint32_t e[4] = {x.x, x.y, x.z, x.w}, f[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t w0 = flip<FMT>(e[i]), w1 = flip<FMT>(f[i]);
+                mma_a<FMT, true>(sc[t], w0, 0, w1, 0, w0, 1, w1, 1, qb[c * 4 + i]);
               }
             }
           }
-        }
-        constexpr int VW = D / 16;  // words of the lane's channels per token (2 channels each)
-        uint32_t v[4][VW];
-        uint32_t bad = 0;
+          const float inf = __int_as_float(0x7f800000);
+          // scales that are not finite make the rows that see the block NaN;
+          // values of magnitude 2^-100 or less (their scale's floor) count as
+          // zeros, of any scale
+          const bool bad = !(fabsf(sc2.x) < inf && fabsf(sc2.y) < inf), none = sc2.y < 8.8e-33f;
+          const float ks = bad ? 1.f : sc2.x, vs = bad || none ? 1.f : sc2.y, lv = __log2f(vs);
+          float ka[2], kb[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = 8 * (i >> 1) + ((i & 1) ? ((2 * q4 + 1) ^ 4) : 2 * q4);
-          uint32_t any = 0;
+          for (int r = 0; r < 2; ++r) {
+            const float f = ks * rf[r];
+            ka[r] = FMT == KV8_INT8 ? f * 16777216.f : f;
+            kb[r] = FMT == KV8_INT8 ? fmaf(-r128[r], f, lv) : lv;
+          }
+          softmax(std::integral_constant<int, 2>{}, sc, ka, kb, __fdividef(1.f, vs), u * kUnit, false, bad ? kAll : 0u);
+          uint32_t p[2][2];  // weights as B fragments of the two k-steps
 #pragma unroll
-          for (int k = 0; k < VW / 4; ++k) {
-            const uint4 x = lds16(vt + row * 2 * D + (((g * (VW / 4) + k) ^ (row & 7)) << 4));
-            const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+          for (int t = 0; t < 2; ++t) {
+            p[t][0] = transpose(kvq::h2_as_u32(__floats2half2_rn(sc[t][0], sc[t][1])));
+            p[t][1] = transpose(kvq::h2_as_u32(__floats2half2_rn(sc[t][2], sc[t][3])));
+            if (none) p[t][0] = p[t][1] = 0u;
+          }
+          // values: lane (g, q4) reads its channels of the k-step's tokens 2 q4,
+          // (2 q4 + 1) ^ 4 and those 8 behind
+          constexpr int VW = D / 32;  // words per token
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              v[i][4 * k + c] = e[c];
-              any |= __vcmpgeu2(e[c] & 0x7fff7fffu, nonfinite_bits<BF16>() * 0x10001u);
+          for (int t = 0; t < 2; ++t) {
+            uint32_t v[4][VW];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int row = 16 * t + 8 * (i >> 1) + ((i & 1) ? ((2 * q4 + 1) ^ 4) : 2 * q4);
+              if (D == 128) {
+                const uint4 x = lds16(vt + row * D + ((g ^ (row & 7)) << 4));
+                v[i][0] = x.x;
+                v[i][1] = x.y;
+                v[i][VW > 2 ? 2 : 0] = VW > 2 ? x.z : x.x;
+                v[i][VW > 3 ? 3 : 0] = VW > 3 ? x.w : x.x;
+              } else {
+                const uint2 x = lds8(vt + row * D + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8);
+                v[i][0] = x.x;
+                v[i][1] = x.y;
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < VW; ++j) {
+              // two tokens' codes interleaved: channels 0, 1 and 2, 3 of the word
+              const uint32_t a0 = flip<FMT>(__byte_perm(v[0][j], v[1][j], 0x5140));
+              const uint32_t a1 = flip<FMT>(__byte_perm(v[0][j], v[1][j], 0x7362));
+              const uint32_t b0 = flip<FMT>(__byte_perm(v[2][j], v[3][j], 0x5140));
+              const uint32_t b1 = flip<FMT>(__byte_perm(v[2][j], v[3][j], 0x7362));
+              mma_a<FMT, false>(acc[2 * j], a0, 0, a0, 1, b0, 0, b0, 1, p[t]);
+              mma_a<FMT, false>(acc[2 * j + 1], a1, 0, a1, 1, b1, 0, b1, 1, p[t]);
             }
           }
-          if (any) bad |= 1u << row;
-        }
-        bad = __reduce_or_sync(kAll, bad);
-        const float zero[2] = {0.f, 0.f};
-        softmax(std::integral_constant<int, 2>{}, sc, qf, zero, 1.f, w.full * kUnit + t0, true, bad);
-        // what a window value times its weight counts in acc
-        constexpr float kWin = (BF16 ? 32768.f : 1.f) / (FMT == KV8_INT8 ? 16777216.f : 1.f);
-        uint32_t p[4], rest[4];
-        if (BF16) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float x = sc[i >> 1][2 * (i & 1)] * kUnshift, y = sc[i >> 1][2 * (i & 1) + 1] * kUnshift;
-            p[i] = pack2<true>(x, y);
-            const float2 f = unpack2<true>(p[i]);
-            rest[i] = pack2<true>(x - f.x, y - f.y);
-          }
         } else {
-          weights(p, sc[0], sc[1]);
-        }
-        if (bad) {  // their weights are NaN where they are seen, and 0 elsewhere
+          // ---- 16 window tokens in 16 bits
+          const int t0 = (u - w.full) * kWinUnit;
+          float sc[1][4] = {{0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const uint32_t at = kt + tok0 * 2 * D + ((((c * 4 + q4) * 2 + hf) ^ (tok0 & 7)) << 4);
+              const uint4 x = lds16(at), y = lds16(at + 16 * D);
+              const uint32_t e[4] = {x.x, x.y, x.z, x.w}, f[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int k = c * 4 + 2 * hf + i;
+                const uint32_t av[4] = {e[2 * i], f[2 * i], e[2 * i + 1], f[2 * i + 1]};
+                if (BF16) {  // the queries in bf16: exact, they came from it
+                  const float2 q0 = unpack2<false>(qb[k][0]), q1 = unpack2<false>(qb[k][1]);
+                  mma_bf16(sc[0], av, pack2<true>(q0.x, q0.y), pack2<true>(q1.x, q1.y));
+                } else {
+                  mma(sc[0], av, qb[k][0], qb[k][1]);
+                }
+              }
+            }
+          constexpr int VW = D / 16;  // words of the lane's channels per token (2 channels each)
+          uint32_t v[4][VW];
+          uint32_t bad = 0;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int row = 8 * (i >> 1) + ((i & 1) ? ((2 * q4 + 1) ^ 4) : 2 * q4);
-            if (bad >> row & 1u)
+            uint32_t any = 0;
 #pragma unroll
-              for (int k = 0; k < VW; ++k) v[i][k] = 0u;
+            for (int k = 0; k < VW / 4; ++k) {
+              const uint4 x = lds16(vt + row * 2 * D + (((g * (VW / 4) + k) ^ (row & 7)) << 4));
+              const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                v[i][4 * k + c] = e[c];
+                any |= __vcmpgeu2(e[c] & 0x7fff7fffu, nonfinite_bits<BF16>() * 0x10001u);
+              }
+            }
+            if (any) bad |= 1u << row;
           }
-        }
+          bad = __reduce_or_sync(kAll, bad);
+          const float zero[2] = {0.f, 0.f};
+          softmax(std::integral_constant<int, 1>{}, sc, rf, zero, 1.f, w.full * kUnit + t0, true, bad);
+          if (bad) {  // their weights are NaN where they are seen, and 0 elsewhere
 #pragma unroll
-        for (int k = 0; k < VW; ++k) {
+            for (int i = 0; i < 4; ++i) {
+              const int row = 8 * (i >> 1) + ((i & 1) ? ((2 * q4 + 1) ^ 4) : 2 * q4);
+              if (bad >> row & 1u)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const uint32_t b0 = __byte_perm(v[0][k], v[1][k], c ? 0x7632 : 0x5410);
-            const uint32_t b1 = __byte_perm(v[2][k], v[3][k], c ? 0x7632 : 0x5410);
+                for (int k = 0; k < VW; ++k) v[i][k] = 0u;
+            }
+          }
+          uint32_t p[2], rest[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float x = sc[0][2 * i] * (BF16 ? kUnshift : 1.f), y = sc[0][2 * i + 1] * (BF16 ? kUnshift : 1.f);
+            const uint32_t hi = pack2<BF16>(x, y);
+            p[i] = transpose(hi);
+            if (BF16) {
+              const float2 f = unpack2<true>(hi);
+              rest[i] = transpose(pack2<true>(x - f.x, y - f.y));
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < VW; ++j) {
+            const uint32_t av[4] = {__byte_perm(v[0][j], v[1][j], 0x5410), __byte_perm(v[0][j], v[1][j], 0x7632),
+                                    __byte_perm(v[2][j], v[3][j], 0x5410), __byte_perm(v[2][j], v[3][j], 0x7632)};
             float o[4] = {0.f, 0.f, 0.f, 0.f};
             if (BF16) {
-              mma_bf16(o, p, b0, b1);
-              mma_bf16(o, rest, b0, b1);
+              mma_bf16(o, av, p[0], p[1]);
+              mma_bf16(o, av, rest[0], rest[1]);
             } else {
-              mma(o, p, b0, b1);
+              mma(o, av, p[0], p[1]);
             }
 #pragma unroll
-            for (int r = 0; r < REGS; ++r) acc[2 * k + c][r] = fmaf(o[r], kWin, acc[2 * k + c][r]);
+            for (int i = 0; i < 4; ++i) acc[j][i] = fmaf(o[i], kWin, acc[j][i]);
+          }
+        }
+        __syncwarp();  // every lane has read the slot
+        fetch(slot);
+        slot = slot + 1 == SM::SLOTS ? 0 : slot + 1;
+      }
+
+      // ---- merge the four warps' states; warp w ends up with quarter w of the
+      // m-tiles
+      float2 *ml = reinterpret_cast<float2 *>(smem + SM::ML);
+      float *xch = reinterpret_cast<float *>(smem + SM::XCH);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        l[r] += __shfl_xor_sync(kAll, l[r], 4);
+        l[r] += __shfl_xor_sync(kAll, l[r], 8);
+        l[r] += __shfl_xor_sync(kAll, l[r], 16);
+        l[r] *= kUnshift;
+        if (g == 0) ml[warp * kRowTile + 2 * q4 + r] = make_float2(m[r], l[r]);
+      }
+      __syncthreads();
+      whole = use.u0 == 0 && use.u1 == w.units;
+      const int part = 2 * blockIdx.x + (use.start + use.u0 == lo ? 0 : 1);
+      constexpr int QT = MT / 4;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float mm = ninf, ll = 0.f;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) mm = fmaxf(mm, ml[i * kRowTile + 2 * q4 + r].x);
+        const float base = mm == ninf ? 0.f : mm;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+          const float2 e = ml[i * kRowTile + 2 * q4 + r];
+          ll += e.y * kvq::fast_exp2(e.x - base);
+        }
+        const float f = kvq::fast_exp2(m[r] - base);
+        if (r) __syncthreads();  // the buffer of the first row has been read
+        float2 o[QT];
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+          float x[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float raw = acc[j][r + 2 * i];
+            x[i] = f * (raw * kUnshift);
+          }
+          const int dst = j / QT;
+          if (dst != warp) {
+            float *b = xch + ((dst * 3 + ((warp - dst - 1) & 3)) * QT + j % QT) * 64 + lane;
+            b[0] = x[0];
+            b[32] = x[1];
+          } else {
+            o[j % QT] = make_float2(x[0], x[1]);
+          }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < QT; ++j)
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            const float *b = xch + ((warp * 3 + i) * QT + j) * 64 + lane;
+            o[j].x += b[0];
+            o[j].y += b[32];
+          }
+        // m-tile j holds channels (D / 8) g + 2 j and the next one
+        const int ch = (D / 8) * g + 2 * QT * warp, row = r0 + 2 * q4 + r;
+        if (row < n_rows) {
+          if (whole) {
+            const float inv = ll == 0.f ? 0.f : 1.f / ll;
+            const int tok = row / a.group;
+            uint16_t *dst = a.out.p + (static_cast<long long>(w.q.row0) + tok) * a.out.row +
+                            (static_cast<long long>(use.h) * a.group + row - tok * a.group) * a.out.head + ch;
+#pragma unroll
+            for (int j = 0; j < QT; ++j)
+              *reinterpret_cast<uint32_t *>(dst + 2 * j) = pack2<BF16>(o[j].x * inv, o[j].y * inv);
+          } else {
+            float *dst = a.part_o + (static_cast<size_t>(part) * kRowTile + 2 * q4 + r) * D + ch;
+#pragma unroll
+            for (int j = 0; j < QT; ++j) *reinterpret_cast<float2 *>(dst + 2 * j) = o[j];
+            if (warp == 0 && g == 0) a.part_ml[part * kRowTile + 2 * q4 + r] = make_float2(mm, ll);
           }
         }
       }
-      __syncwarp();  // every lane has read the slot
-      fetch(slot);
-      slot = slot + 1 == SM::SLOTS ? 0 : slot + 1;
-    }
-
-    // ---- merge the four warps' states; warp w ends up with quarter w of the
-    // n-tiles
-    float2 *ml = reinterpret_cast<float2 *>(smem + SM::ML);
-    float *xch = reinterpret_cast<float *>(smem + SM::XCH);
+    } else {
+      // ================ up to sixteen rows are M, tokens (then channels) N.
+      // ---- the tile's queries as A fragments; lane (g, q4) holds 16 channels
+      // of rows g and g + 8 per 64 channels
+      uint32_t qa[KS][4];
+      float qf[2], q128[2] = {0.f, 0.f};
+      int lim[2];  // last position each row sees
 #pragma unroll
-    for (int r = 0; r < HALVES; ++r) {
-      l[r] += __shfl_xor_sync(kAll, l[r], 1);
-      l[r] += __shfl_xor_sync(kAll, l[r], 2);
-      l[r] *= kUnshift;
+      for (int r = 0; r < 2; ++r) {
+        const int row = r0 + g + 8 * r;
+        const bool valid = (r == 0 || HALVES == 2) && row < n_rows;
+        const int tok = valid ? row / a.group : 0;
+        lim[r] = valid ? w.q.L - w.q.n + tok : -1;
+        const uint16_t *src = a.q.p + (static_cast<long long>(w.q.row0) + tok) * a.q.row +
+                              (static_cast<long long>(use.h) * a.group + (valid ? row - tok * a.group : 0)) * a.q.head;
+        uint32_t big = 0;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
+          if (valid) {
+            x = *reinterpret_cast<const uint4 *>(src + (c * 4 + q4) * 16);
+            y = *reinterpret_cast<const uint4 *>(src + (c * 4 + q4) * 16 + 8);
+          }
+          const uint32_t e[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            qa[c * 4 + i / 2][r + 2 * (i & 1)] = e[i];
+            if (BF16) big = finite_max(big, e[i], 0x7f80u);
+          }
+        }
+        qf[r] = a.zscale;
+        if (BF16) {
+          big = max(big, __shfl_xor_sync(kAll, big, 1));
+          big = max(big, __shfl_xor_sync(kAll, big, 2));
+          const float2 f = bf16_norm(big);
+          qf[r] *= f.y;
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            qa[k][r] = bf16_to_fp16(qa[k][r], f.x);
+            qa[k][r + 2] = bf16_to_fp16(qa[k][r + 2], f.x);
+          }
+        }
+        if (FMT == KV8_INT8 && r < HALVES) {
+          float sum = 0.f;
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            const float2 x = unpack2<false>(qa[k][r]), y = unpack2<false>(qa[k][r + 2]);
+            sum += (x.x + x.y) + (y.x + y.y);
+          }
+          sum += __shfl_xor_sync(kAll, sum, 1);
+          sum += __shfl_xor_sync(kAll, sum, 2);
+          q128[r] = 128.f * sum;
+        }
+      }
+      // every row of the tile sees at least the tokens up to here
+      const int seen_by_all = w.q.L - w.q.n + r0 / a.group;
+
+      float acc[NT][4], m[2] = {ninf, ninf}, l[2] = {0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          acc[j][2 * r + i] = FMT == KV8_INT8 ? fmaf(acc[j][2 * r + i], 512.f, accw[2 * r] * (-128.f * kUnshift))
-                                              : acc[j][2 * r + i] * kUnshift;
-      if (q4 == 0) ml[warp * kRowTile + g + 8 * r] = make_float2(m[r], l[r]);
-    }
-    __syncthreads();
-    const bool whole = use.u0 == 0 && use.u1 == w.units;
-    const int part = 2 * blockIdx.x + (use.start + use.u0 == lo ? 0 : 1);
-    constexpr int QT = NT / 4;
+        for (int r = 0; r < 4; ++r) acc[j][r] = 0.f;
+
+      // Scores of one unit to weights 2^15 w: NB n-tiles of 8 tokens from position
+      // t0; column 2 q4 of a tile is token 2 q4, column 2 q4 + 1 token (2 q4 + 1) ^ 4.
+      // z = s a + b for the two rows; `bad`: tokens that turn what sees them to NaN.
+      auto softmax = [&](auto nb, float (*sc)[4], const float (&ka)[2], const float (&kb)[2], float inv, int t0,
+                         bool window, uint32_t bad) {
+        constexpr int NB = decltype(nb)::value;
+        float mx[2] = {m[0], m[1]};
 #pragma unroll
-    for (int r = 0; r < HALVES; ++r) {
-      float mm = ninf, ll = 0.f;
+        for (int t = 0; t < NB; ++t)
 #pragma unroll
-      for (int i = 0; i < kWarps; ++i) mm = fmaxf(mm, ml[i * kRowTile + g + 8 * r].x);
-      const float base = mm == ninf ? 0.f : mm;
+          for (int i = 0; i < REGS; ++i) sc[t][i] = fmaf(sc[t][i], ka[i >> 1], kb[i >> 1]);
+        if (window || bad || t0 + 8 * NB - 1 > seen_by_all) {
 #pragma unroll
-      for (int i = 0; i < kWarps; ++i) {
-        const float2 e = ml[i * kRowTile + g + 8 * r];
-        ll += e.y * kvq::fast_exp2(e.x - base);
-      }
-      const float f = kvq::fast_exp2(m[r] - base);
-      if (r) __syncthreads();  // the buffer of the first half has been read
+          for (int t = 0; t < NB; ++t)
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        acc[j][2 * r] *= f;
-        acc[j][2 * r + 1] *= f;
-        const int dst = j / QT;
-        if (dst != warp) {
-          float *o = xch + ((dst * 3 + ((warp - dst - 1) & 3)) * QT + j % QT) * 64 + lane;
-          o[0] = acc[j][2 * r];
-          o[32] = acc[j][2 * r + 1];
+            for (int i = 0; i < REGS; ++i) {
+              const int col = 8 * t + ((i & 1) ? ((2 * q4 + 1) ^ 4) : 2 * q4);
+              float z = sc[t][i];
+              if (window) z += z - z;  // an infinite score becomes NaN
+              if (bad >> col & 1u) z = __int_as_float(0x7fc00000);
+              sc[t][i] = t0 + col > lim[i >> 1] ? ninf : z;
+            }
         }
-      }
-      __syncthreads();
-      float o0[QT], o1[QT];
 #pragma unroll
-      for (int j = 0; j < QT; ++j) {
-        o0[j] = o1[j] = 0.f;
+        for (int t = 0; t < NB; ++t)
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (k == warp) {
-            o0[j] = acc[k * QT + j][2 * r];
-            o1[j] = acc[k * QT + j][2 * r + 1];
+          for (int i = 0; i < REGS; i += 2) mx[i >> 1] = fmaxf(fmaxf(mx[i >> 1], sc[t][i]), sc[t][i + 1]);
+#pragma unroll
+        for (int r = 0; r < HALVES; ++r) {
+          mx[r] = fmaxf(mx[r], __shfl_xor_sync(kAll, mx[r], 1));
+          mx[r] = fmaxf(mx[r], __shfl_xor_sync(kAll, mx[r], 2));
+        }
+        bool moved = mx[0] != m[0];
+        if (HALVES == 2) moved |= mx[1] != m[1];
+        if (__any_sync(kAll, moved)) {
+#pragma unroll
+          for (int r = 0; r < HALVES; ++r) {
+            const float f = mx[r] == m[r] ? 1.f : kvq::fast_exp2(m[r] - mx[r]);  // -inf before the first token
+            m[r] = mx[r];
+            l[r] *= f;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              acc[j][2 * r] *= f;
+              acc[j][2 * r + 1] *= f;
+            }
+          }
+        }
+        float sum[2] = {0.f, 0.f};
+#pragma unroll
+        for (int r = 0; r < HALVES; ++r) {
+          const float ms = m[r] == ninf ? 0.f : m[r] - kShift;
+#pragma unroll
+          for (int t = 0; t < NB; ++t) {
+            sc[t][2 * r] = kvq::fast_exp2(sc[t][2 * r] - ms);
+            sc[t][2 * r + 1] = kvq::fast_exp2(sc[t][2 * r + 1] - ms);
+            sum[r] += sc[t][2 * r] + sc[t][2 * r + 1];
+          }
+          l[r] = fmaf(sum[r], inv, l[r]);
+        }
+        if (HALVES == 1)
+#pragma unroll
+          for (int t = 0; t < NB; ++t) sc[t][2] = sc[t][3] = 0.f;
+      };
+      // the weights of n-tiles 2 k, 2 k + 1 as the A operand of k-step k
+      auto weights = [&](uint32_t (&p)[4], const float *lo, const float *hi) {
+        p[0] = kvq::h2_as_u32(__floats2half2_rn(lo[0], lo[1]));
+        p[1] = kvq::h2_as_u32(__floats2half2_rn(lo[2], lo[3]));
+        p[2] = kvq::h2_as_u32(__floats2half2_rn(hi[0], hi[1]));
+        p[3] = kvq::h2_as_u32(__floats2half2_rn(hi[2], hi[3]));
+      };
+
+      for (int u = use.u0 + warp; u < use.u1; u += kWarps) {
+        cp_wait<SM::SLOTS - 1>();
+        __syncwarp();
+        const uint32_t kt = ring + slot * SM::SLOT, vt = kt + SM::HALF;
+        if (u < w.full) {
+          const float2 sc2 = *reinterpret_cast<const float2 *>(smem + SM::META + (warp * SM::SLOTS + slot) * 8);
+          float sc[4][4];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const int row = 8 * t + (g ^ ((g & 1) << 2));
+            const int sw = D == 128 ? (row & 7) : ((row >> 1) & 3);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+              const uint4 x = lds16(kt + row * D + (((c * 4 + q4) ^ sw) << 4));
+              const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t word = flip<FMT>(e[i]);
+                const uint64_t b = widen<FMT, true>(word, 0, word, 1);
+                if (c == 0 && i == 0)
+                  mma_zero(sc[t], qa[0], b);
+                else
+                  mma(sc[t], qa[c * 4 + i], b);
+              }
+            }
+          }
+          const float inf = __int_as_float(0x7f800000);
+          // scales that are not finite make the rows that see the block NaN;
+          // values of magnitude 2^-100 or less (their scale's floor) count as
+          // zeros, of any scale
+          const bool bad = !(fabsf(sc2.x) < inf && fabsf(sc2.y) < inf), none = sc2.y < 8.8e-33f;
+          const float ks = bad ? 1.f : sc2.x, vs = bad || none ? 1.f : sc2.y, lv = __log2f(vs);
+          float ka[2], kb[2];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float f = ks * qf[r];
+            ka[r] = FMT == KV8_INT8 ? f * 16777216.f : f;
+            kb[r] = FMT == KV8_INT8 ? fmaf(-q128[r], f, lv) : lv;
+          }
+          softmax(std::integral_constant<int, 4>{}, sc, ka, kb, __fdividef(1.f, vs), u * kUnit, false, bad ? kAll : 0u);
+          uint32_t p[2][4];
+          weights(p[0], sc[0], sc[1]);
+          weights(p[1], sc[2], sc[3]);
+          if (none)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p[i >> 2][i & 3] = 0u;
+          // values: lane (g, q4) reads its channels of the 8 tokens of its k indices
+          constexpr int VW = D / 32;  // words per token
+          uint32_t v[8][VW];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {  // token: k-step i / 4, k index 2 q4 + (i & 1) + 8 (i / 2 & 1)
+            const int row = 16 * (i >> 2) + 8 * (i >> 1 & 1) + ((i & 1) ? ((2 * q4 + 1) ^ 4) : 2 * q4);
+            if (D == 128) {
+              const uint4 x = lds16(vt + row * D + ((g ^ (row & 7)) << 4));
+              v[i][0] = x.x;
+              v[i][1] = x.y;
+              v[i][VW > 2 ? 2 : 0] = VW > 2 ? x.z : x.x;
+              v[i][VW > 3 ? 3 : 0] = VW > 3 ? x.w : x.x;
+            } else {
+              const uint2 x = lds8(vt + row * D + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8);
+              v[i][0] = x.x;
+              v[i][1] = x.y;
+            }
           }
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
-          const float *x = xch + ((warp * 3 + i) * QT + j) * 64 + lane;
-          o0[j] += x[0];
-          o1[j] += x[32];
-        }
-      }
-      // n-tile j, column c holds channel (D / 8) c + j
-      const int ch0 = (D / 8) * (2 * q4) + warp * QT, ch1 = ch0 + D / 8;
-      const int row = r0 + g + 8 * r;
-      if (row < n_rows) {
-        if (whole) {
-          const float inv = ll == 0.f ? 0.f : 1.f / ll;
-          const int tok = row / a.group;
-          uint16_t *dst = a.out.p + (static_cast<long long>(w.q.row0) + tok) * a.out.row +
-                          (static_cast<long long>(use.h) * a.group + row - tok * a.group) * a.out.head;
+          for (int j = 0; j < VW; ++j) {
+            // two tokens' codes interleaved: channels 0, 1 and 2, 3 of the word
+            uint32_t lo[4], hi[4];
 #pragma unroll
-          for (int j = 0; j < QT; j += 2) {
-            *reinterpret_cast<uint32_t *>(dst + ch0 + j) = pack2<BF16>(o0[j] * inv, o0[j + 1] * inv);
-            *reinterpret_cast<uint32_t *>(dst + ch1 + j) = pack2<BF16>(o1[j] * inv, o1[j + 1] * inv);
+            for (int i = 0; i < 4; ++i) {
+              lo[i] = flip<FMT>(__byte_perm(v[2 * i][j], v[2 * i + 1][j], 0x5140));
+              hi[i] = flip<FMT>(__byte_perm(v[2 * i][j], v[2 * i + 1][j], 0x7362));
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              mma(acc[4 * j], p[k], widen<FMT, false>(lo[2 * k], 0, lo[2 * k + 1], 0));
+              mma(acc[4 * j + 1], p[k], widen<FMT, false>(lo[2 * k], 1, lo[2 * k + 1], 1));
+              mma(acc[4 * j + 2], p[k], widen<FMT, false>(hi[2 * k], 0, hi[2 * k + 1], 0));
+              mma(acc[4 * j + 3], p[k], widen<FMT, false>(hi[2 * k], 1, hi[2 * k + 1], 1));
+            }
           }
         } else {
-          float *dst = a.part_o + (static_cast<size_t>(part) * kRowTile + g + 8 * r) * D;
+          // ---- 16 window tokens in 16 bits
+          const int t0 = (u - w.full) * kWinUnit;
+          float sc[2][4];
+          uint32_t qb[BF16 ? KS : 1][4];  // the queries in bf16: exact, they came from it
+          if (BF16) {
 #pragma unroll
-          for (int j = 0; j < QT; j += 2) {
-            *reinterpret_cast<float2 *>(dst + ch0 + j) = make_float2(o0[j], o0[j + 1]);
-            *reinterpret_cast<float2 *>(dst + ch1 + j) = make_float2(o1[j], o1[j + 1]);
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float2 x = unpack2<false>(qa[k][i]);
+                qb[BF16 ? k : 0][i] = pack2<true>(x.x, x.y);
+              }
           }
-          if (warp == 0 && q4 == 0) a.part_ml[part * kRowTile + g + 8 * r] = make_float2(mm, ll);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int row = 8 * t + (g ^ ((g & 1) << 2));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sc[t][i] = 0.f;
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf) {
+                const uint4 x = lds16(kt + row * 2 * D + ((((c * 4 + q4) * 2 + hf) ^ (row & 7)) << 4));
+                const int k = c * 4 + 2 * hf;
+                if (BF16) {
+                  mma_bf16(sc[t], qb[BF16 ? k : 0], x.x, x.y);
+                  mma_bf16(sc[t], qb[BF16 ? k + 1 : 0], x.z, x.w);
+                } else {
+                  mma(sc[t], qa[k], x.x, x.y);
+                  mma(sc[t], qa[k + 1], x.z, x.w);
+                }
+              }
+            }
+          }
+          constexpr int VW = D / 16;  // words of the lane's channels per token (2 channels each)
+          uint32_t v[4][VW];
+          uint32_t bad = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = 8 * (i >> 1) + ((i & 1) ? ((2 * q4 + 1) ^ 4) : 2 * q4);
+            uint32_t any = 0;
+#pragma unroll
+            for (int k = 0; k < VW / 4; ++k) {
+              const uint4 x = lds16(vt + row * 2 * D + (((g * (VW / 4) + k) ^ (row & 7)) << 4));
+              const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                v[i][4 * k + c] = e[c];
+                any |= __vcmpgeu2(e[c] & 0x7fff7fffu, nonfinite_bits<BF16>() * 0x10001u);
+              }
+            }
+            if (any) bad |= 1u << row;
+          }
+          bad = __reduce_or_sync(kAll, bad);
+          const float zero[2] = {0.f, 0.f};
+          softmax(std::integral_constant<int, 2>{}, sc, qf, zero, 1.f, w.full * kUnit + t0, true, bad);
+          uint32_t p[4], rest[4];
+          if (BF16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float x = sc[i >> 1][2 * (i & 1)] * kUnshift, y = sc[i >> 1][2 * (i & 1) + 1] * kUnshift;
+              p[i] = pack2<true>(x, y);
+              const float2 f = unpack2<true>(p[i]);
+              rest[i] = pack2<true>(x - f.x, y - f.y);
+            }
+          } else {
+            weights(p, sc[0], sc[1]);
+          }
+          if (bad) {  // their weights are NaN where they are seen, and 0 elsewhere
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int row = 8 * (i >> 1) + ((i & 1) ? ((2 * q4 + 1) ^ 4) : 2 * q4);
+              if (bad >> row & 1u)
+#pragma unroll
+                for (int k = 0; k < VW; ++k) v[i][k] = 0u;
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < VW; ++k) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const uint32_t b0 = __byte_perm(v[0][k], v[1][k], c ? 0x7632 : 0x5410);
+              const uint32_t b1 = __byte_perm(v[2][k], v[3][k], c ? 0x7632 : 0x5410);
+              float o[4] = {0.f, 0.f, 0.f, 0.f};
+              if (BF16) {
+                mma_bf16(o, p, b0, b1);
+                mma_bf16(o, rest, b0, b1);
+              } else {
+                mma(o, p, b0, b1);
+              }
+#pragma unroll
+              for (int r = 0; r < REGS; ++r) acc[2 * k + c][r] = fmaf(o[r], kWin, acc[2 * k + c][r]);
+            }
+          }
+        }
+        __syncwarp();  // every lane has read the slot
+        fetch(slot);
+        slot = slot + 1 == SM::SLOTS ? 0 : slot + 1;
+      }
+
+      // ---- merge the four warps' states; warp w ends up with quarter w of the
+      // n-tiles
+      float2 *ml = reinterpret_cast<float2 *>(smem + SM::ML);
+      float *xch = reinterpret_cast<float *>(smem + SM::XCH);
+#pragma unroll
+      for (int r = 0; r < HALVES; ++r) {
+        l[r] += __shfl_xor_sync(kAll, l[r], 1);
+        l[r] += __shfl_xor_sync(kAll, l[r], 2);
+        l[r] *= kUnshift;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            acc[j][2 * r + i] *= kUnshift;
+        if (q4 == 0) ml[warp * kRowTile + g + 8 * r] = make_float2(m[r], l[r]);
+      }
+      __syncthreads();
+      whole = use.u0 == 0 && use.u1 == w.units;
+      const int part = 2 * blockIdx.x + (use.start + use.u0 == lo ? 0 : 1);
+      constexpr int QT = NT / 4;
+#pragma unroll
+      for (int r = 0; r < HALVES; ++r) {
+        float mm = ninf, ll = 0.f;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) mm = fmaxf(mm, ml[i * kRowTile + g + 8 * r].x);
+        const float base = mm == ninf ? 0.f : mm;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+          const float2 e = ml[i * kRowTile + g + 8 * r];
+          ll += e.y * kvq::fast_exp2(e.x - base);
+        }
+        const float f = kvq::fast_exp2(m[r] - base);
+        if (r) __syncthreads();  // the buffer of the first half has been read
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          acc[j][2 * r] *= f;
+          acc[j][2 * r + 1] *= f;
+          const int dst = j / QT;
+          if (dst != warp) {
+            float *o = xch + ((dst * 3 + ((warp - dst - 1) & 3)) * QT + j % QT) * 64 + lane;
+            o[0] = acc[j][2 * r];
+            o[32] = acc[j][2 * r + 1];
+          }
+        }
+        __syncthreads();
+        float o0[QT], o1[QT];
+#pragma unroll
+        for (int j = 0; j < QT; ++j) {
+          o0[j] = o1[j] = 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k == warp) {
+              o0[j] = acc[k * QT + j][2 * r];
+              o1[j] = acc[k * QT + j][2 * r + 1];
+            }
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            const float *x = xch + ((warp * 3 + i) * QT + j) * 64 + lane;
+            o0[j] += x[0];
+            o1[j] += x[32];
+          }
+        }
+        // n-tile j, column c holds channel (D / 8) c + j
+        const int ch0 = (D / 8) * (2 * q4) + warp * QT, ch1 = ch0 + D / 8;
+        const int row = r0 + g + 8 * r;
+        if (row < n_rows) {
+          if (whole) {
+            const float inv = ll == 0.f ? 0.f : 1.f / ll;
+            const int tok = row / a.group;
+            uint16_t *dst = a.out.p + (static_cast<long long>(w.q.row0) + tok) * a.out.row +
+                            (static_cast<long long>(use.h) * a.group + row - tok * a.group) * a.out.head;
+#pragma unroll
+            for (int j = 0; j < QT; j += 2) {
+              *reinterpret_cast<uint32_t *>(dst + ch0 + j) = pack2<BF16>(o0[j] * inv, o0[j + 1] * inv);
+              *reinterpret_cast<uint32_t *>(dst + ch1 + j) = pack2<BF16>(o1[j] * inv, o1[j + 1] * inv);
+            }
+          } else {
+            float *dst = a.part_o + (static_cast<size_t>(part) * kRowTile + g + 8 * r) * D;
+#pragma unroll
+            for (int j = 0; j < QT; j += 2) {
+              *reinterpret_cast<float2 *>(dst + ch0 + j) = make_float2(o0[j], o0[j + 1]);
+              *reinterpret_cast<float2 *>(dst + ch1 + j) = make_float2(o1[j], o1[j + 1]);
+            }
+            if (warp == 0 && q4 == 0) a.part_ml[part * kRowTile + g + 8 * r] = make_float2(mm, ll);
+          }
         }
       }
+
     }
 
     if (!whole) {
@@ -875,12 +1265,16 @@ cudaError_t launch_one(const AttnArgs &a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   int per = dev < 64 ? resident[dev].load() : 0, sms = dev < 64 ? sm_count[dev].load() : 0;
   if (per == 0 || sms == 0) {
-    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::BYTES)) != cudaSuccess)
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D, HALVES>::BYTES)) != cudaSuccess)
       return e;
-    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kWarps * 32, Smem<D>::BYTES)) != cudaSuccess)
+    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kWarps * 32, Smem<D, HALVES>::BYTES)) != cudaSuccess)
       return e;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-    per = max(per, 1);
+    // Three CTAs fit an SM where at most eight rows share the keys.  Few
+    // instructions per byte (int8) keep HBM busy with two, and a third only
+    // spreads the reads (a million tokens x 8 heads: 304 us against 331); the
+    // conversions of e4m3 want it (64 x 8 heads ragged: 111 us against 116).
+    per = min(max(per, 1), FMT == KV8_INT8 ? 2 : 3);
     if (dev < 64) {
       sm_count[dev].store(sms);
       resident[dev].store(per);
@@ -892,7 +1286,7 @@ cudaError_t launch_one(const AttnArgs &a, cudaStream_t stream) {
   const long long units = (a.max_len / kUnit + a.geo.B / kWinUnit) * tiles * a.geo.H * a.geo.S;
   long long grid = min(static_cast<long long>(kMaxCtas), static_cast<long long>(sms) * per);
   grid = max(1LL, min(grid, (units + kWarps - 1) / kWarps));
-  kernel<<<static_cast<unsigned>(grid), kWarps * 32, Smem<D>::BYTES, stream>>>(a);
+  kernel<<<static_cast<unsigned>(grid), kWarps * 32, Smem<D, HALVES>::BYTES, stream>>>(a);
   return cudaGetLastError();
 }
 
