@@ -99,7 +99,7 @@ constexpr int kMaxCtas = 640;
 constexpr int kRowTile = 16;  // (token, query head) rows that share one pass over the keys
 
 // Sequences with more rows per KV head than this go to the tile kernel.
-constexpr int kRowsMax = 64;
+constexpr int kRowsMax = 48;
 constexpr int kTileRows = 256;      // rows of an item of the tile kernel
 constexpr int kMaxTileCtas = 160;
 

@@ -4,17 +4,20 @@
 // A work item is 256 rows -- (new token, query head) pairs of one KV head, two
 // tiles of 128 -- against the keys they see, 128 at a time.  Roles of a CTA:
 //
-//   warps 0-3, 4-7   softmax of row tile 0 and 1: one thread per row.  S comes
-//                    from tensor memory, the weights go back there as fp16.
-//   warps 8-11       bring 128 tokens' codes from the blocks (prefetched one
+//   warps 0-7, 8-15  softmax of row tile 0 and 1: two threads per row, for 64
+//                    keys of a unit each (the instructions of one thread per
+//                    row depend on each other too much to keep the SM busy).
+//                    S comes from tensor memory, the weights go back there as
+//                    fp16.
+//   warps 16-19      bring 128 tokens' codes from the blocks (prefetched one
 //                    tile ahead in registers), widen them to fp16 and store them
 //                    in the 128-byte-swizzled layout the tensor core reads:
 //                    tokens as rows for keys (K-major) and values (MN-major).
-//   warp 12          issues the products: S = Q K^T, then O += P V with P in
+//   warp 20          issues the products: S = Q K^T, then O += P V with P in
 //                    tensor memory.  The two row tiles alternate, so one tile's
 //                    softmax runs under the other's products.
-//   warp 13          walks the CTA's share of the work: a ring of Parts.
-//   warp 14          looks up blocks and scales: a ring of Metas, one per unit.
+//   warp 21          walks the CTA's share of the work: a ring of Parts.
+//   warp 22          looks up blocks and scales: a ring of Metas, one per unit.
 //
 // Parts and Metas live in shared memory so that the other roles keep their
 // registers for data: a spilled register costs an L2 round trip here, as the
@@ -48,7 +51,7 @@ namespace kv8 {
 namespace tiles {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kThreads = 512;
+constexpr int kThreads = 768;
 constexpr int kRows = kTileRows;  // 256 rows of an item
 constexpr int kKeys = 128;        // tokens of a unit
 constexpr int kMetas = 8, kParts = 4, kCols = 4;
@@ -66,12 +69,13 @@ struct Smem {
   static constexpr int META = V + 2 * TILE;       // [kMetas] Meta
   static constexpr int PART = META + kMetas * 128;  // [kParts] Part
   static constexpr int COL = PART + kParts * 64;  // [kCols] window columns: scale_k, log2 scale_v, 1 / scale_v
-  static constexpr int BAR = COL + kCols * 3 * kKeys * 4;
+  static constexpr int ROW = COL + kCols * 3 * kKeys * 4;  // per row: maxima of both halves, two units; exponents, sums
+  static constexpr int BAR = ROW + 6 * kRows * 4;
   static constexpr int MISC = BAR + 48 * 8;
-  static constexpr int BYTES = MISC + 256 + 1024;  // and the alignment of the base
+  static constexpr int BYTES = MISC + 384 + 1024;  // and the alignment of the base
 };
 
-// What the roles need to know of one unit.  A ring of eight: warp 14 reuses a
+// What the roles need to know of one unit.  A ring of eight: warp 22 reuses a
 // slot once keys are stored three units later, which means that the products
 // two units before those are done, and the softmax of the unit before that.
 enum { kPacked, kWindow, kEnd };
@@ -390,82 +394,70 @@ __device__ __forceinline__ uint4 bf16_row_to_fp16(uint4 x, float f) {
   return make_uint4(e[0], e[1], e[2], e[3]);
 }
 
-// The largest z' = S k + log2(scale_v) of a row's 128 columns (EDGE: of the
-// first cmax).  In a window S holds z' already.
+// The largest z' = S k + log2(scale_v) of 64 columns of a row, from group g of 32
+// on (EDGE: of the first cmax).  In a window S holds z' already.
 template <bool EDGE>
-__device__ __forceinline__ float unit_max(std::integral_constant<bool, EDGE>, uint32_t s_at, const Meta &meta, float qf,
-                                          bool window, int cmax) {
+__device__ __forceinline__ float unit_max(std::integral_constant<bool, EDGE>, uint32_t s_at, int g, const Meta &meta,
+                                          float qf, bool window, int cmax) {
   const float ninf = __int_as_float(0xff800000);
   float mx = ninf;
 #pragma unroll 1
-  for (int c = 0; c < 4; c += 2) {
-    uint32_t s[64];
+  for (int c = g; c < g + 2; ++c) {
+    uint32_t s[32];
     tmem_ld32(s, s_at + 32 * c);
-    tmem_ld32(s + 32, s_at + 32 * c + 32);
     wait_ld32(s);
-    wait_ld32(s + 32);
+    const float k = EDGE && window ? 1.f : meta.k[c] * qf, lv = EDGE && window ? 0.f : meta.lv[c];
+    float m[4] = {ninf, ninf, ninf, ninf};
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float k = EDGE && window ? 1.f : meta.k[c + h] * qf, lv = EDGE && window ? 0.f : meta.lv[c + h];
-      float m[4] = {ninf, ninf, ninf, ninf};
-#pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        float x = __uint_as_float(s[32 * h + i]), y = __uint_as_float(s[32 * h + i + 1]);
-        if (EDGE) {
-          const int col = 32 * (c + h) + i;
-          x = col < cmax ? x : ninf;
-          y = col + 1 < cmax ? y : ninf;
-        }
-        m[i / 2 & 3] = fmaxf(fmaxf(m[i / 2 & 3], x), y);
+    for (int i = 0; i < 32; i += 2) {
+      float x = __uint_as_float(s[i]), y = __uint_as_float(s[i + 1]);
+      if (EDGE) {
+        const int col = 32 * c + i;
+        x = col < cmax ? x : ninf;
+        y = col + 1 < cmax ? y : ninf;
       }
-      mx = fmaxf(mx, fmaf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), k, lv));
+      m[i / 2 & 3] = fmaxf(fmaxf(m[i / 2 & 3], x), y);
     }
+    mx = fmaxf(mx, fmaf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), k, lv));
   }
   return mx;
 }
 
-// Weights 2^(z' - ref) of a row's columns, as fp16 over the start of S; their
-// sum over scale_v.
+// Weights 2^(z' - ref) of those columns as fp16 over the start of their half of
+// S; their sum over scale_v.
 template <bool EDGE>
-__device__ __forceinline__ float unit_weights(std::integral_constant<bool, EDGE>, uint32_t s_at, const Meta &meta,
+__device__ __forceinline__ float unit_weights(std::integral_constant<bool, EDGE>, uint32_t s_at, int g, const Meta &meta,
                                               float qf, float ref, bool window, int cmax) {
   const float ninf = __int_as_float(0xff800000);
   float l = 0.f;
-  uint32_t s[2][32];
-  tmem_ld32(s[0], s_at);
-  wait_ld32(s[0]);
 #pragma unroll 1
-  for (int c = 0; c < 4; c += 2) {
+  for (int c = g; c < g + 2; ++c) {
+    uint32_t s[32];
+    tmem_ld32(s, s_at + 32 * c);
+    wait_ld32(s);
+    const float k = EDGE && window ? 1.f : meta.k[c] * qf;
+    const float bias = (EDGE && window ? 0.f : meta.lv[c]) - ref;
+    const uint64_t a2 = pack64(k, k), b2 = pack64(bias, bias);
+    uint64_t sum[2] = {pack64(0.f, 0.f), pack64(0.f, 0.f)};
+    uint32_t pk[16];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      // the next 32 columns are on their way meanwhile
-      if (h == 0 || c == 0) tmem_ld32(s[h ^ 1], s_at + 32 * (c + h + 1));
-      const float k = EDGE && window ? 1.f : meta.k[c + h] * qf;
-      const float bias = (EDGE && window ? 0.f : meta.lv[c + h]) - ref;
-      const uint64_t a2 = pack64(k, k), b2 = pack64(bias, bias);
-      uint64_t sum[2] = {pack64(0.f, 0.f), pack64(0.f, 0.f)};
-      uint32_t pk[16];
-#pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        float x, y;
-        unpack64(fma2(pack64(__uint_as_float(s[h][i]), __uint_as_float(s[h][i + 1])), a2, b2), x, y);
-        if (EDGE) {
-          const int col = 32 * (c + h) + i;
-          x = col < cmax ? x : ninf;
-          y = col + 1 < cmax ? y : ninf;
-        }
-        x = kvq::fast_exp2(x);
-        y = kvq::fast_exp2(y);
-        pk[i / 2] = kvq::h2_as_u32(__floats2half2_rn(x, y));
-        sum[i / 2 & 1] = add2(sum[i / 2 & 1], pack64(x, y));
-      }
+    for (int i = 0; i < 32; i += 2) {
       float x, y;
-      unpack64(add2(sum[0], sum[1]), x, y);
-      l = fmaf(x + y, EDGE && window ? 1.f : meta.inv[c + h], l);
-      if (h == 0 || c == 0) wait_ld32(s[h ^ 1]);
-      // columns 16 .. behind the chunks already read
-      tmem_st16(s_at + 16 * (c + h), pk);
+      unpack64(fma2(pack64(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), a2, b2), x, y);
+      if (EDGE) {
+        const int col = 32 * c + i;
+        x = col < cmax ? x : ninf;
+        y = col + 1 < cmax ? y : ninf;
+      }
+      x = kvq::fast_exp2(x);
+      y = kvq::fast_exp2(y);
+      pk[i / 2] = kvq::h2_as_u32(__floats2half2_rn(x, y));
+      sum[i / 2 & 1] = add2(sum[i / 2 & 1], pack64(x, y));
     }
+    float x, y;
+    unpack64(add2(sum[0], sum[1]), x, y);
+    l = fmaf(x + y, EDGE && window ? 1.f : meta.inv[c], l);
+    tmem_st16(s_at + 32 * g + 16 * (c - g), pk);
   }
   return l;
 }
@@ -528,10 +520,10 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
   }
   if (tid == 0) {
     *dead = 0;
-    kvq::mbar_init(bars + kQFull, 256);
+    kvq::mbar_init(bars + kQFull, 512);
     for (int i = 0; i < kParts; ++i) {
       kvq::mbar_init(bars + kPartFull + i, 1);
-      kvq::mbar_init(bars + kPartFree + i, 10);  // eight softmax warps, the products, the tables
+      kvq::mbar_init(bars + kPartFree + i, 18);  // sixteen softmax warps, the products, the tables
     }
     for (int i = 0; i < kMetas; ++i) {
       kvq::mbar_init(bars + kMetaFull + i, 1);
@@ -544,12 +536,12 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       kvq::mbar_init(bars + kVFull + i, 128);
       kvq::mbar_init(bars + kVEmpty + i, 1);
       kvq::mbar_init(bars + kSFull + i, 1);
-      kvq::mbar_init(bars + kPFull + i, 128);
+      kvq::mbar_init(bars + kPFull + i, 256);
       kvq::mbar_init(bars + kOFull + i, 1);
     }
     kvq::fence_mbar_init();
   }
-  if (warp == 12) {
+  if (warp == 20) {
     tmem_alloc(kvq::smem_u32(tmem_slot));
     tmem_relinquish();
   }
@@ -586,10 +578,10 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
     return bar_all(id, threads, ok);
   };
 
-  if (warp >= 12) {
-    // 2 x 144 + 112 + 80 <= 4 x 128, what the CTA was launched with
-    regs_dec<80>();
-    if (warp == 12) {
+  if (warp >= 20) {
+    // 4 x 80 + 112 + 48 = 6 x 80, what the CTA was launched with
+    regs_dec<48>();
+    if (warp == 20) {
       // ================================================= the products
       // The whole warp goes through the loop, so that addresses and
       // descriptors are uniform, and one lane issues.  The loops over the
@@ -616,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           const uint32_t vd = desc_lo(base + SM::V + (unit & 1) * SM::TILE, SM::HALF);
 #pragma unroll 2
           for (int i = 0; i < kKeys / 16; ++i)
-            mma_ts(kO + t * 128, kS + t * 128 + i * 8, vd + i * (2048 >> 4), id_pv, add || i != 0);
+            mma_ts(kO + t * 128, kS + t * 128 + (i >> 2) * 64 + (i & 3) * 8, vd + i * (2048 >> 4), id_pv, add || i != 0);
           commit(base + SM::BAR + (kOFull + t) * 8);
         }
       };
@@ -662,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           if (more) free_stage(kKEmpty + ((n_unit + 1) & 1));
         }
       }
-    } else if (warp == 13 && lane == 0) {
+    } else if (warp == 21 && lane == 0) {
       // ================================================= the walk
       Walk use;
       use.p = pair_of_slot(a, static_cast<int>(found[0]));
@@ -701,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
         if (!more) break;
         more = use.next(a);
       }
-    } else if (warp == 14) {
+    } else if (warp == 22) {
       // ================================================= blocks and scales
       uint32_t n_unit = 0;
       bool ok = true;
@@ -770,9 +762,9 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
         }
       }
     }
-  } else if (warp >= 8) {
+  } else if (warp >= 16) {
     // =================================================== keys and values
-    regs_dec<112>();
+    regs_inc<112>();
     const int ct = tid & 127;
     // Four threads take 64 bytes of a token, a warp eight tokens: with the
     // swizzle, eight threads' 16-byte stores meet eight bank groups.
@@ -836,7 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       }
     };
 
-    const bool first = warp == 8;
+    const bool first = warp == 16;
     bool ok = true;
     int kind = kEnd;
     if (wait_all(kMetaFull, 0, first, 1, 128, true)) {
@@ -900,19 +892,24 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
     }
   } else {
     // =================================================== softmax
-    regs_inc<144>();
-    const int t = warp >> 2;         // row tile
+    const int t = warp >> 3;         // row tile
+    const int hf = warp >> 2 & 1;    // half of a unit's keys, of a row's channels, of the warp's rows
     const int r = tid & 127;         // row of the tile = lane of tensor memory
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
     const uint32_t s_at = lanes + kS + t * 128, o_at = lanes + kO + t * 128;
     uint32_t n_unit = 0;  // units so far
     uint32_t n_own = 0;   // units of this row tile so far
     // copies of whole rows: LPR lanes a row, RPI rows at a time, NQ times for the warp's 32
-    constexpr int LPR = D / 8, RPI = 32 / LPR, NQ = 32 / RPI;
+    // (two warps share the 32 rows)
+    constexpr int LPR = D / 8, RPI = 32 / LPR, NQ = 16 / RPI;
+    const int i0 = hf * NQ;
+    float *const maxima = reinterpret_cast<float *>(smem + SM::ROW) + t * 128 + r;  // [unit parity][half][kRows]
+    int *const exps = reinterpret_cast<int *>(smem + SM::ROW) + 4 * kRows + t * 128;
+    float *const sums = reinterpret_cast<float *>(smem + SM::ROW) + 4 * kRows + t * 128 + r;  // [half][kRows]
     bool ok = true;
     for (uint32_t n_part = 0;; ++n_part) {
-      // all eight warps go on together, or leave together
-      ok = wait_all(kPartFull + n_part % kParts, (n_part / kParts) & 1, warp == 0, 2, 256, ok);
+      // all sixteen warps go on together, or leave together
+      ok = wait_all(kPartFull + n_part % kParts, (n_part / kParts) & 1, warp == 0, 2, 512, ok);
       if (!ok) break;
       const Part &p = parts[n_part % kParts];
       const int u0 = p.u0, u1 = p.u1;
@@ -933,25 +930,27 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
         uint4 x[NQ];
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
-          const long long off = __shfl_sync(kAll, q_off, i * RPI + lane / LPR);
+          const long long off = __shfl_sync(kAll, q_off, (i0 + i) * RPI + lane / LPR);
           x[i] = make_uint4(0u, 0u, 0u, 0u);
           if (off >= 0) x[i] = *reinterpret_cast<const uint4 *>(a.q.p + off + lane % LPR * 8);
         }
-        int mine = 0;
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
+          const int at = 32 * (warp & 3) + (i0 + i) * RPI + lane / LPR;  // row of the tile
           if (BF16) {
             uint32_t big = mag_max8(x[i]);
 #pragma unroll
             for (int o = 1; o < LPR; o <<= 1) big = max(big, __shfl_xor_sync(kAll, big, o));
             const int e = big ? min(max(static_cast<int>(big >> 7), 20), 254) : 141;
             x[i] = bf16_row_to_fp16(x[i], __int_as_float((268 - e) << 23));
-            const int of_row = __shfl_sync(kAll, e, lane % RPI * LPR);
-            if (lane / RPI == i) mine = of_row;
+            if (lane % LPR == 0) exps[at] = e;
           }
-          sts16(dst + place(32 * (warp & 3) + i * RPI + lane / LPR, lane % LPR), x[i].x, x[i].y, x[i].z, x[i].w);
+          sts16(dst + place(at, lane % LPR), x[i].x, x[i].y, x[i].z, x[i].w);
         }
-        if (BF16) qf *= __int_as_float((mine - 14) << 23);
+        if (BF16) {
+          bar_sync(3 + t, 256);
+          qf *= __int_as_float((exps[r] - 14) << 23);
+        }
         kvq::fence_proxy_async();
       }
       fence_before();
@@ -962,7 +961,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
         // every row of the tile sees at least the tokens up to here
         const int seen_by_all = p.L - p.n + (p.row + t * 128) / a.group;
         for (int u = u0; u < u1; ++u, ++n_unit, ++n_own) {
-          ok = __all_sync(kAll, wait(kSFull + t, n_own & 1));
+          ok = wait_all(kSFull + t, n_own & 1, (warp & 7) == 0, 3 + t, 256, true);
           if (!ok) break;
           fence_after();
           const Meta &meta = metas[n_unit % kMetas];
@@ -975,7 +974,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           if (window) {
             // each token has its own scales: S becomes z + log2 scale_v in place
 #pragma unroll 1
-            for (int c = 0; c < kKeys; c += 16) {
+            for (int c = 64 * hf; c < 64 * hf + 64; c += 16) {
               uint32_t z[16];
               tmem_ld16(z, s_at + c);
               wait_ld16(z);
@@ -990,8 +989,12 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
             wait_st();
           }
           // ---- the maximum
-          const float mx = edge ? unit_max(std::true_type{}, s_at, meta, qf, window, cmax)
-                                : unit_max(std::false_type{}, s_at, meta, qf, window, cmax);
+          float mx = edge ? unit_max(std::true_type{}, s_at, 2 * hf, meta, qf, window, cmax)
+                          : unit_max(std::false_type{}, s_at, 2 * hf, meta, qf, window, cmax);
+          float *const both = maxima + (n_own & 1) * 2 * kRows;
+          both[hf * kRows] = mx;
+          bar_sync(3 + t, 256);
+          mx = fmaxf(mx, both[(hf ^ 1) * kRows]);
           // ---- the reference M, and O where it moved
           const bool move = mx > M + kGrow || (M == ninf && mx > ninf);
           if (__any_sync(kAll, move)) {
@@ -1000,11 +1003,11 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
             M = to;
             l *= f;
             if (u > u0) {
-              ok = __all_sync(kAll, wait(kOFull + t, (n_own - 1) & 1));
-              if (!ok) break;
+              // (given up here, the next wait for S gives up for the whole tile)
+              if (!__all_sync(kAll, wait(kOFull + t, (n_own - 1) & 1))) continue;
               fence_after();
 #pragma unroll 1
-              for (int c = 0; c < D / 16; ++c) {
+              for (int c = hf * (D / 32); c < (hf + 1) * (D / 32); ++c) {
                 uint32_t o[16];
                 tmem_ld16(o, o_at + 16 * c);
                 wait_ld16(o);
@@ -1017,7 +1020,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           const float ref = M == ninf ? 0.f : M - kShift;
           if (window) {
 #pragma unroll 1
-            for (int c = 0; c < kKeys; c += 16) {
+            for (int c = 64 * hf; c < 64 * hf + 64; c += 16) {
               uint32_t z[16];
               tmem_ld16(z, s_at + c);
               wait_ld16(z);
@@ -1027,8 +1030,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
             }
           }
           // ---- weights
-          const float sum = edge ? unit_weights(std::true_type{}, s_at, meta, qf, ref, window, cmax)
-                                 : unit_weights(std::false_type{}, s_at, meta, qf, ref, window, cmax);
+          const float sum = edge ? unit_weights(std::true_type{}, s_at, 2 * hf, meta, qf, ref, window, cmax)
+                                 : unit_weights(std::false_type{}, s_at, 2 * hf, meta, qf, ref, window, cmax);
           if (!window) l += sum;
           wait_st();
           fence_before();
@@ -1056,21 +1059,24 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
                 pack2<BF16>(o[8 * k + 6] * f, o[8 * k + 7] * f));
       };
       auto store_rows = [&]() {
-        __syncwarp();
+        bar_sync(3 + t, 256);
 #pragma unroll 4
         for (int i = 0; i < NQ; ++i) {
-          const long long off = __shfl_sync(kAll, out_off, i * RPI + lane / LPR);
-          const uint4 x = lds16(stage + place(32 * (warp & 3) + i * RPI + lane / LPR, lane % LPR));
+          const long long off = __shfl_sync(kAll, out_off, (i0 + i) * RPI + lane / LPR);
+          const uint4 x = lds16(stage + place(32 * (warp & 3) + (i0 + i) * RPI + lane / LPR, lane % LPR));
           if (off >= 0) *reinterpret_cast<uint4 *>(a.out.p + off + lane % LPR * 8) = x;
         }
-        __syncwarp();
       };
-      if (active && ok) ok = __all_sync(kAll, wait(kOFull + t, (n_own - 1) & 1));
+      if (active) {
+        sums[hf * kRows] = l;
+        ok = wait_all(kOFull + t, (n_own - 1) & 1, (warp & 7) == 0, 3 + t, 256, ok);
+        l += sums[(hf ^ 1) * kRows];
+      }
       if (active && ok) {
         fence_after();
         const float inv = 1.f / l;
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
+        for (int c = hf * (D / 64); c < (hf + 1) * (D / 64); ++c) {
           uint32_t o[32];
           tmem_ld32(o, o_at + 32 * c);
           wait_ld32(o);
@@ -1089,22 +1095,22 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
         }
         if (whole)
           store_rows();
-        else
+        else if (hf == 0)
           a.tile_ml[slot * kRows + t * 128 + r] = make_float2(M, l);
         fence_before();
       }
       if (!whole) {
         __threadfence();
-        ok = bar_all(2, 256, ok);
+        ok = bar_all(2, 512, ok);
         if (!ok) break;
         if (tid == 0) {
           const bool last = kvq::atom_add_acq_rel(a.tile_counters + p.c0, 1) == p.cuts;
           if (last) a.tile_counters[p.c0] = 0;
           *flag = last;
         }
-        bar_sync(2, 256);
+        bar_sync(2, 512);
         const bool merge = *flag;
-        bar_sync(2, 256);  // read before it is set again
+        bar_sync(2, 512);  // read before it is set again
         if (merge && active) {
           __threadfence();
           const int first = p.first, c0 = p.c0, n = p.cuts + 1;
@@ -1118,7 +1124,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           }
           const float inv = ll == 0.f ? 0.f : 1.f / ll;
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
+          for (int c = hf * (D / 64); c < (hf + 1) * (D / 64); ++c) {
             float o[32];
 #pragma unroll
             for (int k = 0; k < 32; ++k) o[k] = 0.f;
@@ -1151,7 +1157,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
   __syncwarp();
   fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 20) {
     fence_after();
     tmem_free(*tmem_slot);
   }
