@@ -129,20 +129,20 @@ def rope_table(rows: int, rot_dim: int, theta: float = 10000.0, device="cuda"):
     return torch.cat([ang.cos(), ang.sin()], 1).float()
 
 
-def _rows(t, cache, name):
-    """kv8_rows of a [rows][heads][D] tensor (any row and head strides)."""
-    if t.dtype != cache.dtype or t.dim() != 3 or t.get_device() != cache.device_index:
-        raise ValueError(f"{name}: a {cache.dtype} tensor [rows][heads][{cache.head_dim}] on {cache.device} is needed")
+def _rows(t, cache, shape, name):
+    """kv8_rows of a tensor of this shape, [rows][heads][D] (any row and head strides)."""
+    if t.dtype is not cache.dtype or t.shape != shape or t.get_device() != cache.device_index:
+        raise ValueError(f"{name}: a {cache.dtype} tensor of shape {tuple(shape)} on {cache.device} is needed")
     row, head, one = t.stride()
-    if (one != 1 and t.shape[0]) or t.shape[2] != cache.head_dim:  # no rows: any strides
-        raise ValueError(f"{name}: heads of {cache.head_dim} contiguous elements are needed")
+    if one != 1 and shape[0]:  # no rows: any strides
+        raise ValueError(f"{name}: the elements of a head must be contiguous")
     return _pack_rows(t.data_ptr(), row, head)
 
 
 def _row_start(row_start, cache):
     if row_start is None:
         return None
-    if row_start.dtype != torch.int32 or row_start.numel() != cache.num_seqs + 1 or not row_start.is_contiguous() \
+    if row_start.dtype is not torch.int32 or row_start.numel() != cache.num_seqs + 1 or not row_start.is_contiguous() \
             or row_start.get_device() != cache.device_index:
         raise ValueError(f"row_start: a contiguous int32 tensor [{cache.num_seqs + 1}] on {cache.device} is needed")
     return row_start.data_ptr()
@@ -154,7 +154,7 @@ def _launch(fn, what, cache, stream, *args):
     if index < 0:
         raise ValueError("the cache is not on a CUDA device")
     raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         code = fn(*args, raw)
     else:
         with torch.cuda.device(index):
@@ -168,28 +168,28 @@ def kv8_append(cache: KV8Cache, k, v, row_start=None, max_new: int = 1, q=None, 
     """k, v: [rows][Hkv][D]; q, q_out: [rows][Hq][D] (rotated along; q_out may
     be q); rope: fp32 [positions][rot_dim] (rope_table) or None.  row_start:
     int32 [S + 1], or None for one row per sequence."""
-    H = cache.num_kv_heads
-    if k.shape != v.shape or k.shape[1] != H:
-        raise ValueError(f"k and v: [rows][{H}][{cache.head_dim}]")
-    ks, vs = _rows(k, cache, "k"), _rows(v, cache, "v")
+    rows, dim = len(k), cache.head_dim
+    shape = (rows, cache.num_kv_heads, dim)
+    ks, vs = _rows(k, cache, shape, "k"), _rows(v, cache, shape, "v")
     qs = os = None
     heads = 0
     if q is not None:
-        if q_out is None or q_out.shape != q.shape or q.shape[0] != k.shape[0]:
-            raise ValueError("q_out: the shape of q, and the rows of k, are needed")
-        heads = q.shape[1]
-        qs, os = _rows(q, cache, "q"), _rows(q_out, cache, "q_out")
+        if q_out is None:
+            raise ValueError("q without q_out")
+        heads = q.size(1) if q.dim() == 3 else 0
+        shape = (rows, heads, dim)
+        qs, os = _rows(q, cache, shape, "q"), _rows(q_out, cache, shape, "q_out")
     elif q_out is not None:
         raise ValueError("q_out without q")
     table, rot, positions = None, 0, 0
     if rope is not None:
-        if rope.dtype != torch.float32 or rope.dim() != 2 or not rope.is_contiguous() \
+        if rope.dtype is not torch.float32 or rope.dim() != 2 or not rope.is_contiguous() \
                 or rope.get_device() != cache.device_index:
             raise ValueError(f"rope: a contiguous float32 tensor [positions][rot_dim] on {cache.device} is needed")
         positions, rot = rope.shape
         table = rope.data_ptr() if rot else None
     _launch(lib.kv8_append, "kv8_append", cache, stream, cache.ref, ks, vs, qs, os, heads,
-            _row_start(row_start, cache), k.shape[0], max_new, table, positions, rot, 1 if interleaved else 0)
+            _row_start(row_start, cache), rows, max_new, table, positions, rot, 1 if interleaved else 0)
 
 
 def attn_workspace_bytes(cache: KV8Cache, num_q_heads: int, max_new: int = 1) -> int:
@@ -207,10 +207,12 @@ def alloc_workspace(cache: KV8Cache, num_q_heads: int, max_new: int = 1):
 def kv8_attn(cache: KV8Cache, q, out, workspace, max_len: int, row_start=None, max_new: int = 1,
              softmax_scale: float = 0.0, stream=None):
     """q, out: [rows][Hq][D] (out may be q); max_len: a bound on seq_len."""
-    if q.shape != out.shape:
-        raise ValueError("q and out differ in shape")
+    if q.dim() != 3:
+        raise ValueError("q: [rows][heads][D] is needed")
+    rows, heads, _ = q.shape
+    shape = (rows, heads, cache.head_dim)
     if workspace.get_device() != cache.device_index or not workspace.is_contiguous():
         raise ValueError(f"workspace: a contiguous tensor on {cache.device} is needed")
-    _launch(lib.kv8_attn, "kv8_attn", cache, stream, cache.ref, q.shape[1], _rows(q, cache, "q"),
-            _rows(out, cache, "out"), _row_start(row_start, cache), q.shape[0], max_new, softmax_scale,
+    _launch(lib.kv8_attn, "kv8_attn", cache, stream, cache.ref, heads, _rows(q, cache, shape, "q"),
+            _rows(out, cache, shape, "out"), _row_start(row_start, cache), rows, max_new, softmax_scale,
             workspace.data_ptr(), workspace.numel() * workspace.element_size(), max_len)
