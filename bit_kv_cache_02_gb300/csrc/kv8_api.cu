@@ -17,6 +17,7 @@ int check_geometry(const kv8_cache *c) {
   if (c->format != KV8_INT8 && c->format != KV8_E4M3) return KVQ_ERR_UNSUPPORTED;
   if (c->dtype != KV8_F16 && c->dtype != KV8_BF16) return KVQ_ERR_UNSUPPORTED;
   if (c->num_seqs > 65535 || c->num_kv_heads > 65535) return KVQ_ERR_UNSUPPORTED;
+  if (c->capacity > KV8_MAX_CAPACITY) return KVQ_ERR_UNSUPPORTED;  // positions are counted in 32 bits
   // (sequence, KV head) pairs are counted in 32 bits
   if (static_cast<int64_t>(c->num_seqs) * c->num_kv_heads > 2147483647LL / 2) return KVQ_ERR_UNSUPPORTED;
   return KVQ_OK;

@@ -50,13 +50,13 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr int kWarps = 4;
 constexpr int kUnit = 32;     // tokens of a unit of quantized blocks
 constexpr int kWinUnit = 16;  // tokens of a unit of the window
-#ifndef KV8_ROWS_SLOTS
-#define KV8_ROWS_SLOTS 2
-#endif
+// Ring slots of a warp for D 128 (twice as many of half the size for D 64).
+// Three or four cost resident CTAs and were slower.
+constexpr int kSlots = 2;
 
 template <int D, int HALVES>
 struct Smem {
-  static constexpr int SLOTS = D == 128 ? KV8_ROWS_SLOTS : 2 * KV8_ROWS_SLOTS;
+  static constexpr int SLOTS = D == 128 ? kSlots : 2 * kSlots;
   static constexpr int HALF = kUnit * D;   // bytes of a unit's keys (and of its values)
   static constexpr int SLOT = 2 * HALF;    // a window unit has the same size
   static constexpr int NT = D / 8;         // n-tiles of the output
@@ -268,9 +268,8 @@ struct Walk {
 template <int D, int FMT, bool BF16, int HALVES>
 __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
   using SM = Smem<D, HALVES>;
-  constexpr int NT = SM::NT;      // output n-tiles
-  constexpr int KS = D / 16;      // k-steps of the scores
-  constexpr int REGS = 2 * HALVES;  // accumulator registers in use per n-tile
+  constexpr int NT = SM::NT;  // output n-tiles
+  constexpr int KS = D / 16;  // k-steps of the scores
   extern __shared__ __align__(128) unsigned char smem[];
   const Geo &geo = a.geo;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q4 = lane & 3;
@@ -572,9 +571,8 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
           }
           const float inf = __int_as_float(0x7f800000);
           // scales that are not finite make the rows that see the block NaN;
-          // values of magnitude 2^-100 or less (their scale's floor) count as
-          // zeros, of any scale
-          const bool bad = !(fabsf(sc2.x) < inf && fabsf(sc2.y) < inf), none = sc2.y < 8.8e-33f;
+          // zeros may have any scale
+          const bool bad = !(fabsf(sc2.x) < inf && fabsf(sc2.y) < inf), none = sc2.y < kZeroScale;
           const float ks = bad ? 1.f : sc2.x, vs = bad || none ? 1.f : sc2.y, lv = __log2f(vs);
           float ka[2], kb[2];
 #pragma unroll
@@ -740,12 +738,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
         float2 o[QT];
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
-          float x[2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float raw = acc[j][r + 2 * i];
-            x[i] = f * (raw * kUnshift);
-          }
+          const float x[2] = {f * (acc[j][r] * kUnshift), f * (acc[j][r + 2] * kUnshift)};
           const int dst = j / QT;
           if (dst != warp) {
             float *b = xch + ((dst * 3 + ((warp - dst - 1) & 3)) * QT + j % QT) * 64 + lane;
@@ -793,7 +786,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int row = r0 + g + 8 * r;
-        const bool valid = (r == 0 || HALVES == 2) && row < n_rows;
+        const bool valid = row < n_rows;
         const int tok = valid ? row / a.group : 0;
         lim[r] = valid ? w.q.L - w.q.n + tok : -1;
         const uint16_t *src = a.q.p + (static_cast<long long>(w.q.row0) + tok) * a.q.row +
@@ -825,7 +818,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
             qa[k][r + 2] = bf16_to_fp16(qa[k][r + 2], f.x);
           }
         }
-        if (FMT == KV8_INT8 && r < HALVES) {
+        if (FMT == KV8_INT8) {
           float sum = 0.f;
 #pragma unroll
           for (int k = 0; k < KS; ++k) {
@@ -856,12 +849,12 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
 #pragma unroll
         for (int t = 0; t < NB; ++t)
 #pragma unroll
-          for (int i = 0; i < REGS; ++i) sc[t][i] = fmaf(sc[t][i], ka[i >> 1], kb[i >> 1]);
+          for (int i = 0; i < 4; ++i) sc[t][i] = fmaf(sc[t][i], ka[i >> 1], kb[i >> 1]);
         if (window || bad || t0 + 8 * NB - 1 > seen_by_all) {
 #pragma unroll
           for (int t = 0; t < NB; ++t)
 #pragma unroll
-            for (int i = 0; i < REGS; ++i) {
+            for (int i = 0; i < 4; ++i) {
               const int col = 8 * t + ((i & 1) ? ((2 * q4 + 1) ^ 4) : 2 * q4);
               float z = sc[t][i];
               if (window) z += z - z;  // an infinite score becomes NaN
@@ -872,17 +865,15 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
 #pragma unroll
         for (int t = 0; t < NB; ++t)
 #pragma unroll
-          for (int i = 0; i < REGS; i += 2) mx[i >> 1] = fmaxf(fmaxf(mx[i >> 1], sc[t][i]), sc[t][i + 1]);
+          for (int i = 0; i < 4; i += 2) mx[i >> 1] = fmaxf(fmaxf(mx[i >> 1], sc[t][i]), sc[t][i + 1]);
 #pragma unroll
-        for (int r = 0; r < HALVES; ++r) {
+        for (int r = 0; r < 2; ++r) {
           mx[r] = fmaxf(mx[r], __shfl_xor_sync(kAll, mx[r], 1));
           mx[r] = fmaxf(mx[r], __shfl_xor_sync(kAll, mx[r], 2));
         }
-        bool moved = mx[0] != m[0];
-        if (HALVES == 2) moved |= mx[1] != m[1];
-        if (__any_sync(kAll, moved)) {
+        if (__any_sync(kAll, mx[0] != m[0] || mx[1] != m[1])) {
 #pragma unroll
-          for (int r = 0; r < HALVES; ++r) {
+          for (int r = 0; r < 2; ++r) {
             const float f = mx[r] == m[r] ? 1.f : kvq::fast_exp2(m[r] - mx[r]);  // -inf before the first token
             m[r] = mx[r];
             l[r] *= f;
@@ -895,7 +886,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
         }
         float sum[2] = {0.f, 0.f};
 #pragma unroll
-        for (int r = 0; r < HALVES; ++r) {
+        for (int r = 0; r < 2; ++r) {
           const float ms = m[r] == ninf ? 0.f : m[r] - kShift;
 #pragma unroll
           for (int t = 0; t < NB; ++t) {
@@ -905,9 +896,6 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
           }
           l[r] = fmaf(sum[r], inv, l[r]);
         }
-        if (HALVES == 1)
-#pragma unroll
-          for (int t = 0; t < NB; ++t) sc[t][2] = sc[t][3] = 0.f;
       };
       // the weights of n-tiles 2 k, 2 k + 1 as the A operand of k-step k
       auto weights = [&](uint32_t (&p)[4], const float *lo, const float *hi) {
@@ -945,9 +933,8 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
           }
           const float inf = __int_as_float(0x7f800000);
           // scales that are not finite make the rows that see the block NaN;
-          // values of magnitude 2^-100 or less (their scale's floor) count as
-          // zeros, of any scale
-          const bool bad = !(fabsf(sc2.x) < inf && fabsf(sc2.y) < inf), none = sc2.y < 8.8e-33f;
+          // zeros may have any scale
+          const bool bad = !(fabsf(sc2.x) < inf && fabsf(sc2.y) < inf), none = sc2.y < kZeroScale;
           const float ks = bad ? 1.f : sc2.x, vs = bad || none ? 1.f : sc2.y, lv = __log2f(vs);
           float ka[2], kb[2];
 #pragma unroll
@@ -1090,7 +1077,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
                 mma(o, p, b0, b1);
               }
 #pragma unroll
-              for (int r = 0; r < REGS; ++r) acc[2 * k + c][r] = fmaf(o[r], kWin, acc[2 * k + c][r]);
+              for (int r = 0; r < 4; ++r) acc[2 * k + c][r] = fmaf(o[r], kWin, acc[2 * k + c][r]);
             }
           }
         }
@@ -1104,7 +1091,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
       float2 *ml = reinterpret_cast<float2 *>(smem + SM::ML);
       float *xch = reinterpret_cast<float *>(smem + SM::XCH);
 #pragma unroll
-      for (int r = 0; r < HALVES; ++r) {
+      for (int r = 0; r < 2; ++r) {
         l[r] += __shfl_xor_sync(kAll, l[r], 1);
         l[r] += __shfl_xor_sync(kAll, l[r], 2);
         l[r] *= kUnshift;
@@ -1120,7 +1107,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
       const int part = 2 * blockIdx.x + (use.start + use.u0 == lo ? 0 : 1);
       constexpr int QT = NT / 4;
 #pragma unroll
-      for (int r = 0; r < HALVES; ++r) {
+      for (int r = 0; r < 2; ++r) {
         float mm = ninf, ll = 0.f;
 #pragma unroll
         for (int i = 0; i < kWarps; ++i) mm = fmaxf(mm, ml[i * kRowTile + g + 8 * r].x);
@@ -1186,7 +1173,6 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
           }
         }
       }
-
     }
 
     if (!whole) {

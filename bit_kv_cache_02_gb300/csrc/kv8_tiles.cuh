@@ -109,7 +109,7 @@ constexpr uint32_t kS = 0, kO = 256;  // two tiles of 128 columns each
 enum Bar {
   kQFull, kKFull, kKEmpty = kKFull + 2, kVFull = kKEmpty + 2, kVEmpty = kVFull + 2, kSFull = kVEmpty + 2,
   kPFull = kSFull + 2, kOFull = kPFull + 2, kPartFull = kOFull + 2, kPartFree = kPartFull + kParts,
-  kMetaFull = kPartFree + kParts, kMetaFree = kMetaFull + kMetas, kBars = kMetaFree + kMetas
+  kMetaFull = kPartFree + kParts, kMetaFree = kMetaFull + kMetas, kDrained = kMetaFree + kMetas, kBars
 };
 static_assert(kBars <= 48, "barriers");
 
@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + SM::MISC + 8);
   int *flag = reinterpret_cast<int *>(smem + SM::MISC + 16);
   long long *found = reinterpret_cast<long long *>(smem + SM::MISC + 32);       // [2]
-  long long *scan_buf = reinterpret_cast<long long *>(smem + SM::MISC + 64);    // [16]
+  long long *scan_buf = reinterpret_cast<long long *>(smem + SM::MISC + 64);    // [kThreads / 32]
   const Geo &geo = a.geo;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int B = geo.B, H = geo.H;
@@ -521,6 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
   if (tid == 0) {
     *dead = 0;
     kvq::mbar_init(bars + kQFull, 512);
+    kvq::mbar_init(bars + kDrained, 1);
     for (int i = 0; i < kParts; ++i) {
       kvq::mbar_init(bars + kPartFull + i, 1);
       kvq::mbar_init(bars + kPartFree + i, 18);  // sixteen softmax warps, the products, the tables
@@ -654,6 +655,11 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           if (more) free_stage(kKEmpty + ((n_unit + 1) & 1));
         }
       }
+      if (!ok) {  // a wait ran out: no product may be left when tensor memory is given back
+        if (leader) commit(base + SM::BAR + kDrained * 8);
+        for (int i = 0; i < 100000 && !kvq::mbar_try_wait(bars + kDrained, 0); ++i) {
+        }
+      }
     } else if (warp == 21 && lane == 0) {
       // ================================================= the walk
       Walk use;
@@ -730,8 +736,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           }
           const float inf = __int_as_float(0x7f800000);
           const bool bad = !(fabsf(sc.x) < inf && fabsf(sc.y) < inf);
-          // values of magnitude 2^-100 or less (the scale's floor): zeros, of any scale
-          const bool flush = !bad && sc.y < 8.8e-33f;
+          // zeros may have any scale
+          const bool flush = !bad && sc.y < kZeroScale;
           const unsigned flushes = __ballot_sync(kAll, flush);
           const float lv = bad ? nan : flush ? 0.f : log2f(sc.y), inv = bad || flush ? 1.f : 1.f / sc.y;
           for (int i = 0; i < 8 && u + i < p.u1; ++i) {
@@ -815,8 +821,9 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           big = max(big, hi16 < nonfinite_bits<BF16>() ? hi16 : 0u);
         }
       }
-      // a power of two that brings the largest element to [2^14, 2^15)
-      if (BF16 && big) f = __int_as_float((268 - max(static_cast<int>(big >> 7), 20)) << 23);
+      // a power of two that brings the largest element to [2^14, 2^15); elements
+      // below 2^-67 count as that, so that sums of f times weights stay finite
+      if (BF16 && big) f = __int_as_float((268 - max(static_cast<int>(big >> 7), 60)) << 23);
     };
     auto store_window = [&](uint32_t dst, const uint16_t *src, bool zero, float f) {
 #pragma unroll 4

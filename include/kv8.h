@@ -43,6 +43,8 @@ extern "C" {
 #define KV8_F16  0  /* IEEE binary16 */
 #define KV8_BF16 1  /* bfloat16 */
 
+#define KV8_MAX_CAPACITY (1 << 30)
+
 /* which buffer for kv8_buffer_bytes() */
 #define KV8_BUF_CODES       0
 #define KV8_BUF_SCALES      1
@@ -85,7 +87,7 @@ typedef struct kv8_cache {
   int32_t  block;         /* tokens per block: 32, 64 or 128     */
   int32_t  format;        /* KV8_INT8 or KV8_E4M3                */
   int32_t  dtype;         /* KV8_F16 or KV8_BF16: 16-bit tensors */
-  int32_t  capacity;      /* max tokens per sequence, >= 1       */
+  int32_t  capacity;      /* max tokens, 1 .. KV8_MAX_CAPACITY   */
   int32_t  num_blocks;    /* pool size, >= 1 when capacity >= block */
   uint8_t  *codes;
   float    *scales;
@@ -150,7 +152,9 @@ int64_t kv8_buffer_bytes(const kv8_cache *cache, int32_t which);
  * A sequence whose row range is not within [0, rows], longer than max_new or
  * than seq_len[s], or whose seq_len[s] exceeds the capacity, is left alone
  * (its rows of q_out too) and sets KVQ_STATUS_BAD_LEN or
- * KVQ_STATUS_CAPACITY.  One kernel.
+ * KVQ_STATUS_CAPACITY.  row_start must not decrease: where it does,
+ * KVQ_STATUS_BAD_LEN is set and other sequences may be left alone too.  One
+ * kernel.
  */
 int kv8_append(const kv8_cache *cache, const kv8_rows *k, const kv8_rows *v,
                const kv8_rows *q, const kv8_rows *q_out, int32_t num_q_heads,
@@ -161,6 +165,10 @@ int kv8_append(const kv8_cache *cache, const kv8_rows *k, const kv8_rows *v,
 /*
  * kv8_attn_workspace_bytes -- scratch size for kv8_attn calls with at most
  * max_new rows per sequence (a multiple of 256); -1 on invalid arguments.
+ * About 10 MiB for D = 128, and 50 MiB where max_new * Hq / Hkv > 48: there a
+ * second kernel, on the tcgen05 tensor cores, takes the sequences with more
+ * than 48 rows per KV head.  A size that serves a larger max_new serves a
+ * smaller one.
  */
 int64_t kv8_attn_workspace_bytes(const kv8_cache *cache, int32_t num_q_heads,
                                  int32_t max_new);
@@ -174,17 +182,23 @@ int64_t kv8_attn_workspace_bytes(const kv8_cache *cache, int32_t num_q_heads,
  *   softmax_scale  multiplier of q.k; <= 0 selects 1/sqrt(D).
  *   workspace  at least kv8_attn_workspace_bytes() bytes, 256-byte aligned,
  *              zero-filled before its first use; every call leaves its
- *              counters zero again.
+ *              counters zero again (zero it after KVQ_STATUS_TIMEOUT, which
+ *              a call that gave up sets, its rows being undefined).
  *   max_len    host bound on every seq_len, 1 .. capacity.
  *
  * Row i of the n rows of sequence s sits at position seq_len[s] - n + i and
  * sees the tokens up to its own position; a row at a negative position sees
  * none and gets zeros.  A sequence with seq_len[s] < 0 or above max_len gets
  * zero rows and sets KVQ_STATUS_MAX_LEN; one whose row range is invalid is
- * left alone and sets KVQ_STATUS_BAD_LEN.  Rows that belong to no sequence
- * are left as they are.  A token with a NaN or an infinity in its keys or
- * values makes the rows that see it NaN (through a whole block once the
- * block is quantized), and no other row.
+ * left alone and sets KVQ_STATUS_BAD_LEN, and so may others be where row_start
+ * decreases.  Rows that belong to no sequence are left as they are.  A token
+ * with a NaN or an infinity in its keys or values makes the rows that see it
+ * NaN (through a whole block once the block is quantized), and no other row.
+ * A block of values whose scale is below 2^-80 counts as zeros, and in bf16
+ * results may overflow where a window token's keys or values are above 2^100 in
+ * magnitude.  Results do not depend on timing: the same call gives the same
+ * bits.  One or two kernels, which read all lengths on the device: a captured
+ * call can be replayed for other lengths within max_len, rows and max_new.
  */
 int kv8_attn(const kv8_cache *cache, int32_t num_q_heads, const kv8_rows *q,
              const kv8_rows *out, const int32_t *row_start, int32_t rows,

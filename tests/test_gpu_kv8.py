@@ -39,13 +39,15 @@ def _host(t):
 class Run:
     """A cache, its oracle and the calls of one test."""
 
-    def __init__(self, kv8, S, H, g, D, B, fmt, dtype, capacity, seed=0, rot=None, interleaved=False, amp=1.0):
+    def __init__(self, kv8, S, H, g, D, B, fmt, dtype, capacity, seed=0, rot=None, interleaved=False, amp=1.0,
+                 spare=3):
         self.kv8, self.S, self.H, self.g, self.D, self.B, self.dtype = kv8, S, H, g, D, B, dtype
         self.rng = np.random.default_rng(seed)
         maxb = capacity // B
-        self.cache = kv8.KV8Cache(S, H, capacity, max(1, S * maxb + 3), head_dim=D, block=B, fmt=fmt,
+        # `spare` blocks stay unused; when there are many of them, the first
+        self.cache = kv8.KV8Cache(S, H, capacity, max(1, S * maxb + spare), head_dim=D, block=B, fmt=fmt,
                                   dtype=getattr(torch, dtype))
-        perm = self.rng.permutation(S * maxb + 3)[: S * maxb].reshape(S, maxb)
+        perm = self.rng.permutation(S * maxb + 3)[: S * maxb].reshape(S, maxb) + spare - 3
         self.cache.block_table.copy_(torch.from_numpy(perm.astype(np.int32)))
         # what no token has been written to must not matter
         self.cache.k_win.fill_(math.nan)
@@ -449,7 +451,141 @@ def test_shared_blocks(kv8):
     assert x.shape[0] == 64
 
 
+@pytest.mark.parametrize("H,g", [(1, 49), (2, 72), (1, 300)])
+def test_token_many_query_heads(kv8, H, g):
+    """Query groups so large that a single token's rows take the other kernel."""
+    r = Run(kv8, 3, H, g, 128, 64, "int8", "float16", 400, seed=g)
+    r.append([1, 150, 390])
+    r.append([1, 1, 1], implicit=True)
+    r.attend(implicit=True)
+    r.attend()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_tiny_values(kv8, fmt):
+    """bf16 values near 2^-100, in blocks before normal ones and in the window:
+    the normalizer, which divides by their scale, stays finite.  A block whose
+    scale is below 2^-80 counts as zeros: its values are below 448 * 2^-80, and
+    so is what the weighted sum loses."""
+    def change(q, k, v):
+        v[:640] = 2.0 ** -99 * np.sign(v[:640])
+        v[704:708] = 2.0 ** -110
+
+    for lead in (640, 704, 720):
+        r = Run(kv8, 1, 1, 2, 128, 32, fmt, "bfloat16", 800, rot=0)
+        r.append([lead], change)
+        r.append([3])
+        want, bound = r.orc.attention(r.q, r.start_host)
+        r.close(_host(r.attend(check=False)), want, bound + 448 * 2.0 ** -80)
+        r.append([40])  # rows enough for the other kernel
+        want, bound = r.orc.attention(r.q, r.start_host)
+        r.close(_host(r.attend(check=False)), want, bound + 448 * 2.0 ** -80)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_long_context_precision(kv8, fmt):
+    """Over a long context of independent values the sums nearly cancel, and the
+    elements' bound says little.  Each weight is off by at most 2^-11 of itself,
+    independently, so the error's 2-norm is at most 2^-11 of the output's; the
+    output's own rounding adds 2^-11 of each element: together 2^(1/2) 2^-11,
+    and 2^-10 leaves a factor of 2^(1/2) for chance and the fp32 sums."""
+    r = Run(kv8, 1, 1, 4, 128, 64, fmt, "float16", 20000, seed=2, rot=0)
+    r.append([19800])
+    for new in (1, 3, 40):  # few rows, more rows, the other kernel
+        r.append([new])
+        want, _ = r.orc.attention(r.q, r.start_host)
+        got = _host(r.attend(check=False))
+        err = np.linalg.norm(got - want) / np.linalg.norm(want)
+        assert err <= 2.0 ** -10, f"{new} tokens: {err:.2e}"
+
+
+def test_pool_past_four_gigabytes(kv8):
+    """Offsets into the pool need more than 32 bits: 16,500 unused blocks of 256
+    KiB come first."""
+    r = Run(kv8, 2, 8, 2, 128, 128, "int8", "float16", 600, spare=16500)
+    assert r.cache.codes.numel() > 2 ** 32
+    r.append([500, 130])
+    r.attend()
+    r.append([1, 1])
+    r.attend()
+    r.append([3, 30])
+    r.attend()
+
+
+def test_rows_before_the_first_sequence(kv8):
+    """row_start may begin behind row 0; rows of no sequence stay as they are."""
+    B, pad = 32, 70
+    for new in ([1, 1], [3, 9], [100, 40]):
+        r = Run(kv8, 2, 2, 3, 128, B, "e4m3", "float16", 300)
+        r.append([45, 0])
+        start = np.concatenate([[0], np.cumsum(new)])
+        x = r.numbers((start[-1] + 2 * pad, 10, 128))
+        t = _dev(x, r.dtype)
+        q_out = torch.full((len(x), 6, 128), 5.0, dtype=t.dtype, device="cuda")
+        out = q_out.clone()
+        rs = torch.from_numpy((start + pad).astype(np.int32)).cuda()
+        r.cache.seq_len += torch.tensor(new, dtype=torch.int32, device="cuda")
+        kv8.kv8_append(r.cache, t[:, 6:8], t[:, 8:], row_start=rs, max_new=max(new), q=t[:, :6], q_out=q_out, rope=r.rope)
+        mid = slice(pad, pad + start[-1])
+        r.q = r.orc.append(x[mid, 6:8], x[mid, 8:], start, r.table, False, x[mid, :6])
+        r.q_out = q_out[mid]
+        r.check_state()
+        kv8.kv8_attn(r.cache, q_out, out, kv8.alloc_workspace(r.cache, 6, max(new)), 300, row_start=rs, max_new=max(new))
+        r.close(_host(out[mid]), *r.orc.attention(r.q, start))
+        for y in (q_out, out):
+            assert (y[:pad] == 5.0).all() and (y[pad + start[-1]:] == 5.0).all()
+
+
+def test_output_in_place(kv8):
+    """out may be q: single tokens, parts of a long line, items cut by CTAs."""
+    for ctx, new in (([300, 5], [1, 1]), ([5000, 3], [2, 4]), ([5000, 200], [90, 30])):
+        r = Run(kv8, 2, 2, 2, 128, 64, "int8", "bfloat16", 6000, rot=0)
+        r.append(ctx)
+        r.append(new)
+        want = r.attend()
+        q = r.q_out.clone()
+        kv8.kv8_attn(r.cache, q, q, kv8.alloc_workspace(r.cache, 4, max(new)), max(r.orc.lengths()), row_start=r.start,
+                     max_new=max(new))
+        assert torch.equal(q, want)
+
+
+def test_falling_row_start(kv8):
+    """Row ranges that go back set the status; nothing outside the tensors is
+    touched and rows of no sequence stay as they are."""
+    r = Run(kv8, 3, 1, 1, 64, 32, "int8", "float16", 200, rot=0)
+    x = _dev(r.numbers((200, 1, 64)), r.dtype)
+    r.cache.seq_len.fill_(150)
+    rs = torch.tensor([0, 150, 90, 150], dtype=torch.int32, device="cuda")
+    out = torch.full_like(x, 5.0)
+    kv8.kv8_append(r.cache, x, x, row_start=rs, max_new=150, q=x, q_out=out)
+    assert int(r.cache.status.item()) == 2
+    assert (out[150:] == 5.0).all()
+    r.cache.status.zero_()
+    kv8.kv8_attn(r.cache, x, out, kv8.alloc_workspace(r.cache, 1, 150), 150, row_start=rs, max_new=150)
+    assert int(r.cache.status.item()) & 2
+    assert (out[150:] == 5.0).all()
+
+
 # -------------------------------------------------------- streams and graphs
+
+def test_two_streams_at_once(kv8):
+    """Two caches with workspaces of their own on two streams: the same results
+    as one after the other."""
+    runs = []
+    for i, (D, new) in enumerate(((128, [300, 80]), (64, [90, 1]))):
+        r = Run(kv8, 2, 2, 2, D, 32, "int8", "float16", 1000, seed=i)
+        r.append([400, 100])
+        r.append(new)
+        q, ws = r.q_out.clone(), kv8.alloc_workspace(r.cache, 4, max(new))
+        runs.append((r, q, ws, max(new), r.attend(), torch.zeros_like(q), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for r, q, ws, new, _, out, stream in runs:
+            kv8.kv8_attn(r.cache, q, out, ws, max(r.orc.lengths()), row_start=r.start, max_new=new, stream=stream)
+    torch.cuda.synchronize()
+    for r, _, _, _, want, out, _ in runs:
+        assert torch.equal(out, want) and int(r.cache.status.item()) == 0
+
 
 def test_other_stream_and_graph(kv8):
     """A step captured on its own stream and replayed, each replay a new step:

@@ -167,6 +167,7 @@ def _attn(kv8, st, **kw):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(num_seqs=0), -1), (dict(num_kv_heads=0), -1), (dict(capacity=0), -1), (dict(num_blocks=-1), -1),
+    (dict(capacity=(1 << 30) + 1), -2),
     (dict(head_dim=96), -2), (dict(block=16), -2), (dict(block=100), -2), (dict(format=2), -2), (dict(dtype=2), -2),
     (dict(num_seqs=65536), -2), (dict(num_seqs=65535, num_kv_heads=65535), -2),
     (dict(codes=0), -1), (dict(scales=0), -1), (dict(k_win=0), -1), (dict(v_win=0), -1), (dict(seq_len=0), -1),
