@@ -195,6 +195,12 @@ template <int D, int FMT, bool BF16, int T, int NI>
 __global__ void __launch_bounds__(T, NI == 4 ? 3 : 1024 / T) append_kernel(const AppendArgs a) {
   constexpr int PAIRS = D / 16;
   if (static_cast<int>(blockIdx.x) >= a.kv_tasks) {
+    if (a.slots && blockIdx.x == gridDim.x - 1) {
+      // a sequence whose row range is invalid may own no slot
+      for (int j = threadIdx.x; j < a.geo.S; j += T)
+        if (!load_seq(a.geo, a.row_start, a.rows, a.max_new, j).ok) set_status(a.geo.status, KVQ_STATUS_BAD_LEN);
+      return;
+    }
     rotate_queries<D, BF16, T>(a, blockIdx.x - a.kv_tasks);
     return;
   }
@@ -204,11 +210,6 @@ __global__ void __launch_bounds__(T, NI == 4 ? 3 : 1024 / T) append_kernel(const
   if (a.split) {
     which = task & 1;
     task >>= 1;
-  }
-  if (a.slots && blockIdx.x == 0) {
-    // a sequence whose row range is invalid may own no slot
-    for (int j = tid; j < geo.S; j += T)
-      if (!load_seq(geo, a.row_start, a.rows, a.max_new, j).ok) set_status(geo.status, KVQ_STATUS_BAD_LEN);
   }
   const int h0 = task % a.head_groups * a.heads, h1 = min(h0 + a.heads, geo.H);
   int s = task / a.head_groups, t = 0;
@@ -366,7 +367,8 @@ cudaError_t launch_append(const Geo &geo, const Rows &k, const Rows &v, const Ro
   // eight threads share a query row's chunk pair, fewer where there are fewer heads
   a.lanes = Hq >= 8 ? 3 : Hq >= 4 ? 2 : Hq >= 2 ? 1 : 0;
   const int per = (min(geo.B * geo.D / 16, 256) / (geo.D / 16)) >> a.lanes;  // query rows of a CTA, see launch_ni
-  const long long grid = tasks + (Hq ? (static_cast<long long>(rows) + per - 1) / per : 0);
+  // and one CTA checks the row ranges where there are slots
+  const long long grid = tasks + (Hq ? (static_cast<long long>(rows) + per - 1) / per : 0) + (a.slots ? 1 : 0);
   if (grid > 2147483647LL) return cudaErrorInvalidConfiguration;
   a.kv_tasks = static_cast<int>(tasks);
   ++*launches;

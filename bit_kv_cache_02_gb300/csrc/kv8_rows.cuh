@@ -62,8 +62,9 @@ struct Smem {
   static constexpr int NT = D / 8;         // n-tiles of the output
   static constexpr int META = kWarps * SLOTS * SLOT;                 // scales of each slot: float2
   static constexpr int ML = META + kWarps * SLOTS * 8;               // [kWarps][16] float2
-  static constexpr int XCH = (ML + kWarps * kRowTile * 8 + 15) / 16 * 16;  // merge buffer
-  static constexpr int FLAG = XCH + kWarps * 3 * (NT / 4) * HALVES * 32 * 4;
+  static constexpr int XCH = (ML + kWarps * kRowTile * 8 + 15) / 16 * 16;  // merge buffer; before that, sixteen rows' queries
+  static_assert(HALVES == 1 || kWarps * 3 * (NT / 4) * 32 * 4 >= D / 16 * 512, "queries");
+  static constexpr int FLAG = XCH + kWarps * 3 * (NT / 4) * 32 * 4;
   static constexpr int BYTES = FLAG + 16;
 };
 
@@ -830,6 +831,22 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
           q128[r] = 128.f * sum;
         }
       }
+      // They wait in shared memory, alike for all warps: in registers they cost
+      // spills (16 sequences with 3 to 8 drafts: 47 us instead of 50).
+      const uint32_t qs = kvq::smem_u32(smem) + SM::XCH + lane * 16;
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(qs + k * 512), "r"(qa[k][0]), "r"(qa[k][1]),
+                     "r"(qa[k][2]), "r"(qa[k][3])
+                     : "memory");
+      __syncwarp();
+      auto query = [&](uint32_t (&r)[4], int k) {
+        const uint4 x = lds16(qs + k * 512);
+        r[0] = x.x;
+        r[1] = x.y;
+        r[2] = x.z;
+        r[3] = x.w;
+      };
       // every row of the tile sees at least the tokens up to here
       const int seen_by_all = w.q.L - w.q.n + r0 / a.group;
 
@@ -913,21 +930,29 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
           const float2 sc2 = *reinterpret_cast<const float2 *>(smem + SM::META + (warp * SM::SLOTS + slot) * 8);
           float sc[4][4];
 #pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const int row = 8 * t + (g ^ ((g & 1) << 2));
-            const int sw = D == 128 ? (row & 7) : ((row >> 1) & 3);
+          for (int c = 0; c < D / 64; ++c) {
+            uint32_t e[4][4];
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
+            for (int t = 0; t < 4; ++t) {
+              const int row = 8 * t + (g ^ ((g & 1) << 2));
+              const int sw = D == 128 ? (row & 7) : ((row >> 1) & 3);
               const uint4 x = lds16(kt + row * D + (((c * 4 + q4) ^ sw) << 4));
-              const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+              e[t][0] = flip<FMT>(x.x);
+              e[t][1] = flip<FMT>(x.y);
+              e[t][2] = flip<FMT>(x.z);
+              e[t][3] = flip<FMT>(x.w);
+            }
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint32_t word = flip<FMT>(e[i]);
-                const uint64_t b = widen<FMT, true>(word, 0, word, 1);
+            for (int i = 0; i < 4; ++i) {
+              uint32_t qa[4];
+              query(qa, c * 4 + i);
+#pragma unroll
+              for (int t = 0; t < 4; ++t) {
+                const uint64_t b = widen<FMT, true>(e[t][i], 0, e[t][i], 1);
                 if (c == 0 && i == 0)
-                  mma_zero(sc[t], qa[0], b);
+                  mma_zero(sc[t], qa, b);
                 else
-                  mma(sc[t], qa[c * 4 + i], b);
+                  mma(sc[t], qa, b);
               }
             }
           }
@@ -989,34 +1014,33 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
           // ---- 16 window tokens in 16 bits
           const int t0 = (u - w.full) * kWinUnit;
           float sc[2][4];
-          uint32_t qb[BF16 ? KS : 1][4];  // the queries in bf16: exact, they came from it
-          if (BF16) {
 #pragma unroll
-            for (int k = 0; k < KS; ++k)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float2 x = unpack2<false>(qa[k][i]);
-                qb[BF16 ? k : 0][i] = pack2<true>(x.x, x.y);
-              }
-          }
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const int row = 8 * t + (g ^ ((g & 1) << 2));
+          for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) sc[t][i] = 0.f;
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
+          for (int k = 0; k < KS; k += 2) {
+            uint32_t q0[4], q1[4];
+            query(q0, k);
+            query(q1, k + 1);
+            if (BF16) {  // the queries in bf16: exact, they came from it
 #pragma unroll
-              for (int hf = 0; hf < 2; ++hf) {
-                const uint4 x = lds16(kt + row * 2 * D + ((((c * 4 + q4) * 2 + hf) ^ (row & 7)) << 4));
-                const int k = c * 4 + 2 * hf;
-                if (BF16) {
-                  mma_bf16(sc[t], qb[BF16 ? k : 0], x.x, x.y);
-                  mma_bf16(sc[t], qb[BF16 ? k + 1 : 0], x.z, x.w);
-                } else {
-                  mma(sc[t], qa[k], x.x, x.y);
-                  mma(sc[t], qa[k + 1], x.z, x.w);
-                }
+              for (int i = 0; i < 4; ++i) {
+                const float2 x = unpack2<false>(q0[i]), y = unpack2<false>(q1[i]);
+                q0[i] = pack2<true>(x.x, x.y);
+                q1[i] = pack2<true>(y.x, y.y);
+              }
+            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const int row = 8 * t + (g ^ ((g & 1) << 2));
+              const uint4 x = lds16(kt + row * 2 * D + ((((k & ~3) * 2 + q4 * 2 + (k >> 1 & 1)) ^ (row & 7)) << 4));
+              if (BF16) {
+                mma_bf16(sc[t], q0, x.x, x.y);
+                mma_bf16(sc[t], q1, x.z, x.w);
+              } else {
+                mma(sc[t], q0, x.x, x.y);
+                mma(sc[t], q1, x.z, x.w);
               }
             }
           }
@@ -1118,36 +1142,26 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
           ll += e.y * kvq::fast_exp2(e.x - base);
         }
         const float f = kvq::fast_exp2(m[r] - base);
-        if (r) __syncthreads();  // the buffer of the first half has been read
+        float o[2][QT];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          acc[j][2 * r] *= f;
-          acc[j][2 * r + 1] *= f;
-          const int dst = j / QT;
-          if (dst != warp) {
-            float *o = xch + ((dst * 3 + ((warp - dst - 1) & 3)) * QT + j % QT) * 64 + lane;
-            o[0] = acc[j][2 * r];
-            o[32] = acc[j][2 * r + 1];
+        for (int c = 0; c < 2; ++c) {
+          if (r || c) __syncthreads();  // the buffer has been read
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            const float x = acc[j][2 * r + c] * f;
+            const int dst = j / QT;
+            if (dst != warp)
+              xch[((dst * 3 + ((warp - dst - 1) & 3)) * QT + j % QT) * 32 + lane] = x;
+            else
+              o[c][j % QT] = x;
           }
+          __syncthreads();
+#pragma unroll
+          for (int j = 0; j < QT; ++j)
+#pragma unroll
+            for (int i = 0; i < 3; ++i) o[c][j] += xch[((warp * 3 + i) * QT + j) * 32 + lane];
         }
-        __syncthreads();
-        float o0[QT], o1[QT];
-#pragma unroll
-        for (int j = 0; j < QT; ++j) {
-          o0[j] = o1[j] = 0.f;
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (k == warp) {
-              o0[j] = acc[k * QT + j][2 * r];
-              o1[j] = acc[k * QT + j][2 * r + 1];
-            }
-#pragma unroll
-          for (int i = 0; i < 3; ++i) {
-            const float *x = xch + ((warp * 3 + i) * QT + j) * 64 + lane;
-            o0[j] += x[0];
-            o1[j] += x[32];
-          }
-        }
+        const float (&o0)[QT] = o[0], (&o1)[QT] = o[1];
         // n-tile j, column c holds channel (D / 8) c + j
         const int ch0 = (D / 8) * (2 * q4) + warp * QT, ch1 = ch0 + D / 8;
         const int row = r0 + g + 8 * r;
