@@ -99,7 +99,8 @@ struct Part {
   int h, s;
   int slot;             // partial slot, or -1: the part is the whole item
   int first, c0, cuts;  // the item's first partial slot, its first CTA, and how many CTAs follow
-  int pad[2];
+  int end0;             // end of the units that row tile 0 sees, in u0 .. u1
+  int pad;
 };
 static_assert(sizeof(Part) == 64, "Part");
 
@@ -269,6 +270,7 @@ struct Pair {
   int stored;     // tokens in complete blocks
   int packed;     // units of complete blocks
   int units;      // and one for the window, where seen; 0: not a pair
+  int units0;     // those that row tile 0 sees
 };
 
 __device__ __forceinline__ int row_start_of(const AttnArgs &a, int s) {
@@ -289,6 +291,8 @@ __device__ __forceinline__ Pair make_pair(const AttnArgs &a, int s, int rt) {
   p.stored = L / a.geo.B * a.geo.B;
   p.packed = min(p.last_seen / kKeys + 1, (p.stored + kKeys - 1) / kKeys);
   p.units = p.packed + (p.last_seen >= p.stored ? 1 : 0);
+  const int last_seen0 = max(L - p.q.n + min(rt * kRows + 127, last_row) / a.group, 0);
+  p.units0 = min(last_seen0 / kKeys + 1, p.packed) + (last_seen0 >= p.stored ? 1 : 0);
   return p;
 }
 
@@ -618,36 +622,34 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
         ok = __all_sync(kAll, wait(kPartFull + n_part % kParts, (n_part / kParts) & 1));
         if (!ok) break;
         const Part &p = parts[n_part % kParts];
-        const int units = p.u1 - p.u0, tiles = p.n * a.group - p.row > 128 ? 2 : 1;
+        const int units = p.u1 - p.u0, units0 = p.end0 - p.u0;  // of both row tiles, of row tile 0
+        const int tiles = p.n * a.group - p.row > 128 ? 2 : 1;
         __syncwarp();
         if (leader) kvq::mbar_arrive(bars + kPartFree + n_part % kParts);
         if (units == 0) break;
         ok = __all_sync(kAll, wait(kQFull, n_part & 1) && wait(kKFull + (n_unit & 1), (n_unit >> 1) & 1));
         if (!ok) break;
         fence_after();
-        for (int t = 0; t < tiles; ++t) qk(t, n_unit);
+        for (int t = 0; t < tiles; ++t)
+          if (t || units0) qk(t, n_unit);
         free_stage(kKEmpty + (n_unit & 1));
         for (int u = 0; u < units && ok; ++u, ++n_unit) {
           const bool more = u + 1 < units;
           ok = wait(kVFull + (n_unit & 1), (n_unit >> 1) & 1);
+          if (more) ok = ok && wait(kKFull + ((n_unit + 1) & 1), ((n_unit + 1) >> 1) & 1);
           ok = __all_sync(kAll, ok);
           for (int t = 0; t < tiles && ok; ++t) {
-            ok = __all_sync(kAll, wait(kPFull + t, (t ? np1 : np0) & 1));
+            const int here = t ? units : units0;
+            if (u >= here) continue;
+            uint32_t &np = t ? np1 : np0;
+            ok = __all_sync(kAll, wait(kPFull + t, np & 1));
             if (!ok) break;
+            ++np;
             fence_after();
             pv(t, n_unit, u != 0);
-            if (more) {
-              if (t == 0) {
-                ok = __all_sync(kAll, wait(kKFull + ((n_unit + 1) & 1), ((n_unit + 1) >> 1) & 1));
-                if (!ok) break;
-                fence_after();
-              }
-              qk(t, n_unit + 1);
-            }
+            if (u + 1 < here) qk(t, n_unit + 1);
           }
           if (!ok) break;
-          ++np0;
-          if (tiles == 2) ++np1;
           free_stage(kVEmpty + (n_unit & 1));
           if (more) free_stage(kKEmpty + ((n_unit + 1) & 1));
         }
@@ -681,6 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           p.h = use.h;
           p.s = use.p.s;
           p.slot = -1;
+          p.end0 = max(min(use.u1, use.p.units0), use.u0);
           if (use.u0 != 0 || use.u1 != use.p.units) {
             const long long unit0 = use.start + kOver;
             auto owner = [&](long long pos) { return static_cast<int>(((pos + 1) * ctas - 1) / total); };
@@ -918,6 +921,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       const Part &p = parts[n_part % kParts];
       const int u0 = p.u0, u1 = p.u1;
       if (u0 == u1) break;
+      const int end = t ? u1 : p.end0;  // behind the units that the row tile sees
       const int n_rows = p.n * a.group;
       const int row = p.row + t * 128 + r;
       const bool active = n_rows - p.row > t * 128;  // the tile has rows
@@ -964,7 +968,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       if (active) {
         // every row of the tile sees at least the tokens up to here
         const int seen_by_all = p.L - p.n + (p.row + t * 128) / a.group;
-        for (int u = u0; u < u1; ++u, ++n_unit, ++n_own) {
+        for (int u = u0; u < end; ++u, ++n_unit, ++n_own) {
           ok = wait_all(kSFull + t, n_own & 1, (warp & 7) == 0, 3 + t, 256, true);
           if (!ok) break;
           fence_after();
@@ -1041,6 +1045,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           fence_before();
           kvq::mbar_arrive(bars + kPFull + t);
         }
+        n_unit += u1 - end;
       } else {
         n_unit += u1 - u0;
       }
@@ -1073,7 +1078,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       };
       if (active) {
         sums[hf * kRows] = l;
-        ok = wait_all(kOFull + t, (n_own - 1) & 1, (warp & 7) == 0, 3 + t, 256, ok);
+        ok = wait_all(kOFull + t, (n_own - 1) & 1, (warp & 7) == 0 && end > u0, 3 + t, 256, ok);
         l += sums[(hf ^ 1) * kRows];
       }
       if (active && ok) {
@@ -1093,8 +1098,9 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
               part[static_cast<size_t>(8 * c + i / 4) * kRows] =
-                  make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]),
-                              __uint_as_float(o[i + 3]));
+                  end > u0 ? make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]),
+                                         __uint_as_float(o[i + 3]))
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
           }
         }
         if (whole)
