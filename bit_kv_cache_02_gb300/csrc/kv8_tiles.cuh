@@ -926,12 +926,13 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       const int row = p.row + t * 128 + r;
       const bool active = n_rows - p.row > t * 128;  // the tile has rows
       const bool valid = row < n_rows;
-      const int tok = valid ? row / a.group : 0;
+      const int some = min(row, n_rows - 1);  // rows behind the last one compute what it does
+      const int tok = some / a.group;
       const int lim = valid ? p.L - p.n + tok : -1;  // last position the row sees
 
       // ---- the warp's 32 queries to shared memory: LPR lanes bring a row
-      const long long head = static_cast<long long>(p.h) * a.group + (valid ? row - tok * a.group : 0);
-      const long long q_off = valid ? (static_cast<long long>(p.row0) + tok) * a.q.row + head * a.q.head : -1;
+      const long long head = static_cast<long long>(p.h) * a.group + some - tok * a.group;
+      const long long q_off = (static_cast<long long>(p.row0) + tok) * a.q.row + head * a.q.head;
       float qf = a.zscale;
       if (active) {
         const uint32_t dst = base + SM::Q + t * SM::TILE;
@@ -939,8 +940,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
           const long long off = __shfl_sync(kAll, q_off, (i0 + i) * RPI + lane / LPR);
-          x[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (off >= 0) x[i] = *reinterpret_cast<const uint4 *>(a.q.p + off + lane % LPR * 8);
+          x[i] = *reinterpret_cast<const uint4 *>(a.q.p + off + lane % LPR * 8);
         }
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
