@@ -38,8 +38,17 @@
 // cut by a border are merged by the last CTA that finishes (fp32 partial O, M
 // and l in the workspace).
 //
-// Bound: the tensor cores (4 D flop per row and key; 128 x 128 x 128 twice per
-// row tile and unit).
+// Bound: the chain of a row tile.  Per unit it works on its softmax for about
+// 2350 clocks and waits 1800 for its products, which take 1270 where no others
+// are in the way: S (u + 1) goes where the weights of u lie, so Q K^T of the
+// next unit comes after P V, and tensor memory (two S, two O of 128 columns)
+// has no place for a second S.  The other tile fills the gaps: the tensor pipe
+// is busy for 56% of the time, the issue slots for 50%, and most of the
+// softmax's instructions take two slots (exp2 four).  2048 tokens x 32 query
+// heads over 8192 tokens, D 128: 224 us, 1.07 PFLOP/s; an item costs 11,000
+// clocks besides its units (queries 3500, first S 1600, outputs 4500), so
+// prompts from position 0 (4 x 32 heads, 1500 to 4096 tokens) take 547 us, 0.78
+// PFLOP/s counting visible pairs only.
 #pragma once
 
 #include <atomic>
@@ -104,8 +113,17 @@ struct Part {
 };
 static_assert(sizeof(Part) == 64, "Part");
 
-// All 512 columns of tensor memory are one CTA's: the address is 0.
-constexpr uint32_t kS = 0, kO = 256;  // two tiles of 128 columns each
+// All 512 columns of tensor memory are one CTA's: the address is 0.  Each row
+// tile has 128 columns for S and 128 for O, of which D 64 leaves the second half
+// free: there P has a place of its own, and the next unit's S need not wait for
+// P V.  For D 128 the weights of 64 tokens lie over the start of their half of S.
+constexpr uint32_t kS = 0, kO = 256;
+template <int D>
+struct Weights {
+  static constexpr bool kApart = D == 64;
+  static constexpr uint32_t kAt = kApart ? kO + 64 : kS;    // first column, and the tile's 128 t
+  static constexpr uint32_t kHalf = kApart ? 32 : 64;       // columns from one half's weights to the other's
+};
 
 enum Bar {
   kQFull, kKFull, kKEmpty = kKFull + 2, kVFull = kKEmpty + 2, kVEmpty = kVFull + 2, kSFull = kVEmpty + 2,
@@ -427,11 +445,11 @@ __device__ __forceinline__ float unit_max(std::integral_constant<bool, EDGE>, ui
   return mx;
 }
 
-// Weights 2^(z' - ref) of those columns as fp16 over the start of their half of
-// S; their sum over scale_v.
+// Weights 2^(z' - ref) of those columns as fp16 from column p_at on; their sum
+// over scale_v.
 template <bool EDGE>
-__device__ __forceinline__ float unit_weights(std::integral_constant<bool, EDGE>, uint32_t s_at, int g, const Meta &meta,
-                                              float qf, float ref, bool window, int cmax) {
+__device__ __forceinline__ float unit_weights(std::integral_constant<bool, EDGE>, uint32_t s_at, uint32_t p_at, int g,
+                                              const Meta &meta, float qf, float ref, bool window, int cmax) {
   const float ninf = __int_as_float(0xff800000);
   float l = 0.f;
 #pragma unroll 1
@@ -461,7 +479,7 @@ __device__ __forceinline__ float unit_weights(std::integral_constant<bool, EDGE>
     float x, y;
     unpack64(add2(sum[0], sum[1]), x, y);
     l = fmaf(x + y, EDGE && window ? 1.f : meta.inv[c], l);
-    tmem_st16(s_at + 32 * g + 16 * (c - g), pk);
+    tmem_st16(p_at + 16 * (c - g), pk);
   }
   return l;
 }
@@ -610,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           const uint32_t vd = desc_lo(base + SM::V + (unit & 1) * SM::TILE, SM::HALF);
 #pragma unroll 2
           for (int i = 0; i < kKeys / 16; ++i)
-            mma_ts(kO + t * 128, kS + t * 128 + (i >> 2) * 64 + (i & 3) * 8, vd + i * (2048 >> 4), id_pv, add || i != 0);
+            mma_ts(kO + t * 128, Weights<D>::kAt + t * 128 + (i >> 2) * Weights<D>::kHalf + (i & 3) * 8, vd + i * (2048 >> 4), id_pv, add || i != 0);
           commit(base + SM::BAR + (kOFull + t) * 8);
         }
       };
@@ -646,8 +664,9 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
             if (!ok) break;
             ++np;
             fence_after();
+            if (Weights<D>::kApart && u + 1 < here) qk(t, n_unit + 1);
             pv(t, n_unit, u != 0);
-            if (u + 1 < here) qk(t, n_unit + 1);
+            if (!Weights<D>::kApart && u + 1 < here) qk(t, n_unit + 1);
           }
           if (!ok) break;
           free_stage(kVEmpty + (n_unit & 1));
@@ -904,6 +923,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
     const int r = tid & 127;         // row of the tile = lane of tensor memory
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
     const uint32_t s_at = lanes + kS + t * 128, o_at = lanes + kO + t * 128;
+    const uint32_t p_at = lanes + Weights<D>::kAt + t * 128 + hf * Weights<D>::kHalf;
     uint32_t n_unit = 0;  // units so far
     uint32_t n_own = 0;   // units of this row tile so far
     // copies of whole rows: LPR lanes a row, RPI rows at a time, NQ times for the warp's 32
@@ -1001,6 +1021,9 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
                           : unit_max(std::false_type{}, s_at, 2 * hf, meta, qf, window, cmax);
           float *const both = maxima + (n_own & 1) * 2 * kRows;
           both[hf * kRows] = mx;
+          // the products with the last weights are done before new ones are stored
+          // (given up here, the next wait for S gives up for the whole tile)
+          if (Weights<D>::kApart && (warp & 7) == 0 && u > u0) wait(kOFull + t, (n_own - 1) & 1);
           bar_sync(3 + t, 256);
           mx = fmaxf(mx, both[(hf ^ 1) * kRows]);
           // ---- the reference M, and O where it moved
@@ -1038,8 +1061,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
             }
           }
           // ---- weights
-          const float sum = edge ? unit_weights(std::true_type{}, s_at, 2 * hf, meta, qf, ref, window, cmax)
-                                 : unit_weights(std::false_type{}, s_at, 2 * hf, meta, qf, ref, window, cmax);
+          const float sum = edge ? unit_weights(std::true_type{}, s_at, p_at, 2 * hf, meta, qf, ref, window, cmax)
+                                 : unit_weights(std::false_type{}, s_at, p_at, 2 * hf, meta, qf, ref, window, cmax);
           if (!window) l += sum;
           wait_st();
           fence_before();
