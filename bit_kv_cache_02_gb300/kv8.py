@@ -43,6 +43,12 @@ _pack_rows = struct.Struct("@Pqq").pack
 assert struct.calcsize("@Pqq") == ctypes.sizeof(RowsStruct)
 
 
+_I32, _F32 = torch.int32, torch.float32
+# what torch.cuda.current_stream and current_device ask, without their checks
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _sign():
     C, R = ctypes.POINTER(CacheStruct), c_void_p  # R: packed bytes, or a reference to a RowsStruct
     sig = {
@@ -142,7 +148,7 @@ def _rows(t, cache, shape, name):
 def _row_start(row_start, cache):
     if row_start is None:
         return None
-    if row_start.dtype is not torch.int32 or row_start.numel() != cache.num_seqs + 1 or not row_start.is_contiguous() \
+    if row_start.dtype is not _I32 or row_start.numel() != cache.num_seqs + 1 or not row_start.is_contiguous() \
             or row_start.get_device() != cache.device_index:
         raise ValueError(f"row_start: a contiguous int32 tensor [{cache.num_seqs + 1}] on {cache.device} is needed")
     return row_start.data_ptr()
@@ -153,8 +159,8 @@ def _launch(fn, what, cache, stream, *args):
     index = cache.device_index
     if index < 0:
         raise ValueError("the cache is not on a CUDA device")
-    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-    if torch._C._cuda_getDevice() == index:
+    raw = _current_stream(index) if stream is None else stream.cuda_stream
+    if _current_device() == index:
         code = fn(*args, raw)
     else:
         with torch.cuda.device(index):
@@ -168,7 +174,7 @@ def kv8_append(cache: KV8Cache, k, v, row_start=None, max_new: int = 1, q=None, 
     """k, v: [rows][Hkv][D]; q, q_out: [rows][Hq][D] (rotated along; q_out may
     be q); rope: fp32 [positions][rot_dim] (rope_table) or None.  row_start:
     int32 [S + 1], or None for one row per sequence."""
-    rows, dim = len(k), cache.head_dim
+    rows, dim = k.shape[0] if k.shape else 0, cache.head_dim  # (len and size take longer than shape)
     shape = (rows, cache.num_kv_heads, dim)
     ks, vs = _rows(k, cache, shape, "k"), _rows(v, cache, shape, "v")
     qs = os = None
@@ -176,17 +182,19 @@ def kv8_append(cache: KV8Cache, k, v, row_start=None, max_new: int = 1, q=None, 
     if q is not None:
         if q_out is None:
             raise ValueError("q without q_out")
-        heads = q.size(1) if q.dim() == 3 else 0
+        shape = q.shape
+        heads = shape[1] if len(shape) == 3 else 0
         shape = (rows, heads, dim)
         qs, os = _rows(q, cache, shape, "q"), _rows(q_out, cache, shape, "q_out")
     elif q_out is not None:
         raise ValueError("q_out without q")
     table, rot, positions = None, 0, 0
     if rope is not None:
-        if rope.dtype is not torch.float32 or rope.dim() != 2 or not rope.is_contiguous() \
+        shape = rope.shape
+        if rope.dtype is not _F32 or len(shape) != 2 or not rope.is_contiguous() \
                 or rope.get_device() != cache.device_index:
             raise ValueError(f"rope: a contiguous float32 tensor [positions][rot_dim] on {cache.device} is needed")
-        positions, rot = rope.shape
+        positions, rot = shape
         table = rope.data_ptr() if rot else None
     _launch(lib.kv8_append, "kv8_append", cache, stream, cache.ref, ks, vs, qs, os, heads,
             _row_start(row_start, cache), rows, max_new, table, positions, rot, 1 if interleaved else 0)
@@ -207,9 +215,10 @@ def alloc_workspace(cache: KV8Cache, num_q_heads: int, max_new: int = 1):
 def kv8_attn(cache: KV8Cache, q, out, workspace, max_len: int, row_start=None, max_new: int = 1,
              softmax_scale: float = 0.0, stream=None):
     """q, out: [rows][Hq][D] (out may be q); max_len: a bound on seq_len."""
-    if q.dim() != 3:
+    shape = q.shape
+    if len(shape) != 3:
         raise ValueError("q: [rows][heads][D] is needed")
-    rows, heads, _ = q.shape
+    rows, heads, _ = shape
     shape = (rows, heads, cache.head_dim)
     if workspace.get_device() != cache.device_index or not workspace.is_contiguous():
         raise ValueError(f"workspace: a contiguous tensor on {cache.device} is needed")
