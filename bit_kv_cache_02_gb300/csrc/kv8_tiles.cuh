@@ -43,7 +43,7 @@
 // are in the way: S (u + 1) goes where the weights of u lie, so Q K^T of the
 // next unit comes after P V, and tensor memory (two S, two O of 128 columns)
 // has no place for a second S.  The other tile fills the gaps: the tensor pipe
-// is busy for 56% of the time, the issue slots for 50%, and most of the
+// is busy for 47% of the time, the issue slots for 54%, and most of the
 // softmax's instructions take two slots (exp2 four).  2048 tokens x 32 query
 // heads over 8192 tokens, D 128: 224 us, 1.07 PFLOP/s; an item costs 11,000
 // clocks besides its units (queries 3500, first S 1600, outputs 4500), so
