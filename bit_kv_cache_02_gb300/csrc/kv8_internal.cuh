@@ -48,6 +48,13 @@ __device__ __forceinline__ Seq load_seq(const Geo &geo, const int *row_start, in
   return q;
 }
 
+// x / y for x >= 0, y > 0.  32 bits are enough but for the longest lines, and a
+// 64-bit division costs hundreds of clocks, which a short call would wait for.
+__device__ __forceinline__ long long divide(long long x, long long y) {
+  if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+  return x / y;
+}
+
 // Largest s with key(s) <= x, where key rises with s (0 if there is none).
 template <typename F>
 __device__ __forceinline__ int last_at_or_below(int S, int x, F key) {

@@ -252,7 +252,7 @@ struct Walk {
     w = seq_work(a, s);
     at = pos;
     end = end_;
-    const int pair = static_cast<int>((pos - base) / w.units);
+    const int pair = static_cast<int>(divide(pos - base, w.units));
     u0 = static_cast<int>((pos - base) - static_cast<long long>(pair) * w.units);
     h = pair / w.tiles;
     tile = pair - h * w.tiles;
@@ -289,47 +289,48 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
   const int B = geo.B, H = geo.H;
   const float ninf = __int_as_float(0xff800000);
 
-  // Sequences with rows and nothing to see: zero rows.
-  for (int s = blockIdx.x; s < geo.S; s += gridDim.x) {
-    const Seq sq = load_seq(geo, a.row_start, a.rows, a.max_new, s);
-    if (!sq.ok) {
-      if (tid == 0) set_status(geo.status, KVQ_STATUS_BAD_LEN);
-      continue;
-    }
-    if (sq.n == 0 || (sq.L > 0 && sq.L <= a.max_len)) continue;
-    if (tid == 0 && sq.L != 0) set_status(geo.status, KVQ_STATUS_MAX_LEN);
-    const int per_row = a.Hq * (D / 8);
-    for (long long i = tid; i < static_cast<long long>(sq.n) * per_row; i += kWarps * 32) {
-      const int row = static_cast<int>(i / per_row), c = static_cast<int>(i % per_row);
-      *reinterpret_cast<uint4 *>(a.out.p + (sq.row0 + row) * a.out.row + (c / (D / 8)) * a.out.head +
-                                 (c % (D / 8)) * 8) = make_uint4(0u, 0u, 0u, 0u);
-    }
-  }
-
-  // The line's length, this CTA's range of it, and where the range starts.
+  // The line's length.  On the way, a CTA writes the zero rows of its share of
+  // the sequences with rows and nothing to see.
   long long total = 0, triples = 0;
-  for (int s = lane; s < geo.S; s += 32) {
-    const Work w = seq_work(a, s);
+  for (int s0 = 0; s0 < geo.S; s0 += 32) {
+    Work w = {};
+    bool blind = false;
+    if (s0 + lane < geo.S) {
+      w = seq_work(a, s0 + lane);
+      blind = !w.q.ok || (w.q.n > 0 && (w.q.L <= 0 || w.q.L > a.max_len));
+    }
     total += line_of(w, H);
     triples += static_cast<long long>(w.tiles) * H;
+    for (unsigned m = __ballot_sync(kAll, blind); m; m &= m - 1) {
+      const int s = s0 + __ffs(m) - 1;
+      if (s % gridDim.x != blockIdx.x) continue;
+      const Seq sq = load_seq(geo, a.row_start, a.rows, a.max_new, s);
+      if (tid == 0 && (!sq.ok || sq.L != 0)) set_status(geo.status, sq.ok ? KVQ_STATUS_MAX_LEN : KVQ_STATUS_BAD_LEN);
+      const int per_row = a.Hq * (D / 8);  // (a bad sequence has no rows)
+      for (long long i = tid; i < static_cast<long long>(sq.n) * per_row; i += kWarps * 32) {
+        const int row = static_cast<int>(i / per_row), c = static_cast<int>(i % per_row);
+        *reinterpret_cast<uint4 *>(a.out.p + (sq.row0 + row) * a.out.row + (c / (D / 8)) * a.out.head +
+                                   (c % (D / 8)) * 8) = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
     total += __shfl_xor_sync(kAll, total, o);
     triples += __shfl_xor_sync(kAll, triples, o);
   }
-  // Two units for each warp at least.  A multiple of the triples where that
+  // This CTA's range of the line.  Two units for each warp at least.  A multiple of the triples where that
   // costs little, for then triples of one length are cut alike, and one CTA for
   // each where they are short: merging parts takes as long as four units of a
   // warp (one sequence of 300 tokens, 8 KV heads: 9.1 us instead of 13.9).
   long long want = min(static_cast<long long>(gridDim.x), (total + 2 * kWarps - 1) / (2 * kWarps));
   if (want >= 4 * triples)
-    want = triples ? want / triples * triples : want;
+    want = triples ? divide(want, triples) * triples : want;
   else if (triples <= gridDim.x && total <= triples * 4 * kWarps)
     want = triples;
   const int ctas = static_cast<int>(min(want, total));
   if (static_cast<int>(blockIdx.x) >= ctas) return;
-  const long long lo = blockIdx.x * total / ctas, hi = (blockIdx.x + 1) * total / ctas;
+  const long long lo = divide(blockIdx.x * total, ctas), hi = divide((blockIdx.x + 1) * total, ctas);
   Walk use;
   {
     long long base = 0;
@@ -1204,7 +1205,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
     if (!whole) {
       // ---- the last CTA with a part of this triple merges them all
       const long long s0 = use.start, s1 = s0 + w.units;  // the triple's place on the line
-      auto owner = [&](long long pos) { return static_cast<int>(((pos + 1) * ctas - 1) / total); };
+      auto owner = [&](long long pos) { return static_cast<int>(divide((pos + 1) * ctas - 1, total)); };
       const int c0 = owner(s0), c1 = owner(s1 - 1);
       int *flag = reinterpret_cast<int *>(smem + SM::FLAG);
       __threadfence();
@@ -1218,7 +1219,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
       __syncthreads();
       if (*flag) {
         __threadfence();
-        const int first = 2 * c0 + (c0 * total / ctas < s0 ? 1 : 0);  // later CTAs begin with their part
+        const int first = 2 * c0 + (divide(c0 * total, ctas) < s0 ? 1 : 0);  // later CTAs begin with their part
         const int parts = c1 - c0 + 1;
         constexpr int W = D / 32;  // channels per lane
         for (int row = warp; row < kRowTile && r0 + row < n_rows; row += kWarps) {

@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
   if (total == 0) return;
   const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + 7) / 8));
   if (static_cast<int>(blockIdx.x) >= ctas) return;
-  const long long lo = blockIdx.x * total / ctas, hi = (blockIdx.x + 1) * total / ctas;
+  const long long lo = divide(blockIdx.x * total, ctas), hi = divide((blockIdx.x + 1) * total, ctas);
   {
     long long at = 0;
     for (int i0 = 0; i0 < slots; i0 += kThreads) {
@@ -682,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       // ================================================= the walk
       Walk use;
       use.p = pair_of_slot(a, static_cast<int>(found[0]));
-      use.h = static_cast<int>(found[1] / (use.p.units + kOver));
+      use.h = static_cast<int>(divide(found[1], use.p.units + kOver));
       use.start = lo - (found[1] - static_cast<long long>(use.h) * (use.p.units + kOver));
       use.lo = lo;
       use.end = hi;
@@ -705,13 +705,13 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           p.end0 = max(min(use.u1, use.p.units0), use.u0);
           if (use.u0 != 0 || use.u1 != use.p.units) {
             const long long unit0 = use.start + kOver;
-            auto owner = [&](long long pos) { return static_cast<int>(((pos + 1) * ctas - 1) / total); };
+            auto owner = [&](long long pos) { return static_cast<int>(divide((pos + 1) * ctas - 1, total)); };
             const int c0 = owner(unit0);
             p.c0 = c0;
             p.cuts = owner(unit0 + use.p.units - 1) - c0;
             // a CTA has partial slots for its range's first part and its last one
             p.slot = 2 * blockIdx.x + (lo < use.start ? 1 : 0);
-            p.first = 2 * c0 + (c0 * total / ctas < use.start ? 1 : 0);
+            p.first = 2 * c0 + (divide(c0 * total, ctas) < use.start ? 1 : 0);
           }
         }
         kvq::mbar_arrive(bars + kPartFull + n_part % kParts);
