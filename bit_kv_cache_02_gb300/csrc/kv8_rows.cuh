@@ -39,7 +39,7 @@
 // 6.0 TB/s; one sequence of 2^20 tokens x 8 heads: 306 us, 7.0 TB/s.  With 12
 // to 32 rows (16 sequences, 2000 to 6000 tokens, 8 heads, 3 to 8 drafts x 4)
 // the keys are read once or twice and the chain of a unit's instructions
-// bounds it, at two warps per scheduler: 47 us; three warps, at 168 registers,
+// bounds it, at two warps per scheduler: 44 us; three warps, at 168 registers,
 // were no faster.
 //
 // 16-byte chunks are XOR swizzled by the token so that neither operand's
@@ -845,7 +845,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
         }
       }
       // They wait in shared memory, alike for all warps: in registers they cost
-      // spills (16 sequences with 3 to 8 drafts: 47 us instead of 50).
+      // spills (16 sequences with 3 to 8 drafts: 3 us).
       const uint32_t qs = kvq::smem_u32(smem) + SM::XCH + lane * 16;
 #pragma unroll
       for (int k = 0; k < KS; ++k)
@@ -1203,63 +1203,83 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
     }
 
     if (!whole) {
-      // ---- the last CTA with a part of this triple merges them all
+      // ---- the last CTA with a part of this triple merges them all, a warp's rows
+      // at once (one after the other the drafts take 47 us instead of 44)
       const long long s0 = use.start, s1 = s0 + w.units;  // the triple's place on the line
       auto owner = [&](long long pos) { return static_cast<int>(divide((pos + 1) * ctas - 1, total)); };
       const int c0 = owner(s0), c1 = owner(s1 - 1);
       int *flag = reinterpret_cast<int *>(smem + SM::FLAG);
-      __threadfence();
       __syncthreads();
       if (tid == 0) {
+        __threadfence();  // for the CTA's stores, which the barrier has ordered before
         const int before = kvq::atom_add_acq_rel(a.counters + c0, 1);
         const bool last = before == c1 - c0;
         if (last) a.counters[c0] = 0;
+        __threadfence();
         *flag = last;
       }
       __syncthreads();
-      if (*flag) {
-        __threadfence();
+      const int rows = min(kRowTile, n_rows - r0);
+      if (*flag && warp < rows) {
         const int first = 2 * c0 + (divide(c0 * total, ctas) < s0 ? 1 : 0);  // later CTAs begin with their part
         const int parts = c1 - c0 + 1;
-        constexpr int W = D / 32;  // channels per lane
-        for (int row = warp; row < kRowTile && r0 + row < n_rows; row += kWarps) {
-          float mm = ninf;
-          for (int i = lane; i < parts; i += 32) {
-            const int sl = i == 0 ? first : 2 * (c0 + i);
-            mm = fmaxf(mm, __ldcg(&a.part_ml[sl * kRowTile + row]).x);
-          }
+        constexpr int W = D / 32;                // channels per lane
+        constexpr int NR = HALVES == 1 ? 2 : 4;  // rows per warp, at once: warp + 4 k, or again the last one
+        float mm[NR], ll[NR], o[NR][W];
+        int row[NR];
 #pragma unroll
-          for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(kAll, mm, o));
-          const float base = mm == ninf ? 0.f : mm;
-          float ll = 0.f, o[W];
+        for (int k = 0; k < NR; ++k) {
+          row[k] = min(warp + kWarps * k, rows - 1);
+          mm[k] = ninf;
+          ll[k] = 0.f;
 #pragma unroll
-          for (int k = 0; k < W; ++k) o[k] = 0.f;
-#pragma unroll 4
-          for (int i = 0; i < parts; ++i) {
-            const int sl = i == 0 ? first : 2 * (c0 + i);
-            const float2 e = __ldcg(&a.part_ml[sl * kRowTile + row]);
-            const float f = kvq::fast_exp2(e.x - base);
-            ll += e.y * f;
-            const float *src = a.part_o + (static_cast<size_t>(sl) * kRowTile + row) * D + lane * W;
-            if (W == 4) {
-              const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
-              o[0] += x.x * f;
-              o[1] += x.y * f;
-              o[W > 2 ? 2 : 0] += W > 2 ? x.z * f : 0.f;
-              o[W > 3 ? 3 : 0] += W > 3 ? x.w * f : 0.f;
-            } else {
-              const float2 x = __ldcg(reinterpret_cast<const float2 *>(src));
-              o[0] += x.x * f;
-              o[1] += x.y * f;
+          for (int j = 0; j < W; ++j) o[k][j] = 0.f;
+        }
+        for (int i = lane; i < parts; i += 32) {
+          const int sl = i == 0 ? first : 2 * (c0 + i);
+#pragma unroll
+          for (int k = 0; k < NR; ++k) mm[k] = fmaxf(mm[k], __ldcg(&a.part_ml[sl * kRowTile + row[k]]).x);
+        }
+#pragma unroll
+        for (int k = 0; k < NR; ++k) {
+#pragma unroll
+          for (int d = 16; d; d >>= 1) mm[k] = fmaxf(mm[k], __shfl_xor_sync(kAll, mm[k], d));
+          if (mm[k] == ninf) mm[k] = 0.f;
+        }
+#pragma unroll(HALVES == 1 ? 4 : 2)
+        for (int i = 0; i < parts; ++i) {
+          const int sl = i == 0 ? first : 2 * (c0 + i);
+          float2 e[NR];
+          float x[NR][W];
+#pragma unroll
+          for (int k = 0; k < NR; ++k) {
+            e[k] = __ldcg(&a.part_ml[sl * kRowTile + row[k]]);
+            const float *src = a.part_o + (static_cast<size_t>(sl) * kRowTile + row[k]) * D + lane * W;
+#pragma unroll
+            for (int j = 0; j < W; j += 2) {
+              const float2 y = __ldcg(reinterpret_cast<const float2 *>(src + j));
+              x[k][j] = y.x;
+              x[k][j + 1] = y.y;
             }
           }
-          const float inv = ll == 0.f ? 0.f : 1.f / ll;
-          const int tok = (r0 + row) / a.group;
-          uint16_t *dst = a.out.p + (static_cast<long long>(w.q.row0) + tok) * a.out.row +
-                          (static_cast<long long>(use.h) * a.group + r0 + row - tok * a.group) * a.out.head + lane * W;
 #pragma unroll
-          for (int k = 0; k < W; k += 2)
-            *reinterpret_cast<uint32_t *>(dst + k) = pack2<BF16>(o[k] * inv, o[k + 1] * inv);
+          for (int k = 0; k < NR; ++k) {
+            const float f = kvq::fast_exp2(e[k].x - mm[k]);
+            ll[k] += e[k].y * f;
+#pragma unroll
+            for (int j = 0; j < W; ++j) o[k][j] += x[k][j] * f;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < NR; ++k) {
+          if (warp + kWarps * k >= rows) break;
+          const float inv = ll[k] == 0.f ? 0.f : 1.f / ll[k];
+          const int tok = (r0 + row[k]) / a.group;
+          uint16_t *dst = a.out.p + (static_cast<long long>(w.q.row0) + tok) * a.out.row +
+                          (static_cast<long long>(use.h) * a.group + r0 + row[k] - tok * a.group) * a.out.head + lane * W;
+#pragma unroll
+          for (int j = 0; j < W; j += 2)
+            *reinterpret_cast<uint32_t *>(dst + j) = pack2<BF16>(o[k][j] * inv, o[k][j + 1] * inv);
         }
       }
     }
