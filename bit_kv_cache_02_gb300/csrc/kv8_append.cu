@@ -355,16 +355,18 @@ cudaError_t launch_append(const Geo &geo, const Rows &k, const Rows &v, const Ro
   // up to B new tokens complete at most one block of a sequence
   a.slots = max_new > geo.B ? rows / geo.B + geo.S : 0;
   // With many blocks keys and values have CTAs of their own (prompts 467
-  // against 543 us, ragged chunks 18 against 22 us), and a CTA takes eight
-  // heads, so that the table's values, as many bytes per token as a head's keys
-  // and values together, come from the first-level cache for seven of them.
-  // With few, a head's keys and values share a CTA: less to start.
+  // against 543 us), and a CTA takes eight heads, so that the table's values, as
+  // many bytes per token as a head's keys and values together, come from the
+  // first-level cache for seven of them.  With few, a head's keys and values
+  // share a CTA: less to start (ragged chunks of 356 blocks 18.5 against 20.0
+  // us, a decode step of 64 x 8 heads 4.2 against 5.6).
   const long long blocks = a.slots ? a.slots : geo.S;
   a.split = blocks * geo.H >= 2048;
   a.heads = blocks * geo.H >= 8192 && rot_dim ? 8 : 1;
   a.head_groups = (geo.H + a.heads - 1) / a.heads;
   const long long tasks = blocks * a.head_groups * (a.split ? 2 : 1);
-  // eight threads share a query row's chunk pair, fewer where there are fewer heads
+  // eight threads share a query row's chunk pair, fewer where there are fewer
+  // heads (four: that decode step takes 5.0 us; sixteen: prompts 483)
   a.lanes = Hq >= 8 ? 3 : Hq >= 4 ? 2 : Hq >= 2 ? 1 : 0;
   const int per = (min(geo.B * geo.D / 16, 256) / (geo.D / 16)) >> a.lanes;  // query rows of a CTA, see launch_ni
   // and one CTA checks the row ranges where there are slots
