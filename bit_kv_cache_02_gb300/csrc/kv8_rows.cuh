@@ -1211,11 +1211,11 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
       int *flag = reinterpret_cast<int *>(smem + SM::FLAG);
       __syncthreads();
       if (tid == 0) {
-        __threadfence();  // for the CTA's stores, which the barrier has ordered before
+        // releases the CTA's stores, which the barrier has ordered before, and
+        // acquires the others' for the reads behind the next barrier
         const int before = kvq::atom_add_acq_rel(a.counters + c0, 1);
         const bool last = before == c1 - c0;
         if (last) a.counters[c0] = 0;
-        __threadfence();
         *flag = last;
       }
       __syncthreads();
@@ -1235,17 +1235,6 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
 #pragma unroll
           for (int j = 0; j < W; ++j) o[k][j] = 0.f;
         }
-        for (int i = lane; i < parts; i += 32) {
-          const int sl = i == 0 ? first : 2 * (c0 + i);
-#pragma unroll
-          for (int k = 0; k < NR; ++k) mm[k] = fmaxf(mm[k], __ldcg(&a.part_ml[sl * kRowTile + row[k]]).x);
-        }
-#pragma unroll
-        for (int k = 0; k < NR; ++k) {
-#pragma unroll
-          for (int d = 16; d; d >>= 1) mm[k] = fmaxf(mm[k], __shfl_xor_sync(kAll, mm[k], d));
-          if (mm[k] == ninf) mm[k] = 0.f;
-        }
 #pragma unroll(HALVES == 1 ? 4 : 2)
         for (int i = 0; i < parts; ++i) {
           const int sl = i == 0 ? first : 2 * (c0 + i);
@@ -1264,10 +1253,12 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
           }
 #pragma unroll
           for (int k = 0; k < NR; ++k) {
-            const float f = kvq::fast_exp2(e[k].x - mm[k]);
-            ll[k] += e[k].y * f;
+            const float top = fmaxf(mm[k], e[k].x), base = top == ninf ? 0.f : top;
+            const float was = kvq::fast_exp2(mm[k] - base), f = kvq::fast_exp2(e[k].x - base);
+            mm[k] = top;
+            ll[k] = fmaf(ll[k], was, e[k].y * f);
 #pragma unroll
-            for (int j = 0; j < W; ++j) o[k][j] += x[k][j] * f;
+            for (int j = 0; j < W; ++j) o[k][j] = fmaf(o[k][j], was, x[k][j] * f);
           }
         }
 #pragma unroll
