@@ -1133,10 +1133,11 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
         fence_before();
       }
       if (!whole) {
-        __threadfence();
         ok = bar_all(2, 512, ok);
         if (!ok) break;
         if (tid == 0) {
+          // releases the CTA's stores, which the barrier has ordered before, and
+          // acquires the others' for the reads behind the next barrier
           const bool last = kvq::atom_add_acq_rel(a.tile_counters + p.c0, 1) == p.cuts;
           if (last) a.tile_counters[p.c0] = 0;
           *flag = last;
@@ -1145,40 +1146,34 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
         const bool merge = *flag;
         bar_sync(2, 512);  // read before it is set again
         if (merge && active) {
-          __threadfence();
           const int first = p.first, c0 = p.c0, n = p.cuts + 1;
-          auto slot_of = [&](int i) { return i == 0 ? first : 2 * (c0 + i); };
-          float mm = ninf, ll = 0.f;
-          for (int i = 0; i < n; ++i) mm = fmaxf(mm, __ldcg(&a.tile_ml[slot_of(i) * kRows + t * 128 + r]).x);
-          const float ref = mm == ninf ? 0.f : mm;
-          for (int i = 0; i < n; ++i) {
-            const float2 e = __ldcg(&a.tile_ml[slot_of(i) * kRows + t * 128 + r]);
-            ll += e.y * kvq::fast_exp2(e.x - ref);
-          }
-          const float inv = ll == 0.f ? 0.f : 1.f / ll;
 #pragma unroll 1
           for (int c = hf * (D / 64); c < (hf + 1) * (D / 64); ++c) {
-            float o[32];
+            float o[32], mm = ninf, ll = 0.f;
 #pragma unroll
             for (int k = 0; k < 32; ++k) o[k] = 0.f;
 #pragma unroll 1
             for (int i = 0; i < n; ++i) {
-              const int sl = slot_of(i);
+              const int sl = i == 0 ? first : 2 * (c0 + i);
               const float4 *src = reinterpret_cast<const float4 *>(a.tile_o) +
                                   (static_cast<size_t>(sl) * (D / 4) + 8 * c) * kRows + t * 128 + r;
+              const float2 e = __ldcg(&a.tile_ml[sl * kRows + t * 128 + r]);
               float4 x[8];
 #pragma unroll
               for (int k = 0; k < 8; ++k) x[k] = __ldcg(src + static_cast<size_t>(k) * kRows);
-              const float f = kvq::fast_exp2(__ldcg(&a.tile_ml[sl * kRows + t * 128 + r]).x - ref) * inv;
+              const float top = fmaxf(mm, e.x), ref = top == ninf ? 0.f : top;
+              const float was = kvq::fast_exp2(mm - ref), f = kvq::fast_exp2(e.x - ref);
+              mm = top;
+              ll = fmaf(ll, was, e.y * f);
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
-                o[4 * k] += x[k].x * f;
-                o[4 * k + 1] += x[k].y * f;
-                o[4 * k + 2] += x[k].z * f;
-                o[4 * k + 3] += x[k].w * f;
+                o[4 * k] = fmaf(o[4 * k], was, x[k].x * f);
+                o[4 * k + 1] = fmaf(o[4 * k + 1], was, x[k].y * f);
+                o[4 * k + 2] = fmaf(o[4 * k + 2], was, x[k].z * f);
+                o[4 * k + 3] = fmaf(o[4 * k + 3], was, x[k].w * f);
               }
             }
-            put(c, o, 1.f);
+            put(c, o, ll == 0.f ? 0.f : 1.f / ll);
           }
           store_rows();
         }
