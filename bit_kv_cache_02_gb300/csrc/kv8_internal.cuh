@@ -111,9 +111,9 @@ constexpr int kRowTile = 16;  // (token, query head) rows that share one pass ov
 
 // Sequences with more rows per KV head than this go to the tile kernel.  The
 // rows kernel reads the keys once for 16 rows, the tile kernel once for 256
-// after a longer start: one sequence of 8 x 16,384 tokens (8 KV heads, D 128)
-// takes 63 us there against 97 us here at 32 rows, 108 against 97 at 64, 196
-// against 93 at 128.
+// after a longer start.  Rows against tile kernel, int8, D 128, 16 sequences x 8
+// KV heads x 4000 tokens: 54 and 89 us at 32 rows, 95 and 90 at 64, 177 and 86
+// at 128; 32 x 32 x 2000 tokens at 48 rows: 284 and 267.
 constexpr int kRowsMax = 48;
 constexpr int kTileRows = 256;      // rows of an item of the tile kernel
 constexpr int kMaxTileCtas = 160;

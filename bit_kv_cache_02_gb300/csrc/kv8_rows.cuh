@@ -34,12 +34,12 @@
 // ends.  A triple cut by CTA borders is merged by the last CTA that finishes.
 //
 // Bound: HBM for one row per query head (2 D bytes per token and KV head).
-// Measured, D 128, reading 4097 tokens x 16 sequences x 32 heads: 90 us, 6.0
+// Measured, D 128, reading 4097 tokens x 16 sequences x 32 heads: 88 us, 6.1
 // TB/s; 64 sequences x 8 heads of four rows, 1024 to 8192 tokens, e4m3: 111 us,
-// 6.0 TB/s; one sequence of 2^20 tokens x 8 heads: 306 us, 7.0 TB/s.  With 12
+// 6.0 TB/s; one sequence of 2^20 tokens x 8 heads: 304 us, 7.1 TB/s.  With 12
 // to 32 rows (16 sequences, 2000 to 6000 tokens, 8 heads, 3 to 8 drafts x 4)
 // the keys are read once or twice and the chain of a unit's instructions
-// bounds it, at two warps per scheduler: 44 us; three warps, at 168 registers,
+// bounds it, at two warps per scheduler: 43 us; three warps, at 168 registers,
 // were no faster.
 //
 // 16-byte chunks are XOR swizzled by the token so that neither operand's

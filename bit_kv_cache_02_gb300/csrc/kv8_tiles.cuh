@@ -47,7 +47,7 @@
 // softmax's instructions take two slots (exp2 four).  2048 tokens x 32 query
 // heads over 8192 tokens, D 128: 224 us, 1.07 PFLOP/s; an item costs 11,000
 // clocks besides its units (queries 3500, first S 1600, outputs 4500), so
-// prompts from position 0 (4 x 32 heads, 1500 to 4096 tokens) take 547 us, 0.78
+// prompts from position 0 (4 x 32 heads, 1500 to 4096 tokens) take 550 us, 0.78
 // PFLOP/s counting visible pairs only.
 #pragma once
 
