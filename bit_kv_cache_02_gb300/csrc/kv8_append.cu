@@ -352,8 +352,9 @@ cudaError_t launch_append(const Geo &geo, const Rows &k, const Rows &v, const Ro
   a.rope = rope;
   a.rot = rot_dim;
   a.interleaved = interleaved;
-  // up to B new tokens complete at most one block of a sequence
-  a.slots = max_new > geo.B ? rows / geo.B + geo.S : 0;
+  // up to B new tokens complete at most one block of a sequence, and without
+  // row_start, whatever max_new allows, each brings one
+  a.slots = row_start && max_new > geo.B ? rows / geo.B + geo.S : 0;
   // With many blocks keys and values have CTAs of their own (prompts 467
   // against 543 us), and a CTA takes eight heads, so that the table's values, as
   // many bytes per token as a head's keys and values together, come from the

@@ -250,6 +250,31 @@ def test_append_device_errors(kv8):
             assert (q_out[40 * bad:40 * bad + 40] == 5.0).all()
 
 
+@pytest.mark.parametrize("D,B,fmt", [(128, 32, "int8"), (64, 64, "e4m3"), (128, 128, "e4m3")])
+def test_append_one_row_each_under_a_larger_bound(kv8, D, B, fmt):
+    """Without row_start every sequence brings one row, also where max_new is
+    the bound of the whole program, above the block: steps across block borders,
+    with rows of no sequence behind, then attention by the same arguments."""
+    S, g, most = 4, 2, 2 * B + 30
+    r = Run(kv8, S, 2, g, D, B, fmt, "float16", 4 * B, seed=B)
+    r.append([B - 2, 0, 2 * B - 1, 5])
+    start = np.arange(S + 1)
+    for _ in range(3):
+        x = r.numbers((S + 2, 2 * g + 4, D))
+        t = _dev(x, r.dtype)
+        q_out = torch.full((S + 2, 2 * g, D), 5.0, dtype=t.dtype, device="cuda")
+        out = q_out.clone()
+        r.cache.seq_len += 1
+        kv8.kv8_append(r.cache, t[:, 2 * g:2 * g + 2], t[:, 2 * g + 2:], max_new=most, q=t[:, :2 * g], q_out=q_out,
+                       rope=r.rope)
+        r.q = r.orc.append(x[:S, 2 * g:2 * g + 2], x[:S, 2 * g + 2:], start, r.table, False, x[:S, :2 * g])
+        r.q_out = q_out[:S]
+        r.check_state()
+        kv8.kv8_attn(r.cache, q_out, out, kv8.alloc_workspace(r.cache, 2 * g, most), 4 * B, max_new=most)
+        r.close(_host(out[:S]), *r.orc.attention(r.q, start))
+        assert (q_out[S:] == 5.0).all() and (out[S:] == 5.0).all()
+
+
 # --------------------------------------------------------------- attention
 
 @pytest.mark.parametrize("fmt,dtype", TYPES)
