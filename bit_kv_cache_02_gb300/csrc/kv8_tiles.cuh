@@ -1025,6 +1025,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           // (given up here, the next wait for S gives up for the whole tile)
           if (Weights<D>::kApart && (warp & 7) == 0 && u > u0) wait(kOFull + t, (n_own - 1) & 1);
           bar_sync(3 + t, 256);
+          if (Weights<D>::kApart) fence_after();  // orders the stores of new weights behind that wait
           mx = fmaxf(mx, both[(hf ^ 1) * kRows]);
           // ---- the reference M, and O where it moved
           const bool move = mx > M + kGrow || (M == ninf && mx > ninf);

@@ -335,6 +335,25 @@ def test_chunk_layouts(kv8):
         assert torch.equal(a, r.attend(ws=ws, check=False)), "a repeated call gave another result"
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_weights_follow_each_other_under_a_still_maximum(kv8, D):
+    """All scores alike, so that from the second unit on the maximum does not
+    move and weights follow weights with nothing but the wait between them;
+    values differ by unit, so that a weight stored too early or too late shows.
+    The same bits every time."""
+    def change(q, k, v):
+        k[:] = 0.5
+        v[:] = (np.arange(len(v)) // 128 % 7 - 3.0)[:, None, None] + np.sign(v) / 4
+
+    r = Run(kv8, 1, 2, 2, D, 64, "e4m3", "float16", 6000, rot=0)
+    r.append([5000], change)
+    r.append([128], change)
+    ws = kv8.alloc_workspace(r.cache, 4, 128)
+    want = r.attend(ws=ws)
+    for _ in range(50):
+        assert torch.equal(want, r.attend(ws=ws, check=False))
+
+
 @pytest.mark.parametrize("fmt,dtype", TYPES)
 def test_rows_without_keys_get_zeros(kv8, fmt, dtype):
     """More rows than tokens, and sequences without a token; with more query
