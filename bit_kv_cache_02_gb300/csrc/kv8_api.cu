@@ -180,7 +180,7 @@ int kv8_attn(const kv8_cache *cache, int32_t num_q_heads, const kv8_rows *q, con
   a.max_len = max_len;
   a.zscale = softmax_scale * 1.4426950408889634f;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
-  a.part_o = reinterpret_cast<float *>(ws);
+  a.part_o = reinterpret_cast<float *>(ws + plan.off_o);
   a.part_ml = reinterpret_cast<float2 *>(ws + plan.off_ml);
   a.counters = reinterpret_cast<int *>(ws + plan.off_cnt);
   a.tile_counters = reinterpret_cast<int *>(ws + plan.off_tile_cnt);
@@ -200,10 +200,12 @@ AttnPlan plan_attn(int D, long long rows_per_head) {
   AttnPlan p;
   auto align = [](size_t x) { return (x + 255) / 256 * 256; };
   p.tiles = rows_per_head > kRowsMax;
-  p.off_ml = static_cast<size_t>(2) * kMaxCtas * kRowTile * D * sizeof(float);
-  p.off_cnt = align(p.off_ml + static_cast<size_t>(2) * kMaxCtas * kRowTile * sizeof(float2));
-  p.off_tile_cnt = p.off_cnt + align(kMaxCtas * sizeof(int));
-  p.off_tile_o = p.off_tile_cnt + align(kMaxTileCtas * sizeof(int));
+  // the counters first, at offsets that no argument moves
+  p.off_cnt = 0;
+  p.off_tile_cnt = align(kMaxCtas * sizeof(int));
+  p.off_o = p.off_tile_cnt + align(kMaxTileCtas * sizeof(int));
+  p.off_ml = p.off_o + static_cast<size_t>(2) * kMaxCtas * kRowTile * D * sizeof(float);
+  p.off_tile_o = align(p.off_ml + static_cast<size_t>(2) * kMaxCtas * kRowTile * sizeof(float2));
   p.off_tile_ml = p.off_tile_o + static_cast<size_t>(2) * kMaxTileCtas * kTileRows * D * sizeof(float);
   p.bytes = p.tiles ? align(p.off_tile_ml + static_cast<size_t>(2) * kMaxTileCtas * kTileRows * sizeof(float2))
                     : p.off_tile_o;

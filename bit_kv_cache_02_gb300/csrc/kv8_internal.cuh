@@ -118,12 +118,14 @@ constexpr int kRowsMax = 48;
 constexpr int kTileRows = 256;      // rows of an item of the tile kernel
 constexpr int kMaxTileCtas = 160;
 
-// Byte offsets of the workspace regions.  Rows kernel: partial outputs
-// [2 kMaxCtas][16][D], their (max, sum), one merge counter per CTA.  Tile
+// Byte offsets of the workspace regions.  One merge counter per CTA of either
+// kernel comes first, at places that do not depend on the call: what a call of
+// one shape leaves of its partial results is never another's counter.  Rows
+// kernel: partial outputs [2 kMaxCtas][16][D] and their (max, sum).  Tile
 // kernel, where a sequence can bring enough rows: the same for
 // [2 kMaxTileCtas][256].
 struct AttnPlan {
-  size_t off_ml, off_cnt, off_tile_cnt, off_tile_o, off_tile_ml, bytes;
+  size_t off_cnt, off_tile_cnt, off_o, off_ml, off_tile_o, off_tile_ml, bytes;
   bool tiles;
 };
 AttnPlan plan_attn(int D, long long rows_per_head);

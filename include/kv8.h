@@ -181,9 +181,13 @@ int64_t kv8_attn_workspace_bytes(const kv8_cache *cache, int32_t num_q_heads,
  *   row_start, rows, max_new  as in kv8_append (max_new >= 1).
  *   softmax_scale  multiplier of q.k; <= 0 selects 1/sqrt(D).
  *   workspace  at least kv8_attn_workspace_bytes() bytes, 256-byte aligned,
- *              zero-filled before its first use; every call leaves its
- *              counters zero again (zero it after KVQ_STATUS_TIMEOUT, which
- *              a call that gave up sets, its rows being undefined).
+ *              zero-filled before its first use and written by kv8_attn
+ *              only.  Every call leaves its counters zero again, at places
+ *              that no argument moves: calls of other caches, head
+ *              dimensions and bounds may follow each other on one workspace
+ *              that is large enough for each (zero it after
+ *              KVQ_STATUS_TIMEOUT, which a call that gave up sets, its rows
+ *              being undefined).
  *   max_len    host bound on every seq_len, 1 .. capacity.
  *
  * Row i of the n rows of sequence s sits at position seq_len[s] - n + i and

@@ -450,6 +450,40 @@ def test_many_sequences_and_splits(kv8):
     assert int(ws[-2560:].view(torch.int32).abs().sum()) == 0
 
 
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+def test_workspace_serves_other_shapes(kv8, dtype):
+    """One workspace for caches of both head dimensions in turn, single tokens
+    and chunks over keys that all CTAs' borders cut: the same as with workspaces
+    of their own.  What one call leaves of its partial results is no other
+    call's counter."""
+    dt = getattr(torch, dtype)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    calls = []
+    for D in (128, 64):
+        L, H, B = 15000, 8, 64
+        c = kv8.KV8Cache(1, H, L, L // B, head_dim=D, block=B, fmt="e4m3", dtype=dt)
+        for j in range(2):
+            c.codes[:, :, j] = torch.randn(c.codes[:, :, j].shape, generator=gen, device="cuda").to(c.codes.dtype)
+        c.scales.fill_(1.0)
+        for win in (c.k_win, c.v_win):
+            win.copy_(torch.randn(win.shape, generator=gen, device="cuda"))
+        c.block_table.copy_(torch.arange(L // B, device="cuda"))
+        c.seq_len.fill_(L)
+        for new in (1, 5, 130):
+            q = torch.randn((new, H, D), generator=gen, device="cuda").to(dt)
+            start = torch.tensor([0, new], dtype=torch.int32, device="cuda")
+            want = torch.full_like(q, 5.0)
+            kv8.kv8_attn(c, q, want, kv8.alloc_workspace(c, H, new), L, row_start=start, max_new=new)
+            calls.append((c, q, start, new, want))
+    ws = kv8.alloc_workspace(calls[0][0], 8, 130)
+    for i in (0, 3, 0, 5, 0, 2, 5, 2, 3, 1, 4, 1, 5, 4, 2):
+        c, q, start, new, want = calls[i]
+        out = torch.full_like(q, 5.0)
+        kv8.kv8_attn(c, q, out, ws, c.capacity, row_start=start, max_new=new)
+        assert torch.equal(out, want) and int(c.status.item()) == 0
+    assert int(ws[:3328].view(torch.int32).abs().sum()) == 0  # the counters
+
+
 def test_attn_device_errors(kv8):
     """Lengths past the bound give zero rows, bad row ranges leave rows alone,
     a bad block gives NaN; each sets its bit."""
