@@ -102,8 +102,12 @@ cudaError_t launch_append(const Geo &geo, const Rows &k, const Rows &v, const Ro
                           int interleaved, cudaStream_t stream, uint64_t *launches);
 
 // Attention counts the values of a block whose scale is smaller (2^-80) as
-// zeros: 1 / scale times the weights of 2^31 tokens stays finite.
+// zeros: 1 / scale times the weights of 2^31 tokens stays finite.  Weights are
+// formed relative to the largest score times scale that a row has met; blocks
+// of zeros enter that maximum with this scale, below all others, so that small
+// values beside them keep their weights' bits.
 constexpr float kZeroScale = 8.27180613e-25f;
+constexpr float kZeroLog = -80.f;
 
 // CTAs of one attention launch at most (sizes the workspace's partial slots).
 constexpr int kMaxCtas = 640;

@@ -7,7 +7,8 @@
 // log2(scale_v), m the running maximum of z, w = 2^(z - m + 15), o the sum of
 // w v_code, l the sum of w / scale_v, out = o / l.  With scale_v in the
 // exponent, o accumulates codes of blocks with different scales in the mma's
-// own registers.
+// own registers.  A block of zeros, which has no scale to speak of, enters m
+// with kZeroLog for it and its weights, formed without, go into l alone.
 //
 // Both products run on mma.sync m16n8k16 with fp32 accumulators.  Up to eight
 // rows are N, tokens (then channels) M: the codes become A fragments and the
@@ -503,8 +504,8 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
       // Scores of NB m-tiles of 16 tokens from position t0 to weights 2^15 w.
       // Row g of a tile is token g ^ 4 (g & 1), row g + 8 the same behind 8.
       const int tok0 = g ^ ((g & 1) << 2);
-      auto softmax = [&](auto nb, float (*sc)[4], const float (&ka)[2], const float (&kb)[2], float inv, int t0,
-                         bool window, uint32_t bad) {
+      auto softmax = [&](auto nb, float (*sc)[4], const float (&ka)[2], const float (&kb)[2], float inv, bool none,
+                         int t0, bool window, uint32_t bad) {
         constexpr int NB = decltype(nb)::value;
         float mx[2] = {m[0], m[1]};
 #pragma unroll
@@ -534,9 +535,10 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
         if (__any_sync(kAll, mx[0] != m[0] || mx[1] != m[1])) {
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const float f = mx[r] == m[r] ? 1.f : kvq::fast_exp2(m[r] - mx[r]);  // -inf before the first token
+            const float h = mx[r] == m[r] ? 1.f : kvq::fast_exp2(0.5f * (m[r] - mx[r]));  // -inf before the first token
+            const float f = h * h;
             m[r] = mx[r];
-            l[r] *= f;
+            l[r] = l[r] * h * h;  // (zeros' sums may outlive a factor that fp32 cannot hold)
 #pragma unroll
             for (int j = 0; j < MT; ++j) {
               acc[j][r] *= f;
@@ -544,6 +546,11 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
             }
           }
         }
+        if (none)
+#pragma unroll
+          for (int t = 0; t < NB; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sc[t][i] -= kZeroLog;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const float ms = m[r] == ninf ? 0.f : m[r] - kShift;
@@ -587,7 +594,8 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
           // scales that are not finite make the rows that see the block NaN;
           // zeros may have any scale
           const bool bad = !(fabsf(sc2.x) < inf && fabsf(sc2.y) < inf), none = sc2.y < kZeroScale;
-          const float ks = bad ? 1.f : sc2.x, vs = bad || none ? 1.f : sc2.y, lv = __log2f(vs);
+          const float ks = bad ? 1.f : sc2.x, vs = bad || none ? 1.f : sc2.y;
+          const float lv = none ? kZeroLog : __log2f(vs);
           float ka[2], kb[2];
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
@@ -595,7 +603,8 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
             ka[r] = FMT == KV8_INT8 ? f * 16777216.f : f;
             kb[r] = FMT == KV8_INT8 ? fmaf(-r128[r], f, lv) : lv;
           }
-          softmax(std::integral_constant<int, 2>{}, sc, ka, kb, __fdividef(1.f, vs), u * kUnit, false, bad ? kAll : 0u);
+          softmax(std::integral_constant<int, 2>{}, sc, ka, kb, __fdividef(1.f, vs), none, u * kUnit, false,
+                  bad ? kAll : 0u);
           uint32_t p[2][2];  // weights as B fragments of the two k-steps
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
@@ -679,7 +688,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
           }
           bad = __reduce_or_sync(kAll, bad);
           const float zero[2] = {0.f, 0.f};
-          softmax(std::integral_constant<int, 1>{}, sc, rf, zero, 1.f, w.full * kUnit + t0, true, bad);
+          softmax(std::integral_constant<int, 1>{}, sc, rf, zero, 1.f, false, w.full * kUnit + t0, true, bad);
           if (bad) {  // their weights are NaN where they are seen, and 0 elsewhere
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -745,7 +754,8 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
 #pragma unroll
         for (int i = 0; i < kWarps; ++i) {
           const float2 e = ml[i * kRowTile + 2 * q4 + r];
-          ll += e.y * kvq::fast_exp2(e.x - base);
+          const float h = kvq::fast_exp2(0.5f * (e.x - base));
+          ll += e.y * h * h;
         }
         const float f = kvq::fast_exp2(m[r] - base);
         if (r) __syncthreads();  // the buffer of the first row has been read
@@ -872,8 +882,8 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
       // Scores of one unit to weights 2^15 w: NB n-tiles of 8 tokens from position
       // t0; column 2 q4 of a tile is token 2 q4, column 2 q4 + 1 token (2 q4 + 1) ^ 4.
       // z = s a + b for the two rows; `bad`: tokens that turn what sees them to NaN.
-      auto softmax = [&](auto nb, float (*sc)[4], const float (&ka)[2], const float (&kb)[2], float inv, int t0,
-                         bool window, uint32_t bad) {
+      auto softmax = [&](auto nb, float (*sc)[4], const float (&ka)[2], const float (&kb)[2], float inv, bool none,
+                         int t0, bool window, uint32_t bad) {
         constexpr int NB = decltype(nb)::value;
         float mx[2] = {m[0], m[1]};
 #pragma unroll
@@ -904,9 +914,10 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
         if (__any_sync(kAll, mx[0] != m[0] || mx[1] != m[1])) {
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const float f = mx[r] == m[r] ? 1.f : kvq::fast_exp2(m[r] - mx[r]);  // -inf before the first token
+            const float h = mx[r] == m[r] ? 1.f : kvq::fast_exp2(0.5f * (m[r] - mx[r]));  // -inf before the first token
+            const float f = h * h;
             m[r] = mx[r];
-            l[r] *= f;
+            l[r] = l[r] * h * h;  // (zeros' sums may outlive a factor that fp32 cannot hold)
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
               acc[j][2 * r] *= f;
@@ -914,6 +925,11 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
             }
           }
         }
+        if (none)
+#pragma unroll
+          for (int t = 0; t < NB; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sc[t][i] -= kZeroLog;
         float sum[2] = {0.f, 0.f};
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -973,7 +989,8 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
           // scales that are not finite make the rows that see the block NaN;
           // zeros may have any scale
           const bool bad = !(fabsf(sc2.x) < inf && fabsf(sc2.y) < inf), none = sc2.y < kZeroScale;
-          const float ks = bad ? 1.f : sc2.x, vs = bad || none ? 1.f : sc2.y, lv = __log2f(vs);
+          const float ks = bad ? 1.f : sc2.x, vs = bad || none ? 1.f : sc2.y;
+          const float lv = none ? kZeroLog : __log2f(vs);
           float ka[2], kb[2];
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
@@ -981,7 +998,8 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
             ka[r] = FMT == KV8_INT8 ? f * 16777216.f : f;
             kb[r] = FMT == KV8_INT8 ? fmaf(-q128[r], f, lv) : lv;
           }
-          softmax(std::integral_constant<int, 4>{}, sc, ka, kb, __fdividef(1.f, vs), u * kUnit, false, bad ? kAll : 0u);
+          softmax(std::integral_constant<int, 4>{}, sc, ka, kb, __fdividef(1.f, vs), none, u * kUnit, false,
+                  bad ? kAll : 0u);
           uint32_t p[2][4];
           weights(p[0], sc[0], sc[1]);
           weights(p[1], sc[2], sc[3]);
@@ -1078,7 +1096,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
           }
           bad = __reduce_or_sync(kAll, bad);
           const float zero[2] = {0.f, 0.f};
-          softmax(std::integral_constant<int, 2>{}, sc, qf, zero, 1.f, w.full * kUnit + t0, true, bad);
+          softmax(std::integral_constant<int, 2>{}, sc, qf, zero, 1.f, false, w.full * kUnit + t0, true, bad);
           uint32_t p[4], rest[4];
           if (BF16) {
 #pragma unroll
@@ -1152,7 +1170,8 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
 #pragma unroll
         for (int i = 0; i < kWarps; ++i) {
           const float2 e = ml[i * kRowTile + g + 8 * r];
-          ll += e.y * kvq::fast_exp2(e.x - base);
+          const float h = kvq::fast_exp2(0.5f * (e.x - base));
+          ll += e.y * h * h;
         }
         const float f = kvq::fast_exp2(m[r] - base);
         float o[2][QT];
@@ -1254,9 +1273,10 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
 #pragma unroll
           for (int k = 0; k < NR; ++k) {
             const float top = fmaxf(mm[k], e[k].x), base = top == ninf ? 0.f : top;
-            const float was = kvq::fast_exp2(mm[k] - base), f = kvq::fast_exp2(e[k].x - base);
+            const float wh = kvq::fast_exp2(0.5f * (mm[k] - base)), fh = kvq::fast_exp2(0.5f * (e[k].x - base));
+            const float was = wh * wh, f = fh * fh;
             mm[k] = top;
-            ll[k] = fmaf(ll[k], was, e[k].y * f);
+            ll[k] = fmaf(ll[k] * wh, wh, e[k].y * fh * fh);
 #pragma unroll
             for (int j = 0; j < W; ++j) o[k][j] = fmaf(o[k][j], was, x[k][j] * f);
           }

@@ -26,7 +26,8 @@
 // Mathematics, in log2 units per row: z_t = q.k_t scale_k softmax_scale log2(e),
 // w_t = 2^(z_t + log2(scale_v) - M + 9), O = sum w_t v_code_t, l = sum w_t /
 // scale_v, out = O / l.  Folding scale_v into the exponent lets O accumulate
-// codes of blocks with different scales in tensor memory.  M follows the row's
+// codes of blocks with different scales in tensor memory (blocks of zeros enter
+// M with kZeroLog, and their weights, formed without, l alone).  M follows the row's
 // maximum of z + log2(scale_v) lazily: O is rescaled only when it grew by more
 // than 2^6, so w stays below 2^15 and weights down to 2^-23 of the largest
 // keep fp16's full precision.  Roundings: w to fp16; bf16 queries scaled to
@@ -446,7 +447,7 @@ __device__ __forceinline__ float unit_max(std::integral_constant<bool, EDGE>, ui
 }
 
 // Weights 2^(z' - ref) of those columns as fp16 from column p_at on; their sum
-// over scale_v.
+// over scale_v.  (A unit with values that count as zeros is EDGE too.)
 template <bool EDGE>
 __device__ __forceinline__ float unit_weights(std::integral_constant<bool, EDGE>, uint32_t s_at, uint32_t p_at, int g,
                                               const Meta &meta, float qf, float ref, bool window, int cmax) {
@@ -458,7 +459,10 @@ __device__ __forceinline__ float unit_weights(std::integral_constant<bool, EDGE>
     tmem_ld32(s, s_at + 32 * c);
     wait_ld32(s);
     const float k = EDGE && window ? 1.f : meta.k[c] * qf;
-    const float bias = (EDGE && window ? 0.f : meta.lv[c]) - ref;
+    // values that count as zeros (their place in V holds zeros): no scale, and
+    // weights that fp16 need not hold
+    const bool zero = EDGE && !window && (meta.flush >> c & 1);
+    const float bias = (EDGE && window ? 0.f : EDGE && zero ? meta.lv[c] - kZeroLog : meta.lv[c]) - ref;
     const uint64_t a2 = pack64(k, k), b2 = pack64(bias, bias);
     uint64_t sum[2] = {pack64(0.f, 0.f), pack64(0.f, 0.f)};
     uint32_t pk[16];
@@ -479,6 +483,10 @@ __device__ __forceinline__ float unit_weights(std::integral_constant<bool, EDGE>
     float x, y;
     unpack64(add2(sum[0], sum[1]), x, y);
     l = fmaf(x + y, EDGE && window ? 1.f : meta.inv[c], l);
+    if (EDGE && zero) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) pk[i] = 0u;
+    }
     tmem_st16(p_at + 16 * (c - g), pk);
   }
   return l;
@@ -760,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           // zeros may have any scale
           const bool zero = !bad && sc.y < kZeroScale;
           const unsigned flushes = __ballot_sync(kAll, none || zero);
-          const float lv = bad ? nan : zero ? 0.f : log2f(sc.y), inv = bad || zero ? 1.f : 1.f / sc.y;
+          const float lv = bad ? nan : zero ? kZeroLog : log2f(sc.y), inv = bad || zero ? 1.f : 1.f / sc.y;
           for (int i = 0; i < 8 && u + i < p.u1; ++i) {
             if (!slot_free()) break;
             Meta &m = metas[n_unit % kMetas];
@@ -997,7 +1005,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           const int t0 = window ? p.stored : u * kKeys;
           const int here = min(kKeys, window ? meta.valid : p.stored - t0);  // tokens of the unit
           const float *col = reinterpret_cast<const float *>(smem + SM::COL) + (n_unit % kCols) * 3 * kKeys;
-          const bool edge = window || here < kKeys || t0 + kKeys - 1 > seen_by_all;
+          const bool edge = window || here < kKeys || t0 + kKeys - 1 > seen_by_all || meta.flush;
           const int cmax = min(here, lim - t0 + 1);  // columns below it are seen
           if (window) {
             // each token has its own scales: S becomes z + log2 scale_v in place
@@ -1031,9 +1039,10 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           const bool move = mx > M + kGrow || (M == ninf && mx > ninf);
           if (__any_sync(kAll, move)) {
             const float to = move ? mx : M;
-            const float f = M == ninf ? (move ? 0.f : 1.f) : kvq::fast_exp2(M - to);
+            const float h = M == ninf ? (move ? 0.f : 1.f) : kvq::fast_exp2(0.5f * (M - to));
+            const float f = h * h;
             M = to;
-            l *= f;
+            l = l * h * h;  // (zeros' sums may outlive a factor that fp32 cannot hold)
             if (u > u0) {
               // (given up here, the next wait for S gives up for the whole tile)
               if (!__all_sync(kAll, wait(kOFull + t, (n_own - 1) & 1))) continue;
@@ -1163,9 +1172,10 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
 #pragma unroll
               for (int k = 0; k < 8; ++k) x[k] = __ldcg(src + static_cast<size_t>(k) * kRows);
               const float top = fmaxf(mm, e.x), ref = top == ninf ? 0.f : top;
-              const float was = kvq::fast_exp2(mm - ref), f = kvq::fast_exp2(e.x - ref);
+              const float wh = kvq::fast_exp2(0.5f * (mm - ref)), fh = kvq::fast_exp2(0.5f * (e.x - ref));
+              const float was = wh * wh, f = fh * fh;
               mm = top;
-              ll = fmaf(ll, was, e.y * f);
+              ll = fmaf(ll * wh, wh, e.y * fh * fh);
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
                 o[4 * k] = fmaf(o[4 * k], was, x[k].x * f);

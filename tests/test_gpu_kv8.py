@@ -561,6 +561,30 @@ def test_tiny_values(kv8, fmt):
 
 
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("e", [-60, -40, 0, 70, 90])
+@pytest.mark.parametrize("first", [True, False])
+def test_zero_blocks_beside_small_and_large_values(kv8, fmt, e, first):
+    """bf16 values around 2^e and, before or behind them, blocks whose values are
+    zero, in one CTA's part and in parts that are merged: neither the small
+    values' bits nor the zeros' share of the weights are lost.  (The bound is
+    relative to the values.)"""
+    def scaled(q, k, v):
+        v *= 2.0 ** e
+
+    def zeroed(q, k, v):
+        v[:] = 0
+
+    for long in (0, 4000):
+        r = Run(kv8, 1, 1, 1, 128, 32, fmt, "bfloat16", 8448, rot=0)
+        r.append([96 + long], zeroed if first else scaled)
+        r.append([96 + long], scaled if first else zeroed)
+        for steps in ([64], [32], [24, 8]):  # the tile kernel, up to sixteen rows at once, up to eight
+            for new in steps:
+                r.append([new], scaled)
+            r.attend()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
 def test_long_context_precision(kv8, fmt):
     """Over a long context of independent values the sums nearly cancel, and the
     elements' bound says little.  Each weight is off by at most 2^-11 of itself,
