@@ -25,7 +25,9 @@
 // per row brings into fp16's range: a rounding only of elements 2^-29 below
 // the row's largest.  Window tokens in bf16 are multiplied as they are (mma in
 // bf16), so that no token's size touches another's; their weights go in as a
-// bf16 part and the bf16 remainder, 2^-17 of themselves off.
+// bf16 part and the bf16 remainder, 2^-17 of themselves off.  Their weights have
+// no scale in the exponent, but in m they count like a block's of their size, or
+// the weights of blocks with small values would leave fp16's range beside them.
 //
 // The units of all (sequence, KV head, 16-row tile) triples form one line,
 // cut into one equal range per CTA whatever the sequences' lengths.  The four
@@ -209,6 +211,23 @@ __device__ __forceinline__ uint32_t finite_max(uint32_t m, uint32_t w, uint32_t 
   const uint32_t lo = w & 0x7fffu, hi = (w >> 16) & 0x7fffu;
   m = max(m, lo < limit ? lo : 0u);
   return max(m, hi < limit ? hi : 0u);
+}
+
+// The larger of each half of two words over the eight lanes with the same q4,
+// which hold all channels of a token between them.
+__device__ __forceinline__ void all_channels(uint32_t &a, uint32_t &b) {
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) {
+    a = __vmaxu2(a, __shfl_xor_sync(kAll, a, o));
+    b = __vmaxu2(b, __shfl_xor_sync(kAll, b, o));
+  }
+}
+
+// What a bf16 window token whose largest value has these bits adds to its score
+// in the maximum: log2 of the scale that a block of such values would have, but
+// no more than 0, nor less than kZeroLog.
+__device__ __forceinline__ float value_log(uint32_t bits) {
+  return static_cast<float>(min(max(static_cast<int>(bits >> 7) - 133, static_cast<int>(kZeroLog)), 0));
 }
 
 // Work of one sequence: its units per (KV head, row tile) pair, and pairs.
@@ -505,7 +524,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
       // Row g of a tile is token g ^ 4 (g & 1), row g + 8 the same behind 8.
       const int tok0 = g ^ ((g & 1) << 2);
       auto softmax = [&](auto nb, float (*sc)[4], const float (&ka)[2], const float (&kb)[2], float inv, bool none,
-                         int t0, bool window, uint32_t bad) {
+                         int t0, bool window, uint32_t bad, const float *off) {
         constexpr int NB = decltype(nb)::value;
         float mx[2] = {m[0], m[1]};
 #pragma unroll
@@ -527,7 +546,9 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
 #pragma unroll
-          for (int t = 0; t < NB; ++t) mx[r] = fmaxf(fmaxf(mx[r], sc[t][r]), sc[t][r + 2]);
+          for (int t = 0; t < NB; ++t)
+            mx[r] = off ? fmaxf(fmaxf(mx[r], sc[t][r] + off[0]), sc[t][r + 2] + off[1])
+                        : fmaxf(fmaxf(mx[r], sc[t][r]), sc[t][r + 2]);
           mx[r] = fmaxf(mx[r], __shfl_xor_sync(kAll, mx[r], 4));
           mx[r] = fmaxf(mx[r], __shfl_xor_sync(kAll, mx[r], 8));
           mx[r] = fmaxf(mx[r], __shfl_xor_sync(kAll, mx[r], 16));
@@ -604,7 +625,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
             kb[r] = FMT == KV8_INT8 ? fmaf(-r128[r], f, lv) : lv;
           }
           softmax(std::integral_constant<int, 2>{}, sc, ka, kb, __fdividef(1.f, vs), none, u * kUnit, false,
-                  bad ? kAll : 0u);
+                  bad ? kAll : 0u, nullptr);
           uint32_t p[2][2];  // weights as B fragments of the two k-steps
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
@@ -668,12 +689,12 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
               }
             }
           constexpr int VW = D / 16;  // words of the lane's channels per token (2 channels each)
-          uint32_t v[4][VW];
+          uint32_t v[4][VW], mag[4];  // mag: the largest magnitude of the lane's channels
           uint32_t bad = 0;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int row = 8 * (i >> 1) + ((i & 1) ? ((2 * q4 + 1) ^ 4) : 2 * q4);
-            uint32_t any = 0;
+            uint32_t big = 0;
 #pragma unroll
             for (int k = 0; k < VW / 4; ++k) {
               const uint4 x = lds16(vt + row * 2 * D + (((g * (VW / 4) + k) ^ (row & 7)) << 4));
@@ -681,14 +702,25 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
                 v[i][4 * k + c] = e[c];
-                any |= __vcmpgeu2(e[c] & 0x7fff7fffu, nonfinite_bits<BF16>() * 0x10001u);
+                big = __vmaxu2(big, e[c] & 0x7fff7fffu);
               }
             }
-            if (any) bad |= 1u << row;
+            mag[i] = max(big & 0xffffu, big >> 16);
+            if (mag[i] >= nonfinite_bits<BF16>()) bad |= 1u << row;
           }
           bad = __reduce_or_sync(kAll, bad);
           const float zero[2] = {0.f, 0.f};
-          softmax(std::integral_constant<int, 1>{}, sc, rf, zero, 1.f, false, w.full * kUnit + t0, true, bad);
+          float off[2];  // of tokens tok0 and tok0 + 8, which lanes with q4 = g / 2 have read
+          if (BF16) {
+            uint32_t lo = mag[0] | mag[1] << 16, hi = mag[2] | mag[3] << 16;
+            all_channels(lo, hi);
+            lo = __shfl_sync(kAll, lo, g >> 1);
+            hi = __shfl_sync(kAll, hi, g >> 1);
+            off[0] = value_log(g & 1 ? lo >> 16 : lo & 0xffffu);
+            off[1] = value_log(g & 1 ? hi >> 16 : hi & 0xffffu);
+          }
+          softmax(std::integral_constant<int, 1>{}, sc, rf, zero, 1.f, false, w.full * kUnit + t0, true, bad,
+                  BF16 ? off : nullptr);
           if (bad) {  // their weights are NaN where they are seen, and 0 elsewhere
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -883,7 +915,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
       // t0; column 2 q4 of a tile is token 2 q4, column 2 q4 + 1 token (2 q4 + 1) ^ 4.
       // z = s a + b for the two rows; `bad`: tokens that turn what sees them to NaN.
       auto softmax = [&](auto nb, float (*sc)[4], const float (&ka)[2], const float (&kb)[2], float inv, bool none,
-                         int t0, bool window, uint32_t bad) {
+                         int t0, bool window, uint32_t bad, const float *off) {
         constexpr int NB = decltype(nb)::value;
         float mx[2] = {m[0], m[1]};
 #pragma unroll
@@ -905,7 +937,9 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
 #pragma unroll
         for (int t = 0; t < NB; ++t)
 #pragma unroll
-          for (int i = 0; i < 4; i += 2) mx[i >> 1] = fmaxf(fmaxf(mx[i >> 1], sc[t][i]), sc[t][i + 1]);
+          for (int i = 0; i < 4; i += 2)
+            mx[i >> 1] = off ? fmaxf(fmaxf(mx[i >> 1], sc[t][i] + off[2 * t]), sc[t][i + 1] + off[2 * t + 1])
+                             : fmaxf(fmaxf(mx[i >> 1], sc[t][i]), sc[t][i + 1]);
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           mx[r] = fmaxf(mx[r], __shfl_xor_sync(kAll, mx[r], 1));
@@ -999,7 +1033,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
             kb[r] = FMT == KV8_INT8 ? fmaf(-q128[r], f, lv) : lv;
           }
           softmax(std::integral_constant<int, 4>{}, sc, ka, kb, __fdividef(1.f, vs), none, u * kUnit, false,
-                  bad ? kAll : 0u);
+                  bad ? kAll : 0u, nullptr);
           uint32_t p[2][4];
           weights(p[0], sc[0], sc[1]);
           weights(p[1], sc[2], sc[3]);
@@ -1076,12 +1110,12 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
             }
           }
           constexpr int VW = D / 16;  // words of the lane's channels per token (2 channels each)
-          uint32_t v[4][VW];
+          uint32_t v[4][VW], mag[4];  // mag: the largest magnitude of the lane's channels
           uint32_t bad = 0;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int row = 8 * (i >> 1) + ((i & 1) ? ((2 * q4 + 1) ^ 4) : 2 * q4);
-            uint32_t any = 0;
+            uint32_t big = 0;
 #pragma unroll
             for (int k = 0; k < VW / 4; ++k) {
               const uint4 x = lds16(vt + row * 2 * D + (((g * (VW / 4) + k) ^ (row & 7)) << 4));
@@ -1089,14 +1123,25 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
                 v[i][4 * k + c] = e[c];
-                any |= __vcmpgeu2(e[c] & 0x7fff7fffu, nonfinite_bits<BF16>() * 0x10001u);
+                big = __vmaxu2(big, e[c] & 0x7fff7fffu);
               }
             }
-            if (any) bad |= 1u << row;
+            mag[i] = max(big & 0xffffu, big >> 16);
+            if (mag[i] >= nonfinite_bits<BF16>()) bad |= 1u << row;
           }
           bad = __reduce_or_sync(kAll, bad);
           const float zero[2] = {0.f, 0.f};
-          softmax(std::integral_constant<int, 2>{}, sc, qf, zero, 1.f, false, w.full * kUnit + t0, true, bad);
+          float off[4];  // of the tokens of v
+          if (BF16) {
+            uint32_t lo = mag[0] | mag[1] << 16, hi = mag[2] | mag[3] << 16;
+            all_channels(lo, hi);
+            off[0] = value_log(lo & 0xffffu);
+            off[1] = value_log(lo >> 16);
+            off[2] = value_log(hi & 0xffffu);
+            off[3] = value_log(hi >> 16);
+          }
+          softmax(std::integral_constant<int, 2>{}, sc, qf, zero, 1.f, false, w.full * kUnit + t0, true, bad,
+                  BF16 ? off : nullptr);
           uint32_t p[4], rest[4];
           if (BF16) {
 #pragma unroll

@@ -78,7 +78,7 @@ struct Smem {
   static constexpr int V = K + 2 * TILE;          // two stages
   static constexpr int META = V + 2 * TILE;       // [kMetas] Meta
   static constexpr int PART = META + kMetas * 128;  // [kParts] Part
-  static constexpr int COL = PART + kParts * 64;  // [kCols] window columns: scale_k, log2 scale_v, 1 / scale_v
+  static constexpr int COL = PART + kParts * 64;  // [kCols] window columns: scale_k, log2 scale_v, - log2 scale_v or 0
   static constexpr int ROW = COL + kCols * 3 * kKeys * 4;  // per row: maxima of both halves, two units; exponents, sums
   static constexpr int BAR = ROW + 6 * kRows * 4;
   static constexpr int MISC = BAR + 48 * 8;
@@ -849,8 +849,9 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
         }
       }
       // a power of two that brings the largest element to [2^14, 2^15); elements
-      // below 2^-67 count as that, so that sums of f times weights stay finite
-      if (BF16 && big) f = __int_as_float((268 - max(static_cast<int>(big >> 7), 60)) << 23);
+      // below 2^-67, zeros too, count as that, so that sums of f times weights
+      // stay finite
+      if (BF16) f = __int_as_float((268 - max(static_cast<int>(big >> 7), 60)) << 23);
     };
     auto store_window = [&](uint32_t dst, const uint16_t *src, bool zero, float f) {
 #pragma unroll 4
@@ -895,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
         col[0] = 1.f / kf;
         // tokens that are not finite turn the rows that see them to NaN
         col[kKeys] = kbad || vbad ? nan : -log2f(vf);
-        col[2 * kKeys] = kbad || vbad ? 1.f : vf;
+        col[2 * kKeys] = kbad || vbad ? 0.f : log2f(vf);
       }
       kvq::fence_proxy_async();
       kvq::mbar_arrive(bars + kKFull + st);
@@ -1067,7 +1068,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
               wait_ld16(z);
 #pragma unroll
               for (int i = 0; i < 16; ++i)
-                l = fmaf(c + i < cmax ? kvq::fast_exp2(__uint_as_float(z[i]) - ref) : 0.f, col[2 * kKeys + c + i], l);
+                l += c + i < cmax ? kvq::fast_exp2(__uint_as_float(z[i]) - ref + col[2 * kKeys + c + i]) : 0.f;
             }
           }
           // ---- weights

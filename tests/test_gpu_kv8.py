@@ -585,6 +585,29 @@ def test_zero_blocks_beside_small_and_large_values(kv8, fmt, e, first):
 
 
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("e", [-60, -40, 0, 70, 90])
+def test_windows_of_zero_small_and_large_values(kv8, fmt, e):
+    """The same where the window holds such tokens, zeros among them, and where
+    hidden tokens of the window are far larger."""
+    def scaled(q, k, v):
+        v *= 2.0 ** e
+        v[1::3] = 0
+
+    def last_large(q, k, v):
+        scaled(q, k, v)
+        v[-1] *= 2.0 ** (95 - max(e, 0) - 6)
+
+    for long in (0, 4000):
+        for change in (scaled, last_large):
+            r = Run(kv8, 1, 1, 1, 128, 64, fmt, "bfloat16", 8448, rot=0)
+            r.append([96 + long], scaled)
+            for new in (63, 15, 3):  # the tile kernel, up to sixteen rows at once, up to eight
+                r.append([new], change)
+                r.attend()
+                r.append([64 + 30 - (new + 30) % 64], scaled)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
 def test_long_context_precision(kv8, fmt):
     """Over a long context of independent values the sums nearly cancel, and the
     elements' bound says little.  Each weight is off by at most 2^-11 of itself,
