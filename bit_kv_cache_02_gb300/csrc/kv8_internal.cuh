@@ -109,6 +109,14 @@ cudaError_t launch_append(const Geo &geo, const Rows &k, const Rows &v, const Ro
 constexpr float kZeroScale = 8.27180613e-25f;
 constexpr float kZeroLog = -80.f;
 
+// What a row's weighted sum is multiplied by, `last` being the last position that
+// the row sees: 0 where it sees no token.  Where it sees some the weights' sum is
+// above 0, but for scores that are all -infinity, as an infinite query can make
+// them: NaN.
+__device__ __forceinline__ float inverse_sum(float sum, int last) {
+  return sum != 0.f ? 1.f / sum : last < 0 ? 0.f : __int_as_float(0x7fc00000);
+}
+
 // CTAs of one attention launch at most (sizes the workspace's partial slots).
 constexpr int kMaxCtas = 640;
 constexpr int kRowTile = 16;  // (token, query head) rows that share one pass over the keys

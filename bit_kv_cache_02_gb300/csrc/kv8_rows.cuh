@@ -817,7 +817,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
         const int ch = (D / 8) * g + 2 * QT * warp, row = r0 + 2 * q4 + r;
         if (row < n_rows) {
           if (whole) {
-            const float inv = ll == 0.f ? 0.f : 1.f / ll;
+            const float inv = inverse_sum(ll, lim[r]);
             const int tok = row / a.group;
             uint16_t *dst = a.out.p + (static_cast<long long>(w.q.row0) + tok) * a.out.row +
                             (static_cast<long long>(use.h) * a.group + row - tok * a.group) * a.out.head + ch;
@@ -1244,7 +1244,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
         const int row = r0 + g + 8 * r;
         if (row < n_rows) {
           if (whole) {
-            const float inv = ll == 0.f ? 0.f : 1.f / ll;
+            const float inv = inverse_sum(ll, lim[r]);
             const int tok = row / a.group;
             uint16_t *dst = a.out.p + (static_cast<long long>(w.q.row0) + tok) * a.out.row +
                             (static_cast<long long>(use.h) * a.group + row - tok * a.group) * a.out.head;
@@ -1329,8 +1329,8 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
 #pragma unroll
         for (int k = 0; k < NR; ++k) {
           if (warp + kWarps * k >= rows) break;
-          const float inv = ll[k] == 0.f ? 0.f : 1.f / ll[k];
           const int tok = (r0 + row[k]) / a.group;
+          const float inv = inverse_sum(ll[k], w.q.L - w.q.n + tok);
           uint16_t *dst = a.out.p + (static_cast<long long>(w.q.row0) + tok) * a.out.row +
                           (static_cast<long long>(use.h) * a.group + r0 + row[k] - tok * a.group) * a.out.head + lane * W;
 #pragma unroll

@@ -1117,7 +1117,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       }
       if (active && ok) {
         fence_after();
-        const float inv = 1.f / l;
+        const float inv = inverse_sum(l, lim);
 #pragma unroll 1
         for (int c = hf * (D / 64); c < (hf + 1) * (D / 64); ++c) {
           uint32_t o[32];
@@ -1127,7 +1127,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
             float x[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) x[i] = l == 0.f ? 0.f : __uint_as_float(o[i]);
-            put(c, x, l == 0.f ? 0.f : inv);
+            put(c, x, inv);
           } else {
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
@@ -1185,7 +1185,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
                 o[4 * k + 3] = fmaf(o[4 * k + 3], was, x[k].w * f);
               }
             }
-            put(c, o, ll == 0.f ? 0.f : 1.f / ll);
+            put(c, o, inverse_sum(ll, lim));
           }
           store_rows();
         }

@@ -198,6 +198,8 @@ int64_t kv8_attn_workspace_bytes(const kv8_cache *cache, int32_t num_q_heads,
  * decreases.  Rows that belong to no sequence are left as they are.  A token
  * with a NaN or an infinity in its keys or values makes the rows that see it
  * NaN (through a whole block once the block is quantized), and no other row.
+ * A query with a NaN or an infinity makes its own row NaN (zeros where the row
+ * sees no token).
  * A block of values whose scale is below 2^-80 counts as zeros, and in bf16
  * results may overflow where a window token's keys or values are above 2^100 in
  * magnitude.  Results do not depend on timing: the same call gives the same

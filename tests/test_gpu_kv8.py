@@ -395,6 +395,30 @@ def test_nonfinite_tokens(kv8, dtype, where, value, g):
         assert not np.isnan(out[:first]).any()
 
 
+@pytest.mark.parametrize("fmt,dtype", TYPES)
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+def test_nonfinite_queries(kv8, fmt, dtype, value):
+    """A query with a NaN or an infinity gives NaN in its own row and head (zeros
+    where it sees no token), also where it makes every score -infinity."""
+    def change(q, k, v):
+        k[:, :, 3] = 1 + np.abs(k[:, :, 3])  # an infinite channel has one sign for all tokens
+
+    for ctx, new in ((70, 1), (70, 12), (64, 70), (5000, 1), (5000, 100)):
+        r = Run(kv8, 1, 2, 3, 128, 64, fmt, dtype, 5200, rot=0)
+        r.append([ctx], change)
+        r.append([new], change)
+        q = r.q.copy()
+        q[new // 2, 1, 3] = q[0, 4, 3] = value
+        out = _host(r.attend(q=q))  # the oracle's NaN are those two heads
+        assert np.isnan(out[new // 2, 1]).all() and np.isnan(out[0, 4]).all() and np.isnan(out).sum() == 2 * 128
+    r = Run(kv8, 1, 1, 3, 64, 32, fmt, dtype, 100)
+    r.append([5])
+    q = r.numbers((30, 3, 64))
+    q[3, 1, 3] = value
+    out = _host(r.attend(np.array([0, 30]), q))
+    assert (out[3] == 0).all() and not np.isnan(out).any()
+
+
 @pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
 def test_large_scores_and_spread_scales(kv8, dtype):
     """Scores in the hundreds, blocks whose scales differ by 2^20, window
