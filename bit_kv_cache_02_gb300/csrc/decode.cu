@@ -95,6 +95,8 @@ int set_wait_test(long long cycles, int wait_before_fetch) {
   return 0;
 }
 
+WaitTest wait_test() { return {g_wait_limit ? g_wait_limit : kWaitLimitCycles, g_wait_before_fetch}; }
+
 cudaError_t launch_plan(const DecodeArgs &a, cudaStream_t stream) {
   decode_plan_kernel<<<1, 1024, 0, stream>>>(a);
   return cudaGetLastError();
@@ -150,8 +152,9 @@ cudaError_t launch_decode(const Geo &geo, int Hq, const __half *q, float softmax
   a.pass_slot0 = p.pass_slot0;
   a.tail_passes = p.tail_passes;
   a.max_len = max_len;
-  a.wait_limit = g_wait_limit ? g_wait_limit : kWaitLimitCycles;
-  a.wait_before_fetch = g_wait_before_fetch;
+  const WaitTest wt = wait_test();
+  a.wait_limit = wt.limit;
+  a.wait_before_fetch = wt.before_fetch;
   a.n_slots = p.pass_slot0 + static_cast<size_t>(geo.S) * geo.H * p.tail_passes;
   a.n_base = p.n_base;
   a.rope_base = reinterpret_cast<const float2 *>(ws + p.off_rope);

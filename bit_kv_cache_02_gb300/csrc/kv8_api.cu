@@ -187,6 +187,9 @@ int kv8_attn(const kv8_cache *cache, int32_t num_q_heads, const kv8_rows *q, con
   a.tile_o = reinterpret_cast<float *>(ws + plan.off_tile_o);
   a.tile_ml = reinterpret_cast<float2 *>(ws + plan.off_tile_ml);
   a.rows_max = plan.tiles ? kv8::kRowsMax : 2147483647;
+  const kvq::WaitTest wt = kvq::wait_test();
+  a.wait_limit = wt.limit;
+  a.wait_test = wt.before_fetch;
   uint64_t n = 0;
   const cudaError_t ce = kv8::launch_attn(a, plan.tiles, static_cast<cudaStream_t>(stream), &n);
   return from_cuda(ce, n);

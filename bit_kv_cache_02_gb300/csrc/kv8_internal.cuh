@@ -156,6 +156,8 @@ struct AttnArgs {
   float2 *tile_ml;    // [2 kMaxTileCtas][256] (reference, sum)
   int *tile_counters; // [kMaxTileCtas], zero on entry, left zero on exit
   int rows_max;       // rows per KV head up to which the rows kernel takes a sequence
+  long long wait_limit;  // SM cycles that a wait of the tile kernel may last before it gives up
+  int wait_test;         // test aid: a wait of the tile kernel that nothing completes
 };
 
 cudaError_t launch_attn(const AttnArgs &a, bool tiles, cudaStream_t stream, uint64_t *launches);

@@ -583,6 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
   Part *const parts = reinterpret_cast<Part *>(smem + SM::PART);
   Meta *const metas = reinterpret_cast<Meta *>(smem + SM::META);
   // A wait of a role; false ends the role (another one's wait ran out, or this).
+  // A limit below a poll's 100 us holds to within that.
   // The polls suspend the warp for long: what it issues is missing to others
   // (a chunk of 2048 tokens over 8192: 229 against 243 us with short polls).
   auto wait = [&](int bar, uint32_t parity) -> bool {
@@ -590,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
     const long long since = clock64();
     while (!kvq::mbar_try_wait_hint(bars + bar, parity, 100000u)) {
       if (*dead) return false;
-      if (clock64() - since > kvq::kWaitLimitCycles) {
+      if (clock64() - since > a.wait_limit) {
         *dead = 1;
         set_status(geo.status, KVQ_STATUS_TIMEOUT);
         return false;
@@ -881,6 +882,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       float vf = 1.f;
       bool vzero = true;
       if (n_unit >= 2 && !wait_all(kKEmpty + st, reuse, first, 1, 128, true)) break;
+      // test aid: the second unit's keys wait for what only a give-up brings about
+      if (n_unit == 1 && a.wait_test && !wait_all(kDrained, 0, first, 1, 128, true)) break;
       if (kind == kPacked) {
         store(kd, kb);
       } else {

@@ -282,8 +282,14 @@ int decode_attn_clearing(const kvq_cache *cache, int32_t num_q_heads, const uint
 int set_decode_warps(int warps);
 // Adds to what kvq_launch_count reports.
 void count_launches(uint64_t n);
-// Test aid: cycle limit of the decode kernel's pipeline waits (0: the
-// default) and whether each warp's first wait comes before its first copy.
+// Test aid: cycle limit of the pipeline waits of the decode kernel and of the
+// 8-bit cache's tile kernel (0: the default), and whether each has a wait that
+// nothing completes.
 int set_wait_test(long long cycles, int wait_before_fetch);
+struct WaitTest {
+  long long limit;
+  int before_fetch;
+};
+WaitTest wait_test();
 
 }  // namespace kvq

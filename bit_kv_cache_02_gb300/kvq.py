@@ -237,7 +237,8 @@ def set_decode_warps(warps: int):
 
 
 def set_wait_test(limit_cycles: int, wait_before_fetch: bool = False):
-    """Test aid for the decode kernel's bounded waits: their cycle limit (0:
-    the default of about two seconds) and whether each warp's first wait
-    comes before its first copy (so that it runs out)."""
+    """Test aid for the bounded waits of the decode kernel and of kv8_attn's
+    kernel for many rows: their cycle limit (0: the default of about two
+    seconds) and whether there is one that nothing completes (so that it runs
+    out)."""
     _check(lib.kvq_set_wait_test(int(limit_cycles), int(bool(wait_before_fetch))), "kvq_set_wait_test")

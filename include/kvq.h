@@ -336,7 +336,8 @@ uint64_t kvq_launch_count(void);
  * KVQ_ERR_INVALID_ARG. */
 int kvq_set_decode_warps(int32_t warps);
 
-/* Test aid (not on the pages) for the bounded waits of the decode kernel.
+/* Test aid (not on the pages) for the bounded waits of the decode kernel and
+ * of kv8_attn's kernel for many rows (kv8.h).
  * limit_cycles: SM clock cycles a pipeline wait may last before it gives up,
  * records KVQ_STATUS_TIMEOUT, lets its own copies in flight land (those
  * waits keep the default bound) and ends its warp's work; 0 restores the
@@ -344,8 +345,10 @@ int kvq_set_decode_warps(int32_t warps);
  * each warp's first wait come before its first copy is issued, on a barrier
  * that nothing completes, so that it runs out: this is how tests exercise the
  * timeout path without a fault (in normal operation every copy of a valid
- * block lands).  It needs limit_cycles > 0.  Affects kv_decode_attn calls made
- * afterwards in this process.  Returns KVQ_OK, or KVQ_ERR_INVALID_ARG for a
+ * block lands).  In kv8_attn it is the keys of each CTA's second 128 tokens that
+ * wait so, with the first tokens' products and weights under way.  It needs
+ * limit_cycles > 0.  Affects kv_decode_attn and kv8_attn calls made afterwards
+ * in this process.  Returns KVQ_OK, or KVQ_ERR_INVALID_ARG for a
  * limit that is negative or above the default, or a bad flag. */
 int kvq_set_wait_test(int64_t limit_cycles, int32_t wait_before_fetch);
 

@@ -715,6 +715,31 @@ def test_falling_row_start(kv8):
     assert (out[150:] == 5.0).all()
 
 
+def test_wait_that_runs_out(kv8):
+    """The tile kernel's waits are bounded.  Here the keys of each CTA's second
+    unit wait, with a limit of 20000 SM cycles, for a barrier that nothing
+    completes: all roles leave, the products under way drain, tensor memory is
+    given back, the status says so and the device stays usable.  On a workspace
+    that is zero again the same call is right."""
+    from bit_kv_cache_02_gb300 import kvq
+    for D, ctx, new in ((128, [5000, 100], [200, 1]), (64, [0, 700], [300, 90])):
+        r = Run(kv8, 2, 2, 2, D, 64, "int8", "bfloat16", 5400, rot=0)
+        r.append(ctx)
+        r.append(new)
+        ws = kv8.alloc_workspace(r.cache, 4, max(new))
+        try:
+            kvq.set_wait_test(20000, True)
+            for _ in range(3):
+                r.attend(ws=ws, check=False)
+                assert int(r.cache.status.item()) == kvq.KVQ_STATUS_TIMEOUT
+                r.cache.status.zero_()
+        finally:
+            kvq.set_wait_test(0, False)
+        ws.zero_()
+        r.attend(ws=ws)
+        assert int(r.cache.status.item()) == 0
+
+
 # -------------------------------------------------------- streams and graphs
 
 def test_two_streams_at_once(kv8):
