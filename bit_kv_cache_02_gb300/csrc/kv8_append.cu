@@ -164,6 +164,7 @@ __device__ __forceinline__ void rotate_queries(const AppendArgs &a, int cta) {
   if (s >= a.geo.S) return;
   const Seq sq = load_seq(a.geo, a.row_start, a.rows, a.max_new, s);
   if (!sq.ok || row < sq.row0 || row >= sq.row0 + sq.n || sq.L < sq.n || sq.L > a.geo.capacity) return;
+  if (!KVQ_IN_BOUNDS(a.geo.status, sq.L - sq.n + row - sq.row0, a.geo.capacity)) return;
   const bool turns = pi < (a.rot >> 4);
   Turn t;
   if (turns) t = load_turn(pi, sq.L - sq.n + row - sq.row0, a);
@@ -233,6 +234,7 @@ __global__ void __launch_bounds__(T, NI == 4 ? 3 : 1024 / T) append_kernel(const
   const int L = sq.L, old = L - sq.n, first = old / B, done = L / B - first;
   if (t < 0 || t >= max(done, 1)) return;
   const int p0 = (first + t) * B;  // position of the block's slot 0
+  if (t < done && !KVQ_IN_BOUNDS(geo.status, first + t, geo.max_blocks)) return;
   const int blk = t < done ? geo.table[static_cast<size_t>(s) * geo.max_blocks + first + t] : -1;
   const int from = max(old, L / B * B);  // first new token that stays in the window
   const int items = B * PAIRS;
@@ -256,7 +258,7 @@ __global__ void __launch_bounds__(T, NI == 4 ? 3 : 1024 / T) append_kernel(const
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
           const int it = tid + i * T, slot = it / PAIRS, p = p0 + slot;
-          if (it < items) {
+          if (it < items && (p < old || KVQ_IN_BOUNDS(geo.status, sq.row0 + p - old, a.rows))) {
             const uint16_t *src = p < old ? win + (static_cast<size_t>(h) * B + slot) * D
                                           : fresh + p * rows.row + h * rows.head;
             x[i] = load16(src);
@@ -267,7 +269,8 @@ __global__ void __launch_bounds__(T, NI == 4 ? 3 : 1024 / T) append_kernel(const
         for (int i = 0; i < NI; ++i) {
           const int it = tid + i * T, p = p0 + it / PAIRS;
           if (it < items) {
-            if (turns && p >= old) rotate<BF16>(x[i], y[i], load_turn(tid % PAIRS, p, a), a.interleaved);
+            if (turns && p >= old && KVQ_IN_BOUNDS(geo.status, p, geo.capacity))
+              rotate<BF16>(x[i], y[i], load_turn(tid % PAIRS, p, a), a.interleaved);
             m = mag_max(mag_max(m, x[i]), y[i]);
           }
         }
@@ -301,6 +304,7 @@ __global__ void __launch_bounds__(T, NI == 4 ? 3 : 1024 / T) append_kernel(const
       // else those behind the last complete block
       for (int it = tid; it < (L - from) * PAIRS; it += T) {
         const int p = from + it / PAIRS, slot = p & (B - 1);
+        if (!KVQ_IN_BOUNDS(geo.status, sq.row0 + p - old, a.rows) || !KVQ_IN_BOUNDS(geo.status, p, geo.capacity)) continue;
         const uint16_t *src = fresh + p * rows.row + h * rows.head;
         uint4 x = load16(src), y = load16(src + apart);
         if (turns) rotate<BF16>(x, y, load_turn(tid % PAIRS, p, a), a.interleaved);

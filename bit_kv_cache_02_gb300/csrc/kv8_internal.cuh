@@ -160,6 +160,12 @@ struct AttnArgs {
   int wait_test;         // test aid: a wait of the tile kernel that nothing completes
 };
 
+// Debug builds: the tensors' row and head of a KV head's row are in range.
+__device__ __forceinline__ bool row_in_bounds(const AttnArgs &a, const Seq &q, int h, int row) {
+  return KVQ_IN_BOUNDS(a.geo.status, static_cast<long long>(q.row0) + row / a.group, a.rows) &&
+         KVQ_IN_BOUNDS(a.geo.status, static_cast<long long>(h) * a.group + row % a.group, a.Hq);
+}
+
 cudaError_t launch_attn(const AttnArgs &a, bool tiles, cudaStream_t stream, uint64_t *launches);
 // the kernels for one head dimension (one translation unit each)
 cudaError_t launch_rows_128(const AttnArgs &a, cudaStream_t stream);

@@ -392,6 +392,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
   };
   auto table_entry = [&]() -> int {
     if (!more || gu >= get.w.full) return 0;
+    if (!KVQ_IN_BOUNDS(geo.status, gu >> ushift, geo.max_blocks) || !KVQ_IN_BOUNDS(geo.status, get.s, geo.S)) return -1;
     return geo.table[static_cast<size_t>(get.s) * geo.max_blocks + (gu >> ushift)];
   };
   settle();
@@ -430,6 +431,9 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
           const uint32_t off = row * 2 * D + ((col ^ (row & 7)) << 4);
           // slots past the sequence's end are not read: zeros
           const size_t src = (row0 + (row < r ? row : 0)) * D + col * 8;
+          if (!KVQ_IN_BOUNDS(geo.status, t0 + (row < r ? row : 0), B) ||
+              !KVQ_IN_BOUNDS(geo.status, static_cast<long long>(get.s) * H + get.h, static_cast<long long>(geo.S) * H))
+            continue;
           cp16z(kdst + off, geo.k_win + src, row < r);
           cp16z(vdst + off, geo.v_win + src, row < r);
         }
@@ -463,7 +467,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
       int lim[2];                         // last position they see
       {
         const int row = r0 + g;
-        const bool valid = row < n_rows;
+        const bool valid = row < n_rows && row_in_bounds(a, w.q, use.h, row);
         const int tok = valid ? row / a.group : 0;
         const uint16_t *src =
             a.q.p + (static_cast<long long>(w.q.row0) + tok) * a.q.row +
@@ -815,7 +819,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
           }
         // m-tile j holds channels (D / 8) g + 2 j and the next one
         const int ch = (D / 8) * g + 2 * QT * warp, row = r0 + 2 * q4 + r;
-        if (row < n_rows) {
+        if (row < n_rows && row_in_bounds(a, w.q, use.h, row) && KVQ_IN_BOUNDS(geo.status, part, 2 * kMaxCtas)) {
           if (whole) {
             const float inv = inverse_sum(ll, lim[r]);
             const int tok = row / a.group;
@@ -842,7 +846,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int row = r0 + g + 8 * r;
-        const bool valid = row < n_rows;
+        const bool valid = row < n_rows && row_in_bounds(a, w.q, use.h, row);
         const int tok = valid ? row / a.group : 0;
         lim[r] = valid ? w.q.L - w.q.n + tok : -1;
         const uint16_t *src = a.q.p + (static_cast<long long>(w.q.row0) + tok) * a.q.row +
@@ -1242,7 +1246,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
         // n-tile j, column c holds channel (D / 8) c + j
         const int ch0 = (D / 8) * (2 * q4) + warp * QT, ch1 = ch0 + D / 8;
         const int row = r0 + g + 8 * r;
-        if (row < n_rows) {
+        if (row < n_rows && row_in_bounds(a, w.q, use.h, row) && KVQ_IN_BOUNDS(geo.status, part, 2 * kMaxCtas)) {
           if (whole) {
             const float inv = inverse_sum(ll, lim[r]);
             const int tok = row / a.group;
@@ -1277,8 +1281,8 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
       if (tid == 0) {
         // releases the CTA's stores, which the barrier has ordered before, and
         // acquires the others' for the reads behind the next barrier
-        const int before = kvq::atom_add_acq_rel(a.counters + c0, 1);
-        const bool last = before == c1 - c0;
+        const bool counted = KVQ_IN_BOUNDS(geo.status, c0, kMaxCtas) && KVQ_IN_BOUNDS(geo.status, c1, kMaxCtas);
+        const bool last = counted && kvq::atom_add_acq_rel(a.counters + c0, 1) == c1 - c0;
         if (last) a.counters[c0] = 0;
         *flag = last;
       }
@@ -1328,7 +1332,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
         }
 #pragma unroll
         for (int k = 0; k < NR; ++k) {
-          if (warp + kWarps * k >= rows) break;
+          if (warp + kWarps * k >= rows || !row_in_bounds(a, w.q, use.h, r0 + row[k])) break;
           const int tok = (r0 + row[k]) / a.group;
           const float inv = inverse_sum(ll[k], w.q.L - w.q.n + tok);
           uint16_t *dst = a.out.p + (static_cast<long long>(w.q.row0) + tok) * a.out.row +

@@ -300,10 +300,11 @@ __device__ __forceinline__ Pair make_pair(const AttnArgs &a, int s, int rt) {
   Pair p;
   p.s = s;
   p.rt = rt;
+  p.units = 0;
+  if (!KVQ_IN_BOUNDS(a.geo.status, s, a.geo.S)) return p;
   p.q = load_seq(a.geo, a.row_start, a.rows, a.max_new, s);
   const int L = p.q.L;
   const int n_rows = p.q.n * a.group;
-  p.units = 0;
   if (n_rows <= kRowsMax || L <= 0 || L > a.max_len || rt < 0 || rt * kRows >= n_rows) return p;
   const int last_row = min((rt + 1) * kRows, n_rows) - 1;
   p.last_seen = max(L - p.q.n + last_row / a.group, 0);
@@ -753,7 +754,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           bool none = true;
           float2 sc = make_float2(1.f, 1.f);
           if (mu < min(p.packed, p.u1) && tok < p.stored) {
-            const int e = geo.table[static_cast<size_t>(p.s) * geo.max_blocks + tok / B];
+            const bool listed = KVQ_IN_BOUNDS(geo.status, p.s, geo.S) && KVQ_IN_BOUNDS(geo.status, tok / B, geo.max_blocks);
+            const int e = listed ? geo.table[static_cast<size_t>(p.s) * geo.max_blocks + tok / B] : -1;
             if (e >= 0 && e < geo.num_blocks) {
               const long long bh = static_cast<long long>(e) * H + p.h;
               off = bh * 2 * B * D + (tok & (B - 1)) * D;
@@ -815,6 +817,9 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       const uint8_t *src = codes + values * B * D;
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
+        if (!KVQ_IN_BOUNDS(geo.status, m.off[i / CH] + (values * B + cr) * D + cc * 16 + (i % CH) * 64,
+                           static_cast<long long>(geo.num_blocks) * H * 2 * B * D - 15))
+          continue;
         buf[i] = __ldg(reinterpret_cast<const uint4 *>(src + m.off[i / CH] + (i % CH) * 64));
       }
     };
@@ -889,7 +894,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       } else {
         float *col = reinterpret_cast<float *>(smem + SM::COL) + (n_unit % kCols) * 3 * kKeys + ct;
         const uint16_t *ks = geo.k_win + m.win + ct * D, *vs = geo.v_win + m.win + ct * D;
-        const bool valid = ct < m.valid;
+        const bool valid = ct < m.valid && KVQ_IN_BOUNDS(geo.status, ct, B) &&
+                           KVQ_IN_BOUNDS(geo.status, m.win / (B * D), static_cast<long long>(geo.S) * H);
         float kf;
         bool kbad, vbad;
         window_row(ks, valid, kf, kbad);
@@ -964,7 +970,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
 
       // ---- the warp's 32 queries to shared memory: LPR lanes bring a row
       const long long head = static_cast<long long>(p.h) * a.group + some - tok * a.group;
-      const long long q_off = (static_cast<long long>(p.row0) + tok) * a.q.row + head * a.q.head;
+      const bool inside = row_in_bounds(a, Seq{p.L, p.n, p.row0, true}, p.h, some);
+      const long long q_off = inside ? (static_cast<long long>(p.row0) + tok) * a.q.row + head * a.q.head : 0;
       float qf = a.zscale;
       if (active) {
         const uint32_t dst = base + SM::Q + t * SM::TILE;
@@ -1092,7 +1099,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       const bool whole = slot < 0;
       float4 *part = reinterpret_cast<float4 *>(a.tile_o) + static_cast<size_t>(max(slot, 0)) * (D / 4) * kRows +
                      t * 128 + r;
-      const long long out_off = valid ? (static_cast<long long>(p.row0) + tok) * a.out.row + head * a.out.head : -1;
+      const long long out_off = valid && inside ? (static_cast<long long>(p.row0) + tok) * a.out.row + head * a.out.head : -1;
       // Outputs go through the queries' place, which the products are done
       // with, so that whole rows are stored: 32 channels of the thread's row
       // from channel 32 c on, then the warp's rows.
@@ -1118,7 +1125,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
         ok = wait_all(kOFull + t, (n_own - 1) & 1, (warp & 7) == 0 && end > u0, 3 + t, 256, ok);
         l += sums[(hf ^ 1) * kRows];
       }
-      if (active && ok) {
+      if (active && ok && (whole || KVQ_IN_BOUNDS(geo.status, slot, 2 * kMaxTileCtas))) {
         fence_after();
         const float inv = inverse_sum(l, lim);
 #pragma unroll 1
@@ -1152,7 +1159,10 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
         if (tid == 0) {
           // releases the CTA's stores, which the barrier has ordered before, and
           // acquires the others' for the reads behind the next barrier
-          const bool last = kvq::atom_add_acq_rel(a.tile_counters + p.c0, 1) == p.cuts;
+          const bool counted = KVQ_IN_BOUNDS(geo.status, p.c0, kMaxTileCtas) &&
+                               KVQ_IN_BOUNDS(geo.status, p.c0 + p.cuts, kMaxTileCtas) &&
+                               KVQ_IN_BOUNDS(geo.status, p.first, 2 * kMaxTileCtas);
+          const bool last = counted && kvq::atom_add_acq_rel(a.tile_counters + p.c0, 1) == p.cuts;
           if (last) a.tile_counters[p.c0] = 0;
           *flag = last;
         }
