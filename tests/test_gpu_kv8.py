@@ -155,6 +155,20 @@ def test_append_bit_exact(kv8, fmt, dtype, D, B):
     assert sum(n // B for n in r.orc.lengths()) >= 6
 
 
+@pytest.mark.parametrize("S,H,D,B,fmt,dtype,n", [(3, 11, 64, 32, "int8", "float16", 8300), (2, 9, 128, 32, "e4m3", "bfloat16", 14700),
+                                                 (3, 9, 128, 32, "int8", "bfloat16", 2900)])
+def test_append_long_prompts(kv8, S, H, D, B, fmt, dtype, n):
+    """The forms of the append for many blocks: keys and values by CTAs of their
+    own and, from 8192 blocks x heads on, eight heads per CTA, the last ones
+    fewer; behind stored tokens, once more behind the result."""
+    r = Run(kv8, S, H, 1, D, B, fmt, dtype, n + 2 * B + 400, seed=n)
+    r.append([B - 3, 0, 7][:S])
+    r.append([n - 211 * s for s in range(S)])
+    r.check_state()
+    r.append([B + 1] * S)
+    r.check_state()
+
+
 @pytest.mark.parametrize("rot,interleaved", [(0, False), (16, False), (48, True), (64, True), (96, False), (128, True)])
 def test_append_rotations(kv8, rot, interleaved):
     r = Run(kv8, 3, 1, 2, 128, 32, "int8", "bfloat16", 200, seed=rot, rot=rot, interleaved=interleaved)
@@ -333,6 +347,17 @@ def test_chunk_layouts(kv8):
         ws = kv8.alloc_workspace(r.cache, H * g, max(new))
         a = r.attend(ws=ws)
         assert torch.equal(a, r.attend(ws=ws, check=False)), "a repeated call gave another result"
+
+
+def test_many_chunks_at_once(kv8):
+    """More sequences with rows for the tile kernel than it has threads to look
+    them up at once, empty ones among them."""
+    S = 700
+    r = Run(kv8, S, 1, 49, 64, 32, "int8", "float16", 100, seed=9)
+    r.append([(37 * s) % 70 for s in range(S)])
+    r.append([(1, 1, 0, 1, 6)[s % 5] for s in range(S)])
+    assert r.start_host[-1] * 49 // 256 + S > 768
+    r.attend()
 
 
 @pytest.mark.parametrize("D", [64, 128])
@@ -551,6 +576,21 @@ def test_shared_blocks(kv8):
     r.append([3, 1])
     r.attend()
     assert x.shape[0] == 64
+
+
+def test_blocks_behind_a_changed_table(kv8):
+    """A sequence whose table is changed to another's blocks sees those, and
+    nothing of the blocks that it had, whatever is in them now."""
+    for new in (1, 30):  # few rows, the other kernel
+        r = Run(kv8, 2, 1, 2, 128, 32, "int8", "float16", 160, rot=0)
+        r.append([64, 64])
+        own = r.cache.block_table[1, :2].long()
+        r.cache.block_table[1, :2] = r.cache.block_table[0, :2]
+        r.cache.codes[own] = 99
+        r.cache.scales[own] = math.nan
+        r.orc.k[1], r.orc.v[1] = r.orc.k[0].copy(), r.orc.v[0].copy()
+        r.append([3, new])
+        r.attend()
 
 
 @pytest.mark.parametrize("H,g", [(1, 49), (2, 72), (1, 300)])
