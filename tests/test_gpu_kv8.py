@@ -5,6 +5,9 @@ type.  Steps are run as a serving loop runs them: raise seq_len, append,
 attend."""
 
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -14,6 +17,7 @@ from oracle import kv8 as ok
 
 pytestmark = pytest.mark.gpu
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 HALF_STEP = {"float16": 2.0 ** -11, "bfloat16": 2.0 ** -8}
 TINY = {"float16": 2.0 ** -25, "bfloat16": 2.0 ** -134}  # half a step of subnormals
 
@@ -593,6 +597,19 @@ def test_blocks_behind_a_changed_table(kv8):
         r.attend()
 
 
+def test_capacity_below_a_block(kv8):
+    """A cache whose tokens never fill a block needs no pool."""
+    for new in (1, 25):
+        r = Run(kv8, 2, 2, 3, 64, 128, "int8", "bfloat16", 90, spare=3)
+        assert r.cache.max_blocks == 0
+        for name in ("codes", "scales", "block_table"):
+            setattr(r.cache.struct, name, None)
+        r.append([40, 0])
+        r.append([new, 20])
+        r.attend()
+        assert int(r.cache.status.item()) == 0
+
+
 @pytest.mark.parametrize("H,g", [(1, 49), (2, 72), (1, 300)])
 def test_token_many_query_heads(kv8, H, g):
     """Query groups so large that a single token's rows take the other kernel."""
@@ -835,6 +852,34 @@ def test_other_stream_and_graph(kv8):
         kv8.kv8_attn(r.cache, q_out, o2, ws, 100, stream=side)
     side.synchronize()
     assert torch.equal(o2, out)
+
+
+def test_first_calls_of_a_process_are_captured(kv8):
+    """Nothing has to run before a capture: append and attention, both kernels,
+    as a new process's first calls."""
+    code = """
+import torch
+from bit_kv_cache_02_gb300 import kv8
+c = kv8.KV8Cache(2, 2, 600, 18, head_dim=128, block=64, fmt="e4m3", dtype=torch.bfloat16)
+c.block_table.copy_(torch.arange(18).view(2, 9))
+x = torch.randn(301, 8, 128, device="cuda").bfloat16()
+q, out, eager = (torch.zeros(301, 4, 128, device="cuda", dtype=torch.bfloat16) for _ in range(3))
+start = torch.tensor([0, 300, 301], dtype=torch.int32, device="cuda")
+ws, rope = kv8.alloc_workspace(c, 4, 300), kv8.rope_table(600, 128)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    c.seq_len += start[1:] - start[:-1]
+    kv8.kv8_append(c, x[:, 4:6], x[:, 6:], row_start=start, max_new=300, q=x[:, :4], q_out=q, rope=rope)
+    kv8.kv8_attn(c, q, out, ws, 600, row_start=start, max_new=300)
+g.replay()
+kv8.kv8_attn(c, q, eager, ws, 600, row_start=start, max_new=300)
+torch.cuda.synchronize()
+assert c.seq_len.tolist() == [300, 1] and int(c.status.item()) == 0
+assert torch.equal(out, eager) and bool((out != 0).any(-1).all())
+print("captured first")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stdout[-500:] + r.stderr[-2000:]
 
 
 def test_serving_loop(kv8):
