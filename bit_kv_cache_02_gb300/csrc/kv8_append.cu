@@ -15,7 +15,7 @@
 // Bound: HBM for prompts (2 bytes read and 1 written per key or value element,
 // 4 per query element): 16 sequences x 4096 tokens x 32 + 2 x 8 heads x 128
 // take 467 us, 5.8 TB/s.  A single token per sequence is a launch and four
-// dependent loads: 2.5 us.
+// dependent loads: 2.6 us.
 #include <cuda_fp8.h>
 
 #include "kv8_internal.cuh"
@@ -365,6 +365,13 @@ cudaError_t launch_append(const Geo &geo, const Rows &k, const Rows &v, const Ro
   // first-level cache for seven of them.  With few, a head's keys and values
   // share a CTA: less to start (ragged chunks of 356 blocks 18.5 against 20.0
   // us, a decode step of 64 x 8 heads 4.2 against 5.6).
+  // Around the borders (int8 bf16, D 128, block 64, 8 x 4 heads; one head per CTA
+  // with keys and values together, one apart, eight): blocks x heads of 544:
+  // 17.0, 18.2, 31.7 us; 1056: 33.9, 35.7, 43.9; 2080: 64.6, 68.0, 60.1; 4160:
+  // 127, 136, 119; 8320: not timed, 274, 234.  One token each for 256 sequences,
+  // 2048: 10.3, 13.1, 6.1.  So eight heads pay from 2048 on, where keys and values
+  // apart by themselves do not: between the borders this rule is 12% off, in that
+  // decode step twofold.
   const long long blocks = a.slots ? a.slots : geo.S;
   a.split = blocks * geo.H >= 2048;
   a.heads = blocks * geo.H >= 8192 && rot_dim ? 8 : 1;

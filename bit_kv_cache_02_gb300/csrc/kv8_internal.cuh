@@ -125,7 +125,10 @@ constexpr int kRowTile = 16;  // (token, query head) rows that share one pass ov
 // rows kernel reads the keys once for 16 rows, the tile kernel once for 256
 // after a longer start.  Rows against tile kernel, int8, D 128, 16 sequences x 8
 // KV heads x 4000 tokens: 54 and 89 us at 32 rows, 95 and 90 at 64, 177 and 86
-// at 128; 32 x 32 x 2000 tokens at 48 rows: 284 and 267.
+// at 128; 32 x 32 x 2000 tokens at 48 rows: 284 and 267.  Rows alone do not
+// decide: with one sequence of 30,000 tokens x 8 heads, which gives the tile
+// kernel few items to fill the SMs with, the border lies higher (34 and 70 us at
+// 32 rows, 49 and 66 at 64, 91 and 69 at 128).
 constexpr int kRowsMax = 48;
 constexpr int kTileRows = 256;      // rows of an item of the tile kernel
 constexpr int kMaxTileCtas = 160;

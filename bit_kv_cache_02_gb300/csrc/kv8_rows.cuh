@@ -21,7 +21,13 @@
 // what is left.
 //
 // Roundings to 16 bits: w to fp16 (the factor 2^15 keeps weights down to 2^-29
-// of the largest at full precision), and bf16 queries, which a power of two
+// of the largest at full precision).  One part is enough here: a weight's 2^-11
+// is at most what an fp16 output's own rounding adds, and less in the mean (the
+// error against 64 bits grows from 2.1e-4 to 2.4e-4 in fp16, 2.6e-4 over long
+// contexts, and from 1.7e-3 by 0.1e-3 at most in bf16), where the 8-bit tokens
+// are off by 9e-3; a second part would double the products with the values.
+// (The 2/4-bit kernels keep two: there a token's scale multiplies its weight.)
+// And bf16 queries, which a power of two
 // per row brings into fp16's range: a rounding only of elements 2^-29 below
 // the row's largest.  Window tokens in bf16 are multiplied as they are (mma in
 // bf16), so that no token's size touches another's; their weights go in as a
@@ -42,7 +48,7 @@
 // 6.0 TB/s; one sequence of 2^20 tokens x 8 heads: 304 us, 7.1 TB/s.  With 12
 // to 32 rows (16 sequences, 2000 to 6000 tokens, 8 heads, 3 to 8 drafts x 4)
 // the keys are read once or twice and the chain of a unit's instructions
-// bounds it, at two warps per scheduler: 43 us; three warps, at 168 registers,
+// bounds it, at two warps per scheduler: 43.5 us; three warps, at 168 registers,
 // were no faster.
 //
 // 16-byte chunks are XOR swizzled by the token so that neither operand's

@@ -30,9 +30,11 @@
 // M with kZeroLog, and their weights, formed without, l alone).  M follows the row's
 // maximum of z + log2(scale_v) lazily: O is rescaled only when it grew by more
 // than 2^6, so w stays below 2^15 and weights down to 2^-23 of the largest
-// keep fp16's full precision.  Roundings: w to fp16; bf16 queries scaled to
-// fp16's range as in the rows kernel; bf16 window tokens scaled token by token
-// (the factors enter z and M like the blocks' scales).
+// keep fp16's full precision.  Roundings: w to fp16, as in the rows kernel; bf16
+// queries scaled to fp16's range as there; bf16 window tokens scaled token by
+// token (the factors enter z and M like the blocks' scales), which the rows
+// kernel need not do: an element 2^-29 below its token's largest loses bits, in
+// all 2^-39 of the largest.
 //
 // The keys of all items form one line of 128-token units, with kOver more for
 // what an item costs by itself, which is cut into one equal range per SM; items
@@ -531,6 +533,11 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
     total = cta_scan(sum, before, scan_buf);
   }
   if (total == 0) return;
+  // Eight line positions per CTA at least.  Long lines, from 1216 on, do not
+  // meet this; short ones would be faster with four (8 KV heads x 4 queries,
+  // D 128: a prompt of 256 tokens 28.9 against 20.6 us, of 512 34.6 against 25.4,
+  // a chunk of 128 over 2000 42.1 against 35.2) and slower with sixteen (47.6,
+  // 49.8, 55.9).
   const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + 7) / 8));
   if (static_cast<int>(blockIdx.x) >= ctas) return;
   const long long lo = divide(blockIdx.x * total, ctas), hi = divide((blockIdx.x + 1) * total, ctas);

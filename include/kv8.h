@@ -1,12 +1,15 @@
 /*
  * kv8.h -- C ABI of the 8-bit paged KV cache (part of libkvq.so, sm_103a).
  *
- * The sibling of the 2/4-bit cache of kvq.h for callers that want nearly
- * 16-bit quality at half the memory: keys and values in 8 bits with one fp32
- * scale per (block of tokens, KV head, keys or values), pages shared by all
- * heads of a sequence, fp16 or bf16 activations, and attention for any number
- * of new tokens per sequence (one while decoding, a few when checking drafts,
- * many in a prompt's chunk).
+ * The sibling of the 2/4-bit cache of kvq.h for callers that want half the
+ * memory of 16 bits: keys and values in 8 bits with one fp32 scale per (block
+ * of tokens, KV head, keys or values), pages shared by all heads of a sequence,
+ * fp16 or bf16 activations, and attention for any number of new tokens per
+ * sequence (one while decoding, a few when checking drafts, many in a prompt's
+ * chunk).  Normal values come back with an error of 0.9% (int8) or 2.7% (e4m3)
+ * of their size, root mean square, and attention over 4096 such tokens with
+ * 1.3% or 3.8%; where four key channels of 128 are six times as large, with 4%
+ * or 8%.
  *
  *   kv8_append  rotates queries and keys to their positions, stores the keys
  *               and values, and quantizes every block that fills.
@@ -200,9 +203,10 @@ int64_t kv8_attn_workspace_bytes(const kv8_cache *cache, int32_t num_q_heads,
  * NaN (through a whole block once the block is quantized), and no other row.
  * A query with a NaN or an infinity makes its own row NaN (zeros where the row
  * sees no token).
- * A block of values whose scale is below 2^-80 counts as zeros, and in bf16
+ * A block of values whose scale is below 2^-80 counts as zeros.  In bf16
  * results may overflow where a window token's keys or values are above 2^100 in
- * magnitude.  Results do not depend on timing: the same call gives the same
+ * magnitude, and a block whose values are not zeros but 2^125 below others that
+ * a row sees may lose its share of the weights.  Results do not depend on timing: the same call gives the same
  * bits.  One or two kernels, which read all lengths on the device: a captured
  * call can be replayed for other lengths within max_len, rows and max_new.
  */
