@@ -34,7 +34,8 @@
 // queries scaled to fp16's range as there; bf16 window tokens scaled token by
 // token (the factors enter z and M like the blocks' scales), which the rows
 // kernel need not do: an element 2^-29 below its token's largest loses bits, in
-// all 2^-39 of the largest.
+// all 2^-39 of the largest, and the token's weight, for its values stand 2^8 above
+// a block's codes, where it is 2^-15 or less of a block's of that size.
 //
 // The keys of all items form one line of 128-token units, with kOver more for
 // what an item costs by itself, which is cut into one equal range per SM; items

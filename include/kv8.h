@@ -203,10 +203,14 @@ int64_t kv8_attn_workspace_bytes(const kv8_cache *cache, int32_t num_q_heads,
  * NaN (through a whole block once the block is quantized), and no other row.
  * A query with a NaN or an infinity makes its own row NaN (zeros where the row
  * sees no token).
- * A block of values whose scale is below 2^-80 counts as zeros.  In bf16
- * results may overflow where a window token's keys or values are above 2^100 in
- * magnitude, and a block whose values are not zeros but 2^125 below others that
- * a row sees may lose its share of the weights.  Results do not depend on timing: the same call gives the same
+ * A block of values whose scale is below 2^-80 counts as zeros.  Weights are
+ * rounded to fp16 relative to the row's largest weight times scale of values:
+ * those 2^23 below it (2^15 for bf16 window tokens beside blocks) lose bits.
+ * That is far below what the tokens' own 8 bits lose, but where values differ
+ * by such factors: a block of large values takes bits of the others even if the
+ * row sees only small ones of it, and in bf16 a block 2^125 below others may
+ * lose its share of the weights.  In bf16 results may overflow where a window
+ * token's keys or values are above 2^100 in magnitude.  Results do not depend on timing: the same call gives the same
  * bits.  One or two kernels, which read all lengths on the device: a captured
  * call can be replayed for other lengths within max_len, rows and max_new.
  */

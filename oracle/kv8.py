@@ -112,17 +112,43 @@ class OracleKV8:
             parts.append(c * scale)
         return np.concatenate(parts + [x[full * self.B:, h]]) if parts else x[:, h]
 
+    def units(self, s, h, rows):
+        """For each token the unit of its values in the products with the
+        weights, and whether its weight is an fp16 number.  Blocks: their
+        scale, 2^-80 where they count as zeros.  The window: fp16 values enter
+        as they are.  bf16 values enter, with more than 48 rows per KV head,
+        times the power of two that brings the token's largest to [2^14, 2^15)
+        (2^81 at most); with fewer as they are, by weights in bf16, and count
+        among the others as a block of their size would, from 2^-80 to 1."""
+        full = len(self.v[s]) // self.B
+        u = [np.zeros(0)]
+        for b in range(full):
+            scale = self.block(s, b, h, True)[1]
+            u.append(np.full(self.B, scale if scale >= 2.0 ** -80 else 2.0 ** -80))
+        win = np.abs(self.v[s][full * self.B:, h])
+        top = np.where(np.isfinite(win), win, 0).max(1, initial=0)
+        e = np.where(top > 0, np.frexp(top)[1], -200)
+        if self.dtype == "float16":
+            u.append(np.ones(len(win)))
+        else:
+            u.append(np.ldexp(1.0, np.maximum(e, -66) - 15 if rows > 48 else np.clip(e - 7, -80, 0)))
+        in_fp16 = np.ones(len(self.v[s]), bool)
+        in_fp16[full * self.B:] = self.dtype == "float16" or rows > 48
+        return np.concatenate(u), in_fp16
+
     def attention(self, q, row_start, softmax_scale=None):
         """q [rows, Hq, D] -> (out, bound): float64 attention, and what the
         kernels' roundings may change it by before the output's own rounding.
 
         The bound.  A weight is rounded to fp16: 2^-11 of itself, or half a
-        step of fp16's subnormals, 2^-25.  The kernels form weights as 2^15 w,
-        or as w scale_v / (the largest of those so far, up to 2^6 more) * 2^9:
-        at least 2^9 of the largest, so the subnormals' part is at most 2^-34
-        of the largest weighted value for each token, 2^-34 seen max|v| in
-        all.  (It matters where the tokens of large weight have zeros in a
-        channel.)  A score is a sum of D products accumulated in fp32 (at most
+        step of fp16's subnormals, 2^-25.  Formed is P = w u / U 2^9 or more,
+        where u is the unit in which a token's values enter the products (see
+        units) and U the largest w u of the row; the sum of P v / u comes back
+        times U 2^-9.  A P below 2^-14, that is a w u below 2^-23 U (2^-22 with
+        what the scores' errors add), is off by 2^-25, its share of the output
+        by 2^-34 U |v| / u.  (It matters where the tokens of large w u have
+        small values in a channel, or none: a block of large values of which
+        the row sees small ones only counts with its scale.)  A score is a sum of D products accumulated in fp32 (at most
         (D + 16) 2^-24 of the sum of magnitudes, the weight's relative change
         being e^x - 1 < 2 x); adding log2(scale_v) and the reference, both
         below 128 but for the score, rounds four times at 2^-24 * 128: 2^-15.
@@ -144,6 +170,7 @@ class OracleKV8:
                 continue
             for h in range(self.H):
                 K, V = self.stored(s, h, False), self.stored(s, h, True)
+                unit, in_fp16 = self.units(s, h, n * g)
                 for i in range(n):
                     seen = L - n + i + 1
                     if seen <= 0:
@@ -164,5 +191,8 @@ class OracleKV8:
                             dz += 2.0 ** -39 * np.abs(x).max() * np.abs(K[:seen]).sum(1).max() * scale
                             dz += 2.0 ** -39 * np.abs(K[:seen]).max() * np.abs(x).sum() * scale
                         rel = 2.0 ** -11 + 2.0 ** -15 + 2 * dz + (2 * seen + 64) * 2.0 ** -24
-                        bound[a + i, j] = rel * (w @ np.abs(V[:seen])) + 2.0 ** -34 * seen * np.abs(V[:seen]).max()
+                        wu = w * unit[:seen]
+                        small = in_fp16[:seen] & (wu < 2.0 ** -22 * wu.max())
+                        lost = (np.abs(V[:seen][small]) / unit[:seen][small][:, None]).sum(0)
+                        bound[a + i, j] = rel * (w @ np.abs(V[:seen])) + 2.0 ** -34 * wu.max() * lost
         return out, bound

@@ -689,6 +689,26 @@ def test_windows_of_zero_small_and_large_values(kv8, fmt, e):
 
 
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("D,B,g", [(128, 32, 1), (64, 64, 3), (128, 64, 9), (64, 32, 20)])
+def test_values_of_all_sizes_side_by_side(kv8, fmt, D, B, g):
+    """bf16 values of 2^-60 to 2^60 by token or by sixteen tokens, zeros among
+    them, so that rows see small tokens of blocks whose hidden ones are large:
+    within the bound, whose subnormals' part counts every token's unit."""
+    for seed, run in ((1, 1), (2, 16)):
+        r = Run(kv8, 3, 2, g, D, B, fmt, "bfloat16", 700, seed=seed, rot=0)
+
+        def change(q, k, v):
+            e = r.rng.integers(-60, 61, len(v) // run + 1).repeat(run)[:len(v)]
+            v *= np.where(r.rng.random(len(v)) < 0.2, 0.0, 2.0 ** e)[:, None, None]
+
+        r.append([2 * B + 5, 0, 300], change)
+        for new in ([70, 1, 100], [3, 1, 8], [1, 1, 1]):
+            r.append(new, change)
+            r.check_state()
+            r.attend()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
 def test_long_context_precision(kv8, fmt):
     """Over a long context of independent values the sums nearly cancel, and the
     elements' bound says little.  Each weight is off by at most 2^-11 of itself,
