@@ -87,6 +87,117 @@ int check_heads(const kv8_cache *c, int32_t num_q_heads, int32_t max_new) {
   return per > 2147483647LL / 2 ? KVQ_ERR_UNSUPPORTED : KVQ_OK;
 }
 
+// Both appends; positions NULL: tokens stand at their places in the cache.
+int append(const kv8_cache *cache, const kv8_rows *k, const kv8_rows *v, const kv8_rows *q, const kv8_rows *q_out,
+           int32_t num_q_heads, const int32_t *row_start, int32_t rows, int32_t max_new, const float *rope,
+           int32_t rope_rows, int32_t rot_dim, int32_t interleaved, const kv8::Axes *axes, void *stream) {
+  int e = check_buffers(cache);
+  if (e) return e;
+  if ((e = check_row_range(cache, row_start, rows, max_new))) return e;
+  const bool with_q = num_q_heads != 0;
+  if (num_q_heads < 0 || with_q != (q != nullptr) || with_q != (q_out != nullptr)) return KVQ_ERR_INVALID_ARG;
+  if (interleaved != 0 && interleaved != 1) return KVQ_ERR_INVALID_ARG;
+  if (rot_dim < 0 || rot_dim > cache->head_dim || rot_dim % 16 != 0) return KVQ_ERR_UNSUPPORTED;
+  if (rot_dim && !rope) return KVQ_ERR_INVALID_ARG;
+  if (!axes && rot_dim && rope_rows < cache->capacity) return KVQ_ERR_CAPACITY;
+  if (!aligned(rope, 16)) return KVQ_ERR_ALIGNMENT;
+  if (rows == 0 || max_new == 0) return KVQ_OK;
+  if ((e = check_rows(k, cache->num_kv_heads, rows, cache->head_dim, false))) return e;
+  if ((e = check_rows(v, cache->num_kv_heads, rows, cache->head_dim, false))) return e;
+  if (with_q) {
+    if ((e = check_rows(q, num_q_heads, rows, cache->head_dim, false))) return e;
+    if ((e = check_rows(q_out, num_q_heads, rows, cache->head_dim, true))) return e;
+    if (q->data == q_out->data && (q->row_stride != q_out->row_stride || q->head_stride != q_out->head_stride))
+      return KVQ_ERR_INVALID_ARG;
+  }
+  const kv8::Rows none = {nullptr, 0, 0};
+  const kv8::Rows qr = with_q ? make_rows(q) : none, os = with_q ? make_rows(q_out) : none;
+  const kv8::Geo geo = make_geo(cache);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint64_t n = 0;
+  const cudaError_t ce =
+      axes ? kv8::launch_append_axes(geo, make_rows(k), make_rows(v), qr, os, num_q_heads, row_start, rows, max_new,
+                                     rope, rot_dim, interleaved, *axes, st, &n)
+           : kv8::launch_append(geo, make_rows(k), make_rows(v), qr, os, num_q_heads, row_start, rows, max_new, rope,
+                                rot_dim, interleaved, st, &n);
+  return from_cuda(ce, n);
+}
+
+// What the attention calls have in common: checks, and the arguments of a launch
+// over the sequences' whole lengths.
+int attn_args(kv8::AttnArgs &a, const kv8_cache *cache, int32_t num_q_heads, const kv8_rows *q, const kv8_rows *out,
+              const int32_t *row_start, int32_t rows, int32_t max_new, float softmax_scale, int32_t max_len) {
+  int e;
+  if (max_new < 1 || max_len < 1) return KVQ_ERR_INVALID_ARG;
+  if ((e = check_heads(cache, num_q_heads, max_new))) return e;
+  if (max_len > cache->capacity) return KVQ_ERR_CAPACITY;
+  if (rows == 0) return KVQ_OK;
+  if ((e = check_rows(q, num_q_heads, rows, cache->head_dim, false))) return e;
+  if ((e = check_rows(out, num_q_heads, rows, cache->head_dim, true))) return e;
+  if (q->data == out->data && (q->row_stride != out->row_stride || q->head_stride != out->head_stride))
+    return KVQ_ERR_INVALID_ARG;
+  if (!(softmax_scale > 0.f) || !isfinite(softmax_scale))
+    softmax_scale = 1.f / sqrtf(static_cast<float>(cache->head_dim));
+  a = kv8::AttnArgs{};
+  a.geo = make_geo(cache);
+  a.Hq = num_q_heads;
+  a.group = num_q_heads / cache->num_kv_heads;
+  a.part = kv8::kWhole;
+  a.causal = 1;
+  a.segs = cache->num_seqs;
+  a.q = make_rows(q);
+  a.out = make_rows(out);
+  a.row_start = row_start;
+  a.rows = rows;
+  a.max_new = max_new;
+  a.max_len = max_len;
+  a.zscale = softmax_scale * 1.4426950408889634f;
+  const kvq::WaitTest wt = kvq::wait_test();
+  a.wait_limit = wt.limit;
+  a.wait_test = wt.before_fetch;
+  return KVQ_OK;
+}
+
+// The regions of one launch's workspace.
+void place(kv8::AttnArgs &a, const kv8::AttnPlan &plan, void *workspace) {
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  a.part_o = reinterpret_cast<float *>(ws + plan.off_o);
+  a.part_ml = reinterpret_cast<float2 *>(ws + plan.off_ml);
+  a.counters = reinterpret_cast<int *>(ws + plan.off_cnt);
+  a.tile_counters = reinterpret_cast<int *>(ws + plan.off_tile_cnt);
+  a.tile_o = reinterpret_cast<float *>(ws + plan.off_tile_o);
+  a.tile_ml = reinterpret_cast<float2 *>(ws + plan.off_tile_ml);
+  a.rows_max = plan.tiles ? kv8::kRowsMax : 2147483647;
+}
+
+int check_workspace(const void *workspace, size_t given, size_t needed) {
+  if (!workspace || given < needed) return KVQ_ERR_WORKSPACE;
+  return aligned(workspace, 256) ? KVQ_OK : KVQ_ERR_ALIGNMENT;
+}
+
+// Attention over whole sequences in one pass.
+int attend(const kv8_cache *cache, int32_t num_q_heads, const kv8_rows *q, const kv8_rows *out,
+           const int32_t *row_start, int32_t rows, int32_t max_new, float softmax_scale, void *workspace,
+           size_t workspace_bytes, int32_t max_len, bool causal, void *stream) {
+  kv8::AttnArgs a;
+  int e = attn_args(a, cache, num_q_heads, q, out, row_start, rows, max_new, softmax_scale, max_len);
+  if (e || rows == 0) return e;
+  const kv8::AttnPlan plan = kv8::plan_attn(cache->head_dim, static_cast<int64_t>(a.group) * max_new);
+  if ((e = check_workspace(workspace, workspace_bytes, plan.bytes))) return e;
+  a.causal = causal;
+  place(a, plan, workspace);
+  uint64_t n = 0;
+  const cudaError_t ce = kv8::launch_attn(a, plan.tiles, static_cast<cudaStream_t>(stream), &n);
+  return from_cuda(ce, n);
+}
+
+// The rows of one segment and the tensors' rows of calls without a bound by the capacity.
+int check_ranges(const kv8_cache *c, const int32_t *row_start, int32_t rows, int32_t max_rows) {
+  if (rows < 0 || max_rows < 0) return KVQ_ERR_INVALID_ARG;
+  if (!aligned(row_start, 4)) return KVQ_ERR_ALIGNMENT;
+  return !row_start && rows < c->num_seqs ? KVQ_ERR_INVALID_ARG : KVQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -114,31 +225,26 @@ int64_t kv8_buffer_bytes(const kv8_cache *c, int32_t which) {
 int kv8_append(const kv8_cache *cache, const kv8_rows *k, const kv8_rows *v, const kv8_rows *q, const kv8_rows *q_out,
                int32_t num_q_heads, const int32_t *row_start, int32_t rows, int32_t max_new, const float *rope,
                int32_t rope_rows, int32_t rot_dim, int32_t interleaved, void *stream) {
-  int e = check_buffers(cache);
-  if (e) return e;
-  if ((e = check_row_range(cache, row_start, rows, max_new))) return e;
-  const bool with_q = num_q_heads != 0;
-  if (num_q_heads < 0 || with_q != (q != nullptr) || with_q != (q_out != nullptr)) return KVQ_ERR_INVALID_ARG;
-  if (interleaved != 0 && interleaved != 1) return KVQ_ERR_INVALID_ARG;
-  if (rot_dim < 0 || rot_dim > cache->head_dim || rot_dim % 16 != 0) return KVQ_ERR_UNSUPPORTED;
-  if (rot_dim && !rope) return KVQ_ERR_INVALID_ARG;
-  if (rot_dim && rope_rows < cache->capacity) return KVQ_ERR_CAPACITY;
-  if (!aligned(rope, 16)) return KVQ_ERR_ALIGNMENT;
-  if (rows == 0 || max_new == 0) return KVQ_OK;
-  if ((e = check_rows(k, cache->num_kv_heads, rows, cache->head_dim, false))) return e;
-  if ((e = check_rows(v, cache->num_kv_heads, rows, cache->head_dim, false))) return e;
-  if (with_q) {
-    if ((e = check_rows(q, num_q_heads, rows, cache->head_dim, false))) return e;
-    if ((e = check_rows(q_out, num_q_heads, rows, cache->head_dim, true))) return e;
-    if (q->data == q_out->data && (q->row_stride != q_out->row_stride || q->head_stride != q_out->head_stride))
-      return KVQ_ERR_INVALID_ARG;
+  return append(cache, k, v, q, q_out, num_q_heads, row_start, rows, max_new, rope, rope_rows, rot_dim, interleaved,
+                nullptr, stream);
+}
+
+int kv8_append_axes(const kv8_cache *cache, const kv8_rows *k, const kv8_rows *v, const kv8_rows *q,
+                    const kv8_rows *q_out, int32_t num_q_heads, const int32_t *row_start, int32_t rows,
+                    int32_t max_new, const float *rope, int32_t rope_rows, int32_t rot_dim, int32_t interleaved,
+                    const int32_t *positions, int64_t axis_stride, int32_t num_axes, const uint8_t *axis_of_pair,
+                    void *stream) {
+  if (num_axes < 1 || num_axes > KV8_MAX_AXES || rot_dim % 16 != 0 || rot_dim > 128) return KVQ_ERR_UNSUPPORTED;
+  if (rot_dim < 16 || rope_rows < 1 || !axis_of_pair) return KVQ_ERR_INVALID_ARG;
+  if (rows > 0 && (!positions || (num_axes > 1 && axis_stride < rows))) return KVQ_ERR_INVALID_ARG;
+  if (!aligned(positions, 4)) return KVQ_ERR_ALIGNMENT;
+  kv8::Axes axes = {positions, num_axes > 1 ? axis_stride : 0, rope_rows, {0, 0, 0, 0}};
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    if (axis_of_pair[i] >= num_axes) return KVQ_ERR_INVALID_ARG;
+    axes.map[i / 16] |= static_cast<uint32_t>(axis_of_pair[i]) << (2 * (i % 16));
   }
-  const kv8::Rows none = {nullptr, 0, 0};
-  uint64_t n = 0;
-  const cudaError_t ce = kv8::launch_append(make_geo(cache), make_rows(k), make_rows(v), with_q ? make_rows(q) : none,
-                                            with_q ? make_rows(q_out) : none, num_q_heads, row_start, rows, max_new,
-                                            rope, rot_dim, interleaved, static_cast<cudaStream_t>(stream), &n);
-  return from_cuda(ce, n);
+  return append(cache, k, v, q, q_out, num_q_heads, row_start, rows, max_new, rope, rope_rows, rot_dim, interleaved,
+                &axes, stream);
 }
 
 int64_t kv8_attn_workspace_bytes(const kv8_cache *cache, int32_t num_q_heads, int32_t max_new) {
@@ -154,44 +260,74 @@ int kv8_attn(const kv8_cache *cache, int32_t num_q_heads, const kv8_rows *q, con
   int e = check_buffers(cache);
   if (e) return e;
   if ((e = check_row_range(cache, row_start, rows, max_new))) return e;
-  if (max_new < 1 || max_len < 1) return KVQ_ERR_INVALID_ARG;
-  if ((e = check_heads(cache, num_q_heads, max_new))) return e;
-  if (max_len > cache->capacity) return KVQ_ERR_CAPACITY;
-  if (rows == 0) return KVQ_OK;
-  if ((e = check_rows(q, num_q_heads, rows, cache->head_dim, false))) return e;
-  if ((e = check_rows(out, num_q_heads, rows, cache->head_dim, true))) return e;
-  if (q->data == out->data && (q->row_stride != out->row_stride || q->head_stride != out->head_stride))
-    return KVQ_ERR_INVALID_ARG;
+  return attend(cache, num_q_heads, q, out, row_start, rows, max_new, softmax_scale, workspace, workspace_bytes,
+                max_len, true, stream);
+}
+
+int64_t kv8_cross_attn_workspace_bytes(const kv8_cache *cache, int32_t num_q_heads, int32_t max_rows) {
+  if (check_geometry(cache) || max_rows < 1 || check_heads(cache, num_q_heads, max_rows)) return -1;
   const int64_t group = num_q_heads / cache->num_kv_heads;
-  const kv8::AttnPlan plan = kv8::plan_attn(cache->head_dim, group * max_new);
-  if (!workspace || workspace_bytes < plan.bytes) return KVQ_ERR_WORKSPACE;
-  if (!aligned(workspace, 256)) return KVQ_ERR_ALIGNMENT;
-  if (!(softmax_scale > 0.f) || !isfinite(softmax_scale))
-    softmax_scale = 1.f / sqrtf(static_cast<float>(cache->head_dim));
+  return static_cast<int64_t>(kv8::plan_attn(cache->head_dim, group * max_rows).bytes);
+}
+
+int kv8_cross_attn(const kv8_cache *cache, int32_t num_q_heads, const kv8_rows *q, const kv8_rows *out,
+                   const int32_t *row_start, int32_t rows, int32_t max_rows, float softmax_scale, void *workspace,
+                   size_t workspace_bytes, int32_t max_len, void *stream) {
+  int e = check_buffers(cache);
+  if (e) return e;
+  if ((e = check_ranges(cache, row_start, rows, max_rows))) return e;
+  return attend(cache, num_q_heads, q, out, row_start, rows, max_rows, softmax_scale, workspace, workspace_bytes,
+                max_len, false, stream);
+}
+
+int64_t kv8_shared_attn_workspace_bytes(const kv8_cache *cache, int32_t num_q_heads, int32_t rows, int32_t max_new,
+                                        int32_t max_group_rows) {
+  if (check_geometry(cache) || rows < 0 || max_new < 1 || max_new > cache->capacity || max_group_rows < 1 ||
+      check_heads(cache, num_q_heads, max_new) || check_heads(cache, num_q_heads, max_group_rows))
+    return -1;
+  return static_cast<int64_t>(kv8::plan_shared(cache->head_dim, num_q_heads / cache->num_kv_heads, num_q_heads, rows,
+                                               max_new, max_group_rows)
+                                  .bytes);
+}
+
+int kv8_shared_attn(const kv8_cache *cache, int32_t num_q_heads, const kv8_rows *q, const kv8_rows *out,
+                    const int32_t *row_start, int32_t rows, int32_t max_new, const int32_t *group_start,
+                    const int32_t *prefix_len, int32_t num_groups, int32_t max_group_rows, float softmax_scale,
+                    void *workspace, size_t workspace_bytes, int32_t max_len, void *stream) {
+  int e = check_buffers(cache);
+  if (e) return e;
+  if ((e = check_row_range(cache, row_start, rows, max_new))) return e;
+  if (num_groups < 1 || max_group_rows < 1 || !group_start || !prefix_len) return KVQ_ERR_INVALID_ARG;
+  if (num_groups > KV8_MAX_GROUPS) return KVQ_ERR_UNSUPPORTED;
+  if (!aligned(group_start, 4) || !aligned(prefix_len, 4)) return KVQ_ERR_ALIGNMENT;
   kv8::AttnArgs a;
-  a.geo = make_geo(cache);
-  a.Hq = num_q_heads;
-  a.group = static_cast<int>(group);
-  a.q = make_rows(q);
-  a.out = make_rows(out);
-  a.row_start = row_start;
-  a.rows = rows;
-  a.max_new = max_new;
-  a.max_len = max_len;
-  a.zscale = softmax_scale * 1.4426950408889634f;
+  if ((e = attn_args(a, cache, num_q_heads, q, out, row_start, rows, max_new, softmax_scale, max_len))) return e;
+  if ((e = check_heads(cache, num_q_heads, max_group_rows))) return e;
+  if (rows == 0) return KVQ_OK;
+  const int64_t group = a.group;
+  const kv8::SharedPlan plan = kv8::plan_shared(cache->head_dim, a.group, num_q_heads, rows, max_new, max_group_rows);
+  if ((e = check_workspace(workspace, workspace_bytes, plan.bytes))) return e;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
-  a.part_o = reinterpret_cast<float *>(ws + plan.off_o);
-  a.part_ml = reinterpret_cast<float2 *>(ws + plan.off_ml);
-  a.counters = reinterpret_cast<int *>(ws + plan.off_cnt);
-  a.tile_counters = reinterpret_cast<int *>(ws + plan.off_tile_cnt);
-  a.tile_o = reinterpret_cast<float *>(ws + plan.off_tile_o);
-  a.tile_ml = reinterpret_cast<float2 *>(ws + plan.off_tile_ml);
-  a.rows_max = plan.tiles ? kv8::kRowsMax : 2147483647;
-  const kvq::WaitTest wt = kvq::wait_test();
-  a.wait_limit = wt.limit;
-  a.wait_test = wt.before_fetch;
+  a.group_start = group_start;
+  a.prefix_len = prefix_len;
+  a.groups = num_groups;
+  a.max_group_rows = max_group_rows;
+  a.carry_ml = reinterpret_cast<float2 *>(ws + plan.off_ml);
+  a.carry_o = reinterpret_cast<float *>(ws + plan.off_o);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint64_t n = 0;
-  const cudaError_t ce = kv8::launch_attn(a, plan.tiles, static_cast<cudaStream_t>(stream), &n);
+  a.part = kv8::kPrefix;
+  a.causal = 0;
+  a.segs = num_groups;
+  place(a, kv8::plan_attn(cache->head_dim, group * max_group_rows), workspace);
+  cudaError_t ce = kv8::launch_attn(a, plan.prefix_tiles, st, &n);
+  if (ce == cudaSuccess) {
+    a.part = kv8::kOwn;
+    a.causal = 1;
+    a.segs = cache->num_seqs;
+    place(a, kv8::plan_attn(cache->head_dim, group * max_new), workspace);
+    ce = kv8::launch_attn(a, plan.own_tiles, st, &n);
+  }
   return from_cuda(ce, n);
 }
 
@@ -215,12 +351,27 @@ AttnPlan plan_attn(int D, long long rows_per_head) {
   return p;
 }
 
+SharedPlan plan_shared(int D, int group, int num_q_heads, long long rows, long long max_new, long long max_group_rows) {
+  SharedPlan p;
+  const AttnPlan own = plan_attn(D, group * max_new), prefix = plan_attn(D, group * max_group_rows);
+  p.own_tiles = own.tiles;
+  p.prefix_tiles = prefix.tiles;
+  p.off_ml = own.bytes > prefix.bytes ? own.bytes : prefix.bytes;
+  const size_t n = static_cast<size_t>(rows) * num_q_heads;
+  p.off_o = p.off_ml + (n * sizeof(float2) + 255) / 256 * 256;
+  p.bytes = p.off_o + (n * D * sizeof(float) + 255) / 256 * 256;
+  return p;
+}
+
 cudaError_t launch_attn(const AttnArgs &a, bool tiles, cudaStream_t stream, uint64_t *launches) {
+  const bool wide = a.geo.D == 128, shared = a.part != kWhole;
   ++*launches;
-  cudaError_t e = a.geo.D == 128 ? launch_rows_128(a, stream) : launch_rows_64(a, stream);
+  cudaError_t e = shared ? (wide ? launch_rows_128_shared(a, stream) : launch_rows_64_shared(a, stream))
+                         : (wide ? launch_rows_128(a, stream) : launch_rows_64(a, stream));
   if (e != cudaSuccess || !tiles) return e;
   ++*launches;
-  return a.geo.D == 128 ? launch_tiles_128(a, stream) : launch_tiles_64(a, stream);
+  return shared ? (wide ? launch_tiles_128_shared(a, stream) : launch_tiles_64_shared(a, stream))
+                : (wide ? launch_tiles_128(a, stream) : launch_tiles_64(a, stream));
 }
 
 }  // namespace kv8

@@ -97,9 +97,21 @@ __host__ __device__ constexpr uint32_t nonfinite_bits() {
 
 // ------------------------------------------------------- host-side launchers
 
+// Positions of each row on several axes, and the axis that each pair of channels
+// turns by: two bits per pair.
+struct Axes {
+  const int *positions;  // [axes][stride]
+  long long stride;
+  int table_rows;
+  uint32_t map[4];
+};
+
 cudaError_t launch_append(const Geo &geo, const Rows &k, const Rows &v, const Rows &q, const Rows &q_out, int Hq,
                           const int *row_start, int rows, int max_new, const float *rope, int rot_dim,
                           int interleaved, cudaStream_t stream, uint64_t *launches);
+cudaError_t launch_append_axes(const Geo &geo, const Rows &k, const Rows &v, const Rows &q, const Rows &q_out, int Hq,
+                               const int *row_start, int rows, int max_new, const float *rope, int rot_dim,
+                               int interleaved, const Axes &axes, cudaStream_t stream, uint64_t *launches);
 
 // Attention counts the values of a block whose scale is smaller (2^-80) as
 // zeros: 1 / scale times the weights of 2^31 tokens stays finite.  Weights are
@@ -145,9 +157,31 @@ struct AttnPlan {
 };
 AttnPlan plan_attn(int D, long long rows_per_head);
 
+// Attention with shared blocks: the two launches follow each other on the same
+// regions, and the partial results that one leaves for the other lie behind them.
+struct SharedPlan {
+  size_t off_ml, off_o, bytes;
+  bool own_tiles, prefix_tiles;
+};
+SharedPlan plan_shared(int D, int group, int num_q_heads, long long rows, long long max_new, long long max_group_rows);
+
+// What one launch attends to, segment by segment.
+enum {
+  kWhole,   // sequences: their whole length
+  kPrefix,  // groups of sequences: the blocks that they share, for the rows of all; leaves partial results
+  kOwn,     // sequences: what lies behind the blocks shared with their group; joins the partial results
+};
+
 struct AttnArgs {
   Geo geo;
   int Hq, group;
+  int part;    // kWhole, kPrefix or kOwn
+  int causal;  // 1: a row sees up to its own position, 0: all of its segment
+  int segs;    // segments: sequences or groups
+  const int *group_start, *prefix_len;  // [groups + 1], [groups]; with kPrefix and kOwn
+  int groups, max_group_rows;
+  float *carry_o;    // [rows][Hq][D]: unnormalized outputs over the shared blocks
+  float2 *carry_ml;  // [rows][Hq]: (max, sum) in log2 units
   Rows q, out;
   const int *row_start;
   int rows, max_new, max_len;
@@ -163,9 +197,104 @@ struct AttnArgs {
   int wait_test;         // test aid: a wait of the tile kernel that nothing completes
 };
 
+// A segment: its tokens and rows.  A sequence whose row range is invalid has
+// no rows and is not ok, as are all of a group whose shared blocks or rows are invalid.
+struct Seg {
+  int L, n, row0;  // tokens behind `base`; rows, and the first one
+  int base;        // blocks in front, which another launch has seen
+  int entry;       // the sequence whose blocks these are
+  bool ok;
+};
+
+// A group's first sequence, its shared blocks and its rows.  Not ok: bad bounds,
+// more rows than announced, or a first sequence whose stored tokens end within them.
+struct Group {
+  int first, blocks, row0, n;
+  bool ok;
+};
+__device__ __forceinline__ Group load_group(const AttnArgs &a, int g) {
+  Group x;
+  x.first = a.group_start[g];
+  const int end = a.group_start[g + 1], prefix = a.prefix_len[g];
+  x.ok = x.first >= 0 && end >= x.first && end <= a.geo.S && prefix >= 0 && prefix <= a.max_len;
+  x.blocks = x.row0 = x.n = 0;
+  if (!x.ok || end == x.first) return x;
+  int r0 = x.first, r1 = end, own = r0 + 1;
+  if (a.row_start) {
+    r0 = a.row_start[r0];
+    r1 = a.row_start[r1];
+    own = a.row_start[own];
+  }
+  x.blocks = prefix / a.geo.B;
+  x.ok = r0 >= 0 && r1 >= r0 && r1 <= a.rows && r1 - r0 <= a.max_group_rows && own >= r0 && own <= r1 &&
+         (x.blocks == 0 || a.geo.seq_len[x.first] - (own - r0) >= x.blocks * a.geo.B);
+  x.row0 = r0;
+  x.n = x.ok ? r1 - r0 : 0;
+  return x;
+}
+
+// SHARED: a launch over shared blocks, or over what lies behind them (kernels of
+// their own: what they keep besides cost the others registers).
+template <bool SHARED>
+__device__ __forceinline__ Seg load_seg(const AttnArgs &a, int s) {
+  Seg x;
+  x.base = 0;
+  if (SHARED && a.part == kPrefix) {
+    const Group g = load_group(a, s);
+    x.ok = g.ok;
+    x.L = g.blocks * a.geo.B;
+    x.n = x.L ? g.n : 0;
+    x.row0 = g.row0;
+    x.entry = g.ok ? g.first : 0;
+    return x;
+  }
+  const Seq q = load_seq(a.geo, a.row_start, a.rows, a.max_new, s);
+  x.L = q.L;
+  x.n = q.n;
+  x.row0 = q.row0;
+  x.entry = s;
+  x.ok = q.ok;
+  if (SHARED && a.part == kOwn && q.n > 0 && q.L <= a.max_len) {
+    const int g = last_at_or_below(a.groups, s, [&](int i) { return a.group_start[i]; });
+    if (a.group_start[g] <= s && s < a.group_start[g + 1]) {
+      const Group of = load_group(a, g);
+      if (!of.ok || (of.blocks && q.L - q.n < of.blocks * a.geo.B)) {
+        x.ok = false;
+        x.n = 0;
+      } else {
+        x.base = of.blocks;
+        x.L -= of.blocks * a.geo.B;
+      }
+    }
+  }
+  return x;
+}
+
+// The last position of the segment that rows of its new token `tok` see.
+template <typename T>
+__device__ __forceinline__ int last_seen(const AttnArgs &a, const T &q, int tok) {
+  return a.causal ? q.L - q.n + tok : q.L - 1;
+}
+
+// The place of a (row, query head) among the partial results.
+__device__ __forceinline__ size_t carry_at(const AttnArgs &a, int row, int head) {
+  return static_cast<size_t>(row) * a.Hq + head;
+}
+
+// The factors that join two partial results (max, sum), and what their weighted
+// sum is divided by: out = o x + other y over z.
+struct Join {
+  float x, y, sum;
+};
+__device__ __forceinline__ Join join(float2 own, float2 other) {
+  const float top = fmaxf(own.x, other.x), base = top == __int_as_float(0xff800000) ? 0.f : top;
+  const float h = kvq::fast_exp2(0.5f * (own.x - base)), k = kvq::fast_exp2(0.5f * (other.x - base));
+  return {h * h, k * k, fmaf(own.y * h, h, other.y * k * k)};
+}
+
 // Debug builds: the tensors' row and head of a KV head's row are in range.
-__device__ __forceinline__ bool row_in_bounds(const AttnArgs &a, const Seq &q, int h, int row) {
-  return KVQ_IN_BOUNDS(a.geo.status, static_cast<long long>(q.row0) + row / a.group, a.rows) &&
+__device__ __forceinline__ bool row_in_bounds(const AttnArgs &a, int row0, int h, int row) {
+  return KVQ_IN_BOUNDS(a.geo.status, static_cast<long long>(row0) + row / a.group, a.rows) &&
          KVQ_IN_BOUNDS(a.geo.status, static_cast<long long>(h) * a.group + row % a.group, a.Hq);
 }
 
@@ -175,5 +304,9 @@ cudaError_t launch_rows_128(const AttnArgs &a, cudaStream_t stream);
 cudaError_t launch_rows_64(const AttnArgs &a, cudaStream_t stream);
 cudaError_t launch_tiles_128(const AttnArgs &a, cudaStream_t stream);
 cudaError_t launch_tiles_64(const AttnArgs &a, cudaStream_t stream);
+cudaError_t launch_rows_128_shared(const AttnArgs &a, cudaStream_t stream);
+cudaError_t launch_rows_64_shared(const AttnArgs &a, cudaStream_t stream);
+cudaError_t launch_tiles_128_shared(const AttnArgs &a, cudaStream_t stream);
+cudaError_t launch_tiles_64_shared(const AttnArgs &a, cudaStream_t stream);
 
 }  // namespace kv8

@@ -238,15 +238,16 @@ __device__ __forceinline__ float value_log(uint32_t bits) {
 
 // Work of one sequence: its units per (KV head, row tile) pair, and pairs.
 struct Work {
-  Seq q;
+  Seg q;
   int full;   // units of complete blocks
   int units;  // all units
   int tiles;  // row tiles per KV head
 };
 
+template <bool SHARED>
 __device__ __forceinline__ Work seq_work(const AttnArgs &a, int s) {
   Work w;
-  w.q = load_seq(a.geo, a.row_start, a.rows, a.max_new, s);
+  w.q = load_seg<SHARED>(a, s);
   const int L = w.q.L;
   const bool some = w.q.n > 0 && w.q.n * a.group <= a.rows_max && L > 0 && L <= a.max_len;
   const int nb = L / a.geo.B;
@@ -261,6 +262,7 @@ __device__ __forceinline__ long long line_of(const Work &w, int H) {
 
 // Walks a CTA's range of the line, one part of a (sequence, head, tile)
 // triple at a time.
+template <bool SHARED>
 struct Walk {
   Work w;
   int s, h, tile;
@@ -275,7 +277,7 @@ struct Walk {
   // the sequence that holds line position `pos`, whose own line starts at `base`
   __device__ __forceinline__ void enter(const AttnArgs &a, int seq, long long base, long long pos, long long end_) {
     s = seq;
-    w = seq_work(a, s);
+    w = seq_work<SHARED>(a, s);
     at = pos;
     end = end_;
     const int pair = static_cast<int>(divide(pos - base, w.units));
@@ -294,8 +296,8 @@ struct Walk {
       if (++h >= a.geo.H) {
         h = 0;
         do {
-          if (++s >= a.geo.S) return false;
-          w = seq_work(a, s);
+          if (++s >= a.segs) return false;
+          w = seq_work<SHARED>(a, s);
         } while (w.units == 0);
       }
     }
@@ -304,7 +306,7 @@ struct Walk {
   }
 };
 
-template <int D, int FMT, bool BF16, int HALVES>
+template <int D, int FMT, bool BF16, int HALVES, bool SHARED>
 __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
   using SM = Smem<D, HALVES>;
   constexpr int NT = SM::NT;  // output n-tiles
@@ -318,11 +320,11 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
   // The line's length.  On the way, a CTA writes the zero rows of its share of
   // the sequences with rows and nothing to see.
   long long total = 0, triples = 0;
-  for (int s0 = 0; s0 < geo.S; s0 += 32) {
+  for (int s0 = 0; s0 < a.segs; s0 += 32) {
     Work w = {};
     bool blind = false;
-    if (s0 + lane < geo.S) {
-      w = seq_work(a, s0 + lane);
+    if (s0 + lane < a.segs) {
+      w = seq_work<SHARED>(a, s0 + lane);
       blind = !w.q.ok || (w.q.n > 0 && (w.q.L <= 0 || w.q.L > a.max_len));
     }
     total += line_of(w, H);
@@ -330,7 +332,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
     for (unsigned m = __ballot_sync(kAll, blind); m; m &= m - 1) {
       const int s = s0 + __ffs(m) - 1;
       if (s % gridDim.x != blockIdx.x) continue;
-      const Seq sq = load_seq(geo, a.row_start, a.rows, a.max_new, s);
+      const Seg sq = load_seg<SHARED>(a, s);
       if (tid == 0 && (!sq.ok || sq.L != 0)) set_status(geo.status, sq.ok ? KVQ_STATUS_MAX_LEN : KVQ_STATUS_BAD_LEN);
       const int per_row = a.Hq * (D / 8);  // (a bad sequence has no rows)
       for (long long i = tid; i < static_cast<long long>(sq.n) * per_row; i += kWarps * 32) {
@@ -357,11 +359,11 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
   const int ctas = static_cast<int>(min(want, total));
   if (static_cast<int>(blockIdx.x) >= ctas) return;
   const long long lo = divide(blockIdx.x * total, ctas), hi = divide((blockIdx.x + 1) * total, ctas);
-  Walk use;
+  Walk<SHARED> use;
   {
     long long base = 0;
     for (int s0 = 0;; s0 += 32) {
-      const long long mine = s0 + lane < geo.S ? line_of(seq_work(a, s0 + lane), H) : 0;
+      const long long mine = s0 + lane < a.segs ? line_of(seq_work<SHARED>(a, s0 + lane), H) : 0;
       long long incl = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -379,7 +381,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
   }
 
   // ---- fetch: the warp's units, in the order it will use them
-  Walk get = use;
+  Walk<SHARED> get = use;
   bool more = true;
   int gu = get.u0 + warp;  // next unit to fetch
   const uint32_t ring = kvq::smem_u32(smem) + warp * SM::SLOTS * SM::SLOT;
@@ -398,8 +400,9 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
   };
   auto table_entry = [&]() -> int {
     if (!more || gu >= get.w.full) return 0;
-    if (!KVQ_IN_BOUNDS(geo.status, gu >> ushift, geo.max_blocks) || !KVQ_IN_BOUNDS(geo.status, get.s, geo.S)) return -1;
-    return geo.table[static_cast<size_t>(get.s) * geo.max_blocks + (gu >> ushift)];
+    const int at = get.w.q.base + (gu >> ushift);
+    if (!KVQ_IN_BOUNDS(geo.status, at, geo.max_blocks) || !KVQ_IN_BOUNDS(geo.status, get.w.q.entry, geo.S)) return -1;
+    return geo.table[static_cast<size_t>(get.w.q.entry) * geo.max_blocks + at];
   };
   settle();
   int entry = table_entry();
@@ -473,7 +476,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
       int lim[2];                         // last position they see
       {
         const int row = r0 + g;
-        const bool valid = row < n_rows && row_in_bounds(a, w.q, use.h, row);
+        const bool valid = row < n_rows && row_in_bounds(a, w.q.row0, use.h, row);
         const int tok = valid ? row / a.group : 0;
         const uint16_t *src =
             a.q.p + (static_cast<long long>(w.q.row0) + tok) * a.q.row +
@@ -519,10 +522,10 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
           rf[i] = __shfl_sync(kAll, f, 4 * (2 * q4 + i));
           if (FMT == KV8_INT8) r128[i] = 128.f * __shfl_sync(kAll, sum, 4 * (2 * q4 + i));
           const int rr = r0 + 2 * q4 + i;
-          lim[i] = rr < n_rows ? w.q.L - w.q.n + rr / a.group : -1;
+          lim[i] = rr < n_rows ? last_seen(a, w.q, rr / a.group) : -1;
         }
       }
-      const int seen_by_all = w.q.L - w.q.n + r0 / a.group;
+      const int seen_by_all = last_seen(a, w.q, r0 / a.group);
       constexpr int MT = D / 16;  // m-tiles of the output
       float acc[MT][4], m[2] = {ninf, ninf}, l[2] = {0.f, 0.f};
 #pragma unroll
@@ -825,12 +828,28 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
           }
         // m-tile j holds channels (D / 8) g + 2 j and the next one
         const int ch = (D / 8) * g + 2 * QT * warp, row = r0 + 2 * q4 + r;
-        if (row < n_rows && row_in_bounds(a, w.q, use.h, row) && KVQ_IN_BOUNDS(geo.status, part, 2 * kMaxCtas)) {
-          if (whole) {
-            const float inv = inverse_sum(ll, lim[r]);
-            const int tok = row / a.group;
-            uint16_t *dst = a.out.p + (static_cast<long long>(w.q.row0) + tok) * a.out.row +
-                            (static_cast<long long>(use.h) * a.group + row - tok * a.group) * a.out.head + ch;
+        if (row < n_rows && row_in_bounds(a, w.q.row0, use.h, row) && KVQ_IN_BOUNDS(geo.status, part, 2 * kMaxCtas)) {
+          const int tok = row / a.group, head = use.h * a.group + row - tok * a.group;
+          if (SHARED && whole && a.part == kPrefix) {
+            const size_t at = carry_at(a, w.q.row0 + tok, head);
+            float *dst = a.carry_o + at * D + ch;
+#pragma unroll
+            for (int j = 0; j < QT; ++j) *reinterpret_cast<float2 *>(dst + 2 * j) = o[j];
+            if (warp == 0 && g == 0) a.carry_ml[at] = make_float2(mm, ll);
+          } else if (whole) {
+            float inv = inverse_sum(ll, lim[r]);
+            if (SHARED && w.q.base) {
+              const size_t at = carry_at(a, w.q.row0 + tok, head);
+              const float *src = a.carry_o + at * D + ch;
+              const Join n = join(make_float2(mm, ll), a.carry_ml[at]);
+              inv = inverse_sum(n.sum, lim[r]);
+#pragma unroll
+              for (int j = 0; j < QT; ++j) {
+                const float2 c = *reinterpret_cast<const float2 *>(src + 2 * j);
+                o[j] = make_float2(fmaf(o[j].x, n.x, c.x * n.y), fmaf(o[j].y, n.x, c.y * n.y));
+              }
+            }
+            uint16_t *dst = a.out.p + (static_cast<long long>(w.q.row0) + tok) * a.out.row + head * a.out.head + ch;
 #pragma unroll
             for (int j = 0; j < QT; ++j)
               *reinterpret_cast<uint32_t *>(dst + 2 * j) = pack2<BF16>(o[j].x * inv, o[j].y * inv);
@@ -852,9 +871,9 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int row = r0 + g + 8 * r;
-        const bool valid = row < n_rows && row_in_bounds(a, w.q, use.h, row);
+        const bool valid = row < n_rows && row_in_bounds(a, w.q.row0, use.h, row);
         const int tok = valid ? row / a.group : 0;
-        lim[r] = valid ? w.q.L - w.q.n + tok : -1;
+        lim[r] = valid ? last_seen(a, w.q, tok) : -1;
         const uint16_t *src = a.q.p + (static_cast<long long>(w.q.row0) + tok) * a.q.row +
                               (static_cast<long long>(use.h) * a.group + (valid ? row - tok * a.group : 0)) * a.q.head;
         uint32_t big = 0;
@@ -913,7 +932,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
         r[3] = x.w;
       };
       // every row of the tile sees at least the tokens up to here
-      const int seen_by_all = w.q.L - w.q.n + r0 / a.group;
+      const int seen_by_all = last_seen(a, w.q, r0 / a.group);
 
       float acc[NT][4], m[2] = {ninf, ninf}, l[2] = {0.f, 0.f};
 #pragma unroll
@@ -1248,16 +1267,35 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
 #pragma unroll
             for (int i = 0; i < 3; ++i) o[c][j] += xch[((warp * 3 + i) * QT + j) * 32 + lane];
         }
-        const float (&o0)[QT] = o[0], (&o1)[QT] = o[1];
+        float (&o0)[QT] = o[0], (&o1)[QT] = o[1];
         // n-tile j, column c holds channel (D / 8) c + j
         const int ch0 = (D / 8) * (2 * q4) + warp * QT, ch1 = ch0 + D / 8;
         const int row = r0 + g + 8 * r;
-        if (row < n_rows && row_in_bounds(a, w.q, use.h, row) && KVQ_IN_BOUNDS(geo.status, part, 2 * kMaxCtas)) {
-          if (whole) {
-            const float inv = inverse_sum(ll, lim[r]);
-            const int tok = row / a.group;
-            uint16_t *dst = a.out.p + (static_cast<long long>(w.q.row0) + tok) * a.out.row +
-                            (static_cast<long long>(use.h) * a.group + row - tok * a.group) * a.out.head;
+        if (row < n_rows && row_in_bounds(a, w.q.row0, use.h, row) && KVQ_IN_BOUNDS(geo.status, part, 2 * kMaxCtas)) {
+          const int tok = row / a.group, head = use.h * a.group + row - tok * a.group;
+          if (SHARED && whole && a.part == kPrefix) {
+            const size_t at = carry_at(a, w.q.row0 + tok, head);
+            float *dst = a.carry_o + at * D;
+#pragma unroll
+            for (int j = 0; j < QT; j += 2) {
+              *reinterpret_cast<float2 *>(dst + ch0 + j) = make_float2(o0[j], o0[j + 1]);
+              *reinterpret_cast<float2 *>(dst + ch1 + j) = make_float2(o1[j], o1[j + 1]);
+            }
+            if (warp == 0 && q4 == 0) a.carry_ml[at] = make_float2(mm, ll);
+          } else if (whole) {
+            float inv = inverse_sum(ll, lim[r]);
+            if (SHARED && w.q.base) {
+              const size_t at = carry_at(a, w.q.row0 + tok, head);
+              const float *src = a.carry_o + at * D;
+              const Join n = join(make_float2(mm, ll), a.carry_ml[at]);
+              inv = inverse_sum(n.sum, lim[r]);
+#pragma unroll
+              for (int j = 0; j < QT; ++j) {
+                o0[j] = fmaf(o0[j], n.x, src[ch0 + j] * n.y);
+                o1[j] = fmaf(o1[j], n.x, src[ch1 + j] * n.y);
+              }
+            }
+            uint16_t *dst = a.out.p + (static_cast<long long>(w.q.row0) + tok) * a.out.row + head * a.out.head;
 #pragma unroll
             for (int j = 0; j < QT; j += 2) {
               *reinterpret_cast<uint32_t *>(dst + ch0 + j) = pack2<BF16>(o0[j] * inv, o0[j + 1] * inv);
@@ -1338,11 +1376,27 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
         }
 #pragma unroll
         for (int k = 0; k < NR; ++k) {
-          if (warp + kWarps * k >= rows || !row_in_bounds(a, w.q, use.h, r0 + row[k])) break;
+          if (warp + kWarps * k >= rows || !row_in_bounds(a, w.q.row0, use.h, r0 + row[k])) break;
           const int tok = (r0 + row[k]) / a.group;
-          const float inv = inverse_sum(ll[k], w.q.L - w.q.n + tok);
-          uint16_t *dst = a.out.p + (static_cast<long long>(w.q.row0) + tok) * a.out.row +
-                          (static_cast<long long>(use.h) * a.group + r0 + row[k] - tok * a.group) * a.out.head + lane * W;
+          const int head = use.h * a.group + r0 + row[k] - tok * a.group;
+          const size_t at = carry_at(a, w.q.row0 + tok, head);
+          if (SHARED && a.part == kPrefix) {
+            float *dst = a.carry_o + at * D + lane * W;
+#pragma unroll
+            for (int j = 0; j < W; j += 2) *reinterpret_cast<float2 *>(dst + j) = make_float2(o[k][j], o[k][j + 1]);
+            if (lane == 0) a.carry_ml[at] = make_float2(mm[k], ll[k]);
+            continue;
+          }
+          float sum = ll[k];
+          if (SHARED && w.q.base) {
+            const float *src = a.carry_o + at * D + lane * W;
+            const Join n = join(make_float2(mm[k], sum), a.carry_ml[at]);
+            sum = n.sum;
+#pragma unroll
+            for (int j = 0; j < W; ++j) o[k][j] = fmaf(o[k][j], n.x, src[j] * n.y);
+          }
+          const float inv = inverse_sum(sum, last_seen(a, w.q, tok));
+          uint16_t *dst = a.out.p + (static_cast<long long>(w.q.row0) + tok) * a.out.row + head * a.out.head + lane * W;
 #pragma unroll
           for (int j = 0; j < W; j += 2)
             *reinterpret_cast<uint32_t *>(dst + j) = pack2<BF16>(o[k][j] * inv, o[k][j + 1] * inv);
@@ -1354,9 +1408,9 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
   cp_wait<0>();
 }
 
-template <int D, int FMT, bool BF16, int HALVES>
+template <int D, int FMT, bool BF16, int HALVES, bool SHARED>
 cudaError_t launch_one(const AttnArgs &a, cudaStream_t stream) {
-  auto kernel = rows_kernel<D, FMT, BF16, HALVES>;
+  auto kernel = rows_kernel<D, FMT, BF16, HALVES, SHARED>;
   // resident CTAs and SMs of each device, once looked up
   static std::atomic<int> resident[64], sm_count[64];
   int dev = 0;
@@ -1380,26 +1434,30 @@ cudaError_t launch_one(const AttnArgs &a, cudaStream_t stream) {
     }
   }
   // no more CTAs than units for their warps, as far as the host can tell
-  const long long most = min(static_cast<long long>(a.max_new) * a.group, static_cast<long long>(a.rows_max));
+  const long long seg_rows = SHARED && a.part == kPrefix ? a.max_group_rows : a.max_new;
+  const long long most = min(seg_rows * a.group, static_cast<long long>(a.rows_max));
   const long long tiles = (most + kRowTile - 1) / kRowTile;
-  const long long units = (a.max_len / kUnit + a.geo.B / kWinUnit) * tiles * a.geo.H * a.geo.S;
+  const long long units = (a.max_len / kUnit + a.geo.B / kWinUnit) * tiles * a.geo.H * a.segs;
   long long grid = min(static_cast<long long>(kMaxCtas), static_cast<long long>(sms) * per);
   grid = max(1LL, min(grid, (units + kWarps - 1) / kWarps));
   kernel<<<static_cast<unsigned>(grid), kWarps * 32, Smem<D, HALVES>::BYTES, stream>>>(a);
   return cudaGetLastError();
 }
 
-template <int D, int FMT, bool BF16>
+template <int D, int FMT, bool BF16, bool SHARED>
 cudaError_t launch_halves(const AttnArgs &a, cudaStream_t stream) {
-  return static_cast<long long>(a.max_new) * a.group <= 8 ? launch_one<D, FMT, BF16, 1>(a, stream)
-                                                          : launch_one<D, FMT, BF16, 2>(a, stream);
+  const long long seg_rows = SHARED && a.part == kPrefix ? a.max_group_rows : a.max_new;
+  return seg_rows * a.group <= 8 ? launch_one<D, FMT, BF16, 1, SHARED>(a, stream)
+                                 : launch_one<D, FMT, BF16, 2, SHARED>(a, stream);
 }
 
-template <int D>
+template <int D, bool SHARED>
 cudaError_t launch_dim(const AttnArgs &a, cudaStream_t stream) {
   if (a.geo.fmt == KV8_INT8)
-    return a.geo.bf16 ? launch_halves<D, KV8_INT8, true>(a, stream) : launch_halves<D, KV8_INT8, false>(a, stream);
-  return a.geo.bf16 ? launch_halves<D, KV8_E4M3, true>(a, stream) : launch_halves<D, KV8_E4M3, false>(a, stream);
+    return a.geo.bf16 ? launch_halves<D, KV8_INT8, true, SHARED>(a, stream)
+                      : launch_halves<D, KV8_INT8, false, SHARED>(a, stream);
+  return a.geo.bf16 ? launch_halves<D, KV8_E4M3, true, SHARED>(a, stream)
+                    : launch_halves<D, KV8_E4M3, false, SHARED>(a, stream);
 }
 
 }  // namespace rows

@@ -1,0 +1,6 @@
+// The same for groups that share blocks, head_dim 128.
+#include "kv8_rows.cuh"
+
+namespace kv8 {
+cudaError_t launch_rows_128_shared(const AttnArgs &a, cudaStream_t stream) { return rows::launch_dim<128, true>(a, stream); }
+}  // namespace kv8

@@ -2,5 +2,5 @@
 #include "kv8_rows.cuh"
 
 namespace kv8 {
-cudaError_t launch_rows_64(const AttnArgs &a, cudaStream_t stream) { return rows::launch_dim<64>(a, stream); }
+cudaError_t launch_rows_64(const AttnArgs &a, cudaStream_t stream) { return rows::launch_dim<64, false>(a, stream); }
 }  // namespace kv8

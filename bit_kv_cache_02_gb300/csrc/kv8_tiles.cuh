@@ -109,11 +109,11 @@ struct Part {
   int packed, stored;   // units and tokens of complete blocks
   int L, n, row0;       // the sequence's tokens, new rows and first row
   int row;              // the item's first row among the sequence's rows of a KV head
-  int h, s;
+  int h, s;             // KV head, and the sequence whose blocks these are
   int slot;             // partial slot, or -1: the part is the whole item
   int first, c0, cuts;  // the item's first partial slot, its first CTA, and how many CTAs follow
   int end0;             // end of the units that row tile 0 sees, in u0 .. u1
-  int pad;
+  int base;             // blocks in front of the segment's
 };
 static_assert(sizeof(Part) == 64, "Part");
 
@@ -286,7 +286,7 @@ __device__ __forceinline__ uint32_t place(int row, int cc) {
 
 // A (sequence, row tile pair): what its items share.
 struct Pair {
-  Seq q;
+  Seg q;
   int s, rt;
   int last_seen;  // last position that any of its rows sees (at least 0)
   int stored;     // tokens in complete blocks
@@ -295,39 +295,44 @@ struct Pair {
   int units0;     // those that row tile 0 sees
 };
 
+template <bool SHARED>
 __device__ __forceinline__ int row_start_of(const AttnArgs &a, int s) {
+  if (SHARED && a.part == kPrefix) s = min(max(a.group_start[s], 0), a.geo.S);
   return a.row_start ? max(a.row_start[s], 0) : s;
 }
 
+template <bool SHARED>
 __device__ __forceinline__ Pair make_pair(const AttnArgs &a, int s, int rt) {
   Pair p;
   p.s = s;
   p.rt = rt;
   p.units = 0;
-  if (!KVQ_IN_BOUNDS(a.geo.status, s, a.geo.S)) return p;
-  p.q = load_seq(a.geo, a.row_start, a.rows, a.max_new, s);
+  if (!KVQ_IN_BOUNDS(a.geo.status, s, a.segs)) return p;
+  p.q = load_seg<SHARED>(a, s);
   const int L = p.q.L;
   const int n_rows = p.q.n * a.group;
   if (n_rows <= kRowsMax || L <= 0 || L > a.max_len || rt < 0 || rt * kRows >= n_rows) return p;
   const int last_row = min((rt + 1) * kRows, n_rows) - 1;
-  p.last_seen = max(L - p.q.n + last_row / a.group, 0);
+  p.last_seen = max(last_seen(a, p.q, last_row / a.group), 0);
   p.stored = L / a.geo.B * a.geo.B;
   p.packed = min(p.last_seen / kKeys + 1, (p.stored + kKeys - 1) / kKeys);
   p.units = p.packed + (p.last_seen >= p.stored ? 1 : 0);
-  const int last_seen0 = max(L - p.q.n + min(rt * kRows + 127, last_row) / a.group, 0);
+  const int last_seen0 = max(last_seen(a, p.q, min(rt * kRows + 127, last_row) / a.group), 0);
   p.units0 = min(last_seen0 / kKeys + 1, p.packed) + (last_seen0 >= p.stored ? 1 : 0);
   return p;
 }
 
 // Sequence s owns the slots from row_start[s] * group / 256 + s on: at least
 // as many as row tile pairs.
+template <bool SHARED>
 __device__ __forceinline__ Pair pair_of_slot(const AttnArgs &a, int slot) {
-  auto base = [&](int s) { return static_cast<int>(static_cast<long long>(row_start_of(a, s)) * a.group / kRows) + s; };
-  const int s = last_at_or_below(a.geo.S, slot, base);
-  return make_pair(a, s, slot - base(s));
+  auto base = [&](int s) { return static_cast<int>(static_cast<long long>(row_start_of<SHARED>(a, s)) * a.group / kRows) + s; };
+  const int s = last_at_or_below(a.segs, slot, base);
+  return make_pair<SHARED>(a, s, slot - base(s));
 }
 
 // An item's kOver + units line positions; unit u is at start + kOver + u.
+template <bool SHARED>
 struct Walk {
   Pair p;
   int h, u0, u1;    // KV head and units of the current part
@@ -348,10 +353,10 @@ struct Walk {
       h = 0;
       int s = p.s, rt = p.rt + 1;
       for (;;) {
-        p = make_pair(a, s, rt);
+        p = make_pair<SHARED>(a, s, rt);
         if (p.units) break;
         rt = 0;
-        if (++s >= a.geo.S) return false;
+        if (++s >= a.segs) return false;
       }
     }
     return part();
@@ -496,7 +501,7 @@ __device__ __forceinline__ float unit_weights(std::integral_constant<bool, EDGE>
   return l;
 }
 
-template <int D, int FMT, bool BF16>
+template <int D, int FMT, bool BF16, bool SHARED>
 __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
   using SM = Smem<D>;
   extern __shared__ unsigned char raw[];
@@ -515,8 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
 
   // ---- this CTA's range of the line
   long long total = 0;
-  const int slots = static_cast<int>(static_cast<long long>(a.row_start ? min(max(a.row_start[geo.S], 0), a.rows)
-                                                                        : geo.S) * a.group / kRows) + geo.S;
+  const int slots = static_cast<int>(static_cast<long long>(min(row_start_of<SHARED>(a, a.segs), a.rows)) * a.group / kRows) + a.segs;
   Pair mine;
   {
     // the slots below need row_start to rise
@@ -524,10 +528,13 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
     if (a.row_start)
       for (int s = tid; s < geo.S; s += kThreads)
         falls |= a.row_start[s] < 0 || a.row_start[s + 1] < a.row_start[s] || a.row_start[s + 1] > a.rows;
+    if (SHARED && a.part == kPrefix)
+      for (int s = tid; s < a.segs; s += kThreads)
+        falls |= a.group_start[s] < 0 || a.group_start[s + 1] < a.group_start[s] || a.group_start[s + 1] > geo.S;
     if (__syncthreads_or(falls)) return;  // the rows kernel has set the status
     long long sum = 0;
     for (int i = tid; i < slots; i += kThreads) {
-      mine = pair_of_slot(a, i);
+      mine = pair_of_slot<SHARED>(a, i);
       sum += line_of(mine, H);
     }
     long long before;
@@ -545,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
   {
     long long at = 0;
     for (int i0 = 0; i0 < slots; i0 += kThreads) {
-      if (i0 + tid < slots && slots > kThreads) mine = pair_of_slot(a, i0 + tid);
+      if (i0 + tid < slots && slots > kThreads) mine = pair_of_slot<SHARED>(a, i0 + tid);
       const long long u = i0 + tid < slots ? line_of(mine, H) : 0;
       long long before;
       const long long sum = cta_scan(u, before, scan_buf);
@@ -698,8 +705,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       }
     } else if (warp == 21 && lane == 0) {
       // ================================================= the walk
-      Walk use;
-      use.p = pair_of_slot(a, static_cast<int>(found[0]));
+      Walk<SHARED> use;
+      use.p = pair_of_slot<SHARED>(a, static_cast<int>(found[0]));
       use.h = static_cast<int>(divide(found[1], use.p.units + kOver));
       use.start = lo - (found[1] - static_cast<long long>(use.h) * (use.p.units + kOver));
       use.lo = lo;
@@ -718,7 +725,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           p.row0 = use.p.q.row0;
           p.row = use.p.rt * kRows;
           p.h = use.h;
-          p.s = use.p.s;
+          p.s = use.p.q.entry;
+          p.base = SHARED ? use.p.q.base : 0;
           p.slot = -1;
           p.end0 = max(min(use.u1, use.p.units0), use.u0);
           if (use.u0 != 0 || use.u1 != use.p.units) {
@@ -762,8 +770,9 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           bool none = true;
           float2 sc = make_float2(1.f, 1.f);
           if (mu < min(p.packed, p.u1) && tok < p.stored) {
-            const bool listed = KVQ_IN_BOUNDS(geo.status, p.s, geo.S) && KVQ_IN_BOUNDS(geo.status, tok / B, geo.max_blocks);
-            const int e = listed ? geo.table[static_cast<size_t>(p.s) * geo.max_blocks + tok / B] : -1;
+            const int at = SHARED ? p.base + tok / B : tok / B;
+            const bool listed = KVQ_IN_BOUNDS(geo.status, p.s, geo.S) && KVQ_IN_BOUNDS(geo.status, at, geo.max_blocks);
+            const int e = listed ? geo.table[static_cast<size_t>(p.s) * geo.max_blocks + at] : -1;
             if (e >= 0 && e < geo.num_blocks) {
               const long long bh = static_cast<long long>(e) * H + p.h;
               off = bh * 2 * B * D + (tok & (B - 1)) * D;
@@ -974,11 +983,11 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       const bool valid = row < n_rows;
       const int some = min(row, n_rows - 1);  // rows behind the last one compute what it does
       const int tok = some / a.group;
-      const int lim = valid ? p.L - p.n + tok : -1;  // last position the row sees
+      const int lim = valid ? last_seen(a, p, tok) : -1;  // last position the row sees
 
       // ---- the warp's 32 queries to shared memory: LPR lanes bring a row
       const long long head = static_cast<long long>(p.h) * a.group + some - tok * a.group;
-      const bool inside = row_in_bounds(a, Seq{p.L, p.n, p.row0, true}, p.h, some);
+      const bool inside = row_in_bounds(a, p.row0, p.h, some);
       const long long q_off = inside ? (static_cast<long long>(p.row0) + tok) * a.q.row + head * a.q.head : 0;
       float qf = a.zscale;
       if (active) {
@@ -1014,7 +1023,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       float M = ninf, l = 0.f;
       if (active) {
         // every row of the tile sees at least the tokens up to here
-        const int seen_by_all = p.L - p.n + (p.row + t * 128) / a.group;
+        const int seen_by_all = last_seen(a, p, (p.row + t * 128) / a.group);
         for (int u = u0; u < end; ++u, ++n_unit, ++n_own) {
           ok = wait_all(kSFull + t, n_own & 1, (warp & 7) == 0, 3 + t, 256, true);
           if (!ok) break;
@@ -1119,6 +1128,32 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
                 pack2<BF16>(o[8 * k + 2] * f, o[8 * k + 3] * f), pack2<BF16>(o[8 * k + 4] * f, o[8 * k + 5] * f),
                 pack2<BF16>(o[8 * k + 6] * f, o[8 * k + 7] * f));
       };
+      // With shared blocks: 32 channels of the row's partial result, for the
+      // launch that joins it, or joined with what the other launch has left.
+      const size_t carry = SHARED ? carry_at(a, p.row0 + tok, static_cast<int>(head)) : 0;
+      auto leave = [&](int c, const float *o, float top, float sum) {
+        if (!valid || !inside) return;
+        float4 *dst = reinterpret_cast<float4 *>(a.carry_o + carry * D) + 8 * c;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        if (c == 0) a.carry_ml[carry] = make_float2(top == ninf ? top : top - kShift, sum);
+      };
+      auto finish = [&](int c, float *o, float top, float sum) {
+        if (SHARED && p.base && valid && inside) {
+          const Join n = join(make_float2(top == ninf ? top : top - kShift, sum), a.carry_ml[carry]);
+          const float4 *src = reinterpret_cast<const float4 *>(a.carry_o + carry * D) + 8 * c;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float4 x = src[k];
+            o[4 * k] = fmaf(o[4 * k], n.x, x.x * n.y);
+            o[4 * k + 1] = fmaf(o[4 * k + 1], n.x, x.y * n.y);
+            o[4 * k + 2] = fmaf(o[4 * k + 2], n.x, x.z * n.y);
+            o[4 * k + 3] = fmaf(o[4 * k + 3], n.x, x.w * n.y);
+          }
+          sum = n.sum;
+        }
+        put(c, o, inverse_sum(sum, lim));
+      };
       auto store_rows = [&]() {
         bar_sync(3 + t, 256);
 #pragma unroll 4
@@ -1135,7 +1170,6 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       }
       if (active && ok && (whole || KVQ_IN_BOUNDS(geo.status, slot, 2 * kMaxTileCtas))) {
         fence_after();
-        const float inv = inverse_sum(l, lim);
 #pragma unroll 1
         for (int c = hf * (D / 64); c < (hf + 1) * (D / 64); ++c) {
           uint32_t o[32];
@@ -1145,7 +1179,10 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
             float x[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) x[i] = l == 0.f ? 0.f : __uint_as_float(o[i]);
-            put(c, x, inv);
+            if (SHARED && a.part == kPrefix)
+              leave(c, x, M, l);
+            else
+              finish(c, x, M, l);
           } else {
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
@@ -1155,9 +1192,9 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
                            : make_float4(0.f, 0.f, 0.f, 0.f);
           }
         }
-        if (whole)
+        if (whole && !(SHARED && a.part == kPrefix))
           store_rows();
-        else if (hf == 0)
+        else if (!whole && hf == 0)
           a.tile_ml[slot * kRows + t * 128 + r] = make_float2(M, l);
         fence_before();
       }
@@ -1206,9 +1243,12 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
                 o[4 * k + 3] = fmaf(o[4 * k + 3], was, x[k].w * f);
               }
             }
-            put(c, o, inverse_sum(ll, lim));
+            if (SHARED && a.part == kPrefix)
+              leave(c, o, mm, ll);
+            else
+              finish(c, o, mm, ll);
           }
-          store_rows();
+          if (!(SHARED && a.part == kPrefix)) store_rows();
         }
       }
       __syncwarp();
@@ -1224,9 +1264,9 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
   }
 }
 
-template <int D, int FMT, bool BF16>
+template <int D, int FMT, bool BF16, bool SHARED>
 cudaError_t launch_one(const AttnArgs &a, cudaStream_t stream) {
-  auto kernel = tiles_kernel<D, FMT, BF16>;
+  auto kernel = tiles_kernel<D, FMT, BF16, SHARED>;
   static std::atomic<int> sm_count[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1242,11 +1282,13 @@ cudaError_t launch_one(const AttnArgs &a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-template <int D>
+template <int D, bool SHARED>
 cudaError_t launch_dim(const AttnArgs &a, cudaStream_t stream) {
   if (a.geo.fmt == KV8_INT8)
-    return a.geo.bf16 ? launch_one<D, KV8_INT8, true>(a, stream) : launch_one<D, KV8_INT8, false>(a, stream);
-  return a.geo.bf16 ? launch_one<D, KV8_E4M3, true>(a, stream) : launch_one<D, KV8_E4M3, false>(a, stream);
+    return a.geo.bf16 ? launch_one<D, KV8_INT8, true, SHARED>(a, stream)
+                      : launch_one<D, KV8_INT8, false, SHARED>(a, stream);
+  return a.geo.bf16 ? launch_one<D, KV8_E4M3, true, SHARED>(a, stream)
+                    : launch_one<D, KV8_E4M3, false, SHARED>(a, stream);
 }
 
 }  // namespace tiles

@@ -19,7 +19,9 @@ DTYPES = {torch.float16: 0, torch.bfloat16: 1}
 CODE_DTYPES = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}
 BUF_CODES, BUF_SCALES, BUF_K_WIN, BUF_V_WIN, BUF_SEQ_LEN, BUF_BLOCK_TABLE = range(6)
 
-EXPORTED = ("kv8_max_blocks", "kv8_buffer_bytes", "kv8_append", "kv8_attn_workspace_bytes", "kv8_attn")
+EXPORTED = ("kv8_max_blocks", "kv8_buffer_bytes", "kv8_append", "kv8_append_axes", "kv8_attn_workspace_bytes",
+            "kv8_attn", "kv8_cross_attn_workspace_bytes", "kv8_cross_attn", "kv8_shared_attn_workspace_bytes",
+            "kv8_shared_attn")
 
 
 class CacheStruct(ctypes.Structure):
@@ -59,7 +61,14 @@ def _sign():
         "kv8_attn_workspace_bytes": (c_int64, [C, c_int32, c_int32]),
         "kv8_attn": (ctypes.c_int, [C, c_int32, R, R, c_void_p, c_int32, c_int32, c_float, c_void_p, c_size_t,
                                     c_int32, c_void_p]),
+        "kv8_append_axes": (ctypes.c_int, [C, R, R, R, R, c_int32, c_void_p, c_int32, c_int32, c_void_p, c_int32,
+                                           c_int32, c_int32, c_void_p, c_int64, c_int32, ctypes.c_char_p, c_void_p]),
+        "kv8_cross_attn_workspace_bytes": (c_int64, [C, c_int32, c_int32]),
+        "kv8_shared_attn_workspace_bytes": (c_int64, [C, c_int32, c_int32, c_int32, c_int32]),
+        "kv8_shared_attn": (ctypes.c_int, [C, c_int32, R, R, c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_int32,
+                                           c_int32, c_float, c_void_p, c_size_t, c_int32, c_void_p]),
     }
+    sig["kv8_cross_attn"] = sig["kv8_attn"]
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
         fn.restype = res
@@ -169,11 +178,7 @@ def _launch(fn, what, cache, stream, *args):
         raise KvqError(code, what)
 
 
-def kv8_append(cache: KV8Cache, k, v, row_start=None, max_new: int = 1, q=None, q_out=None, rope=None,
-               interleaved: bool = False, stream=None):
-    """k, v: [rows][Hkv][D]; q, q_out: [rows][Hq][D] (rotated along; q_out may
-    be q); rope: fp32 [positions][rot_dim] (rope_table) or None.  row_start:
-    int32 [S + 1], or None for one row per sequence."""
+def _append_tensors(cache, k, v, q, q_out):
     rows, dim = k.shape[0] if k.shape else 0, cache.head_dim  # (len and size take longer than shape)
     shape = (rows, cache.num_kv_heads, dim)
     ks, vs = _rows(k, cache, shape, "k"), _rows(v, cache, shape, "v")
@@ -188,16 +193,54 @@ def kv8_append(cache: KV8Cache, k, v, row_start=None, max_new: int = 1, q=None, 
         qs, os = _rows(q, cache, shape, "q"), _rows(q_out, cache, shape, "q_out")
     elif q_out is not None:
         raise ValueError("q_out without q")
+    return rows, ks, vs, qs, os, heads
+
+
+def _table(rope, cache):
+    shape = rope.shape
+    if rope.dtype is not _F32 or len(shape) != 2 or not rope.is_contiguous() \
+            or rope.get_device() != cache.device_index:
+        raise ValueError(f"rope: a contiguous float32 tensor [positions][rot_dim] on {cache.device} is needed")
+    return shape
+
+
+def kv8_append(cache: KV8Cache, k, v, row_start=None, max_new: int = 1, q=None, q_out=None, rope=None,
+               interleaved: bool = False, stream=None):
+    """k, v: [rows][Hkv][D]; q, q_out: [rows][Hq][D] (rotated along; q_out may
+    be q); rope: fp32 [positions][rot_dim] (rope_table) or None.  row_start:
+    int32 [S + 1], or None for one row per sequence."""
+    rows, ks, vs, qs, os, heads = _append_tensors(cache, k, v, q, q_out)
     table, rot, positions = None, 0, 0
     if rope is not None:
-        shape = rope.shape
-        if rope.dtype is not _F32 or len(shape) != 2 or not rope.is_contiguous() \
-                or rope.get_device() != cache.device_index:
-            raise ValueError(f"rope: a contiguous float32 tensor [positions][rot_dim] on {cache.device} is needed")
-        positions, rot = shape
+        positions, rot = _table(rope, cache)
         table = rope.data_ptr() if rot else None
     _launch(lib.kv8_append, "kv8_append", cache, stream, cache.ref, ks, vs, qs, os, heads,
             _row_start(row_start, cache), rows, max_new, table, positions, rot, 1 if interleaved else 0)
+
+
+def rope_axes(axes) -> bytes:
+    """The axes argument of kv8_append_axes: the axis (0 to 3) that each pair of
+    channels turns by, rot_dim / 2 in all.  Sections of 16, 24 and 24 pairs are
+    rope_axes([0] * 16 + [1] * 24 + [2] * 24)."""
+    return bytes(axes)
+
+
+def kv8_append_axes(cache: KV8Cache, k, v, positions, axes: bytes, rope, row_start=None, max_new: int = 1, q=None,
+                    q_out=None, interleaved: bool = False, stream=None):
+    """kv8_append with positions: int32 [axes][rows], each line contiguous; axes:
+    the axis of each channel pair (rope_axes); rope: fp32 [positions][rot_dim]
+    for the positions that occur, whatever the capacity."""
+    rows, ks, vs, qs, os, heads = _append_tensors(cache, k, v, q, q_out)
+    table_rows, rot = _table(rope, cache)
+    shape = positions.shape
+    if positions.dtype is not _I32 or len(shape) != 2 or shape[1] != rows or (rows > 1 and positions.stride(1) != 1) \
+            or positions.get_device() != cache.device_index:
+        raise ValueError(f"positions: an int32 tensor [axes][{rows}] with contiguous lines on {cache.device} is needed")
+    if type(axes) is not bytes or 2 * len(axes) != rot:
+        raise ValueError(f"axes: rope_axes of {rot // 2} axes is needed")
+    _launch(lib.kv8_append_axes, "kv8_append_axes", cache, stream, cache.ref, ks, vs, qs, os, heads,
+            _row_start(row_start, cache), rows, max_new, rope.data_ptr(), table_rows, rot, 1 if interleaved else 0,
+            positions.data_ptr(), positions.stride(0), shape[0], axes)
 
 
 def attn_workspace_bytes(cache: KV8Cache, num_q_heads: int, max_new: int = 1) -> int:
@@ -212,9 +255,35 @@ def alloc_workspace(cache: KV8Cache, num_q_heads: int, max_new: int = 1):
     return torch.zeros(attn_workspace_bytes(cache, num_q_heads, max_new), dtype=torch.uint8, device=cache.device)
 
 
-def kv8_attn(cache: KV8Cache, q, out, workspace, max_len: int, row_start=None, max_new: int = 1,
-             softmax_scale: float = 0.0, stream=None):
-    """q, out: [rows][Hq][D] (out may be q); max_len: a bound on seq_len."""
+def cross_attn_workspace_bytes(cache: KV8Cache, num_q_heads: int, max_rows: int = 1) -> int:
+    n = lib.kv8_cross_attn_workspace_bytes(cache.ref, num_q_heads, max_rows)
+    if n < 0:
+        raise KvqError(-1, "kv8_cross_attn_workspace_bytes")
+    return n
+
+
+def alloc_cross_workspace(cache: KV8Cache, num_q_heads: int, max_rows: int = 1):
+    """A torch-allocated, zero-filled workspace for kv8_cross_attn."""
+    return torch.zeros(cross_attn_workspace_bytes(cache, num_q_heads, max_rows), dtype=torch.uint8,
+                       device=cache.device)
+
+
+def shared_attn_workspace_bytes(cache: KV8Cache, num_q_heads: int, rows: int, max_new: int,
+                                max_group_rows: int) -> int:
+    n = lib.kv8_shared_attn_workspace_bytes(cache.ref, num_q_heads, rows, max_new, max_group_rows)
+    if n < 0:
+        raise KvqError(-1, "kv8_shared_attn_workspace_bytes")
+    return n
+
+
+def alloc_shared_workspace(cache: KV8Cache, num_q_heads: int, rows: int, max_new: int, max_group_rows: int):
+    """A torch-allocated, zero-filled workspace for kv8_shared_attn."""
+    return torch.zeros(shared_attn_workspace_bytes(cache, num_q_heads, rows, max_new, max_group_rows),
+                       dtype=torch.uint8, device=cache.device)
+
+
+def _attn_tensors(cache, q, out, workspace):
+    """(rows, heads, q, out, workspace, its bytes)"""
     shape = q.shape
     if len(shape) != 3:
         raise ValueError("q: [rows][heads][D] is needed")
@@ -222,6 +291,41 @@ def kv8_attn(cache: KV8Cache, q, out, workspace, max_len: int, row_start=None, m
     shape = (rows, heads, cache.head_dim)
     if workspace.get_device() != cache.device_index or not workspace.is_contiguous():
         raise ValueError(f"workspace: a contiguous tensor on {cache.device} is needed")
-    _launch(lib.kv8_attn, "kv8_attn", cache, stream, cache.ref, heads, _rows(q, cache, shape, "q"),
-            _rows(out, cache, shape, "out"), _row_start(row_start, cache), rows, max_new, softmax_scale,
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), max_len)
+    return (rows, heads, _rows(q, cache, shape, "q"), _rows(out, cache, shape, "out"), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
+
+
+def kv8_attn(cache: KV8Cache, q, out, workspace, max_len: int, row_start=None, max_new: int = 1,
+             softmax_scale: float = 0.0, stream=None):
+    """q, out: [rows][Hq][D] (out may be q); max_len: a bound on seq_len."""
+    rows, heads, qs, os, ws, size = _attn_tensors(cache, q, out, workspace)
+    _launch(lib.kv8_attn, "kv8_attn", cache, stream, cache.ref, heads, qs, os, _row_start(row_start, cache), rows,
+            max_new, softmax_scale, ws, size, max_len)
+
+
+def kv8_cross_attn(cache: KV8Cache, q, out, workspace, max_len: int, row_start=None, max_rows: int = 1,
+                   softmax_scale: float = 0.0, stream=None):
+    """kv8_attn without order: each row sees all seq_len tokens of the sequence
+    that row_start gives it to.  max_rows: a bound on the rows of a sequence."""
+    rows, heads, qs, os, ws, size = _attn_tensors(cache, q, out, workspace)
+    _launch(lib.kv8_cross_attn, "kv8_cross_attn", cache, stream, cache.ref, heads, qs, os,
+            _row_start(row_start, cache), rows, max_rows, softmax_scale, ws, size, max_len)
+
+
+def _groups(t, cache, name, n):
+    if t.dtype is not _I32 or t.dim() != 1 or not t.is_contiguous() or t.get_device() != cache.device_index \
+            or t.shape[0] != n:
+        raise ValueError(f"{name}: a contiguous int32 tensor [{n}] on {cache.device} is needed")
+    return t.data_ptr()
+
+
+def kv8_shared_attn(cache: KV8Cache, q, out, workspace, max_len: int, group_start, prefix_len, max_group_rows: int,
+                    row_start=None, max_new: int = 1, softmax_scale: float = 0.0, stream=None):
+    """kv8_attn where sequences group_start[g] .. group_start[g + 1] - 1 share
+    the whole blocks of their first prefix_len[g] tokens (int32 [groups + 1] and
+    [groups]).  max_group_rows: a bound on the rows of a group."""
+    rows, heads, qs, os, ws, size = _attn_tensors(cache, q, out, workspace)
+    groups = prefix_len.shape[0] if prefix_len.dim() == 1 else 0
+    _launch(lib.kv8_shared_attn, "kv8_shared_attn", cache, stream, cache.ref, heads, qs, os,
+            _row_start(row_start, cache), rows, max_new, _groups(group_start, cache, "group_start", groups + 1),
+            _groups(prefix_len, cache, "prefix_len", groups), groups, max_group_rows, softmax_scale, ws, size, max_len)

@@ -14,6 +14,13 @@
  *   kv8_append  rotates queries and keys to their positions, stores the keys
  *               and values, and quantizes every block that fills.
  *   kv8_attn    attention of the new tokens' queries over the cache, causal.
+ *   kv8_append_axes   the append with positions that have several axes (time,
+ *               height and width of image patches) or are not the tokens' places
+ *               in the cache.
+ *   kv8_cross_attn    attention to all tokens of each sequence: an encoder's
+ *               states, by a decoder's rows of any number.
+ *   kv8_shared_attn   kv8_attn for sequences of which groups share their first
+ *               blocks, which it reads once per group.
  *
  * A step of a serving loop raises seq_len by the new tokens of each sequence,
  * calls kv8_append, then kv8_attn with the same seq_len and row_start.
@@ -47,6 +54,11 @@ extern "C" {
 #define KV8_BF16 1  /* bfloat16 */
 
 #define KV8_MAX_CAPACITY (1 << 30)
+#define KV8_MAX_AXES 4
+#define KV8_MAX_GROUPS 65535
+
+/* a bit of the status word, beside KVQ_STATUS_*: a position outside the table */
+#define KV8_STATUS_BAD_POSITION 64
 
 /* which buffer for kv8_buffer_bytes() */
 #define KV8_BUF_CODES       0
@@ -166,6 +178,36 @@ int kv8_append(const kv8_cache *cache, const kv8_rows *k, const kv8_rows *v,
                int32_t interleaved, void *stream);
 
 /*
+ * kv8_append_axes -- kv8_append for positions that are given.
+ *
+ *   positions  device int32: position of row r on axis x at
+ *              positions[x * axis_stride + r].  Rows of no sequence are not read.
+ *   axis_stride  at least `rows`; not used with one axis.
+ *   num_axes   1 .. KV8_MAX_AXES.
+ *   axis_of_pair  HOST array of rot_dim / 2 axes, read before the call returns:
+ *              channel pair i (as in kv8_append, i + rot_dim / 2 or 2 i + 1
+ *              beside it) turns by the angle i of the table's row
+ *              positions[axis_of_pair[i]].  In order (the first pairs by the first
+ *              axis, ...) or in turn, as the model has them; in order is faster
+ *              where four aligned pairs have one axis.
+ *   rope, rope_rows  as in kv8_append, for positions 0 .. rope_rows - 1, whatever
+ *              the capacity.  The table's columns may have any angles: one
+ *              sequence of frequencies over all pairs, or one anew for each axis.
+ *   rot_dim    a multiple of 16, 16 .. D.
+ *
+ * All else is as in kv8_append: tokens are stored at places seq_len[s] - n ..
+ * seq_len[s] - 1 of their sequence, whatever their positions.  A position outside
+ * the table is not read at: the channels that turn by it become NaN, in queries
+ * and keys, and KV8_STATUS_BAD_POSITION is set.  With one axis whose positions
+ * are the tokens' places the results are kv8_append's, bit for bit.  One kernel.
+ */
+int kv8_append_axes(const kv8_cache *cache, const kv8_rows *k, const kv8_rows *v, const kv8_rows *q,
+                    const kv8_rows *q_out, int32_t num_q_heads, const int32_t *row_start, int32_t rows,
+                    int32_t max_new, const float *rope, int32_t rope_rows, int32_t rot_dim, int32_t interleaved,
+                    const int32_t *positions, int64_t axis_stride, int32_t num_axes, const uint8_t *axis_of_pair,
+                    void *stream);
+
+/*
  * kv8_attn_workspace_bytes -- scratch size for kv8_attn calls with at most
  * max_new rows per sequence (a multiple of 256); -1 on invalid arguments.
  * About 10 MiB for D = 128, and 50 MiB where max_new * Hq / Hkv > 48: there a
@@ -218,6 +260,71 @@ int kv8_attn(const kv8_cache *cache, int32_t num_q_heads, const kv8_rows *q,
              const kv8_rows *out, const int32_t *row_start, int32_t rows,
              int32_t max_new, float softmax_scale, void *workspace,
              size_t workspace_bytes, int32_t max_len, void *stream);
+
+/*
+ * kv8_cross_attn -- softmax attention to all tokens of each sequence, without
+ * order: a decoder's rows over an encoder's states, which kv8_append (without
+ * rope, or kv8_append_axes) has stored.
+ *
+ *   q, out     [rows][Hq][D] as in kv8_attn.
+ *   row_start  device int32 [S + 1]: rows row_start[s] .. row_start[s + 1] - 1
+ *              attend to sequence s: tokens of the decoder, beams that share the
+ *              states, or both.  Their number has nothing to do with seq_len[s].
+ *              NULL: one row per sequence, row s.
+ *   max_rows   host bound on the rows of one sequence, from 1 on; not bound by
+ *              the capacity.  max_rows * Hq / Hkv is below 2^30.
+ *   softmax_scale, workspace, max_len, and all else, as in kv8_attn; the
+ *              workspace has at least kv8_cross_attn_workspace_bytes(), which is
+ *              kv8_attn_workspace_bytes() where that takes the bound, and the calls
+ *              may share one.
+ *
+ * Every row sees the seq_len[s] tokens of its sequence.  Rows of a sequence
+ * without tokens get zeros.
+ */
+int64_t kv8_cross_attn_workspace_bytes(const kv8_cache *cache, int32_t num_q_heads, int32_t max_rows);
+int kv8_cross_attn(const kv8_cache *cache, int32_t num_q_heads, const kv8_rows *q, const kv8_rows *out,
+                   const int32_t *row_start, int32_t rows, int32_t max_rows, float softmax_scale, void *workspace,
+                   size_t workspace_bytes, int32_t max_len, void *stream);
+
+/*
+ * kv8_shared_attn -- kv8_attn where groups of sequences share their first blocks
+ * (a system prompt, a document, the prompt of several answers): the rows of all
+ * sequences of a group attend to those blocks at once, and each sequence's rows
+ * to what lies behind them; both results are joined in 32 bits.
+ *
+ *   q, out, row_start, rows, max_new, softmax_scale, max_len  as in kv8_attn.
+ *   group_start  device int32 [num_groups + 1]: group g is sequences
+ *              group_start[g] .. group_start[g + 1] - 1.  Groups may be empty;
+ *              sequences before the first or behind the last group share
+ *              nothing.
+ *   prefix_len  device int32 [num_groups]: tokens that a group shares, at most
+ *              max_len, rounded down to whole blocks.  The blocks are those of the
+ *              block table's line of the group's first sequence; the other
+ *              sequences' entries for them are not read.  Each sequence of the
+ *              group has stored them before the call's new tokens: prefix_len,
+ *              rounded down, is at most seq_len[s] minus its new rows.
+ *   num_groups 1 .. KV8_MAX_GROUPS.
+ *   max_group_rows  host bound on the rows of one group's sequences together.
+ *   workspace  at least kv8_shared_attn_workspace_bytes() for these rows, max_new
+ *              and max_group_rows (a size that serves larger ones serves smaller
+ *              ones), with the rules of kv8_attn's; it may serve kv8_attn and
+ *              kv8_cross_attn too.  4 D + 8 bytes per row and query head on top of
+ *              kv8_attn's size.
+ *
+ * A group with bad bounds, a bad prefix_len, more rows than max_group_rows or a
+ * first sequence that ends within the shared blocks is invalid: the rows of its
+ * sequences are left alone, as are those of a sequence that ends within them, and
+ * KVQ_STATUS_BAD_LEN is set.  Neither row_start nor group_start may decrease:
+ * where one does, that bit is set and the rows of all sequences are undefined.
+ * Otherwise results are as kv8_attn describes them, for a table in which all
+ * sequences of a group have its first one's entries.  Two to four kernels.
+ */
+int64_t kv8_shared_attn_workspace_bytes(const kv8_cache *cache, int32_t num_q_heads, int32_t rows, int32_t max_new,
+                                        int32_t max_group_rows);
+int kv8_shared_attn(const kv8_cache *cache, int32_t num_q_heads, const kv8_rows *q, const kv8_rows *out,
+                    const int32_t *row_start, int32_t rows, int32_t max_new, const int32_t *group_start,
+                    const int32_t *prefix_len, int32_t num_groups, int32_t max_group_rows, float softmax_scale,
+                    void *workspace, size_t workspace_bytes, int32_t max_len, void *stream);
 
 #ifdef __cplusplus
 }
