@@ -285,8 +285,8 @@ int64_t kv8_shared_attn_workspace_bytes(const kv8_cache *cache, int32_t num_q_he
   if (check_geometry(cache) || rows < 0 || max_new < 1 || max_new > cache->capacity || max_group_rows < 1 ||
       check_heads(cache, num_q_heads, max_new) || check_heads(cache, num_q_heads, max_group_rows))
     return -1;
-  return static_cast<int64_t>(kv8::plan_shared(cache->head_dim, num_q_heads / cache->num_kv_heads, num_q_heads, rows,
-                                               max_new, max_group_rows)
+  return static_cast<int64_t>(kv8::plan_shared(cache->head_dim, cache->num_seqs, cache->num_kv_heads, num_q_heads,
+                                               rows, max_new, max_group_rows)
                                   .bytes);
 }
 
@@ -297,30 +297,39 @@ int kv8_shared_attn(const kv8_cache *cache, int32_t num_q_heads, const kv8_rows 
   int e = check_buffers(cache);
   if (e) return e;
   if ((e = check_row_range(cache, row_start, rows, max_new))) return e;
-  if (num_groups < 1 || max_group_rows < 1 || !group_start || !prefix_len) return KVQ_ERR_INVALID_ARG;
-  if (num_groups > KV8_MAX_GROUPS) return KVQ_ERR_UNSUPPORTED;
+  if (num_groups < 1 || num_groups > cache->num_seqs || max_group_rows < 1 || !group_start || !prefix_len)
+    return KVQ_ERR_INVALID_ARG;
   if (!aligned(group_start, 4) || !aligned(prefix_len, 4)) return KVQ_ERR_ALIGNMENT;
   kv8::AttnArgs a;
   if ((e = attn_args(a, cache, num_q_heads, q, out, row_start, rows, max_new, softmax_scale, max_len))) return e;
   if ((e = check_heads(cache, num_q_heads, max_group_rows))) return e;
   if (rows == 0) return KVQ_OK;
   const int64_t group = a.group;
-  const kv8::SharedPlan plan = kv8::plan_shared(cache->head_dim, a.group, num_q_heads, rows, max_new, max_group_rows);
+  const kv8::SharedPlan plan = kv8::plan_shared(cache->head_dim, cache->num_seqs, cache->num_kv_heads, num_q_heads, rows,
+                                                max_new, max_group_rows);
   if ((e = check_workspace(workspace, workspace_bytes, plan.bytes))) return e;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   a.group_start = group_start;
   a.prefix_len = prefix_len;
   a.groups = num_groups;
   a.max_group_rows = max_group_rows;
+  a.plan = reinterpret_cast<int4 *>(ws + plan.off_segs);
+  a.items = reinterpret_cast<int4 *>(ws + plan.off_items);
   a.carry_ml = reinterpret_cast<float2 *>(ws + plan.off_ml);
   a.carry_o = reinterpret_cast<float *>(ws + plan.off_o);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  uint64_t n = 0;
+  uint64_t n = 1;
+  cudaError_t ce = kv8::launch_segments(a, st);
+  if (ce != cudaSuccess) return from_cuda(ce, n);
   a.part = kv8::kPrefix;
   a.causal = 0;
   a.segs = num_groups;
   place(a, kv8::plan_attn(cache->head_dim, group * max_group_rows), workspace);
-  cudaError_t ce = kv8::launch_attn(a, plan.prefix_tiles, st, &n);
+  ce = kv8::launch_attn(a, plan.prefix_tiles, st, &n);
+  if (ce == cudaSuccess && plan.prefix_tiles) {
+    ++n;
+    ce = kv8::launch_join(a, st);
+  }
   if (ce == cudaSuccess) {
     a.part = kv8::kOwn;
     a.causal = 1;
@@ -351,15 +360,22 @@ AttnPlan plan_attn(int D, long long rows_per_head) {
   return p;
 }
 
-SharedPlan plan_shared(int D, int group, int num_q_heads, long long rows, long long max_new, long long max_group_rows) {
+SharedPlan plan_shared(int D, int S, int H, int num_q_heads, long long rows, long long max_new,
+                       long long max_group_rows) {
   SharedPlan p;
+  auto align = [](size_t x) { return (x + 255) / 256 * 256; };
+  const int group = num_q_heads / H;
   const AttnPlan own = plan_attn(D, group * max_new), prefix = plan_attn(D, group * max_group_rows);
   p.own_tiles = own.tiles;
   p.prefix_tiles = prefix.tiles;
-  p.off_ml = own.bytes > prefix.bytes ? own.bytes : prefix.bytes;
+  p.off_segs = own.bytes > prefix.bytes ? own.bytes : prefix.bytes;
+  p.off_items = align(p.off_segs + static_cast<size_t>(2) * S * 2 * sizeof(int4));
+  // (a group has at most one row tile pair that is not full)
+  const size_t items = p.prefix_tiles ? (static_cast<size_t>(rows) * group / kTileRows + S) * H : 0;
+  p.off_ml = align(p.off_items + items * sizeof(int4));
   const size_t n = static_cast<size_t>(rows) * num_q_heads;
-  p.off_o = p.off_ml + (n * sizeof(float2) + 255) / 256 * 256;
-  p.bytes = p.off_o + (n * D * sizeof(float) + 255) / 256 * 256;
+  p.off_o = align(p.off_ml + n * sizeof(float2));
+  p.bytes = align(p.off_o + n * D * sizeof(float));
   return p;
 }
 

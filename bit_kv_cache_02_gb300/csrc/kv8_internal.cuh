@@ -160,10 +160,11 @@ AttnPlan plan_attn(int D, long long rows_per_head);
 // Attention with shared blocks: the two launches follow each other on the same
 // regions, and the partial results that one leaves for the other lie behind them.
 struct SharedPlan {
-  size_t off_ml, off_o, bytes;
+  size_t off_segs, off_items, off_ml, off_o, bytes;
   bool own_tiles, prefix_tiles;
 };
-SharedPlan plan_shared(int D, int group, int num_q_heads, long long rows, long long max_new, long long max_group_rows);
+SharedPlan plan_shared(int D, int S, int H, int num_q_heads, long long rows, long long max_new,
+                       long long max_group_rows);
 
 // What one launch attends to, segment by segment.
 enum {
@@ -180,6 +181,8 @@ struct AttnArgs {
   int segs;    // segments: sequences or groups
   const int *group_start, *prefix_len;  // [groups + 1], [groups]; with kPrefix and kOwn
   int groups, max_group_rows;
+  int4 *plan;        // two per segment: the groups', then the sequences'
+  int4 *items;       // of the tile kernel's items over shared blocks: the parts to join
   float *carry_o;    // [rows][Hq][D]: unnormalized outputs over the shared blocks
   float2 *carry_ml;  // [rows][Hq]: (max, sum) in log2 units
   Rows q, out;
@@ -233,28 +236,11 @@ __device__ __forceinline__ Group load_group(const AttnArgs &a, int g) {
   return x;
 }
 
-// SHARED: a launch over shared blocks, or over what lies behind them (kernels of
-// their own: what they keep besides cost the others registers).
-template <bool SHARED>
-__device__ __forceinline__ Seg load_seg(const AttnArgs &a, int s) {
-  Seg x;
-  x.base = 0;
-  if (SHARED && a.part == kPrefix) {
-    const Group g = load_group(a, s);
-    x.ok = g.ok;
-    x.L = g.blocks * a.geo.B;
-    x.n = x.L ? g.n : 0;
-    x.row0 = g.row0;
-    x.entry = g.ok ? g.first : 0;
-    return x;
-  }
+// The sequence's segment, behind the blocks that it shares with its group.
+__device__ __forceinline__ Seg own_seg(const AttnArgs &a, int s) {
   const Seq q = load_seq(a.geo, a.row_start, a.rows, a.max_new, s);
-  x.L = q.L;
-  x.n = q.n;
-  x.row0 = q.row0;
-  x.entry = s;
-  x.ok = q.ok;
-  if (SHARED && a.part == kOwn && q.n > 0 && q.L <= a.max_len) {
+  Seg x = {q.L, q.n, q.row0, 0, s, q.ok};
+  if (q.n > 0 && q.L <= a.max_len) {
     const int g = last_at_or_below(a.groups, s, [&](int i) { return a.group_start[i]; });
     if (a.group_start[g] <= s && s < a.group_start[g + 1]) {
       const Group of = load_group(a, g);
@@ -268,6 +254,51 @@ __device__ __forceinline__ Seg load_seg(const AttnArgs &a, int s) {
     }
   }
   return x;
+}
+__device__ __forceinline__ Seg group_seg(const AttnArgs &a, int g) {
+  const Group x = load_group(a, g);
+  const int L = x.blocks * a.geo.B;
+  return {L, L ? x.n : 0, x.row0, 0, x.ok ? x.first : 0, x.ok};
+}
+
+// SHARED: a launch over shared blocks, or over what lies behind them (kernels of
+// their own: what they keep besides cost the others registers).  Their segments
+// have been looked up by a kernel before: each is a chain of six loads, which
+// every CTA would wait for, for every sequence.
+template <bool SHARED>
+__device__ __forceinline__ Seg load_seg(const AttnArgs &a, int s) {
+  if (SHARED) {
+    const int4 *p = a.plan + 2 * (static_cast<size_t>(a.part == kOwn ? a.groups : 0) + s);
+    const int4 x = p[0], y = p[1];
+    return {x.x, x.y, x.z, x.w, y.x, y.y != 0};
+  }
+  const Seq q = load_seq(a.geo, a.row_start, a.rows, a.max_new, s);
+  return {q.L, q.n, q.row0, 0, s, q.ok};
+}
+
+// The kernels of one call with shared blocks are launched while the one before
+// still runs; each waits here, first of all, until that one's results are there.
+template <bool SHARED>
+__device__ __forceinline__ void follow() {
+  if (SHARED) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+  }
+}
+template <typename... A>
+cudaError_t launch_after(void (*kernel)(A...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream,
+                         A... args) {
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t config = {};
+  config.gridDim = dim3(grid);
+  config.blockDim = dim3(threads);
+  config.dynamicSmemBytes = smem;
+  config.stream = stream;
+  config.attrs = &attr;
+  config.numAttrs = 1;
+  return cudaLaunchKernelEx(&config, kernel, args...);
 }
 
 // The last position of the segment that rows of its new token `tok` see.
@@ -299,6 +330,10 @@ __device__ __forceinline__ bool row_in_bounds(const AttnArgs &a, int row0, int h
 }
 
 cudaError_t launch_attn(const AttnArgs &a, bool tiles, cudaStream_t stream, uint64_t *launches);
+// looks up the segments of a call with shared blocks
+cudaError_t launch_segments(const AttnArgs &a, cudaStream_t stream);
+// joins the parts of the tile kernel's items over shared blocks
+cudaError_t launch_join(const AttnArgs &a, cudaStream_t stream);
 // the kernels for one head dimension (one translation unit each)
 cudaError_t launch_rows_128(const AttnArgs &a, cudaStream_t stream);
 cudaError_t launch_rows_64(const AttnArgs &a, cudaStream_t stream);

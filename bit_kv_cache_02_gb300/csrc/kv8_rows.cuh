@@ -74,7 +74,7 @@ constexpr int kWinUnit = 16;  // tokens of a unit of the window
 // Three or four cost resident CTAs and were slower.
 constexpr int kSlots = 2;
 
-template <int D, int HALVES>
+template <int D, int HALVES, bool FINE>
 struct Smem {
   static constexpr int SLOTS = D == 128 ? kSlots : 2 * kSlots;
   static constexpr int HALF = kUnit * D;   // bytes of a unit's keys (and of its values)
@@ -84,8 +84,11 @@ struct Smem {
   static constexpr int ML = META + kWarps * SLOTS * 8;               // [kWarps][16] float2
   // the merge buffer; before the merge, sixteen rows' queries
   static constexpr int XCH = (ML + kWarps * kRowTile * 8 + 15) / 16 * 16;
-  static_assert(HALVES == 1 || kWarps * 3 * (NT / 4) * 32 * 4 >= D / 16 * 512, "queries");
-  static constexpr int FLAG = XCH + kWarps * 3 * (NT / 4) * 32 * 4;
+  // (with FINE of each warp: they may be at different triples)
+  static constexpr int QUERIES = HALVES == 1 ? 0 : D / 16 * 512;
+  static constexpr int MERGE = kWarps * 3 * (NT / 4) * 32 * 4;
+  static_assert(MERGE >= QUERIES, "queries");
+  static constexpr int FLAG = XCH + (FINE && kWarps * QUERIES > MERGE ? kWarps * QUERIES : MERGE);
   static constexpr int BYTES = FLAG + 16;
 };
 
@@ -244,10 +247,10 @@ struct Work {
   int tiles;  // row tiles per KV head
 };
 
-template <bool SHARED>
+template <bool FINE>
 __device__ __forceinline__ Work seq_work(const AttnArgs &a, int s) {
   Work w;
-  w.q = load_seg<SHARED>(a, s);
+  w.q = load_seg<FINE>(a, s);
   const int L = w.q.L;
   const bool some = w.q.n > 0 && w.q.n * a.group <= a.rows_max && L > 0 && L <= a.max_len;
   const int nb = L / a.geo.B;
@@ -256,14 +259,35 @@ __device__ __forceinline__ Work seq_work(const AttnArgs &a, int s) {
   w.tiles = some ? (w.q.n * a.group + kRowTile - 1) / kRowTile : 0;
   return w;
 }
-__device__ __forceinline__ long long line_of(const Work &w, int H) {
-  return static_cast<long long>(w.units) * w.tiles * H;
+
+// How a triple counts on the line.  Plainly, by its units.
+struct Plain {
+  __device__ __forceinline__ int cost(const Work &w) const { return w.units; }
+};
+// Finely (FINE): a triple costs more than its units, for its queries, the merge
+// of the warps and the outputs, whatever its length.  Short ones are not cut, and
+// one warp does all of a short one, its neighbours the next ones: they cost
+// little besides, and no barrier.  `each`: one triple per CTA, none cut.
+constexpr int kShort = 4, kOverShort = 2, kOver = 8;
+constexpr int kEach = 4 * kWarps;
+struct Fine {
+  bool each;
+  __device__ __forceinline__ bool is_short(const Work &w) const { return !each && w.units <= kShort; }
+  __device__ __forceinline__ int over(const Work &w) const { return w.units <= kShort ? kOverShort : kOver; }
+  __device__ __forceinline__ int cost(const Work &w) const { return w.units == 0 ? 0 : each ? 1 : w.units + over(w); }
+};
+template <typename C>
+__device__ __forceinline__ long long line_of(const C &c, const Work &w, int H) {
+  return static_cast<long long>(c.cost(w)) * w.tiles * H;
 }
 
 // Walks a CTA's range of the line, one part of a (sequence, head, tile)
 // triple at a time.
-template <bool SHARED>
-struct Walk {
+template <bool FINE>
+struct Walk;
+
+template <>
+struct Walk<false> {
   Work w;
   int s, h, tile;
   long long at, end;  // line position and end of the range
@@ -275,9 +299,10 @@ struct Walk {
     start = at - u0;
   }
   // the sequence that holds line position `pos`, whose own line starts at `base`
-  __device__ __forceinline__ void enter(const AttnArgs &a, int seq, long long base, long long pos, long long end_) {
+  __device__ __forceinline__ bool enter(const AttnArgs &a, Plain, int seq, long long base, long long pos,
+                                        long long end_) {
     s = seq;
-    w = seq_work<SHARED>(a, s);
+    w = seq_work<false>(a, s);
     at = pos;
     end = end_;
     const int pair = static_cast<int>(divide(pos - base, w.units));
@@ -285,6 +310,7 @@ struct Walk {
     h = pair / w.tiles;
     tile = pair - h * w.tiles;
     part();
+    return true;
   }
   // the next part; false at the end of the range
   __device__ __forceinline__ bool next(const AttnArgs &a) {
@@ -297,21 +323,148 @@ struct Walk {
         h = 0;
         do {
           if (++s >= a.segs) return false;
-          w = seq_work<SHARED>(a, s);
+          w = seq_work<false>(a, s);
         } while (w.units == 0);
       }
     }
     part();
     return true;
   }
+  // a warp's first unit of the part, and the step to its next one
+  __device__ __forceinline__ int begin(int warp) const { return u0 + warp; }
+  __device__ __forceinline__ int step() const { return kWarps; }
+  __device__ __forceinline__ bool alone() const { return false; }
+  __device__ __forceinline__ bool behind(long long lo) const { return start + u0 != lo; }
+  __device__ __forceinline__ long long front() const { return start; }
 };
 
-template <int D, int FMT, bool BF16, int HALVES, bool SHARED>
+template <>
+struct Walk<true> {
+  Work w;
+  int s, h, tile;
+  Fine c;
+  int u0, u1, turn;  // units of the current part; whose turn it is to take a short triple
+  long long lo, end;
+  long long first;   // the triple's first line position
+  long long start;   // the position of its unit 0
+
+  __device__ __forceinline__ bool part() {
+    start = first + (c.each ? 0 : c.over(w));
+    if (alone()) turn = (turn + 1) & (kWarps - 1);
+    if (c.each || alone()) {  // the CTA that has the first position has all of it
+      u0 = 0;
+      u1 = w.units;
+      return first >= lo;
+    }
+    u0 = static_cast<int>(max(lo - start, 0ll));
+    u1 = static_cast<int>(min(static_cast<long long>(w.units), end - start));
+    return u1 > u0;
+  }
+  __device__ __forceinline__ bool enter(const AttnArgs &a, Fine cost, int seq, long long base, long long pos,
+                                        long long end_) {
+    s = seq;
+    c = cost;
+    w = seq_work<true>(a, s);
+    turn = 0;
+    lo = pos;
+    end = end_;
+    const int pair = static_cast<int>(divide(pos - base, c.cost(w)));
+    first = base + static_cast<long long>(pair) * c.cost(w);
+    h = pair / w.tiles;
+    tile = pair - h * w.tiles;
+    return part() || next(a);
+  }
+  __device__ __forceinline__ bool next(const AttnArgs &a) {
+    do {
+      first += c.cost(w);
+      if (first >= end) return false;
+      if (++tile >= w.tiles) {
+        tile = 0;
+        if (++h >= a.geo.H) {
+          h = 0;
+          do {
+            if (++s >= a.segs) return false;
+            w = seq_work<true>(a, s);
+          } while (w.units == 0);
+        }
+      }
+    } while (!part());
+    return true;
+  }
+  __device__ __forceinline__ int begin(int warp) const { return !alone() ? u0 + warp : turn == warp ? 0 : u1; }
+  __device__ __forceinline__ int step() const { return alone() ? 1 : kWarps; }
+  __device__ __forceinline__ bool alone() const { return c.is_short(w); }
+  // whether the triple begins behind the range's start
+  __device__ __forceinline__ bool behind(long long) const { return lo < first; }
+  __device__ __forceinline__ long long front() const { return first; }
+};
+
+// N contiguous channels of a row, in 4 N bytes or as 16-bit floats.
+template <int N>
+__device__ __forceinline__ void put32(float *dst, const float (&o)[N]) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int j = 0; j < N; j += 4)
+      *reinterpret_cast<float4 *>(dst + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; j += 2) *reinterpret_cast<float2 *>(dst + j) = make_float2(o[j], o[j + 1]);
+  }
+}
+template <bool BF16, int N>
+__device__ __forceinline__ void put16(uint16_t *dst, const float (&o)[N], float f) {
+  uint32_t e[N / 2];
+#pragma unroll
+  for (int j = 0; j < N / 2; ++j) e[j] = pack2<BF16>(o[2 * j] * f, o[2 * j + 1] * f);
+  if constexpr (N % 8 == 0) {
+#pragma unroll
+    for (int j = 0; j < N / 2; j += 4) *reinterpret_cast<uint4 *>(dst + 2 * j) = make_uint4(e[j], e[j + 1], e[j + 2], e[j + 3]);
+  } else if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int j = 0; j < N / 2; j += 2) *reinterpret_cast<uint2 *>(dst + 2 * j) = make_uint2(e[j], e[j + 1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) *reinterpret_cast<uint32_t *>(dst + 2 * j) = e[j];
+  }
+}
+
+// N channels from `ch` on of a row's weighted sum: divided and stored, joined
+// before with what the launch over the shared blocks has left, or left for the
+// launch behind it (`lead`: this thread leaves max and sum too).
+template <int D, bool BF16, bool FINE, int N>
+__device__ __forceinline__ void emit(const AttnArgs &a, const Work &w, int h, int row, int ch, float (&o)[N], float m,
+                                     float l, bool lead) {
+  const int tok = row / a.group, head = h * a.group + row - tok * a.group;
+  if (FINE && a.part == kPrefix) {
+    const size_t at = carry_at(a, w.q.row0 + tok, head);
+    put32(a.carry_o + at * D + ch, o);
+    if (lead) a.carry_ml[at] = make_float2(m, l);
+    return;
+  }
+  float sum = l;
+  if (FINE && w.q.base) {
+    const size_t at = carry_at(a, w.q.row0 + tok, head);
+    const float *src = a.carry_o + at * D + ch;
+    const Join n = join(make_float2(m, l), a.carry_ml[at]);
+    sum = n.sum;
+#pragma unroll
+    for (int j = 0; j < N; j += 2) {
+      const float2 x = *reinterpret_cast<const float2 *>(src + j);
+      o[j] = fmaf(o[j], n.x, x.x * n.y);
+      o[j + 1] = fmaf(o[j + 1], n.x, x.y * n.y);
+    }
+  }
+  put16<BF16>(a.out.p + (static_cast<long long>(w.q.row0) + tok) * a.out.row + head * a.out.head + ch, o,
+              inverse_sum(sum, last_seen(a, w.q, tok)));
+}
+
+template <int D, int FMT, bool BF16, int HALVES, bool FINE>
 __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
-  using SM = Smem<D, HALVES>;
+  using SM = Smem<D, HALVES, FINE>;
   constexpr int NT = SM::NT;  // output n-tiles
   constexpr int KS = D / 16;  // k-steps of the scores
   extern __shared__ __align__(128) unsigned char smem[];
+  follow<FINE>();
   const Geo &geo = a.geo;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q4 = lane & 3;
   const int B = geo.B, H = geo.H;
@@ -319,20 +472,28 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
 
   // The line's length.  On the way, a CTA writes the zero rows of its share of
   // the sequences with rows and nothing to see.
-  long long total = 0, triples = 0;
+  // (FINE: `total` counts a triple's units alone at first)
+  using Cost = std::conditional_t<FINE, Fine, Plain>;
+  Cost cost = {};
+  long long total = 0, triples = 0, dear = 0;
+  int most = 0;
   for (int s0 = 0; s0 < a.segs; s0 += 32) {
     Work w = {};
     bool blind = false;
     if (s0 + lane < a.segs) {
-      w = seq_work<SHARED>(a, s0 + lane);
+      w = seq_work<FINE>(a, s0 + lane);
       blind = !w.q.ok || (w.q.n > 0 && (w.q.L <= 0 || w.q.L > a.max_len));
     }
-    total += line_of(w, H);
+    total += line_of(Plain{}, w, H);
     triples += static_cast<long long>(w.tiles) * H;
+    if constexpr (FINE) {
+      dear += line_of(cost, w, H);
+      most = max(most, w.units);
+    }
     for (unsigned m = __ballot_sync(kAll, blind); m; m &= m - 1) {
       const int s = s0 + __ffs(m) - 1;
       if (s % gridDim.x != blockIdx.x) continue;
-      const Seg sq = load_seg<SHARED>(a, s);
+      const Seg sq = load_seg<FINE>(a, s);
       if (tid == 0 && (!sq.ok || sq.L != 0)) set_status(geo.status, sq.ok ? KVQ_STATUS_MAX_LEN : KVQ_STATUS_BAD_LEN);
       const int per_row = a.Hq * (D / 8);  // (a bad sequence has no rows)
       for (long long i = tid; i < static_cast<long long>(sq.n) * per_row; i += kWarps * 32) {
@@ -346,24 +507,32 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
   for (int o = 16; o; o >>= 1) {
     total += __shfl_xor_sync(kAll, total, o);
     triples += __shfl_xor_sync(kAll, triples, o);
+    if (FINE) dear += __shfl_xor_sync(kAll, dear, o);
   }
   // This CTA's range of the line.  Two units for each warp at least.  A multiple of the triples where that
   // costs little, for then triples of one length are cut alike, and one CTA for
   // each where they are short: merging parts takes as long as four units of a
   // warp (one sequence of 300 tokens, 8 KV heads: 9.1 us instead of 13.9).
   long long want = min(static_cast<long long>(gridDim.x), (total + 2 * kWarps - 1) / (2 * kWarps));
-  if (want >= 4 * triples)
+  if constexpr (FINE) {
+    // As many CTAs as triples where those are few and none is long.
+    most = __reduce_max_sync(kAll, most);
+    cost.each = triples <= gridDim.x && most <= kEach;
+    total = cost.each ? triples : dear;
+    if (cost.each) want = triples;
+  } else if (want >= 4 * triples)
     want = triples ? divide(want, triples) * triples : want;
   else if (triples <= gridDim.x && total <= triples * 4 * kWarps)
     want = triples;
   const int ctas = static_cast<int>(min(want, total));
   if (static_cast<int>(blockIdx.x) >= ctas) return;
   const long long lo = divide(blockIdx.x * total, ctas), hi = divide((blockIdx.x + 1) * total, ctas);
-  Walk<SHARED> use;
+  Walk<FINE> use;
+  bool live;
   {
     long long base = 0;
     for (int s0 = 0;; s0 += 32) {
-      const long long mine = s0 + lane < a.segs ? line_of(seq_work<SHARED>(a, s0 + lane), H) : 0;
+      const long long mine = s0 + lane < a.segs ? line_of(cost, seq_work<FINE>(a, s0 + lane), H) : 0;
       long long incl = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -373,7 +542,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
       const unsigned past = __ballot_sync(kAll, base + incl > lo);
       if (past) {
         const int j = __ffs(past) - 1;
-        use.enter(a, s0 + j, base + __shfl_sync(kAll, incl - mine, j), lo, hi);
+        live = use.enter(a, cost, s0 + j, base + __shfl_sync(kAll, incl - mine, j), lo, hi);
         break;
       }
       base += __shfl_sync(kAll, incl, 31);
@@ -381,9 +550,9 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
   }
 
   // ---- fetch: the warp's units, in the order it will use them
-  Walk<SHARED> get = use;
-  bool more = true;
-  int gu = get.u0 + warp;  // next unit to fetch
+  Walk<FINE> get = use;
+  bool more = live;
+  int gu = get.begin(warp);  // next unit to fetch
   const uint32_t ring = kvq::smem_u32(smem) + warp * SM::SLOTS * SM::SLOT;
   const uint32_t meta = kvq::smem_u32(smem) + SM::META + warp * SM::SLOTS * 8;
   const int ushift = 26 - __clz(B);  // units per block: 1 << ushift
@@ -395,7 +564,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
   auto settle = [&]() {  // move to a part that has a unit for this warp
     while (more && gu >= get.u1) {
       more = get.next(a);
-      gu = get.u0 + warp;
+      gu = get.begin(warp);
     }
   };
   auto table_entry = [&]() -> int {
@@ -447,7 +616,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
           cp16z(vdst + off, geo.v_win + src, row < r);
         }
       }
-      gu += kWarps;
+      gu += get.step();
       settle();
       entry = table_entry();
     }
@@ -458,7 +627,8 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
   for (int i = 0; i < SM::SLOTS; ++i) fetch(i);
   int slot = 0;
 
-  for (bool live = true; live; live = use.next(a)) {
+  for (; live; live = use.next(a)) {
+    if (use.alone() && use.begin(warp) == use.u1) continue;  // another warp's
     const Work &w = use.w;
     const int n_rows = w.q.n * a.group;  // rows of this KV head
     const int r0 = use.tile * kRowTile;  // first row of the tile
@@ -599,7 +769,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
         }
       };
 
-      for (int u = use.u0 + warp; u < use.u1; u += kWarps) {
+      for (int u = use.begin(warp); u < use.u1; u += use.step()) {
         cp_wait<SM::SLOTS - 1>();
         __syncwarp();
         const uint32_t kt = ring + slot * SM::SLOT, vt = kt + SM::HALF;
@@ -786,9 +956,24 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
         l[r] *= kUnshift;
         if (g == 0) ml[warp * kRowTile + 2 * q4 + r] = make_float2(m[r], l[r]);
       }
+      if (FINE && use.alone()) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int row = r0 + 2 * q4 + r;
+          float x[2 * MT];
+#pragma unroll
+          for (int j = 0; j < MT; ++j) {
+            x[2 * j] = acc[j][r] * kUnshift;
+            x[2 * j + 1] = acc[j][r + 2] * kUnshift;
+          }
+          if (row < n_rows && row_in_bounds(a, w.q.row0, use.h, row))
+            emit<D, BF16, FINE>(a, w, use.h, row, (D / 8) * g, x, m[r], l[r], g == 0);
+        }
+        continue;
+      }
       __syncthreads();
       whole = use.u0 == 0 && use.u1 == w.units;
-      const int part = 2 * blockIdx.x + (use.start + use.u0 == lo ? 0 : 1);
+      const int part = 2 * blockIdx.x + (use.behind(lo) ? 1 : 0);
       constexpr int QT = MT / 4;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -829,30 +1014,14 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
         // m-tile j holds channels (D / 8) g + 2 j and the next one
         const int ch = (D / 8) * g + 2 * QT * warp, row = r0 + 2 * q4 + r;
         if (row < n_rows && row_in_bounds(a, w.q.row0, use.h, row) && KVQ_IN_BOUNDS(geo.status, part, 2 * kMaxCtas)) {
-          const int tok = row / a.group, head = use.h * a.group + row - tok * a.group;
-          if (SHARED && whole && a.part == kPrefix) {
-            const size_t at = carry_at(a, w.q.row0 + tok, head);
-            float *dst = a.carry_o + at * D + ch;
+          if (whole) {
+            float x[2 * QT];
 #pragma unroll
-            for (int j = 0; j < QT; ++j) *reinterpret_cast<float2 *>(dst + 2 * j) = o[j];
-            if (warp == 0 && g == 0) a.carry_ml[at] = make_float2(mm, ll);
-          } else if (whole) {
-            float inv = inverse_sum(ll, lim[r]);
-            if (SHARED && w.q.base) {
-              const size_t at = carry_at(a, w.q.row0 + tok, head);
-              const float *src = a.carry_o + at * D + ch;
-              const Join n = join(make_float2(mm, ll), a.carry_ml[at]);
-              inv = inverse_sum(n.sum, lim[r]);
-#pragma unroll
-              for (int j = 0; j < QT; ++j) {
-                const float2 c = *reinterpret_cast<const float2 *>(src + 2 * j);
-                o[j] = make_float2(fmaf(o[j].x, n.x, c.x * n.y), fmaf(o[j].y, n.x, c.y * n.y));
-              }
+            for (int j = 0; j < QT; ++j) {
+              x[2 * j] = o[j].x;
+              x[2 * j + 1] = o[j].y;
             }
-            uint16_t *dst = a.out.p + (static_cast<long long>(w.q.row0) + tok) * a.out.row + head * a.out.head + ch;
-#pragma unroll
-            for (int j = 0; j < QT; ++j)
-              *reinterpret_cast<uint32_t *>(dst + 2 * j) = pack2<BF16>(o[j].x * inv, o[j].y * inv);
+            emit<D, BF16, FINE>(a, w, use.h, row, ch, x, mm, ll, warp == 0 && g == 0);
           } else {
             float *dst = a.part_o + (static_cast<size_t>(part) * kRowTile + 2 * q4 + r) * D + ch;
 #pragma unroll
@@ -915,9 +1084,9 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
           q128[r] = 128.f * sum;
         }
       }
-      // They wait in shared memory, alike for all warps: in registers they cost
+      // They wait in shared memory, alike for all warps (but see FINE): in registers they cost
       // spills (16 sequences with 3 to 8 drafts: 3 us).
-      const uint32_t qs = kvq::smem_u32(smem) + SM::XCH + lane * 16;
+      const uint32_t qs = kvq::smem_u32(smem) + SM::XCH + (FINE ? warp * SM::QUERIES : 0) + lane * 16;
 #pragma unroll
       for (int k = 0; k < KS; ++k)
         asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(qs + k * 512), "r"(qa[k][0]), "r"(qa[k][1]),
@@ -1014,7 +1183,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
         p[3] = kvq::h2_as_u32(__floats2half2_rn(hi[2], hi[3]));
       };
 
-      for (int u = use.u0 + warp; u < use.u1; u += kWarps) {
+      for (int u = use.begin(warp); u < use.u1; u += use.step()) {
         cp_wait<SM::SLOTS - 1>();
         __syncwarp();
         const uint32_t kt = ring + slot * SM::SLOT, vt = kt + SM::HALF;
@@ -1231,9 +1400,24 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
             acc[j][2 * r + i] *= kUnshift;
         if (q4 == 0) ml[warp * kRowTile + g + 8 * r] = make_float2(m[r], l[r]);
       }
+      if (FINE && use.alone()) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int row = r0 + g + 8 * r;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float x[NT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) x[j] = acc[j][2 * r + c];
+            if (row < n_rows && row_in_bounds(a, w.q.row0, use.h, row))
+              emit<D, BF16, FINE>(a, w, use.h, row, (D / 8) * (2 * q4 + c), x, m[r], l[r], q4 == 0 && c == 0);
+          }
+        }
+        continue;
+      }
       __syncthreads();
       whole = use.u0 == 0 && use.u1 == w.units;
-      const int part = 2 * blockIdx.x + (use.start + use.u0 == lo ? 0 : 1);
+      const int part = 2 * blockIdx.x + (use.behind(lo) ? 1 : 0);
       constexpr int QT = NT / 4;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -1272,35 +1456,9 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
         const int ch0 = (D / 8) * (2 * q4) + warp * QT, ch1 = ch0 + D / 8;
         const int row = r0 + g + 8 * r;
         if (row < n_rows && row_in_bounds(a, w.q.row0, use.h, row) && KVQ_IN_BOUNDS(geo.status, part, 2 * kMaxCtas)) {
-          const int tok = row / a.group, head = use.h * a.group + row - tok * a.group;
-          if (SHARED && whole && a.part == kPrefix) {
-            const size_t at = carry_at(a, w.q.row0 + tok, head);
-            float *dst = a.carry_o + at * D;
-#pragma unroll
-            for (int j = 0; j < QT; j += 2) {
-              *reinterpret_cast<float2 *>(dst + ch0 + j) = make_float2(o0[j], o0[j + 1]);
-              *reinterpret_cast<float2 *>(dst + ch1 + j) = make_float2(o1[j], o1[j + 1]);
-            }
-            if (warp == 0 && q4 == 0) a.carry_ml[at] = make_float2(mm, ll);
-          } else if (whole) {
-            float inv = inverse_sum(ll, lim[r]);
-            if (SHARED && w.q.base) {
-              const size_t at = carry_at(a, w.q.row0 + tok, head);
-              const float *src = a.carry_o + at * D;
-              const Join n = join(make_float2(mm, ll), a.carry_ml[at]);
-              inv = inverse_sum(n.sum, lim[r]);
-#pragma unroll
-              for (int j = 0; j < QT; ++j) {
-                o0[j] = fmaf(o0[j], n.x, src[ch0 + j] * n.y);
-                o1[j] = fmaf(o1[j], n.x, src[ch1 + j] * n.y);
-              }
-            }
-            uint16_t *dst = a.out.p + (static_cast<long long>(w.q.row0) + tok) * a.out.row + head * a.out.head;
-#pragma unroll
-            for (int j = 0; j < QT; j += 2) {
-              *reinterpret_cast<uint32_t *>(dst + ch0 + j) = pack2<BF16>(o0[j] * inv, o0[j + 1] * inv);
-              *reinterpret_cast<uint32_t *>(dst + ch1 + j) = pack2<BF16>(o1[j] * inv, o1[j + 1] * inv);
-            }
+          if (whole) {
+            emit<D, BF16, FINE>(a, w, use.h, row, ch0, o0, mm, ll, warp == 0 && q4 == 0);
+            emit<D, BF16, FINE>(a, w, use.h, row, ch1, o1, mm, ll, false);
           } else {
             float *dst = a.part_o + (static_cast<size_t>(part) * kRowTile + g + 8 * r) * D;
 #pragma unroll
@@ -1333,7 +1491,8 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
       __syncthreads();
       const int rows = min(kRowTile, n_rows - r0);
       if (*flag && warp < rows) {
-        const int first = 2 * c0 + (divide(c0 * total, ctas) < s0 ? 1 : 0);  // later CTAs begin with their part
+        // later CTAs begin with their part
+        const int first = 2 * c0 + (divide(c0 * total, ctas) < use.front() ? 1 : 0);
         const int parts = c1 - c0 + 1;
         constexpr int W = D / 32;                // channels per lane
         constexpr int NR = HALVES == 1 ? 2 : 4;  // rows per warp, at once: warp + 4 k, or again the last one
@@ -1377,29 +1536,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
 #pragma unroll
         for (int k = 0; k < NR; ++k) {
           if (warp + kWarps * k >= rows || !row_in_bounds(a, w.q.row0, use.h, r0 + row[k])) break;
-          const int tok = (r0 + row[k]) / a.group;
-          const int head = use.h * a.group + r0 + row[k] - tok * a.group;
-          const size_t at = carry_at(a, w.q.row0 + tok, head);
-          if (SHARED && a.part == kPrefix) {
-            float *dst = a.carry_o + at * D + lane * W;
-#pragma unroll
-            for (int j = 0; j < W; j += 2) *reinterpret_cast<float2 *>(dst + j) = make_float2(o[k][j], o[k][j + 1]);
-            if (lane == 0) a.carry_ml[at] = make_float2(mm[k], ll[k]);
-            continue;
-          }
-          float sum = ll[k];
-          if (SHARED && w.q.base) {
-            const float *src = a.carry_o + at * D + lane * W;
-            const Join n = join(make_float2(mm[k], sum), a.carry_ml[at]);
-            sum = n.sum;
-#pragma unroll
-            for (int j = 0; j < W; ++j) o[k][j] = fmaf(o[k][j], n.x, src[j] * n.y);
-          }
-          const float inv = inverse_sum(sum, last_seen(a, w.q, tok));
-          uint16_t *dst = a.out.p + (static_cast<long long>(w.q.row0) + tok) * a.out.row + head * a.out.head + lane * W;
-#pragma unroll
-          for (int j = 0; j < W; j += 2)
-            *reinterpret_cast<uint32_t *>(dst + j) = pack2<BF16>(o[k][j] * inv, o[k][j + 1] * inv);
+          emit<D, BF16, FINE>(a, w, use.h, r0 + row[k], lane * W, o[k], mm[k], ll[k], lane == 0);
         }
       }
     }
@@ -1408,9 +1545,9 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
   cp_wait<0>();
 }
 
-template <int D, int FMT, bool BF16, int HALVES, bool SHARED>
+template <int D, int FMT, bool BF16, int HALVES, bool FINE>
 cudaError_t launch_one(const AttnArgs &a, cudaStream_t stream) {
-  auto kernel = rows_kernel<D, FMT, BF16, HALVES, SHARED>;
+  auto kernel = rows_kernel<D, FMT, BF16, HALVES, FINE>;
   // resident CTAs and SMs of each device, once looked up
   static std::atomic<int> resident[64], sm_count[64];
   int dev = 0;
@@ -1418,9 +1555,9 @@ cudaError_t launch_one(const AttnArgs &a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   int per = dev < 64 ? resident[dev].load() : 0, sms = dev < 64 ? sm_count[dev].load() : 0;
   if (per == 0 || sms == 0) {
-    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D, HALVES>::BYTES)) != cudaSuccess)
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D, HALVES, FINE>::BYTES)) != cudaSuccess)
       return e;
-    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kWarps * 32, Smem<D, HALVES>::BYTES)) != cudaSuccess)
+    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kWarps * 32, Smem<D, HALVES, FINE>::BYTES)) != cudaSuccess)
       return e;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
     // Three CTAs fit an SM where at most eight rows share the keys.  Few
@@ -1434,30 +1571,31 @@ cudaError_t launch_one(const AttnArgs &a, cudaStream_t stream) {
     }
   }
   // no more CTAs than units for their warps, as far as the host can tell
-  const long long seg_rows = SHARED && a.part == kPrefix ? a.max_group_rows : a.max_new;
+  const long long seg_rows = FINE && a.part == kPrefix ? a.max_group_rows : a.max_new;
   const long long most = min(seg_rows * a.group, static_cast<long long>(a.rows_max));
   const long long tiles = (most + kRowTile - 1) / kRowTile;
   const long long units = (a.max_len / kUnit + a.geo.B / kWinUnit) * tiles * a.geo.H * a.segs;
   long long grid = min(static_cast<long long>(kMaxCtas), static_cast<long long>(sms) * per);
   grid = max(1LL, min(grid, (units + kWarps - 1) / kWarps));
-  kernel<<<static_cast<unsigned>(grid), kWarps * 32, Smem<D, HALVES>::BYTES, stream>>>(a);
+  if (FINE) return launch_after(kernel, static_cast<unsigned>(grid), kWarps * 32, Smem<D, HALVES, FINE>::BYTES, stream, a);
+  kernel<<<static_cast<unsigned>(grid), kWarps * 32, Smem<D, HALVES, FINE>::BYTES, stream>>>(a);
   return cudaGetLastError();
 }
 
-template <int D, int FMT, bool BF16, bool SHARED>
+template <int D, int FMT, bool BF16, bool FINE>
 cudaError_t launch_halves(const AttnArgs &a, cudaStream_t stream) {
-  const long long seg_rows = SHARED && a.part == kPrefix ? a.max_group_rows : a.max_new;
-  return seg_rows * a.group <= 8 ? launch_one<D, FMT, BF16, 1, SHARED>(a, stream)
-                                 : launch_one<D, FMT, BF16, 2, SHARED>(a, stream);
+  const long long seg_rows = FINE && a.part == kPrefix ? a.max_group_rows : a.max_new;
+  return seg_rows * a.group <= 8 ? launch_one<D, FMT, BF16, 1, FINE>(a, stream)
+                                 : launch_one<D, FMT, BF16, 2, FINE>(a, stream);
 }
 
-template <int D, bool SHARED>
+template <int D, bool FINE>
 cudaError_t launch_dim(const AttnArgs &a, cudaStream_t stream) {
   if (a.geo.fmt == KV8_INT8)
-    return a.geo.bf16 ? launch_halves<D, KV8_INT8, true, SHARED>(a, stream)
-                      : launch_halves<D, KV8_INT8, false, SHARED>(a, stream);
-  return a.geo.bf16 ? launch_halves<D, KV8_E4M3, true, SHARED>(a, stream)
-                    : launch_halves<D, KV8_E4M3, false, SHARED>(a, stream);
+    return a.geo.bf16 ? launch_halves<D, KV8_INT8, true, FINE>(a, stream)
+                      : launch_halves<D, KV8_INT8, false, FINE>(a, stream);
+  return a.geo.bf16 ? launch_halves<D, KV8_E4M3, true, FINE>(a, stream)
+                    : launch_halves<D, KV8_E4M3, false, FINE>(a, stream);
 }
 
 }  // namespace rows

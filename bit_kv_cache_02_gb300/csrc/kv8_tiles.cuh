@@ -325,8 +325,12 @@ __device__ __forceinline__ Pair make_pair(const AttnArgs &a, int s, int rt) {
 // Sequence s owns the slots from row_start[s] * group / 256 + s on: at least
 // as many as row tile pairs.
 template <bool SHARED>
+__device__ __forceinline__ int slot_base(const AttnArgs &a, int s) {
+  return static_cast<int>(static_cast<long long>(row_start_of<SHARED>(a, s)) * a.group / kRows) + s;
+}
+template <bool SHARED>
 __device__ __forceinline__ Pair pair_of_slot(const AttnArgs &a, int slot) {
-  auto base = [&](int s) { return static_cast<int>(static_cast<long long>(row_start_of<SHARED>(a, s)) * a.group / kRows) + s; };
+  auto base = [&](int s) { return slot_base<SHARED>(a, s); };
   const int s = last_at_or_below(a.segs, slot, base);
   return make_pair<SHARED>(a, s, slot - base(s));
 }
@@ -505,6 +509,7 @@ template <int D, int FMT, bool BF16, bool SHARED>
 __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
   using SM = Smem<D>;
   extern __shared__ unsigned char raw[];
+  follow<SHARED>();
   unsigned char *smem = raw + ((1024 - (kvq::smem_u32(raw) & 1023)) & 1023);
   const uint32_t base = kvq::smem_u32(smem);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + SM::BAR);
@@ -546,7 +551,9 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
   // D 128: a prompt of 256 tokens 28.9 against 20.6 us, of 512 34.6 against 25.4,
   // a chunk of 128 over 2000 42.1 against 35.2) and slower with sixteen (47.6,
   // 49.8, 55.9).
-  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + 7) / 8));
+  // Over shared blocks two: their parts are joined by another kernel, by all SMs.
+  const int least = SHARED && a.part == kPrefix ? 2 : 8;
+  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + least - 1) / least));
   if (static_cast<int>(blockIdx.x) >= ctas) return;
   const long long lo = divide(blockIdx.x * total, ctas), hi = divide((blockIdx.x + 1) * total, ctas);
   {
@@ -739,6 +746,10 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
             p.slot = 2 * blockIdx.x + (lo < use.start ? 1 : 0);
             p.first = 2 * c0 + (divide(c0 * total, ctas) < use.start ? 1 : 0);
           }
+          // for the kernel that joins them
+          if (SHARED && a.part == kPrefix && use.u0 == 0)
+            a.items[static_cast<size_t>(slot_base<SHARED>(a, use.p.s) + use.p.rt) * H + use.h] =
+                make_int4(p.first, p.c0, p.slot < 0 ? 0 : p.cuts + 1, 0);
         }
         kvq::mbar_arrive(bars + kPartFull + n_part % kParts);
         if (!more) break;
@@ -1128,8 +1139,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
                 pack2<BF16>(o[8 * k + 2] * f, o[8 * k + 3] * f), pack2<BF16>(o[8 * k + 4] * f, o[8 * k + 5] * f),
                 pack2<BF16>(o[8 * k + 6] * f, o[8 * k + 7] * f));
       };
-      // With shared blocks: 32 channels of the row's partial result, for the
-      // launch that joins it, or joined with what the other launch has left.
+      // With shared blocks: 32 channels of the row's partial result, left for the
+      // other launch, or joined with what that has left.
       const size_t carry = SHARED ? carry_at(a, p.row0 + tok, static_cast<int>(head)) : 0;
       auto leave = [&](int c, const float *o, float top, float sum) {
         if (!valid || !inside) return;
@@ -1198,7 +1209,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           a.tile_ml[slot * kRows + t * 128 + r] = make_float2(M, l);
         fence_before();
       }
-      if (!whole) {
+      if (!whole && !(SHARED && a.part == kPrefix)) {
         ok = bar_all(2, 512, ok);
         if (!ok) break;
         if (tid == 0) {
@@ -1243,12 +1254,9 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
                 o[4 * k + 3] = fmaf(o[4 * k + 3], was, x[k].w * f);
               }
             }
-            if (SHARED && a.part == kPrefix)
-              leave(c, o, mm, ll);
-            else
-              finish(c, o, mm, ll);
+            finish(c, o, mm, ll);
           }
-          if (!(SHARED && a.part == kPrefix)) store_rows();
+          store_rows();
         }
       }
       __syncwarp();
@@ -1278,6 +1286,7 @@ cudaError_t launch_one(const AttnArgs &a, cudaStream_t stream) {
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
     if (dev < 64) sm_count[dev].store(sms);
   }
+  if (SHARED) return launch_after(kernel, min(sms, kMaxTileCtas), kThreads, Smem<D>::BYTES, stream, a);
   kernel<<<min(sms, kMaxTileCtas), kThreads, Smem<D>::BYTES, stream>>>(a);
   return cudaGetLastError();
 }

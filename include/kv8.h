@@ -55,7 +55,6 @@ extern "C" {
 
 #define KV8_MAX_CAPACITY (1 << 30)
 #define KV8_MAX_AXES 4
-#define KV8_MAX_GROUPS 65535
 
 /* a bit of the status word, beside KVQ_STATUS_*: a position outside the table */
 #define KV8_STATUS_BAD_POSITION 64
@@ -303,13 +302,13 @@ int kv8_cross_attn(const kv8_cache *cache, int32_t num_q_heads, const kv8_rows *
  *              sequences' entries for them are not read.  Each sequence of the
  *              group has stored them before the call's new tokens: prefix_len,
  *              rounded down, is at most seq_len[s] minus its new rows.
- *   num_groups 1 .. KV8_MAX_GROUPS.
+ *   num_groups 1 .. S.
  *   max_group_rows  host bound on the rows of one group's sequences together.
  *   workspace  at least kv8_shared_attn_workspace_bytes() for these rows, max_new
  *              and max_group_rows (a size that serves larger ones serves smaller
  *              ones), with the rules of kv8_attn's; it may serve kv8_attn and
- *              kv8_cross_attn too.  4 D + 8 bytes per row and query head on top of
- *              kv8_attn's size.
+ *              kv8_cross_attn too.  4 D + 8 bytes per row and query head, and a
+ *              few per sequence, on top of kv8_attn's size.
  *
  * A group with bad bounds, a bad prefix_len, more rows than max_group_rows or a
  * first sequence that ends within the shared blocks is invalid: the rows of its
@@ -317,7 +316,7 @@ int kv8_cross_attn(const kv8_cache *cache, int32_t num_q_heads, const kv8_rows *
  * KVQ_STATUS_BAD_LEN is set.  Neither row_start nor group_start may decrease:
  * where one does, that bit is set and the rows of all sequences are undefined.
  * Otherwise results are as kv8_attn describes them, for a table in which all
- * sequences of a group have its first one's entries.  Two to four kernels.
+ * sequences of a group have its first one's entries.  Three to six kernels.
  */
 int64_t kv8_shared_attn_workspace_bytes(const kv8_cache *cache, int32_t num_q_heads, int32_t rows, int32_t max_new,
                                         int32_t max_group_rows);
