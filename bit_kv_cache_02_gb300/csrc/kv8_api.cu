@@ -159,12 +159,12 @@ int attn_args(kv8::AttnArgs &a, const kv8_cache *cache, int32_t num_q_heads, con
 }
 
 // The regions of one launch's workspace.
-void place(kv8::AttnArgs &a, const kv8::AttnPlan &plan, void *workspace) {
-  uint8_t *ws = static_cast<uint8_t *>(workspace);
+void place(kv8::AttnArgs &a, const kv8::AttnPlan &plan, void *counters, void *regions) {
+  uint8_t *ws = static_cast<uint8_t *>(regions), *cnt = static_cast<uint8_t *>(counters);
   a.part_o = reinterpret_cast<float *>(ws + plan.off_o);
   a.part_ml = reinterpret_cast<float2 *>(ws + plan.off_ml);
-  a.counters = reinterpret_cast<int *>(ws + plan.off_cnt);
-  a.tile_counters = reinterpret_cast<int *>(ws + plan.off_tile_cnt);
+  a.counters = reinterpret_cast<int *>(cnt + plan.off_cnt);
+  a.tile_counters = reinterpret_cast<int *>(cnt + plan.off_tile_cnt);
   a.tile_o = reinterpret_cast<float *>(ws + plan.off_tile_o);
   a.tile_ml = reinterpret_cast<float2 *>(ws + plan.off_tile_ml);
   a.rows_max = plan.tiles ? kv8::kRowsMax : 2147483647;
@@ -185,7 +185,7 @@ int attend(const kv8_cache *cache, int32_t num_q_heads, const kv8_rows *q, const
   const kv8::AttnPlan plan = kv8::plan_attn(cache->head_dim, static_cast<int64_t>(a.group) * max_new);
   if ((e = check_workspace(workspace, workspace_bytes, plan.bytes))) return e;
   a.causal = causal;
-  place(a, plan, workspace);
+  place(a, plan, workspace, workspace);
   uint64_t n = 0;
   const cudaError_t ce = kv8::launch_attn(a, plan.tiles, static_cast<cudaStream_t>(stream), &n);
   return from_cuda(ce, n);
@@ -321,21 +321,21 @@ int kv8_shared_attn(const kv8_cache *cache, int32_t num_q_heads, const kv8_rows 
   uint64_t n = 1;
   cudaError_t ce = kv8::launch_segments(a, st);
   if (ce != cudaSuccess) return from_cuda(ce, n);
-  a.part = kv8::kPrefix;
-  a.causal = 0;
-  a.segs = num_groups;
-  place(a, kv8::plan_attn(cache->head_dim, group * max_group_rows), workspace);
-  ce = kv8::launch_attn(a, plan.prefix_tiles, st, &n);
+  a.part = kv8::kOwn;
+  a.first = 1;
+  place(a, kv8::plan_attn(cache->head_dim, group * max_new), ws, ws);
+  ce = kv8::launch_attn(a, plan.own_tiles, st, &n);
+  if (ce == cudaSuccess) {
+    a.part = kv8::kPrefix;
+    a.first = 0;
+    a.causal = 0;
+    a.segs = num_groups;
+    place(a, kv8::plan_attn(cache->head_dim, group * max_group_rows), ws + kv8::kCounters, ws + plan.off_prefix);
+    ce = kv8::launch_attn(a, plan.prefix_tiles, st, &n);
+  }
   if (ce == cudaSuccess && plan.prefix_tiles) {
     ++n;
     ce = kv8::launch_join(a, st);
-  }
-  if (ce == cudaSuccess) {
-    a.part = kv8::kOwn;
-    a.causal = 1;
-    a.segs = cache->num_seqs;
-    place(a, kv8::plan_attn(cache->head_dim, group * max_new), workspace);
-    ce = kv8::launch_attn(a, plan.own_tiles, st, &n);
   }
   return from_cuda(ce, n);
 }
@@ -351,7 +351,8 @@ AttnPlan plan_attn(int D, long long rows_per_head) {
   // the counters first, at offsets that no argument moves
   p.off_cnt = 0;
   p.off_tile_cnt = align(kMaxCtas * sizeof(int));
-  p.off_o = p.off_tile_cnt + align(kMaxTileCtas * sizeof(int));
+  static_assert(kCounters >= (kMaxCtas * sizeof(int) + 255) / 256 * 256 + kMaxTileCtas * sizeof(int), "counters");
+  p.off_o = 2 * kCounters;
   p.off_ml = p.off_o + static_cast<size_t>(2) * kMaxCtas * kRowTile * D * sizeof(float);
   p.off_tile_o = align(p.off_ml + static_cast<size_t>(2) * kMaxCtas * kRowTile * sizeof(float2));
   p.off_tile_ml = p.off_tile_o + static_cast<size_t>(2) * kMaxTileCtas * kTileRows * D * sizeof(float);
@@ -368,7 +369,8 @@ SharedPlan plan_shared(int D, int S, int H, int num_q_heads, long long rows, lon
   const AttnPlan own = plan_attn(D, group * max_new), prefix = plan_attn(D, group * max_group_rows);
   p.own_tiles = own.tiles;
   p.prefix_tiles = prefix.tiles;
-  p.off_segs = own.bytes > prefix.bytes ? own.bytes : prefix.bytes;
+  p.off_prefix = own.bytes;
+  p.off_segs = own.bytes + prefix.bytes;
   p.off_items = align(p.off_segs + static_cast<size_t>(2) * S * 2 * sizeof(int4));
   // (a group has at most one row tile pair that is not full)
   const size_t items = p.prefix_tiles ? (static_cast<size_t>(rows) * group / kTileRows + S) * H : 0;
@@ -381,13 +383,22 @@ SharedPlan plan_shared(int D, int S, int H, int num_q_heads, long long rows, lon
 
 cudaError_t launch_attn(const AttnArgs &a, bool tiles, cudaStream_t stream, uint64_t *launches) {
   const bool wide = a.geo.D == 128, shared = a.part != kWhole;
-  ++*launches;
-  cudaError_t e = shared ? (wide ? launch_rows_128_shared(a, stream) : launch_rows_64_shared(a, stream))
-                         : (wide ? launch_rows_128(a, stream) : launch_rows_64(a, stream));
-  if (e != cudaSuccess || !tiles) return e;
-  ++*launches;
-  return shared ? (wide ? launch_tiles_128_shared(a, stream) : launch_tiles_64_shared(a, stream))
-                : (wide ? launch_tiles_128(a, stream) : launch_tiles_64(a, stream));
+  auto rows_kernel = [&]() {
+    ++*launches;
+    return shared ? (wide ? launch_rows_128_shared(a, stream) : launch_rows_64_shared(a, stream))
+                  : (wide ? launch_rows_128(a, stream) : launch_rows_64(a, stream));
+  };
+  auto tile_kernel = [&]() {
+    ++*launches;
+    return shared ? (wide ? launch_tiles_128_shared(a, stream) : launch_tiles_64_shared(a, stream))
+                  : (wide ? launch_tiles_128(a, stream) : launch_tiles_64(a, stream));
+  };
+  if (!tiles) return rows_kernel();
+  // Over shared blocks the tile kernel goes first: the CTAs of the other one, which
+  // wait for all before them, would keep it from the SMs.
+  cudaError_t e = a.part == kPrefix ? tile_kernel() : rows_kernel();
+  if (e != cudaSuccess) return e;
+  return a.part == kPrefix ? rows_kernel() : tile_kernel();
 }
 
 }  // namespace kv8

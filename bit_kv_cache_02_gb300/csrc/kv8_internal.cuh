@@ -146,21 +146,25 @@ constexpr int kTileRows = 256;      // rows of an item of the tile kernel
 constexpr int kMaxTileCtas = 160;
 
 // Byte offsets of the workspace regions.  One merge counter per CTA of either
-// kernel comes first, at places that do not depend on the call: what a call of
-// one shape leaves of its partial results is never another's counter.  Rows
+// kernel comes first, and a second set for the launches over shared blocks, at
+// places that do not depend on the call: what a call of one shape leaves of its
+// partial results is never another's counter.  Rows
 // kernel: partial outputs [2 kMaxCtas][16][D] and their (max, sum).  Tile
 // kernel, where a sequence can bring enough rows: the same for
 // [2 kMaxTileCtas][256].
+constexpr size_t kCounters = 3328;  // bytes of a set: kMaxCtas and kMaxTileCtas counters, to 256
 struct AttnPlan {
   size_t off_cnt, off_tile_cnt, off_o, off_ml, off_tile_o, off_tile_ml, bytes;
   bool tiles;
 };
 AttnPlan plan_attn(int D, long long rows_per_head);
 
-// Attention with shared blocks: the two launches follow each other on the same
-// regions, and the partial results that one leaves for the other lie behind them.
+// Attention with shared blocks.  What lies behind them comes first: its kernels
+// leave partial results (carry) for the rows whose group shares blocks.  The
+// kernels over the shared blocks join them and write the outputs.  They need not
+// wait for the others until then, so each has regions of its own.
 struct SharedPlan {
-  size_t off_segs, off_items, off_ml, off_o, bytes;
+  size_t off_prefix, off_segs, off_items, off_ml, off_o, bytes;
   bool own_tiles, prefix_tiles;
 };
 SharedPlan plan_shared(int D, int S, int H, int num_q_heads, long long rows, long long max_new,
@@ -169,8 +173,8 @@ SharedPlan plan_shared(int D, int S, int H, int num_q_heads, long long rows, lon
 // What one launch attends to, segment by segment.
 enum {
   kWhole,   // sequences: their whole length
-  kPrefix,  // groups of sequences: the blocks that they share, for the rows of all; leaves partial results
-  kOwn,     // sequences: what lies behind the blocks shared with their group; joins the partial results
+  kOwn,     // sequences: what lies behind the blocks shared with their group; leaves partial results
+  kPrefix,  // groups of sequences: the blocks that they share, for the rows of all; joins the partial results
 };
 
 struct AttnArgs {
@@ -183,8 +187,9 @@ struct AttnArgs {
   int groups, max_group_rows;
   int4 *plan;        // two per segment: the groups', then the sequences'
   int4 *items;       // of the tile kernel's items over shared blocks: the parts to join
-  float *carry_o;    // [rows][Hq][D]: unnormalized outputs over the shared blocks
-  float2 *carry_ml;  // [rows][Hq]: (max, sum) in log2 units
+  int first;         // the first launch behind the lookup of the segments
+  float *carry_o;    // [rows][Hq][D]: unnormalized outputs over what lies behind the shared blocks
+  float2 *carry_ml;  // [rows][Hq]: (max, sum) in log2 units; sum -1: the row is not to be written
   Rows q, out;
   const int *row_start;
   int rows, max_new, max_len;
@@ -237,13 +242,14 @@ __device__ __forceinline__ Group load_group(const AttnArgs &a, int g) {
 }
 
 // The sequence's segment, behind the blocks that it shares with its group.
-__device__ __forceinline__ Seg own_seg(const AttnArgs &a, int s) {
+// `shut`: the group has shared blocks, but this sequence's rows have no part in them.
+__device__ __forceinline__ Seg own_seg(const AttnArgs &a, int s, bool &shut) {
   const Seq q = load_seq(a.geo, a.row_start, a.rows, a.max_new, s);
   Seg x = {q.L, q.n, q.row0, 0, s, q.ok};
-  if (q.n > 0 && q.L <= a.max_len) {
-    const int g = last_at_or_below(a.groups, s, [&](int i) { return a.group_start[i]; });
-    if (a.group_start[g] <= s && s < a.group_start[g + 1]) {
-      const Group of = load_group(a, g);
+  const int g = last_at_or_below(a.groups, s, [&](int i) { return a.group_start[i]; });
+  if (a.group_start[g] <= s && s < a.group_start[g + 1]) {
+    const Group of = load_group(a, g);
+    if (q.n > 0 && q.L <= a.max_len) {
       if (!of.ok || (of.blocks && q.L - q.n < of.blocks * a.geo.B)) {
         x.ok = false;
         x.n = 0;
@@ -252,6 +258,7 @@ __device__ __forceinline__ Seg own_seg(const AttnArgs &a, int s) {
         x.L -= of.blocks * a.geo.B;
       }
     }
+    shut = of.ok && of.blocks && !x.base;
   }
   return x;
 }
@@ -276,14 +283,21 @@ __device__ __forceinline__ Seg load_seg(const AttnArgs &a, int s) {
   return {q.L, q.n, q.row0, 0, s, q.ok};
 }
 
-// The kernels of one call with shared blocks are launched while the one before
-// still runs; each waits here, first of all, until that one's results are there.
+// The kernels of one call with shared blocks start while the ones before still
+// run.  Each lets the next one start once the segments are there: the first waits
+// for them, and the others start behind it.  Each waits for the one before it
+// at the latest before it ends, so that the end of one is the end of all before.
+__device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 template <bool SHARED>
-__device__ __forceinline__ void follow() {
+__device__ __forceinline__ void start(const AttnArgs &a) {
   if (SHARED) {
-    asm volatile("griddepcontrol.launch_dependents;");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (a.first) wait_before();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   }
+}
+template <bool SHARED>
+__device__ __forceinline__ void finish() {
+  if (SHARED) wait_before();
 }
 template <typename... A>
 cudaError_t launch_after(void (*kernel)(A...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream,

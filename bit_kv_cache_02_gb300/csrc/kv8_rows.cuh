@@ -268,7 +268,7 @@ struct Plain {
 // of the warps and the outputs, whatever its length.  Short ones are not cut, and
 // one warp does all of a short one, its neighbours the next ones: they cost
 // little besides, and no barrier.  `each`: one triple per CTA, none cut.
-constexpr int kShort = 4, kOverShort = 2, kOver = 8;
+constexpr int kShort = 4, kOverShort = 2, kOver = 14;
 constexpr int kEach = 4 * kWarps;
 struct Fine {
   bool each;
@@ -429,23 +429,26 @@ __device__ __forceinline__ void put16(uint16_t *dst, const float (&o)[N], float 
 }
 
 // N channels from `ch` on of a row's weighted sum: divided and stored, joined
-// before with what the launch over the shared blocks has left, or left for the
-// launch behind it (`lead`: this thread leaves max and sum too).
+// before with what the launch behind the shared blocks has left, or left for
+// the launch over them (`lead`: this thread leaves max and sum too).
 template <int D, bool BF16, bool FINE, int N>
 __device__ __forceinline__ void emit(const AttnArgs &a, const Work &w, int h, int row, int ch, float (&o)[N], float m,
                                      float l, bool lead) {
   const int tok = row / a.group, head = h * a.group + row - tok * a.group;
-  if (FINE && a.part == kPrefix) {
+  if (FINE && w.q.base) {
     const size_t at = carry_at(a, w.q.row0 + tok, head);
     put32(a.carry_o + at * D + ch, o);
     if (lead) a.carry_ml[at] = make_float2(m, l);
     return;
   }
   float sum = l;
-  if (FINE && w.q.base) {
+  if (FINE && a.part == kPrefix) {
+    wait_before();
     const size_t at = carry_at(a, w.q.row0 + tok, head);
+    const float2 own = a.carry_ml[at];
+    if (own.y < 0.f) return;
     const float *src = a.carry_o + at * D + ch;
-    const Join n = join(make_float2(m, l), a.carry_ml[at]);
+    const Join n = join(make_float2(m, l), own);
     sum = n.sum;
 #pragma unroll
     for (int j = 0; j < N; j += 2) {
@@ -459,12 +462,12 @@ __device__ __forceinline__ void emit(const AttnArgs &a, const Work &w, int h, in
 }
 
 template <int D, int FMT, bool BF16, int HALVES, bool FINE>
-__global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, FINE && HALVES == 1 && (FMT == KV8_E4M3 || D == 64) ? 3 : 1) rows_kernel(const AttnArgs a) {
   using SM = Smem<D, HALVES, FINE>;
   constexpr int NT = SM::NT;  // output n-tiles
   constexpr int KS = D / 16;  // k-steps of the scores
   extern __shared__ __align__(128) unsigned char smem[];
-  follow<FINE>();
+  start<FINE>(a);
   const Geo &geo = a.geo;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q4 = lane & 3;
   const int B = geo.B, H = geo.H;
@@ -525,7 +528,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
   else if (triples <= gridDim.x && total <= triples * 4 * kWarps)
     want = triples;
   const int ctas = static_cast<int>(min(want, total));
-  if (static_cast<int>(blockIdx.x) >= ctas) return;
+  if (static_cast<int>(blockIdx.x) >= ctas) return finish<FINE>();
   const long long lo = divide(blockIdx.x * total, ctas), hi = divide((blockIdx.x + 1) * total, ctas);
   Walk<FINE> use;
   bool live;
@@ -1543,6 +1546,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const AttnArgs a) {
     __syncthreads();  // the merge buffers are free for the next part
   }
   cp_wait<0>();
+  finish<FINE>();
 }
 
 template <int D, int FMT, bool BF16, int HALVES, bool FINE>

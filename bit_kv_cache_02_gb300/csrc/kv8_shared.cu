@@ -7,66 +7,101 @@ namespace kv8 {
 namespace shared {
 
 constexpr int kSegThreads = 128;
-constexpr int kQuads = 4;  // float4 of a row that a thread of the join takes
 
 // A thread per group, then per sequence.
 __global__ void __launch_bounds__(kSegThreads) segments_kernel(const AttnArgs a) {
   asm volatile("griddepcontrol.launch_dependents;");
   const int i = blockIdx.x * kSegThreads + threadIdx.x;
   if (i >= a.groups + a.geo.S) return;
-  const Seg x = i < a.groups ? group_seg(a, i) : own_seg(a, i - a.groups);
+  bool shut = false;
+  const Seg x = i < a.groups ? group_seg(a, i) : own_seg(a, i - a.groups, shut);
   a.plan[2 * i] = make_int4(x.L, x.n, x.row0, x.base);
   a.plan[2 * i + 1] = make_int4(x.entry, x.ok, 0, 0);
+  if (shut) {
+    // rows that the launch over their group's blocks is not to write
+    const int s = i - a.groups;
+    const long long from = max(a.row_start ? a.row_start[s] : s, 0);
+    const long long to = min(a.row_start ? a.row_start[s + 1] : s + 1, a.rows);
+    for (long long k = from * a.Hq; k < to * a.Hq; ++k) a.carry_ml[k] = make_float2(0.f, -1.f);
+  }
 }
 
-// The parts of an item, a (group, 256 rows, KV head), over its keys: the CTAs of
-// the tile kernel leave them, and here a thread per row and 16 channels joins
-// them, all SMs together.  (The last CTA that finishes would read them alone: a
-// group of 256 rows, 8 KV heads, has 19 for each head.)
-template <int D>
-__global__ void __launch_bounds__(tiles::kRows) join_kernel(const AttnArgs a) {
-  follow<true>();
-  constexpr int PIECES = D / 4 / kQuads;
-  const int piece = blockIdx.x % PIECES, h = blockIdx.x / PIECES % a.geo.H;
-  const int slot = blockIdx.x / PIECES / a.geo.H, r = threadIdx.x;
+// The parts of an item, a (group, 256 rows, KV head), over its keys, and what the
+// launches behind the shared blocks have left: the CTAs of the tile kernel leave
+// them, and here a CTA joins 32 rows, 64 channels.  (The last CTA that finishes
+// would read them alone: a group of 256 rows, 8 KV heads, has 19 for each head.)
+// A thread takes eight channels of a row, from the parts with 32 rows side by
+// side, eight parts at a time; shared memory turns them into whole rows.
+constexpr int kJoinRows = 32, kJoinThreads = 256, kAtOnce = 8;
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnArgs a) {
+  constexpr int PIECES = D / 64, SUBS = tiles::kRows / kJoinRows;
+  const int piece = blockIdx.x % PIECES, sub = blockIdx.x / PIECES % SUBS, h = blockIdx.x / (PIECES * SUBS) % a.geo.H;
+  const int slot = blockIdx.x / (PIECES * SUBS) / a.geo.H;
   const tiles::Pair p = tiles::pair_of_slot<true>(a, slot);
-  if (!p.units) return;
-  const int row = p.rt * tiles::kRows + r;
-  if (row >= p.q.n * a.group || !row_in_bounds(a, p.q.row0, h, row)) return;
+  const int row0 = p.rt * tiles::kRows + sub * kJoinRows;  // (of no meaning without units)
+  const int n_rows = p.units ? p.q.n * a.group : 0;
+  wait_before();
+  if (!p.units || row0 >= n_rows) return;
   const int4 item = a.items[static_cast<size_t>(slot) * a.geo.H + h];
   const int first = item.x, c0 = item.y, n = item.z;
   // (where row_start or group_start falls, or a wait ran out, nothing was left here)
   if (n <= 0 || n > kMaxTileCtas || c0 < 0 || c0 > kMaxTileCtas - n || first < 0 || first >= 2 * kMaxTileCtas) return;
+  __shared__ float4 turned[kJoinRows][17];
+  __shared__ float2 sums[kJoinRows];
   const float ninf = __int_as_float(0xff800000);
-  float o[4 * kQuads], mm = ninf, ll = 0.f;
+  {
+    const int r = threadIdx.x & 31, q = threadIdx.x >> 5;  // row, and two of its float4
+    float4 o[2] = {};
+    float2 ml = make_float2(ninf, 0.f);
+    const size_t at = static_cast<size_t>(sub) * kJoinRows + r;
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += kAtOnce) {
+      float2 e[kAtOnce];
+      float4 x[kAtOnce][2];
 #pragma unroll
-  for (int k = 0; k < 4 * kQuads; ++k) o[k] = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const int sl = i == 0 ? first : 2 * (c0 + i);
-    const float4 *src = reinterpret_cast<const float4 *>(a.tile_o) +
-                        (static_cast<size_t>(sl) * (D / 4) + piece * kQuads) * tiles::kRows + r;
-    const float2 e = a.tile_ml[sl * tiles::kRows + r];
-    float4 x[kQuads];
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int sl = i0 + i == 0 ? first : 2 * (c0 + min(i0 + i, n - 1));
+        e[i] = __ldcg(a.tile_ml + static_cast<size_t>(sl) * tiles::kRows + at);
+        const float4 *src = reinterpret_cast<const float4 *>(a.tile_o) +
+                            (static_cast<size_t>(sl) * (D / 4) + 16 * piece + 2 * q) * tiles::kRows + at;
+        x[i][0] = __ldcg(src);
+        x[i][1] = __ldcg(src + tiles::kRows);
+      }
 #pragma unroll
-    for (int k = 0; k < kQuads; ++k) x[k] = src[static_cast<size_t>(k) * tiles::kRows];
-    const Join j = join(make_float2(mm, ll), e);
-    mm = fmaxf(mm, e.x);
-    ll = j.sum;
+      for (int i = 0; i < kAtOnce; ++i) {
+        if (i0 + i >= n) break;  // (the last part again)
+        const Join j = join(ml, e[i]);
+        ml = make_float2(fmaxf(ml.x, e[i].x), j.sum);
 #pragma unroll
-    for (int k = 0; k < kQuads; ++k) {
-      o[4 * k] = fmaf(o[4 * k], j.x, x[k].x * j.y);
-      o[4 * k + 1] = fmaf(o[4 * k + 1], j.x, x[k].y * j.y);
-      o[4 * k + 2] = fmaf(o[4 * k + 2], j.x, x[k].z * j.y);
-      o[4 * k + 3] = fmaf(o[4 * k + 3], j.x, x[k].w * j.y);
+        for (int k = 0; k < 2; ++k)
+          o[k] = make_float4(fmaf(o[k].x, j.x, x[i][k].x * j.y), fmaf(o[k].y, j.x, x[i][k].y * j.y),
+                             fmaf(o[k].z, j.x, x[i][k].z * j.y), fmaf(o[k].w, j.x, x[i][k].w * j.y));
+      }
     }
+    turned[r][2 * q] = o[0];
+    turned[r][2 * q + 1] = o[1];
+    if (q == 0) sums[r] = make_float2(ml.x == ninf ? ninf : ml.x - tiles::kShift, ml.y);
   }
-  const int tok = row / a.group;
-  const size_t at = carry_at(a, p.q.row0 + tok, h * a.group + row - tok * a.group);
-  float4 *dst = reinterpret_cast<float4 *>(a.carry_o + at * D) + piece * kQuads;
+  __syncthreads();
+  const int r = threadIdx.x >> 3, q = threadIdx.x & 7, row = row0 + r;
+  if (row >= n_rows || !row_in_bounds(a, p.q.row0, h, row)) return;
+  const int tok = row / a.group, head = h * a.group + row - tok * a.group;
+  const size_t at = carry_at(a, p.q.row0 + tok, head);
+  const float2 own = a.carry_ml[at];
+  if (own.y < 0.f) return;
+  const Join j = join(sums[r], own);
+  const float f = inverse_sum(j.sum, 0);
+  uint32_t e[4];
 #pragma unroll
-  for (int k = 0; k < kQuads; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-  if (piece == 0) a.carry_ml[at] = make_float2(mm == ninf ? mm : mm - tiles::kShift, ll);
+  for (int k = 0; k < 2; ++k) {
+    const float4 x = turned[r][2 * q + k];
+    const float4 y = *reinterpret_cast<const float4 *>(a.carry_o + at * D + 64 * piece + 8 * q + 4 * k);
+    e[2 * k] = pack2<BF16>(fmaf(x.x, j.x, y.x * j.y) * f, fmaf(x.y, j.x, y.y * j.y) * f);
+    e[2 * k + 1] = pack2<BF16>(fmaf(x.z, j.x, y.z * j.y) * f, fmaf(x.w, j.x, y.w * j.y) * f);
+  }
+  *reinterpret_cast<uint4 *>(a.out.p + (static_cast<long long>(p.q.row0) + tok) * a.out.row + head * a.out.head +
+                             64 * piece + 8 * q) = make_uint4(e[0], e[1], e[2], e[3]);
 }
 
 }  // namespace shared
@@ -79,10 +114,11 @@ cudaError_t launch_segments(const AttnArgs &a, cudaStream_t stream) {
 
 cudaError_t launch_join(const AttnArgs &a, cudaStream_t stream) {
   const long long slots = static_cast<long long>(a.rows) * a.group / kTileRows + a.segs;
-  const long long grid = slots * a.geo.H * (a.geo.D / 4 / shared::kQuads);
+  const long long grid = slots * a.geo.H * (a.geo.D / 64) * (kTileRows / shared::kJoinRows);
   if (grid > 2147483647LL) return cudaErrorInvalidConfiguration;
-  return launch_after(a.geo.D == 128 ? shared::join_kernel<128> : shared::join_kernel<64>, static_cast<unsigned>(grid),
-                      kTileRows, 0, stream, a);
+  auto kernel = a.geo.D == 128 ? (a.geo.bf16 ? shared::join_kernel<128, true> : shared::join_kernel<128, false>)
+                               : (a.geo.bf16 ? shared::join_kernel<64, true> : shared::join_kernel<64, false>);
+  return launch_after(kernel, static_cast<unsigned>(grid), shared::kJoinThreads, 0, stream, a);
 }
 
 }  // namespace kv8

@@ -335,6 +335,8 @@ __device__ __forceinline__ Pair pair_of_slot(const AttnArgs &a, int slot) {
   return make_pair<SHARED>(a, s, slot - base(s));
 }
 
+static_assert(64 + 8 * (kThreads / 32) + sizeof(Pair) <= 384, "a pair's place beside the barriers");
+
 // An item's kOver + units line positions; unit u is at start + kOver + u.
 template <bool SHARED>
 struct Walk {
@@ -509,14 +511,15 @@ template <int D, int FMT, bool BF16, bool SHARED>
 __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
   using SM = Smem<D>;
   extern __shared__ unsigned char raw[];
-  follow<SHARED>();
+  start<SHARED>(a);
   unsigned char *smem = raw + ((1024 - (kvq::smem_u32(raw) & 1023)) & 1023);
   const uint32_t base = kvq::smem_u32(smem);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + SM::BAR);
   volatile int *dead = reinterpret_cast<volatile int *>(smem + SM::MISC);       // a wait gave up
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + SM::MISC + 8);
   int *flag = reinterpret_cast<int *>(smem + SM::MISC + 16);
-  long long *found = reinterpret_cast<long long *>(smem + SM::MISC + 32);       // [2]
+  long long *found = reinterpret_cast<long long *>(smem + SM::MISC + 32);       // where the range begins in its pair
+  Pair *found_pair = reinterpret_cast<Pair *>(smem + SM::MISC + 64 + 8 * (kThreads / 32));
   long long *scan_buf = reinterpret_cast<long long *>(smem + SM::MISC + 64);    // [kThreads / 32]
   const Geo &geo = a.geo;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -524,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
   const float ninf = __int_as_float(0xff800000), nan = __int_as_float(0x7fc00000);
 
   // ---- this CTA's range of the line
-  long long total = 0;
+  long long total = 0, before = 0;
   const int slots = static_cast<int>(static_cast<long long>(min(row_start_of<SHARED>(a, a.segs), a.rows)) * a.group / kRows) + a.segs;
   Pair mine;
   {
@@ -536,16 +539,15 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
     if (SHARED && a.part == kPrefix)
       for (int s = tid; s < a.segs; s += kThreads)
         falls |= a.group_start[s] < 0 || a.group_start[s + 1] < a.group_start[s] || a.group_start[s + 1] > geo.S;
-    if (__syncthreads_or(falls)) return;  // the rows kernel has set the status
+    if (__syncthreads_or(falls)) return finish<SHARED>();  // the rows kernel has set the status
     long long sum = 0;
     for (int i = tid; i < slots; i += kThreads) {
       mine = pair_of_slot<SHARED>(a, i);
       sum += line_of(mine, H);
     }
-    long long before;
     total = cta_scan(sum, before, scan_buf);
   }
-  if (total == 0) return;
+  if (total == 0) return finish<SHARED>();
   // Eight line positions per CTA at least.  Long lines, from 1216 on, do not
   // meet this; short ones would be faster with four (8 KV heads x 4 queries,
   // D 128: a prompt of 256 tokens 28.9 against 20.6 us, of 512 34.6 against 25.4,
@@ -554,18 +556,20 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
   // Over shared blocks two: their parts are joined by another kernel, by all SMs.
   const int least = SHARED && a.part == kPrefix ? 2 : 8;
   const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + least - 1) / least));
-  if (static_cast<int>(blockIdx.x) >= ctas) return;
+  if (static_cast<int>(blockIdx.x) >= ctas) return finish<SHARED>();
   const long long lo = divide(blockIdx.x * total, ctas), hi = divide((blockIdx.x + 1) * total, ctas);
   {
     long long at = 0;
     for (int i0 = 0; i0 < slots; i0 += kThreads) {
-      if (i0 + tid < slots && slots > kThreads) mine = pair_of_slot<SHARED>(a, i0 + tid);
+      long long sum = total;
+      if (slots > kThreads) {  // else each thread has its only pair, and its place on the line
+        if (i0 + tid < slots) mine = pair_of_slot<SHARED>(a, i0 + tid);
+        sum = cta_scan(i0 + tid < slots ? line_of(mine, H) : 0, before, scan_buf);
+      }
       const long long u = i0 + tid < slots ? line_of(mine, H) : 0;
-      long long before;
-      const long long sum = cta_scan(u, before, scan_buf);
       if (lo >= at + before && lo < at + before + u) {
-        found[0] = i0 + tid;
-        found[1] = lo - (at + before);
+        *found = lo - (at + before);
+        *found_pair = mine;
       }
       at += sum;
       if (lo < at) break;
@@ -713,9 +717,9 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
     } else if (warp == 21 && lane == 0) {
       // ================================================= the walk
       Walk<SHARED> use;
-      use.p = pair_of_slot<SHARED>(a, static_cast<int>(found[0]));
-      use.h = static_cast<int>(divide(found[1], use.p.units + kOver));
-      use.start = lo - (found[1] - static_cast<long long>(use.h) * (use.p.units + kOver));
+      use.p = *found_pair;
+      use.h = static_cast<int>(divide(*found, use.p.units + kOver));
+      use.start = lo - (*found - static_cast<long long>(use.h) * (use.p.units + kOver));
       use.lo = lo;
       use.end = hi;
       bool more = use.part();
@@ -1003,24 +1007,29 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       float qf = a.zscale;
       if (active) {
         const uint32_t dst = base + SM::Q + t * SM::TILE;
-        uint4 x[NQ];
+        // (half of them at a time: their code runs once per item, and comes from far)
+        constexpr int NB = NQ / 2;
+#pragma unroll 1
+        for (int i1 = i0; i1 < i0 + NQ; i1 += NB) {
+          uint4 x[NB];
 #pragma unroll
-        for (int i = 0; i < NQ; ++i) {
-          const long long off = __shfl_sync(kAll, q_off, (i0 + i) * RPI + lane / LPR);
-          x[i] = *reinterpret_cast<const uint4 *>(a.q.p + off + lane % LPR * 8);
-        }
-#pragma unroll
-        for (int i = 0; i < NQ; ++i) {
-          const int at = 32 * (warp & 3) + (i0 + i) * RPI + lane / LPR;  // row of the tile
-          if (BF16) {
-            uint32_t big = mag_max8(x[i]);
-#pragma unroll
-            for (int o = 1; o < LPR; o <<= 1) big = max(big, __shfl_xor_sync(kAll, big, o));
-            const int e = big ? min(max(static_cast<int>(big >> 7), 20), 254) : 141;
-            x[i] = bf16_row_to_fp16(x[i], __int_as_float((268 - e) << 23));
-            if (lane % LPR == 0) exps[at] = e;
+          for (int i = 0; i < NB; ++i) {
+            const long long off = __shfl_sync(kAll, q_off, (i1 + i) * RPI + lane / LPR);
+            x[i] = *reinterpret_cast<const uint4 *>(a.q.p + off + lane % LPR * 8);
           }
-          sts16(dst + place(at, lane % LPR), x[i].x, x[i].y, x[i].z, x[i].w);
+#pragma unroll
+          for (int i = 0; i < NB; ++i) {
+            const int at = 32 * (warp & 3) + (i1 + i) * RPI + lane / LPR;  // row of the tile
+            if (BF16) {
+              uint32_t big = mag_max8(x[i]);
+#pragma unroll
+              for (int o = 1; o < LPR; o <<= 1) big = max(big, __shfl_xor_sync(kAll, big, o));
+              const int e = big ? min(max(static_cast<int>(big >> 7), 20), 254) : 141;
+              x[i] = bf16_row_to_fp16(x[i], __int_as_float((268 - e) << 23));
+              if (lane % LPR == 0) exps[at] = e;
+            }
+            sts16(dst + place(at, lane % LPR), x[i].x, x[i].y, x[i].z, x[i].w);
+          }
         }
         if (BF16) {
           bar_sync(3 + t, 256);
@@ -1142,15 +1151,18 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       // With shared blocks: 32 channels of the row's partial result, left for the
       // other launch, or joined with what that has left.
       const size_t carry = SHARED ? carry_at(a, p.row0 + tok, static_cast<int>(head)) : 0;
-      auto leave = [&](int c, const float *o, float top, float sum) {
-        if (!valid || !inside) return;
-        float4 *dst = reinterpret_cast<float4 *>(a.carry_o + carry * D) + 8 * c;
+      const bool leaves = SHARED && p.base, joins = SHARED && a.part == kPrefix;
+      auto finish_row = [&](int c, float *o, float top, float sum) {
+        if (leaves) {
+          if (!valid || !inside) return;
+          float4 *dst = reinterpret_cast<float4 *>(a.carry_o + carry * D) + 8 * c;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-        if (c == 0) a.carry_ml[carry] = make_float2(top == ninf ? top : top - kShift, sum);
-      };
-      auto finish = [&](int c, float *o, float top, float sum) {
-        if (SHARED && p.base && valid && inside) {
+          for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          if (c == 0) a.carry_ml[carry] = make_float2(top == ninf ? top : top - kShift, sum);
+          return;
+        }
+        if (joins) wait_before();
+        if (joins && valid && inside) {
           const Join n = join(make_float2(top == ninf ? top : top - kShift, sum), a.carry_ml[carry]);
           const float4 *src = reinterpret_cast<const float4 *>(a.carry_o + carry * D) + 8 * c;
 #pragma unroll
@@ -1167,9 +1179,11 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       };
       auto store_rows = [&]() {
         bar_sync(3 + t, 256);
+        // (a row that is not to be written)
+        const bool shut = joins && out_off >= 0 && a.carry_ml[carry].y < 0.f;
 #pragma unroll 4
         for (int i = 0; i < NQ; ++i) {
-          const long long off = __shfl_sync(kAll, out_off, (i0 + i) * RPI + lane / LPR);
+          const long long off = __shfl_sync(kAll, shut ? -1 : out_off, (i0 + i) * RPI + lane / LPR);
           const uint4 x = lds16(stage + place(32 * (warp & 3) + (i0 + i) * RPI + lane / LPR, lane % LPR));
           if (off >= 0) *reinterpret_cast<uint4 *>(a.out.p + off + lane % LPR * 8) = x;
         }
@@ -1190,10 +1204,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
             float x[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) x[i] = l == 0.f ? 0.f : __uint_as_float(o[i]);
-            if (SHARED && a.part == kPrefix)
-              leave(c, x, M, l);
-            else
-              finish(c, x, M, l);
+            finish_row(c, x, M, l);
           } else {
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
@@ -1203,7 +1214,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
                            : make_float4(0.f, 0.f, 0.f, 0.f);
           }
         }
-        if (whole && !(SHARED && a.part == kPrefix))
+        if (whole && !leaves)
           store_rows();
         else if (!whole && hf == 0)
           a.tile_ml[slot * kRows + t * 128 + r] = make_float2(M, l);
@@ -1254,9 +1265,9 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
                 o[4 * k + 3] = fmaf(o[4 * k + 3], was, x[k].w * f);
               }
             }
-            finish(c, o, mm, ll);
+            finish_row(c, o, mm, ll);
           }
-          store_rows();
+          if (!leaves) store_rows();
         }
       }
       __syncwarp();
@@ -1270,6 +1281,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
     fence_after();
     tmem_free(*tmem_slot);
   }
+  finish<SHARED>();
 }
 
 template <int D, int FMT, bool BF16, bool SHARED>
