@@ -175,6 +175,9 @@ int check_workspace(const void *workspace, size_t given, size_t needed) {
   return aligned(workspace, 256) ? KVQ_OK : KVQ_ERR_ALIGNMENT;
 }
 
+// The segments of whole sequences, two int4 each.
+size_t seg_bytes(const kv8_cache *c) { return (static_cast<size_t>(c->num_seqs) * 32 + 255) / 256 * 256; }
+
 // Attention over whole sequences in one pass.
 int attend(const kv8_cache *cache, int32_t num_q_heads, const kv8_rows *q, const kv8_rows *out,
            const int32_t *row_start, int32_t rows, int32_t max_new, float softmax_scale, void *workspace,
@@ -183,11 +186,20 @@ int attend(const kv8_cache *cache, int32_t num_q_heads, const kv8_rows *q, const
   int e = attn_args(a, cache, num_q_heads, q, out, row_start, rows, max_new, softmax_scale, max_len);
   if (e || rows == 0) return e;
   const kv8::AttnPlan plan = kv8::plan_attn(cache->head_dim, static_cast<int64_t>(a.group) * max_new);
-  if ((e = check_workspace(workspace, workspace_bytes, plan.bytes))) return e;
+  const size_t segs = causal ? 0 : seg_bytes(cache);
+  if ((e = check_workspace(workspace, workspace_bytes, plan.bytes + segs))) return e;
   a.causal = causal;
   place(a, plan, workspace, workspace);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint64_t n = 0;
-  const cudaError_t ce = kv8::launch_attn(a, plan.tiles, static_cast<cudaStream_t>(stream), &n);
+  cudaError_t ce = cudaSuccess;
+  if (!causal) {
+    a.plan = reinterpret_cast<int4 *>(static_cast<uint8_t *>(workspace) + plan.bytes);
+    a.fine = a.first = 1;
+    ++n;
+    ce = kv8::launch_segments(a, st);
+  }
+  if (ce == cudaSuccess) ce = kv8::launch_attn(a, plan.tiles, st, &n);
   return from_cuda(ce, n);
 }
 
@@ -267,7 +279,7 @@ int kv8_attn(const kv8_cache *cache, int32_t num_q_heads, const kv8_rows *q, con
 int64_t kv8_cross_attn_workspace_bytes(const kv8_cache *cache, int32_t num_q_heads, int32_t max_rows) {
   if (check_geometry(cache) || max_rows < 1 || check_heads(cache, num_q_heads, max_rows)) return -1;
   const int64_t group = num_q_heads / cache->num_kv_heads;
-  return static_cast<int64_t>(kv8::plan_attn(cache->head_dim, group * max_rows).bytes);
+  return static_cast<int64_t>(kv8::plan_attn(cache->head_dim, group * max_rows).bytes + seg_bytes(cache));
 }
 
 int kv8_cross_attn(const kv8_cache *cache, int32_t num_q_heads, const kv8_rows *q, const kv8_rows *out,
@@ -316,13 +328,17 @@ int kv8_shared_attn(const kv8_cache *cache, int32_t num_q_heads, const kv8_rows 
   a.plan = reinterpret_cast<int4 *>(ws + plan.off_segs);
   a.items = reinterpret_cast<int4 *>(ws + plan.off_items);
   a.carry_ml = reinterpret_cast<float2 *>(ws + plan.off_ml);
-  a.carry_o = reinterpret_cast<float *>(ws + plan.off_o);
+  a.carry_o = reinterpret_cast<float4 *>(ws + plan.off_o);
+  a.carry_blocks = plan.carry_blocks;
+  a.carry_wide = plan.own_tiles;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint64_t n = 1;
+  a.rows_max = plan.own_tiles ? kv8::kRowsMax : 2147483647;
+  a.group_rows_max = plan.prefix_tiles ? kv8::kRowsMax : 2147483647;
   cudaError_t ce = kv8::launch_segments(a, st);
   if (ce != cudaSuccess) return from_cuda(ce, n);
   a.part = kv8::kOwn;
-  a.first = 1;
+  a.first = a.fine = 1;
   place(a, kv8::plan_attn(cache->head_dim, group * max_new), ws, ws);
   ce = kv8::launch_attn(a, plan.own_tiles, st, &n);
   if (ce == cudaSuccess) {
@@ -375,7 +391,8 @@ SharedPlan plan_shared(int D, int S, int H, int num_q_heads, long long rows, lon
   // (a group has at most one row tile pair that is not full)
   const size_t items = p.prefix_tiles ? (static_cast<size_t>(rows) * group / kTileRows + S) * H : 0;
   p.off_ml = align(p.off_items + items * sizeof(int4));
-  const size_t n = static_cast<size_t>(rows) * num_q_heads;
+  p.carry_blocks = (rows * group + 31) / 32;
+  const size_t n = static_cast<size_t>(H) * p.carry_blocks * 32;
   p.off_o = align(p.off_ml + n * sizeof(float2));
   p.bytes = align(p.off_o + n * D * sizeof(float));
   return p;
@@ -385,7 +402,7 @@ cudaError_t launch_attn(const AttnArgs &a, bool tiles, cudaStream_t stream, uint
   const bool wide = a.geo.D == 128, shared = a.part != kWhole;
   auto rows_kernel = [&]() {
     ++*launches;
-    return shared ? (wide ? launch_rows_128_shared(a, stream) : launch_rows_64_shared(a, stream))
+    return a.fine ? (wide ? launch_rows_128_shared(a, stream) : launch_rows_64_shared(a, stream))
                   : (wide ? launch_rows_128(a, stream) : launch_rows_64(a, stream));
   };
   auto tile_kernel = [&]() {

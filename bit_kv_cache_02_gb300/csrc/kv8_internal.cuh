@@ -165,6 +165,7 @@ AttnPlan plan_attn(int D, long long rows_per_head);
 // wait for the others until then, so each has regions of its own.
 struct SharedPlan {
   size_t off_prefix, off_segs, off_items, off_ml, off_o, bytes;
+  long long carry_blocks;
   bool own_tiles, prefix_tiles;
 };
 SharedPlan plan_shared(int D, int S, int H, int num_q_heads, long long rows, long long max_new,
@@ -181,6 +182,7 @@ struct AttnArgs {
   Geo geo;
   int Hq, group;
   int part;    // kWhole, kPrefix or kOwn
+  int fine;    // 1: the kernels whose segments are looked up before
   int causal;  // 1: a row sees up to its own position, 0: all of its segment
   int segs;    // segments: sequences or groups
   const int *group_start, *prefix_len;  // [groups + 1], [groups]; with kPrefix and kOwn
@@ -188,8 +190,12 @@ struct AttnArgs {
   int4 *plan;        // two per segment: the groups', then the sequences'
   int4 *items;       // of the tile kernel's items over shared blocks: the parts to join
   int first;         // the first launch behind the lookup of the segments
-  float *carry_o;    // [rows][Hq][D]: unnormalized outputs over what lies behind the shared blocks
-  float2 *carry_ml;  // [rows][Hq]: (max, sum) in log2 units; sum -1: the row is not to be written
+  // Partial results over what lies behind the shared blocks, of the rows of each
+  // KV head, (tensor row, query head of the KV head):
+  long long carry_blocks;  // per KV head: the rows, in blocks of 32
+  float4 *carry_o;         // [H][carry_blocks] of [32][D / 4], or of [D / 4][32]: unnormalized outputs
+  float2 *carry_ml;        // [H][carry_blocks][32]: (max, sum) in log2 units; sum -1: not to be written
+  int carry_wide;          // 1: rows side by side
   Rows q, out;
   const int *row_start;
   int rows, max_new, max_len;
@@ -201,6 +207,7 @@ struct AttnArgs {
   float2 *tile_ml;    // [2 kMaxTileCtas][256] (reference, sum)
   int *tile_counters; // [kMaxTileCtas], zero on entry, left zero on exit
   int rows_max;       // rows per KV head up to which the rows kernel takes a sequence
+  int group_rows_max; // and a group
   long long wait_limit;  // SM cycles that a wait of the tile kernel may last before it gives up
   int wait_test;         // test aid: a wait of the tile kernel that nothing completes
 };
@@ -268,16 +275,28 @@ __device__ __forceinline__ Seg group_seg(const AttnArgs &a, int g) {
   return {L, L ? x.n : 0, x.row0, 0, x.ok ? x.first : 0, x.ok};
 }
 
-// SHARED: a launch over shared blocks, or over what lies behind them (kernels of
-// their own: what they keep besides cost the others registers).  Their segments
-// have been looked up by a kernel before: each is a chain of six loads, which
-// every CTA would wait for, for every sequence.
-template <bool SHARED>
+// FINE: kernels whose segments have been looked up by a kernel before, two int4
+// each.  With shared blocks each is a chain of six loads, which every CTA would
+// wait for, for every sequence; and what a CTA runs once comes from far, so that
+// the code counts too (a branch for whole sequences beside this one: 2 to 4 us).
+struct Plan {
+  int full, units, tiles;  // for the rows kernel: units of complete blocks, all units, row tiles per KV head
+};
+__device__ __forceinline__ void store_plan(const AttnArgs &a, int i, const Seg &x, const Plan &w) {
+  a.plan[2 * i] = make_int4(x.L, x.n, x.row0, x.base);
+  a.plan[2 * i + 1] = make_int4(x.ok ? x.entry : -1, w.full, w.units, w.tiles);
+}
+__device__ __forceinline__ Seg load_plan(const AttnArgs &a, int s, Plan &w) {
+  const int4 *p = a.plan + 2 * (static_cast<size_t>(a.part == kOwn ? a.groups : 0) + s);
+  const int4 x = p[0], y = p[1];
+  w = {y.y, y.z, y.w};
+  return {x.x, x.y, x.z, x.w, max(y.x, 0), y.x >= 0};
+}
+template <bool FINE>
 __device__ __forceinline__ Seg load_seg(const AttnArgs &a, int s) {
-  if (SHARED) {
-    const int4 *p = a.plan + 2 * (static_cast<size_t>(a.part == kOwn ? a.groups : 0) + s);
-    const int4 x = p[0], y = p[1];
-    return {x.x, x.y, x.z, x.w, y.x, y.y != 0};
+  if (FINE) {
+    Plan w;
+    return load_plan(a, s, w);
   }
   const Seq q = load_seq(a.geo, a.row_start, a.rows, a.max_new, s);
   return {q.L, q.n, q.row0, 0, s, q.ok};
@@ -288,16 +307,16 @@ __device__ __forceinline__ Seg load_seg(const AttnArgs &a, int s) {
 // for them, and the others start behind it.  Each waits for the one before it
 // at the latest before it ends, so that the end of one is the end of all before.
 __device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-template <bool SHARED>
+template <bool FINE>
 __device__ __forceinline__ void start(const AttnArgs &a) {
-  if (SHARED) {
+  if (FINE) {
     if (a.first) wait_before();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   }
 }
-template <bool SHARED>
+template <bool FINE>
 __device__ __forceinline__ void finish() {
-  if (SHARED) wait_before();
+  if (FINE) wait_before();
 }
 template <typename... A>
 cudaError_t launch_after(void (*kernel)(A...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream,
@@ -321,9 +340,23 @@ __device__ __forceinline__ int last_seen(const AttnArgs &a, const T &q, int tok)
   return a.causal ? q.L - q.n + tok : q.L - 1;
 }
 
-// The place of a (row, query head) among the partial results.
-__device__ __forceinline__ size_t carry_at(const AttnArgs &a, int row, int head) {
-  return static_cast<size_t>(row) * a.Hq + head;
+// A row of KV head h among the partial results: (max, sum), and channels 4 c
+// to 4 c + 3.  A thread of the tile kernel has a row, and a warp 32 neighbours:
+// with rows side by side its accesses are 512 bytes each.  The rows kernel has a
+// row's channels side by side (11 groups of 3 to 25 sequences, few rows: 28.5 us,
+// 37 the other way), so its order is taken where no sequence's rows are many.
+struct CarryRow {
+  float2 *ml;
+  float4 *o;
+  int step;
+  __device__ __forceinline__ float4 &at(int c) const { return o[step * c]; }
+};
+template <int D>
+__device__ __forceinline__ CarryRow carry_row(const AttnArgs &a, int h, int row0, int row) {
+  const long long r = static_cast<long long>(row0) * a.group + row;
+  const size_t at = static_cast<size_t>(h * a.carry_blocks) * 32 + r;
+  const int lane = static_cast<int>(r & 31);
+  return {a.carry_ml + at, a.carry_o + (a.carry_wide ? (at - lane) * (D / 4) + lane : at * (D / 4)), a.carry_wide ? 32 : 1};
 }
 
 // The factors that join two partial results (max, sum), and what their weighted

@@ -247,16 +247,33 @@ struct Work {
   int tiles;  // row tiles per KV head
 };
 
+__device__ __forceinline__ Plan plan_of(const AttnArgs &a, const Seg &q, int rows_max) {
+  const int L = q.L;
+  const bool some = q.n > 0 && q.n * a.group <= rows_max && L > 0 && L <= a.max_len;
+  const int nb = L / a.geo.B;
+  Plan w;
+  w.full = some ? nb * (a.geo.B / kUnit) : 0;
+  w.units = some ? w.full + (L - nb * a.geo.B + kWinUnit - 1) / kWinUnit : 0;
+  w.tiles = some ? (q.n * a.group + kRowTile - 1) / kRowTile : 0;
+  return w;
+}
+
 template <bool FINE>
 __device__ __forceinline__ Work seq_work(const AttnArgs &a, int s) {
   Work w;
-  w.q = load_seg<FINE>(a, s);
-  const int L = w.q.L;
-  const bool some = w.q.n > 0 && w.q.n * a.group <= a.rows_max && L > 0 && L <= a.max_len;
-  const int nb = L / a.geo.B;
-  w.full = some ? nb * (a.geo.B / kUnit) : 0;
-  w.units = some ? w.full + (L - nb * a.geo.B + kWinUnit - 1) / kWinUnit : 0;
-  w.tiles = some ? (w.q.n * a.group + kRowTile - 1) / kRowTile : 0;
+  if (FINE) {
+    Plan p;
+    w.q = load_plan(a, s, p);
+    w.full = p.full;
+    w.units = p.units;
+    w.tiles = p.tiles;
+    return w;
+  }
+  w.q = load_seg<false>(a, s);
+  const auto p = plan_of(a, w.q, a.rows_max);
+  w.full = p.full;
+  w.units = p.units;
+  w.tiles = p.tiles;
   return w;
 }
 
@@ -399,16 +416,25 @@ struct Walk<true> {
   __device__ __forceinline__ long long front() const { return first; }
 };
 
-// N contiguous channels of a row, in 4 N bytes or as 16-bit floats.
+// N contiguous channels of a row, from `ch` on, left among the partial results or
+// joined with what is there; as 16-bit floats.
 template <int N>
-__device__ __forceinline__ void put32(float *dst, const float (&o)[N]) {
+__device__ __forceinline__ void put_carry(const CarryRow &c, int ch, const float (&o)[N]) {
   if constexpr (N % 4 == 0) {
 #pragma unroll
-    for (int j = 0; j < N; j += 4)
-      *reinterpret_cast<float4 *>(dst + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+    for (int j = 0; j < N; j += 4) c.at((ch + j) / 4) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
   } else {
+    static_assert(N == 2, "channels");
+    reinterpret_cast<float2 *>(&c.at(ch / 4))[ch / 2 & 1] = make_float2(o[0], o[1]);
+  }
+}
+template <int N>
+__device__ __forceinline__ void join_carry(const CarryRow &c, int ch, float (&o)[N], const Join &n) {
 #pragma unroll
-    for (int j = 0; j < N; j += 2) *reinterpret_cast<float2 *>(dst + j) = make_float2(o[j], o[j + 1]);
+  for (int j = 0; j < N; j += 2) {
+    const float2 x = reinterpret_cast<const float2 *>(&c.at((ch + j) / 4))[(ch + j) / 2 & 1];
+    o[j] = fmaf(o[j], n.x, x.x * n.y);
+    o[j + 1] = fmaf(o[j + 1], n.x, x.y * n.y);
   }
 }
 template <bool BF16, int N>
@@ -436,33 +462,27 @@ __device__ __forceinline__ void emit(const AttnArgs &a, const Work &w, int h, in
                                      float l, bool lead) {
   const int tok = row / a.group, head = h * a.group + row - tok * a.group;
   if (FINE && w.q.base) {
-    const size_t at = carry_at(a, w.q.row0 + tok, head);
-    put32(a.carry_o + at * D + ch, o);
-    if (lead) a.carry_ml[at] = make_float2(m, l);
+    const CarryRow c = carry_row<D>(a, h, w.q.row0, row);
+    put_carry(c, ch, o);
+    if (lead) *c.ml = make_float2(m, l);
     return;
   }
   float sum = l;
   if (FINE && a.part == kPrefix) {
     wait_before();
-    const size_t at = carry_at(a, w.q.row0 + tok, head);
-    const float2 own = a.carry_ml[at];
+    const CarryRow c = carry_row<D>(a, h, w.q.row0, row);
+    const float2 own = *c.ml;
     if (own.y < 0.f) return;
-    const float *src = a.carry_o + at * D + ch;
     const Join n = join(make_float2(m, l), own);
     sum = n.sum;
-#pragma unroll
-    for (int j = 0; j < N; j += 2) {
-      const float2 x = *reinterpret_cast<const float2 *>(src + j);
-      o[j] = fmaf(o[j], n.x, x.x * n.y);
-      o[j + 1] = fmaf(o[j + 1], n.x, x.y * n.y);
-    }
+    join_carry(c, ch, o, n);
   }
   put16<BF16>(a.out.p + (static_cast<long long>(w.q.row0) + tok) * a.out.row + head * a.out.head + ch, o,
               inverse_sum(sum, last_seen(a, w.q, tok)));
 }
 
 template <int D, int FMT, bool BF16, int HALVES, bool FINE>
-__global__ void __launch_bounds__(kWarps * 32, FINE && HALVES == 1 && (FMT == KV8_E4M3 || D == 64) ? 3 : 1) rows_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, FINE && (D == 64 || (HALVES == 1 && FMT == KV8_E4M3)) ? 3 : 0) rows_kernel(const AttnArgs a) {
   using SM = Smem<D, HALVES, FINE>;
   constexpr int NT = SM::NT;  // output n-tiles
   constexpr int KS = D / 16;  // k-steps of the scores

@@ -1,6 +1,7 @@
-// What attention behind shared blocks needs besides the kernels of the two
+// What attention with shared blocks needs besides the kernels of the two
 // attentions: the segments, looked up once for all CTAs, and the join of the
 // tile kernel's parts.
+#include "kv8_rows.cuh"
 #include "kv8_tiles.cuh"
 
 namespace kv8 {
@@ -8,21 +9,22 @@ namespace shared {
 
 constexpr int kSegThreads = 128;
 
-// A thread per group, then per sequence.
+// A thread per group, if there are any, then per sequence.
 __global__ void __launch_bounds__(kSegThreads) segments_kernel(const AttnArgs a) {
   asm volatile("griddepcontrol.launch_dependents;");
   const int i = blockIdx.x * kSegThreads + threadIdx.x;
   if (i >= a.groups + a.geo.S) return;
   bool shut = false;
-  const Seg x = i < a.groups ? group_seg(a, i) : own_seg(a, i - a.groups, shut);
-  a.plan[2 * i] = make_int4(x.L, x.n, x.row0, x.base);
-  a.plan[2 * i + 1] = make_int4(x.entry, x.ok, 0, 0);
+  const Seg x = i < a.groups ? group_seg(a, i) : a.groups ? own_seg(a, i - a.groups, shut) : load_seg<false>(a, i);
+  store_plan(a, i, x, rows::plan_of(a, x, i < a.groups ? a.group_rows_max : a.rows_max));
   if (shut) {
     // rows that the launch over their group's blocks is not to write
     const int s = i - a.groups;
     const long long from = max(a.row_start ? a.row_start[s] : s, 0);
     const long long to = min(a.row_start ? a.row_start[s + 1] : s + 1, a.rows);
-    for (long long k = from * a.Hq; k < to * a.Hq; ++k) a.carry_ml[k] = make_float2(0.f, -1.f);
+    for (int h = 0; h < a.geo.H; ++h)
+      for (long long r = from * a.group; r < to * a.group; ++r)
+        a.carry_ml[h * a.carry_blocks * 32 + r] = make_float2(0.f, -1.f);
   }
 }
 
@@ -87,8 +89,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnArgs a) {
   const int r = threadIdx.x >> 3, q = threadIdx.x & 7, row = row0 + r;
   if (row >= n_rows || !row_in_bounds(a, p.q.row0, h, row)) return;
   const int tok = row / a.group, head = h * a.group + row - tok * a.group;
-  const size_t at = carry_at(a, p.q.row0 + tok, head);
-  const float2 own = a.carry_ml[at];
+  const CarryRow carry = carry_row<D>(a, h, p.q.row0, row);
+  const float2 own = *carry.ml;
   if (own.y < 0.f) return;
   const Join j = join(sums[r], own);
   const float f = inverse_sum(j.sum, 0);
@@ -96,7 +98,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnArgs a) {
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const float4 x = turned[r][2 * q + k];
-    const float4 y = *reinterpret_cast<const float4 *>(a.carry_o + at * D + 64 * piece + 8 * q + 4 * k);
+    const float4 y = carry.at(16 * piece + 2 * q + k);
     e[2 * k] = pack2<BF16>(fmaf(x.x, j.x, y.x * j.y) * f, fmaf(x.y, j.x, y.y * j.y) * f);
     e[2 * k + 1] = pack2<BF16>(fmaf(x.z, j.x, y.z * j.y) * f, fmaf(x.w, j.x, y.w * j.y) * f);
   }

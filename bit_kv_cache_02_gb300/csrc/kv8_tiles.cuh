@@ -18,6 +18,7 @@
 //                    softmax runs under the other's products.
 //   warp 21          walks the CTA's share of the work: a ring of Parts.
 //   warp 22          looks up blocks and scales: a ring of Metas, one per unit.
+//   warp 23          prefetches the queries of the parts to come.
 //
 // Parts and Metas live in shared memory so that the other roles keep their
 // registers for data: a spilled register costs an L2 round trip here, as the
@@ -581,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
     kvq::mbar_init(bars + kDrained, 1);
     for (int i = 0; i < kParts; ++i) {
       kvq::mbar_init(bars + kPartFull + i, 1);
-      kvq::mbar_init(bars + kPartFree + i, 18);  // sixteen softmax warps, the products, the tables
+      kvq::mbar_init(bars + kPartFree + i, 19);  // sixteen softmax warps, the products, the tables, the queries
     }
     for (int i = 0; i < kMetas; ++i) {
       kvq::mbar_init(bars + kMetaFull + i, 1);
@@ -712,6 +713,28 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       if (!ok) {  // a wait ran out: no product may be left when tensor memory is given back
         if (leader) commit(base + SM::BAR + kDrained * 8);
         for (int i = 0; i < 100000 && !kvq::mbar_try_wait(bars + kDrained, 0); ++i) {
+        }
+      }
+    } else if (warp == 23) {
+      // ================================================= queries ahead
+      // A part's queries come to the second-level cache while the parts before it
+      // are computed: their rows are not read before, and an item waited longer
+      // for them than for its first keys.
+      for (uint32_t n_part = 0;; ++n_part) {
+        if (!__all_sync(kAll, wait(kPartFull + n_part % kParts, (n_part / kParts) & 1))) break;
+        const Part &p = parts[n_part % kParts];
+        const bool end = p.u0 == p.u1;
+        const int row = p.row, h = p.h, row0 = p.row0, n_rows = p.n * a.group;
+        __syncwarp();
+        if (lane == 0) kvq::mbar_arrive(bars + kPartFree + n_part % kParts);
+        if (end) break;
+        for (int r = row + lane; r < min(row + kRows, n_rows); r += 32) {
+          if (!row_in_bounds(a, row0, h, r)) continue;
+          const int tok = r / a.group;
+          const uint16_t *q = a.q.p + (static_cast<long long>(row0) + tok) * a.q.row +
+                              (static_cast<long long>(h) * a.group + r - tok * a.group) * a.q.head;
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+          if (D == 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 64));
         }
       }
     } else if (warp == 21 && lane == 0) {
@@ -1150,24 +1173,23 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       };
       // With shared blocks: 32 channels of the row's partial result, left for the
       // other launch, or joined with what that has left.
-      const size_t carry = SHARED ? carry_at(a, p.row0 + tok, static_cast<int>(head)) : 0;
+      const CarryRow carry = SHARED ? carry_row<D>(a, p.h, p.row0, some) : CarryRow{};
       const bool leaves = SHARED && p.base, joins = SHARED && a.part == kPrefix;
       auto finish_row = [&](int c, float *o, float top, float sum) {
         if (leaves) {
           if (!valid || !inside) return;
-          float4 *dst = reinterpret_cast<float4 *>(a.carry_o + carry * D) + 8 * c;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-          if (c == 0) a.carry_ml[carry] = make_float2(top == ninf ? top : top - kShift, sum);
+          for (int k = 0; k < 8; ++k)
+            carry.at(8 * c + k) = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          if (c == 0) *carry.ml = make_float2(top == ninf ? top : top - kShift, sum);
           return;
         }
         if (joins) wait_before();
         if (joins && valid && inside) {
-          const Join n = join(make_float2(top == ninf ? top : top - kShift, sum), a.carry_ml[carry]);
-          const float4 *src = reinterpret_cast<const float4 *>(a.carry_o + carry * D) + 8 * c;
+          const Join n = join(make_float2(top == ninf ? top : top - kShift, sum), *carry.ml);
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const float4 x = src[k];
+            const float4 x = carry.at(8 * c + k);
             o[4 * k] = fmaf(o[4 * k], n.x, x.x * n.y);
             o[4 * k + 1] = fmaf(o[4 * k + 1], n.x, x.y * n.y);
             o[4 * k + 2] = fmaf(o[4 * k + 2], n.x, x.z * n.y);
@@ -1180,7 +1202,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       auto store_rows = [&]() {
         bar_sync(3 + t, 256);
         // (a row that is not to be written)
-        const bool shut = joins && out_off >= 0 && a.carry_ml[carry].y < 0.f;
+        const bool shut = joins && out_off >= 0 && carry.ml->y < 0.f;
 #pragma unroll 4
         for (int i = 0; i < NQ; ++i) {
           const long long off = __shfl_sync(kAll, shut ? -1 : out_off, (i0 + i) * RPI + lane / LPR);
