@@ -92,8 +92,8 @@ __device__ __forceinline__ Turn load_turn(int pi, int pos, const AppendArgs &a) 
 // Cosines and sines of the four angles from `angle` on (a multiple of 4) for
 // tensor row `row`.  Four angles of one axis, as all are where each axis has its
 // own section of the angles, are one load each.  A position outside the table
-// gives NaN.
-__device__ __forceinline__ void load_axes(float4 &c, float4 &s, int angle, int row, const AppendArgs &a) {
+// gives NaN, and false.
+__device__ __forceinline__ bool load_axes(float4 &c, float4 &s, int angle, int row, const AppendArgs &a) {
   const Axes &ax = a.ax;
   const uint32_t word = angle < 32 ? (angle < 16 ? ax.map[0] : ax.map[1]) : (angle < 48 ? ax.map[2] : ax.map[3]);
   const uint32_t axes = word >> (2 * (angle & 15)) & 0xffu;
@@ -123,17 +123,24 @@ __device__ __forceinline__ void load_axes(float4 &c, float4 &s, int angle, int r
     c = make_float4(x[0], x[1], x[2], x[3]);
     s = make_float4(y[0], y[1], y[2], y[3]);
   }
-  if (!good) set_status(a.geo.status, KV8_STATUS_BAD_POSITION);
+  return good;
+}
+// The 16 values of a chunk pair of tensor row `row`.
+__device__ __forceinline__ Turn axes_turn(int pi, int row, const AppendArgs &a, bool &good) {
+  const int2 ch = chunk_pair(pi, a.rot);
+  Turn t;
+  good = load_axes(t.c0, t.s0, a.interleaved ? 4 * ch.x : 8 * pi, row, a);
+  good &= load_axes(t.c1, t.s1, a.interleaved ? 4 * ch.y : 8 * pi + 4, row, a);
+  return t;
 }
 
 // The table values of a chunk pair of the token at position `pos`, in tensor row `row`.
 template <bool AXES>
 __device__ __forceinline__ Turn turn_of(int pi, int pos, int row, const AppendArgs &a) {
   if (!AXES) return load_turn(pi, pos, a);
-  const int2 ch = chunk_pair(pi, a.rot);
-  Turn t;
-  load_axes(t.c0, t.s0, a.interleaved ? 4 * ch.x : 8 * pi, row, a);
-  load_axes(t.c1, t.s1, a.interleaved ? 4 * ch.y : 8 * pi + 4, row, a);
+  bool good;
+  const Turn t = axes_turn(pi, row, a, good);
+  if (!good) set_status(a.geo.status, KV8_STATUS_BAD_POSITION);
   return t;
 }
 
@@ -214,27 +221,40 @@ __device__ __forceinline__ void rotate_queries(const AppendArgs &a, int cta) {
   const int pi = threadIdx.x % PAIRS, lane = at & (lanes - 1);
   const int row = cta * ((T / PAIRS) >> a.lanes) + (at >> a.lanes);
   if (row >= a.rows || lane >= a.Hq) return;
+  const bool turns = pi < (a.rot >> 4);
+  const int2 ch = chunk_pair(pi, a.rot);
+  const uint16_t *src = a.q.p + row * a.q.row + lane * a.q.head;
+  uint16_t *dst = a.q_out.p + row * a.q_out.row + lane * a.q_out.head;
+  const long long in = a.q.head << a.lanes, out = a.q_out.head << a.lanes;
+  Turn t;
+  bool good = true;
+  uint4 x, y, z, w;
+  auto load = [&](bool two) {
+    x = load16(src + 8 * ch.x);
+    y = load16(src + 8 * ch.y);
+    if (two) {
+      z = load16(src + in + 8 * ch.x);
+      w = load16(src + in + 8 * ch.y);
+    }
+  };
+  // With axes the row alone says where its angles are: they and the first queries
+  // are on their way while the row's sequence is looked up.
+  if (AXES) {
+    load(lane + lanes < a.Hq);
+    if (turns) t = axes_turn(pi, row, a, good);
+  }
   int s = row;
   if (a.row_start) s = last_at_or_below(a.geo.S, row, [&](int j) { return a.row_start[j]; });
   if (s >= a.geo.S) return;
   const Seq sq = load_seq(a.geo, a.row_start, a.rows, a.max_new, s);
   if (!sq.ok || row < sq.row0 || row >= sq.row0 + sq.n || sq.L < sq.n || sq.L > a.geo.capacity) return;
   if (!KVQ_IN_BOUNDS(a.geo.status, sq.L - sq.n + row - sq.row0, a.geo.capacity)) return;
-  const bool turns = pi < (a.rot >> 4);
-  Turn t;
-  if (turns) t = turn_of<AXES>(pi, sq.L - sq.n + row - sq.row0, row, a);
-  const int2 ch = chunk_pair(pi, a.rot);
-  const uint16_t *src = a.q.p + row * a.q.row + lane * a.q.head;
-  uint16_t *dst = a.q_out.p + row * a.q_out.row + lane * a.q_out.head;
-  const long long in = a.q.head << a.lanes, out = a.q_out.head << a.lanes;
+  if (!AXES && turns) t = load_turn(pi, sq.L - sq.n + row - sq.row0, a);
+  if (AXES && !good) set_status(a.geo.status, KV8_STATUS_BAD_POSITION);
 #pragma unroll 1
   for (int h = lane; h < a.Hq; h += 2 * lanes, src += 2 * in, dst += 2 * out) {
     const bool two = h + lanes < a.Hq;
-    uint4 x = load16(src + 8 * ch.x), y = load16(src + 8 * ch.y), z, w;
-    if (two) {
-      z = load16(src + in + 8 * ch.x);
-      w = load16(src + in + 8 * ch.y);
-    }
+    if (!AXES || h != lane) load(two);
     if (turns) rotate<BF16>(x, y, t, a.interleaved);
     store16(dst + 8 * ch.x, x);
     store16(dst + 8 * ch.y, y);
@@ -431,7 +451,10 @@ cudaError_t launch(const Geo &geo, const Rows &k, const Rows &v, const Rows &q, 
   // decode step twofold.
   const long long blocks = a.slots ? a.slots : geo.S;
   a.split = blocks * geo.H >= 2048;
-  a.heads = blocks * geo.H >= 8192 && rot_dim ? 8 : 1;
+  // (With axes a token's angles cost its positions too: eight heads from 2048 on.
+  // Prompts of 40573 tokens, 8 + 32 heads, 5200 blocks x heads: 164 us, one head
+  // per CTA 191, two 175, four 167.)
+  a.heads = blocks * geo.H >= (AXES ? 2048 : 8192) && rot_dim ? 8 : 1;
   a.head_groups = (geo.H + a.heads - 1) / a.heads;
   const long long tasks = blocks * a.head_groups * (a.split ? 2 : 1);
   // eight threads share a query row's chunk pair, fewer where there are fewer

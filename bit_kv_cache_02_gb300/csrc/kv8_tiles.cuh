@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
   // a chunk of 128 over 2000 42.1 against 35.2) and slower with sixteen (47.6,
   // 49.8, 55.9).
   // Over shared blocks two: their parts are joined by another kernel, by all SMs.
-  const int least = SHARED && a.part == kPrefix ? 2 : 8;
+  const int least = SHARED && a.part == kPrefix ? 2 : a.causal ? 8 : 4;
   const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + least - 1) / least));
   if (static_cast<int>(blockIdx.x) >= ctas) return finish<SHARED>();
   const long long lo = divide(blockIdx.x * total, ctas), hi = divide((blockIdx.x + 1) * total, ctas);

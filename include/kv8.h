@@ -180,7 +180,8 @@ int kv8_append(const kv8_cache *cache, const kv8_rows *k, const kv8_rows *v,
  * kv8_append_axes -- kv8_append for positions that are given.
  *
  *   positions  device int32: position of row r on axis x at
- *              positions[x * axis_stride + r].  Rows of no sequence are not read.
+ *              positions[x * axis_stride + r].  Those of rows of no
+ *              sequence may hold anything.
  *   axis_stride  at least `rows`; not used with one axis.
  *   num_axes   1 .. KV8_MAX_AXES.
  *   axis_of_pair  HOST array of rot_dim / 2 axes, read before the call returns:
@@ -273,12 +274,11 @@ int kv8_attn(const kv8_cache *cache, int32_t num_q_heads, const kv8_rows *q,
  *   max_rows   host bound on the rows of one sequence, from 1 on; not bound by
  *              the capacity.  max_rows * Hq / Hkv is below 2^30.
  *   softmax_scale, workspace, max_len, and all else, as in kv8_attn; the
- *              workspace has at least kv8_cross_attn_workspace_bytes(), which is
- *              kv8_attn_workspace_bytes() where that takes the bound, and the calls
- *              may share one.
+ *              workspace has at least kv8_cross_attn_workspace_bytes(), a few
+ *              bytes per sequence more than kv8_attn's, and may serve both.
  *
  * Every row sees the seq_len[s] tokens of its sequence.  Rows of a sequence
- * without tokens get zeros.
+ * without tokens get zeros.  Two or three kernels.
  */
 int64_t kv8_cross_attn_workspace_bytes(const kv8_cache *cache, int32_t num_q_heads, int32_t max_rows);
 int kv8_cross_attn(const kv8_cache *cache, int32_t num_q_heads, const kv8_rows *q, const kv8_rows *out,

@@ -1,5 +1,6 @@
-"""The 8-bit paged cache in plain numpy: what kv8_append stores and what
-kv8_attn returns (include/kv8.h), written from the definitions.
+"""The 8-bit paged cache in plain numpy: what kv8_append and kv8_append_axes
+store and what kv8_attn, kv8_cross_attn and kv8_shared_attn return
+(include/kv8.h), written from the definitions.
 
 16-bit numbers are carried as float64 arrays that hold representable values.
 Every rounding the definition names happens once, at the place it names;
@@ -59,6 +60,19 @@ def rotate(x, table_rows, interleaved, dtype):
     return y
 
 
+def axes_rows(table, positions, axis_of):
+    """table [p, r], positions [axes, rows], axis_of: the axis of each of the
+    r / 2 pairs -> [rows, r]: the cosines, then the sines, of the rows' pairs;
+    NaN where a position is outside the table."""
+    half = table.shape[1] // 2
+    out = np.full((positions.shape[1], 2 * half), math.nan)
+    for i in range(half):
+        at = positions[axis_of[i]]
+        ok = (at >= 0) & (at < len(table))
+        out[ok, i], out[ok, half + i] = table[at[ok], i], table[at[ok], half + i]
+    return out
+
+
 def quantize_block(x, fmt):
     """x [block, D] -> (code values [block, D], fp32 scale as float64)."""
     if not np.isfinite(x).all():
@@ -84,13 +98,14 @@ class OracleKV8:
     def lengths(self):
         return [len(x) for x in self.k]
 
-    def append(self, k, v, row_start, table=None, interleaved=False, q=None):
-        """Returns the rotated queries (rows of no sequence as they were)."""
+    def append(self, k, v, row_start, table=None, interleaved=False, q=None, angles=None):
+        """Returns the rotated queries (rows of no sequence as they were).
+        angles [rows, r] (axes_rows): the rows' own, whatever their places."""
         q_out = None if q is None else np.array(q, np.float64)
         for s in range(self.S):
             a, b = row_start[s], row_start[s + 1]
             at = np.arange(len(self.k[s]), len(self.k[s]) + b - a)
-            rows = np.zeros((b - a, 0)) if table is None else table[at]
+            rows = angles[a:b] if angles is not None else np.zeros((b - a, 0)) if table is None else table[at]
             self.k[s] = np.concatenate([self.k[s], rotate(k[a:b], rows, interleaved, self.dtype)])
             self.v[s] = np.concatenate([self.v[s], np.array(v[a:b], np.float64)])
             if q is not None:
@@ -136,8 +151,9 @@ class OracleKV8:
         in_fp16[full * self.B:] = self.dtype == "float16" or rows > 48
         return np.concatenate(u), in_fp16
 
-    def attention(self, q, row_start, softmax_scale=None):
-        """q [rows, Hq, D] -> (out, bound): float64 attention, and what the
+    def attention(self, q, row_start, softmax_scale=None, causal=True):
+        """Each row up to its own position, or (causal False) all tokens.
+        q [rows, Hq, D] -> (out, bound): float64 attention, and what the
         kernels' roundings may change it by before the output's own rounding.
 
         The bound.  A weight is rounded to fp16: 2^-11 of itself, or half a
@@ -172,7 +188,7 @@ class OracleKV8:
                 K, V = self.stored(s, h, False), self.stored(s, h, True)
                 unit, in_fp16 = self.units(s, h, n * g)
                 for i in range(n):
-                    seen = L - n + i + 1
+                    seen = L - n + i + 1 if causal else L
                     if seen <= 0:
                         continue
                     for j in range(h * g, (h + 1) * g):
