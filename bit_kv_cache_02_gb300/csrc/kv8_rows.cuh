@@ -538,9 +538,10 @@ __global__ void __launch_bounds__(kWarps * 32, FINE && (D == 64 || (HALVES == 1 
   // warp (one sequence of 300 tokens, 8 KV heads: 9.1 us instead of 13.9).
   long long want = min(static_cast<long long>(gridDim.x), (total + 2 * kWarps - 1) / (2 * kWarps));
   if constexpr (FINE) {
-    // As many CTAs as triples where those are few and none is long.
+    // As many CTAs as triples where those are few and none is much longer than a
+    // CTA's share of the line.
     most = __reduce_max_sync(kAll, most);
-    cost.each = triples <= gridDim.x && most <= kEach;
+    cost.each = triples <= gridDim.x && most <= total / gridDim.x + kEach;
     total = cost.each ? triples : dear;
     if (cost.each) want = triples;
   } else if (want >= 4 * triples)

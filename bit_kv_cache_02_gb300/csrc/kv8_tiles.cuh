@@ -533,14 +533,13 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
   Pair mine;
   {
     // the slots below need row_start to rise
+    // (with shared blocks, where the rows of all sequences are undefined otherwise,
+    // a look at each costs the start more than the items that it saves)
     bool falls = false;
-    if (a.row_start)
+    if (!SHARED && a.row_start)
       for (int s = tid; s < geo.S; s += kThreads)
         falls |= a.row_start[s] < 0 || a.row_start[s + 1] < a.row_start[s] || a.row_start[s + 1] > a.rows;
-    if (SHARED && a.part == kPrefix)
-      for (int s = tid; s < a.segs; s += kThreads)
-        falls |= a.group_start[s] < 0 || a.group_start[s + 1] < a.group_start[s] || a.group_start[s + 1] > geo.S;
-    if (__syncthreads_or(falls)) return finish<SHARED>();  // the rows kernel has set the status
+    if (!SHARED && __syncthreads_or(falls)) return;  // the rows kernel has set the status
     long long sum = 0;
     for (int i = tid; i < slots; i += kThreads) {
       mine = pair_of_slot<SHARED>(a, i);
