@@ -248,7 +248,7 @@ int kv8_append_axes(const kv8_cache *cache, const kv8_rows *k, const kv8_rows *v
                     void *stream) {
   if (num_axes < 1 || num_axes > KV8_MAX_AXES || rot_dim % 16 != 0 || rot_dim > 128) return KVQ_ERR_UNSUPPORTED;
   if (rot_dim < 16 || rope_rows < 1 || !axis_of_pair) return KVQ_ERR_INVALID_ARG;
-  if (rows > 0 && (!positions || (num_axes > 1 && axis_stride < rows))) return KVQ_ERR_INVALID_ARG;
+  if (rows > 0 && !positions) return KVQ_ERR_INVALID_ARG;
   if (!aligned(positions, 4)) return KVQ_ERR_ALIGNMENT;
   kv8::Axes axes = {positions, num_axes > 1 ? axis_stride : 0, rope_rows, {0, 0, 0, 0}};
   for (int i = 0; i < rot_dim / 2; ++i) {

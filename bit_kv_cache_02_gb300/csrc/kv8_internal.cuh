@@ -231,9 +231,11 @@ __device__ __forceinline__ Group load_group(const AttnArgs &a, int g) {
   Group x;
   x.first = a.group_start[g];
   const int end = a.group_start[g + 1], prefix = a.prefix_len[g];
-  x.ok = x.first >= 0 && end >= x.first && end <= a.geo.S && prefix >= 0 && prefix <= a.max_len;
   x.blocks = x.row0 = x.n = 0;
+  x.ok = x.first >= 0 && end >= x.first && end <= a.geo.S;
   if (!x.ok || end == x.first) return x;
+  x.ok = prefix >= 0 && prefix <= a.max_len;
+  if (!x.ok) return x;
   int r0 = x.first, r1 = end, own = r0 + 1;
   if (a.row_start) {
     r0 = a.row_start[r0];
@@ -257,7 +259,7 @@ __device__ __forceinline__ Seg own_seg(const AttnArgs &a, int s, bool &shut) {
   if (a.group_start[g] <= s && s < a.group_start[g + 1]) {
     const Group of = load_group(a, g);
     if (q.n > 0 && q.L <= a.max_len) {
-      if (!of.ok || (of.blocks && q.L - q.n < of.blocks * a.geo.B)) {
+      if (!of.ok || (of.blocks && (q.L <= 0 || q.L - q.n < of.blocks * a.geo.B))) {
         x.ok = false;
         x.n = 0;
       } else {
@@ -287,6 +289,7 @@ __device__ __forceinline__ void store_plan(const AttnArgs &a, int i, const Seg &
   a.plan[2 * i + 1] = make_int4(x.ok ? x.entry : -1, w.full, w.units, w.tiles);
 }
 __device__ __forceinline__ Seg load_plan(const AttnArgs &a, int s, Plan &w) {
+  if (!KVQ_IN_BOUNDS(a.geo.status, s, a.segs)) s = 0;
   const int4 *p = a.plan + 2 * (static_cast<size_t>(a.part == kOwn ? a.groups : 0) + s);
   const int4 x = p[0], y = p[1];
   w = {y.y, y.z, y.w};
@@ -354,7 +357,8 @@ struct CarryRow {
 template <int D>
 __device__ __forceinline__ CarryRow carry_row(const AttnArgs &a, int h, int row0, int row) {
   const long long r = static_cast<long long>(row0) * a.group + row;
-  const size_t at = static_cast<size_t>(h * a.carry_blocks) * 32 + r;
+  size_t at = static_cast<size_t>(h * a.carry_blocks) * 32 + r;
+  if (!KVQ_IN_BOUNDS(a.geo.status, r, a.carry_blocks * 32) || !KVQ_IN_BOUNDS(a.geo.status, h, a.geo.H)) at = 0;
   const int lane = static_cast<int>(r & 31);
   return {a.carry_ml + at, a.carry_o + (a.carry_wide ? (at - lane) * (D / 4) + lane : at * (D / 4)), a.carry_wide ? 32 : 1};
 }

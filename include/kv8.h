@@ -182,7 +182,7 @@ int kv8_append(const kv8_cache *cache, const kv8_rows *k, const kv8_rows *v,
  *   positions  device int32: position of row r on axis x at
  *              positions[x * axis_stride + r].  Those of rows of no
  *              sequence may hold anything.
- *   axis_stride  at least `rows`; not used with one axis.
+ *   axis_stride  any (0: all axes have the first one's); not used with one axis.
  *   num_axes   1 .. KV8_MAX_AXES.
  *   axis_of_pair  HOST array of rot_dim / 2 axes, read before the call returns:
  *              channel pair i (as in kv8_append, i + rot_dim / 2 or 2 i + 1

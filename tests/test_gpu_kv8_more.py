@@ -118,6 +118,20 @@ def test_axes_of_places_are_the_plain_append(kv8):
         b.check_state()
 
 
+def test_axes_that_are_one_line(kv8):
+    """Positions expanded from one line (stride 0), as a text's are."""
+    r = AxesRun(kv8, 1, 1, 1, 64, 32, "int8", "float16", 100, axes=3, axis_of=[i % 3 for i in range(32)])
+    x = _dev(r.numbers((40, 1, 64)), r.dtype)
+    line, outs = _i32(r.rng.integers(0, 300, 40)), []
+    for pos in (line.expand(3, 40), line.repeat(3, 1)):
+        r.cache.seq_len.fill_(40)
+        q_out = torch.empty_like(x)
+        kv8.kv8_append_axes(r.cache, x, x, pos, kv8.rope_axes(r.axis_of), r.rope, row_start=_i32([0, 40]), max_new=40,
+                            q=x, q_out=q_out)
+        outs.append((q_out, r.cache.codes[r.cache.block_table[0, 0].long()].clone()))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
 def test_axes_positions_beyond_the_capacity(kv8):
     """Positions of a long text in a small cache, rows far apart in the table."""
     r = AxesRun(kv8, 2, 1, 1, 64, 32, "int8", "float16", 100, axes=1, axis_of=[0] * 32, top=70000)
@@ -413,7 +427,7 @@ def test_shared_chunks(kv8, fmt, dtype, D, B, g):
     r.shared()
 
 
-@pytest.mark.parametrize("D,g,S,prefix", [(128, 8, 40, 5000), (64, 4, 64, 3000), (128, 4, 13, 9000), (64, 16, 2, 6000)])
+@pytest.mark.parametrize("D,g,S,prefix", [(128, 8, 36, 2500), (64, 4, 64, 1500), (128, 4, 13, 5000), (64, 16, 2, 6000)])
 def test_shared_long_prefix(kv8, D, g, S, prefix):
     """One long prefix, whose keys many CTAs share: all of their parts are joined,
     the same bits every time; the workspace's counters are left zero."""
@@ -502,6 +516,12 @@ def test_shared_device_errors(kv8, g):
                dict(group_start=[5, 0, -3]), dict(group_start=[2 ** 31 - 1, -2 ** 31, 0])):
         assert call(**kw)[1] & 2, kw
     out, st = call()
+    assert st == 0 and torch.equal(out, full)
+    # an empty group, whatever its prefix
+    q_of, prefix = r.prefix_len, _i32([2 * B, 12345, -3, 3 * B + 1])
+    r.prefix_len = prefix
+    out, st = call(group_start=[0, 3, 3, 3, 5])
+    r.prefix_len = q_of
     assert st == 0 and torch.equal(out, full)
     # the first sequence's entry of a shared block
     r.cache.block_table[0, 1] = r.cache.num_blocks
@@ -630,7 +650,7 @@ def test_two_streams_with_workspaces_of_their_own(kv8):
     r.append([(7 * s) % 100 for s in range(20)])
     r.append([1] * 20)
     q = _dev(r.q, r.dtype)
-    want = r.shared()
+    want = r.shared(check=False)
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in range(2)]
     space = [kv8.alloc_shared_workspace(r.cache, 16, 20, 1, 20) for _ in range(2)]

@@ -138,8 +138,7 @@ def test_bad_cache_refused(kv8, kw, code):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(axes=0), -2), (dict(axes=5), -2), (dict(axes=2), -1),           # the map names a third axis
-    (dict(map=None), -1), (dict(positions=None), -1), (dict(positions=BASE + 2), -5), (dict(stride=9), -1),
-    (dict(stride=-10), -1), (dict(rot=0), -1), (dict(rot=-16), -1), (dict(rot=24), -2), (dict(rot=144), -2),
+    (dict(map=None), -1), (dict(positions=None), -1), (dict(positions=BASE + 2), -5), (dict(rot=0), -1), (dict(rot=-16), -1), (dict(rot=24), -2), (dict(rot=144), -2),
     (dict(rope=None), -1), (dict(rope=BASE + 4), -5), (dict(rope_rows=0), -1), (dict(inter=2), -1),
     (dict(rows=-1), -1), (dict(max_new=1001), -3), (dict(row_start=BASE + 2), -5), (dict(row_start=None, rows=2), -1),
     (dict(k="null"), -1), (dict(q_out="null"), -1), (dict(heads=0), -1), (dict(v=(BASE, 252, 128)), -5),
