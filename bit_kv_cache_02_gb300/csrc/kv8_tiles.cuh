@@ -552,9 +552,11 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
   // meet this; short ones would be faster with four (8 KV heads x 4 queries,
   // D 128: a prompt of 256 tokens 28.9 against 20.6 us, of 512 34.6 against 25.4,
   // a chunk of 128 over 2000 42.1 against 35.2) and slower with sixteen (47.6,
-  // 49.8, 55.9).
-  // Over shared blocks two: their parts are joined by another kernel, by all SMs.
-  const int least = SHARED && a.part == kPrefix ? 2 : a.causal ? 8 : 4;
+  // 49.8, 55.9); kv8_attn keeps the parts, and with them the bits, that it had.
+  // The other calls take four (10 sequences of 37 to 63 rows x 4 KV heads x 7 over
+  // 1 to 4 tokens: 32 against 22 us).  Over shared blocks two: their parts are
+  // joined by another kernel, by all SMs.
+  const int least = SHARED && a.part == kPrefix ? 2 : SHARED || !a.causal ? 4 : 8;
   const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + least - 1) / least));
   if (static_cast<int>(blockIdx.x) >= ctas) return finish<SHARED>();
   const long long lo = divide(blockIdx.x * total, ctas), hi = divide((blockIdx.x + 1) * total, ctas);
