@@ -118,6 +118,12 @@ struct Part {
 };
 static_assert(sizeof(Part) == 64, "Part");
 
+// Over shared blocks: whether an item of so many cuts is left to the join kernel.
+// Its last CTA would read the parts alone, but a few it has read before that
+// kernel has started (six questions of 100 to 500 tokens behind 8192 shared ones,
+// most items cut once: 306 us, 311 with all of them left).
+__device__ __forceinline__ bool joined_later(int cuts) { return cuts >= 4; }
+
 // All 512 columns of tensor memory are one CTA's: the address is 0.  Each row
 // tile has 128 columns for S and 128 for O, of which D 64 leaves the second half
 // free: there P has a place of its own, and the next unit's S need not wait for
@@ -777,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           // for the kernel that joins them
           if (SHARED && a.part == kPrefix && use.u0 == 0)
             a.items[static_cast<size_t>(slot_base<SHARED>(a, use.p.s) + use.p.rt) * H + use.h] =
-                make_int4(p.first, p.c0, p.slot < 0 ? 0 : p.cuts + 1, 0);
+                make_int4(p.first, p.c0, p.slot >= 0 && joined_later(p.cuts) ? p.cuts + 1 : 0, 0);
         }
         kvq::mbar_arrive(bars + kPartFull + n_part % kParts);
         if (!more) break;
@@ -1243,7 +1249,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           a.tile_ml[slot * kRows + t * 128 + r] = make_float2(M, l);
         fence_before();
       }
-      if (!whole && !(SHARED && a.part == kPrefix)) {
+      if (!whole && !(SHARED && a.part == kPrefix && joined_later(p.cuts))) {
         ok = bar_all(2, 512, ok);
         if (!ok) break;
         if (tid == 0) {
