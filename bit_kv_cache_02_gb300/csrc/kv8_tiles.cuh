@@ -18,7 +18,6 @@
 //                    softmax runs under the other's products.
 //   warp 21          walks the CTA's share of the work: a ring of Parts.
 //   warp 22          looks up blocks and scales: a ring of Metas, one per unit.
-//   warp 23          prefetches the queries of the parts to come.
 //
 // Parts and Metas live in shared memory so that the other roles keep their
 // registers for data: a spilled register costs an L2 round trip here, as the
@@ -589,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
     kvq::mbar_init(bars + kDrained, 1);
     for (int i = 0; i < kParts; ++i) {
       kvq::mbar_init(bars + kPartFull + i, 1);
-      kvq::mbar_init(bars + kPartFree + i, 19);  // sixteen softmax warps, the products, the tables, the queries
+      kvq::mbar_init(bars + kPartFree + i, 18);  // sixteen softmax warps, the products, the tables
     }
     for (int i = 0; i < kMetas; ++i) {
       kvq::mbar_init(bars + kMetaFull + i, 1);
@@ -720,28 +719,6 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       if (!ok) {  // a wait ran out: no product may be left when tensor memory is given back
         if (leader) commit(base + SM::BAR + kDrained * 8);
         for (int i = 0; i < 100000 && !kvq::mbar_try_wait(bars + kDrained, 0); ++i) {
-        }
-      }
-    } else if (warp == 23) {
-      // ================================================= queries ahead
-      // A part's queries come to the second-level cache while the parts before it
-      // are computed: their rows are not read before, and an item waited longer
-      // for them than for its first keys.
-      for (uint32_t n_part = 0;; ++n_part) {
-        if (!__all_sync(kAll, wait(kPartFull + n_part % kParts, (n_part / kParts) & 1))) break;
-        const Part &p = parts[n_part % kParts];
-        const bool end = p.u0 == p.u1;
-        const int row = p.row, h = p.h, row0 = p.row0, n_rows = p.n * a.group;
-        __syncwarp();
-        if (lane == 0) kvq::mbar_arrive(bars + kPartFree + n_part % kParts);
-        if (end) break;
-        for (int r = row + lane; r < min(row + kRows, n_rows); r += 32) {
-          if (!row_in_bounds(a, row0, h, r)) continue;
-          const int tok = r / a.group;
-          const uint16_t *q = a.q.p + (static_cast<long long>(row0) + tok) * a.q.row +
-                              (static_cast<long long>(h) * a.group + r - tok * a.group) * a.q.head;
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
-          if (D == 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 64));
         }
       }
     } else if (warp == 21 && lane == 0) {
