@@ -7,7 +7,8 @@ The compute lives in libkvq.so (C ABI: include/kvq.h).  Modules:
   build  -- compiles csrc/*.cu for sm_103a into libkvq.so (in-tree)
   kvq    -- ctypes binding of the C ABI (argument marshalling only)
   kv8    -- the 8-bit paged cache (C ABI: include/kv8.h): append with rotation,
-            attention for decoding, draft checking and prompts
+            attention for decoding, draft checking and prompts, positions with
+            axes, cross attention, shared prefixes
   synth  -- seeded synthetic workloads (shapes of the benchmark configs)
 """
 

@@ -42,6 +42,13 @@
 // cut by a border are merged by the last CTA that finishes (fp32 partial O, M
 // and l in the workspace).
 //
+// SHARED: the launches of attention with shared blocks.  Over them, few rows make
+// few items, which are cut into parts of two units: 256 rows x 8 KV heads over 4096
+// shared tokens take 20 us, 5 of them for the products and weights of two units and
+// the rest for what comes once (3.3 until the line is cut, 3.3 until the part is
+// known, 4.1 for queries, 1 for keys, 5 for outputs).  1830 rows x 32 query heads
+// over 8192: 240 us, 1.02 PFLOP/s.
+//
 // Bound: the chain of a row tile.  Per unit it works on its softmax for about
 // 2350 clocks and waits 1800 for its products, which take 1270 where no others
 // are in the way: S (u + 1) goes where the weights of u lie, so Q K^T of the
