@@ -388,9 +388,7 @@ SharedPlan plan_shared(int D, int S, int H, int num_q_heads, long long rows, lon
   p.off_prefix = own.bytes;
   p.off_segs = own.bytes + prefix.bytes;
   p.off_items = align(p.off_segs + static_cast<size_t>(2) * S * 2 * sizeof(int4));
-  // (a group has at most one row tile pair that is not full)
-  const size_t items = p.prefix_tiles ? (static_cast<size_t>(rows) * group / kTileRows + S) * H : 0;
-  p.off_ml = align(p.off_items + items * sizeof(int4));
+  p.off_ml = align(p.off_items + static_cast<size_t>(2) * kMaxTileCtas * sizeof(int4));
   p.carry_blocks = (rows * group + 31) / 32;
   const size_t n = static_cast<size_t>(H) * p.carry_blocks * 32;
   p.off_o = align(p.off_ml + n * sizeof(float2));
@@ -400,22 +398,24 @@ SharedPlan plan_shared(int D, int S, int H, int num_q_heads, long long rows, lon
 
 cudaError_t launch_attn(const AttnArgs &a, bool tiles, cudaStream_t stream, uint64_t *launches) {
   const bool wide = a.geo.D == 128, shared = a.part != kWhole;
-  auto rows_kernel = [&]() {
+  auto rows_kernel = [&](const AttnArgs &a) {
     ++*launches;
     return a.fine ? (wide ? launch_rows_128_shared(a, stream) : launch_rows_64_shared(a, stream))
                   : (wide ? launch_rows_128(a, stream) : launch_rows_64(a, stream));
   };
-  auto tile_kernel = [&]() {
+  auto tile_kernel = [&](const AttnArgs &a) {
     ++*launches;
     return shared ? (wide ? launch_tiles_128_shared(a, stream) : launch_tiles_64_shared(a, stream))
                   : (wide ? launch_tiles_128(a, stream) : launch_tiles_64(a, stream));
   };
-  if (!tiles) return rows_kernel();
+  if (!tiles) return rows_kernel(a);
   // Over shared blocks the tile kernel goes first: the CTAs of the other one, which
   // wait for all before them, would keep it from the SMs.
-  cudaError_t e = a.part == kPrefix ? tile_kernel() : rows_kernel();
+  cudaError_t e = a.part == kPrefix ? tile_kernel(a) : rows_kernel(a);
   if (e != cudaSuccess) return e;
-  return a.part == kPrefix ? rows_kernel() : tile_kernel();
+  AttnArgs second = a;
+  second.first = 0;
+  return a.part == kPrefix ? rows_kernel(second) : tile_kernel(second);
 }
 
 }  // namespace kv8

@@ -188,7 +188,7 @@ struct AttnArgs {
   const int *group_start, *prefix_len;  // [groups + 1], [groups]; with kPrefix and kOwn
   int groups, max_group_rows;
   int4 *plan;        // two per segment: the groups', then the sequences'
-  int4 *items;       // of the tile kernel's items over shared blocks: the parts to join
+  int4 *items;       // [kMaxTileCtas][2]: what the join kernel joins, by the first CTA of its parts
   int first;         // the first launch behind the lookup of the segments
   // Partial results over what lies behind the shared blocks, of the rows of each
   // KV head, (tensor row, query head of the KV head):
@@ -244,7 +244,7 @@ __device__ __forceinline__ Group load_group(const AttnArgs &a, int g) {
   }
   x.blocks = prefix / a.geo.B;
   x.ok = r0 >= 0 && r1 >= r0 && r1 <= a.rows && r1 - r0 <= a.max_group_rows && own >= r0 && own <= r1 &&
-         (x.blocks == 0 || a.geo.seq_len[x.first] - (own - r0) >= x.blocks * a.geo.B);
+         (x.blocks == 0 || a.geo.seq_len[x.first] - static_cast<long long>(own - r0) >= x.blocks * a.geo.B);
   x.row0 = r0;
   x.n = x.ok ? r1 - r0 : 0;
   return x;

@@ -14,6 +14,8 @@ constexpr int kSegThreads = 128;
 __global__ void __launch_bounds__(kSegThreads) segments_kernel(const AttnArgs a) {
   asm volatile("griddepcontrol.launch_dependents;");
   const int i = blockIdx.x * kSegThreads + threadIdx.x;
+  if (a.groups)  // nothing to join so far
+    for (int k = i; k < kMaxTileCtas; k += gridDim.x * kSegThreads) a.items[2 * k] = make_int4(0, 0, 0, 0);
   if (i >= a.groups + a.geo.S) return;
   bool shut = false;
   const Seg x = i < a.groups ? group_seg(a, i) : a.groups ? own_seg(a, i - a.groups, shut) : load_seg<false>(a, i);
@@ -34,22 +36,34 @@ __global__ void __launch_bounds__(kSegThreads) segments_kernel(const AttnArgs a)
 // them, and here a CTA joins 32 rows, 64 channels.  (The last CTA that finishes
 // would read them alone: a group of 256 rows, 8 KV heads, has 19 for each head.)
 // A thread takes eight channels of a row, from the parts with 32 rows side by
-// side, eight parts at a time; shared memory turns them into whole rows.
+// side, eight parts at a time; shared memory turns them into whole rows.  An item
+// of so many parts ends four CTAs behind its first: there are kMaxTileCtas / 4 at
+// most, found by a look at all.
 constexpr int kJoinRows = 32, kJoinThreads = 256, kAtOnce = 8;
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnArgs a) {
   constexpr int PIECES = D / 64, SUBS = tiles::kRows / kJoinRows;
-  const int piece = blockIdx.x % PIECES, sub = blockIdx.x / PIECES % SUBS, h = blockIdx.x / (PIECES * SUBS) % a.geo.H;
-  const int slot = blockIdx.x / (PIECES * SUBS) / a.geo.H;
-  const tiles::Pair p = tiles::pair_of_slot<true>(a, slot);
-  const int row0 = p.rt * tiles::kRows + sub * kJoinRows;  // (of no meaning without units)
-  const int n_rows = p.units ? p.q.n * a.group : 0;
+  const int piece = blockIdx.x % PIECES, sub = blockIdx.x / PIECES % SUBS, nth = blockIdx.x / (PIECES * SUBS);
+  __shared__ int counts[kJoinThreads / 32], found;
   wait_before();
-  if (!p.units || row0 >= n_rows) return;
-  const int4 item = a.items[static_cast<size_t>(slot) * a.geo.H + h];
-  const int first = item.x, c0 = item.y, n = item.z;
-  // (where row_start or group_start falls, or a wait ran out, nothing was left here)
-  if (n <= 0 || n > kMaxTileCtas || c0 < 0 || c0 > kMaxTileCtas - n || first < 0 || first >= 2 * kMaxTileCtas) return;
+  const bool has = threadIdx.x < kMaxTileCtas && a.items[2 * threadIdx.x].y > 0;
+  const unsigned mask = __ballot_sync(0xffffffffu, has);
+  if (threadIdx.x == 0) found = -1;
+  if ((threadIdx.x & 31) == 0) counts[threadIdx.x >> 5] = __popc(mask);
+  __syncthreads();
+  int before = __popc(mask & ((1u << (threadIdx.x & 31)) - 1u));
+  for (int w = 0; w < static_cast<int>(threadIdx.x >> 5); ++w) before += counts[w];
+  if (has && before == nth) found = threadIdx.x;
+  __syncthreads();
+  const int c0 = found;
+  if (c0 < 0) return;
+  const int4 item = a.items[2 * c0];
+  const int first = item.x, n = item.y, h = item.z, row0 = item.w + sub * kJoinRows;
+  const int4 rows = a.items[2 * c0 + 1];
+  const int t0 = rows.x, n_rows = rows.y;  // the group's first tensor row, its rows of a KV head
+  if (row0 >= n_rows || !KVQ_IN_BOUNDS(a.geo.status, first, 2 * kMaxTileCtas) ||
+      !KVQ_IN_BOUNDS(a.geo.status, c0 + n - 1, kMaxTileCtas))
+    return;
   __shared__ float4 turned[kJoinRows][17];
   __shared__ float2 sums[kJoinRows];
   const float ninf = __int_as_float(0xff800000);
@@ -88,9 +102,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnArgs a) {
   }
   __syncthreads();
   const int r = threadIdx.x >> 3, q = threadIdx.x & 7, row = row0 + r;
-  if (row >= n_rows || !row_in_bounds(a, p.q.row0, h, row)) return;
+  if (row >= n_rows || !row_in_bounds(a, t0, h, row)) return;
   const int tok = row / a.group, head = h * a.group + row - tok * a.group;
-  const CarryRow carry = carry_row<D>(a, h, p.q.row0, row);
+  const CarryRow carry = carry_row<D>(a, h, t0, row);
   const float2 own = *carry.ml;
   if (own.y < 0.f) return;
   const Join j = join(sums[r], own);
@@ -103,7 +117,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnArgs a) {
     e[2 * k] = pack2<BF16>(fmaf(x.x, j.x, y.x * j.y) * f, fmaf(x.y, j.x, y.y * j.y) * f);
     e[2 * k + 1] = pack2<BF16>(fmaf(x.z, j.x, y.z * j.y) * f, fmaf(x.w, j.x, y.w * j.y) * f);
   }
-  *reinterpret_cast<uint4 *>(a.out.p + (static_cast<long long>(p.q.row0) + tok) * a.out.row + head * a.out.head +
+  *reinterpret_cast<uint4 *>(a.out.p + (static_cast<long long>(t0) + tok) * a.out.row + head * a.out.head +
                              64 * piece + 8 * q) = make_uint4(e[0], e[1], e[2], e[3]);
 }
 
@@ -116,12 +130,11 @@ cudaError_t launch_segments(const AttnArgs &a, cudaStream_t stream) {
 }
 
 cudaError_t launch_join(const AttnArgs &a, cudaStream_t stream) {
-  const long long slots = static_cast<long long>(a.rows) * a.group / kTileRows + a.segs;
-  const long long grid = slots * a.geo.H * (a.geo.D / 64) * (kTileRows / shared::kJoinRows);
-  if (grid > 2147483647LL) return cudaErrorInvalidConfiguration;
+  static_assert(kMaxTileCtas <= shared::kJoinThreads, "a thread per CTA of the tile kernel");
+  const unsigned grid = kMaxTileCtas / 4 * (a.geo.D / 64) * (kTileRows / shared::kJoinRows);
   auto kernel = a.geo.D == 128 ? (a.geo.bf16 ? shared::join_kernel<128, true> : shared::join_kernel<128, false>)
                                : (a.geo.bf16 ? shared::join_kernel<64, true> : shared::join_kernel<64, false>);
-  return launch_after(kernel, static_cast<unsigned>(grid), shared::kJoinThreads, 0, stream, a);
+  return launch_after(kernel, grid, shared::kJoinThreads, 0, stream, a);
 }
 
 }  // namespace kv8

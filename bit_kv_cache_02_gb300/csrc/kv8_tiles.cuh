@@ -44,9 +44,9 @@
 //
 // SHARED: the launches of attention with shared blocks.  Over them, few rows make
 // few items, which are cut into parts of two units: 256 rows x 8 KV heads over 4096
-// shared tokens take 20 us, 5 of them for the products and weights of two units and
-// the rest for what comes once (3.3 until the line is cut, 3.3 until the part is
-// known, 4.1 for queries, 1 for keys, 5 for outputs).  1830 rows x 32 query heads
+// shared tokens take 21 us, of which the second unit is 1.2: the rest comes once
+// (3.3 until the line is cut, 3.6 until the part is known, 4.1 for queries, 1 for
+// the first scores, 5 for the first unit, 4 for outputs and the end).  1830 rows x 32 query heads
 // over 8192: 240 us, 1.02 PFLOP/s.
 //
 // Bound: the chain of a row tile.  Per unit it works on its softmax for about
@@ -338,12 +338,8 @@ __device__ __forceinline__ Pair make_pair(const AttnArgs &a, int s, int rt) {
 // Sequence s owns the slots from row_start[s] * group / 256 + s on: at least
 // as many as row tile pairs.
 template <bool SHARED>
-__device__ __forceinline__ int slot_base(const AttnArgs &a, int s) {
-  return static_cast<int>(static_cast<long long>(row_start_of<SHARED>(a, s)) * a.group / kRows) + s;
-}
-template <bool SHARED>
 __device__ __forceinline__ Pair pair_of_slot(const AttnArgs &a, int slot) {
-  auto base = [&](int s) { return slot_base<SHARED>(a, s); };
+  auto base = [&](int s) { return static_cast<int>(static_cast<long long>(row_start_of<SHARED>(a, s)) * a.group / kRows) + s; };
   const int s = last_at_or_below(a.segs, slot, base);
   return make_pair<SHARED>(a, s, slot - base(s));
 }
@@ -764,10 +760,11 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
             p.slot = 2 * blockIdx.x + (lo < use.start ? 1 : 0);
             p.first = 2 * c0 + (divide(c0 * total, ctas) < use.start ? 1 : 0);
           }
-          // for the kernel that joins them
-          if (SHARED && a.part == kPrefix && use.u0 == 0)
-            a.items[static_cast<size_t>(slot_base<SHARED>(a, use.p.s) + use.p.rt) * H + use.h] =
-                make_int4(p.first, p.c0, p.slot >= 0 && joined_later(p.cuts) ? p.cuts + 1 : 0, 0);
+          // for the kernel that joins them (a CTA begins one such item at most, its last)
+          if (SHARED && a.part == kPrefix && use.u0 == 0 && p.slot >= 0 && joined_later(p.cuts)) {
+            a.items[2 * blockIdx.x] = make_int4(p.first, p.cuts + 1, p.h, p.row);
+            a.items[2 * blockIdx.x + 1] = make_int4(p.row0, p.n * a.group, 0, 0);
+          }
         }
         kvq::mbar_arrive(bars + kPartFull + n_part % kParts);
         if (!more) break;
