@@ -551,6 +551,47 @@ def test_shared_nonfinite(kv8, new, g):
     assert out[3 * new:].all() and not out[:new].any() and not out[2 * new:3 * new].any()
 
 
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("g", [2, 20])
+def test_shared_zeros_and_spread_scales(kv8, dtype, g):
+    """Blocks of zeros and values of 2^-40 to 2^10 on either side of the prefix's
+    end, scores in the hundreds: both parts' sums keep their shares."""
+    def spread(which):
+        def change(q, k, v):
+            q *= 6
+            k[:, :, 3] *= 8
+            n = len(v)
+            if which == "zeros in front":
+                v[: n // 2] = 0
+            elif which == "zeros behind":
+                v[n // 2:] = 0
+            elif which == "small in front":
+                v[: n // 2] *= 2.0 ** -12
+            else:
+                v[n // 2:] *= 2.0 ** (-40 if dtype == "bfloat16" else -8)
+                v[0] *= 2.0 ** 10
+        return change
+
+    for fmt in ("int8", "e4m3"):
+        for which in ("zeros in front", "zeros behind", "small in front", "small behind"):
+            r = Groups(kv8, [3], [0], 1, g, 128, 32, fmt, dtype, 400, rot=0, seed=3)
+            # the prefix by hand, so that its values are changed too
+            x = r.numbers((128, 1, 128))
+            kk, vv = x.copy(), r.numbers((128, 1, 128))
+            spread(which)(np.zeros((128, g, 128)), kk, vv)
+
+            def alike(q, k, v):
+                for s in range(3):
+                    k[128 * s:128 * s + 128], v[128 * s:128 * s + 128] = kk, vv
+
+            r.append([128] * 3, alike)
+            r.cache.block_table[1:, :4] = -1
+            r.prefix_len.fill_(128)
+            r.append([40, 3, 70], spread(which))
+            r.append([1, 2, 1], lambda q, k, v: q.__imul__(6))
+            r.shared()
+
+
 def test_shared_captured_and_replayed(kv8):
     """A captured call is replayed for other lengths, rows and groups within its
     bounds, and on another stream than the tensors' own."""
