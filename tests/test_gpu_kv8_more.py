@@ -7,13 +7,15 @@ join multiplies by powers of two with 2^-22 and adds once, which the bound's
 sums of 2^-24 per token and its 2^-15 of a score cover.)"""
 
 import math
+import subprocess
+import sys
 
 import numpy as np
 import pytest
 import torch
 
 from oracle import kv8 as ok
-from test_gpu_kv8 import TYPES, Run, _dev, _host, kv8  # noqa: F401  (kv8: the fixture)
+from test_gpu_kv8 import ROOT, TYPES, Run, _dev, _host, kv8  # noqa: F401  (kv8: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -703,6 +705,63 @@ def test_two_streams_with_workspaces_of_their_own(kv8):
                                 row_start=r.start, stream=streams[j])
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for line in outs for o in line)
+
+
+@pytest.mark.parametrize("new", [1, 30])
+def test_pool_past_four_gib(kv8, new):
+    """Blocks behind 4 GiB of the pool, for both kernels of either attention, and
+    stored there by an append with axes."""
+    r = Groups(kv8, [3], [300], 4, 2, 128, 128, "int8", "bfloat16", 600, seed=4, spare=34000)
+    assert r.cache.codes.numel() > 2 ** 32 and int(r.cache.block_table.max()) * r.cache.codes[0].numel() > 2 ** 32
+    r.append([100, 150, 3])
+    r.append([new] * 3)
+    r.shared()
+    r.cache.block_table[1:, :2] = r.cache.block_table[0, :2]
+    cross(r, [new, 2, 1])
+    a = AxesRun(kv8, 2, 4, 1, 128, 128, "int8", "bfloat16", 600, seed=5, spare=34000)
+    a.append([260, 130])
+    tab = a.cache.block_table.cpu().numpy()
+    for s, L in enumerate(a.orc.lengths()):
+        for b in range(L // 128):
+            for h in range(4):
+                for j in (0, 1):
+                    want, scale = a.orc.block(s, b, h, j == 1)
+                    np.testing.assert_array_equal(_host(a.cache.codes[int(tab[s, b]), h, j]), want)
+                    assert float(a.cache.scales[int(tab[s, b]), h, j]) == np.float32(scale)
+
+
+def test_first_calls_of_a_process_are_captured(kv8):
+    """Nothing has to run before a capture, for any of the kernels."""
+    code = """
+import torch
+from bit_kv_cache_02_gb300 import kv8
+c = kv8.KV8Cache(2, 2, 600, 18, head_dim=128, block=64, fmt="e4m3", dtype=torch.bfloat16)
+c.block_table.copy_(torch.arange(18).view(2, 9))
+x = torch.randn(400, 8, 128, device="cuda").bfloat16()
+q = torch.zeros(400, 4, 128, device="cuda", dtype=torch.bfloat16)
+outs = [torch.zeros_like(q) for _ in range(4)]
+i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+start, late, groups, prefix = i32([0, 300, 400]), i32([0, 100, 101]), i32([0, 2]), i32([64])
+pos, rope, axes = torch.arange(400, device="cuda").int().expand(2, 400), kv8.rope_table(600, 128), kv8.rope_axes([0, 1] * 32)
+ws, wc = kv8.alloc_shared_workspace(c, 4, 101, 100, 101), kv8.alloc_cross_workspace(c, 4, 100)
+g = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(g):
+    c.seq_len += start[1:] - start[:-1]
+    kv8.kv8_append_axes(c, x[:, 4:6], x[:, 6:], pos, axes, rope, row_start=start, max_new=300, q=x[:, :4], q_out=q)
+    kv8.kv8_shared_attn(c, q[:101], outs[0][:101], ws, 600, groups, prefix, 101, row_start=late, max_new=100)
+    kv8.kv8_cross_attn(c, q[:101], outs[1][:101], wc, 600, row_start=late, max_rows=100)
+g.replay()
+kv8.kv8_shared_attn(c, q[:101], outs[2][:101], ws, 600, groups, prefix, 101, row_start=late, max_new=100)
+kv8.kv8_cross_attn(c, q[:101], outs[3][:101], wc, 600, row_start=late, max_rows=100)
+torch.cuda.synchronize()
+assert c.seq_len.tolist() == [300, 100] and int(c.status.item()) == 0
+assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[3])
+assert all(bool((o[:100] != 0).any(-1).all()) for o in outs[1::2])
+print("captured first")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stdout[-500:] + r.stderr[-2000:]
 
 
 def test_wait_that_runs_out(kv8):
