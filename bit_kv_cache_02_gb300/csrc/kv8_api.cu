@@ -241,22 +241,22 @@ int kv8_append(const kv8_cache *cache, const kv8_rows *k, const kv8_rows *v, con
                 nullptr, stream);
 }
 
-int kv8_append_axes(const kv8_cache *cache, const kv8_rows *k, const kv8_rows *v, const kv8_rows *q,
-                    const kv8_rows *q_out, int32_t num_q_heads, const int32_t *row_start, int32_t rows,
-                    int32_t max_new, const float *rope, int32_t rope_rows, int32_t rot_dim, int32_t interleaved,
-                    const int32_t *positions, int64_t axis_stride, int32_t num_axes, const uint8_t *axis_of_pair,
-                    void *stream) {
-  if (num_axes < 1 || num_axes > KV8_MAX_AXES || rot_dim % 16 != 0 || rot_dim > 128) return KVQ_ERR_UNSUPPORTED;
-  if (rot_dim < 16 || rope_rows < 1 || !axis_of_pair) return KVQ_ERR_INVALID_ARG;
-  if (rows > 0 && !positions) return KVQ_ERR_INVALID_ARG;
-  if (!aligned(positions, 4)) return KVQ_ERR_ALIGNMENT;
-  kv8::Axes axes = {positions, num_axes > 1 ? axis_stride : 0, rope_rows, {0, 0, 0, 0}};
-  for (int i = 0; i < rot_dim / 2; ++i) {
-    if (axis_of_pair[i] >= num_axes) return KVQ_ERR_INVALID_ARG;
-    axes.map[i / 16] |= static_cast<uint32_t>(axis_of_pair[i]) << (2 * (i % 16));
+int kv8_append_axes(const kv8_cache *cache, const kv8_axes_append *x, void *stream) {
+  if (!x) return KVQ_ERR_INVALID_ARG;
+  if (x->num_axes < 1 || x->num_axes > KV8_MAX_AXES || x->rot_dim % 16 != 0 || x->rot_dim > 128)
+    return KVQ_ERR_UNSUPPORTED;
+  if (x->rot_dim < 16 || x->rope_rows < 1 || (x->rows > 0 && !x->positions)) return KVQ_ERR_INVALID_ARG;
+  if (!aligned(x->positions, 4)) return KVQ_ERR_ALIGNMENT;
+  kv8::Axes axes = {x->positions, x->num_axes > 1 ? x->axis_stride : 0, x->rope_rows, {0, 0, 0, 0}};
+  for (int i = 0; i < x->rot_dim / 2; ++i) {
+    if (x->axis_of_pair[i] >= x->num_axes) return KVQ_ERR_INVALID_ARG;
+    axes.map[i / 16] |= static_cast<uint32_t>(x->axis_of_pair[i]) << (2 * (i % 16));
   }
-  return append(cache, k, v, q, q_out, num_q_heads, row_start, rows, max_new, rope, rope_rows, rot_dim, interleaved,
-                &axes, stream);
+  // (without rows the queries' tensors may have no data either)
+  const bool with_q = x->num_q_heads != 0;
+  return append(cache, &x->k, &x->v, with_q || x->q.data ? &x->q : nullptr,
+                with_q || x->q_out.data ? &x->q_out : nullptr, x->num_q_heads, x->row_start, x->rows, x->max_new,
+                x->rope, x->rope_rows, x->rot_dim, x->interleaved, &axes, stream);
 }
 
 int64_t kv8_attn_workspace_bytes(const kv8_cache *cache, int32_t num_q_heads, int32_t max_new) {

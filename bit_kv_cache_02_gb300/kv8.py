@@ -39,10 +39,23 @@ class RowsStruct(ctypes.Structure):
     _fields_ = [("data", c_void_p), ("row_stride", c_int64), ("head_stride", c_int64)]
 
 
+class AxesStruct(ctypes.Structure):
+    """Mirror of `kv8_axes_append` (include/kv8.h)."""
+    _fields_ = [
+        ("k", RowsStruct), ("v", RowsStruct), ("q", RowsStruct), ("q_out", RowsStruct),
+        ("row_start", c_void_p), ("rope", c_void_p), ("positions", c_void_p), ("axis_stride", c_int64),
+        ("num_q_heads", c_int32), ("rows", c_int32), ("max_new", c_int32), ("rope_rows", c_int32),
+        ("rot_dim", c_int32), ("interleaved", c_int32), ("num_axes", c_int32), ("axis_of_pair", ctypes.c_uint8 * 64),
+    ]
+
+
 # The same bytes, packed at a tenth of the cost of a ctypes structure: a call's
 # host time is what a one-token step waits for.
 _pack_rows = struct.Struct("@Pqq").pack
+_pack_axes = struct.Struct("@24s24s24s24sPPPq7i64s4x").pack
+_NO_ROWS = _pack_rows(0, 0, 0)
 assert struct.calcsize("@Pqq") == ctypes.sizeof(RowsStruct)
+assert struct.calcsize("@24s24s24s24sPPPq7i64s4x") == ctypes.sizeof(AxesStruct)
 
 
 _I32, _F32 = torch.int32, torch.float32
@@ -61,8 +74,7 @@ def _sign():
         "kv8_attn_workspace_bytes": (c_int64, [C, c_int32, c_int32]),
         "kv8_attn": (ctypes.c_int, [C, c_int32, R, R, c_void_p, c_int32, c_int32, c_float, c_void_p, c_size_t,
                                     c_int32, c_void_p]),
-        "kv8_append_axes": (ctypes.c_int, [C, R, R, R, R, c_int32, c_void_p, c_int32, c_int32, c_void_p, c_int32,
-                                           c_int32, c_int32, c_void_p, c_int64, c_int32, ctypes.c_char_p, c_void_p]),
+        "kv8_append_axes": (ctypes.c_int, [C, R, c_void_p]),
         "kv8_cross_attn_workspace_bytes": (c_int64, [C, c_int32, c_int32]),
         "kv8_shared_attn_workspace_bytes": (c_int64, [C, c_int32, c_int32, c_int32, c_int32]),
         "kv8_shared_attn": (ctypes.c_int, [C, c_int32, R, R, c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_int32,
@@ -232,15 +244,18 @@ def kv8_append_axes(cache: KV8Cache, k, v, positions, axes: bytes, rope, row_sta
     for the positions that occur, whatever the capacity."""
     rows, ks, vs, qs, os, heads = _append_tensors(cache, k, v, q, q_out)
     table_rows, rot = _table(rope, cache)
-    shape = positions.shape
-    if positions.dtype is not _I32 or len(shape) != 2 or shape[1] != rows or (rows > 1 and positions.stride(1) != 1) \
+    shape, stride = positions.shape, positions.stride()
+    if positions.dtype is not _I32 or len(shape) != 2 or shape[1] != rows or (rows > 1 and stride[1] != 1) \
             or positions.get_device() != cache.device_index:
         raise ValueError(f"positions: an int32 tensor [axes][{rows}] with contiguous lines on {cache.device} is needed")
     if type(axes) is not bytes or 2 * len(axes) != rot:
         raise ValueError(f"axes: rope_axes of {rot // 2} axes is needed")
-    _launch(lib.kv8_append_axes, "kv8_append_axes", cache, stream, cache.ref, ks, vs, qs, os, heads,
-            _row_start(row_start, cache), rows, max_new, rope.data_ptr(), table_rows, rot, 1 if interleaved else 0,
-            positions.data_ptr(), positions.stride(0), shape[0], axes)
+    if heads == 0 and q is not None:
+        raise ValueError("q: [rows][heads][D] with heads is needed")
+    _launch(lib.kv8_append_axes, "kv8_append_axes", cache, stream, cache.ref,
+            _pack_axes(ks, vs, qs or _NO_ROWS, os or _NO_ROWS, _row_start(row_start, cache) or 0, rope.data_ptr(),
+                       positions.data_ptr(), stride[0], heads, rows, max_new, table_rows, rot,
+                       1 if interleaved else 0, shape[0], axes))
 
 
 def attn_workspace_bytes(cache: KV8Cache, num_q_heads: int, max_new: int = 1) -> int:

@@ -177,19 +177,23 @@ int kv8_append(const kv8_cache *cache, const kv8_rows *k, const kv8_rows *v,
                int32_t interleaved, void *stream);
 
 /*
- * kv8_append_axes -- kv8_append for positions that are given.
+ * kv8_append_axes -- kv8_append for positions that are given.  Its arguments are
+ * one struct, which is read before the call returns: a call's host time is what a
+ * one-token step waits for, and most of that is the passing of arguments.
  *
+ *   k, v, q, q_out, num_q_heads, row_start, rows, max_new, interleaved  as in
+ *              kv8_append (without queries: num_q_heads 0, q and q_out without
+ *              data).
  *   positions  device int32: position of row r on axis x at
  *              positions[x * axis_stride + r].  Those of rows of no
  *              sequence may hold anything.
  *   axis_stride  any (0: all axes have the first one's); not used with one axis.
  *   num_axes   1 .. KV8_MAX_AXES.
- *   axis_of_pair  HOST array of rot_dim / 2 axes, read before the call returns:
- *              channel pair i (as in kv8_append, i + rot_dim / 2 or 2 i + 1
- *              beside it) turns by the angle i of the table's row
- *              positions[axis_of_pair[i]].  In order (the first pairs by the first
- *              axis, ...) or in turn, as the model has them; in order is faster
- *              where four aligned pairs have one axis.
+ *   axis_of_pair  the first rot_dim / 2 count: channel pair i (as in kv8_append,
+ *              i + rot_dim / 2 or 2 i + 1 beside it) turns by the angle i of the
+ *              table's row positions[axis_of_pair[i]].  In order (the first pairs by
+ *              the first axis, ...) or in turn, as the model has them; in order is
+ *              faster where four aligned pairs have one axis.
  *   rope, rope_rows  as in kv8_append, for positions 0 .. rope_rows - 1, whatever
  *              the capacity.  The table's columns may have any angles: one
  *              sequence of frequencies over all pairs, or one anew for each axis.
@@ -201,11 +205,19 @@ int kv8_append(const kv8_cache *cache, const kv8_rows *k, const kv8_rows *v,
  * and keys, and KV8_STATUS_BAD_POSITION is set.  With one axis whose positions
  * are the tokens' places the results are kv8_append's, bit for bit.  One kernel.
  */
-int kv8_append_axes(const kv8_cache *cache, const kv8_rows *k, const kv8_rows *v, const kv8_rows *q,
-                    const kv8_rows *q_out, int32_t num_q_heads, const int32_t *row_start, int32_t rows,
-                    int32_t max_new, const float *rope, int32_t rope_rows, int32_t rot_dim, int32_t interleaved,
-                    const int32_t *positions, int64_t axis_stride, int32_t num_axes, const uint8_t *axis_of_pair,
-                    void *stream);
+typedef struct kv8_axes_append {
+  kv8_rows k, v, q, q_out;
+  const int32_t *row_start;
+  const float   *rope;
+  const int32_t *positions;
+  int64_t  axis_stride;
+  int32_t  num_q_heads, rows, max_new;
+  int32_t  rope_rows, rot_dim, interleaved;
+  int32_t  num_axes;
+  uint8_t  axis_of_pair[64];
+} kv8_axes_append;
+
+int kv8_append_axes(const kv8_cache *cache, const kv8_axes_append *args, void *stream);
 
 /*
  * kv8_attn_workspace_bytes -- scratch size for kv8_attn calls with at most

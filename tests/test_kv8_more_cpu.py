@@ -94,13 +94,31 @@ def _ref(x):
 
 def _axes(kv8, st, **kw):
     R = kv8.RowsStruct
-    d = dict(k=R(BASE, 256, 128), v=R(BASE, 256, 128), q=R(BASE, 512, 128), q_out=R(BASE, 512, 128), heads=4,
-             row_start=BASE, rows=10, max_new=10, rope=BASE, rope_rows=5, rot=128, inter=0, positions=BASE, stride=10,
-             axes=3, map=bytes([0] * 20 + [1] * 20 + [2] * 24))
+    d = dict(k=R(BASE, 256, 128), v=R(BASE, 256, 128), q=R(BASE, 512, 128), q_out=R(BASE, 512, 128), num_q_heads=4,
+             row_start=BASE, rows=10, max_new=10, rope=BASE, rope_rows=5, rot_dim=128, interleaved=0, positions=BASE,
+             axis_stride=10, num_axes=3, axis_of_pair=bytes([0] * 20 + [1] * 20 + [2] * 24))
     d.update(kw)
-    return kv8.lib.kv8_append_axes(ctypes.byref(st), _ref(d["k"]), _ref(d["v"]), _ref(d["q"]), _ref(d["q_out"]),
-                                   d["heads"], d["row_start"], d["rows"], d["max_new"], d["rope"], d["rope_rows"],
-                                   d["rot"], d["inter"], d["positions"], d["stride"], d["axes"], d["map"], None)
+    args = kv8.AxesStruct()
+    for k, v in d.items():
+        if k == "axis_of_pair":
+            v = (ctypes.c_uint8 * 64)(*v)
+        setattr(args, k, v if v is not None or k not in "kvqq_out" else R(0, 0, 0))
+    return kv8.lib.kv8_append_axes(ctypes.byref(st), ctypes.byref(args), None)
+
+
+def test_axes_struct_layout(kv8):
+    """The packed bytes of a call are the struct's."""
+    A, R = kv8.AxesStruct, kv8.RowsStruct
+    axes = bytes(range(4)) * 16
+    rows = [kv8._pack_rows(8 * i + 1, 8 * i + 2, 8 * i + 3) for i in range(4)]
+    raw = kv8._pack_axes(*rows, 101, 102, 103, -104, 1, 2, 3, 4, 5, 6, 7, axes)
+    x = A.from_buffer_copy(raw)
+    for i, t in enumerate((x.k, x.v, x.q, x.q_out)):
+        assert (t.data, t.row_stride, t.head_stride) == (8 * i + 1, 8 * i + 2, 8 * i + 3)
+    assert (x.row_start, x.rope, x.positions, x.axis_stride) == (101, 102, 103, -104)
+    assert (x.num_q_heads, x.rows, x.max_new, x.rope_rows, x.rot_dim, x.interleaved, x.num_axes) == tuple(range(1, 8))
+    assert bytes(x.axis_of_pair) == axes and ctypes.sizeof(R) == 24 and ctypes.sizeof(A) == 224
+    assert kv8.lib.kv8_append_axes(ctypes.byref(_struct(kv8)), None, None) == -1
 
 
 def _cross(kv8, st, **kw):
@@ -137,12 +155,13 @@ def test_bad_cache_refused(kv8, kw, code):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(axes=0), -2), (dict(axes=5), -2), (dict(axes=2), -1),           # the map names a third axis
-    (dict(map=None), -1), (dict(positions=None), -1), (dict(positions=BASE + 2), -5), (dict(rot=0), -1), (dict(rot=-16), -1), (dict(rot=24), -2), (dict(rot=144), -2),
-    (dict(rope=None), -1), (dict(rope=BASE + 4), -5), (dict(rope_rows=0), -1), (dict(inter=2), -1),
+    (dict(num_axes=0), -2), (dict(num_axes=5), -2), (dict(num_axes=2), -1),           # the map names a third axis
+    (dict(axis_of_pair=bytes([0] * 63 + [4])), -1), (dict(positions=None), -1), (dict(positions=BASE + 2), -5),
+    (dict(rot_dim=0), -1), (dict(rot_dim=-16), -1), (dict(rot_dim=24), -2), (dict(rot_dim=144), -2),
+    (dict(rope=None), -1), (dict(rope=BASE + 4), -5), (dict(rope_rows=0), -1), (dict(interleaved=2), -1),
     (dict(rows=-1), -1), (dict(max_new=1001), -3), (dict(row_start=BASE + 2), -5), (dict(row_start=None, rows=2), -1),
-    (dict(k="null"), -1), (dict(q_out="null"), -1), (dict(heads=0), -1), (dict(v=(BASE, 252, 128)), -5),
-    (dict(q_out=(BASE, 1024, 128)), -1),
+    (dict(k="null"), -1), (dict(q="null"), -1), (dict(q_out="null"), -1), (dict(num_q_heads=0), -1),
+    (dict(v=(BASE, 252, 128)), -5), (dict(q_out=(BASE, 1024, 128)), -1),
 ])
 def test_bad_append_axes_refused(kv8, kw, code):
     assert _axes(kv8, _struct(kv8), **_args(kv8, kw)) == code
@@ -180,6 +199,8 @@ def test_bad_shared_refused(kv8, kw, code):
 def test_nothing_to_do_is_ok(kv8):
     st = _struct(kv8)
     assert _axes(kv8, st, rows=0) == 0 and _axes(kv8, st, max_new=0) == 0
+    assert _axes(kv8, st, rows=0, q=None, q_out=None, positions=None) == 0
+    assert _axes(kv8, st, rows=0, num_q_heads=0, q=None, q_out=None) == 0
     assert _cross(kv8, st, rows=0) == 0 and _shared(kv8, st, rows=0) == 0
 
 
@@ -211,6 +232,8 @@ def test_python_checks(kv8):
     rope, pos = kv8.rope_table(10, 64, device="cpu"), torch.zeros(3, 2, dtype=torch.int32)
     axes = kv8.rope_axes([0] * 8 + [1] * 12 + [2] * 12)
     assert axes == bytes([0] * 8 + [1] * 12 + [2] * 12)
+    with pytest.raises(ValueError, match="heads"):
+        kv8.kv8_append_axes(c, x, x, pos, axes, rope, q=x[:, :0], q_out=x[:, :0])
     for bad in (dict(positions=pos.long()), dict(positions=pos[:, :1]), dict(positions=pos[0]),
                 dict(positions=torch.zeros(2, 3, dtype=torch.int32).T), dict(axes=axes[:-1]), dict(axes=list(axes)),
                 dict(rope=rope.double()), dict(rope=rope[:, :32]), dict(k=x.half()), dict(q=x),
