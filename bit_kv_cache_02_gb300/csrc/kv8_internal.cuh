@@ -345,9 +345,10 @@ __device__ __forceinline__ int last_seen(const AttnArgs &a, const T &q, int tok)
 
 // A row of KV head h among the partial results: (max, sum), and channels 4 c
 // to 4 c + 3.  A thread of the tile kernel has a row, and a warp 32 neighbours:
-// with rows side by side its accesses are 512 bytes each.  The rows kernel has a
-// row's channels side by side (11 groups of 3 to 25 sequences, few rows: 28.5 us,
-// 37 the other way), so its order is taken where no sequence's rows are many.
+// with rows side by side its accesses are 512 bytes each (six questions of 100 to
+// 500 tokens behind 8192 shared ones: 312 us, 315 the other way).  The rows kernel
+// has a row's channels side by side, and its order is taken where no sequence's rows
+// are many (12 groups of drafts: 54 us, 55.8 the other way).
 struct CarryRow {
   float2 *ml;
   float4 *o;
@@ -360,7 +361,8 @@ __device__ __forceinline__ CarryRow carry_row(const AttnArgs &a, int h, int row0
   size_t at = static_cast<size_t>(h * a.carry_blocks) * 32 + r;
   if (!KVQ_IN_BOUNDS(a.geo.status, r, a.carry_blocks * 32) || !KVQ_IN_BOUNDS(a.geo.status, h, a.geo.H)) at = 0;
   const int lane = static_cast<int>(r & 31);
-  return {a.carry_ml + at, a.carry_o + (a.carry_wide ? (at - lane) * (D / 4) + lane : at * (D / 4)), a.carry_wide ? 32 : 1};
+  return {a.carry_ml + at, a.carry_o + (a.carry_wide ? (at - lane) * (D / 4) + lane : at * (D / 4)),
+          a.carry_wide ? 32 : 1};
 }
 
 // The factors that join two partial results (max, sum), and what their weighted

@@ -489,8 +489,16 @@ __device__ __forceinline__ void emit(const AttnArgs &a, const Work &w, int h, in
               inverse_sum(sum, last_seen(a, w.q, tok)));
 }
 
+// CTAs per SM that the registers are cut for; 0: as the compiler likes.  Three
+// where launch_one wants, or might take, as many: with what FINE keeps the
+// compiler would take registers for two.
+template <int D, int FMT, int HALVES, bool FINE>
+constexpr int min_ctas() {
+  return FINE && (D == 64 || (HALVES == 1 && FMT == KV8_E4M3)) ? 3 : 0;
+}
+
 template <int D, int FMT, bool BF16, int HALVES, bool FINE>
-__global__ void __launch_bounds__(kWarps * 32, FINE && (D == 64 || (HALVES == 1 && FMT == KV8_E4M3)) ? 3 : 0) rows_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, min_ctas<D, FMT, HALVES, FINE>()) rows_kernel(const AttnArgs a) {
   using SM = Smem<D, HALVES, FINE>;
   constexpr int NT = SM::NT;  // output n-tiles
   constexpr int KS = D / 16;  // k-steps of the scores

@@ -339,7 +339,9 @@ __device__ __forceinline__ Pair make_pair(const AttnArgs &a, int s, int rt) {
 // as many as row tile pairs.
 template <bool SHARED>
 __device__ __forceinline__ Pair pair_of_slot(const AttnArgs &a, int slot) {
-  auto base = [&](int s) { return static_cast<int>(static_cast<long long>(row_start_of<SHARED>(a, s)) * a.group / kRows) + s; };
+  auto base = [&](int s) {
+    return static_cast<int>(static_cast<long long>(row_start_of<SHARED>(a, s)) * a.group / kRows) + s;
+  };
   const int s = last_at_or_below(a.segs, slot, base);
   return make_pair<SHARED>(a, s, slot - base(s));
 }
@@ -537,7 +539,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
 
   // ---- this CTA's range of the line
   long long total = 0, before = 0;
-  const int slots = static_cast<int>(static_cast<long long>(min(row_start_of<SHARED>(a, a.segs), a.rows)) * a.group / kRows) + a.segs;
+  const long long last_row = min(row_start_of<SHARED>(a, a.segs), a.rows);
+  const int slots = static_cast<int>(last_row * a.group / kRows) + a.segs;
   Pair mine;
   {
     // the slots below need row_start to rise
