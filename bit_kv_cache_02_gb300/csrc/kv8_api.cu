@@ -397,7 +397,7 @@ SharedPlan plan_shared(int D, int S, int H, int num_q_heads, long long rows, lon
 }
 
 cudaError_t launch_attn(const AttnArgs &a, bool tiles, cudaStream_t stream, uint64_t *launches) {
-  const bool wide = a.geo.D == 128, shared = a.part != kWhole;
+  const bool wide = a.geo.D == 128;
   auto rows_kernel = [&](const AttnArgs &a) {
     ++*launches;
     return a.fine ? (wide ? launch_rows_128_shared(a, stream) : launch_rows_64_shared(a, stream))
@@ -405,7 +405,7 @@ cudaError_t launch_attn(const AttnArgs &a, bool tiles, cudaStream_t stream, uint
   };
   auto tile_kernel = [&](const AttnArgs &a) {
     ++*launches;
-    return shared ? (wide ? launch_tiles_128_shared(a, stream) : launch_tiles_64_shared(a, stream))
+    return a.fine ? (wide ? launch_tiles_128_shared(a, stream) : launch_tiles_64_shared(a, stream))
                   : (wide ? launch_tiles_128(a, stream) : launch_tiles_64(a, stream));
   };
   if (!tiles) return rows_kernel(a);

@@ -305,8 +305,8 @@ __device__ __forceinline__ Seg load_seg(const AttnArgs &a, int s) {
   return {q.L, q.n, q.row0, 0, s, q.ok};
 }
 
-// The kernels of one call with shared blocks start while the ones before still
-// run.  Each lets the next one start once the segments are there: the first waits
+// The kernels of one call of cross attention or with shared blocks start while the
+// ones before still run.  Each lets the next one start once the segments are there: the first waits
 // for them, and the others start behind it.  Each waits for the one before it
 // at the latest before it ends, so that the end of one is the end of all before.
 __device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

@@ -1,4 +1,4 @@
-// The same for groups that share blocks, head_dim 64.
+// The few-rows kernels of cross attention and shared blocks for head_dim 64.
 #include "kv8_rows.cuh"
 
 namespace kv8 {

@@ -42,7 +42,11 @@
 // cut by a border are merged by the last CTA that finishes (fp32 partial O, M
 // and l in the workspace).
 //
-// SHARED: the launches of attention with shared blocks.  Over them, few rows make
+// SHARED: the kernels of cross attention and of attention with shared blocks, whose
+// segments have been looked up before.  They start beside the rows kernel; joining
+// partial results costs them registers, and long calls 3 to 4% (16 entries x 16
+// heads of 200 to 448 rows over 1500 tokens, D 64: 115 us replayed, 112 without),
+// but short ones gain a quarter (27.5 against 21 us).  Over shared blocks, few rows make
 // few items, which are cut into parts of two units: 256 rows x 8 KV heads over 4096
 // shared tokens take 21 us, of which the second unit is 1.2: the rest comes once
 // (3.3 until the line is cut, 3.6 until the part is known, 4.1 for queries, 1 for
@@ -544,8 +548,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
   Pair mine;
   {
     // the slots below need row_start to rise
-    // (with shared blocks, where the rows of all sequences are undefined otherwise,
-    // a look at each costs the start more than the items that it saves)
+    // (SHARED: a look at each costs the start more than the items that it saves; an
+    // item that it loses is rows left alone)
     bool falls = false;
     if (!SHARED && a.row_start)
       for (int s = tid; s < geo.S; s += kThreads)
@@ -567,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
   // The other calls take four (10 sequences of 37 to 63 rows x 4 KV heads x 7 over
   // 1 to 4 tokens: 32 against 22 us).  Over shared blocks two: their parts are
   // joined by another kernel, by all SMs.
-  const int least = SHARED && a.part == kPrefix ? 2 : SHARED || !a.causal ? 4 : 8;
+  const int least = !SHARED ? 8 : a.part == kPrefix ? 2 : 4;
   const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + least - 1) / least));
   if (static_cast<int>(blockIdx.x) >= ctas) return finish<SHARED>();
   const long long lo = divide(blockIdx.x * total, ctas), hi = divide((blockIdx.x + 1) * total, ctas);
@@ -1164,11 +1168,12 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       };
       // With shared blocks: 32 channels of the row's partial result, left for the
       // other launch, or joined with what that has left.
-      const CarryRow carry = SHARED ? carry_row<D>(a, p.h, p.row0, some) : CarryRow{};
+      auto carry_of = [&]() { return carry_row<D>(a, p.h, p.row0, min(p.row + t * 128 + r, p.n * a.group - 1)); };
       const bool leaves = SHARED && p.base, joins = SHARED && a.part == kPrefix;
       auto finish_row = [&](int c, float *o, float top, float sum) {
         if (leaves) {
           if (!valid || !inside) return;
+          const CarryRow carry = carry_of();
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             carry.at(8 * c + k) = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
@@ -1177,6 +1182,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
         }
         if (joins) wait_before();
         if (joins && valid && inside) {
+          const CarryRow carry = carry_of();
           const Join n = join(make_float2(top == ninf ? top : top - kShift, sum), *carry.ml);
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
@@ -1193,7 +1199,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       auto store_rows = [&]() {
         bar_sync(3 + t, 256);
         // (a row that is not to be written)
-        const bool shut = joins && out_off >= 0 && carry.ml->y < 0.f;
+        const bool shut = joins && out_off >= 0 && carry_of().ml->y < 0.f;
 #pragma unroll 4
         for (int i = 0; i < NQ; ++i) {
           const long long off = __shfl_sync(kAll, shut ? -1 : out_off, (i0 + i) * RPI + lane / LPR);
