@@ -1,7 +1,8 @@
 // What cross attention and attention with shared blocks need besides the rows and
 // the tile kernel: the segments, looked up once for all CTAs, and the join of the
-// tile kernel's parts over shared blocks.  Both are bound by latency: 3 us for 65 segments, of which
-// a launch is two, and 8 us for 8 items of 19 parts of 256 rows (18 MB).
+// tile kernel's parts over shared blocks.  Both are bound by latency: 3 us for 65
+// segments, of which a launch is two, and 8 us for 8 items of 19 parts of 256 rows
+// (18 MB).
 #include "kv8_rows.cuh"
 #include "kv8_tiles.cuh"
 
