@@ -293,6 +293,11 @@ struct Plain {
 // of the warps and the outputs, whatever its length.  Short ones are not cut, and
 // one warp does all of a short one, its neighbours the next ones: they cost
 // little besides, and no barrier.  `each`: one triple per CTA, none cut.
+// Drawn batches with other constants, replayed: short up to 8 or 16 units 26.5 and
+// 29.9 us instead of 24.5; 8 units besides a long triple's instead of 14, 17.4 for
+// 16.2; `each` for 8 units more than a CTA's share instead of 16, 17.5 for 12.1, and
+// for triples of 16 units at most, whatever the share, 22.9 for 17.0 (16 x 16 heads,
+// four rows over 1500 tokens).
 constexpr int kShort = 4, kOverShort = 2, kOver = 14;
 constexpr int kEach = 4 * kWarps;
 struct Fine {
