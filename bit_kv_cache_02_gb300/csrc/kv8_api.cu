@@ -175,8 +175,10 @@ int check_workspace(const void *workspace, size_t given, size_t needed) {
   return aligned(workspace, 256) ? KVQ_OK : KVQ_ERR_ALIGNMENT;
 }
 
-// The segments of whole sequences, two int4 each.
-size_t seg_bytes(const kv8_cache *c) { return (static_cast<size_t>(c->num_seqs) * 32 + 255) / 256 * 256; }
+// The segments of whole sequences, two int4 each, and the words behind them.
+size_t seg_bytes(const kv8_cache *c) {
+  return (static_cast<size_t>(c->num_seqs) * 32 + kv8::fall_words(0, c->num_seqs) * sizeof(int) + 255) / 256 * 256;
+}
 
 // Attention over whole sequences in one pass.
 int attend(const kv8_cache *cache, int32_t num_q_heads, const kv8_rows *q, const kv8_rows *out,
@@ -195,6 +197,8 @@ int attend(const kv8_cache *cache, int32_t num_q_heads, const kv8_rows *q, const
   cudaError_t ce = cudaSuccess;
   if (!causal) {
     a.plan = reinterpret_cast<int4 *>(static_cast<uint8_t *>(workspace) + plan.bytes);
+    a.falls = reinterpret_cast<int *>(a.plan + 2 * static_cast<size_t>(cache->num_seqs));
+    a.fall_words = kv8::fall_words(0, cache->num_seqs);
     a.fine = a.first = 1;
     ++n;
     ce = kv8::launch_segments(a, st);
@@ -327,6 +331,8 @@ int kv8_shared_attn(const kv8_cache *cache, int32_t num_q_heads, const kv8_rows 
   a.max_group_rows = max_group_rows;
   a.plan = reinterpret_cast<int4 *>(ws + plan.off_segs);
   a.items = reinterpret_cast<int4 *>(ws + plan.off_items);
+  a.falls = reinterpret_cast<int *>(ws + plan.off_falls);
+  a.fall_words = kv8::fall_words(num_groups, cache->num_seqs);
   a.carry_ml = reinterpret_cast<float2 *>(ws + plan.off_ml);
   a.carry_o = reinterpret_cast<float4 *>(ws + plan.off_o);
   a.carry_blocks = plan.carry_blocks;
@@ -388,7 +394,8 @@ SharedPlan plan_shared(int D, int S, int H, int num_q_heads, long long rows, lon
   p.off_prefix = own.bytes;
   p.off_segs = own.bytes + prefix.bytes;
   p.off_items = align(p.off_segs + static_cast<size_t>(2) * S * 2 * sizeof(int4));
-  p.off_ml = align(p.off_items + static_cast<size_t>(2) * kMaxTileCtas * sizeof(int4));
+  p.off_falls = p.off_items + static_cast<size_t>(2) * kMaxTileCtas * sizeof(int4);
+  p.off_ml = align(p.off_falls + fall_words(S, S) * sizeof(int));
   p.carry_blocks = (rows * group + 31) / 32;
   const size_t n = static_cast<size_t>(H) * p.carry_blocks * 32;
   p.off_o = align(p.off_ml + n * sizeof(float2));

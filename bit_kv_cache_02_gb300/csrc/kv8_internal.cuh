@@ -164,12 +164,18 @@ AttnPlan plan_attn(int D, long long rows_per_head);
 // kernels over the shared blocks join them and write the outputs.  They need not
 // wait for the others until then, so each has regions of its own.
 struct SharedPlan {
-  size_t off_prefix, off_segs, off_items, off_ml, off_o, bytes;
+  size_t off_prefix, off_segs, off_items, off_falls, off_ml, off_o, bytes;
   long long carry_blocks;
   bool own_tiles, prefix_tiles;
 };
 SharedPlan plan_shared(int D, int S, int H, int num_q_heads, long long rows, long long max_new,
                        long long max_group_rows);
+
+// Threads of a CTA of the kernel that looks up the segments, its CTAs, and the
+// words in which its warps say whether row_start or group_start falls.
+constexpr int kSegThreads = 128;
+inline int seg_ctas(int groups, int S) { return (groups + S + kSegThreads - 1) / kSegThreads; }
+inline int fall_words(int groups, int S) { return seg_ctas(groups, S) * (kSegThreads / 32); }
 
 // What one launch attends to, segment by segment.
 enum {
@@ -189,6 +195,8 @@ struct AttnArgs {
   int groups, max_group_rows;
   int4 *plan;        // two per segment: the groups', then the sequences'
   int4 *items;       // [kMaxTileCtas][2]: what the join kernel joins, by the first CTA of its parts
+  int *falls;        // [fall_words]: whether row_start or group_start falls
+  int fall_words;
   int first;         // the first launch behind the lookup of the segments
   // Partial results over what lies behind the shared blocks, of the rows of each
   // KV head, (tensor row, query head of the KV head):

@@ -9,21 +9,26 @@
 namespace kv8 {
 namespace shared {
 
-constexpr int kSegThreads = 128;
-
 // A thread per group, if there are any, then per sequence.
 __global__ void __launch_bounds__(kSegThreads) segments_kernel(const AttnArgs a) {
   asm volatile("griddepcontrol.launch_dependents;");
   const int i = blockIdx.x * kSegThreads + threadIdx.x;
   if (a.groups)  // nothing to join so far
     for (int k = i; k < kMaxTileCtas; k += gridDim.x * kSegThreads) a.items[2 * k] = make_int4(0, 0, 0, 0);
-  if (i >= a.groups + a.geo.S) return;
-  bool shut = false;
-  const Seg x = i < a.groups ? group_seg(a, i) : a.groups ? own_seg(a, i - a.groups, shut) : load_seg<false>(a, i);
-  store_plan(a, i, x, rows::plan_of(a, x, i < a.groups ? a.group_rows_max : a.rows_max));
+  const int s = i - a.groups;
+  bool shut = false, falls = false;
+  if (i < a.groups + a.geo.S) {
+    if (i < a.groups)
+      falls = a.group_start[i + 1] < a.group_start[i];
+    else if (a.row_start)
+      falls = a.row_start[s + 1] < a.row_start[s];
+    const Seg x = i < a.groups ? group_seg(a, i) : a.groups ? own_seg(a, s, shut) : load_seg<false>(a, i);
+    store_plan(a, i, x, rows::plan_of(a, x, i < a.groups ? a.group_rows_max : a.rows_max));
+  }
+  falls = __any_sync(0xffffffffu, falls);
+  if ((i & 31) == 0) a.falls[i >> 5] = falls;
   if (shut) {
     // rows that the launch over their group's blocks is not to write
-    const int s = i - a.groups;
     const long long from = max(a.row_start ? a.row_start[s] : s, 0);
     const long long to = min(a.row_start ? a.row_start[s + 1] : s + 1, a.rows);
     for (int h = 0; h < a.geo.H; ++h)
@@ -63,7 +68,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnArgs a) {
   const int4 rows = a.items[2 * c0 + 1];
   const int t0 = rows.x, n_rows = rows.y;  // the group's first tensor row, its rows of a KV head
   if (row0 >= n_rows || !KVQ_IN_BOUNDS(a.geo.status, first, 2 * kMaxTileCtas) ||
-      !KVQ_IN_BOUNDS(a.geo.status, c0 + n - 1, kMaxTileCtas))
+      !KVQ_IN_BOUNDS(a.geo.status, c0 + n - 1, kMaxTileCtas) || c0 + n > kMaxTileCtas)
     return;
   __shared__ float4 turned[kJoinRows][17];
   __shared__ float2 sums[kJoinRows];
@@ -125,8 +130,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnArgs a) {
 }  // namespace shared
 
 cudaError_t launch_segments(const AttnArgs &a, cudaStream_t stream) {
-  const int n = a.groups + a.geo.S;
-  shared::segments_kernel<<<(n + shared::kSegThreads - 1) / shared::kSegThreads, shared::kSegThreads, 0, stream>>>(a);
+  shared::segments_kernel<<<seg_ctas(a.groups, a.geo.S), kSegThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

@@ -312,10 +312,13 @@ struct Pair {
   int units0;     // those that row tile 0 sees
 };
 
+// (SHARED: a start behind the rows, where a range is invalid, must not move the
+// slots of others)
 template <bool SHARED>
 __device__ __forceinline__ int row_start_of(const AttnArgs &a, int s) {
   if (SHARED && a.part == kPrefix) s = min(max(a.group_start[s], 0), a.geo.S);
-  return a.row_start ? max(a.row_start[s], 0) : s;
+  if (!a.row_start) return s;
+  return SHARED ? min(max(a.row_start[s], 0), a.rows) : max(a.row_start[s], 0);
 }
 
 template <bool SHARED>
@@ -547,9 +550,14 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
   const int slots = static_cast<int>(last_row * a.group / kRows) + a.segs;
   Pair mine;
   {
-    // the slots below need row_start to rise
-    // (SHARED: a look at each costs the start more than the items that it saves; an
-    // item that it loses is rows left alone)
+    // The slots below need row_start, and group_start, to rise: the line is counted
+    // by slots and walked by segments, and where the two differ CTAs disagree on
+    // an item's parts, counters stay set and places lie behind the last.
+    // (SHARED: the lookup has found out.  Its words are asked for first and used
+    // last, and a fall makes the line's sum longer than any line: no wait and no
+    // barrier of its own, which would cost short calls 1 us)
+    constexpr long long kFalls = 1ll << 53;
+    int fell = SHARED && tid < a.fall_words ? a.falls[tid] : 0;
     bool falls = false;
     if (!SHARED && a.row_start)
       for (int s = tid; s < geo.S; s += kThreads)
@@ -560,7 +568,12 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       mine = pair_of_slot<SHARED>(a, i);
       sum += line_of(mine, H);
     }
+    if (SHARED) {
+      for (int i = tid + kThreads; i < a.fall_words; i += kThreads) fell |= a.falls[i];
+      if (fell) sum = kFalls;
+    }
     total = cta_scan(sum, before, scan_buf);
+    if (SHARED && total >= kFalls) total = 0;
   }
   if (total == 0) return finish<SHARED>();
   // Eight line positions per CTA at least.  Long lines, from 1216 on, do not

@@ -326,7 +326,8 @@ int kv8_cross_attn(const kv8_cache *cache, int32_t num_q_heads, const kv8_rows *
  * first sequence that ends within the shared blocks is invalid: the rows of its
  * sequences are left alone, as are those of a sequence that ends within them, and
  * KVQ_STATUS_BAD_LEN is set.  Neither row_start nor group_start may decrease:
- * where one does, that bit is set and the rows of all sequences are undefined.
+ * where one does, that bit is set and the rows of all sequences are undefined
+ * (nothing else is: the workspace serves the next call).
  * Otherwise results are as kv8_attn describes them, for a table in which all
  * sequences of a group have its first one's entries.  Three to six kernels.
  */
