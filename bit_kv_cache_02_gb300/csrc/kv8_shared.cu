@@ -27,12 +27,15 @@ __global__ void __launch_bounds__(kSegThreads) segments_kernel(const AttnArgs a)
   }
   falls = __any_sync(0xffffffffu, falls);
   if ((i & 31) == 0) a.falls[i >> 5] = falls;
-  if (shut) {
-    // rows that the launch over their group's blocks is not to write
-    const long long from = max(a.row_start ? a.row_start[s] : s, 0);
-    const long long to = min(a.row_start ? a.row_start[s + 1] : s + 1, a.rows);
+  // Rows that the launch over their group's blocks is not to write, a sequence after
+  // the other by the whole warp: all later kernels wait for this one (2000 rows x
+  // 32 query heads: 25 us; by the sequence's thread alone 330).
+  for (unsigned m = __ballot_sync(0xffffffffu, shut); m; m &= m - 1) {
+    const int j = __shfl_sync(0xffffffffu, s, __ffs(m) - 1);
+    const long long from = max(a.row_start ? a.row_start[j] : j, 0);
+    const long long to = min(a.row_start ? a.row_start[j + 1] : j + 1, a.rows);
     for (int h = 0; h < a.geo.H; ++h)
-      for (long long r = from * a.group; r < to * a.group; ++r)
+      for (long long r = from * a.group + (threadIdx.x & 31); r < to * a.group; r += 32)
         a.carry_ml[h * a.carry_blocks * 32 + r] = make_float2(0.f, -1.f);
   }
 }

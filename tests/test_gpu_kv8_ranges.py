@@ -105,6 +105,32 @@ def test_shared_bounds_that_fall(kv8, H, g, units, falling):
         assert st == 0 and torch.equal(again, want), kw
 
 
+def test_a_shut_out_sequence_does_not_stall_the_call(kv8):
+    """A sequence above max_len that shares blocks has its rows taken out of its
+    group's join.  That takes no longer than the zeros that it gets anyway: a call
+    in which it is of no group takes as long, to within half."""
+    n = 2000
+    r = Filled(kv8, [300, 9000, 300], 8, 4, n + 2)
+    ws = kv8.alloc_shared_workspace(r.cache, 32, n + 2, n, n + 2)
+    start, prefix, out = _i32([0, 1, n + 1, n + 2]), _i32([256]), torch.empty_like(r.q)
+
+    def time(groups):
+        groups, best = _i32(groups), float("inf")
+        for _ in range(6):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            for _ in range(10):
+                kv8.kv8_shared_attn(r.cache, r.q, out, ws, 8000, groups, prefix, n + 2, row_start=start, max_new=n)
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return best
+
+    alone = time([0, 1])
+    assert time([0, 3]) <= 1.5 * alone
+    assert (out[1:n + 1] == 0).all() and (out[[0, n + 1]] != 0).any()
+
+
 def test_a_start_far_behind_the_rows(kv8):
     """A row range that ends at 2^31 - 1, whose rows times the queries per KV head
     pass 32 bits, is invalid; the other sequences' rows are what they were."""
