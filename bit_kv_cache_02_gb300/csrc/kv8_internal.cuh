@@ -299,7 +299,7 @@ __device__ __forceinline__ void store_plan(const AttnArgs &a, int i, const Seg &
 __device__ __forceinline__ Seg load_plan(const AttnArgs &a, int s, Plan &w) {
   if (!KVQ_IN_BOUNDS(a.geo.status, s, a.segs)) s = 0;
   const int4 *p = a.plan + 2 * (static_cast<size_t>(a.part == kOwn ? a.groups : 0) + s);
-  const int4 x = p[0], y = p[1];
+  const int4 x = a.first ? p[0] : __ldcg(p), y = a.first ? p[1] : __ldcg(p + 1);
   w = {y.y, y.z, y.w};
   return {x.x, x.y, x.z, x.w, max(y.x, 0), y.x >= 0};
 }
@@ -317,6 +317,14 @@ __device__ __forceinline__ Seg load_seg(const AttnArgs &a, int s) {
 // ones before still run.  Each lets the next one start once the segments are there: the first waits
 // for them, and the others start behind it.  Each waits for the one before it
 // at the latest before it ends, so that the end of one is the end of all before.
+//
+// A wait makes the writes of the grid before visible, and the first launch waits
+// for the lookup.  The later ones read the lookup's words without a wait of their
+// own.  They rely on two things: all CTAs of the first launch have waited, that is,
+// the lookup's writes have been performed, before any of theirs starts; and their
+// loads go past the first-level cache (load_plan), which may hold lines from before.
+// (In the first launch that would cost beams 0.9 us and a batch's cross attention
+// 1.4; a fence at the start of the later ones costs calls with shared blocks 0.7.)
 __device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 template <bool FINE>
 __device__ __forceinline__ void start(const AttnArgs &a) {

@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
     // last, and a fall makes the line's sum longer than any line: no wait and no
     // barrier of its own, which would cost short calls 1 us)
     constexpr long long kFalls = 1ll << 53;
-    int fell = SHARED && tid < a.fall_words ? a.falls[tid] : 0;
+    int fell = SHARED && tid < a.fall_words ? __ldcg(a.falls + tid) : 0;
     bool falls = false;
     if (!SHARED && a.row_start)
       for (int s = tid; s < geo.S; s += kThreads)
@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       sum += line_of(mine, H);
     }
     if (SHARED) {
-      for (int i = tid + kThreads; i < a.fall_words; i += kThreads) fell |= a.falls[i];
+      for (int i = tid + kThreads; i < a.fall_words; i += kThreads) fell |= __ldcg(a.falls + i);
       if (fell) sum = kFalls;
     }
     total = cta_scan(sum, before, scan_buf);
