@@ -286,7 +286,7 @@ int kv8_attn(const kv8_cache *cache, int32_t num_q_heads, const kv8_rows *q,
  *   max_rows   host bound on the rows of one sequence, from 1 on; not bound by
  *              the capacity.  max_rows * Hq / Hkv is below 2^30.
  *   softmax_scale, workspace, max_len, and all else, as in kv8_attn; the
- *              workspace has at least kv8_cross_attn_workspace_bytes(), a few
+ *              workspace has at least kv8_cross_attn_workspace_bytes(), about 32
  *              bytes per sequence more than kv8_attn's, and may serve both.
  *
  * Every row sees the seq_len[s] tokens of its sequence.  Rows of a sequence
@@ -319,8 +319,9 @@ int kv8_cross_attn(const kv8_cache *cache, int32_t num_q_heads, const kv8_rows *
  *   workspace  at least kv8_shared_attn_workspace_bytes() for these rows, max_new
  *              and max_group_rows (a size that serves larger ones serves smaller
  *              ones), with the rules of kv8_attn's; it may serve kv8_attn and
- *              kv8_cross_attn too.  4 D + 8 bytes per row and query head, and a
- *              few per sequence, on top of kv8_attn's size.
+ *              kv8_cross_attn too.  It is as large as kv8_attn's for max_new and
+ *              kv8_attn's for max_group_rows rows of a sequence together, and 4 D + 8
+ *              bytes per row and query head and about 70 per sequence more.
  *
  * A group with bad bounds, a bad prefix_len, more rows than max_group_rows or a
  * first sequence that ends within the shared blocks is invalid: the rows of its

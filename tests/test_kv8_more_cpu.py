@@ -226,6 +226,21 @@ def test_workspace_sizes(kv8):
     assert size(p, 8, 100000, 1, 5) - size(p, 8, 0, 1, 5) >= 100000 * 8 * (4 * 128 + 8)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_workspace_sizes_are_what_they_hold(kv8, D):
+    """No more than include/kv8.h says: the sizes of kv8_attn for either part, the
+    partial results of the rows, and a few bytes per sequence."""
+    for S, Hq, rows, new, most in ((1, 2, 1, 1, 1), (64, 8, 64, 1, 64), (6, 32, 1900, 400, 1900), (3, 2, 900, 900, 30),
+                                   (65535, 2, 70000, 2, 500)):
+        st = _struct(kv8, num_seqs=S, head_dim=D)
+        p, L = ctypes.byref(st), kv8.lib
+        own, group = L.kv8_attn_workspace_bytes(p, Hq, new), L.kv8_attn_workspace_bytes(p, Hq, min(most, 1000))
+        size = L.kv8_shared_attn_workspace_bytes(p, Hq, rows, new, most)
+        rest = size - own - group - (rows * Hq + 32 * 2) * (4 * D + 8)
+        assert -32 * 2 * (4 * D + 8) <= rest <= 70 * S + 13000, (S, rest)
+        assert 32 * S <= L.kv8_cross_attn_workspace_bytes(p, Hq, new) - own <= 34 * S + 512
+
+
 def test_python_checks(kv8):
     c = kv8.KV8Cache(2, 2, 100, 4, head_dim=64, block=32, dtype=torch.bfloat16, device="cpu")
     x, ws = torch.zeros(2, 2, 64, dtype=torch.bfloat16), torch.zeros(1 << 20, dtype=torch.uint8)
