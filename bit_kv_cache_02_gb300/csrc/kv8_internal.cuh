@@ -266,14 +266,13 @@ __device__ __forceinline__ Seg own_seg(const AttnArgs &a, int s, bool &shut) {
   const int g = last_at_or_below(a.groups, s, [&](int i) { return a.group_start[i]; });
   if (a.group_start[g] <= s && s < a.group_start[g + 1]) {
     const Group of = load_group(a, g);
-    if (q.n > 0 && q.L <= a.max_len) {
-      if (!of.ok || (of.blocks && (q.L <= 0 || q.L - q.n < of.blocks * a.geo.B))) {
-        x.ok = false;
-        x.n = 0;
-      } else {
-        x.base = of.blocks;
-        x.L -= of.blocks * a.geo.B;
-      }
+    const bool bounded = q.L <= a.max_len;  // (else zeros)
+    if (!of.ok || (q.n > 0 && bounded && of.blocks && (q.L <= 0 || q.L - q.n < of.blocks * a.geo.B))) {
+      x.ok = false;
+      x.n = 0;
+    } else if (q.n > 0 && bounded) {
+      x.base = of.blocks;
+      x.L -= of.blocks * a.geo.B;
     }
     shut = of.ok && of.blocks && !x.base;
   }

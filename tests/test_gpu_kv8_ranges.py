@@ -131,6 +131,39 @@ def test_a_shut_out_sequence_does_not_stall_the_call(kv8):
     assert (out[1:n + 1] == 0).all() and (out[[0, n + 1]] != 0).any()
 
 
+def test_an_invalid_group_s_rows_are_left_alone(kv8):
+    """All of them, those of a sequence above max_len too, which gets zeros in a
+    valid group."""
+    r = Filled(kv8, [300, 900, 310, 400], 2, 4, 8)
+    ws = kv8.alloc_shared_workspace(r.cache, 8, 8, 2, 8)
+    start = [0, 2, 4, 6, 8]
+
+    def call(prefix, max_len, group_rows=6):
+        r.capacity, was = max_len, r.capacity
+        out, st = r.call("shared", ws, start, 2, groups=[0, 3], prefix=[prefix], group_rows=group_rows)
+        r.capacity = was
+        return out, st
+
+    # Other rows are the same within the roundings: without the sequence the work is
+    # cut at other places, so that weights are rounded to fp16 relative to other
+    # maxima.  Each is off by 2^-11 of itself at most, an output by 2^-11 of the
+    # largest value, and by 2^-11 of itself once it is fp16; sums in fp32 of 300
+    # tokens by 300 * 2^-24 of that value.  Two of them differ by twice that.
+    value = max(1.27, float(r.cache.v_win.abs().max()))  # of blocks: 127 * 0.01
+    want, st = call(256, 900)
+    assert st == 0
+
+    def same(rows):
+        x, y = out[rows].double(), want[rows].double()
+        return bool(((x - y).abs() <= 2.0 ** -10 * (value * (1 + 300 * 2.0 ** -13) + y.abs())).all())
+
+    out, st = call(256, 500)
+    assert st == 8 and (out[2:4] == 0).all() and same([0, 1, 4, 5, 6, 7])
+    for prefix, group_rows in ((-1, 6), (501, 6), (320, 6), (256, 5)):
+        out, st = call(prefix, 500, group_rows)
+        assert st == 2 and (out[:6] == 3.0).all() and same([6, 7]), (prefix, group_rows)
+
+
 def test_a_start_far_behind_the_rows(kv8):
     """A row range that ends at 2^31 - 1, whose rows times the queries per KV head
     pass 32 bits, is invalid; the other sequences' rows are what they were."""
