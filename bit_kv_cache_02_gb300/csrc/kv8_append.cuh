@@ -20,8 +20,8 @@
 // AXES: each row has a position on up to four axes, and each pair of channels
 // turns by the axis that a map names; all else is the same.  The map has two
 // bits per pair and travels with the launch.  40573 tokens of 16 prompts x 32 + 2 x
-// 8 heads x 128, three axes in sections: 162 us, 5.7 TB/s; a token 3.1 us, of 64
-// sequences 4.5.
+// 8 heads x 128, three axes in sections: 164 us replayed, 5.6 TB/s; a token 3.1 us, of
+// 64 sequences 4.4.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -454,8 +454,8 @@ cudaError_t launch(const Geo &geo, const Rows &k, const Rows &v, const Rows &q, 
   const long long blocks = a.slots ? a.slots : geo.S;
   a.split = blocks * geo.H >= 2048;
   // (With axes a token's angles cost its positions too: eight heads from 2048 on.
-  // Prompts of 40573 tokens, 8 + 32 heads, 5200 blocks x heads: 164 us, one head
-  // per CTA 191, two 175, four 167.)
+  // Prompts of 40573 tokens, 8 + 32 heads, 5200 blocks x heads, replayed: 164 us, one
+  // head per CTA 191, two 175, four 167.)
   a.heads = blocks * geo.H >= (AXES ? 2048 : 8192) && rot_dim ? 8 : 1;
   a.head_groups = (geo.H + a.heads - 1) / a.heads;
   const long long tasks = blocks * a.head_groups * (a.split ? 2 : 1);

@@ -293,11 +293,15 @@ struct Plain {
 // of the warps and the outputs, whatever its length.  Short ones are not cut, and
 // one warp does all of a short one, its neighbours the next ones: they cost
 // little besides, and no barrier.  `each`: one triple per CTA, none cut.
-// Drawn batches with other constants, replayed: short up to 8 or 16 units 26.5 and
-// 29.9 us instead of 24.5; 8 units besides a long triple's instead of 14, 17.4 for
-// 16.2; `each` for 8 units more than a CTA's share instead of 16, 17.5 for 12.1, and
-// for triples of 16 units at most, whatever the share, 22.9 for 17.0 (16 x 16 heads,
-// four rows over 1500 tokens).
+// Cross attention of one row with other constants, replayed (sequences x KV heads x
+// queries each).  Short up to 8 or 16 units instead of 4: 64 x 8 x 4 over 100 to 900
+// tokens 30.4 and 32.4 us for 25.3, 40 x 8 x 4 over 200 to 3000 36.0 and 39.6 for
+// 35.5; but 200 x 8 x 4 over 100 to 400, where nearly all are then short, 50.8 and
+// 41.2 for 49.9.  8 or 20 units besides a long triple's instead of 14: 14 x 8 x 4 over
+// 500 to 900 tokens 15.9 and 14.8 for 14.8, 24 x 8 x 4 over 900 to 1100 18.9 and 19.5
+// for 18.5.  `each` for triples of 16 units at most, whatever a CTA's share: 16 x 16
+// x 1, four rows over 1500 tokens, 21.4 for 17.2; for 8 units more than the share
+// instead of 16 no difference in these.
 constexpr int kShort = 4, kOverShort = 2, kOver = 14;
 constexpr int kEach = 4 * kWarps;
 struct Fine {

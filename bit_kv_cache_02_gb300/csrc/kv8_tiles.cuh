@@ -21,7 +21,9 @@
 //
 // Parts and Metas live in shared memory so that the other roles keep their
 // registers for data: a spilled register costs an L2 round trip here, as the
-// tiles leave no first-level cache to speak of.
+// tiles leave no first-level cache to speak of.  (The 28 bytes that kv8_attn's
+// forms spill do not show: a chunk of 2048 tokens over 8192 takes 215 us, the form
+// without spills before 218, prompts from position 0 561 and 560.)
 //
 // Mathematics, in log2 units per row: z_t = q.k_t scale_k softmax_scale log2(e),
 // w_t = 2^(z_t + log2(scale_v) - M + 9), O = sum w_t v_code_t, l = sum w_t /

@@ -301,7 +301,13 @@ int kv8_cross_attn(const kv8_cache *cache, int32_t num_q_heads, const kv8_rows *
  * kv8_shared_attn -- kv8_attn where groups of sequences share their first blocks
  * (a system prompt, a document, the prompt of several answers): the rows of all
  * sequences of a group attend to those blocks at once, and each sequence's rows
- * to what lies behind them; both results are joined in 32 bits.
+ * to what lies behind them; both results are joined in 32 bits.  It pays where many
+ * sequences of few rows share a group's blocks.  Where each sequence's line of the
+ * table names the shared blocks too, kv8_attn gives the same rows, and reads blocks
+ * that others have read from L2: 64 single tokens behind 4096 shared ones 51 us
+ * here and 76 there (8 KV heads of 4), but four behind 512 tokens 19 and 14, 12 groups
+ * of 1 to 8 sequences with drafts 52 and 36, six chunks of 100 to 500 rows behind 8192
+ * 294 and 274.
  *
  *   q, out, row_start, rows, max_new, softmax_scale, max_len  as in kv8_attn.
  *   group_start  device int32 [num_groups + 1]: group g is sequences
